@@ -248,5 +248,7 @@ class Layer:
             pass
 
 
-__all__ = ["Layer", "MonoError", "lib", "strerror", "make_spec", "Spec", "Weights", "StepArgs",
+from moe_decode_layer_mxfp8_gb300.cache import CACHE_EXPORTS, Cache, verify_drafts  # noqa: E402
+
+__all__ = ["Layer", "Cache", "verify_drafts", "CACHE_EXPORTS", "MonoError", "lib", "strerror", "make_spec", "Spec", "Weights", "StepArgs",
            "FfnArgs", "BUF", "EXPORTS", "LIB_PATH", "ATTN_WEIGHT_FIELDS"]
