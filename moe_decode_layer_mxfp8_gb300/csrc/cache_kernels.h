@@ -35,7 +35,6 @@ struct AttendArgs {
   float* lse;  // [rows, n_q] (the caller's, or the workspace's when only weights are asked for)
   float* weights;
   long long weights_stride;
-  float* part;  // workspace: partial results
   int* status;
 };
 
@@ -65,8 +64,10 @@ struct VerifyArgs {
   int *accepted, *tokens;
 };
 
-size_t attend_workspace_bytes(int n_q, int head_dim, int max_rows);
-cudaError_t launch_attend(const Launch&, const AttendArgs&);
+size_t attend_workspace_bytes(int max_rows, int sms);
+cudaError_t attend_prepare();  // raises the dynamic shared-memory limit
+cudaError_t launch_attend(const Launch&, const AttendArgs&, uint8_t* workspace, int max_rows,
+                          int sms);
 cudaError_t launch_evict(const Launch&, const EvictArgs&);
 cudaError_t launch_verify(const Launch&, const VerifyArgs&, int dtype);
 

@@ -13,7 +13,8 @@ struct mono_cache {
   int device = 0;
   uint8_t* arena = nullptr;
   float* lse = nullptr;
-  float* part = nullptr;
+  uint8_t* attend_ws = nullptr;
+  int sms = 0;
   int* status = nullptr;
 };
 
@@ -87,17 +88,19 @@ int mono_cache_build(const mono_cache_spec* spec, mono_cache_t** out) {
   h->spec = *spec;
   h->device = dev;
   const size_t lse = ((size_t)spec->max_rows * spec->n_q_heads * 4 + 255) / 256 * 256;
-  const size_t part = attend_workspace_bytes(spec->n_q_heads, spec->head_dim, spec->max_rows);
+  const size_t part = attend_workspace_bytes(spec->max_rows, prop.multiProcessorCount);
   cudaError_t e = cudaMalloc(&h->arena, 256 + lse + part);
   if (e == cudaSuccess) e = cudaMemset(h->arena, 0, 256 + lse + part);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = attend_prepare();
   if (e != cudaSuccess) {
     mono_cache_free(h);
     return cuda_code(e);
   }
   h->status = reinterpret_cast<int*>(h->arena);
   h->lse = reinterpret_cast<float*>(h->arena + 256);
-  h->part = reinterpret_cast<float*>(h->arena + 256 + lse);
+  h->attend_ws = h->arena + 256 + lse;
+  h->sms = prop.multiProcessorCount;
   *out = h;
   return MONO_OK;
 }
@@ -158,9 +161,9 @@ int mono_cache_attend(mono_cache_t* h, const mono_attend_args* a, void* stream) 
   k.lse = a->lse ? a->lse : h->lse;
   k.weights = a->weights;
   k.weights_stride = a->weights_stride;
-  k.part = h->part;
   k.status = h->status;
-  return cuda_code(launch_attend(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k));
+  return cuda_code(launch_attend(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k,
+                                 h->attend_ws, s.max_rows, h->sms));
 }
 
 int mono_cache_evict(mono_cache_t* h, const mono_evict_args* a, void* stream) {
