@@ -39,12 +39,15 @@ constexpr int TT = 128;        // tokens per tile
 constexpr int NQ = 96;         // query columns at most
 constexpr int MERGE = 64;      // up to here both terms are columns of one MMA
 constexpr int GROUP = 16;      // rows of a group at most
+constexpr int ALT = 48;        // up to here the two softmax halves take turns with whole tiles
 constexpr int ST = 6;          // tiles in the ring
-constexpr int AHEAD = 5;       // of these in flight
 constexpr int MAX_REQ = 1024;
-constexpr int THREADS = 13 * 32;
-constexpr int SOFT_WARPS = 8, LOAD_WARP = 8, MMA_WARP = 12;
-constexpr float JUMP = 40.0f;      // log2 of how far a score may pass m_q
+constexpr int THREADS = 16 * 32;
+constexpr int SOFT_WARPS = 8, LOAD_WARP = 8, LOAD_WARPS = 4, MMA_WARP = 12;
+// registers a thread: softmax warps take what the others give up (in all, the launch's 128)
+constexpr int SOFT_REGS = 200, OTHER_REGS = 56;
+static_assert(SOFT_REGS * 256 + OTHER_REGS * 256 == 128 * THREADS, "register split");
+constexpr float JUMP = 40.0f;      // log2 of how far a weight may pass 1
 constexpr float UNSET = -1.0e30f;  // m_q of a query that has seen no token
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
@@ -53,8 +56,8 @@ constexpr int P_BUF = 2 * TT * 128;  // hi terms, then lo terms (merged: hi and 
 constexpr int P_OFF = K_OFF + ST * TT * 128;
 constexpr int Q_OFF = P_OFF + 2 * P_BUF;  // hi rows, then lo rows
 constexpr int IMG = 512;
-constexpr int PIMG_OFF = Q_OFF + 2 * NQ * 128;  // [2 buffers][hi, lo]
-constexpr int QIMG_OFF = PIMG_OFF + 4 * IMG;
+constexpr int PIMG_OFF = Q_OFF + 2 * NQ * 128;  // [2 buffers]
+constexpr int QIMG_OFF = PIMG_OFF + 2 * IMG;
 constexpr int ONE_OFF = QIMG_OFF + IMG;
 constexpr int SC_OFF = ONE_OFF + IMG;  // token scales [ST][128]
 constexpr int PLAN_OFF = SC_OFF + ST * TT * 4;
@@ -63,7 +66,7 @@ static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 static_assert(P_OFF % 1024 == 0 && Q_OFF % 1024 == 0 && (NQ * 128) % 1024 == 0, "swizzle atoms");
 
 // TMEM columns
-constexpr int S_COL = 0, O_COL = 256, SF_ONE = 384, SF_Q = 388, SF_P = 392;  // two images each
+constexpr int S_COL = 0, O_COL = 256, O_ALT = 96, SF_ONE = 480, SF_Q = 484, SF_P = 488;
 // Instruction descriptor of kind::mxf8f6f4: e4m3 x e4m3, E8M0 scales, M = 128; N, the scale-byte
 // selectors and the transposes are or-ed in.
 constexpr uint32_t IDESC = (1u << 23) | ((uint32_t)(TT >> 4) << 24);
@@ -171,14 +174,22 @@ __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Two f16 values as e4m3 hi codes and, of 16 times what is left, lo codes (a code pair each).
+// Two f16 values as e4m3 hi codes and the codes of what is left (a pair each).
 __device__ __forceinline__ void hilo_f16x2(uint32_t x, uint32_t& hi, uint32_t& lo) {
-  asm("{\n .reg .b16 h, l;\n .reg .b32 f, r, s;\n"
+  asm("{\n .reg .b16 h, l;\n .reg .b32 f, r;\n"
       " cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n cvt.rn.f16x2.e4m3x2 f, h;\n"
-      " sub.rn.f16x2 r, %2, f;\n mov.b32 s, 0x4C004C00;\n mul.rn.f16x2 r, r, s;\n"
+      " sub.rn.f16x2 r, %2, f;\n"
       " cvt.rn.satfinite.e4m3x2.f16x2 l, r;\n cvt.u32.u16 %0, h;\n cvt.u32.u16 %1, l;\n}"
       : "=r"(hi), "=r"(lo)
       : "r"(x));
+}
+template <int REGS>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 template <int N>
 __device__ __forceinline__ void bar_sync(int id) {
@@ -195,11 +206,7 @@ __device__ __forceinline__ bool bar_any(int id, bool v) {
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // The whole warp's view of the abort flag.
 __device__ __forceinline__ bool stopped(volatile int* abort) {
   return __any_sync(0xffffffffu, *abort != 0);
@@ -212,19 +219,239 @@ __device__ __forceinline__ float warp_max_any(float v) {
   return __int_as_float(i < 0 ? i ^ 0x7FFFFFFF : i);
 }
 
+struct Shared {
+  uint64_t full[ST], empty[ST], s_full[2], p_full[2], pv_done[2], q_full, drain;
+  float neg_m[2][NQ], fac[2][NQ], red[SOFT_WARPS][NQ];  // [stream] (one unless the halves take turns)
+  uint32_t tmem, valid[ST][4];
+  int col_hi[NQ], col_lo[NQ], group_row[GROUP], group_pos[GROUP];
+  int cols, abort;
+  long long warp_tot[THREADS / 32];
+};
+
+// What a softmax warp knows of its item.
+struct Soft {
+  Span span;
+  int t0, n, it;        // the item's first tile and tile count, the ring's next tile
+  int nqp, c0, stream;  // columns of the item, this half's first one, its (O, m) set
+  int min_hi, max_lo;   // tokens that every row sees: [max_lo, min_hi] and the sinks
+  float to_log2;
+  uint32_t tmem;        // with the warp's lane quadrant
+};
+
+// The softmax of C columns over an item's tiles (TURNS: every other one), a token per thread.
+// l: this thread's share of the columns' sums, in units of 2^m.
+template <int C, bool TURNS, bool MERGED>
+__device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, Shared& sh, uint8_t* sm,
+                                           float* l_out) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quad = warp & 3, half = warp >> 2, tok = 32 * quad + lane;
+  volatile int* abort = &sh.abort;
+  float* neg_m = sh.neg_m[w.stream];
+  float* fac = sh.fac[w.stream];
+  float l[C], s[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) l[c] = 0.0f;
+  const int first = TURNS ? (half ^ (w.it & 1)) : 0, stride = TURNS ? 2 : 1;
+  for (int i = first; i < w.n; i += stride) {
+    const int it = w.it + i, st = it % ST, pb = it & 1;
+    const int t0 = w.span.token(w.t0 + i), t = t0 + tok;
+    warp_wait(&sh.full[st], (it / ST) & 1, a.status, abort);
+    const float raw = reinterpret_cast<const float*>(sm + SC_OFF)[st * TT + tok];
+    const uint32_t ok = sh.valid[st][quad];
+    const bool fin = fabsf(raw) <= 3.0e38f;
+    const float ct = fin ? raw * w.to_log2 : __int_as_float(0x7FC00000);
+    const float sc = fin ? raw : 0.0f;
+    // some of the tile's tokens are not every row's to see
+    const bool part = __any_sync(0xffffffffu, ok != 0xffffffffu || t0 + TT - 1 > w.min_hi ||
+                                                  (t0 < w.max_lo && t0 + TT > a.sinks));
+    // a weight says nothing of a token of next to no scale
+    const bool faint = __any_sync(0xffffffffu, !(sc > 1.0e-12f));
+    warp_wait(&sh.s_full[pb], (it >> 1) & 1, a.status, abort);
+    tc_fence_after();
+    const uint32_t scol = w.tmem + S_COL + 128 * pb + w.c0;
+    auto load = [&]() {  // the products of the tile
+#pragma unroll
+      for (int g = 0; g < C; g += 8) tc_ld8(scol + g, s + g);
+      if (MERGED) {
+#pragma unroll
+        for (int g = 0; g < C; g += 16) {
+          float x[16];
+          tc_ld8(scol + w.nqp + g, x);
+          tc_ld8(scol + w.nqp + g + 8, x + 8);
+          tc_wait_ld();
+          tc_loaded(x);
+          tc_loaded(x + 8);
+          if (g == 0)
+#pragma unroll
+            for (int k = 0; k < C; k += 8) tc_loaded(s + k);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[g + e] += x[e];
+        }
+      } else {
+        tc_wait_ld();
+#pragma unroll
+        for (int g = 0; g < C; g += 8) tc_loaded(s + g);
+      }
+    };
+    auto mask = [&](float v, int c) {
+      const bool see = ((ok >> lane) & 1) && t <= sh.col_hi[w.c0 + c] &&
+                       (t >= sh.col_lo[w.c0 + c] || t < a.sinks);
+      return see ? v : -INFINITY;
+    };
+    auto weigh = [&]() {  // s: products -> 2^(score - m)
+      const float4* nm = reinterpret_cast<const float4*>(neg_m + w.c0);
+#pragma unroll
+      for (int c = 0; c < C; c += 4) {
+        const float4 m = nm[c / 4];
+        s[c] = fmaf(s[c], ct, m.x);
+        s[c + 1] = fmaf(s[c + 1], ct, m.y);
+        s[c + 2] = fmaf(s[c + 2], ct, m.z);
+        s[c + 3] = fmaf(s[c + 3], ct, m.w);
+      }
+      if (part) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) s[c] = mask(s[c], c);
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) s[c] = ex2(s[c]);
+    };
+    uint32_t mx[C];  // exponent bits of the block's largest weight times scale
+    uint32_t top = 0;
+    auto blocks = [&]() {
+      top = 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        mx[c] = __reduce_max_sync(0xffffffffu, __float_as_uint(s[c] * sc));
+        top = max(top, mx[c]);
+      }
+    };
+    load();
+    weigh();
+    blocks();
+    bool over = top >= (uint32_t)(127 + (int)JUMP) << 23;
+    if (faint) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) over |= s[c] > exp2f(JUMP);
+    }
+    if (bar_any(2 + half, over)) {
+      // m moves where a weight passes 2^(JUMP / 2) (always in an item's first tile)
+      load();
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float v = s[c] * ct;
+        if (part) v = mask(v, c);
+        const float m = warp_max_any(v > -INFINITY ? v : -INFINITY);
+        if (lane == 0) sh.red[warp][w.c0 + c] = m;
+      }
+      bar_sync<128>(4 + half);
+      if (quad == 0)
+        for (int c = w.c0 + lane; c < w.c0 + C; c += 32) {
+          const float(*r)[NQ] = sh.red + 4 * half;
+          const float m = fmaxf(fmaxf(r[0][c], r[1][c]), fmaxf(r[2][c], r[3][c]));
+          const float old = -neg_m[c];
+          float f = 1.0f;
+          if (m - old > 0.5f * JUMP) {
+            const float now = fminf(ceilf(m), 3.0e38f);
+            f = old == UNSET ? 0.0f : ex2(old - now);
+            neg_m[c] = -now;
+          }
+          fac[c] = f;
+        }
+      bar_sync<128>(4 + half);
+#pragma unroll
+      for (int c = 0; c < C; ++c) l[c] *= fac[w.c0 + c];
+      if (i > first) {
+        const int prev = it - stride;  // its product is in O
+        warp_wait(&sh.pv_done[prev & 1], (prev >> 1) & 1, a.status, abort);
+        tc_fence_after();
+        for (int term = 0; term < (MERGED ? 2 : 1); ++term)
+          for (int g = 0; g < C; g += 8) {
+            float x[8];
+            const uint32_t oc = w.tmem + O_COL + O_ALT * w.stream + term * w.nqp + w.c0 + g;
+            tc_ld8(oc, x);
+            tc_wait_ld();
+            tc_loaded(x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= fac[w.c0 + g + e];
+            tc_st8(oc, x);
+          }
+        tc_wait_st();
+      }
+      load();
+      weigh();
+      blocks();
+    }
+    if (it >= 2) warp_wait(&sh.pv_done[pb], ((it >> 1) - 1) & 1, a.status, abort);
+    if (part && (TURNS || half == 0)) {
+      // NaN codes of tokens that some row must not see would reach it as 0 * NaN
+      uint32_t* k = reinterpret_cast<uint32_t*>(sm + K_OFF + st * TT * 128 + tok * 128);
+#pragma unroll 1
+      for (int e = 0; e < 32; ++e) {
+        const int j = (e + 4 * lane) & 31;
+        const uint32_t v = k[j];
+        const uint32_t nan = (((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
+        if (nan) k[j] = v & ~(nan * 0xFFu);
+      }
+    }
+    // weights times scales under their blocks' scales, as two e4m3 terms
+    uint8_t* prow = sm + P_OFF + pb * P_BUF + tok * 128;
+    uint8_t* img = sm + PIMG_OFF + pb * IMG;
+#pragma unroll
+    for (int g = 0; g < C; g += 16) {
+      uint32_t hi[4], lo[4];
+      uint32_t mine = 0;
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        float y[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c = g + e + k;
+          // the block's largest in [2^7, 2^8); exponents 15..254
+          const uint32_t mb = min(max(mx[c] & 0x7F800000u, 15u << 23), 254u << 23);
+          if (lane == e + k) mine = mb;
+          l[c] += s[c];
+          y[k] = s[c] * sc * __uint_as_float((261u << 23) - mb);
+        }
+        uint32_t h, r;
+        hilo_f16x2(f16x2_of(y[0], y[1]), h, r);
+        if (e & 2) {
+          hi[e >> 2] |= h << 16;
+          lo[e >> 2] |= r << 16;
+        } else {
+          hi[e >> 2] = h;
+          lo[e >> 2] = r;
+        }
+      }
+      if (lane < 16) {
+        const int n = w.c0 + g + lane, nl = w.nqp + n;
+        const uint8_t code = (uint8_t)((mine >> 23) - 7);
+        img[(n & 31) * 16 + (n >> 5) * 4 + quad] = code;
+        if (MERGED) img[(nl & 31) * 16 + (nl >> 5) * 4 + quad] = code;
+      }
+      const int ch = (w.c0 + g) >> 4, cl = MERGED ? (w.nqp + w.c0 + g) >> 4 : ch;
+      *reinterpret_cast<uint4*>(prow + ((ch ^ (tok & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(prow + (MERGED ? 0 : TT * 128) + ((cl ^ (tok & 7)) << 4)) =
+          make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    fence_proxy_async_shared();
+    tc_fence_before();
+    __syncwarp();
+    if (lane < (TURNS ? 2 : 1)) mbar_arrive(&sh.p_full[pb]);  // eight arrivals a tile either way
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const float v = warp_sum(l[c]);
+    if (lane == 0) l_out[w.c0 + c] = v;
+  }
+}
+
 __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
   const AttendArgs& a = ar.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~uintptr_t(1023));
-  __shared__ __align__(8) uint64_t full[ST], empty[ST], s_full[2], p_full[2], pv_done[2], q_full, drain;
-  __shared__ uint32_t s_tmem, valid[ST][4];
-  __shared__ int s_abort;
-  __shared__ __align__(16) float neg_m[NQ], fac[NQ], red[4][NQ];
-  __shared__ int col_hi[NQ], col_lo[NQ];
-  __shared__ int group_row[GROUP], group_pos[GROUP], s_rows;
-  __shared__ long long warp_tot[THREADS / 32];
-  volatile int* abort = &s_abort;
+  __shared__ __align__(16) Shared ss;
+  volatile int* abort = &ss.abort;
   Plan plan;
   plan.pre = reinterpret_cast<long long*>(sm + PLAN_OFF);
   plan.pmax = reinterpret_cast<int*>(plan.pre + MAX_REQ + 1);
@@ -235,18 +462,18 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
   const int chunk_bytes = min(128, a.kv_dim - 128 * chunk);
 
   if (tid == 0) {
-    for (int s = 0; s < ST; ++s) mbar_init(&full[s], 128), mbar_init(&empty[s], 1);
+    // a tile lands with its copies (the loading warp's lanes) and its mask (lane 0)
+    for (int s = 0; s < ST; ++s) mbar_init(&ss.full[s], 33), mbar_init(&ss.empty[s], 1);
     for (int s = 0; s < 2; ++s)
-      mbar_init(&s_full[s], 1), mbar_init(&p_full[s], SOFT_WARPS), mbar_init(&pv_done[s], 1);
-    mbar_init(&q_full, SOFT_WARPS);
-    mbar_init(&drain, 1);
-    s_abort = 0;
-    fence_mbar_init();
+      mbar_init(&ss.s_full[s], 1), mbar_init(&ss.p_full[s], SOFT_WARPS), mbar_init(&ss.pv_done[s], 1);
+    mbar_init(&ss.q_full, SOFT_WARPS);
+    mbar_init(&ss.drain, 1);
+    ss.abort = 0;
   }
-  if (warp == MMA_WARP) tmem_alloc<512>(&s_tmem);
+  if (warp == MMA_WARP) tmem_alloc<512>(&ss.tmem);
   for (int i = tid; i < IMG / 4; i += THREADS)
     reinterpret_cast<uint32_t*>(sm + ONE_OFF)[i] = 0x7F7F7F7Fu;
-  for (int i = tid; i < 5 * IMG / 4; i += THREADS)
+  for (int i = tid; i < 3 * IMG / 4; i += THREADS)
     reinterpret_cast<uint32_t*>(sm + PIMG_OFF)[i] = 0x7F7F7F7Fu;
   fence_proxy_async_shared();
 
@@ -289,12 +516,12 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
       const long long y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    if (lane == 31) warp_tot[warp] = x;
+    if (lane == 31) ss.warp_tot[warp] = x;
     __syncthreads();
     long long before = base;
     for (int i = 0; i < THREADS / 32; ++i) {
-      if (i < warp) before += warp_tot[i];
-      base += warp_tot[i];
+      if (i < warp) before += ss.warp_tot[i];
+      base += ss.warp_tot[i];
     }
     if (b < a.n_req) plan.pre[b + 1] = before + x;
     __syncthreads();
@@ -303,7 +530,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = ss.tmem;
 
   // where the second kernel finds the rows' results
   if (blockIdx.x == 0 && tid == 0) *ar.total = plan.pre[a.n_req];
@@ -323,86 +550,93 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
 
   if (team >= sh.teams) {
     // no team: nothing to do
-  } else if (warp >= LOAD_WARP && warp < LOAD_WARP + 4) {
-    // ------------------------------------------------------------------------------ loads
+  } else if (warp >= LOAD_WARP && warp < LOAD_WARP + LOAD_WARPS) {
+    // --------------------------------------------------- loads: a warp takes every fourth tile
+    regs_down<OTHER_REGS>();
     const int lw = warp - LOAD_WARP, piece = lane & 7;
+    const bool in_chunk = 16 * piece < chunk_bytes;
     int it = 0;
-    auto landed = [&](int i) {
-      fence_proxy_async_shared();
-      mbar_arrive(&full[i % ST]);
-    };
     for_items(a, plan, sh, team, [&](const Item& im) {
-      for (int i = 0; i < im.n; ++i, ++it) {
-        const int s = it % ST;
-        const int t = im.span.token(im.t0 + i) + 32 * lw + lane;
-        long long off = -1;
-        if (t <= im.span.hi && (t >= im.span.lo || t < a.sinks)) {
-          off = record_offset(a.kv, im.b, t);
-          if (off < 0) atomicOr(a.status, ST_UNMAPPED_PAGE);
-        }
-        const uint32_t ok = __ballot_sync(0xffffffffu, off >= 0);
-        if (it >= ST) warp_wait(&empty[s], ((it / ST) - 1) & 1, a.status, abort);
-        if (!stopped(abort)) {
-          uint8_t* st = sm + K_OFF + s * TT * 128;
+      for (int i = (lw - it) & 3; i < im.n; i += LOAD_WARPS) {
+        const int j = it + i, s = j % ST, t0 = im.span.token(im.t0 + i) + lane;
+        long long off[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int row = 4 * j + (lane >> 3);
-            const long long ro = __shfl_sync(0xffffffffu, off, row);
-            const bool in = ro >= 0 && 16 * piece < chunk_bytes;
-            cp_async16(st + (32 * lw + row) * 128 + ((piece ^ (row & 7)) << 4),
-                       a.kv.base + (in ? ro + 128 * chunk + 16 * piece : 0), in ? 16 : 0);
+        for (int q = 0; q < 4; ++q) {
+          const int t = t0 + 32 * q;
+          off[q] = -1;
+          if (t <= im.span.hi && (t >= im.span.lo || t < a.sinks)) {
+            off[q] = record_offset(a.kv, im.b, t);
+            if (off[q] < 0) atomicOr(a.status, ST_UNMAPPED_PAGE);
           }
-          cp_async4(sm + SC_OFF + (s * TT + 32 * lw + lane) * 4,
-                    a.kv.base + (off >= 0 ? off + a.kv_dim : 0), off >= 0 ? 4 : 0);
         }
-        if (lane == 0) valid[s][lw] = ok;
-        cp_async_commit();
-        if (it >= AHEAD - 1) {
-          cp_async_wait<AHEAD - 1>();
-          landed(it - (AHEAD - 1));
+        if (j >= ST) warp_wait(&ss.empty[s], ((j / ST) - 1) & 1, a.status, abort);
+        const bool go = !stopped(abort);
+        uint8_t* st = sm + K_OFF + s * TT * 128;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t ok = __ballot_sync(0xffffffffu, off[q] >= 0);
+          if (lane == 0) ss.valid[s][q] = ok;
+          if (go) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int row = 4 * e + (lane >> 3);
+              const long long ro = __shfl_sync(0xffffffffu, off[q], row);
+              const bool in = ro >= 0 && in_chunk;
+              cp_async16(st + (32 * q + row) * 128 + ((piece ^ (row & 7)) << 4),
+                         a.kv.base + (in ? ro + 128 * chunk + 16 * piece : 0), in ? 16 : 0);
+            }
+            cp_async4(sm + SC_OFF + (s * TT + 32 * q + lane) * 4,
+                      a.kv.base + (off[q] >= 0 ? off[q] + a.kv_dim : 0), off[q] >= 0 ? 4 : 0);
+          }
         }
+        cp_async_arrive_noinc(&ss.full[s]);
+        if (lane == 0) mbar_arrive(&ss.full[s]);
       }
+      it += im.n;
     });
-    cp_async_wait<0>();
-    for (int i = max(0, it - (AHEAD - 1)); i < it; ++i) landed(i);
+    cp_async_wait_all();
+  } else if (warp > MMA_WARP) {
+    regs_down<OTHER_REGS>();  // (idle: they complete the warpgroup)
   } else if (warp == MMA_WARP) {
     // -------------------------------------------------------------------------- MMA issue
+    regs_down<OTHER_REGS>();
     const uint32_t k0 = smem_u32(sm + K_OFF), p0 = smem_u32(sm + P_OFF), q0 = smem_u32(sm + Q_OFF);
     int it = 0, item = 0;
-    auto pv = [&](int i, int nqp, bool first) {  // tile i's second product
-      warp_wait(&p_full[i & 1], (i >> 1) & 1, a.status, abort);
+    // tile i's second product; first: O's first of the item
+    auto pv = [&](int i, int nqp, bool first) {
+      warp_wait(&ss.p_full[i & 1], (i >> 1) & 1, a.status, abort);
       if (!stopped(abort) && elect_one()) {
         tc_fence_after();
         const bool merged = nqp <= MERGE;
         const uint32_t ka = k0 + (i % ST) * TT * 128, pb = p0 + (i & 1) * P_BUF;
-        const uint8_t* img = sm + PIMG_OFF + (i & 1) * 2 * IMG;
-        tc_cp_img(tmem + SF_P, img);
-        if (!merged) tc_cp_img(tmem + SF_P + 4, img + IMG);
+        const uint32_t o = tmem + O_COL + (nqp <= ALT ? O_ALT * (i & 1) : 0);
+        tc_cp_img(tmem + SF_P, sm + PIMG_OFF + (i & 1) * IMG);
         const uint32_t idesc = IDESC | TRANS | ((uint32_t)((merged ? 2 * nqp : nqp) >> 3) << 17);
         for (int term = 0; term < (merged ? 1 : 2); ++term)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            tc_mma_mxf8(tmem + O_COL, desc_sw128(ka + 4096 * k),
-                        desc_sw128(pb + term * TT * 128 + 4096 * k),
+            tc_mma_mxf8(o, desc_sw128(ka + 4096 * k), desc_sw128(pb + term * TT * 128 + 4096 * k),
                         idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), tmem + SF_ONE,
-                        tmem + SF_P + 4 * term, !first || term > 0 || k > 0);
-        tc_commit(&empty[i % ST]);
-        tc_commit(&pv_done[i & 1]);
+                        tmem + SF_P, !first || term > 0 || k > 0);
+        tc_commit(&ss.empty[i % ST]);
+        tc_commit(&ss.pv_done[i & 1]);
       }
       __syncwarp();
     };
     if (elect_one()) tc_cp_img(tmem + SF_ONE, sm + ONE_OFF);
     __syncwarp();
     for_items(a, plan, sh, team, [&](const Item& im) {
-      warp_wait(&q_full, item & 1, a.status, abort);
-      const int nqp = s_rows;  // columns of the item, published before q_full
+      warp_wait(&ss.q_full, item & 1, a.status, abort);
+      const int nqp = ss.cols;
       ++item;
       const bool merged = nqp <= MERGE;
+      const int firsts = nqp <= ALT ? 2 : 1;
       const uint32_t idesc = IDESC | ((uint32_t)((merged ? 2 * nqp : nqp) >> 3) << 17);
       for (int i = 0; i < im.n; ++i) {
         const int j = it + i;
-        warp_wait(&full[j % ST], (j / ST) & 1, a.status, abort);
+        warp_wait(&ss.full[j % ST], (j / ST) & 1, a.status, abort);
         if (!stopped(abort) && elect_one()) {
+          fence_proxy_async_shared();  // the copies, seen to have landed, before the MMA's reads
           tc_fence_after();
           if (i == 0) tc_cp_img(tmem + SF_Q, sm + QIMG_OFF);
           const uint32_t ka = k0 + (j % ST) * TT * 128;
@@ -413,28 +647,27 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
                           desc_sw128(q0 + term * NQ * 128 + 32 * k),
                           idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), tmem + SF_ONE,
                           tmem + SF_Q, term > 0 || k > 0);
-          tc_commit(&s_full[j & 1]);
+          tc_commit(&ss.s_full[j & 1]);
         }
         __syncwarp();
-        if (i > 0) pv(j - 1, nqp, i == 1);
+        if (i > 0) pv(j - 1, nqp, i - 1 < firsts);
       }
-      pv(it + im.n - 1, nqp, im.n == 1);
+      pv(it + im.n - 1, nqp, im.n - 1 < firsts);
       it += im.n;
     });
     // after a wait that ran out: what was issued completes before TMEM is freed
     if (stopped(abort) && elect_one()) {
-      tc_commit(&drain);
-      (void)mbar_wait(&drain, 0, a.status, 100000000ull);
+      tc_commit(&ss.drain);
+      (void)mbar_wait(&ss.drain, 0, a.status, 100000000ull);
     }
     __syncwarp();
-  } else if (warp < SOFT_WARPS) {
+  } else {
     // ---------------------------------------------------------------------------- softmax
-    const int quad = warp & 3, half = warp >> 2, tok = 32 * quad + lane;
-    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    regs_up<SOFT_REGS>();
+    const int quad = warp & 3, half = warp >> 2;
     const int hpg = a.n_q / (a.kv_dim / a.head_dim);
     const int cheads = hpg * (chunk_bytes > a.head_dim ? 2 : 1);  // heads per row of this chunk
     const int dshift = a.head_dim == 64 ? 6 : 7;
-    const float to_log2 = a.scale * LOG2E;
     int it = 0;
     for_items(a, plan, sh, team, [&](const Item& im) {
       // ---- the group's rows and queries
@@ -447,24 +680,25 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
           const int p = r < a.rows && a.row_req[r] == im.b ? a.positions[r] : -1;
           const uint32_t m = __ballot_sync(0xffffffffu, p >= 0);
           const int rank = seen + __popc(m & ((1u << lane) - 1)) - first;
-          if (p >= 0 && rank >= 0 && rank < sh.rows_per) group_row[rank] = r, group_pos[rank] = p;
+          if (p >= 0 && rank >= 0 && rank < sh.rows_per)
+            ss.group_row[rank] = r, ss.group_pos[rank] = p;
           seen += __popc(m);
           n = max(0, min(sh.rows_per, seen - first));
         }
-        if (lane == 0) s_rows = ((n * cheads + 15) & ~15) | (n << 16);
+        if (lane == 0) ss.cols = ((n * cheads + 15) & ~15) | (n << 16);
       }
       bar_sync<256>(1);
-      const int nrows = s_rows >> 16, nqp = s_rows & 0xFFFF, nq = nrows * cheads;
-      const bool merged = nqp <= MERGE;
+      const int nrows = ss.cols >> 16, nqp = ss.cols & 0xFFFF, nq = nrows * cheads;
+      const bool merged = nqp <= MERGE, turns = nqp <= ALT;
       if (tid < NQ) {
         int hi = 0x7FFFFFFF, lo = 0;  // padding columns see everything
         if (tid < nq) {
-          hi = a.causal ? group_pos[tid / cheads] : im.span.hi;
+          hi = a.causal ? ss.group_pos[tid / cheads] : im.span.hi;
           lo = a.window > 0 ? max(0, hi - a.window + 1) : 0;
         }
-        col_hi[tid] = hi;
-        col_lo[tid] = lo;
-        neg_m[tid] = -UNSET;
+        ss.col_hi[tid] = hi;
+        ss.col_lo[tid] = lo;
+        ss.neg_m[0][tid] = ss.neg_m[1][tid] = -UNSET;
       }
       // queries as two e4m3 terms, rows of 128 bytes: hi in row c, lo in row nqp + c (merged)
       // or NQ + c
@@ -477,7 +711,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
         const bool in = c < nq && (d >> dshift) == sl;
         if (in)
           bf16x8_to_f32(*reinterpret_cast<const uint4*>(
-                            a.q + group_row[j] * a.q_stride +
+                            a.q + ss.group_row[j] * a.q_stride +
                             ((long long)chunk * sh.heads + h) * a.head_dim + (d - (sl << dshift))),
                         v);
         float m = 0.0f;
@@ -510,222 +744,102 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
         }
       }
       fence_proxy_async_shared();
-      bar_sync<256>(1);
-      if (tid == 0) s_rows = nqp;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&q_full);
-      int min_hi = 0x7FFFFFFF, max_lo = 0;
+      Soft w;
+      w.min_hi = 0x7FFFFFFF;
+      w.max_lo = 0;
       for (int j = 0; j < nrows; ++j) {
-        const int hi = a.causal ? group_pos[j] : im.span.hi;
-        min_hi = min(min_hi, hi);
-        max_lo = max(max_lo, a.window > 0 ? max(0, hi - a.window + 1) : 0);
+        const int hi = a.causal ? ss.group_pos[j] : im.span.hi;
+        w.min_hi = min(w.min_hi, hi);
+        w.max_lo = max(w.max_lo, a.window > 0 ? max(0, hi - a.window + 1) : 0);
       }
-
-      const int ng = nqp / 16;          // groups of 8 columns of this half
-      const int c0 = half * 8 * ng;     // its first column
-      float l[NQ / 2], s[NQ / 2];
-#pragma unroll
-      for (int c = 0; c < NQ / 2; ++c) l[c] = 0.0f;
-
-      for (int i = 0; i < im.n; ++i, ++it) {
-        const int st = it % ST, pb = it & 1;
-        const int t0 = im.span.token(im.t0 + i), t = t0 + tok;
-        warp_wait(&full[st], (it / ST) & 1, a.status, abort);
-        const float raw = reinterpret_cast<const float*>(sm + SC_OFF)[st * TT + tok];
-        const uint32_t ok = valid[st][quad];
-        const bool fin = fabsf(raw) <= 3.0e38f;
-        const float ct = fin ? raw * to_log2 : __int_as_float(0x7FC00000);
-        const float sc = fin ? raw : 0.0f;
-        // some of the tile's tokens are not every row's to see
-        const bool part = ok != 0xffffffffu || t0 + TT - 1 > min_hi ||
-                          (t0 < max_lo && t0 + TT > a.sinks);
-        warp_wait(&s_full[pb], (it >> 1) & 1, a.status, abort);
-        tc_fence_after();
-        const uint32_t scol = tmem + lanes + S_COL + 128 * pb + c0;
-        // scores in log2 units, masked ones -inf
-        auto load_scores = [&]() {
-#pragma unroll
-          for (int g = 0; g < NQ / 16; ++g)
-            if (g < ng) tc_ld8(scol + 8 * g, s + 8 * g);
-          tc_wait_ld();
-#pragma unroll
-          for (int g = 0; g < NQ / 16; ++g)
-            if (g < ng) tc_loaded(s + 8 * g);
-          if (merged) {
-#pragma unroll
-            for (int g = 0; g < MERGE / 16; ++g)
-              if (g < ng) {
-                float x[8];
-                tc_ld8(scol + nqp + 8 * g, x);
-                tc_wait_ld();
-                tc_loaded(x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) s[8 * g + e] += x[e];
-              }
-          }
-#pragma unroll
-          for (int c = 0; c < NQ / 2; ++c)
-            if (c < 8 * ng) s[c] *= ct;
-          if (part) {
-            const bool mapped = (ok >> lane) & 1;
-#pragma unroll
-            for (int c = 0; c < NQ / 2; ++c)
-              if (c < 8 * ng) {
-                const bool see = mapped && t <= col_hi[c0 + c] &&
-                                 (t >= col_lo[c0 + c] || t < a.sinks);
-                if (!see) s[c] = -INFINITY;
-              }
-          }
-        };
-        load_scores();
-        bool over = false;
-#pragma unroll
-        for (int c = 0; c < NQ / 2; ++c)
-          if (c < 8 * ng) over |= s[c] + neg_m[c0 + c] > JUMP;
-        if (bar_any(2 + half, over)) {
-          // m_q moves where a score passes it (always in an item's first tile)
-#pragma unroll
-          for (int c = 0; c < NQ / 2; ++c)
-            if (c < 8 * ng) {
-              const float m = warp_max_any(s[c] > -INFINITY ? s[c] : -INFINITY);
-              if (lane == 0) red[quad][c0 + c] = m;
-            }
-          bar_sync<128>(4 + half);
-          if (quad == 0)
-            for (int c = c0 + lane; c < c0 + 8 * ng; c += 32) {
-              const float m = fmaxf(fmaxf(red[0][c], red[1][c]), fmaxf(red[2][c], red[3][c]));
-              const float old = -neg_m[c];
-              float f = 1.0f;
-              if (m - old > JUMP) {
-                const float now = fminf(ceilf(m), 3.0e38f);
-                f = old == UNSET ? 0.0f : ex2(old - now);
-                neg_m[c] = -now;
-              }
-              fac[c] = f;
-            }
-          bar_sync<128>(4 + half);
-#pragma unroll
-          for (int c = 0; c < NQ / 2; ++c)
-            if (c < 8 * ng) l[c] *= fac[c0 + c];
-          if (i > 0) {
-            warp_wait(&pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1, a.status, abort);
-            tc_fence_after();
-            for (int term = 0; term < (merged ? 2 : 1); ++term)
-              for (int g = 0; g < ng; ++g) {
-                float x[8];
-                const uint32_t oc = tmem + lanes + O_COL + term * nqp + c0 + 8 * g;
-                tc_ld8(oc, x);
-                tc_wait_ld();
-                tc_loaded(x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= fac[c0 + 8 * g + e];
-                tc_st8(oc, x);
-              }
-            tc_wait_st();
-          }
-        }
-        if (it >= 2) warp_wait(&pv_done[pb], ((it >> 1) - 1) & 1, a.status, abort);
-        if (part && half == 0) {
-          // NaN codes of tokens that some row must not see would reach it as 0 * NaN
-          for (int j = 0; j < 8; ++j) {
-            uint32_t* w = reinterpret_cast<uint32_t*>(sm + K_OFF + st * TT * 128 + tok * 128 + 16 * j);
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t v = w[e], x = v & 0x7F7F7F7Fu;
-              const uint32_t nan = ((x + 0x01010101u) & 0x80808080u) >> 7;  // bytes equal to 0x7F
-              if (nan) w[e] = v & ~(nan * 0xFFu);
-            }
-          }
-        }
-        // weights: P scale_t under its block's scale, as two e4m3 terms
-        uint8_t* prow = sm + P_OFF + pb * P_BUF + tok * 128;
-        uint8_t* img = sm + PIMG_OFF + pb * 2 * IMG;
-#pragma unroll
-        for (int g = 0; g < NQ / 16; ++g)
-          if (g < ng) {
-            float w[8], mul[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int c = 8 * g + e;
-              const float p = ex2(s[c] + neg_m[c0 + c]);
-              l[c] += p;
-              w[e] = p * sc;
-            }
-            int mine = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t mx = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(w[e])));
-              const int code = max((int)(mx >> 23) - 7, 8);
-              mul[e] = __uint_as_float((uint32_t)(254 - code) << 23);
-              if (lane == e) mine = code;
-            }
-            if (lane < 8) {
-              const int n = c0 + 8 * g + lane;
-              img[(n & 31) * 16 + (n >> 5) * 4 + quad] = (uint8_t)mine;
-              const int nl = merged ? nqp + n : n;
-              (merged ? img : img + IMG)[(nl & 31) * 16 + (nl >> 5) * 4 + quad] = (uint8_t)(mine - 4);
-            }
-            uint32_t hb[4], lb[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              hilo_f16x2(f16x2_of(w[2 * e] * mul[2 * e], w[2 * e + 1] * mul[2 * e + 1]), hb[e], lb[e]);
-            const int ch = c0 + 8 * g, cl = merged ? nqp + ch : ch;
-            uint8_t* rl = merged ? prow : prow + TT * 128;
-            *reinterpret_cast<uint2*>(prow + (((ch >> 4) ^ (tok & 7)) << 4) + (ch & 15)) =
-                make_uint2(hb[0] | hb[1] << 16, hb[2] | hb[3] << 16);
-            *reinterpret_cast<uint2*>(rl + (((cl >> 4) ^ (tok & 7)) << 4) + (cl & 15)) =
-                make_uint2(lb[0] | lb[1] << 16, lb[2] | lb[3] << 16);
-          }
-        fence_proxy_async_shared();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[pb]);
+      bar_sync<256>(1);
+      if (tid == 0) ss.cols = nqp;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ss.q_full);
+      w.span = im.span;
+      w.t0 = im.t0;
+      w.n = im.n;
+      w.it = it;
+      w.nqp = nqp;
+      w.to_log2 = a.scale * LOG2E;
+      w.tmem = tmem + ((uint32_t)(32 * quad) << 16);
+      // the halves take turns with whole tiles (their own O and m each), or share the columns
+      w.stream = turns ? half : 0;
+      const int half0 = (nqp / 16 + 1) / 2 * 16;  // columns of half 0 where they share
+      w.c0 = turns || half == 0 ? 0 : half0;
+      const int cols = turns ? nqp : half == 0 ? half0 : nqp - half0;
+      float* lo = ss.red[warp];
+      if (turns) {
+        if (cols == 16) soft_tiles<16, true, true>(a, w, ss, sm, lo);
+        else if (cols == 32) soft_tiles<32, true, true>(a, w, ss, sm, lo);
+        else soft_tiles<48, true, true>(a, w, ss, sm, lo);
+      } else if (merged) {
+        soft_tiles<32, false, true>(a, w, ss, sm, lo);
+      } else if (cols == 32) {
+        soft_tiles<32, false, false>(a, w, ss, sm, lo);
+      } else {
+        soft_tiles<48, false, false>(a, w, ss, sm, lo);
       }
+      const int first_stream = it & 1;
+      it += im.n;
 
-      // ---- the item's result: sums over the tokens, then O
-#pragma unroll
-      for (int c = 0; c < NQ / 2; ++c)
-        if (c < 8 * ng) {
-          const float v = warp_sum(l[c]);
-          if (lane == 0) red[quad][c0 + c] = v;
-        }
-      const int last = it - 1;
-      warp_wait(&pv_done[last & 1], (last >> 1) & 1, a.status, abort);
+      // ---- the item's result
+      for (int i = max(it - 2, it - im.n); i < it; ++i)
+        warp_wait(&ss.pv_done[i & 1], (i >> 1) & 1, a.status, abort);
       tc_fence_after();
       bar_sync<256>(1);
       const bool whole = im.n == im.span.tiles;  // nobody else has tiles of this group
       float* pt = ar.part + ((size_t)(team * 2 + (im.t0 > 0 ? 0 : 1)) * sh.chunks + chunk) * NQ * PART_LD;
-      const int d = tok;  // this thread's dimension of the chunk
-      for (int g = 0; g < ng; ++g) {
-        float x[8];
-        tc_ld8(tmem + lanes + O_COL + c0 + 8 * g, x);
-        tc_wait_ld();
-        tc_loaded(x);
-        if (merged) {
-          float y[8];
-          tc_ld8(tmem + lanes + O_COL + nqp + c0 + 8 * g, y);
-          tc_wait_ld();
-          tc_loaded(y);
+      const int d = 32 * quad + lane;  // this thread's dimension of the chunk
+      for (int c8 = 8 * half; c8 < nqp; c8 += 16) {
+        float acc[8], m[8], lt[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] += y[e];
+        for (int e = 0; e < 8; ++e) acc[e] = lt[e] = 0.0f, m[e] = UNSET;
+        for (int k = 0; k < (turns ? 2 : 1); ++k) {
+          if (turns && im.n == 1 && k != first_stream) continue;  // a stream without a tile
+          float x[8];
+          const uint32_t oc = w.tmem + O_COL + O_ALT * k + c8;
+          tc_ld8(oc, x);
+          tc_wait_ld();
+          tc_loaded(x);
+          if (merged) {
+            float y[8];
+            tc_ld8(oc + nqp, y);
+            tc_wait_ld();
+            tc_loaded(y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += y[e];
+          }
+          const float(*r)[NQ] = ss.red + (turns ? 4 * k : c8 < half0 ? 0 : 4);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int c = c8 + e;
+            const float lk = (r[0][c] + r[1][c]) + (r[2][c] + r[3][c]);
+            const float mk = -ss.neg_m[k][c], mn = fmaxf(m[e], mk);
+            const float f0 = m[e] == UNSET ? 0.0f : ex2(m[e] - mn);
+            const float f1 = mk == UNSET && lk == 0.0f ? 0.0f : ex2(mk - mn);
+            acc[e] = acc[e] * f0 + (f1 == 0.0f ? 0.0f : x[e] * f1);
+            lt[e] = lt[e] * f0 + lk * f1;
+            m[e] = mn;
+          }
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int c = c0 + 8 * g + e;
+          const int c = c8 + e;
           if (c >= nq) continue;
           const int j = c / cheads, h = c - j * cheads, sl = h / hpg;
-          const float lt = (red[0][c] + red[1][c]) + (red[2][c] + red[3][c]);
           const long long head = (long long)chunk * sh.heads + h;
+          const bool mine = (d >> dshift) == sl;
           if (whole) {
-            const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
-            if ((d >> dshift) == sl)
-              a.o[group_row[j] * a.o_stride + head * a.head_dim + (d - (sl << dshift))] =
-                  __float2bfloat16_rn(lt == 0.0f ? 0.0f : x[e] * inv);
+            if (mine)
+              a.o[ss.group_row[j] * a.o_stride + head * a.head_dim + (d - (sl << dshift))] =
+                  __float2bfloat16_rn(lt[e] == 0.0f ? 0.0f : acc[e] / lt[e]);
             if (d == 0)
-              a.lse[(long long)group_row[j] * a.n_q + head] =
-                  lt == 0.0f ? -INFINITY : (log2f(lt) - neg_m[c]) * LN2;
+              a.lse[(long long)ss.group_row[j] * a.n_q + head] =
+                  lt[e] == 0.0f ? -INFINITY : (log2f(lt[e]) + m[e]) * LN2;
           } else {
-            if ((d >> dshift) == sl) pt[c * PART_LD + 4 + (d - (sl << dshift))] = x[e];
-            if (d == 0) pt[c * PART_LD] = -neg_m[c], pt[c * PART_LD + 1] = lt;
+            if (mine) pt[c * PART_LD + 4 + (d - (sl << dshift))] = acc[e];
+            if (d == 0) pt[c * PART_LD] = m[e], pt[c * PART_LD + 1] = lt[e];
           }
         }
       }
@@ -847,6 +961,11 @@ Layout layout(int max_rows, int sms) {
 size_t attend_workspace_bytes(int max_rows, int sms) { return layout(max_rows, sms).bytes; }
 
 cudaError_t attend_prepare() {
+  // the roles' register split adds up to what a block launches with: 128 a thread
+  cudaFuncAttributes f;
+  cudaError_t e = cudaFuncGetAttributes(&f, attend_kernel);
+  if (e == cudaSuccess && f.numRegs != 128) e = cudaErrorInvalidConfiguration;
+  if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
 }
 
