@@ -5,16 +5,18 @@
 //   P[t, q] = 2^(S log2e - m_q)                   O[d, q] = sum_t codes_t[d] scale_t P[t, q]
 //
 // A 128-byte run of a record (a chunk: one 128-wide latent slice, or two 64-wide ones) and 128
-// tokens make a tile, and both products take it as it lies in the cache: e4m3, 128 bytes a
-// token, is a K-major A operand of the first (M = tokens, K = dimensions) and, transposed, an
-// MN-major A operand of the second (M = dimensions, K = tokens).  So queries are the MMA's N:
-// the heads that share a latent slice, times the rows of a request that share its context (1 to
-// 96 columns, no padding beyond 16), and the cache is read once for all of them.
-// kind::mxf8f6f4 takes the other operand as e4m3 under one power-of-two scale per 32 K
-// elements.  A bf16 query is the exact sum of two such terms; P scale_t gets its scale per
-// (query, 32 tokens) from the largest of the 32, and two terms carry 8 bits of each and no
-// less than 2^-21 of that largest.  O stays in TMEM over a whole run of tiles: m_q, an
-// integer, moves only when a score passes it by 2^40 (then O is rescaled, exactly).
+// tokens make a tile.  Tokens are the M of the first product, dimensions that of the second, and
+// queries the N of both: the heads that share a latent slice, times the rows of a request that
+// share its context (1 to 96 columns, no padding beyond 16), so the cache is read once for all of
+// them.  The first product takes the e4m3 tile as it lies in the cache (kind::mxf8f6f4); a bf16
+// query is the exact sum of two e4m3 terms under one power-of-two scale per 32 dimensions.  The
+// second takes P scale_t in bf16 (the one rounding between the scores and o: 8 bits, as o
+// itself, of a weight of any size) and the tile widened to bf16: moving a code's bits into place
+// reads as 2^-120 of its value, which P's own factor makes up for.  (Weights as two e4m3 terms
+// under block scales would spare the widening, but cost each weight three times the
+// instructions: 270 us against 60 at 48 rows over 8 contexts of 1K..64K.)
+// O stays in TMEM over a whole run of tiles: m_q, an integer, moves only when a weight passes it
+// by far (then O is rescaled, exactly).
 //
 // Work: the tiles of all (request, group of rows) pairs in one line, cut evenly into as many
 // pieces as there are teams; a team is one CTA per chunk, so that the CTAs that read the same
@@ -23,10 +25,16 @@
 // the workspace, which a second kernel joins.
 //
 // Roles: warps 0-7 softmax (TMEM lane quadrant = warp % 4: one token per thread; warp / 4: half
-// of the columns), 8-11 loads (cp.async through the page table, any page size), 12 MMA issue.
+// of the columns), 8-11 widening, 12 the first product's MMAs, 13 the second's, 14 and 15 loads
+// (cp.async through the page table, any page size; every other tile each).  What runs once per launch or item is kept short,
+// in rolled loops: its instructions come from L2 or further away.
 // Every mbarrier wait is bounded; a wait that runs out is reported, and from then on every role
 // runs its loop without waiting, copying or issuing, so that the barriers among warps still
 // complete and TMEM is freed.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
 #include "cache_kernels.h"
 #include "tc_common.cuh"
 
@@ -37,45 +45,51 @@ using namespace tc;
 
 constexpr int TT = 128;        // tokens per tile
 constexpr int NQ = 96;         // query columns at most
-constexpr int MERGE = 64;      // up to here both terms are columns of one MMA
+constexpr int MERGE = 64;      // up to here both terms of the queries are columns of one MMA
 constexpr int GROUP = 16;      // rows of a group at most
-constexpr int ALT = 48;        // up to here the two softmax halves take turns with whole tiles
-constexpr int ST = 6;          // tiles in the ring
+constexpr int ST = 5;          // tiles in the ring
 constexpr int MAX_REQ = 1024;
 constexpr int THREADS = 16 * 32;
-constexpr int SOFT_WARPS = 8, LOAD_WARP = 8, LOAD_WARPS = 4, MMA_WARP = 12;
+constexpr int SOFT_WARPS = 8, WIDE_WARP = 8, WIDE_WARPS = 4, S_WARP = 12, O_WARP = 13;
+constexpr int LOAD_WARP = 14, LOAD_WARPS = 2;
 // registers a thread: softmax warps take what the others give up (in all, the launch's 128)
-constexpr int SOFT_REGS = 200, OTHER_REGS = 56;
-static_assert(SOFT_REGS * 256 + OTHER_REGS * 256 == 128 * THREADS, "register split");
-constexpr float JUMP = 40.0f;      // log2 of how far a weight may pass 1
+constexpr int SOFT_REGS = 168, WIDE_REGS = 96, MMA_REGS = 80;
+static_assert(SOFT_REGS * 256 + WIDE_REGS * 128 + MMA_REGS * 128 == 128 * THREADS, "register split");
+constexpr float JUMP = 24.0f;      // log2 of how far a weight may pass 1
 constexpr float UNSET = -1.0e30f;  // m_q of a query that has seen no token
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+// P carries 2^64 and the widened codes 2^-120: O is 2^-56 of its value, and a token's scale may
+// reach 2^39 beside a weight of 2^JUMP
+constexpr float P_UP = 18446744073709551616.0f, O_UP = 72057594037927936.0f;
 
+constexpr int K_TILE = TT * 128, V_TILE = 2 * K_TILE;
 constexpr int K_OFF = 0;
-constexpr int P_BUF = 2 * TT * 128;  // hi terms, then lo terms (merged: hi and lo in the first)
-constexpr int P_OFF = K_OFF + ST * TT * 128;
-constexpr int Q_OFF = P_OFF + 2 * P_BUF;  // hi rows, then lo rows
+constexpr int V_OFF = K_OFF + ST * K_TILE;  // widened tiles [2]: dimensions 0..63, then 64..127
+constexpr int P_OFF = V_OFF + 2 * V_TILE;   // weights: columns 0..63, then 64..95
+constexpr int Q_OFF = P_OFF + V_TILE;       // hi rows, then lo rows
 constexpr int IMG = 512;
-constexpr int PIMG_OFF = Q_OFF + 2 * NQ * 128;  // [2 buffers]
-constexpr int QIMG_OFF = PIMG_OFF + 2 * IMG;
+constexpr int QIMG_OFF = Q_OFF + 2 * NQ * 128;
 constexpr int ONE_OFF = QIMG_OFF + IMG;
 constexpr int SC_OFF = ONE_OFF + IMG;  // token scales [ST][128]
 constexpr int PLAN_OFF = SC_OFF + ST * TT * 4;
-constexpr int SMEM_BYTES = PLAN_OFF + (MAX_REQ + 1) * 8 + 2 * MAX_REQ * 4 + 1024;
-static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-static_assert(P_OFF % 1024 == 0 && Q_OFF % 1024 == 0 && (NQ * 128) % 1024 == 0, "swizzle atoms");
+constexpr int SMEM_BYTES = PLAN_OFF + (3 * MAX_REQ + 4) * 4 + 1024;
+static_assert(V_OFF % 1024 == 0 && P_OFF % 1024 == 0 && Q_OFF % 1024 == 0 && (NQ * 128) % 1024 == 0,
+              "swizzle atoms");
+static_assert(SOFT_WARPS * (NQ / 2) * 32 * 4 <= V_TILE + 2 * NQ * 128, "the sums' scratch");
 
 // TMEM columns
-constexpr int S_COL = 0, O_COL = 256, O_ALT = 96, SF_ONE = 480, SF_Q = 484, SF_P = 488;
-// Instruction descriptor of kind::mxf8f6f4: e4m3 x e4m3, E8M0 scales, M = 128; N, the scale-byte
-// selectors and the transposes are or-ed in.
-constexpr uint32_t IDESC = (1u << 23) | ((uint32_t)(TT >> 4) << 24);
-constexpr uint32_t TRANS = (1u << 15) | (1u << 16);
+constexpr int S_COL = 0, O_COL = 256, SF_ONE = 384, SF_Q = 388;
+// Instruction descriptors, M = 128; N, and the scale-byte selectors, are or-ed in.
+// kind::mxf8f6f4: e4m3 x e4m3, E8M0 scales, both K-major.
+constexpr uint32_t S_IDESC = (1u << 23) | ((uint32_t)(TT >> 4) << 24);
+// kind::f16: bf16 x bf16, f32 accumulators, both MN-major.
+constexpr uint32_t O_IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
+                             ((uint32_t)(TT >> 4) << 24);
 
 // The step as every CTA derives it: per request its rows' largest and smallest position, and
 // the units (tiles times row groups) of all requests before it.
 struct Plan {
-  long long* pre;  // [n_req + 1]
+  int* pre;  // [n_req + 1]
   int *pmax, *pmin;
 };
 
@@ -118,49 +132,63 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int pmax, int pmin)
   return s;
 }
 
+// The cut: W units over the teams, no team (of those that get any) more than one unit above
+// another.
+struct Cut {
+  int teams, each, more;  // team k starts at each * k + min(k, more)
+  __device__ Cut(int W, int n) : teams(min(n, W)) {
+    each = teams ? W / teams : 0;
+    more = W - each * teams;
+  }
+  __device__ int start(int k) const { return each * k + min(k, more); }
+  __device__ int size(int k) const { return k < teams ? each + (k < more ? 1 : 0) : 0; }
+  __device__ int team_of(int g) const {
+    const int big = (each + 1) * more;
+    return g < big ? g / (each + 1) : more + (g - big) / each;
+  }
+};
+
 // One piece of work of a team: tiles [t0, t0 + n) of a row group of a request.
 struct Item {
   int b, group, t0, n;
   Span span;
 };
 
-// The items of a team in order: fn(item) for each.
-template <class F>
-__device__ __forceinline__ void for_items(const AttendArgs& a, const Plan& p, const Shape& sh,
-                                          int team, F&& fn) {
-  const long long W = p.pre[a.n_req];
-  long long w = W * team / sh.teams;
-  const long long w1 = W * (team + 1) / sh.teams;
-  if (w >= w1) return;
-  int b = 0;
-  for (int step = MAX_REQ / 2; step > 0; step >>= 1)  // the last request that starts at or before w
-    if (b + step < a.n_req && p.pre[b + step] <= w) b += step;
-  while (w < w1) {
-    while (p.pre[b + 1] <= w) ++b;
-    Item it;
-    it.b = b;
-    it.span = span_of(a, p.pmax[b], p.pmin[b]);
-    const long long u = w - p.pre[b];
-    it.group = (int)(u / it.span.tiles);
-    it.t0 = (int)(u - (long long)it.group * it.span.tiles);
-    it.n = (int)min((long long)(it.span.tiles - it.t0), w1 - w);
-    fn(it);
-    w += it.n;
+// The items of a team in order, from the place that the plan found for its first unit.
+struct Items {
+  int b, group, t0, left;
+};
+__device__ __forceinline__ bool next_item(const AttendArgs& a, const Plan& p, Items& w, Item& it) {
+  if (w.left <= 0) return false;
+  it.b = w.b;
+  it.group = w.group;
+  it.t0 = w.t0;
+  it.span = span_of(a, p.pmax[w.b], p.pmin[w.b]);
+  it.n = min(it.span.tiles - w.t0, w.left);
+  w.left -= it.n;
+  w.t0 = 0;
+  ++w.group;
+  if (w.left > 0 && p.pre[w.b] + w.group * it.span.tiles >= p.pre[w.b + 1]) {
+    w.group = 0;
+    do ++w.b;
+    while (p.pre[w.b + 1] <= p.pre[w.b]);  // (units are left, so there is such a request)
   }
+  return true;
 }
 
 // Where row r's results are: its request's and group's units [g0, g0 + tiles) and its place in
 // the group; tiles 0: nothing to see.
 struct RowInfo {
-  long long g0;
-  int tiles, place;
+  int g0, tiles, place;
 };
 
 struct Args {
+  CUtensorMap map;  // the cache as [pages][tokens][kv_dim bytes], boxes of 128 bytes x box tokens
+  int box;          // 0: no map
   AttendArgs a;
   float* part;     // [teams][2 slots][chunks][NQ][128 + 2]: O, then m and l
   RowInfo* rows;   // [rows]
-  long long* total;  // units of the step
+  int* total;      // units of the step
 };
 constexpr int PART_LD = 128 + 4;
 
@@ -169,19 +197,28 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
+// Two f32 as bf16, the first in the low half.
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
   uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Two f16 values as e4m3 hi codes and the codes of what is left (a pair each).
-__device__ __forceinline__ void hilo_f16x2(uint32_t x, uint32_t& hi, uint32_t& lo) {
-  asm("{\n .reg .b16 h, l;\n .reg .b32 f, r;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n cvt.rn.f16x2.e4m3x2 f, h;\n"
-      " sub.rn.f16x2 r, %2, f;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 l, r;\n cvt.u32.u16 %0, h;\n cvt.u32.u16 %1, l;\n}"
-      : "=r"(hi), "=r"(lo)
-      : "r"(x));
+// Two e4m3 codes, in the high bytes of the halves of u, as bf16 numbers of 2^-120 of their value
+// (sign, four exponent and three mantissa bits moved into place; a NaN code reads as 480).
+__device__ __forceinline__ uint32_t widen(uint32_t u) {
+  return (u & 0x80008000u) | ((u >> 4) & 0x07F007F0u);
+}
+// Matrix descriptor as desc_sw128, MN-major with `lbo` bytes between 128-byte runs along MN.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
+  return (desc_sw128(saddr) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(lbo >> 4) << 16);
+}
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
 }
 template <int REGS>
 __device__ __forceinline__ void regs_up() {
@@ -220,86 +257,102 @@ __device__ __forceinline__ float warp_max_any(float v) {
 }
 
 struct Shared {
-  uint64_t full[ST], empty[ST], s_full[2], p_full[2], pv_done[2], q_full, drain;
-  float neg_m[2][NQ], fac[2][NQ], red[SOFT_WARPS][NQ];  // [stream] (one unless the halves take turns)
-  uint32_t tmem, valid[ST][4];
-  int col_hi[NQ], col_lo[NQ], group_row[GROUP], group_pos[GROUP];
+  uint64_t full[ST], k_free[ST], s_full[2], p_full[2], v_full[2], pv_done[2], q_full, drain;
+  float neg_m[NQ], fac[NQ], red[SOFT_WARPS][NQ];
+  uint32_t valid[ST][4];
+  long long out[NQ];  // where a column's first value goes: o or the workspace
+  int slice[NQ], group_row[GROUP], group_pos[GROUP];
+  uint32_t tmem;
   int cols, abort;
-  long long warp_tot[THREADS / 32];
+  Items start;
 };
+
+static_assert(SMEM_BYTES + sizeof(Shared) <= 227 * 1024, "shared memory");
 
 // What a softmax warp knows of its item.
 struct Soft {
   Span span;
   int t0, n, it;        // the item's first tile and tile count, the ring's next tile
-  int nqp, c0, stream;  // columns of the item, this half's first one, its (O, m) set
+  int nqp, c0;          // columns of the item, this half's first one
+  int nrows, cheads;    // its rows and the heads (columns) of each
   int min_hi, max_lo;   // tokens that every row sees: [max_lo, min_hi] and the sinks
   float to_log2;
   uint32_t tmem;        // with the warp's lane quadrant
 };
 
-// The softmax of C columns over an item's tiles (TURNS: every other one), a token per thread.
-// l: this thread's share of the columns' sums, in units of 2^m.
-template <int C, bool TURNS, bool MERGED>
-__device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, Shared& sh, uint8_t* sm,
-                                           float* l_out) {
+// The softmax of a half's C columns over an item's tiles, a token per thread; leaves the
+// thread's share of every column's sum, in units of 2^m, in the scratch.
+template <int C>
+__device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, Shared& sh,
+                                           uint8_t* sm) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, half = warp >> 2, tok = 32 * quad + lane;
+  const bool merged = w.nqp <= MERGE;
   volatile int* abort = &sh.abort;
-  float* neg_m = sh.neg_m[w.stream];
-  float* fac = sh.fac[w.stream];
   float l[C], s[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) l[c] = 0.0f;
-  const int first = TURNS ? (half ^ (w.it & 1)) : 0, stride = TURNS ? 2 : 1;
-  for (int i = first; i < w.n; i += stride) {
-    const int it = w.it + i, st = it % ST, pb = it & 1;
+#pragma unroll 1
+  for (int i = 0; i < w.n; ++i) {
+    const int it = w.it + i, st = it % ST, b = it & 1;
+    const uint32_t ph = (it >> 1) & 1;
     const int t0 = w.span.token(w.t0 + i), t = t0 + tok;
     warp_wait(&sh.full[st], (it / ST) & 1, a.status, abort);
     const float raw = reinterpret_cast<const float*>(sm + SC_OFF)[st * TT + tok];
     const uint32_t ok = sh.valid[st][quad];
     const bool fin = fabsf(raw) <= 3.0e38f;
     const float ct = fin ? raw * w.to_log2 : __int_as_float(0x7FC00000);
-    const float sc = fin ? raw : 0.0f;
+    const float sc = fin ? raw * P_UP : 0.0f;
     // some of the tile's tokens are not every row's to see
     const bool part = __any_sync(0xffffffffu, ok != 0xffffffffu || t0 + TT - 1 > w.min_hi ||
                                                   (t0 < w.max_lo && t0 + TT > a.sinks));
-    // a weight says nothing of a token of next to no scale
-    const bool faint = __any_sync(0xffffffffu, !(sc > 1.0e-12f));
-    warp_wait(&sh.s_full[pb], (it >> 1) & 1, a.status, abort);
-    tc_fence_after();
-    const uint32_t scol = w.tmem + S_COL + 128 * pb + w.c0;
-    auto load = [&]() {  // the products of the tile
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.k_free[st]);
+    uint32_t see[(C + 31) / 32];
+    if (part) {  // this half's columns that see the token
+#pragma unroll
+      for (int k = 0; k < (C + 31) / 32; ++k) see[k] = 0xffffffffu;
+#pragma unroll 1
+      for (int j = 0; j < w.nrows; ++j) {
+        const int hi = a.causal ? sh.group_pos[j] : w.span.hi;
+        const int lo = a.window > 0 ? max(0, hi - a.window + 1) : 0;
+        if (((ok >> lane) & 1) && t <= hi && (t >= lo || t < a.sinks)) continue;
+        // columns [c, c + cheads) of the item, from this half's first on
+        const int c = j * w.cheads - w.c0, e = c + w.cheads;
+#pragma unroll
+        for (int k = 0; k < (C + 31) / 32; ++k) {
+          const int x = min(max(c - 32 * k, 0), 32), y = min(max(e - 32 * k, 0), 32);
+          const uint32_t below_y = y == 32 ? 0xffffffffu : (1u << y) - 1;
+          const uint32_t below_x = x == 32 ? 0xffffffffu : (1u << x) - 1;
+          see[k] &= ~(below_y & ~below_x);
+        }
+      }
+    }
+    warp_wait(&sh.s_full[b], ph, a.status, abort);
+    const uint32_t scol = w.tmem + S_COL + 128 * b + w.c0;
+    // weights; a second round where some query's m has to move (always in an item's first tile)
+#pragma unroll 1
+    for (bool moved = false;; moved = true) {
+      tc_fence_after();
 #pragma unroll
       for (int g = 0; g < C; g += 8) tc_ld8(scol + g, s + g);
-      if (MERGED) {
+      if (merged) {
 #pragma unroll
-        for (int g = 0; g < C; g += 16) {
-          float x[16];
+        for (int g = 0; g < C; g += 8) {
+          float x[8];
           tc_ld8(scol + w.nqp + g, x);
-          tc_ld8(scol + w.nqp + g + 8, x + 8);
           tc_wait_ld();
           tc_loaded(x);
-          tc_loaded(x + 8);
-          if (g == 0)
+          tc_loaded(s + g);
 #pragma unroll
-            for (int k = 0; k < C; k += 8) tc_loaded(s + k);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) s[g + e] += x[e];
+          for (int e = 0; e < 8; ++e) s[g + e] += x[e];
         }
       } else {
         tc_wait_ld();
 #pragma unroll
         for (int g = 0; g < C; g += 8) tc_loaded(s + g);
       }
-    };
-    auto mask = [&](float v, int c) {
-      const bool see = ((ok >> lane) & 1) && t <= sh.col_hi[w.c0 + c] &&
-                       (t >= sh.col_lo[w.c0 + c] || t < a.sinks);
-      return see ? v : -INFINITY;
-    };
-    auto weigh = [&]() {  // s: products -> 2^(score - m)
-      const float4* nm = reinterpret_cast<const float4*>(neg_m + w.c0);
+      const float4* nm = reinterpret_cast<const float4*>(sh.neg_m + w.c0);
 #pragma unroll
       for (int c = 0; c < C; c += 4) {
         const float4 m = nm[c / 4];
@@ -310,142 +363,98 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, S
       }
       if (part) {
 #pragma unroll
-        for (int c = 0; c < C; ++c) s[c] = mask(s[c], c);
+        for (int c = 0; c < C; ++c)
+          if (!((see[c / 32] >> (c % 32)) & 1)) s[c] = -INFINITY;
       }
+      float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < C; ++c) s[c] = ex2(s[c]);
-    };
-    uint32_t mx[C];  // exponent bits of the block's largest weight times scale
-    uint32_t top = 0;
-    auto blocks = [&]() {
-      top = 0;
+      for (int c = 0; c < C; ++c) top = fmaxf(top, s[c]);
+      if (!bar_any(2 + half, !moved && top > JUMP)) break;
+      // the columns' largest scores of the tile
+#pragma unroll 1
+      for (int g = 0; g < C; g += 8) {
+        const uint32_t bits = (g >= 32 ? see[(C - 1) / 32] : see[0]) >> (g & 31);
+        float x[8], y[8];
+        tc_ld8(scol + g, x);
+        if (merged) tc_ld8(scol + w.nqp + g, y);
+        tc_wait_ld();
+        tc_loaded(x);
+        if (merged) tc_loaded(y);
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        mx[c] = __reduce_max_sync(0xffffffffu, __float_as_uint(s[c] * sc));
-        top = max(top, mx[c]);
-      }
-    };
-    load();
-    weigh();
-    blocks();
-    bool over = top >= (uint32_t)(127 + (int)JUMP) << 23;
-    if (faint) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) over |= s[c] > exp2f(JUMP);
-    }
-    if (bar_any(2 + half, over)) {
-      // m moves where a weight passes 2^(JUMP / 2) (always in an item's first tile)
-      load();
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        float v = s[c] * ct;
-        if (part) v = mask(v, c);
-        const float m = warp_max_any(v > -INFINITY ? v : -INFINITY);
-        if (lane == 0) sh.red[warp][w.c0 + c] = m;
+        for (int e = 0; e < 8; ++e) {
+          float v = (merged ? x[e] + y[e] : x[e]) * ct;
+          if (!(v > -INFINITY) || (part && !((bits >> e) & 1))) v = -INFINITY;
+          const float m = warp_max_any(v);
+          if (lane == 0) sh.red[warp][w.c0 + g + e] = m;
+        }
       }
       bar_sync<128>(4 + half);
       if (quad == 0)
+#pragma unroll 1
         for (int c = w.c0 + lane; c < w.c0 + C; c += 32) {
           const float(*r)[NQ] = sh.red + 4 * half;
           const float m = fmaxf(fmaxf(r[0][c], r[1][c]), fmaxf(r[2][c], r[3][c]));
-          const float old = -neg_m[c];
+          const float old = -sh.neg_m[c];
           float f = 1.0f;
           if (m - old > 0.5f * JUMP) {
             const float now = fminf(ceilf(m), 3.0e38f);
             f = old == UNSET ? 0.0f : ex2(old - now);
-            neg_m[c] = -now;
+            sh.neg_m[c] = -now;
           }
-          fac[c] = f;
+          sh.fac[c] = f;
         }
       bar_sync<128>(4 + half);
 #pragma unroll
-      for (int c = 0; c < C; ++c) l[c] *= fac[w.c0 + c];
-      if (i > first) {
-        const int prev = it - stride;  // its product is in O
-        warp_wait(&sh.pv_done[prev & 1], (prev >> 1) & 1, a.status, abort);
+      for (int c = 0; c < C; ++c) l[c] *= sh.fac[w.c0 + c];
+      if (i > 0) {
+        warp_wait(&sh.pv_done[b ^ 1], ((it - 1) >> 1) & 1, a.status, abort);
         tc_fence_after();
-        for (int term = 0; term < (MERGED ? 2 : 1); ++term)
-          for (int g = 0; g < C; g += 8) {
-            float x[8];
-            const uint32_t oc = w.tmem + O_COL + O_ALT * w.stream + term * w.nqp + w.c0 + g;
-            tc_ld8(oc, x);
-            tc_wait_ld();
-            tc_loaded(x);
+#pragma unroll 1
+        for (int g = 0; g < C; g += 8) {
+          float x[8];
+          const uint32_t oc = w.tmem + O_COL + w.c0 + g;
+          tc_ld8(oc, x);
+          tc_wait_ld();
+          tc_loaded(x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= fac[w.c0 + g + e];
-            tc_st8(oc, x);
-          }
+          for (int e = 0; e < 8; ++e) x[e] *= sh.fac[w.c0 + g + e];
+          tc_st8(oc, x);
+        }
         tc_wait_st();
       }
-      load();
-      weigh();
-      blocks();
     }
-    if (it >= 2) warp_wait(&sh.pv_done[pb], ((it >> 1) - 1) & 1, a.status, abort);
-    if (part && (TURNS || half == 0)) {
-      // NaN codes of tokens that some row must not see would reach it as 0 * NaN
-      uint32_t* k = reinterpret_cast<uint32_t*>(sm + K_OFF + st * TT * 128 + tok * 128);
-#pragma unroll 1
-      for (int e = 0; e < 32; ++e) {
-        const int j = (e + 4 * lane) & 31;
-        const uint32_t v = k[j];
-        const uint32_t nan = (((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
-        if (nan) k[j] = v & ~(nan * 0xFFu);
-      }
-    }
-    // weights times scales under their blocks' scales, as two e4m3 terms
-    uint8_t* prow = sm + P_OFF + pb * P_BUF + tok * 128;
-    uint8_t* img = sm + PIMG_OFF + pb * IMG;
+    // weights times scales, rows of 128 bytes per token; the buffer's last reader has finished
+    if (it > 0) warp_wait(&sh.pv_done[b ^ 1], ((it - 1) >> 1) & 1, a.status, abort);
 #pragma unroll
-    for (int g = 0; g < C; g += 16) {
-      uint32_t hi[4], lo[4];
-      uint32_t mine = 0;
+    for (int g = 0; g < C; g += 8) {
+      uint32_t o[4];
 #pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        float y[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int c = g + e + k;
-          // the block's largest in [2^7, 2^8); exponents 15..254
-          const uint32_t mb = min(max(mx[c] & 0x7F800000u, 15u << 23), 254u << 23);
-          if (lane == e + k) mine = mb;
-          l[c] += s[c];
-          y[k] = s[c] * sc * __uint_as_float((261u << 23) - mb);
-        }
-        uint32_t h, r;
-        hilo_f16x2(f16x2_of(y[0], y[1]), h, r);
-        if (e & 2) {
-          hi[e >> 2] |= h << 16;
-          lo[e >> 2] |= r << 16;
-        } else {
-          hi[e >> 2] = h;
-          lo[e >> 2] = r;
-        }
+      for (int e = 0; e < 8; e += 2) {
+        const float p0 = ex2(s[g + e]), p1 = ex2(s[g + e + 1]);
+        l[g + e] += p0;
+        l[g + e + 1] += p1;
+        o[e / 2] = bf16x2_of(p0 * sc, p1 * sc);
       }
-      if (lane < 16) {
-        const int n = w.c0 + g + lane, nl = w.nqp + n;
-        const uint8_t code = (uint8_t)((mine >> 23) - 7);
-        img[(n & 31) * 16 + (n >> 5) * 4 + quad] = code;
-        if (MERGED) img[(nl & 31) * 16 + (nl >> 5) * 4 + quad] = code;
-      }
-      const int ch = (w.c0 + g) >> 4, cl = MERGED ? (w.nqp + w.c0 + g) >> 4 : ch;
-      *reinterpret_cast<uint4*>(prow + ((ch ^ (tok & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(prow + (MERGED ? 0 : TT * 128) + ((cl ^ (tok & 7)) << 4)) =
-          make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      const int col = w.c0 + g;
+      *reinterpret_cast<uint4*>(sm + P_OFF + (col >> 6) * K_TILE + tok * 128 +
+                                ((((col & 63) >> 3) ^ (tok & 7)) << 4)) =
+          make_uint4(o[0], o[1], o[2], o[3]);
     }
     fence_proxy_async_shared();
     tc_fence_before();
     __syncwarp();
-    if (lane < (TURNS ? 2 : 1)) mbar_arrive(&sh.p_full[pb]);  // eight arrivals a tile either way
+    if (lane == 0) mbar_arrive(&sh.p_full[b]);
   }
+  // every product of the item is done: the weights' and the queries' buffers are scratch
+  const int last = w.it + w.n - 1;
+  warp_wait(&sh.pv_done[last & 1], (last >> 1) & 1, a.status, abort);
+  tc_fence_after();
+  float* scratch = reinterpret_cast<float*>(sm + P_OFF) + warp * (NQ / 2) * 32 + lane;
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const float v = warp_sum(l[c]);
-    if (lane == 0) l_out[w.c0 + c] = v;
-  }
+  for (int c = 0; c < C; ++c) scratch[32 * c] = l[c];
 }
 
-__global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
+__global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constant__ Args ar) {
   const AttendArgs& a = ar.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -453,8 +462,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
   __shared__ __align__(16) Shared ss;
   volatile int* abort = &ss.abort;
   Plan plan;
-  plan.pre = reinterpret_cast<long long*>(sm + PLAN_OFF);
-  plan.pmax = reinterpret_cast<int*>(plan.pre + MAX_REQ + 1);
+  plan.pre = reinterpret_cast<int*>(sm + PLAN_OFF);
+  plan.pmax = plan.pre + MAX_REQ + 4;
   plan.pmin = plan.pmax + MAX_REQ;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Shape sh = shape_of(a, gridDim.x);
@@ -462,30 +471,34 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
   const int chunk_bytes = min(128, a.kv_dim - 128 * chunk);
 
   if (tid == 0) {
-    // a tile lands with its copies (the loading warp's lanes) and its mask (lane 0)
-    for (int s = 0; s < ST; ++s) mbar_init(&ss.full[s], 33), mbar_init(&ss.empty[s], 1);
-    for (int s = 0; s < 2; ++s)
-      mbar_init(&ss.s_full[s], 1), mbar_init(&ss.p_full[s], SOFT_WARPS), mbar_init(&ss.pv_done[s], 1);
+    // a tile lands with its copies (the loading warp's lanes) and its masks (lane 0); it is
+    // free when the first product, the widening and the softmax warps have read it
+    for (int s = 0; s < ST; ++s)
+      mbar_init(&ss.full[s], 33), mbar_init(&ss.k_free[s], 1 + WIDE_WARPS + SOFT_WARPS);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ss.s_full[s], 1), mbar_init(&ss.pv_done[s], 1);
+      mbar_init(&ss.p_full[s], SOFT_WARPS), mbar_init(&ss.v_full[s], WIDE_WARPS);
+    }
     mbar_init(&ss.q_full, SOFT_WARPS);
-    mbar_init(&ss.drain, 1);
+    mbar_init(&ss.drain, 2);
     ss.abort = 0;
+    fence_mbar_init();
   }
-  if (warp == MMA_WARP) tmem_alloc<512>(&ss.tmem);
-  for (int i = tid; i < IMG / 4; i += THREADS)
-    reinterpret_cast<uint32_t*>(sm + ONE_OFF)[i] = 0x7F7F7F7Fu;
-  for (int i = tid; i < 3 * IMG / 4; i += THREADS)
-    reinterpret_cast<uint32_t*>(sm + PIMG_OFF)[i] = 0x7F7F7F7Fu;
+  if (warp == S_WARP) tmem_alloc<512>(&ss.tmem);
+  if (tid < 2 * IMG / 4) reinterpret_cast<uint32_t*>(sm + QIMG_OFF)[tid] = 0x7F7F7F7Fu;
   fence_proxy_async_shared();
 
   // ---------------------------------------------------------------------------- the cut
+#pragma unroll 1
   for (int b = tid; b < a.n_req; b += THREADS) {
     plan.pmax[b] = -1;
     plan.pmin[b] = 0x7FFFFFFF;
-    reinterpret_cast<int*>(&plan.pre[b + 1])[0] = 0;  // rows so far
+    plan.pre[b + 1] = 0;  // rows so far
   }
   pdl_trigger();
   pdl_wait();
   __syncthreads();
+#pragma unroll 1
   for (int r = tid; r < a.rows; r += THREADS) {
     const int p = a.positions[r], b = a.row_req[r];
     if (p < 0) continue;
@@ -495,171 +508,275 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
     }
     atomicMax(&plan.pmax[b], p);
     atomicMin(&plan.pmin[b], p);
-    atomicAdd(reinterpret_cast<int*>(&plan.pre[b + 1]), 1);
+    atomicAdd(&plan.pre[b + 1], 1);
   }
   __syncthreads();
-  long long base = 0;
-  for (int b0 = 0; b0 < a.n_req; b0 += THREADS) {
-    const int b = b0 + tid;
-    long long u = 0;
-    if (b < a.n_req) {
-      const int n = reinterpret_cast<int*>(&plan.pre[b + 1])[0];
+  if (warp == 0) {
+    int W = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.n_req; b0 += 32) {
+      const int b = b0 + lane;
+      const int n = b < a.n_req ? plan.pre[b + 1] : 0;
+      int u = 0;
       if (n > 0) {
-        u = (long long)((n + sh.rows_per - 1) / sh.rows_per) *
-            span_of(a, plan.pmax[b], plan.pmin[b]).tiles;
+        u = (n + sh.rows_per - 1) / sh.rows_per * span_of(a, plan.pmax[b], plan.pmin[b]).tiles;
         if (plan.pmax[b] >= (long long)a.kv.max_blocks * a.kv.block_size && blockIdx.x == 0)
           atomicOr(a.status, ST_UNMAPPED_PAGE);
       }
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, u, o);
+        if (lane >= o) u += y;
+      }
+      if (b < a.n_req) plan.pre[b + 1] = W + u;
+      W += __shfl_sync(0xffffffffu, u, 31);
     }
-    long long x = u;
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+    __syncwarp();
+    if (lane == 0) {  // the team's first unit
+      plan.pre[0] = 0;
+      const Cut cut(W, sh.teams);
+      const int w0 = cut.start(team);
+      Items w = {0, 0, 0, team < sh.teams ? cut.size(team) : 0};
+      if (w.left > 0) {
+        int hi = a.n_req;  // the last request that starts by w0
+#pragma unroll 1
+        while (hi - w.b > 1) {
+          const int mid = (w.b + hi) >> 1;
+          if (plan.pre[mid] <= w0) w.b = mid; else hi = mid;
+        }
+        const int u = w0 - (w.b ? plan.pre[w.b] : 0);
+        const int tiles = span_of(a, plan.pmax[w.b], plan.pmin[w.b]).tiles;
+        w.group = u / tiles;
+        w.t0 = u - w.group * tiles;
+      }
+      ss.start = w;
+      if (blockIdx.x == 0) *ar.total = W;
     }
-    if (lane == 31) ss.warp_tot[warp] = x;
-    __syncthreads();
-    long long before = base;
-    for (int i = 0; i < THREADS / 32; ++i) {
-      if (i < warp) before += ss.warp_tot[i];
-      base += ss.warp_tot[i];
-    }
-    if (b < a.n_req) plan.pre[b + 1] = before + x;
-    __syncthreads();
   }
-  if (tid == 0) plan.pre[0] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ss.tmem;
+  Items items = ss.start;
+  Item im;
 
-  // where the second kernel finds the rows' results
-  if (blockIdx.x == 0 && tid == 0) *ar.total = plan.pre[a.n_req];
-  for (int r = blockIdx.x + gridDim.x * warp; r < a.rows; r += gridDim.x * (THREADS / 32)) {
-    const int b = a.row_req[r];
-    RowInfo info = {0, 0, 0};
-    if (a.positions[r] >= 0 && b >= 0 && b < a.n_req) {
-      int rank = 0;
-      for (int i = lane; i < r; i += 32) rank += a.row_req[i] == b && a.positions[i] >= 0;
-      rank = __reduce_add_sync(0xffffffffu, rank);
-      const Span s = span_of(a, plan.pmax[b], plan.pmin[b]);
-      const int group = rank / sh.rows_per;
-      info = {plan.pre[b] + (long long)group * s.tiles, s.tiles, rank - group * sh.rows_per};
-    }
-    if (lane == 0) ar.rows[r] = info;
-  }
-
-  if (team >= sh.teams) {
-    // no team: nothing to do
-  } else if (warp >= LOAD_WARP && warp < LOAD_WARP + LOAD_WARPS) {
-    // --------------------------------------------------- loads: a warp takes every fourth tile
-    regs_down<OTHER_REGS>();
-    const int lw = warp - LOAD_WARP, piece = lane & 7;
+  if (warp >= LOAD_WARP) {
+    // ------------------------------------------------------- loads: a warp takes every other tile
+    regs_down<MMA_REGS>();
+    const int piece = lane & 7, r4 = lane >> 3;
     const bool in_chunk = 16 * piece < chunk_bytes;
-    int it = 0;
-    for_items(a, plan, sh, team, [&](const Item& im) {
-      for (int i = (lw - it) & 3; i < im.n; i += LOAD_WARPS) {
-        const int j = it + i, s = j % ST, t0 = im.span.token(im.t0 + i) + lane;
-        long long off[4];
+    const long long piece_off = 128 * chunk + 16 * piece;
+    int ni = warp - LOAD_WARP;
+    bool more = next_item(a, plan, items, im);
+    // this warp's next tile: its tokens' pages are on their way while the one before is loaded
+    int page[4], slot[4];
+    auto locate = [&]() {
+#pragma unroll 1
+      while (more && ni >= im.n) ni -= im.n, more = next_item(a, plan, items, im);
+      if (!more) return;
+      const int t0 = im.span.token(im.t0 + ni) + lane;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int t = t0 + 32 * q;
-          off[q] = -1;
-          if (t <= im.span.hi && (t >= im.span.lo || t < a.sinks)) {
-            off[q] = record_offset(a.kv, im.b, t);
-            if (off[q] < 0) atomicOr(a.status, ST_UNMAPPED_PAGE);
-          }
+      for (int q = 0; q < 4; ++q) {
+        const int t = t0 + 32 * q, lb = t / a.kv.block_size;
+        page[q] = -1;
+        slot[q] = -1;
+        if (t <= im.span.hi && (t >= im.span.lo || t < a.sinks)) {
+          slot[q] = t - lb * a.kv.block_size;
+          if (lb < a.kv.max_blocks) page[q] = __ldg(a.kv.table + (size_t)im.b * a.kv.max_blocks + lb);
         }
-        if (j >= ST) warp_wait(&ss.empty[s], ((j / ST) - 1) & 1, a.status, abort);
-        const bool go = !stopped(abort);
-        uint8_t* st = sm + K_OFF + s * TT * 128;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t ok = __ballot_sync(0xffffffffu, off[q] >= 0);
-          if (lane == 0) ss.valid[s][q] = ok;
-          if (go) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int row = 4 * e + (lane >> 3);
-              const long long ro = __shfl_sync(0xffffffffu, off[q], row);
-              const bool in = ro >= 0 && in_chunk;
-              cp_async16(st + (32 * q + row) * 128 + ((piece ^ (row & 7)) << 4),
-                         a.kv.base + (in ? ro + 128 * chunk + 16 * piece : 0), in ? 16 : 0);
-            }
-            cp_async4(sm + SC_OFF + (s * TT + 32 * q + lane) * 4,
-                      a.kv.base + (off[q] >= 0 ? off[q] + a.kv_dim : 0), off[q] >= 0 ? 4 : 0);
-          }
-        }
-        cp_async_arrive_noinc(&ss.full[s]);
-        if (lane == 0) mbar_arrive(&ss.full[s]);
       }
-      it += im.n;
-    });
-    cp_async_wait_all();
-  } else if (warp > MMA_WARP) {
-    regs_down<OTHER_REGS>();  // (idle: they complete the warpgroup)
-  } else if (warp == MMA_WARP) {
-    // -------------------------------------------------------------------------- MMA issue
-    regs_down<OTHER_REGS>();
-    const uint32_t k0 = smem_u32(sm + K_OFF), p0 = smem_u32(sm + P_OFF), q0 = smem_u32(sm + Q_OFF);
-    int it = 0, item = 0;
-    // tile i's second product; first: O's first of the item
-    auto pv = [&](int i, int nqp, bool first) {
-      warp_wait(&ss.p_full[i & 1], (i >> 1) & 1, a.status, abort);
-      if (!stopped(abort) && elect_one()) {
-        tc_fence_after();
-        const bool merged = nqp <= MERGE;
-        const uint32_t ka = k0 + (i % ST) * TT * 128, pb = p0 + (i & 1) * P_BUF;
-        const uint32_t o = tmem + O_COL + (nqp <= ALT ? O_ALT * (i & 1) : 0);
-        tc_cp_img(tmem + SF_P, sm + PIMG_OFF + (i & 1) * IMG);
-        const uint32_t idesc = IDESC | TRANS | ((uint32_t)((merged ? 2 * nqp : nqp) >> 3) << 17);
-        for (int term = 0; term < (merged ? 1 : 2); ++term)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_mxf8(o, desc_sw128(ka + 4096 * k), desc_sw128(pb + term * TT * 128 + 4096 * k),
-                        idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), tmem + SF_ONE,
-                        tmem + SF_P, !first || term > 0 || k > 0);
-        tc_commit(&ss.empty[i % ST]);
-        tc_commit(&ss.pv_done[i & 1]);
-      }
-      __syncwarp();
     };
+    locate();
+    const int box = ar.box, boxes = box ? TT / box : 0;
+#pragma unroll 1
+    for (int it = warp - LOAD_WARP; more; it += LOAD_WARPS) {
+      const int s = it % ST;
+      if (it >= ST) warp_wait(&ss.k_free[s], ((it / ST) - 1) & 1, a.status, abort);
+      const bool go = !stopped(abort);
+      uint8_t* st = sm + K_OFF + s * K_TILE;
+      uint32_t ok[4];
+      long long off[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const bool mapped = page[q] >= 0 && page[q] < a.kv.num_blocks;
+        if (slot[q] >= 0 && !mapped) atomicOr(a.status, ST_UNMAPPED_PAGE);
+        off[q] = mapped ? page[q] * a.kv.stride_block + slot[q] * a.kv.stride_tok : -1;
+        ok[q] = __ballot_sync(0xffffffffu, mapped);
+        if (go)
+          cp_async4(sm + SC_OFF + (s * TT + 32 * q + lane) * 4,
+                    a.kv.base + (mapped ? off[q] + a.kv_dim : 0), mapped ? 4 : 0);
+      }
+      if (lane < 4) ss.valid[s][lane] = lane == 0 ? ok[0] : lane == 1 ? ok[1] : lane == 2 ? ok[2] : ok[3];
+      __syncwarp();
+      if (box) {
+        // a lane per box: boxes with a token to see are copied (their pages' other tokens and the
+        // rest of the slot are masked, and widening makes any code a number)
+        const int at = lane * box, q = at >> 5;
+        const uint32_t w = q == 0 ? ok[0] : q == 1 ? ok[1] : q == 2 ? ok[2] : ok[3];
+        bool want = false;
+        int src = 0;
+        if (lane < boxes) {
+          if (box >= 32) {
+            for (int k = 0; k < 4; ++k)
+              if (k >= q && k < q + (box >> 5) && !want) {
+                const uint32_t v = k == 0 ? ok[0] : k == 1 ? ok[1] : k == 2 ? ok[2] : ok[3];
+                if (v) want = true, src = 32 * k + __ffs(v) - 1;
+              }
+          } else {
+            const uint32_t v = (w >> (at & 31)) & ((1u << box) - 1);
+            if (v) want = true, src = at + __ffs(v) - 1;
+          }
+        }
+        // the page of the box: that of its first token to see
+        int pg = 0, in_page = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int p = __shfl_sync(0xffffffffu, page[k], src & 31);
+          const int x = __shfl_sync(0xffffffffu, slot[k], src & 31);
+          if ((src >> 5) == k) pg = p, in_page = x;
+        }
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, want));
+        if (go && lane == 0) mbar_arrive_expect_tx(&ss.full[s], n * box * 128);
+        __syncwarp();
+        if (go && want)
+          tma_load_3d(st + at * 128, &ar.map, 128 * chunk, in_page - (src - at), pg, &ss.full[s]);
+      } else {
+#pragma unroll 1
+        for (int e = 0; e < 32; ++e) {
+          const int row = 4 * e + r4;
+          long long ro = -1;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const long long x = __shfl_sync(0xffffffffu, off[q], row & 31);
+            if ((row >> 5) == q) ro = x;
+          }
+          const bool in = ro >= 0 && in_chunk;
+          if (go)
+            cp_async16(st + row * 128 + ((piece ^ (row & 7)) << 4),
+                       a.kv.base + (in ? ro + piece_off : 0), in ? 16 : 0);
+        }
+      }
+      cp_async_arrive_noinc(&ss.full[s]);
+      if (lane == 0 && !(box && go)) mbar_arrive(&ss.full[s]);
+      ni += LOAD_WARPS;
+      locate();
+    }
+    cp_async_wait_all();
+  } else if (warp >= WIDE_WARP && warp < WIDE_WARP + WIDE_WARPS) {
+    // ------------------------------------------------------------ widening: 32 tokens of every tile
+    regs_down<WIDE_REGS>();
+    const int lw = warp - WIDE_WARP, piece = lane & 7, r4 = lane >> 3;
+    const int total = items.left;
+#pragma unroll 1
+    for (int it = 0; it < total; ++it) {
+      const int s = it % ST, b = it & 1;
+      warp_wait(&ss.full[s], (it / ST) & 1, a.status, abort);
+      if (it >= 2) warp_wait(&ss.pv_done[b], ((it >> 1) - 1) & 1, a.status, abort);
+      const uint8_t* src = sm + K_OFF + s * K_TILE + 32 * lw * 128;
+      uint8_t* dst = sm + V_OFF + b * V_TILE + (piece >> 2) * K_TILE + 32 * lw * 128;
+      uint4 v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int row = 4 * e + r4;
+        v[e] = lds128(src + row * 128 + ((piece ^ (row & 7)) << 4));
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int row = 4 * e + r4, c = 2 * (piece & 3);
+        uint4 x, y;
+        x.x = widen(__byte_perm(v[e].x, 0, 0x1404)), x.y = widen(__byte_perm(v[e].x, 0, 0x3424));
+        x.z = widen(__byte_perm(v[e].y, 0, 0x1404)), x.w = widen(__byte_perm(v[e].y, 0, 0x3424));
+        y.x = widen(__byte_perm(v[e].z, 0, 0x1404)), y.y = widen(__byte_perm(v[e].z, 0, 0x3424));
+        y.z = widen(__byte_perm(v[e].w, 0, 0x1404)), y.w = widen(__byte_perm(v[e].w, 0, 0x3424));
+        *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = x;
+        *reinterpret_cast<uint4*>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) = y;
+      }
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ss.v_full[b]), mbar_arrive(&ss.k_free[s]);
+    }
+  } else if (warp == S_WARP) {
+    // ------------------------------------------------------------- the first product's MMAs
+    regs_down<MMA_REGS>();
+    const uint32_t k0 = smem_u32(sm + K_OFF);
+    const uint64_t q0 = desc_sw128(smem_u32(sm + Q_OFF));
+    int it = 0;
     if (elect_one()) tc_cp_img(tmem + SF_ONE, sm + ONE_OFF);
     __syncwarp();
-    for_items(a, plan, sh, team, [&](const Item& im) {
+#pragma unroll 1
+    for (int item = 0; next_item(a, plan, items, im); ++item) {
       warp_wait(&ss.q_full, item & 1, a.status, abort);
       const int nqp = ss.cols;
-      ++item;
       const bool merged = nqp <= MERGE;
-      const int firsts = nqp <= ALT ? 2 : 1;
-      const uint32_t idesc = IDESC | ((uint32_t)((merged ? 2 * nqp : nqp) >> 3) << 17);
-      for (int i = 0; i < im.n; ++i) {
-        const int j = it + i;
-        warp_wait(&ss.full[j % ST], (j / ST) & 1, a.status, abort);
-        if (!stopped(abort) && elect_one()) {
+      const uint32_t idesc = S_IDESC | ((uint32_t)((merged ? 2 * nqp : nqp) >> 3) << 17);
+#pragma unroll 1
+      for (int i = 0; i < im.n; ++i, ++it) {
+        const int st = it % ST, b = it & 1;
+        bool ok = warp_wait(&ss.full[st], (it / ST) & 1, a.status, abort);
+        if (it >= 2) ok &= warp_wait(&ss.p_full[b], ((it >> 1) - 1) & 1, a.status, abort);
+        if (ok && elect_one()) {
           fence_proxy_async_shared();  // the copies, seen to have landed, before the MMA's reads
           tc_fence_after();
           if (i == 0) tc_cp_img(tmem + SF_Q, sm + QIMG_OFF);
-          const uint32_t ka = k0 + (j % ST) * TT * 128;
+          const uint64_t kd = desc_sw128(k0 + st * K_TILE);
+#pragma unroll 1
           for (int term = 0; term < (merged ? 1 : 2); ++term)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc_mma_mxf8(tmem + S_COL + 128 * (j & 1), desc_sw128(ka + 32 * k),
-                          desc_sw128(q0 + term * NQ * 128 + 32 * k),
+              tc_mma_mxf8(tmem + S_COL + 128 * b, kd + 2 * k, q0 + term * (NQ * 128 / 16) + 2 * k,
                           idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), tmem + SF_ONE,
                           tmem + SF_Q, term > 0 || k > 0);
-          tc_commit(&ss.s_full[j & 1]);
+          tc_commit(&ss.s_full[b]);
+          tc_commit(&ss.k_free[st]);
         }
         __syncwarp();
-        if (i > 0) pv(j - 1, nqp, i - 1 < firsts);
       }
-      pv(it + im.n - 1, nqp, im.n - 1 < firsts);
-      it += im.n;
-    });
-    // after a wait that ran out: what was issued completes before TMEM is freed
-    if (stopped(abort) && elect_one()) {
-      tc_commit(&ss.drain);
-      (void)mbar_wait(&ss.drain, 0, a.status, 100000000ull);
     }
+    if (elect_one()) tc_commit(&ss.drain);  // (what was issued has completed at this arrival)
+    __syncwarp();
+  } else if (warp == O_WARP) {
+    // ------------------------------------------------------------ the second product's MMAs
+    regs_down<MMA_REGS>();
+    const uint64_t v0 = desc_mn(smem_u32(sm + V_OFF), K_TILE);
+    const uint64_t p0 = desc_mn(smem_u32(sm + P_OFF), K_TILE);
+    // first, where the second kernel finds the rows' results
+#pragma unroll 1
+    for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
+      const int b = a.row_req[r];
+      RowInfo info = {0, 0, 0};
+      if (a.positions[r] >= 0 && b >= 0 && b < a.n_req) {
+        int rank = 0;
+#pragma unroll 1
+        for (int i = lane; i < r; i += 32) rank += a.row_req[i] == b && a.positions[i] >= 0;
+        rank = __reduce_add_sync(0xffffffffu, rank);
+        const Span s = span_of(a, plan.pmax[b], plan.pmin[b]);
+        const int group = rank / sh.rows_per;
+        info = {plan.pre[b] + group * s.tiles, s.tiles, rank - group * sh.rows_per};
+      }
+      if (lane == 0) ar.rows[r] = info;
+    }
+    int it = 0;
+#pragma unroll 1
+    while (next_item(a, plan, items, im)) {
+      uint32_t idesc = 0;
+#pragma unroll 1
+      for (int i = 0; i < im.n; ++i, ++it) {
+        const int b = it & 1;
+        bool ok = warp_wait(&ss.p_full[b], (it >> 1) & 1, a.status, abort);
+        ok &= warp_wait(&ss.v_full[b], (it >> 1) & 1, a.status, abort);
+        if (i == 0) idesc = O_IDESC | ((uint32_t)(ss.cols >> 3) << 17);
+        if (ok && elect_one()) {
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)  // 16 tokens each
+            mma_bf16(tmem + O_COL, v0 + b * (V_TILE / 16) + k * (2048 / 16), p0 + k * (2048 / 16),
+                     idesc, i > 0 || k > 0);
+          tc_commit(&ss.pv_done[b]);
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) tc_commit(&ss.drain);
     __syncwarp();
   } else {
     // ---------------------------------------------------------------------------- softmax
@@ -668,13 +785,19 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
     const int hpg = a.n_q / (a.kv_dim / a.head_dim);
     const int cheads = hpg * (chunk_bytes > a.head_dim ? 2 : 1);  // heads per row of this chunk
     const int dshift = a.head_dim == 64 ? 6 : 7;
-    int it = 0;
-    for_items(a, plan, sh, team, [&](const Item& im) {
+    Soft w;
+    w.it = 0;
+    w.cheads = cheads;
+    w.to_log2 = a.scale * LOG2E;
+    w.tmem = tmem + ((uint32_t)(32 * quad) << 16);
+#pragma unroll 1
+    while (next_item(a, plan, items, im)) {
       // ---- the group's rows and queries
       bar_sync<256>(1);  // the previous item's columns are no longer in use
       if (warp == 0) {
         const int first = im.group * sh.rows_per;
         int seen = 0, n = 0;
+#pragma unroll 1
         for (int r0 = 0; r0 < a.rows && n < sh.rows_per; r0 += 32) {
           const int r = r0 + lane;
           const int p = r < a.rows && a.row_req[r] == im.b ? a.positions[r] : -1;
@@ -689,31 +812,37 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
       }
       bar_sync<256>(1);
       const int nrows = ss.cols >> 16, nqp = ss.cols & 0xFFFF, nq = nrows * cheads;
-      const bool merged = nqp <= MERGE, turns = nqp <= ALT;
-      if (tid < NQ) {
-        int hi = 0x7FFFFFFF, lo = 0;  // padding columns see everything
-        if (tid < nq) {
-          hi = a.causal ? ss.group_pos[tid / cheads] : im.span.hi;
-          lo = a.window > 0 ? max(0, hi - a.window + 1) : 0;
-        }
-        ss.col_hi[tid] = hi;
-        ss.col_lo[tid] = lo;
-        ss.neg_m[0][tid] = ss.neg_m[1][tid] = -UNSET;
+      const bool merged = nqp <= MERGE;
+      const bool whole = im.n == im.span.tiles;  // nobody else has tiles of this group
+      const long long slot = (long long)(team * 2 + (im.t0 > 0 ? 0 : 1)) * sh.chunks + chunk;
+      if (tid < nqp) {
+        const int j = tid / cheads, h = tid - j * cheads, sl = h / hpg;
+        const long long head = (long long)chunk * sh.heads + h;
+        ss.neg_m[tid] = -UNSET;
+        ss.slice[tid] = tid < nq ? sl : -1;
+        if (tid < nq)
+          ss.out[tid] = whole ? ss.group_row[j] * a.o_stride + head * a.head_dim
+                              : (slot * NQ + tid) * PART_LD + 4;
       }
       // queries as two e4m3 terms, rows of 128 bytes: hi in row c, lo in row nqp + c (merged)
       // or NQ + c
-      for (int i = tid; i < nqp * 16; i += 256) {
+#pragma unroll 1
+      for (int i = tid; i < nqp * 16; i += 256) {  // first copied as they are, all at once
         const int c = i >> 4, d = (i & 15) * 8;
         const int j = c / cheads, h = c - j * cheads, sl = h / hpg;
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
         const bool in = c < nq && (d >> dshift) == sl;
-        if (in)
-          bf16x8_to_f32(*reinterpret_cast<const uint4*>(
-                            a.q + ss.group_row[j] * a.q_stride +
-                            ((long long)chunk * sh.heads + h) * a.head_dim + (d - (sl << dshift))),
-                        v);
+        cp_async16(sm + P_OFF + i * 16,
+                   a.q + (in ? ss.group_row[j] * a.q_stride +
+                                   ((long long)chunk * sh.heads + h) * a.head_dim + (d - (sl << dshift))
+                             : 0),
+                   in ? 16 : 0);
+      }
+      cp_async_wait_all();
+#pragma unroll 1
+      for (int i = tid; i < nqp * 16; i += 256) {
+        const int c = i >> 4, d = (i & 15) * 8;
+        float v[8];
+        bf16x8_to_f32(lds128(sm + P_OFF + i * 16), v);
         float m = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -733,10 +862,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
           lw[e >> 2] |= lb << (8 * (e & 3));
         }
         const int rl = (merged ? nqp : NQ) + c;
-        const int o = (d >> 4), w = d & 8;
-        *reinterpret_cast<uint2*>(sm + Q_OFF + c * 128 + ((o ^ (c & 7)) << 4) + w) =
+        const int o = (d >> 4), x = d & 8;
+        *reinterpret_cast<uint2*>(sm + Q_OFF + c * 128 + ((o ^ (c & 7)) << 4) + x) =
             make_uint2(hw[0], hw[1]);
-        *reinterpret_cast<uint2*>(sm + Q_OFF + rl * 128 + ((o ^ (rl & 7)) << 4) + w) =
+        *reinterpret_cast<uint2*>(sm + Q_OFF + rl * 128 + ((o ^ (rl & 7)) << 4) + x) =
             make_uint2(lw[0], lw[1]);
         if ((d & 31) == 0) {
           sm[QIMG_OFF + (c & 31) * 16 + (c >> 5) * 4 + (d >> 5)] = (uint8_t)code;
@@ -744,9 +873,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
         }
       }
       fence_proxy_async_shared();
-      Soft w;
       w.min_hi = 0x7FFFFFFF;
       w.max_lo = 0;
+#pragma unroll 1
       for (int j = 0; j < nrows; ++j) {
         const int hi = a.causal ? ss.group_pos[j] : im.span.hi;
         w.min_hi = min(w.min_hi, hi);
@@ -759,96 +888,78 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const Args ar) {
       w.span = im.span;
       w.t0 = im.t0;
       w.n = im.n;
-      w.it = it;
       w.nqp = nqp;
-      w.to_log2 = a.scale * LOG2E;
-      w.tmem = tmem + ((uint32_t)(32 * quad) << 16);
-      // the halves take turns with whole tiles (their own O and m each), or share the columns
-      w.stream = turns ? half : 0;
-      const int half0 = (nqp / 16 + 1) / 2 * 16;  // columns of half 0 where they share
-      w.c0 = turns || half == 0 ? 0 : half0;
-      const int cols = turns ? nqp : half == 0 ? half0 : nqp - half0;
-      float* lo = ss.red[warp];
-      if (turns) {
-        if (cols == 16) soft_tiles<16, true, true>(a, w, ss, sm, lo);
-        else if (cols == 32) soft_tiles<32, true, true>(a, w, ss, sm, lo);
-        else soft_tiles<48, true, true>(a, w, ss, sm, lo);
-      } else if (merged) {
-        soft_tiles<32, false, true>(a, w, ss, sm, lo);
-      } else if (cols == 32) {
-        soft_tiles<32, false, false>(a, w, ss, sm, lo);
-      } else {
-        soft_tiles<48, false, false>(a, w, ss, sm, lo);
+      w.nrows = nrows;
+      const int cols = nqp / 2;
+      w.c0 = half * cols;
+      switch (cols) {
+        case 8: soft_tiles<8>(a, w, ss, sm); break;
+        case 16: soft_tiles<16>(a, w, ss, sm); break;
+        case 24: soft_tiles<24>(a, w, ss, sm); break;
+        case 32: soft_tiles<32>(a, w, ss, sm); break;
+        case 40: soft_tiles<40>(a, w, ss, sm); break;
+        default: soft_tiles<48>(a, w, ss, sm); break;
       }
-      const int first_stream = it & 1;
-      it += im.n;
+      w.it += im.n;
 
-      // ---- the item's result
-      for (int i = max(it - 2, it - im.n); i < it; ++i)
-        warp_wait(&ss.pv_done[i & 1], (i >> 1) & 1, a.status, abort);
-      tc_fence_after();
+      // ---- the item's result: the columns' sums over the tokens, then O
+      const float* scratch = reinterpret_cast<const float*>(sm + P_OFF);
+      __syncwarp();
+#pragma unroll 1
+      for (int c = lane; c < cols; c += 32) {  // this warp's share of each
+        float v = 0.0f;
+#pragma unroll 4
+        for (int k = 0; k < 32; ++k) v += scratch[(warp * (NQ / 2) + c) * 32 + ((k + lane) & 31)];
+        ss.red[warp][w.c0 + c] = v;
+      }
       bar_sync<256>(1);
-      const bool whole = im.n == im.span.tiles;  // nobody else has tiles of this group
-      float* pt = ar.part + ((size_t)(team * 2 + (im.t0 > 0 ? 0 : 1)) * sh.chunks + chunk) * NQ * PART_LD;
-      const int d = 32 * quad + lane;  // this thread's dimension of the chunk
-      for (int c8 = 8 * half; c8 < nqp; c8 += 16) {
-        float acc[8], m[8], lt[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = lt[e] = 0.0f, m[e] = UNSET;
-        for (int k = 0; k < (turns ? 2 : 1); ++k) {
-          if (turns && im.n == 1 && k != first_stream) continue;  // a stream without a tile
-          float x[8];
-          const uint32_t oc = w.tmem + O_COL + O_ALT * k + c8;
-          tc_ld8(oc, x);
-          tc_wait_ld();
-          tc_loaded(x);
-          if (merged) {
-            float y[8];
-            tc_ld8(oc + nqp, y);
-            tc_wait_ld();
-            tc_loaded(y);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] += y[e];
-          }
-          const float(*r)[NQ] = ss.red + (turns ? 4 * k : c8 < half0 ? 0 : 4);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int c = c8 + e;
-            const float lk = (r[0][c] + r[1][c]) + (r[2][c] + r[3][c]);
-            const float mk = -ss.neg_m[k][c], mn = fmaxf(m[e], mk);
-            const float f0 = m[e] == UNSET ? 0.0f : ex2(m[e] - mn);
-            const float f1 = mk == UNSET && lk == 0.0f ? 0.0f : ex2(mk - mn);
-            acc[e] = acc[e] * f0 + (f1 == 0.0f ? 0.0f : x[e] * f1);
-            lt[e] = lt[e] * f0 + lk * f1;
-            m[e] = mn;
-          }
+      if (tid < nq) {
+        const float(*r)[NQ] = ss.red + (tid < cols ? 0 : 4);
+        const float lt = (r[0][tid] + r[1][tid]) + (r[2][tid] + r[3][tid]);
+        const float m = -ss.neg_m[tid];
+        if (whole) {
+          const int j = tid / cheads;
+          ss.fac[tid] = lt == 0.0f ? 0.0f : O_UP / lt;
+          a.lse[(long long)ss.group_row[j] * a.n_q + chunk * sh.heads + tid - j * cheads] =
+              lt == 0.0f ? -INFINITY : (log2f(lt) + m) * LN2;
+        } else {
+          ss.fac[tid] = O_UP;
+          ar.part[ss.out[tid] - 4] = m;
+          ar.part[ss.out[tid] - 3] = lt;
         }
+      }
+      bar_sync<256>(1);
+      const int d = 32 * quad + lane;  // this thread's dimension of the chunk
+      const int sl = d >> dshift, dl = d - (sl << dshift);
+#pragma unroll 1
+      for (int c8 = 8 * half; c8 < nqp; c8 += 16) {
+        float x[8], f[8];
+        long long at[8];
+        tc_ld8(w.tmem + O_COL + c8, x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int c = c8 + e;
-          if (c >= nq) continue;
-          const int j = c / cheads, h = c - j * cheads, sl = h / hpg;
-          const long long head = (long long)chunk * sh.heads + h;
-          const bool mine = (d >> dshift) == sl;
+          f[e] = ss.fac[c8 + e];
+          at[e] = ss.slice[c8 + e] == sl ? ss.out[c8 + e] + dl : -1;
+        }
+        tc_wait_ld();
+        tc_loaded(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float v = f[e] == 0.0f ? 0.0f : x[e] * f[e];
           if (whole) {
-            if (mine)
-              a.o[ss.group_row[j] * a.o_stride + head * a.head_dim + (d - (sl << dshift))] =
-                  __float2bfloat16_rn(lt[e] == 0.0f ? 0.0f : acc[e] / lt[e]);
-            if (d == 0)
-              a.lse[(long long)ss.group_row[j] * a.n_q + head] =
-                  lt[e] == 0.0f ? -INFINITY : (log2f(lt[e]) + m[e]) * LN2;
+            if (at[e] >= 0) a.o[at[e]] = __float2bfloat16_rn(v);
           } else {
-            if (mine) pt[c * PART_LD + 4 + (d - (sl << dshift))] = acc[e];
-            if (d == 0) pt[c * PART_LD] = m[e], pt[c * PART_LD + 1] = lt[e];
+            if (at[e] >= 0) ar.part[at[e]] = v;
           }
         }
       }
       tc_fence_before();
-    });
+    }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == MMA_WARP) {
+  if (warp == S_WARP) {
+    (void)warp_wait(&ss.drain, 0, a.status, abort);  // (at once unless a wait ran out before)
     tc_fence_after();
     tmem_dealloc<512>(tmem);
   }
@@ -872,31 +983,21 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attend_join_kernel(const Args
     if (lane == 0) a.lse[(long long)r * a.n_q + h] = -INFINITY;
     return;
   }
-  const long long W = *ar.total, g1 = info.g0 + info.tiles - 1;
-  // the team that holds unit g: the last k with W k / teams <= g
-  auto team_of = [&](long long g) {
-    int k = (int)(g * sh.teams / W);
-    while (W * (k + 1) / sh.teams <= g) ++k;
-    while (W * k / sh.teams > g) --k;
-    return k;
-  };
-  const int k0 = team_of(info.g0), k1 = team_of(g1);
+  const Cut cut(*ar.total, sh.teams);
+  const int k0 = cut.team_of(info.g0), k1 = cut.team_of(info.g0 + info.tiles - 1);
   if (k0 == k1) return;  // whole in one team
   const int chunk = h / sh.heads, hpg = a.n_q / (a.kv_dim / a.head_dim);
   const int cheads = hpg * (min(128, a.kv_dim - 128 * chunk) > a.head_dim ? 2 : 1);
   const int c = info.place * cheads + (h - chunk * sh.heads);
   auto piece = [&](int k) {
-    const int slot = W * k / sh.teams > info.g0 ? 0 : 1;  // began before this team, or in it
+    const int slot = cut.start(k) > info.g0 ? 0 : 1;  // began before this team, or in it
     return ar.part + (((size_t)(k * 2 + slot) * sh.chunks + chunk) * NQ + c) * PART_LD;
   };
-  auto empty = [&](int k) { return W * k / sh.teams == W * (k + 1) / sh.teams; };
   float M = UNSET;
-  for (int k = k0 + lane; k <= k1; k += 32)
-    if (!empty(k)) M = fmaxf(M, piece(k)[0]);
+  for (int k = k0 + lane; k <= k1; k += 32) M = fmaxf(M, piece(k)[0]);
   M = warp_max(M);
   float num[4] = {0.0f, 0.0f, 0.0f, 0.0f}, den = 0.0f;
   for (int k = k0; k <= k1; ++k) {
-    if (empty(k)) continue;
     const float* p = piece(k);
     const float f = ex2(p[0] - M);
     den = fmaf(f, p[1], den);
@@ -944,6 +1045,32 @@ __global__ void __launch_bounds__(TT) attend_weights_kernel(AttendArgs a, int ti
   }
 }
 
+// The records' codes as a 3D byte tensor [pages][tokens][kv_dim], boxes of 128 bytes x box tokens
+// under the 128-byte swizzle (bytes beyond kv_dim read as 0); false where its strides are beyond a
+// tensor map's.
+bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int kv_dim, int box) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  if (!encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || !fn) {
+      (void)cudaGetLastError();
+      return false;
+    }
+    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  if (kv.stride_block >= (1ll << 40) || kv.stride_tok >= (1ll << 40)) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)kv_dim, (cuuint64_t)kv.block_size, (cuuint64_t)kv.num_blocks};
+  const cuuint64_t strides[2] = {(cuuint64_t)kv.stride_tok, (cuuint64_t)kv.stride_block};
+  const cuuint32_t boxes[3] = {128, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(kv.base), dims, strides,
+                boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Layout {
   size_t rows, total, part, bytes;
 };
@@ -971,8 +1098,14 @@ cudaError_t attend_prepare() {
 
 cudaError_t launch_attend(const Launch& L, const AttendArgs& a, uint8_t* ws, int max_rows, int sms) {
   const Layout l = layout(max_rows, sms);
-  Args ar = {a, reinterpret_cast<float*>(ws + l.part), reinterpret_cast<RowInfo*>(ws + l.rows),
-             reinterpret_cast<long long*>(ws + l.total)};
+  Args ar = {{}, 0, a, reinterpret_cast<float*>(ws + l.part), reinterpret_cast<RowInfo*>(ws + l.rows),
+             reinterpret_cast<int*>(ws + l.total)};
+  // boxes of whole runs of a page, 8 rows (a swizzle atom) or more, that tiles are made of
+  const int bs = a.kv.block_size;
+  if (bs % 8 == 0 && a.kv.num_blocks <= INT32_MAX) {
+    const int box = std::min(bs & -bs, TT);
+    if (encode_cache_map(&ar.map, a.kv, a.kv_dim, box)) ar.box = box;
+  }
   cudaError_t e = launch_ex(L, dim3(sms), dim3(THREADS), SMEM_BYTES, attend_kernel, ar);
   if (e == cudaSuccess)
     e = launch_ex(L, dim3(a.rows, (a.n_q + JOIN_WARPS - 1) / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0,

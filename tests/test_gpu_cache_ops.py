@@ -153,6 +153,15 @@ def test_attend_many_requests():
     check_attend(_m(), TINY, lengths, [min(2, n) for n in lengths], seed=6)
 
 
+@pytest.mark.parametrize("spec,lengths,rows", [
+    (FULL, [9000], [42]), (FULL, [6000, 200, 5000], [12, 6, 11]),
+    (FULL, [4100 + 97 * i for i in range(12)], [1] * 12), (THREE, [20000, 9000], [16, 7]),
+    (ODD, [15000, 15001], [13, 16])], ids=["groups", "mixed", "single", "three", "odd"])
+def test_attend_many_tiles_per_block(spec, lengths, rows):
+    """Every block goes round its rings of buffers several times, over several items."""
+    check_attend(_m(), spec, lengths, rows, seed=lengths[0])
+
+
 def test_attend_scale_and_short_weight_rows():
     check_attend(_m(), WIDE, [300, 20], [2, 2], seed=8, scale=0.31, n_weights=150)
 
@@ -205,6 +214,37 @@ def test_attend_zero_scales_and_zero_codes():
     q = make_q(WIDE, 1, 13)
     o, lse, _, st = run_attend(m, WIDE, q, [299], [0], table, cache)
     eo, tol, el, ltol, _, _ = co.attend(WIDE, q.double().numpy(), [299], [0], table, cache)
+    assert st == 0 and (np.abs(o - eo) <= tol).all() and (np.abs(lse - el) <= ltol).all()
+
+
+def test_attend_codes_below_the_normal_range():
+    """Records of subnormal codes only: o keeps 8 bits of them (weights to 2^-8 each, o's rounding
+    2^-8, and 2^-12 for the scores' and sums' roundings)."""
+    m = _m()
+    table, cache = make_cache(WIDE, [300], 21)
+    rng = np.random.default_rng(21)
+    for t in range(300):
+        cache[table[0, t // 64], t % 64, :128] = rng.integers(1, 8, 128)
+        cache[table[0, t // 64], t % 64, 128:132] = np.frombuffer(np.float32(0.37).tobytes(), np.uint8)
+    q = make_q(WIDE, 2, 21)
+    o, _, _, st = run_attend(m, WIDE, q, [150, 299], [0, 0], table, cache)
+    eo, *_ = co.attend(WIDE, q.double().numpy(), [150, 299], [0, 0], table, cache)
+    assert st == 0 and (np.abs(o - eo) <= (2.0 ** -7 + 2.0 ** -12) * np.abs(eo)).all()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -40, 2.0 ** 30])
+def test_attend_scales_far_from_one(scale):
+    """Records of tiny and of huge values (the queries and the score factor make up for it)."""
+    m = _m()
+    table, cache = make_cache(WIDE, [200], 22)
+    f = np.float32(scale)
+    for t in range(200):
+        r = cache[table[0, t // 64], t % 64]
+        r[128:132] = np.frombuffer((r[128:132].copy().view(np.float32) * f).tobytes(), np.uint8)
+    q = make_q(WIDE, 1, 22)
+    k = 0.125 / scale
+    o, lse, _, st = run_attend(m, WIDE, q, [199], [0], table, cache, scale=k)
+    eo, tol, el, ltol, _, _ = co.attend(WIDE, q.double().numpy(), [199], [0], table, cache, scale=k)
     assert st == 0 and (np.abs(o - eo) <= tol).all() and (np.abs(lse - el) <= ltol).all()
 
 
