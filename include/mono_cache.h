@@ -26,7 +26,7 @@ typedef struct mono_cache mono_cache_t; /* opaque handle: a cache layout and its
  * The cache layout (the fields of mono_layer_spec of the same names, with the same
  * constraints: head_dim 64 or 128; kv_dim a multiple of head_dim, at most 1024; n_q_heads a
  * multiple of kv_dim/head_dim with at most 16 heads per latent slice; kv_record_bytes >=
- * kv_dim + 4 and a multiple of 16) and the largest step: 1..1024 rows of 1..1024 requests.
+ * kv_dim + 4 and a multiple of 16) and the largest step: 1..1024 rows of 1..512 requests.
  */
 typedef struct {
   int32_t n_q_heads, head_dim, kv_dim;

@@ -36,7 +36,7 @@ int check_layout(const mono_cache_spec& s) {
   if (s.block_size <= 0 || s.block_size > (1 << 20)) return MONO_ERR_UNSUPPORTED_DIMS;
   if (s.kv_record_bytes < s.kv_dim + 4 || s.kv_record_bytes % 16 || s.kv_record_bytes > (1 << 20))
     return MONO_ERR_UNSUPPORTED_DIMS;
-  if (s.max_rows < 1 || s.max_rows > 1024 || s.max_req < 1 || s.max_req > 1024)
+  if (s.max_rows < 1 || s.max_rows > 1024 || s.max_req < 1 || s.max_req > 512)
     return MONO_ERR_TOO_MANY_ROWS;
   return MONO_OK;
 }

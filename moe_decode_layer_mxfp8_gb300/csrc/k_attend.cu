@@ -26,7 +26,8 @@
 //
 // Roles: warps 0-7 softmax (TMEM lane quadrant = warp % 4: one token per thread; warp / 4: half
 // of the columns), 8-11 widening, 12 the first product's MMAs, 13 the second's, 14 and 15 loads
-// (cp.async through the page table, any page size; every other tile each).  What runs once per launch or item is kept short,
+// (every other tile each: TMA boxes through the page table, or cp.async for page sizes that are no
+// multiple of 8).  What runs once per launch or item is kept short,
 // in rolled loops: its instructions come from L2 or further away.
 // Every mbarrier wait is bounded; a wait that runs out is reported, and from then on every role
 // runs its loop without waiting, copying or issuing, so that the barriers among warps still
@@ -48,7 +49,7 @@ constexpr int NQ = 96;         // query columns at most
 constexpr int MERGE = 64;      // up to here both terms of the queries are columns of one MMA
 constexpr int GROUP = 16;      // rows of a group at most
 constexpr int ST = 5;          // tiles in the ring
-constexpr int MAX_REQ = 1024;
+constexpr int MAX_REQ = 512;
 constexpr int THREADS = 16 * 32;
 constexpr int SOFT_WARPS = 8, WIDE_WARP = 8, WIDE_WARPS = 4, S_WARP = 12, O_WARP = 13;
 constexpr int LOAD_WARP = 14, LOAD_WARPS = 2;
@@ -70,8 +71,8 @@ constexpr int Q_OFF = P_OFF + V_TILE;       // hi rows, then lo rows
 constexpr int IMG = 512;
 constexpr int QIMG_OFF = Q_OFF + 2 * NQ * 128;
 constexpr int ONE_OFF = QIMG_OFF + IMG;
-constexpr int SC_OFF = ONE_OFF + IMG;  // token scales [ST][128]
-constexpr int PLAN_OFF = SC_OFF + ST * TT * 4;
+constexpr int SC_OFF = ONE_OFF + IMG;  // the 16 bytes behind the codes, scale first [ST][128]
+constexpr int PLAN_OFF = SC_OFF + ST * TT * 16;
 constexpr int SMEM_BYTES = PLAN_OFF + (3 * MAX_REQ + 4) * 4 + 1024;
 static_assert(V_OFF % 1024 == 0 && P_OFF % 1024 == 0 && Q_OFF % 1024 == 0 && (NQ * 128) % 1024 == 0,
               "swizzle atoms");
@@ -183,8 +184,8 @@ struct RowInfo {
 };
 
 struct Args {
-  CUtensorMap map;  // the cache as [pages][tokens][kv_dim bytes], boxes of 128 bytes x box tokens
-  int box;          // 0: no map
+  CUtensorMap codes, scales;  // the cache as [pages][tokens][bytes], boxes of box tokens
+  int box;                    // 0: no maps
   AttendArgs a;
   float* part;     // [teams][2 slots][chunks][NQ][128 + 2]: O, then m and l
   RowInfo* rows;   // [rows]
@@ -244,9 +245,19 @@ __device__ __forceinline__ bool bar_any(int id, bool v) {
   return r != 0;
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// The whole warp's view of the abort flag.
-__device__ __forceinline__ bool stopped(volatile int* abort) {
-  return __any_sync(0xffffffffu, *abort != 0);
+// A wait for an mbarrier phase by a whole warp, in few instructions: some 10^7 polls (a good part
+// of a second) at most, none once another wait has run out.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
+  uint32_t polls = 0;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort || ++polls == (1u << 23)) {
+      atomicOr(status, ST_WAIT_TIMEOUT);
+      *abort = 1;
+      break;
+    }
+  }
+  return !__any_sync(0xffffffffu, *abort != 0);
 }
 // A maximum over the warp, every lane gets it (floats as ordered integers).
 __device__ __forceinline__ float warp_max_any(float v) {
@@ -297,8 +308,8 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, S
     const int it = w.it + i, st = it % ST, b = it & 1;
     const uint32_t ph = (it >> 1) & 1;
     const int t0 = w.span.token(w.t0 + i), t = t0 + tok;
-    warp_wait(&sh.full[st], (it / ST) & 1, a.status, abort);
-    const float raw = reinterpret_cast<const float*>(sm + SC_OFF)[st * TT + tok];
+    wait(&sh.full[st], (it / ST) & 1, a.status, abort);
+    const float raw = reinterpret_cast<const float*>(sm + SC_OFF)[(st * TT + tok) * 4];
     const uint32_t ok = sh.valid[st][quad];
     const bool fin = fabsf(raw) <= 3.0e38f;
     const float ct = fin ? raw * w.to_log2 : __int_as_float(0x7FC00000);
@@ -309,7 +320,7 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, S
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.k_free[st]);
     uint32_t see[(C + 31) / 32];
-    if (part) {  // this half's columns that see the token
+    if (__builtin_expect(part, 0)) {  // this half's columns that see the token
 #pragma unroll
       for (int k = 0; k < (C + 31) / 32; ++k) see[k] = 0xffffffffu;
 #pragma unroll 1
@@ -328,7 +339,7 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, S
         }
       }
     }
-    warp_wait(&sh.s_full[b], ph, a.status, abort);
+    wait(&sh.s_full[b], ph, a.status, abort);
     const uint32_t scol = w.tmem + S_COL + 128 * b + w.c0;
     // weights; a second round where some query's m has to move (always in an item's first tile)
 #pragma unroll 1
@@ -361,7 +372,7 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, S
         s[c + 2] = fmaf(s[c + 2], ct, m.z);
         s[c + 3] = fmaf(s[c + 3], ct, m.w);
       }
-      if (part) {
+      if (__builtin_expect(part, 0)) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
           if (!((see[c / 32] >> (c % 32)) & 1)) s[c] = -INFINITY;
@@ -369,7 +380,7 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, S
       float top = -INFINITY;
 #pragma unroll
       for (int c = 0; c < C; ++c) top = fmaxf(top, s[c]);
-      if (!bar_any(2 + half, !moved && top > JUMP)) break;
+      if (__builtin_expect(!bar_any(2 + half, !moved && top > JUMP), 1)) break;
       // the columns' largest scores of the tile
 #pragma unroll 1
       for (int g = 0; g < C; g += 8) {
@@ -407,7 +418,7 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, S
 #pragma unroll
       for (int c = 0; c < C; ++c) l[c] *= sh.fac[w.c0 + c];
       if (i > 0) {
-        warp_wait(&sh.pv_done[b ^ 1], ((it - 1) >> 1) & 1, a.status, abort);
+        wait(&sh.pv_done[b ^ 1], ((it - 1) >> 1) & 1, a.status, abort);
         tc_fence_after();
 #pragma unroll 1
         for (int g = 0; g < C; g += 8) {
@@ -424,7 +435,7 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, S
       }
     }
     // weights times scales, rows of 128 bytes per token; the buffer's last reader has finished
-    if (it > 0) warp_wait(&sh.pv_done[b ^ 1], ((it - 1) >> 1) & 1, a.status, abort);
+    if (it > 0) wait(&sh.pv_done[b ^ 1], ((it - 1) >> 1) & 1, a.status, abort);
 #pragma unroll
     for (int g = 0; g < C; g += 8) {
       uint32_t o[4];
@@ -447,7 +458,7 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, S
   }
   // every product of the item is done: the weights' and the queries' buffers are scratch
   const int last = w.it + w.n - 1;
-  warp_wait(&sh.pv_done[last & 1], (last >> 1) & 1, a.status, abort);
+  wait(&sh.pv_done[last & 1], (last >> 1) & 1, a.status, abort);
   tc_fence_after();
   float* scratch = reinterpret_cast<float*>(sm + P_OFF) + warp * (NQ / 2) * 32 + lane;
 #pragma unroll
@@ -471,10 +482,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   const int chunk_bytes = min(128, a.kv_dim - 128 * chunk);
 
   if (tid == 0) {
-    // a tile lands with its copies (the loading warp's lanes) and its masks (lane 0); it is
-    // free when the first product, the widening and the softmax warps have read it
+    // a tile is free when the first product, the widening and the softmax warps have read it
     for (int s = 0; s < ST; ++s)
-      mbar_init(&ss.full[s], 33), mbar_init(&ss.k_free[s], 1 + WIDE_WARPS + SOFT_WARPS);
+      mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], 1 + WIDE_WARPS + SOFT_WARPS);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ss.s_full[s], 1), mbar_init(&ss.pv_done[s], 1);
       mbar_init(&ss.p_full[s], SOFT_WARPS), mbar_init(&ss.v_full[s], WIDE_WARPS);
@@ -563,105 +573,94 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   if (warp >= LOAD_WARP) {
     // ------------------------------------------------------- loads: a warp takes every other tile
     regs_down<MMA_REGS>();
-    const int piece = lane & 7, r4 = lane >> 3;
-    const bool in_chunk = 16 * piece < chunk_bytes;
-    const long long piece_off = 128 * chunk + 16 * piece;
     int ni = warp - LOAD_WARP;
     bool more = next_item(a, plan, items, im);
-    // this warp's next tile: its tokens' pages are on their way while the one before is loaded
-    int page[4], slot[4];
+    // a lane per box of the next tile (of a token each without maps, four times): its page, on its
+    // way while the tile before is loaded, and its first token's place in it
+    const int box = ar.box ? ar.box : 1, bs = a.kv.block_size;
+    const int shift = __ffs(box) - 1, boxes = TT >> shift;
+    int page[4], row[4], t0 = 0;
     auto locate = [&]() {
 #pragma unroll 1
       while (more && ni >= im.n) ni -= im.n, more = next_item(a, plan, items, im);
       if (!more) return;
-      const int t0 = im.span.token(im.t0 + ni) + lane;
+      t0 = im.span.token(im.t0 + ni);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int t = t0 + 32 * q, lb = t / a.kv.block_size;
+        if (32 * q >= boxes) break;
+        const int t = t0 + ((32 * q + lane) << shift), lb = t / bs;
         page[q] = -1;
-        slot[q] = -1;
-        if (t <= im.span.hi && (t >= im.span.lo || t < a.sinks)) {
-          slot[q] = t - lb * a.kv.block_size;
-          if (lb < a.kv.max_blocks) page[q] = __ldg(a.kv.table + (size_t)im.b * a.kv.max_blocks + lb);
-        }
+        row[q] = t - lb * bs;
+        if (32 * q + lane < boxes && lb < a.kv.max_blocks && t <= im.span.hi &&
+            (t + box > im.span.lo || t < a.sinks))
+          page[q] = __ldg(a.kv.table + (size_t)im.b * a.kv.max_blocks + lb);
+        else
+          row[q] = -1;
       }
     };
+    auto mapped = [&](int q) {
+      const bool m = page[q] >= 0 && page[q] < a.kv.num_blocks;
+      if (row[q] >= 0 && !m) atomicOr(a.status, ST_UNMAPPED_PAGE);
+      return m;
+    };
     locate();
-    const int box = ar.box, boxes = box ? TT / box : 0;
 #pragma unroll 1
     for (int it = warp - LOAD_WARP; more; it += LOAD_WARPS) {
       const int s = it % ST;
-      if (it >= ST) warp_wait(&ss.k_free[s], ((it / ST) - 1) & 1, a.status, abort);
-      const bool go = !stopped(abort);
+      bool go = true;
+      if (it >= ST) go = wait(&ss.k_free[s], ((it / ST) - 1) & 1, a.status, abort);
       uint8_t* st = sm + K_OFF + s * K_TILE;
-      uint32_t ok[4];
-      long long off[4];
+      uint8_t* sc = sm + SC_OFF + s * TT * 16;
+      if (ar.box) {
+        // boxes with a token to see; their other tokens, and what the rest of the slot holds, are
+        // masked (widening makes any code a number)
+        const bool m = mapped(0);
+        const uint32_t have = __ballot_sync(0xffffffffu, m);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const bool mapped = page[q] >= 0 && page[q] < a.kv.num_blocks;
-        if (slot[q] >= 0 && !mapped) atomicOr(a.status, ST_UNMAPPED_PAGE);
-        off[q] = mapped ? page[q] * a.kv.stride_block + slot[q] * a.kv.stride_tok : -1;
-        ok[q] = __ballot_sync(0xffffffffu, mapped);
-        if (go)
-          cp_async4(sm + SC_OFF + (s * TT + 32 * q + lane) * 4,
-                    a.kv.base + (mapped ? off[q] + a.kv_dim : 0), mapped ? 4 : 0);
-      }
-      if (lane < 4) ss.valid[s][lane] = lane == 0 ? ok[0] : lane == 1 ? ok[1] : lane == 2 ? ok[2] : ok[3];
-      __syncwarp();
-      if (box) {
-        // a lane per box: boxes with a token to see are copied (their pages' other tokens and the
-        // rest of the slot are masked, and widening makes any code a number)
-        const int at = lane * box, q = at >> 5;
-        const uint32_t w = q == 0 ? ok[0] : q == 1 ? ok[1] : q == 2 ? ok[2] : ok[3];
-        bool want = false;
-        int src = 0;
-        if (lane < boxes) {
-          if (box >= 32) {
-            for (int k = 0; k < 4; ++k)
-              if (k >= q && k < q + (box >> 5) && !want) {
-                const uint32_t v = k == 0 ? ok[0] : k == 1 ? ok[1] : k == 2 ? ok[2] : ok[3];
-                if (v) want = true, src = 32 * k + __ffs(v) - 1;
-              }
-          } else {
-            const uint32_t v = (w >> (at & 31)) & ((1u << box) - 1);
-            if (v) want = true, src = at + __ffs(v) - 1;
-          }
+        for (int q = 0; q < 4; ++q) {
+          const int t = t0 + 32 * q + lane;
+          const bool see = ((have >> ((32 * q + lane) >> shift)) & 1) && t <= im.span.hi &&
+                           (t >= im.span.lo || t < a.sinks);
+          const uint32_t w = __ballot_sync(0xffffffffu, see);
+          if (lane == q) ss.valid[s][q] = w;
         }
-        // the page of the box: that of its first token to see
-        int pg = 0, in_page = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int p = __shfl_sync(0xffffffffu, page[k], src & 31);
-          const int x = __shfl_sync(0xffffffffu, slot[k], src & 31);
-          if ((src >> 5) == k) pg = p, in_page = x;
-        }
-        const uint32_t n = __popc(__ballot_sync(0xffffffffu, want));
-        if (go && lane == 0) mbar_arrive_expect_tx(&ss.full[s], n * box * 128);
         __syncwarp();
-        if (go && want)
-          tma_load_3d(st + at * 128, &ar.map, 128 * chunk, in_page - (src - at), pg, &ss.full[s]);
-      } else {
-#pragma unroll 1
-        for (int e = 0; e < 32; ++e) {
-          const int row = 4 * e + r4;
-          long long ro = -1;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const long long x = __shfl_sync(0xffffffffu, off[q], row & 31);
-            if ((row >> 5) == q) ro = x;
-          }
-          const bool in = ro >= 0 && in_chunk;
-          if (go)
-            cp_async16(st + row * 128 + ((piece ^ (row & 7)) << 4),
-                       a.kv.base + (in ? ro + piece_off : 0), in ? 16 : 0);
+        if (lane == 0) mbar_arrive_expect_tx(&ss.full[s], go ? __popc(have) * box * (128 + 16) : 0);
+        __syncwarp();
+        if (m && go) {
+          tma_load_3d(st + ((lane * 128) << shift), &ar.codes, 128 * chunk, row[0], page[0], &ss.full[s]);
+          tma_load_3d(sc + ((lane * 16) << shift), &ar.scales, a.kv_dim, row[0], page[0], &ss.full[s]);
         }
+      } else {
+        const int piece = lane & 7;
+        const bool in_chunk = go && 16 * piece < chunk_bytes;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          const int pg = q == 0 ? page[0] : q == 1 ? page[1] : q == 2 ? page[2] : page[3];
+          const int rw = q == 0 ? row[0] : q == 1 ? row[1] : q == 2 ? row[2] : row[3];
+          const bool m = pg >= 0 && pg < a.kv.num_blocks;
+          if (rw >= 0 && !m) atomicOr(a.status, ST_UNMAPPED_PAGE);
+          const long long off = m ? pg * a.kv.stride_block + rw * a.kv.stride_tok : 0;
+          const uint32_t w = __ballot_sync(0xffffffffu, m);
+          if (lane == 0) ss.valid[s][q] = w;
+#pragma unroll 1
+          for (int e = 0; e < 8; ++e) {
+            const int k = 4 * e + (lane >> 3), r = 32 * q + k;
+            const long long ro = __shfl_sync(0xffffffffu, off, k);
+            if (in_chunk && ((w >> k) & 1))
+              cp_async16(st + r * 128 + ((piece ^ (r & 7)) << 4), a.kv.base + ro + 128 * chunk + 16 * piece,
+                         16);
+          }
+          if (go && m) cp_async16(sc + (32 * q + lane) * 16, a.kv.base + off + a.kv_dim, 16);
+        }
+        cp_async_wait_all();
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ss.full[s]);
       }
-      cp_async_arrive_noinc(&ss.full[s]);
-      if (lane == 0 && !(box && go)) mbar_arrive(&ss.full[s]);
       ni += LOAD_WARPS;
       locate();
     }
-    cp_async_wait_all();
   } else if (warp >= WIDE_WARP && warp < WIDE_WARP + WIDE_WARPS) {
     // ------------------------------------------------------------ widening: 32 tokens of every tile
     regs_down<WIDE_REGS>();
@@ -670,8 +669,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 #pragma unroll 1
     for (int it = 0; it < total; ++it) {
       const int s = it % ST, b = it & 1;
-      warp_wait(&ss.full[s], (it / ST) & 1, a.status, abort);
-      if (it >= 2) warp_wait(&ss.pv_done[b], ((it >> 1) - 1) & 1, a.status, abort);
+      wait(&ss.full[s], (it / ST) & 1, a.status, abort);
+      if (it >= 2) wait(&ss.pv_done[b], ((it >> 1) - 1) & 1, a.status, abort);
       const uint8_t* src = sm + K_OFF + s * K_TILE + 32 * lw * 128;
       uint8_t* dst = sm + V_OFF + b * V_TILE + (piece >> 2) * K_TILE + 32 * lw * 128;
       uint4 v[8];
@@ -705,17 +704,16 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     __syncwarp();
 #pragma unroll 1
     for (int item = 0; next_item(a, plan, items, im); ++item) {
-      warp_wait(&ss.q_full, item & 1, a.status, abort);
+      wait(&ss.q_full, item & 1, a.status, abort);
       const int nqp = ss.cols;
       const bool merged = nqp <= MERGE;
       const uint32_t idesc = S_IDESC | ((uint32_t)((merged ? 2 * nqp : nqp) >> 3) << 17);
 #pragma unroll 1
       for (int i = 0; i < im.n; ++i, ++it) {
         const int st = it % ST, b = it & 1;
-        bool ok = warp_wait(&ss.full[st], (it / ST) & 1, a.status, abort);
-        if (it >= 2) ok &= warp_wait(&ss.p_full[b], ((it >> 1) - 1) & 1, a.status, abort);
+        bool ok = wait(&ss.full[st], (it / ST) & 1, a.status, abort);
+        if (it >= 2) ok &= wait(&ss.p_full[b], ((it >> 1) - 1) & 1, a.status, abort);
         if (ok && elect_one()) {
-          fence_proxy_async_shared();  // the copies, seen to have landed, before the MMA's reads
           tc_fence_after();
           if (i == 0) tc_cp_img(tmem + SF_Q, sm + QIMG_OFF);
           const uint64_t kd = desc_sw128(k0 + st * K_TILE);
@@ -762,8 +760,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 #pragma unroll 1
       for (int i = 0; i < im.n; ++i, ++it) {
         const int b = it & 1;
-        bool ok = warp_wait(&ss.p_full[b], (it >> 1) & 1, a.status, abort);
-        ok &= warp_wait(&ss.v_full[b], (it >> 1) & 1, a.status, abort);
+        bool ok = wait(&ss.p_full[b], (it >> 1) & 1, a.status, abort);
+        ok &= wait(&ss.v_full[b], (it >> 1) & 1, a.status, abort);
         if (i == 0) idesc = O_IDESC | ((uint32_t)(ss.cols >> 3) << 17);
         if (ok && elect_one()) {
           tc_fence_after();
@@ -959,13 +957,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   tc_fence_before();
   __syncthreads();
   if (warp == S_WARP) {
-    (void)warp_wait(&ss.drain, 0, a.status, abort);  // (at once unless a wait ran out before)
+    (void)wait(&ss.drain, 0, a.status, abort);  // (at once unless a wait ran out before)
     tc_fence_after();
     tmem_dealloc<512>(tmem);
   }
 }
 
-// Joins the pieces of a (row, head): a warp each, 4 (2) dimensions a lane.  Rows that one piece
+// Joins the pieces of a (row, head): a warp each, 4 dimensions a lane.  Rows that one piece
 // holds are done; pad rows and rows that see nothing get zeros.
 constexpr int JOIN_WARPS = 4;
 __global__ void __launch_bounds__(JOIN_WARPS * 32) attend_join_kernel(const Args ar, int grid) {
@@ -976,10 +974,10 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attend_join_kernel(const Args
   if (h >= a.n_q) return;
   const Shape sh = shape_of(a, grid);
   const RowInfo info = ar.rows[r];
-  const int per = a.head_dim / 32, d = lane * per;
+  const int d = 4 * lane & (a.head_dim - 1);
   __nv_bfloat16* o = a.o + r * a.o_stride + (long long)h * a.head_dim + d;
   if (info.tiles == 0) {
-    for (int e = 0; e < per; ++e) o[e] = __float2bfloat16_rn(0.0f);
+    *reinterpret_cast<uint2*>(o) = make_uint2(0u, 0u);
     if (lane == 0) a.lse[(long long)r * a.n_q + h] = -INFINITY;
     return;
   }
@@ -994,16 +992,31 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attend_join_kernel(const Args
     return ar.part + (((size_t)(k * 2 + slot) * sh.chunks + chunk) * NQ + c) * PART_LD;
   };
   float M = UNSET;
+#pragma unroll 1
   for (int k = k0 + lane; k <= k1; k += 32) M = fmaxf(M, piece(k)[0]);
   M = warp_max(M);
-  float num[4] = {0.0f, 0.0f, 0.0f, 0.0f}, den = 0.0f;
-  for (int k = k0; k <= k1; ++k) {
+  float4 num = {0.0f, 0.0f, 0.0f, 0.0f};
+  float den = 0.0f;
+  // 64 wide: the upper half warp takes every other piece
+  const int first = a.head_dim == 64 ? lane >> 4 : 0, step = a.head_dim == 64 ? 2 : 1;
+#pragma unroll 2
+  for (int k = k0 + first; k <= k1; k += step) {
     const float* p = piece(k);
     const float f = ex2(p[0] - M);
+    const float4 x = *reinterpret_cast<const float4*>(p + 4 + d);
     den = fmaf(f, p[1], den);
-    for (int e = 0; e < per; ++e) num[e] = fmaf(f, p[4 + d + e], num[e]);
+    num.x = fmaf(f, x.x, num.x), num.y = fmaf(f, x.y, num.y);
+    num.z = fmaf(f, x.z, num.z), num.w = fmaf(f, x.w, num.w);
   }
-  for (int e = 0; e < per; ++e) o[e] = __float2bfloat16_rn(den == 0.0f ? 0.0f : num[e] / den);
+  if (a.head_dim == 64) {
+    den += __shfl_xor_sync(0xffffffffu, den, 16);
+    num.x += __shfl_xor_sync(0xffffffffu, num.x, 16), num.y += __shfl_xor_sync(0xffffffffu, num.y, 16);
+    num.z += __shfl_xor_sync(0xffffffffu, num.z, 16), num.w += __shfl_xor_sync(0xffffffffu, num.w, 16);
+  }
+  const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+  if (den == 0.0f) num = {0.0f, 0.0f, 0.0f, 0.0f};
+  *reinterpret_cast<uint2*>(o) =
+      make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
   if (lane == 0)
     a.lse[(long long)r * a.n_q + h] = den == 0.0f ? -INFINITY : (log2f(den) + M) * LN2;
 }
@@ -1045,10 +1058,9 @@ __global__ void __launch_bounds__(TT) attend_weights_kernel(AttendArgs a, int ti
   }
 }
 
-// The records' codes as a 3D byte tensor [pages][tokens][kv_dim], boxes of 128 bytes x box tokens
-// under the 128-byte swizzle (bytes beyond kv_dim read as 0); false where its strides are beyond a
-// tensor map's.
-bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int kv_dim, int box) {
+// The records as a 3D byte tensor [pages][tokens][width], boxes of run (128: swizzled, bytes beyond
+// width read as 0) x box tokens; false where its strides are beyond a tensor map's.
+bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int width, int run, int box) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (!encode) {
     void* fn = nullptr;
@@ -1062,11 +1074,12 @@ bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int kv_dim, int box) 
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
   if (kv.stride_block >= (1ll << 40) || kv.stride_tok >= (1ll << 40)) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)kv_dim, (cuuint64_t)kv.block_size, (cuuint64_t)kv.num_blocks};
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)kv.block_size, (cuuint64_t)kv.num_blocks};
   const cuuint64_t strides[2] = {(cuuint64_t)kv.stride_tok, (cuuint64_t)kv.stride_block};
-  const cuuint32_t boxes[3] = {128, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
+  const cuuint32_t boxes[3] = {(cuuint32_t)run, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(kv.base), dims, strides,
-                boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                run == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1098,13 +1111,15 @@ cudaError_t attend_prepare() {
 
 cudaError_t launch_attend(const Launch& L, const AttendArgs& a, uint8_t* ws, int max_rows, int sms) {
   const Layout l = layout(max_rows, sms);
-  Args ar = {{}, 0, a, reinterpret_cast<float*>(ws + l.part), reinterpret_cast<RowInfo*>(ws + l.rows),
+  Args ar = {{}, {}, 0, a, reinterpret_cast<float*>(ws + l.part), reinterpret_cast<RowInfo*>(ws + l.rows),
              reinterpret_cast<int*>(ws + l.total)};
   // boxes of whole runs of a page, 8 rows (a swizzle atom) or more, that tiles are made of
   const int bs = a.kv.block_size;
   if (bs % 8 == 0 && a.kv.num_blocks <= INT32_MAX) {
     const int box = std::min(bs & -bs, TT);
-    if (encode_cache_map(&ar.map, a.kv, a.kv_dim, box)) ar.box = box;
+    if (encode_cache_map(&ar.codes, a.kv, a.kv_dim, 128, box) &&
+        encode_cache_map(&ar.scales, a.kv, a.kv_dim + 16, 16, box))
+      ar.box = box;
   }
   cudaError_t e = launch_ex(L, dim3(sms), dim3(THREADS), SMEM_BYTES, attend_kernel, ar);
   if (e == cudaSuccess)

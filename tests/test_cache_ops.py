@@ -54,7 +54,7 @@ def test_struct_layout_matches_header(tmp_path):
     (dict(n_q_heads=7), -2), (dict(n_q_heads=34), -2), (dict(n_q_heads=0), -2),
     (dict(block_size=0), -2), (dict(kv_record_bytes=128), -2), (dict(kv_record_bytes=150), -2),
     (dict(max_rows=0), -3), (dict(max_rows=1025), -3), (dict(max_req=0), -3),
-    (dict(max_req=1025), -3)])
+    (dict(max_req=513), -3)])
 def test_bad_layouts_are_refused(built, change, code):
     s = mc.CacheSpec(**dict(SPEC, max_rows=4, max_req=4, **{}) | change)
     h = C.c_void_p(1)
