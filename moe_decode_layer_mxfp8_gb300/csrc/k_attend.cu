@@ -50,12 +50,13 @@ constexpr int MERGE = 64;      // up to here both terms of the queries are colum
 constexpr int GROUP = 16;      // rows of a group at most
 constexpr int ST = 5;          // tiles in the ring
 constexpr int MAX_REQ = 512;
-constexpr int THREADS = 16 * 32;
-constexpr int SOFT_WARPS = 8, WIDE_WARP = 8, WIDE_WARPS = 4, S_WARP = 12, O_WARP = 13;
-constexpr int LOAD_WARP = 14, LOAD_WARPS = 2;
-// registers a thread: softmax warps take what the others give up (in all, the launch's 128)
-constexpr int SOFT_REGS = 168, WIDE_REGS = 96, MMA_REGS = 80;
-static_assert(SOFT_REGS * 256 + WIDE_REGS * 128 + MMA_REGS * 128 == 128 * THREADS, "register split");
+constexpr int THREADS = 24 * 32;
+constexpr int SOFT_WARPS = 16, SOFT = SOFT_WARPS * 32, GROUPS = SOFT_WARPS / 4;
+constexpr int WIDE_WARP = 16, WIDE_WARPS = 4, S_WARP = 20, O_WARP = 21;
+constexpr int LOAD_WARP = 22, LOAD_WARPS = 2;
+// registers a thread: softmax warps take what the others give up (in all, the launch's)
+constexpr int REGS = 80, SOFT_REGS = 88, OTHER_REGS = 64;
+static_assert(SOFT_REGS * SOFT + OTHER_REGS * 256 == REGS * THREADS, "register split");
 constexpr float JUMP = 24.0f;      // log2 of how far a weight may pass 1
 constexpr float UNSET = -1.0e30f;  // m_q of a query that has seen no token
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
@@ -76,7 +77,8 @@ constexpr int PLAN_OFF = SC_OFF + ST * TT * 16;
 constexpr int SMEM_BYTES = PLAN_OFF + (3 * MAX_REQ + 4) * 4 + 1024;
 static_assert(V_OFF % 1024 == 0 && P_OFF % 1024 == 0 && Q_OFF % 1024 == 0 && (NQ * 128) % 1024 == 0,
               "swizzle atoms");
-static_assert(SOFT_WARPS * (NQ / 2) * 32 * 4 <= V_TILE + 2 * NQ * 128, "the sums' scratch");
+constexpr int CMAX = NQ / GROUPS;  // columns of a softmax warp at most
+static_assert(SOFT_WARPS * CMAX * 32 * 4 <= V_TILE + 2 * NQ * 128, "the sums' scratch");
 
 // TMEM columns
 constexpr int S_COL = 0, O_COL = 256, SF_ONE = 384, SF_Q = 388;
@@ -246,7 +248,7 @@ __device__ __forceinline__ bool bar_any(int id, bool v) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // A wait for an mbarrier phase by a whole warp, in few instructions: some 10^7 polls (a good part
-// of a second) at most, none once another wait has run out.
+// of a second) at most, none once another wait has run out.  False if it ran out.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
   uint32_t polls = 0;
 #pragma unroll 1
@@ -254,11 +256,32 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status
     if (*abort || ++polls == (1u << 23)) {
       atomicOr(status, ST_WAIT_TIMEOUT);
       *abort = 1;
+      polls = ~0u;
       break;
     }
   }
-  return !__any_sync(0xffffffffu, *abort != 0);
+  return __all_sync(0xffffffffu, polls != ~0u);
 }
+// How an item's columns are dealt out (see the head of the file).
+struct Deal {
+  int nqp, streams, bufs;  // columns; streams of softmax groups; score buffers
+  __device__ explicit Deal(int cols) : nqp(cols), streams(cols <= 16 ? 4 : cols <= 48 ? 2 : 1) {
+    bufs = streams == 4 ? 4 : 2;
+  }
+  __device__ bool merged() const { return nqp <= MERGE; }
+  __device__ uint32_t s_col(int it) const { return S_COL + (256 / bufs) * (it & (bufs - 1)); }
+  __device__ int flat(int stream) const { return streams == 4 ? 16 * stream : 48 * stream; }
+  __device__ int slot(int it) const { return it & (bufs - 1); }
+  // parity of buffer slot(i)'s phase of an item's tile i, and the phases that an item of n tiles
+  // leaves (ph: the slots' parities at its start, a bit each)
+  __device__ uint32_t parity(uint32_t ph, int i) const { return ((ph >> slot(i)) ^ (i / bufs)) & 1; }
+  __device__ void advance(uint32_t& ph, int n) const {
+    for (int b = 0; b < bufs; ++b) ph ^= (uint32_t)((n + bufs - 1 - b) / bufs & 1) << b;
+  }
+  // where stream k's weights lie in the rows of the weights' buffer
+  __device__ int p_off(int stream) const { return streams == 4 ? 32 * stream : K_TILE * stream; }
+};
+
 // A maximum over the warp, every lane gets it (floats as ordered integers).
 __device__ __forceinline__ float warp_max_any(float v) {
   int i = __float_as_int(v);
@@ -268,45 +291,48 @@ __device__ __forceinline__ float warp_max_any(float v) {
 }
 
 struct Shared {
-  uint64_t full[ST], k_free[ST], s_full[2], p_full[2], v_full[2], pv_done[2], q_full, drain;
-  float neg_m[NQ], fac[NQ], red[SOFT_WARPS][NQ];
+  uint64_t full[ST], k_free[ST], s_full[4], p_full[4], pv_done[4], v_full[2], v_free[2], q_full, drain;
+  float neg_m[NQ], fac[NQ], red[SOFT_WARPS][CMAX];  // m and its change: [stream][column]
   uint32_t valid[ST][4];
   long long out[NQ];  // where a column's first value goes: o or the workspace
+  float fin[NQ][4];   // a column's factor for each stream's O
   int slice[NQ], group_row[GROUP], group_pos[GROUP];
   uint32_t tmem;
-  int cols, abort;
+  int cols, nrows, abort;
   Items start;
 };
-
 static_assert(SMEM_BYTES + sizeof(Shared) <= 227 * 1024, "shared memory");
 
 // What a softmax warp knows of its item.
 struct Soft {
   Span span;
-  int t0, n, it;        // the item's first tile and tile count, the ring's next tile
-  int nqp, c0;          // columns of the item, this half's first one
-  int nrows, cheads;    // its rows and the heads (columns) of each
-  int min_hi, max_lo;   // tokens that every row sees: [max_lo, min_hi] and the sinks
+  int t0, n, it;      // the item's first tile and tile count, the ring's next tile
+  int c0, col, flat;  // this group's first column; of its stream's set: in TMEM and in m
+  int first, stride;  // the group's tiles
+  int nrows, cheads;  // the item's rows and the heads (columns) of each
+  int min_hi, max_lo; // tokens that every row sees: [max_lo, min_hi] and the sinks
   float to_log2;
-  uint32_t tmem;        // with the warp's lane quadrant
+  uint32_t tmem;      // with the warp's lane quadrant
+  uint32_t p_row;     // the thread's row of its stream's weights, and their first 16-byte piece
+  uint32_t p_chunk;
+  uint32_t ph;        // the buffers' barriers' phases at the item's start
 };
 
-// The softmax of a half's C columns over an item's tiles, a token per thread; leaves the
+// The softmax of a group's C columns over its tiles of an item, a token per thread; leaves the
 // thread's share of every column's sum, in units of 2^m, in the scratch.
 template <int C>
-__device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, Shared& sh,
-                                           uint8_t* sm) {
+__device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, const Deal& deal,
+                                           Shared& sh, uint8_t* sm) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quad = warp & 3, half = warp >> 2, tok = 32 * quad + lane;
-  const bool merged = w.nqp <= MERGE;
+  const int quad = warp & 3, group = warp >> 2, tok = 32 * quad + lane;
+  const bool merged = deal.merged();
   volatile int* abort = &sh.abort;
   float l[C], s[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) l[c] = 0.0f;
 #pragma unroll 1
-  for (int i = 0; i < w.n; ++i) {
-    const int it = w.it + i, st = it % ST, b = it & 1;
-    const uint32_t ph = (it >> 1) & 1;
+  for (int i = w.first; i < w.n; i += w.stride) {
+    const int it = w.it + i, st = it % ST, b = deal.slot(i);
     const int t0 = w.span.token(w.t0 + i), t = t0 + tok;
     wait(&sh.full[st], (it / ST) & 1, a.status, abort);
     const float raw = reinterpret_cast<const float*>(sm + SC_OFF)[(st * TT + tok) * 4];
@@ -314,33 +340,26 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, S
     const bool fin = fabsf(raw) <= 3.0e38f;
     const float ct = fin ? raw * w.to_log2 : __int_as_float(0x7FC00000);
     const float sc = fin ? raw * P_UP : 0.0f;
-    // some of the tile's tokens are not every row's to see
-    const bool part = __any_sync(0xffffffffu, ok != 0xffffffffu || t0 + TT - 1 > w.min_hi ||
-                                                  (t0 < w.max_lo && t0 + TT > a.sinks));
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.k_free[st]);
-    uint32_t see[(C + 31) / 32];
-    if (__builtin_expect(part, 0)) {  // this half's columns that see the token
-#pragma unroll
-      for (int k = 0; k < (C + 31) / 32; ++k) see[k] = 0xffffffffu;
+    if (lane < w.stride) mbar_arrive(&sh.k_free[st]);  // (as many arrivals whoever takes the tile)
+    // some of the tile's tokens are not every row's to see
+    const bool part = ok != 0xffffffffu || t0 + TT - 1 > w.min_hi ||
+                      (t0 < w.max_lo && t0 + TT > a.sinks);
+    uint32_t see = 0xffffffffu;
+    if (__builtin_expect(part, 0)) {  // the group's columns that see the token
 #pragma unroll 1
       for (int j = 0; j < w.nrows; ++j) {
         const int hi = a.causal ? sh.group_pos[j] : w.span.hi;
         const int lo = a.window > 0 ? max(0, hi - a.window + 1) : 0;
         if (((ok >> lane) & 1) && t <= hi && (t >= lo || t < a.sinks)) continue;
-        // columns [c, c + cheads) of the item, from this half's first on
-        const int c = j * w.cheads - w.c0, e = c + w.cheads;
-#pragma unroll
-        for (int k = 0; k < (C + 31) / 32; ++k) {
-          const int x = min(max(c - 32 * k, 0), 32), y = min(max(e - 32 * k, 0), 32);
-          const uint32_t below_y = y == 32 ? 0xffffffffu : (1u << y) - 1;
-          const uint32_t below_x = x == 32 ? 0xffffffffu : (1u << x) - 1;
-          see[k] &= ~(below_y & ~below_x);
-        }
+        // columns [c, c + cheads) of the item, from this group's first on
+        const int c = j * w.cheads - w.c0;
+        const int x = min(max(c, 0), 31), y = min(max(c + w.cheads, 0), 31);
+        see &= ~((1u << y) - (1u << x));
       }
     }
-    wait(&sh.s_full[b], ph, a.status, abort);
-    const uint32_t scol = w.tmem + S_COL + 128 * b + w.c0;
+    wait(&sh.s_full[b], deal.parity(w.ph, i), a.status, abort);
+    const uint32_t scol = w.tmem + deal.s_col(i) + w.c0;
     // weights; a second round where some query's m has to move (always in an item's first tile)
 #pragma unroll 1
     for (bool moved = false;; moved = true) {
@@ -351,7 +370,7 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, S
 #pragma unroll
         for (int g = 0; g < C; g += 8) {
           float x[8];
-          tc_ld8(scol + w.nqp + g, x);
+          tc_ld8(scol + deal.nqp + g, x);
           tc_wait_ld();
           tc_loaded(x);
           tc_loaded(s + g);
@@ -363,7 +382,8 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, S
 #pragma unroll
         for (int g = 0; g < C; g += 8) tc_loaded(s + g);
       }
-      const float4* nm = reinterpret_cast<const float4*>(sh.neg_m + w.c0);
+      const float4* nm = reinterpret_cast<const float4*>(sh.neg_m + w.flat);
+      float top = -INFINITY;
 #pragma unroll
       for (int c = 0; c < C; c += 4) {
         const float4 m = nm[c / 4];
@@ -375,67 +395,68 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, S
       if (__builtin_expect(part, 0)) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
-          if (!((see[c / 32] >> (c % 32)) & 1)) s[c] = -INFINITY;
+          if (!((see >> c) & 1)) s[c] = -INFINITY;
       }
-      float top = -INFINITY;
 #pragma unroll
       for (int c = 0; c < C; ++c) top = fmaxf(top, s[c]);
-      if (__builtin_expect(!bar_any(2 + half, !moved && top > JUMP), 1)) break;
+      if (__builtin_expect(!bar_any(2 + group, !moved && top > JUMP), 1)) break;
       // the columns' largest scores of the tile
 #pragma unroll 1
       for (int g = 0; g < C; g += 8) {
-        const uint32_t bits = (g >= 32 ? see[(C - 1) / 32] : see[0]) >> (g & 31);
-        float x[8], y[8];
+        float x[8], y[8], mine = 0.0f;
         tc_ld8(scol + g, x);
-        if (merged) tc_ld8(scol + w.nqp + g, y);
+        if (merged) tc_ld8(scol + deal.nqp + g, y);
         tc_wait_ld();
         tc_loaded(x);
         if (merged) tc_loaded(y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float v = (merged ? x[e] + y[e] : x[e]) * ct;
-          if (!(v > -INFINITY) || (part && !((bits >> e) & 1))) v = -INFINITY;
+          if (!(v > -INFINITY) || !((see >> (g + e)) & 1)) v = -INFINITY;
           const float m = warp_max_any(v);
-          if (lane == 0) sh.red[warp][w.c0 + g + e] = m;
+          if (lane == e) mine = m;
         }
+        if (lane < 8) sh.red[warp][g + lane] = mine;
       }
-      bar_sync<128>(4 + half);
-      if (quad == 0)
-#pragma unroll 1
-        for (int c = w.c0 + lane; c < w.c0 + C; c += 32) {
-          const float(*r)[NQ] = sh.red + 4 * half;
-          const float m = fmaxf(fmaxf(r[0][c], r[1][c]), fmaxf(r[2][c], r[3][c]));
-          const float old = -sh.neg_m[c];
-          float f = 1.0f;
-          if (m - old > 0.5f * JUMP) {
-            const float now = fminf(ceilf(m), 3.0e38f);
-            f = old == UNSET ? 0.0f : ex2(old - now);
-            sh.neg_m[c] = -now;
-          }
-          sh.fac[c] = f;
+      bar_sync<128>(6 + group);
+      if (quad == 0 && lane < C) {
+        const float(*r)[CMAX] = sh.red + 4 * group;
+        const float m = fmaxf(fmaxf(r[0][lane], r[1][lane]), fmaxf(r[2][lane], r[3][lane]));
+        const float old = -sh.neg_m[w.flat + lane];
+        float f = 1.0f;
+        if (m - old > 0.5f * JUMP) {
+          const float now = fminf(ceilf(m), 3.0e38f);
+          f = old == UNSET ? 0.0f : ex2(old - now);
+          sh.neg_m[w.flat + lane] = -now;
         }
-      bar_sync<128>(4 + half);
+        sh.fac[w.flat + lane] = f;
+      }
+      bar_sync<128>(6 + group);
 #pragma unroll
-      for (int c = 0; c < C; ++c) l[c] *= sh.fac[w.c0 + c];
-      if (i > 0) {
-        wait(&sh.pv_done[b ^ 1], ((it - 1) >> 1) & 1, a.status, abort);
+      for (int c = 0; c < C; ++c) l[c] *= sh.fac[w.flat + c];
+      if (i >= w.stride) {
+        const int pi = i - w.stride;  // the group's tile before: its product is in O
+        wait(&sh.pv_done[deal.slot(pi)], deal.parity(w.ph, pi), a.status, abort);
         tc_fence_after();
 #pragma unroll 1
         for (int g = 0; g < C; g += 8) {
           float x[8];
-          const uint32_t oc = w.tmem + O_COL + w.c0 + g;
+          const uint32_t oc = w.tmem + O_COL + w.col + g;
           tc_ld8(oc, x);
           tc_wait_ld();
           tc_loaded(x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= sh.fac[w.c0 + g + e];
+          for (int e = 0; e < 8; ++e) x[e] *= sh.fac[w.flat + g + e];
           tc_st8(oc, x);
         }
         tc_wait_st();
       }
     }
     // weights times scales, rows of 128 bytes per token; the buffer's last reader has finished
-    if (it > 0) wait(&sh.pv_done[b ^ 1], ((it - 1) >> 1) & 1, a.status, abort);
+    if (i >= w.stride) {
+      const int pi = i - w.stride;
+      wait(&sh.pv_done[deal.slot(pi)], deal.parity(w.ph, pi), a.status, abort);
+    }
 #pragma unroll
     for (int g = 0; g < C; g += 8) {
       uint32_t o[4];
@@ -447,20 +468,21 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, S
         o[e / 2] = bf16x2_of(p0 * sc, p1 * sc);
       }
       const int col = w.c0 + g;
-      *reinterpret_cast<uint4*>(sm + P_OFF + (col >> 6) * K_TILE + tok * 128 +
-                                ((((col & 63) >> 3) ^ (tok & 7)) << 4)) =
+      *reinterpret_cast<uint4*>(sm + w.p_row + (col >> 6) * K_TILE +
+                                (((w.p_chunk + ((col & 63) >> 3)) ^ (tok & 7)) << 4)) =
           make_uint4(o[0], o[1], o[2], o[3]);
     }
     fence_proxy_async_shared();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.p_full[b]);
+    if (lane < w.stride) mbar_arrive(&sh.p_full[b]);
   }
   // every product of the item is done: the weights' and the queries' buffers are scratch
-  const int last = w.it + w.n - 1;
-  wait(&sh.pv_done[last & 1], (last >> 1) & 1, a.status, abort);
+#pragma unroll 1
+  for (int i = max(0, w.n - deal.bufs); i < w.n; ++i)
+    wait(&sh.pv_done[deal.slot(i)], deal.parity(w.ph, i), a.status, abort);
   tc_fence_after();
-  float* scratch = reinterpret_cast<float*>(sm + P_OFF) + warp * (NQ / 2) * 32 + lane;
+  float* scratch = reinterpret_cast<float*>(sm + P_OFF) + warp * CMAX * 32 + lane;
 #pragma unroll
   for (int c = 0; c < C; ++c) scratch[32 * c] = l[c];
 }
@@ -485,10 +507,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     // a tile is free when the first product, the widening and the softmax warps have read it
     for (int s = 0; s < ST; ++s)
       mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], 1 + WIDE_WARPS + SOFT_WARPS);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&ss.s_full[s], 1), mbar_init(&ss.pv_done[s], 1);
-      mbar_init(&ss.p_full[s], SOFT_WARPS), mbar_init(&ss.v_full[s], WIDE_WARPS);
-    }
+    for (int s = 0; s < 4; ++s)
+      mbar_init(&ss.s_full[s], 1), mbar_init(&ss.pv_done[s], 1), mbar_init(&ss.p_full[s], SOFT_WARPS);
+    for (int s = 0; s < 2; ++s) mbar_init(&ss.v_full[s], WIDE_WARPS), mbar_init(&ss.v_free[s], 1);
     mbar_init(&ss.q_full, SOFT_WARPS);
     mbar_init(&ss.drain, 2);
     ss.abort = 0;
@@ -572,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 
   if (warp >= LOAD_WARP) {
     // ------------------------------------------------------- loads: a warp takes every other tile
-    regs_down<MMA_REGS>();
+    regs_down<OTHER_REGS>();
     int ni = warp - LOAD_WARP;
     bool more = next_item(a, plan, items, im);
     // a lane per box of the next tile (of a token each without maps, four times): its page, on its
@@ -663,32 +684,35 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     }
   } else if (warp >= WIDE_WARP && warp < WIDE_WARP + WIDE_WARPS) {
     // ------------------------------------------------------------ widening: 32 tokens of every tile
-    regs_down<WIDE_REGS>();
+    regs_down<OTHER_REGS>();
     const int lw = warp - WIDE_WARP, piece = lane & 7, r4 = lane >> 3;
     const int total = items.left;
 #pragma unroll 1
     for (int it = 0; it < total; ++it) {
       const int s = it % ST, b = it & 1;
       wait(&ss.full[s], (it / ST) & 1, a.status, abort);
-      if (it >= 2) wait(&ss.pv_done[b], ((it >> 1) - 1) & 1, a.status, abort);
+      if (it >= 2) wait(&ss.v_free[b], ((it >> 1) - 1) & 1, a.status, abort);
       const uint8_t* src = sm + K_OFF + s * K_TILE + 32 * lw * 128;
       uint8_t* dst = sm + V_OFF + b * V_TILE + (piece >> 2) * K_TILE + 32 * lw * 128;
-      uint4 v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int row = 4 * e + r4;
-        v[e] = lds128(src + row * 128 + ((piece ^ (row & 7)) << 4));
-      }
+      for (int h = 0; h < 2; ++h) {
+        uint4 v[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int row = 4 * e + r4, c = 2 * (piece & 3);
-        uint4 x, y;
-        x.x = widen(__byte_perm(v[e].x, 0, 0x1404)), x.y = widen(__byte_perm(v[e].x, 0, 0x3424));
-        x.z = widen(__byte_perm(v[e].y, 0, 0x1404)), x.w = widen(__byte_perm(v[e].y, 0, 0x3424));
-        y.x = widen(__byte_perm(v[e].z, 0, 0x1404)), y.y = widen(__byte_perm(v[e].z, 0, 0x3424));
-        y.z = widen(__byte_perm(v[e].w, 0, 0x1404)), y.w = widen(__byte_perm(v[e].w, 0, 0x3424));
-        *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = x;
-        *reinterpret_cast<uint4*>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) = y;
+        for (int e = 0; e < 4; ++e) {
+          const int row = 16 * h + 4 * e + r4;
+          v[e] = lds128(src + row * 128 + ((piece ^ (row & 7)) << 4));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = 16 * h + 4 * e + r4, c = 2 * (piece & 3);
+          uint4 x, y;
+          x.x = widen(__byte_perm(v[e].x, 0, 0x1404)), x.y = widen(__byte_perm(v[e].x, 0, 0x3424));
+          x.z = widen(__byte_perm(v[e].y, 0, 0x1404)), x.w = widen(__byte_perm(v[e].y, 0, 0x3424));
+          y.x = widen(__byte_perm(v[e].z, 0, 0x1404)), y.y = widen(__byte_perm(v[e].z, 0, 0x3424));
+          y.z = widen(__byte_perm(v[e].w, 0, 0x1404)), y.w = widen(__byte_perm(v[e].w, 0, 0x3424));
+          *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = x;
+          *reinterpret_cast<uint4*>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) = y;
+        }
       }
       fence_proxy_async_shared();
       __syncwarp();
@@ -696,23 +720,24 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     }
   } else if (warp == S_WARP) {
     // ------------------------------------------------------------- the first product's MMAs
-    regs_down<MMA_REGS>();
+    regs_down<OTHER_REGS>();
     const uint32_t k0 = smem_u32(sm + K_OFF);
     const uint64_t q0 = desc_sw128(smem_u32(sm + Q_OFF));
     int it = 0;
+    uint32_t ph = 0;
     if (elect_one()) tc_cp_img(tmem + SF_ONE, sm + ONE_OFF);
     __syncwarp();
 #pragma unroll 1
     for (int item = 0; next_item(a, plan, items, im); ++item) {
       wait(&ss.q_full, item & 1, a.status, abort);
-      const int nqp = ss.cols;
-      const bool merged = nqp <= MERGE;
-      const uint32_t idesc = S_IDESC | ((uint32_t)((merged ? 2 * nqp : nqp) >> 3) << 17);
+      const Deal deal(ss.cols);
+      const bool merged = deal.merged();
+      const uint32_t idesc = S_IDESC | ((uint32_t)((merged ? 2 * deal.nqp : deal.nqp) >> 3) << 17);
 #pragma unroll 1
-      for (int i = 0; i < im.n; ++i, ++it) {
-        const int st = it % ST, b = it & 1;
-        bool ok = wait(&ss.full[st], (it / ST) & 1, a.status, abort);
-        if (it >= 2) ok &= wait(&ss.p_full[b], ((it >> 1) - 1) & 1, a.status, abort);
+      for (int i = 0; i < im.n; ++i) {
+        const int st = (it + i) % ST, b = deal.slot(i);
+        bool ok = wait(&ss.full[st], ((it + i) / ST) & 1, a.status, abort);
+        if (i >= deal.bufs) ok &= wait(&ss.p_full[b], deal.parity(ph, i - deal.bufs), a.status, abort);
         if (ok && elect_one()) {
           tc_fence_after();
           if (i == 0) tc_cp_img(tmem + SF_Q, sm + QIMG_OFF);
@@ -721,7 +746,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           for (int term = 0; term < (merged ? 1 : 2); ++term)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              tc_mma_mxf8(tmem + S_COL + 128 * b, kd + 2 * k, q0 + term * (NQ * 128 / 16) + 2 * k,
+              tc_mma_mxf8(tmem + deal.s_col(i), kd + 2 * k, q0 + term * (NQ * 128 / 16) + 2 * k,
                           idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), tmem + SF_ONE,
                           tmem + SF_Q, term > 0 || k > 0);
           tc_commit(&ss.s_full[b]);
@@ -729,12 +754,14 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         }
         __syncwarp();
       }
+      it += im.n;
+      deal.advance(ph, im.n);
     }
     if (elect_one()) tc_commit(&ss.drain);  // (what was issued has completed at this arrival)
     __syncwarp();
   } else if (warp == O_WARP) {
     // ------------------------------------------------------------ the second product's MMAs
-    regs_down<MMA_REGS>();
+    regs_down<OTHER_REGS>();
     const uint64_t v0 = desc_mn(smem_u32(sm + V_OFF), K_TILE);
     const uint64_t p0 = desc_mn(smem_u32(sm + P_OFF), K_TILE);
     // first, where the second kernel finds the rows' results
@@ -754,51 +781,58 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       if (lane == 0) ar.rows[r] = info;
     }
     int it = 0;
+    uint32_t ph = 0;
 #pragma unroll 1
-    while (next_item(a, plan, items, im)) {
-      uint32_t idesc = 0;
+    for (int item = 0; next_item(a, plan, items, im); ++item) {
+      wait(&ss.q_full, item & 1, a.status, abort);
+      const Deal deal(ss.cols);
+      const uint32_t idesc = O_IDESC | ((uint32_t)(deal.nqp >> 3) << 17);
 #pragma unroll 1
       for (int i = 0; i < im.n; ++i, ++it) {
-        const int b = it & 1;
-        bool ok = wait(&ss.p_full[b], (it >> 1) & 1, a.status, abort);
-        ok &= wait(&ss.v_full[b], (it >> 1) & 1, a.status, abort);
-        if (i == 0) idesc = O_IDESC | ((uint32_t)(ss.cols >> 3) << 17);
+        const int b = deal.slot(i), v = it & 1, stream = i & (deal.streams - 1);
+        bool ok = wait(&ss.p_full[b], deal.parity(ph, i), a.status, abort);
+        ok &= wait(&ss.v_full[v], (it >> 1) & 1, a.status, abort);
         if (ok && elect_one()) {
           tc_fence_after();
+          const uint64_t pd = p0 + (deal.p_off(stream) >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // 16 tokens each
-            mma_bf16(tmem + O_COL, v0 + b * (V_TILE / 16) + k * (2048 / 16), p0 + k * (2048 / 16),
-                     idesc, i > 0 || k > 0);
+            mma_bf16(tmem + O_COL + deal.flat(stream), v0 + v * (V_TILE / 16) + k * (2048 / 16),
+                     pd + k * (2048 / 16), idesc, i >= deal.streams || k > 0);
           tc_commit(&ss.pv_done[b]);
+          tc_commit(&ss.v_free[v]);
         }
         __syncwarp();
       }
+      deal.advance(ph, im.n);
     }
     if (elect_one()) tc_commit(&ss.drain);
     __syncwarp();
   } else {
     // ---------------------------------------------------------------------------- softmax
     regs_up<SOFT_REGS>();
-    const int quad = warp & 3, half = warp >> 2;
+    const int quad = warp & 3, group = warp >> 2;
     const int hpg = a.n_q / (a.kv_dim / a.head_dim);
     const int cheads = hpg * (chunk_bytes > a.head_dim ? 2 : 1);  // heads per row of this chunk
     const int dshift = a.head_dim == 64 ? 6 : 7;
     Soft w;
     w.it = 0;
+    w.ph = 0;
     w.cheads = cheads;
     w.to_log2 = a.scale * LOG2E;
     w.tmem = tmem + ((uint32_t)(32 * quad) << 16);
 #pragma unroll 1
     while (next_item(a, plan, items, im)) {
       // ---- the group's rows and queries
-      bar_sync<256>(1);  // the previous item's columns are no longer in use
+      bar_sync<SOFT>(1);  // the previous item's columns are no longer in use
       if (warp == 0) {
         const int first = im.group * sh.rows_per;
         int seen = 0, n = 0;
 #pragma unroll 1
         for (int r0 = 0; r0 < a.rows && n < sh.rows_per; r0 += 32) {
           const int r = r0 + lane;
-          const int p = r < a.rows && a.row_req[r] == im.b ? a.positions[r] : -1;
+          const int q = r < a.rows ? a.row_req[r] : -1, p0 = r < a.rows ? a.positions[r] : -1;
+          const int p = q == im.b ? p0 : -1;
           const uint32_t m = __ballot_sync(0xffffffffu, p >= 0);
           const int rank = seen + __popc(m & ((1u << lane) - 1)) - first;
           if (p >= 0 && rank >= 0 && rank < sh.rows_per)
@@ -806,17 +840,20 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           seen += __popc(m);
           n = max(0, min(sh.rows_per, seen - first));
         }
-        if (lane == 0) ss.cols = ((n * cheads + 15) & ~15) | (n << 16);
+        const int cols = (n * cheads + 15) & ~15;
+        if (lane == 0) ss.cols = cols == 80 ? 96 : cols, ss.nrows = n;
       }
-      bar_sync<256>(1);
-      const int nrows = ss.cols >> 16, nqp = ss.cols & 0xFFFF, nq = nrows * cheads;
-      const bool merged = nqp <= MERGE;
+      bar_sync<SOFT>(1);
+      const int nrows = ss.nrows, nq = nrows * cheads;
+      const Deal deal(ss.cols);
+      const int nqp = deal.nqp;
+      const bool merged = deal.merged();
       const bool whole = im.n == im.span.tiles;  // nobody else has tiles of this group
       const long long slot = (long long)(team * 2 + (im.t0 > 0 ? 0 : 1)) * sh.chunks + chunk;
-      if (tid < nqp) {
+      if (tid < NQ) {
+        ss.neg_m[tid] = -UNSET;
         const int j = tid / cheads, h = tid - j * cheads, sl = h / hpg;
         const long long head = (long long)chunk * sh.heads + h;
-        ss.neg_m[tid] = -UNSET;
         ss.slice[tid] = tid < nq ? sl : -1;
         if (tid < nq)
           ss.out[tid] = whole ? ss.group_row[j] * a.o_stride + head * a.head_dim
@@ -825,7 +862,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       // queries as two e4m3 terms, rows of 128 bytes: hi in row c, lo in row nqp + c (merged)
       // or NQ + c
 #pragma unroll 1
-      for (int i = tid; i < nqp * 16; i += 256) {  // first copied as they are, all at once
+      for (int i = tid; i < nqp * 16; i += SOFT) {  // first copied as they are, all at once
         const int c = i >> 4, d = (i & 15) * 8;
         const int j = c / cheads, h = c - j * cheads, sl = h / hpg;
         const bool in = c < nq && (d >> dshift) == sl;
@@ -836,11 +873,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                    in ? 16 : 0);
       }
       cp_async_wait_all();
+      // (every lane takes part in the blocks' maxima)
 #pragma unroll 1
-      for (int i = tid; i < nqp * 16; i += 256) {
-        const int c = i >> 4, d = (i & 15) * 8;
+      for (int i = tid; i < ((nqp * 16 + SOFT - 1) & ~(SOFT - 1)); i += SOFT) {
+        const bool live = i < nqp * 16;
+        const int c = live ? i >> 4 : 0, d = (i & 15) * 8;
         float v[8];
-        bf16x8_to_f32(lds128(sm + P_OFF + i * 16), v);
+        bf16x8_to_f32(live ? lds128(sm + P_OFF + i * 16) : make_uint4(0, 0, 0, 0), v);
         float m = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -861,6 +900,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         }
         const int rl = (merged ? nqp : NQ) + c;
         const int o = (d >> 4), x = d & 8;
+        if (!live) continue;
         *reinterpret_cast<uint2*>(sm + Q_OFF + c * 128 + ((o ^ (c & 7)) << 4) + x) =
             make_uint2(hw[0], hw[1]);
         *reinterpret_cast<uint2*>(sm + Q_OFF + rl * 128 + ((o ^ (rl & 7)) << 4) + x) =
@@ -871,6 +911,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         }
       }
       fence_proxy_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ss.q_full);
       w.min_hi = 0x7FFFFFFF;
       w.max_lo = 0;
 #pragma unroll 1
@@ -879,75 +921,94 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         w.min_hi = min(w.min_hi, hi);
         w.max_lo = max(w.max_lo, a.window > 0 ? max(0, hi - a.window + 1) : 0);
       }
-      bar_sync<256>(1);
-      if (tid == 0) ss.cols = nqp;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ss.q_full);
+      bar_sync<SOFT>(1);  // (the staged queries have been read: weights may take their place)
       w.span = im.span;
       w.t0 = im.t0;
       w.n = im.n;
-      w.nqp = nqp;
       w.nrows = nrows;
-      const int cols = nqp / 2;
-      w.c0 = half * cols;
-      switch (cols) {
-        case 8: soft_tiles<8>(a, w, ss, sm); break;
-        case 16: soft_tiles<16>(a, w, ss, sm); break;
-        case 24: soft_tiles<24>(a, w, ss, sm); break;
-        case 32: soft_tiles<32>(a, w, ss, sm); break;
-        case 40: soft_tiles<40>(a, w, ss, sm); break;
-        default: soft_tiles<48>(a, w, ss, sm); break;
-      }
+      const int stream = group & (deal.streams - 1), cols = nqp * deal.streams / GROUPS;
+      w.first = stream;
+      w.stride = deal.streams;
+      w.c0 = group / deal.streams * cols;
+      w.flat = deal.flat(stream) + w.c0;
+      w.col = w.flat;
+      w.p_row = P_OFF + (32 * quad + lane) * 128 + (deal.streams == 2 ? K_TILE * stream : 0);
+      w.p_chunk = deal.streams == 4 ? 2 * stream : 0;
+      if (cols == 16)
+        soft_tiles<16>(a, w, deal, ss, sm);
+      else
+        soft_tiles<24>(a, w, deal, ss, sm);
       w.it += im.n;
+      deal.advance(w.ph, im.n);
 
       // ---- the item's result: the columns' sums over the tokens, then O
       const float* scratch = reinterpret_cast<const float*>(sm + P_OFF);
       __syncwarp();
-#pragma unroll 1
-      for (int c = lane; c < cols; c += 32) {  // this warp's share of each
+      if (lane < cols) {  // this warp's share of each
         float v = 0.0f;
 #pragma unroll 4
-        for (int k = 0; k < 32; ++k) v += scratch[(warp * (NQ / 2) + c) * 32 + ((k + lane) & 31)];
-        ss.red[warp][w.c0 + c] = v;
+        for (int k = 0; k < 32; ++k) v += scratch[(warp * CMAX + lane) * 32 + ((k + lane) & 31)];
+        ss.red[warp][lane] = v;
       }
-      bar_sync<256>(1);
+      bar_sync<SOFT>(1);
       if (tid < nq) {
-        const float(*r)[NQ] = ss.red + (tid < cols ? 0 : 4);
-        const float lt = (r[0][tid] + r[1][tid]) + (r[2][tid] + r[3][tid]);
-        const float m = -ss.neg_m[tid];
+        // the streams' sums and O in the largest m (one stream: as they are)
+        float m = UNSET, lt = 0.0f;
+#pragma unroll 1
+        for (int k = 0; k < min(deal.streams, im.n); ++k) m = fmaxf(m, -ss.neg_m[deal.flat(k) + tid]);
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          float f = 0.0f;
+          if (k < min(deal.streams, im.n)) {
+            const int g = k + tid / cols * deal.streams, c = tid % cols;
+            const float(*r)[CMAX] = ss.red + 4 * g;
+            const float mk = -ss.neg_m[deal.flat(k) + tid];
+            const float lk = (r[0][c] + r[1][c]) + (r[2][c] + r[3][c]);
+            f = lk != lk ? 1.0f : mk == UNSET ? 0.0f : ex2(mk - m);  // (a NaN stays one)
+            if (f != 0.0f) lt = fmaf(lk, f, lt);
+          }
+          ss.fin[tid][k] = f;
+        }
+        const float up = !whole ? O_UP : lt == 0.0f ? 0.0f : O_UP / lt;
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) ss.fin[tid][k] *= up;
         if (whole) {
           const int j = tid / cheads;
-          ss.fac[tid] = lt == 0.0f ? 0.0f : O_UP / lt;
           a.lse[(long long)ss.group_row[j] * a.n_q + chunk * sh.heads + tid - j * cheads] =
               lt == 0.0f ? -INFINITY : (log2f(lt) + m) * LN2;
         } else {
-          ss.fac[tid] = O_UP;
           ar.part[ss.out[tid] - 4] = m;
           ar.part[ss.out[tid] - 3] = lt;
         }
       }
-      bar_sync<256>(1);
+      bar_sync<SOFT>(1);
       const int d = 32 * quad + lane;  // this thread's dimension of the chunk
       const int sl = d >> dshift, dl = d - (sl << dshift);
 #pragma unroll 1
-      for (int c8 = 8 * half; c8 < nqp; c8 += 16) {
-        float x[8], f[8];
-        long long at[8];
-        tc_ld8(w.tmem + O_COL + c8, x);
+      for (int c8 = 8 * group; c8 < nqp; c8 += 8 * GROUPS) {
+        float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          f[e] = ss.fac[c8 + e];
-          at[e] = ss.slice[c8 + e] == sl ? ss.out[c8 + e] + dl : -1;
+        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+#pragma unroll 1
+        for (int k = 0; k < min(deal.streams, im.n); ++k) {
+          float x[8];
+          tc_ld8(w.tmem + O_COL + deal.flat(k) + c8, x);
+          tc_wait_ld();
+          tc_loaded(x);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float f = ss.fin[c8 + e][k];
+            if (f != 0.0f) v[e] = fmaf(x[e], f, v[e]);
+          }
         }
-        tc_wait_ld();
-        tc_loaded(x);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float v = f[e] == 0.0f ? 0.0f : x[e] * f[e];
+          const long long at = ss.out[c8 + e] + dl;
+          const bool mine = ss.slice[c8 + e] == sl;
           if (whole) {
-            if (at[e] >= 0) a.o[at[e]] = __float2bfloat16_rn(v);
+            if (mine) a.o[at] = __float2bfloat16_rn(v[e]);
           } else {
-            if (at[e] >= 0) ar.part[at[e]] = v;
+            if (mine) ar.part[at] = v[e];
           }
         }
       }
@@ -1101,10 +1162,10 @@ Layout layout(int max_rows, int sms) {
 size_t attend_workspace_bytes(int max_rows, int sms) { return layout(max_rows, sms).bytes; }
 
 cudaError_t attend_prepare() {
-  // the roles' register split adds up to what a block launches with: 128 a thread
+  // the roles' register split adds up to what a block launches with
   cudaFuncAttributes f;
   cudaError_t e = cudaFuncGetAttributes(&f, attend_kernel);
-  if (e == cudaSuccess && f.numRegs != 128) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess && f.numRegs != REGS) e = cudaErrorInvalidConfiguration;
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
 }
