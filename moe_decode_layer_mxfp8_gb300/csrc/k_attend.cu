@@ -10,11 +10,12 @@
 // share its context (1 to 96 columns, no padding beyond 16), so the cache is read once for all of
 // them.  The first product takes the e4m3 tile as it lies in the cache (kind::mxf8f6f4); a bf16
 // query is the exact sum of two e4m3 terms under one power-of-two scale per 32 dimensions.  The
-// second takes P scale_t in bf16 (the one rounding between the scores and o: 8 bits, as o
-// itself, of a weight of any size) and the tile widened to bf16: moving a code's bits into place
-// reads as 2^-120 of its value, which P's own factor makes up for.  (Weights as two e4m3 terms
-// under block scales would spare the widening, but cost each weight three times the
-// instructions: 270 us against 60 at 48 rows over 8 contexts of 1K..64K.)
+// second takes P scale_t in f16 (the one rounding between the scores and o: 11 bits) and the tile
+// widened to f16, which is exact.  m_q is chosen so that the largest P scale_t is about 2^6: what
+// f16 cannot hold lies 2^-31 below it.  (Weights as two e4m3 terms under block scales would spare
+// the widening, but cost each weight three times the instructions: 270 us against
+// 145 at 48 rows over 8 contexts of 1K..64K when both were young; weights in bf16 took three
+// instructions per two codes to widen the tile, f16 takes one.)
 // O stays in TMEM over a whole run of tiles: m_q, an integer, moves only when a weight passes it
 // by far (then O is rescaled, exactly).
 //
@@ -57,12 +58,11 @@ constexpr int LOAD_WARP = 22, LOAD_WARPS = 2;
 // registers a thread: softmax warps take what the others give up (in all, the launch's)
 constexpr int REGS = 80, SOFT_REGS = 88, OTHER_REGS = 64;
 static_assert(SOFT_REGS * SOFT + OTHER_REGS * 256 == REGS * THREADS, "register split");
-constexpr float JUMP = 24.0f;      // log2 of how far a weight may pass 1
+// log2 of a weight times its token's scale: at most TOP, and m_q puts the largest of the tile that
+// moves it at BASE; scales below 2^LEAST (and zeros) count as that in the choice of m_q
+constexpr float TOP = 15.0f, BASE = 6.0f, LEAST = -90.0f;
 constexpr float UNSET = -1.0e30f;  // m_q of a query that has seen no token
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-// P carries 2^64 and the widened codes 2^-120: O is 2^-56 of its value, and a token's scale may
-// reach 2^39 beside a weight of 2^JUMP
-constexpr float P_UP = 18446744073709551616.0f, O_UP = 72057594037927936.0f;
 
 constexpr int K_TILE = TT * 128, V_TILE = 2 * K_TILE;
 constexpr int K_OFF = 0;
@@ -85,9 +85,8 @@ constexpr int S_COL = 0, O_COL = 256, SF_ONE = 384, SF_Q = 388;
 // Instruction descriptors, M = 128; N, and the scale-byte selectors, are or-ed in.
 // kind::mxf8f6f4: e4m3 x e4m3, E8M0 scales, both K-major.
 constexpr uint32_t S_IDESC = (1u << 23) | ((uint32_t)(TT >> 4) << 24);
-// kind::f16: bf16 x bf16, f32 accumulators, both MN-major.
-constexpr uint32_t O_IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
-                             ((uint32_t)(TT >> 4) << 24);
+// kind::f16: f16 x f16, f32 accumulators, both MN-major.
+constexpr uint32_t O_IDESC = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(TT >> 4) << 24);
 
 // The step as every CTA derives it: per request its rows' largest and smallest position, and
 // the units (tiles times row groups) of all requests before it.
@@ -195,27 +194,46 @@ struct Args {
 };
 constexpr int PART_LD = 128 + 4;
 
+__device__ __forceinline__ float log2_of(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Two f32 as bf16, the first in the low half.
-__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+// Two f32 as f16, the first in the low half.
+__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
   uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Two e4m3 codes, in the high bytes of the halves of u, as bf16 numbers of 2^-120 of their value
-// (sign, four exponent and three mantissa bits moved into place; a NaN code reads as 480).
-__device__ __forceinline__ uint32_t widen(uint32_t u) {
-  return (u & 0x80008000u) | ((u >> 4) & 0x07F007F0u);
+// Packed f32 arithmetic.
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float bx, float by) {  // x = x a + bx
+  asm("{\n .reg .b64 s, m, b;\n mov.b64 s, {%0, %1};\n mov.b64 m, {%2, %2};\n mov.b64 b, {%3, %4};\n"
+      " fma.rn.f32x2 s, s, m, b;\n mov.b64 {%0, %1}, s;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(bx), "f"(by));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float bx, float by) {
+  asm("{\n .reg .b64 s, b;\n mov.b64 s, {%0, %1};\n mov.b64 b, {%2, %3};\n"
+      " add.rn.f32x2 s, s, b;\n mov.b64 {%0, %1}, s;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(bx), "f"(by));
+}
+__device__ __forceinline__ void mul2(float& x, float& y, float a) {
+  asm("{\n .reg .b64 s, m;\n mov.b64 s, {%0, %1};\n mov.b64 m, {%2, %2};\n"
+      " mul.rn.f32x2 s, s, m;\n mov.b64 {%0, %1}, s;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(a));
 }
 // Matrix descriptor as desc_sw128, MN-major with `lbo` bytes between 128-byte runs along MN.
 __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
   return (desc_sw128(saddr) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(lbo >> 4) << 16);
 }
-__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred q;\n setp.ne.b32 q, %4, 0;\n"
@@ -293,7 +311,7 @@ __device__ __forceinline__ float warp_max_any(float v) {
 struct Shared {
   uint64_t full[ST], k_free[ST], s_full[4], p_full[4], pv_done[4], v_full[2], v_free[2], q_full, drain;
   float neg_m[NQ], fac[NQ], red[SOFT_WARPS][CMAX];  // m and its change: [stream][column]
-  uint32_t valid[ST][4];
+  uint32_t valid[ST][4], mask[ST];  // tokens that are there; whether some row masks some token
   long long out[NQ];  // where a column's first value goes: o or the workspace
   float fin[NQ][4];   // a column's factor for each stream's O
   int slice[NQ], group_row[GROUP], group_pos[GROUP];
@@ -339,7 +357,8 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
     const uint32_t ok = sh.valid[st][quad];
     const bool fin = fabsf(raw) <= 3.0e38f;
     const float ct = fin ? raw * w.to_log2 : __int_as_float(0x7FC00000);
-    const float sc = fin ? raw * P_UP : 0.0f;
+    const float sc = fin ? raw : 0.0f;
+    const float lsc = sc > 0.0f ? fmaxf(log2_of(sc), LEAST) : LEAST;
     __syncwarp();
     if (lane < w.stride) mbar_arrive(&sh.k_free[st]);  // (as many arrivals whoever takes the tile)
     // some of the tile's tokens are not every row's to see
@@ -387,10 +406,8 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
 #pragma unroll
       for (int c = 0; c < C; c += 4) {
         const float4 m = nm[c / 4];
-        s[c] = fmaf(s[c], ct, m.x);
-        s[c + 1] = fmaf(s[c + 1], ct, m.y);
-        s[c + 2] = fmaf(s[c + 2], ct, m.z);
-        s[c + 3] = fmaf(s[c + 3], ct, m.w);
+        fma2(s[c], s[c + 1], ct, m.x, m.y);
+        fma2(s[c + 2], s[c + 3], ct, m.z, m.w);
       }
       if (__builtin_expect(part, 0)) {
 #pragma unroll
@@ -399,8 +416,8 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
       }
 #pragma unroll
       for (int c = 0; c < C; ++c) top = fmaxf(top, s[c]);
-      if (__builtin_expect(!bar_any(2 + group, !moved && top > JUMP), 1)) break;
-      // the columns' largest scores of the tile
+      if (__builtin_expect(!bar_any(2 + group, !moved && top + lsc > TOP), 1)) break;
+      // the columns' largest weights times scales of the tile
 #pragma unroll 1
       for (int g = 0; g < C; g += 8) {
         float x[8], y[8], mine = 0.0f;
@@ -411,7 +428,7 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
         if (merged) tc_loaded(y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float v = (merged ? x[e] + y[e] : x[e]) * ct;
+          float v = fmaf(merged ? x[e] + y[e] : x[e], ct, lsc);
           if (!(v > -INFINITY) || !((see >> (g + e)) & 1)) v = -INFINITY;
           const float m = warp_max_any(v);
           if (lane == e) mine = m;
@@ -424,8 +441,8 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
         const float m = fmaxf(fmaxf(r[0][lane], r[1][lane]), fmaxf(r[2][lane], r[3][lane]));
         const float old = -sh.neg_m[w.flat + lane];
         float f = 1.0f;
-        if (m - old > 0.5f * JUMP) {
-          const float now = fminf(ceilf(m), 3.0e38f);
+        if (m - old > BASE) {
+          const float now = fminf(ceilf(m) - BASE, 3.0e38f);
           f = old == UNSET ? 0.0f : ex2(old - now);
           sh.neg_m[w.flat + lane] = -now;
         }
@@ -462,10 +479,10 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
       uint32_t o[4];
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
-        const float p0 = ex2(s[g + e]), p1 = ex2(s[g + e + 1]);
-        l[g + e] += p0;
-        l[g + e + 1] += p1;
-        o[e / 2] = bf16x2_of(p0 * sc, p1 * sc);
+        float p0 = ex2(s[g + e]), p1 = ex2(s[g + e + 1]);
+        add2(l[g + e], l[g + e + 1], p0, p1);
+        mul2(p0, p1, sc);
+        o[e / 2] = f16x2_of(p0, p1);
       }
       const int col = w.c0 + g;
       *reinterpret_cast<uint4*>(sm + w.p_row + (col >> 6) * K_TILE +
@@ -485,6 +502,14 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
   float* scratch = reinterpret_cast<float*>(sm + P_OFF) + warp * CMAX * 32 + lane;
 #pragma unroll
   for (int c = 0; c < C; ++c) scratch[32 * c] = l[c];
+}
+
+__device__ __forceinline__ uint32_t without_nan(uint32_t v) {
+  const uint32_t nan = (((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
+  return v & ~(nan * 0xFFu);
+}
+__device__ __forceinline__ uint4 without_nan(uint4 v) {
+  return make_uint4(without_nan(v.x), without_nan(v.y), without_nan(v.z), without_nan(v.w));
 }
 
 __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constant__ Args ar) {
@@ -624,6 +649,12 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       if (row[q] >= 0 && !m) atomicOr(a.status, ST_UNMAPPED_PAGE);
       return m;
     };
+    auto masks = [&](uint32_t there) {  // for some row of the request
+      const int first = a.causal ? plan.pmin[im.b] : im.span.hi;
+      const int last_lo = a.window > 0 ? max(0, im.span.hi - a.window + 1) : 0;
+      return (uint32_t)(there != 0xffffffffu || t0 + TT - 1 > first ||
+                        (t0 < last_lo && t0 + TT > a.sinks));
+    };
     locate();
 #pragma unroll 1
     for (int it = warp - LOAD_WARP; more; it += LOAD_WARPS) {
@@ -632,9 +663,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       if (it >= ST) go = wait(&ss.k_free[s], ((it / ST) - 1) & 1, a.status, abort);
       uint8_t* st = sm + K_OFF + s * K_TILE;
       uint8_t* sc = sm + SC_OFF + s * TT * 16;
+      uint32_t there = 0xffffffffu;
       if (ar.box) {
         // boxes with a token to see; their other tokens, and what the rest of the slot holds, are
-        // masked (widening makes any code a number)
+        // masked
         const bool m = mapped(0);
         const uint32_t have = __ballot_sync(0xffffffffu, m);
 #pragma unroll
@@ -644,7 +676,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                            (t >= im.span.lo || t < a.sinks);
           const uint32_t w = __ballot_sync(0xffffffffu, see);
           if (lane == q) ss.valid[s][q] = w;
+          there &= w;
         }
+        if (lane == 0) ss.mask[s] = masks(there);
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&ss.full[s], go ? __popc(have) * box * (128 + 16) : 0);
         __syncwarp();
@@ -664,6 +698,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           const long long off = m ? pg * a.kv.stride_block + rw * a.kv.stride_tok : 0;
           const uint32_t w = __ballot_sync(0xffffffffu, m);
           if (lane == 0) ss.valid[s][q] = w;
+          there &= w;
 #pragma unroll 1
           for (int e = 0; e < 8; ++e) {
             const int k = 4 * e + (lane >> 3), r = 32 * q + k;
@@ -674,6 +709,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           }
           if (go && m) cp_async16(sc + (32 * q + lane) * 16, a.kv.base + off + a.kv_dim, 16);
         }
+        if (lane == 0) ss.mask[s] = masks(there);
         cp_async_wait_all();
         fence_proxy_async_shared();
         __syncwarp();
@@ -692,6 +728,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       const int s = it % ST, b = it & 1;
       wait(&ss.full[s], (it / ST) & 1, a.status, abort);
       if (it >= 2) wait(&ss.v_free[b], ((it >> 1) - 1) & 1, a.status, abort);
+      const bool mask = ss.mask[s] != 0;
       const uint8_t* src = sm + K_OFF + s * K_TILE + 32 * lw * 128;
       uint8_t* dst = sm + V_OFF + b * V_TILE + (piece >> 2) * K_TILE + 32 * lw * 128;
 #pragma unroll
@@ -704,12 +741,16 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
+          // a NaN code that some row must not see would reach it as 0 * NaN (rows that do see the
+          // token are NaN by their scores)
+          if (__builtin_expect(mask, 0)) v[e] = without_nan(v[e]);
           const int row = 16 * h + 4 * e + r4, c = 2 * (piece & 3);
           uint4 x, y;
-          x.x = widen(__byte_perm(v[e].x, 0, 0x1404)), x.y = widen(__byte_perm(v[e].x, 0, 0x3424));
-          x.z = widen(__byte_perm(v[e].y, 0, 0x1404)), x.w = widen(__byte_perm(v[e].y, 0, 0x3424));
-          y.x = widen(__byte_perm(v[e].z, 0, 0x1404)), y.y = widen(__byte_perm(v[e].z, 0, 0x3424));
-          y.z = widen(__byte_perm(v[e].w, 0, 0x1404)), y.w = widen(__byte_perm(v[e].w, 0, 0x3424));
+          uint32_t f[2];
+          e4m3x4_to_f16x4(v[e].x, f), x.x = f[0], x.y = f[1];
+          e4m3x4_to_f16x4(v[e].y, f), x.z = f[0], x.w = f[1];
+          e4m3x4_to_f16x4(v[e].z, f), y.x = f[0], y.y = f[1];
+          e4m3x4_to_f16x4(v[e].w, f), y.z = f[0], y.w = f[1];
           *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = x;
           *reinterpret_cast<uint4*>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) = y;
         }
@@ -797,7 +838,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           const uint64_t pd = p0 + (deal.p_off(stream) >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // 16 tokens each
-            mma_bf16(tmem + O_COL + deal.flat(stream), v0 + v * (V_TILE / 16) + k * (2048 / 16),
+            tc_mma_f16(tmem + O_COL + deal.flat(stream), v0 + v * (V_TILE / 16) + k * (2048 / 16),
                      pd + k * (2048 / 16), idesc, i >= deal.streams || k > 0);
           tc_commit(&ss.pv_done[b]);
           tc_commit(&ss.v_free[v]);
@@ -969,7 +1010,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           }
           ss.fin[tid][k] = f;
         }
-        const float up = !whole ? O_UP : lt == 0.0f ? 0.0f : O_UP / lt;
+        const float up = !whole ? 1.0f : lt == 0.0f ? 0.0f : 1.0f / lt;
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) ss.fin[tid][k] *= up;
         if (whole) {
