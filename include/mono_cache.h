@@ -100,7 +100,10 @@ int mono_cache_attend(mono_cache_t *h, const mono_attend_args *args, void *strea
  * stride, compacts them in place; any other overlap is undefined.  new_lengths may be lengths.
  * No two requests may share a page.  Slots and pages beyond the kept tokens are left as they
  * were.  Lengths beyond the pages of the table or the weights' rows are cut to them, records of
- * unmapped pages are not moved; both raise MONO_STATUS_UNMAPPED_PAGE.
+ * unmapped pages are not moved; both raise MONO_STATUS_UNMAPPED_PAGE.  A call keeps at most
+ * 2^24 tokens over its requests, each counted with the budget (or what its table or weights
+ * row hold, if less) rounded up to 64: MONO_ERR_TOO_MANY_ROWS.  Calls share the handle's workspace,
+ * as mono_cache_attend's do.
  */
 typedef struct {
   const float *weights;       /* [n_req, weights_stride] */

@@ -68,7 +68,11 @@ size_t attend_workspace_bytes(int max_rows, int sms);
 cudaError_t attend_prepare();  // raises the dynamic shared-memory limit
 cudaError_t launch_attend(const Launch&, const AttendArgs&, uint8_t* workspace, int max_rows,
                           int sms);
-cudaError_t launch_evict(const Launch&, const EvictArgs&);
-cudaError_t launch_verify(const Launch&, const VerifyArgs&, int dtype);
+constexpr int EVICT_MAX_CHUNKS = 1 << 18;  // moves of 64 kept tokens that a call may have
+size_t evict_workspace_bytes(int max_req);
+bool evict_fits(int n_req, int budget, long long cap);
+cudaError_t evict_prepare();
+cudaError_t launch_evict(const Launch&, const EvictArgs&, uint8_t* workspace, int max_req, int sms);
+cudaError_t launch_verify(const Launch&, const VerifyArgs&, int dtype, int sms);
 
 }  // namespace mono

@@ -1,5 +1,6 @@
 // Host side of the cache operators' C ABI (include/mono_cache.h): argument checks, the
 // workspace, launches.
+#include <algorithm>
 #include <cmath>
 #include <new>
 
@@ -14,6 +15,7 @@ struct mono_cache {
   uint8_t* arena = nullptr;
   float* lse = nullptr;
   uint8_t* attend_ws = nullptr;
+  uint8_t* evict_ws = nullptr;
   int sms = 0;
   int* status = nullptr;
 };
@@ -89,17 +91,21 @@ int mono_cache_build(const mono_cache_spec* spec, mono_cache_t** out) {
   h->device = dev;
   const size_t lse = ((size_t)spec->max_rows * spec->n_q_heads * 4 + 255) / 256 * 256;
   const size_t part = attend_workspace_bytes(spec->max_rows, prop.multiProcessorCount);
-  cudaError_t e = cudaMalloc(&h->arena, 256 + lse + part);
-  if (e == cudaSuccess) e = cudaMemset(h->arena, 0, 256 + lse + part);
+  const size_t ev = (evict_workspace_bytes(spec->max_req) + 255) / 256 * 256;
+  const size_t bytes = 256 + lse + ev + part;
+  cudaError_t e = cudaMalloc(&h->arena, bytes);
+  if (e == cudaSuccess) e = cudaMemset(h->arena, 0, bytes);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = attend_prepare();
+  if (e == cudaSuccess) e = evict_prepare();
   if (e != cudaSuccess) {
     mono_cache_free(h);
     return cuda_code(e);
   }
   h->status = reinterpret_cast<int*>(h->arena);
   h->lse = reinterpret_cast<float*>(h->arena + 256);
-  h->attend_ws = h->arena + 256 + lse;
+  h->evict_ws = h->arena + 256 + lse;
+  h->attend_ws = h->evict_ws + ev;
   h->sms = prop.multiProcessorCount;
   *out = h;
   return MONO_OK;
@@ -209,6 +215,9 @@ int mono_cache_evict(mono_cache_t* h, const mono_evict_args* a, void* stream) {
     TRY(check_view(s, k.dst_base, k.dst.stride_block, k.dst.stride_tok, k.dst.num_blocks,
                    a->dst_max_blocks));
   }
+  if (!evict_fits(a->n_req, a->budget,
+                  std::min((int64_t)a->max_blocks * s.block_size, a->weights_stride)))
+    return MONO_ERR_TOO_MANY_ROWS;
   TRY(check_device(h));
   k.weights = a->weights;
   k.weights_out = a->weights_out ? a->weights_out : const_cast<float*>(a->weights);
@@ -224,7 +233,8 @@ int mono_cache_evict(mono_cache_t* h, const mono_evict_args* a, void* stream) {
   k.n_req = a->n_req;
   k.copy_bytes = (s.kv_dim + 4 + 15) / 16 * 16;
   k.status = h->status;
-  return cuda_code(launch_evict(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k));
+  return cuda_code(launch_evict(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k,
+                                h->evict_ws, s.max_req, h->sms));
 }
 
 int mono_verify_drafts(const mono_verify_args* a, void* stream) {
@@ -241,17 +251,18 @@ int mono_verify_drafts(const mono_verify_args* a, void* stream) {
       !aligned(a->draft_tokens, 4) || !aligned(a->u, 4) || !aligned(a->r, 4) ||
       !aligned(a->greedy, 4) || !aligned(a->accepted, 4) || !aligned(a->tokens, 4))
     return MONO_ERR_BAD_ALIGNMENT;
-  int dev = 0, major = 0, minor = 0;
+  int dev = 0, major = 0, minor = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_code(e);
   if (major != 10 || minor != 3) return MONO_ERR_UNSUPPORTED_DEVICE;
   VerifyArgs k = {a->target, a->draft, a->target_stride, a->draft_stride, a->vocab, a->rows,
                   a->n_req, a->row_start, a->draft_tokens, a->greedy, a->u, a->r, a->accepted,
                   a->tokens};
   return cuda_code(
-      launch_verify(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k, a->dtype));
+      launch_verify(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k, a->dtype, sms));
 }
 
 }  // extern "C"

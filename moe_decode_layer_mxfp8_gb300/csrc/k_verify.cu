@@ -1,7 +1,17 @@
 // Verification of drafted tokens against the target's probabilities (rejection sampling).
 //
-// CTA = request.  The accept tests u q(x) < p(x) are exact (a product of two f32 in f64); the
-// drawn token inverts the distribution function, with every sum in f64.
+//   draft x_j stands while u_j q_j(x_j) < p_j(x_j); at the first that falls the token is drawn from
+//   w = max(p - q, 0), else from w = p in the last row: the smallest v with
+//   sum_{i <= v} w_i > r sum_i w_i
+//
+// Bound by reading the one row pair that the token is drawn from.  A request is a cluster of up
+// to 16 CTAs, each with a run of the vocabulary, cut once more into a run per warp: one pass sums
+// the runs (16-byte loads), the CTAs exchange their sums through
+// distributed shared memory, and the one warp whose run holds the threshold reads its run again,
+// in order.  A request whose residual is empty takes a second pass over p.
+// The tests multiply two f32 in f64 (exact).  Sums decide which token is drawn, so they are
+// carried in two f32 each (error-free additions, and the difference p - q as a sum of two f32:
+// FP64 runs at a fraction of the FP32 rate here), and across lanes in f64.
 #include <cuda_fp16.h>
 
 #include "cache_kernels.h"
@@ -9,109 +19,357 @@
 namespace mono {
 namespace {
 
-constexpr int THREADS = 512;
+constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int MAX_CS = 16;
 
 __device__ __forceinline__ float as_f32(float v) { return v; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float as_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ double weight0(float v) { return v > 0.0f ? (double)v : 0.0; }
+__device__ __forceinline__ float positive(float v) { return v > 0.0f ? v : 0.0f; }
+
+// A sum in two f32: s, and the rounding errors of the additions to it.
+struct Sum2 {
+  float s = 0.0f, e = 0.0f;
+  __device__ void add(float x) {
+    const float t = s + x, b = t - s;
+    e += (s - (t - b)) + (x - b);
+    s = t;
+  }
+  __device__ double value() const { return (double)s + (double)e; }
+};
 
 template <class T>
-__global__ void __launch_bounds__(THREADS) verify_kernel(VerifyArgs a) {
-  __shared__ double sums[THREADS];
-  __shared__ float bv[THREADS];
-  __shared__ int bi[THREADS];
-  __shared__ int s_tok;
+struct Row {  // a row of the vocabulary as 16-byte vectors from its first aligned address on
+  static constexpr int VEC = 16 / sizeof(T);
+  const T* p;
+  int lead;  // elements of vector 0 that lie before the row
+  __device__ explicit Row(const T* q) : p(q) {
+    lead = (int)((reinterpret_cast<uintptr_t>(q) & 15) / sizeof(T));
+  }
+};
+
+// VEC elements from v0 on; those outside [0, V) as 0.
+template <class T>
+__device__ __forceinline__ void load_vec(const T* p, int v0, int V, bool aligned,
+                                         float (&f)[16 / sizeof(T)]) {
+  constexpr int VEC = 16 / sizeof(T);
+  if (aligned && v0 >= 0 && v0 + VEC <= V) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p + v0));
+    const T* t = reinterpret_cast<const T*>(&x);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = as_f32(t[e]);
+  } else {  // a row's ends, or q out of step with p: rare, and short code
+    float t[VEC];
+#pragma unroll 1
+    for (int e = 0; e < VEC; ++e) t[e] = v0 + e >= 0 && v0 + e < V ? as_f32(p[v0 + e]) : 0.0f;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = t[e];
+  }
+}
+
+template <class T>
+struct Draw {  // what a token is drawn from
+  static constexpr int VEC = 16 / sizeof(T);
+  const T *p, *q;  // q null: nothing is taken off (but `certain`, all of it)
+  int V, certain, lead;
+  bool q_aligned;
+  __device__ Draw(const T* p_, const T* q_, int V_, int certain_)
+      : p(p_), q(q_), V(V_), certain(certain_), lead(Row<T>(p_).lead) {
+    q_aligned = q && Row<T>(q).lead == lead;
+  }
+  __device__ int vectors() const { return (V + lead + VEC - 1) / VEC; }
+  // weight e of a loaded vector in two f32: the difference and what rounding took off it
+  __device__ float weight(const float* a, const float* b, int v0, int e, float& err) const {
+    const float x = positive(a[e]);
+    err = 0.0f;
+    if (q) {
+      const float y = positive(b[e]), d = x - y;
+      if (!(d > 0.0f)) return 0.0f;
+      const float t = x - d;  // d + t' = x exactly where y is replaced by t
+      const float back = d + t;
+      err = (x - back) + (t - y);
+      return d;
+    }
+    if (v0 + e == certain) {
+      const float d = x - 1.0f;
+      return d > 0.0f ? d : 0.0f;
+    }
+    return x;
+  }
+  __device__ void load(int vec, float (&a)[VEC], float (&b)[VEC]) const {
+    const int v0 = vec * VEC - lead;
+    load_vec(p, v0, V, true, a);
+    if (q) load_vec(q, v0, V, q_aligned, b);
+  }
+};
+
+__device__ __forceinline__ double warp_sum_f64(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ double ld_dsmem_f64(uint32_t cluster_addr) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint64_t ld_dsmem_u64(uint32_t cluster_addr) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+// Larger value first, then lower index: as an integer that orders so (values by their bits made
+// monotonic; a NaN as -inf).
+__device__ __forceinline__ uint64_t arg_key(float v, int i) {
+  if (v != v) v = -INFINITY;
+  uint32_t b = __float_as_uint(v + 0.0f);
+  b = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return ((uint64_t)b << 32) | (uint32_t)~i;
+}
+
+template <class T>
+__global__ void __launch_bounds__(THREADS) verify_kernel(VerifyArgs a, int cs) {
+  constexpr int VEC = 16 / sizeof(T);
+  __shared__ double s_warp[WARPS], s_cta[2];  // sums of the warps' runs, of the CTA's (two passes)
+  __shared__ uint64_t s_best[2][WARPS + 1];   // first maxima, by the row's parity
+  __shared__ int s_row, s_tok;
+  pdl_trigger();
   pdl_wait();
-  const int b = blockIdx.x, tid = threadIdx.x, V = a.vocab;
+  const int b = blockIdx.x / cs, rank = blockIdx.x - b * cs;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, V = a.vocab;
   const int r0 = min(max(a.row_start[b], 0), a.rows);
   const int r1 = min(max(a.row_start[b + 1], r0), a.rows);
   if (r1 == r0) {
-    if (tid == 0) a.accepted[b] = 0;
-    return;
+    if (tid == 0 && rank == 0) a.accepted[b] = 0;
+    return;  // (the whole cluster)
   }
   const T* tp = reinterpret_cast<const T*>(a.target);
   const T* dp = reinterpret_cast<const T*>(a.draft);
   const bool greedy = a.greedy && a.greedy[b] != 0;
+  const int runs = cs * WARPS, run = rank * WARPS + warp;
   int j = r0, tok = -1;
-  for (;; ++j) {
-    const T* p = tp + (long long)j * a.target_stride;
-    const int x = a.draft_tokens[j];
-    const bool valid = j < r1 - 1 && x >= 0 && x < V;
-    if (greedy) {
-      float best = -INFINITY;
-      int idx = V;
-      for (int v = tid; v < V; v += THREADS) {
-        const float f = as_f32(p[v]);
-        if (f > best || (idx == V && !(f != f))) best = f, idx = v;
+  bool writer = false;  // this CTA knows the token
+  if (greedy) {
+    // row by row: the first maximum of the CTAs' runs, exchanged by the cluster
+    for (;; ++j) {
+      const T* p = tp + (long long)j * a.target_stride;
+      const Draw<T> d(p, nullptr, V, -1);
+      const int nv = (d.vectors() + runs - 1) / runs, first = run * nv;
+      const int last = min(first + nv, d.vectors());
+      uint64_t best = 0;
+#pragma unroll 1
+      for (int k = first + lane; k < last; k += 32) {
+        float f[VEC];
+        const int v0 = k * VEC - d.lead;
+        load_vec(p, v0, V, true, f);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (v0 + e >= 0 && v0 + e < V) best = max(best, arg_key(f[e], v0 + e));
       }
-      bv[tid] = best;
-      bi[tid] = idx;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+      uint64_t* sb = s_best[(j - r0) & 1];
+      if (lane == 0) sb[warp] = best;
       __syncthreads();
-      for (int n = THREADS / 2; n > 0; n >>= 1) {
-        if (tid < n && (bv[tid + n] > bv[tid] || (bv[tid + n] == bv[tid] && bi[tid + n] < bi[tid])))
-          bv[tid] = bv[tid + n], bi[tid] = bi[tid + n];
-        __syncthreads();
+      if (tid == 0) {
+#pragma unroll 1
+        for (int w = 1; w < WARPS; ++w) best = max(best, sb[w]);
+        sb[WARPS] = best;
       }
-      tok = bi[0] < V ? bi[0] : 0;
-      __syncthreads();
-      if (valid && tok == x) continue;
-      break;
+      if (cs > 1) cluster_sync_all(); else __syncthreads();
+      best = sb[WARPS];
+#pragma unroll 1
+      for (int k = 0; k < cs; ++k)
+        if (k != rank) best = max(best, ld_dsmem_u64(mapa_shared(smem_u32(&sb[WARPS]), k)));
+      tok = (int)~(uint32_t)best;
+      if (j == r1 - 1 || a.draft_tokens[j] != tok) break;
     }
-    if (valid) {
-      const double px = weight0(as_f32(p[x]));
-      const double qx = dp ? weight0(as_f32(dp[(long long)j * a.draft_stride + x])) : 1.0;
-      if ((double)a.u[j] * qx < px) continue;
-    }
-    // the drawn token
-    const int per = (V + THREADS - 1) / THREADS, v0 = min(V, tid * per), v1 = min(V, v0 + per);
-    const bool bonus = j == r1 - 1;
-    for (int pass = bonus ? 1 : 0; pass < 2; ++pass) {  // 0: the residual, 1: the row itself
-      const T* q = dp ? dp + (long long)j * a.draft_stride : nullptr;
-      auto weight = [&](int v) {
-        double w = weight0(as_f32(p[v]));
-        if (pass == 0) w -= q ? weight0(as_f32(q[v])) : (v == x ? 1.0 : 0.0);
-        return w > 0.0 ? w : 0.0;
-      };
-      double s = 0.0;
-      for (int v = v0; v < v1; ++v) s += weight(v);
-      sums[tid] = s;
-      if (tid == 0) s_tok = -1;
-      __syncthreads();
-      double before = 0.0, total = 0.0;
-      for (int i = 0; i < THREADS; ++i) {
-        if (i < tid) before += sums[i];
-        total += sums[i];
-      }
-      const double want = (double)a.r[b] * total;
-      if (s > 0.0 && before <= want && want < before + s) {
-        double c = before;
-        for (int v = v0; v < v1; ++v) {
-          const double w = weight(v);
-          c += w;
-          if (w > 0.0) s_tok = v;  // (the last one, should roundings leave c at want)
-          if (c > want) break;
+    writer = rank == 0;
+    if (cs > 1) cluster_sync_all();  // (nobody leaves while its shared memory is read)
+  } else {
+    // the first draft that falls: a lane per draft
+    if (warp == 0) {
+      int fall = r1 - 1;
+      for (int k0 = r0; k0 < r1 - 1; k0 += 32) {
+        const int k = k0 + lane;
+        bool falls = false;
+        if (k < r1 - 1) {
+          const int x = a.draft_tokens[k];
+          falls = true;
+          if (x >= 0 && x < V) {
+            const float px = positive(as_f32(tp[(long long)k * a.target_stride + x]));
+            const float qx = dp ? positive(as_f32(dp[(long long)k * a.draft_stride + x])) : 1.0f;
+            falls = !((double)a.u[k] * (double)qx < (double)px);
+          }
+        }
+        const uint32_t m = __ballot_sync(0xffffffffu, falls);
+        if (m) {
+          fall = k0 + __ffs(m) - 1;
+          break;
         }
       }
-      __syncthreads();
-      tok = s_tok;
-      __syncthreads();
-      if (total > 0.0) break;
+      if (lane == 0) s_row = fall;
     }
-    break;
+    __syncthreads();
+    j = s_row;
+    const T* p = tp + (long long)j * a.target_stride;
+    const int x = a.draft_tokens[j];
+    // (in [0, 1), whatever comes)
+    const double r = fmin(fmax((double)a.r[b], 0.0), 1.0 - 1.0 / 16777216.0);
+    double before = 0.0, total = 0.0;
+    int pass = j == r1 - 1 ? 1 : 0;  // 0: the residual, 1: the row itself
+    for (;; ++pass) {
+      const Draw<T> d(p, pass == 0 && dp ? dp + (long long)j * a.draft_stride : nullptr, V,
+                      pass == 0 && !dp ? x : -1);
+      const int nv = (d.vectors() + runs - 1) / runs, first = run * nv;
+      const int last = min(first + nv, d.vectors());
+      Sum2 sum;
+      constexpr int U = 2;
+#pragma unroll 1
+      for (int k0 = first + lane; k0 < last; k0 += 32 * U) {
+        float fa[U][VEC], fb[U][VEC];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (k0 + 32 * u < last) d.load(k0 + 32 * u, fa[u], fb[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (k0 + 32 * u < last) {
+            const int v0 = (k0 + 32 * u) * VEC - d.lead;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              float err;
+              const float w = d.weight(fa[u], fb[u], v0, e, err);
+              sum.add(w);
+              sum.e += err;
+            }
+          }
+      }
+      const double mine = warp_sum_f64(sum.value());
+      if (lane == 0) s_warp[warp] = mine;
+      __syncthreads();
+      if (tid == 0) {
+        double t = 0.0;
+#pragma unroll 1
+        for (int w = 0; w < WARPS; ++w) t += s_warp[w];
+        s_cta[pass] = t;
+      }
+      if (cs > 1) cluster_sync_all(); else __syncthreads();
+      before = total = 0.0;
+#pragma unroll 1
+      for (int k = 0; k < cs; ++k) {
+        const double t = k == rank ? s_cta[pass] : ld_dsmem_f64(mapa_shared(smem_u32(&s_cta[pass]), k));
+        if (k == rank) before = total;
+        total += t;
+      }
+      if (total > 0.0 || pass == 1) {
+        // the run that holds the threshold; every partial sum here is one that `total` went through
+        const double want = r * total;
+        const bool sound = total > 0.0 && total < 1.0e300;  // (else there is nothing to draw from)
+        const bool here = sound && before <= want && want < before + s_cta[pass];
+        writer = here || (!sound && rank == 0);
+        if (tid == 0) s_tok = -1;
+        __syncthreads();
+        if (here) {
+          const double local = want - before;
+          double c = 0.0;
+          int owner = -1;
+#pragma unroll 1
+          for (int w = 0; w < WARPS; ++w) {
+            if (s_warp[w] > 0.0 && (owner < 0 || c <= local)) owner = w, before = c;
+            c += s_warp[w];
+          }
+          if (warp == owner) {
+            // in order: a vector per lane at a time
+            const double goal = local - before;
+            double done = 0.0;
+            int found = -1, fallback = -1;
+#pragma unroll 1
+            for (int k0 = first; k0 < last && found < 0; k0 += 32) {
+              const int k = k0 + lane;
+              float fa[VEC], fb[VEC];
+              double w[VEC], own = 0.0;
+              const int v0 = k * VEC - d.lead;
+              if (k < last) d.load(k, fa, fb);
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) {
+                float err = 0.0f;
+                const float x0 = k < last ? d.weight(fa, fb, v0, e, err) : 0.0f;
+                w[e] = (double)x0 + (double)err;
+                own += w[e];
+              }
+              double incl = own;
+#pragma unroll
+              for (int o = 1; o < 32; o <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+              }
+              double at = done + (incl - own);
+              int hit = -1, any = -1;
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) {
+                at += w[e];
+                if (w[e] > 0.0) {
+                  any = v0 + e;
+                  if (hit < 0 && at > goal) hit = v0 + e;
+                }
+              }
+              const uint32_t m = __ballot_sync(0xffffffffu, hit >= 0);
+              if (m) found = __shfl_sync(0xffffffffu, hit, __ffs(m) - 1);
+              const uint32_t n = __ballot_sync(0xffffffffu, any >= 0);
+              if (n) fallback = __shfl_sync(0xffffffffu, any, 31 - __clz(n));
+              done += __shfl_sync(0xffffffffu, incl, 31);
+            }
+            // (the last weight, should roundings leave the sum at the threshold)
+            if (lane == 0) s_tok = found >= 0 ? found : fallback;
+          }
+        }
+        __syncthreads();
+        tok = s_tok;
+        if (cs > 1) cluster_sync_all();  // (nobody leaves while its shared memory is read)
+        break;
+      }
+    }
   }
-  if (tid == 0) a.accepted[b] = j - r0;
-  for (int i = r0 + tid; i < r1; i += THREADS)
-    a.tokens[i] = i < j ? a.draft_tokens[i] : i == j ? tok : -1;
+  if (writer) {
+    if (tid == 0) a.accepted[b] = j - r0;
+#pragma unroll 1
+    for (int i = r0 + tid; i < r1; i += THREADS)
+      a.tokens[i] = i < j ? a.draft_tokens[i] : i == j ? tok : -1;
+  }
+}
+
+template <class T>
+cudaError_t launch(const Launch& L, const VerifyArgs& a, int sms) {
+  // as many CTAs a request as give the GPU four each, at least one vector a lane
+  int cs = 1;
+  const int vectors = (a.vocab + Row<T>::VEC - 1) / Row<T>::VEC;
+  while (cs < MAX_CS && (long long)a.n_req * cs * 2 <= 4 * sms && cs * 2 * THREADS <= vectors) cs *= 2;
+  cudaError_t e = cudaSuccess;
+  if (cs > 8) e = cudaFuncSetAttribute(verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.n_req * cs);
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = L.pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, verify_kernel<T>, a, cs);
 }
 
 }  // namespace
 
-cudaError_t launch_verify(const Launch& L, const VerifyArgs& a, int dtype) {
-  const dim3 grid(a.n_req), block(THREADS);
-  if (dtype == 0) return launch_ex(L, grid, block, 0, verify_kernel<float>, a);
-  if (dtype == 1) return launch_ex(L, grid, block, 0, verify_kernel<__nv_bfloat16>, a);
-  return launch_ex(L, grid, block, 0, verify_kernel<__half>, a);
+cudaError_t launch_verify(const Launch& L, const VerifyArgs& a, int dtype, int sms) {
+  if (dtype == 0) return launch<float>(L, a, sms);
+  if (dtype == 1) return launch<__nv_bfloat16>(L, a, sms);
+  return launch<__half>(L, a, sms);
 }
 
 }  // namespace mono
