@@ -4,14 +4,15 @@
 //   w = max(p - q, 0), else from w = p in the last row: the smallest v with
 //   sum_{i <= v} w_i > r sum_i w_i
 //
-// Bound by reading the one row pair that the token is drawn from.  A request is a cluster of up
-// to 16 CTAs, each with a run of the vocabulary, cut once more into a run per warp: one pass sums
-// the runs (16-byte loads), the CTAs exchange their sums through
-// distributed shared memory, and the one warp whose run holds the threshold reads its run again,
-// in order.  A request whose residual is empty takes a second pass over p.
+// Bound by reading the one row pair that the token is drawn from; small ones by latencies.  A
+// request is a cluster of up to 16 CTAs, each with a run of the vocabulary, cut once more into a
+// run per warp and that into blocks: one pass sums the blocks (16-byte loads), the CTAs exchange
+// their sums through distributed shared memory, and the one warp whose run holds the threshold
+// finds the block and reads it again, in order.  A request whose residual is empty takes a second
+// pass over p.
 // The tests multiply two f32 in f64 (exact).  Sums decide which token is drawn, so they are
-// carried in two f32 each (error-free additions, and the difference p - q as a sum of two f32:
-// FP64 runs at a fraction of the FP32 rate here), and across lanes in f64.
+// carried as pairs of f32 (error-free additions, and p - q as a pair): FP64 adds run at a 64th of
+// the FP32 rate here, and a search in f64 took 40 us of a CTA's 45.
 #include <cuda_fp16.h>
 
 #include "cache_kernels.h"
@@ -21,13 +22,53 @@ namespace {
 
 constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int MAX_CS = 16;
+constexpr int BLOCKS = 32;  // of a warp's run
 
 __device__ __forceinline__ float as_f32(float v) { return v; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float as_f32(__half v) { return __half2float(v); }
 __device__ __forceinline__ float positive(float v) { return v > 0.0f ? v : 0.0f; }
 
-// A sum in two f32: s, and the rounding errors of the additions to it.
+// A number as h + l, |l| at most half a unit of h's last place.
+struct Pair {
+  float h = 0.0f, l = 0.0f;
+  __device__ double value() const { return (double)h + (double)l; }
+};
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  const float s = a.h + b.h, v = s - a.h;
+  const float e = ((a.h - (s - v)) + (b.h - v)) + (a.l + b.l);
+  Pair r;
+  r.h = s + e;
+  r.l = e - (r.h - s);
+  return r;
+}
+__device__ __forceinline__ Pair shfl_xor(Pair a, int o) {
+  Pair r;
+  r.h = __shfl_xor_sync(0xffffffffu, a.h, o);
+  r.l = __shfl_xor_sync(0xffffffffu, a.l, o);
+  return r;
+}
+// Inclusive prefix sums over the lanes.
+__device__ __forceinline__ Pair warp_scan(Pair a) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    Pair b;
+    b.h = __shfl_up_sync(0xffffffffu, a.h, o);
+    b.l = __shfl_up_sync(0xffffffffu, a.l, o);
+    if (lane >= o) a = b + a;
+  }
+  return a;
+}
+// The value before this lane's of a scan.
+__device__ __forceinline__ Pair shfl_before(Pair incl) {
+  Pair b;
+  b.h = __shfl_up_sync(0xffffffffu, incl.h, 1);
+  b.l = __shfl_up_sync(0xffffffffu, incl.l, 1);
+  if ((threadIdx.x & 31) == 0) b.h = b.l = 0.0f;
+  return b;
+}
+// A sum of f32 in the making: s, and the rounding errors of the additions to it.
 struct Sum2 {
   float s = 0.0f, e = 0.0f;
   __device__ void add(float x) {
@@ -35,7 +76,12 @@ struct Sum2 {
     e += (s - (t - b)) + (x - b);
     s = t;
   }
-  __device__ double value() const { return (double)s + (double)e; }
+  __device__ Pair pair() const {
+    Pair r;
+    r.h = s + e;
+    r.l = e - (r.h - s);
+    return r;
+  }
 };
 
 template <class T>
@@ -103,15 +149,13 @@ struct Draw {  // what a token is drawn from
   }
 };
 
-__device__ __forceinline__ double warp_sum_f64(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-__device__ __forceinline__ double ld_dsmem_f64(uint32_t cluster_addr) {
-  double v;
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(cluster_addr) : "memory");
-  return v;
+// The last lane of those below n whose weight is positive and whose prefix is at most x.
+__device__ __forceinline__ int lane_of(Pair before, Pair own, int n, double x) {
+  const int lane = threadIdx.x & 31;
+  const bool some = lane < n && own.h > 0.0f;
+  const uint32_t below = __ballot_sync(0xffffffffu, some && before.value() <= x);
+  const uint32_t any = __ballot_sync(0xffffffffu, some);
+  return below ? 31 - __clz(below) : __ffs(any) - 1;
 }
 __device__ __forceinline__ uint64_t ld_dsmem_u64(uint32_t cluster_addr) {
   uint64_t v;
@@ -129,9 +173,9 @@ __device__ __forceinline__ uint64_t arg_key(float v, int i) {
 }
 
 template <class T>
-__global__ void __launch_bounds__(THREADS) verify_kernel(VerifyArgs a, int cs) {
+__global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a, int cs) {
   constexpr int VEC = 16 / sizeof(T);
-  __shared__ double s_warp[WARPS], s_cta[2];  // sums of the warps' runs, of the CTA's (two passes)
+  __shared__ Pair s_block[WARPS][BLOCKS], s_warp[WARPS], s_cta[2];  // sums (the CTA's: two passes)
   __shared__ uint64_t s_best[2][WARPS + 1];   // first maxima, by the row's parity
   __shared__ int s_row, s_tok;
   pdl_trigger();
@@ -157,16 +201,26 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(VerifyArgs a, int cs) {
       const Draw<T> d(p, nullptr, V, -1);
       const int nv = (d.vectors() + runs - 1) / runs, first = run * nv;
       const int last = min(first + nv, d.vectors());
-      uint64_t best = 0;
+      float top = 0.0f;
+      int at = -1;
 #pragma unroll 1
-      for (int k = first + lane; k < last; k += 32) {
-        float f[VEC];
-        const int v0 = k * VEC - d.lead;
-        load_vec(p, v0, V, true, f);
+      for (int k0 = first + lane; k0 < last; k0 += 32 * 2) {
+        float f[2][VEC];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if (v0 + e >= 0 && v0 + e < V) best = max(best, arg_key(f[e], v0 + e));
+        for (int u = 0; u < 2; ++u)
+          if (k0 + 32 * u < last) load_vec(p, (k0 + 32 * u) * VEC - d.lead, V, true, f[u]);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int v0 = (k0 + 32 * u) * VEC - d.lead;
+          if (k0 + 32 * u >= last) break;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {  // (in a lane indices rise)
+            const float x = f[u][e] == f[u][e] ? f[u][e] : -INFINITY;
+            if (v0 + e >= 0 && v0 + e < V && (at < 0 || x > top)) top = x, at = v0 + e;
+          }
+        }
       }
+      uint64_t best = at >= 0 ? arg_key(top, at) : 0;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
       uint64_t* sb = s_best[(j - r0) & 1];
@@ -178,10 +232,9 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(VerifyArgs a, int cs) {
         sb[WARPS] = best;
       }
       if (cs > 1) cluster_sync_all(); else __syncthreads();
-      best = sb[WARPS];
-#pragma unroll 1
-      for (int k = 0; k < cs; ++k)
-        if (k != rank) best = max(best, ld_dsmem_u64(mapa_shared(smem_u32(&sb[WARPS]), k)));
+      best = lane < cs ? ld_dsmem_u64(mapa_shared(smem_u32(&sb[WARPS]), lane)) : 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
       tok = (int)~(uint32_t)best;
       if (j == r1 - 1 || a.draft_tokens[j] != tok) break;
     }
@@ -217,118 +270,121 @@ __global__ void __launch_bounds__(THREADS) verify_kernel(VerifyArgs a, int cs) {
     const int x = a.draft_tokens[j];
     // (in [0, 1), whatever comes)
     const double r = fmin(fmax((double)a.r[b], 0.0), 1.0 - 1.0 / 16777216.0);
-    double before = 0.0, total = 0.0;
     int pass = j == r1 - 1 ? 1 : 0;  // 0: the residual, 1: the row itself
+#pragma unroll 1
     for (;; ++pass) {
       const Draw<T> d(p, pass == 0 && dp ? dp + (long long)j * a.draft_stride : nullptr, V,
                       pass == 0 && !dp ? x : -1);
       const int nv = (d.vectors() + runs - 1) / runs, first = run * nv;
       const int last = min(first + nv, d.vectors());
-      Sum2 sum;
-      constexpr int U = 2;
+      // rounds of a vector per lane, `per` of them a block
+      const int rounds = max(0, (last - first + 31) / 32), per = (rounds + BLOCKS - 1) / BLOCKS;
+      Pair mine;
+      int blk = 0;
 #pragma unroll 1
-      for (int k0 = first + lane; k0 < last; k0 += 32 * U) {
-        float fa[U][VEC], fb[U][VEC];
+      for (int q = 0; q < rounds; q += per, ++blk) {
+        Sum2 sum;
+        constexpr int U = 2;
+#pragma unroll 1
+        for (int i = q; i < min(q + per, rounds); i += U) {
+          float fa[U][VEC], fb[U][VEC];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (k0 + 32 * u < last) d.load(k0 + 32 * u, fa[u], fb[u]);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (k0 + 32 * u < last) {
-            const int v0 = (k0 + 32 * u) * VEC - d.lead;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              float err;
-              const float w = d.weight(fa[u], fb[u], v0, e, err);
-              sum.add(w);
-              sum.e += err;
-            }
+          for (int u = 0; u < U; ++u) {
+            const int k = first + (i + u) * 32 + lane;
+            if (i + u < q + per && k < last) d.load(k, fa[u], fb[u]);
           }
-      }
-      const double mine = warp_sum_f64(sum.value());
-      if (lane == 0) s_warp[warp] = mine;
-      __syncthreads();
-      if (tid == 0) {
-        double t = 0.0;
-#pragma unroll 1
-        for (int w = 0; w < WARPS; ++w) t += s_warp[w];
-        s_cta[pass] = t;
-      }
-      if (cs > 1) cluster_sync_all(); else __syncthreads();
-      before = total = 0.0;
-#pragma unroll 1
-      for (int k = 0; k < cs; ++k) {
-        const double t = k == rank ? s_cta[pass] : ld_dsmem_f64(mapa_shared(smem_u32(&s_cta[pass]), k));
-        if (k == rank) before = total;
-        total += t;
-      }
-      if (total > 0.0 || pass == 1) {
-        // the run that holds the threshold; every partial sum here is one that `total` went through
-        const double want = r * total;
-        const bool sound = total > 0.0 && total < 1.0e300;  // (else there is nothing to draw from)
-        const bool here = sound && before <= want && want < before + s_cta[pass];
-        writer = here || (!sound && rank == 0);
-        if (tid == 0) s_tok = -1;
-        __syncthreads();
-        if (here) {
-          const double local = want - before;
-          double c = 0.0;
-          int owner = -1;
-#pragma unroll 1
-          for (int w = 0; w < WARPS; ++w) {
-            if (s_warp[w] > 0.0 && (owner < 0 || c <= local)) owner = w, before = c;
-            c += s_warp[w];
-          }
-          if (warp == owner) {
-            // in order: a vector per lane at a time
-            const double goal = local - before;
-            double done = 0.0;
-            int found = -1, fallback = -1;
-#pragma unroll 1
-            for (int k0 = first; k0 < last && found < 0; k0 += 32) {
-              const int k = k0 + lane;
-              float fa[VEC], fb[VEC];
-              double w[VEC], own = 0.0;
-              const int v0 = k * VEC - d.lead;
-              if (k < last) d.load(k, fa, fb);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int k = first + (i + u) * 32 + lane;
+            if (i + u < q + per && k < last) {
 #pragma unroll
               for (int e = 0; e < VEC; ++e) {
-                float err = 0.0f;
-                const float x0 = k < last ? d.weight(fa, fb, v0, e, err) : 0.0f;
-                w[e] = (double)x0 + (double)err;
-                own += w[e];
+                float err;
+                const float w = d.weight(fa[u], fb[u], k * VEC - d.lead, e, err);
+                sum.add(w);
+                sum.e += err;
               }
-              double incl = own;
-#pragma unroll
-              for (int o = 1; o < 32; o <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += y;
-              }
-              double at = done + (incl - own);
-              int hit = -1, any = -1;
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) {
-                at += w[e];
-                if (w[e] > 0.0) {
-                  any = v0 + e;
-                  if (hit < 0 && at > goal) hit = v0 + e;
-                }
-              }
-              const uint32_t m = __ballot_sync(0xffffffffu, hit >= 0);
-              if (m) found = __shfl_sync(0xffffffffu, hit, __ffs(m) - 1);
-              const uint32_t n = __ballot_sync(0xffffffffu, any >= 0);
-              if (n) fallback = __shfl_sync(0xffffffffu, any, 31 - __clz(n));
-              done += __shfl_sync(0xffffffffu, incl, 31);
             }
-            // (the last weight, should roundings leave the sum at the threshold)
-            if (lane == 0) s_tok = found >= 0 ? found : fallback;
           }
         }
-        __syncthreads();
-        tok = s_tok;
-        if (cs > 1) cluster_sync_all();  // (nobody leaves while its shared memory is read)
-        break;
+        Pair t = sum.pair();
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t = t + shfl_xor(t, o);
+        if (lane == 0) s_block[warp][blk] = t;
+        mine = mine + t;
       }
+      if (lane == 0) s_warp[warp] = mine;
+      __syncthreads();
+      Pair own = lane < WARPS ? s_warp[lane] : Pair(), incl = warp_scan(own);
+      if (tid == WARPS - 1) s_cta[pass] = incl;
+      if (cs > 1) cluster_sync_all(); else __syncthreads();
+      // every warp: the CTAs' sums, their total, and whose run holds the threshold
+      Pair cta;
+      if (lane < cs) {
+        const uint64_t v = ld_dsmem_u64(mapa_shared(smem_u32(&s_cta[pass]), lane));
+        cta.h = __uint_as_float((uint32_t)v);
+        cta.l = __uint_as_float((uint32_t)(v >> 32));
+      }
+      const Pair to = warp_scan(cta);
+      const double total = __shfl_sync(0xffffffffu, to.value(), 31);
+      const bool sound = total > 0.0 && total < 1.0e300;  // (else there is nothing to draw from)
+      if (!sound && pass == 0) continue;
+      const double want = r * total;
+      const int owner = sound ? lane_of(shfl_before(to), cta, cs, want) : 0;
+      writer = owner == rank;
+      if (tid == 0) s_tok = -1;
+      __syncthreads();
+      if (sound && writer) {
+        const double in_cta = want - __shfl_sync(0xffffffffu, shfl_before(to).value(), owner);
+        const Pair before = shfl_before(incl);
+        const int w = lane_of(before, own, WARPS, in_cta);
+        if (warp == w) {
+          const double in_warp = in_cta - __shfl_sync(0xffffffffu, before.value(), w);
+          own = lane < blk ? s_block[warp][lane] : Pair();
+          const Pair b0 = shfl_before(warp_scan(own));
+          const int bl = lane_of(b0, own, blk, in_warp);
+          double goal = in_warp - __shfl_sync(0xffffffffu, b0.value(), bl);
+          int found = -1, fallback = -1;
+#pragma unroll 1
+          for (int i = bl * per; i < min((bl + 1) * per, rounds) && found < 0; ++i) {  // in order
+            const int k = first + i * 32 + lane, v0 = k * VEC - d.lead;
+            float fa[VEC], fb[VEC], wt[VEC], err[VEC];
+            Sum2 sum;
+            if (k < last) d.load(k, fa, fb);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              err[e] = wt[e] = 0.0f;
+              if (k < last) wt[e] = d.weight(fa, fb, v0, e, err[e]);
+              sum.add(wt[e]);
+              sum.e += err[e];
+            }
+            const Pair run_incl = warp_scan(sum.pair());
+            // the first lane that passes the goal looks for the element
+            const uint32_t m = __ballot_sync(0xffffffffu, sum.s > 0.0f && run_incl.value() > goal);
+            const uint32_t n = __ballot_sync(0xffffffffu, sum.s > 0.0f);
+            const int pick = m ? __ffs(m) - 1 : n ? 31 - __clz(n) : -1;
+            if (pick >= 0) {
+              double at = shfl_before(run_incl).value();
+              int hit = -1;
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) {
+                if (wt[e] > 0.0f && at <= goal) hit = v0 + e;  // the last that begins by the goal
+                at += (double)wt[e] + (double)err[e];
+              }
+              hit = __shfl_sync(0xffffffffu, hit, pick);
+              if (m) found = hit;
+              fallback = hit;
+            }
+            goal -= __shfl_sync(0xffffffffu, run_incl.value(), 31);
+          }
+          // (the block's last weight, should roundings leave the sum at the threshold)
+          if (lane == 0) s_tok = found >= 0 ? found : fallback;
+        }
+      }
+      __syncthreads();
+      tok = s_tok;
+      if (cs > 1) cluster_sync_all();  // (nobody leaves while its shared memory is read)
+      break;
     }
   }
   if (writer) {
