@@ -140,8 +140,8 @@ int mono_cache_evict(mono_cache_t *h, const mono_evict_args *args, void *stream)
  * logits; a NaN counts as -inf).
  *   accepted[b] = number of accepted drafts
  *   tokens[row] = accepted drafts, then the drawn token, then -1
- * Tests and sums are carried in enough bits (products exact, sums to 2^-40 of the total or
- * better) that roundings of sums decide nothing in practice.  Rows need not be normalised;
+ * Tests and sums are carried in enough bits (products exact, sums in two f32) that roundings
+ * decide nothing in practice.  Rows need not be normalised;
  * negative and NaN entries count as 0 where a token is drawn, and a draw from zeros yields -1.  Drafted tokens
  * outside [0, vocab) are refused.  Requests without rows get accepted[b] = 0; rows outside
  * every request keep their tokens; row_start entries are cut to [0, rows].

@@ -210,25 +210,6 @@ __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Packed f32 arithmetic.
-__device__ __forceinline__ void fma2(float& x, float& y, float a, float bx, float by) {  // x = x a + bx
-  asm("{\n .reg .b64 s, m, b;\n mov.b64 s, {%0, %1};\n mov.b64 m, {%2, %2};\n mov.b64 b, {%3, %4};\n"
-      " fma.rn.f32x2 s, s, m, b;\n mov.b64 {%0, %1}, s;\n}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(bx), "f"(by));
-}
-__device__ __forceinline__ void add2(float& x, float& y, float bx, float by) {
-  asm("{\n .reg .b64 s, b;\n mov.b64 s, {%0, %1};\n mov.b64 b, {%2, %3};\n"
-      " add.rn.f32x2 s, s, b;\n mov.b64 {%0, %1}, s;\n}"
-      : "+f"(x), "+f"(y)
-      : "f"(bx), "f"(by));
-}
-__device__ __forceinline__ void mul2(float& x, float& y, float a) {
-  asm("{\n .reg .b64 s, m;\n mov.b64 s, {%0, %1};\n mov.b64 m, {%2, %2};\n"
-      " mul.rn.f32x2 s, s, m;\n mov.b64 {%0, %1}, s;\n}"
-      : "+f"(x), "+f"(y)
-      : "f"(a));
-}
 // Matrix descriptor as desc_sw128, MN-major with `lbo` bytes between 128-byte runs along MN.
 __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
   return (desc_sw128(saddr) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(lbo >> 4) << 16);

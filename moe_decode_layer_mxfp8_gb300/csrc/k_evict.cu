@@ -27,7 +27,7 @@ constexpr int CACHED = 12288;  // weights of a CTA's run kept in shared memory (
 constexpr int CHUNK = 64;      // kept tokens per move
 constexpr int MOVE_THREADS = 256;
 constexpr int PER_RECORD = 8;  // lanes of a record, 16 bytes each at a time
-constexpr int ROUNDS = CHUNK * PER_RECORD / MOVE_THREADS, STEPS = 9;  // records up to 1152 bytes
+constexpr int ROUNDS = CHUNK * PER_RECORD / MOVE_THREADS;
 
 // Order-preserving key: larger weight, larger key; -0 as +0, NaN as -inf.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -206,7 +206,9 @@ __device__ __forceinline__ void wait_loaded(const int* p, int* status) {
 }
 
 // ordered: records or weights move within the storage that they are read from.  The grid's last
-// n_req CTAs (by ticket) zero the weights behind the kept ones.
+// n_req CTAs (by ticket) zero the weights behind the kept ones.  STEPS runs of 128 bytes hold a
+// record: as few as do, since its registers bound the chunks in flight.
+template <int STEPS>
 __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(EvictArgs a, Work ws, int chunks,
                                                                   int ordered) {
   __shared__ int s_ticket, s_kept[CHUNK];
@@ -324,8 +326,9 @@ cudaError_t launch_evict(const Launch& L, const EvictArgs& a, uint8_t* workspace
   cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, ws, cs, chunks);
   if (e != cudaSuccess) return e;
   const int ordered = a.in_place || a.weights_out == a.weights;
-  return launch_ex(L, dim3((chunks + 1) * a.n_req), dim3(MOVE_THREADS), 0, evict_move_kernel, a, ws,
-                   chunks, ordered);
+  const auto move = a.copy_bytes <= 256 ? evict_move_kernel<2>
+                    : a.copy_bytes <= 640 ? evict_move_kernel<5> : evict_move_kernel<9>;
+  return launch_ex(L, dim3((chunks + 1) * a.n_req), dim3(MOVE_THREADS), 0, move, a, ws, chunks, ordered);
 }
 
 }  // namespace mono

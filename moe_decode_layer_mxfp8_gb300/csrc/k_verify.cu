@@ -15,12 +15,14 @@
 // the FP32 rate here, and a search in f64 took 40 us of a CTA's 45.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "cache_kernels.h"
 
 namespace mono {
 namespace {
 
-constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int MAX_CS = 16;
 constexpr int BLOCKS = 32;  // of a warp's run
 
@@ -68,19 +70,29 @@ __device__ __forceinline__ Pair shfl_before(Pair incl) {
   if ((threadIdx.x & 31) == 0) b.h = b.l = 0.0f;
   return b;
 }
-// A sum of f32 in the making: s, and the rounding errors of the additions to it.
+// Sums of f32 in the making, two side by side: s, and the rounding errors of the additions to it.
 struct Sum2 {
-  float s = 0.0f, e = 0.0f;
-  __device__ void add(float x) {
-    const float t = s + x, b = t - s;
-    e += (s - (t - b)) + (x - b);
-    s = t;
+  float s0 = 0.0f, s1 = 0.0f, e0 = 0.0f, e1 = 0.0f;
+  __device__ void add(float x0, float x1) {
+    float t0 = s0, t1 = s1;
+    add2(t0, t1, x0, x1);
+    float b0 = t0, b1 = t1;  // what of x went into t
+    add2(b0, b1, -s0, -s1);
+    float a0 = t0, a1 = t1;  // what of s did
+    add2(a0, a1, -b0, -b1);
+    add2(s0, s1, -a0, -a1);
+    add2(x0, x1, -b0, -b1);
+    add2(e0, e1, s0, s1);
+    add2(e0, e1, x0, x1);
+    s0 = t0;
+    s1 = t1;
   }
+  __device__ void error(float x0, float x1) { add2(e0, e1, x0, x1); }
   __device__ Pair pair() const {
-    Pair r;
-    r.h = s + e;
-    r.l = e - (r.h - s);
-    return r;
+    Pair a, b;
+    a.h = s0 + e0, a.l = e0 - (a.h - s0);
+    b.h = s1 + e1, b.l = e1 - (b.h - s1);
+    return a + b;
   }
 };
 
@@ -94,23 +106,43 @@ struct Row {  // a row of the vocabulary as 16-byte vectors from its first align
   }
 };
 
-// VEC elements from v0 on; those outside [0, V) as 0.
+// VEC elements from v0 on, as loaded.
 template <class T>
-__device__ __forceinline__ void load_vec(const T* p, int v0, int V, bool aligned,
-                                         float (&f)[16 / sizeof(T)]) {
-  constexpr int VEC = 16 / sizeof(T);
-  if (aligned && v0 >= 0 && v0 + VEC <= V) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p + v0));
-    const T* t = reinterpret_cast<const T*>(&x);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) f[e] = as_f32(t[e]);
-  } else {  // a row's ends, or q out of step with p: rare, and short code
-    float t[VEC];
-#pragma unroll 1
-    for (int e = 0; e < VEC; ++e) t[e] = v0 + e >= 0 && v0 + e < V ? as_f32(p[v0 + e]) : 0.0f;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) f[e] = t[e];
+struct Vec {
+  static constexpr int VEC = 16 / sizeof(T);
+  uint4 x;
+  __device__ float operator[](int e) const {  // (e a constant)
+    const uint32_t w = e * sizeof(T) / 4 == 0 ? x.x : e * sizeof(T) / 4 == 1 ? x.y
+                       : e * sizeof(T) / 4 == 2 ? x.z : x.w;
+    if (sizeof(T) == 4) return __uint_as_float(w);
+    const unsigned short h = (unsigned short)(e & 1 ? w >> 16 : w & 0xFFFF);
+    if (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(h));
+    return __uint_as_float((uint32_t)h << 16);
   }
+};
+// Elements outside [0, V) are 0.
+template <class T>
+__device__ __forceinline__ Vec<T> load_vec(const T* p, int v0, int V, bool aligned) {
+  constexpr int VEC = 16 / sizeof(T);
+  Vec<T> r;
+  if (aligned && v0 >= 0 && v0 + VEC <= V) {
+    r.x = __ldg(reinterpret_cast<const uint4*>(p + v0));
+  } else {  // a row's ends, or q out of step with p: rare, and short code
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll 1
+    for (int e = 0; e < VEC; ++e) {
+      if (v0 + e < 0 || v0 + e >= V) continue;
+      uint32_t bits;
+      if (sizeof(T) == 4) bits = reinterpret_cast<const uint32_t*>(p)[v0 + e];
+      else bits = (uint32_t)reinterpret_cast<const unsigned short*>(p)[v0 + e] << (e & 1 ? 16 : 0);
+      const int i = e * (int)sizeof(T) / 4;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (i == k) w[k] |= bits;
+    }
+    r.x = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return r;
 }
 
 template <class T>
@@ -124,28 +156,36 @@ struct Draw {  // what a token is drawn from
     q_aligned = q && Row<T>(q).lead == lead;
   }
   __device__ int vectors() const { return (V + lead + VEC - 1) / VEC; }
-  // weight e of a loaded vector in two f32: the difference and what rounding took off it
-  __device__ float weight(const float* a, const float* b, int v0, int e, float& err) const {
-    const float x = positive(a[e]);
-    err = 0.0f;
+  // The weights of a loaded vector, in two f32: the differences and what rounding took off them
+  // (for 16-bit types nothing worth carrying: a rounding needs p beyond 2^16 q).
+  __device__ void weights(const Vec<T>& a, const Vec<T>& b, int v0, float (&w)[VEC], float (&err)[VEC]) const {
     if (q) {
-      const float y = positive(b[e]), d = x - y;
-      if (!(d > 0.0f)) return 0.0f;
-      const float t = x - d;  // d + t' = x exactly where y is replaced by t
-      const float back = d + t;
-      err = (x - back) + (t - y);
-      return d;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float x = a[e], y = positive(b[e]), d = x - y;
+        if (sizeof(T) == 4) {
+          const float t = x - d, r = (x - (d + t)) + (t - y);
+          err[e] = d > 0.0f ? r : 0.0f;
+        }
+        w[e] = positive(d);  // (nothing for a negative or NaN p)
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) w[e] = positive(a[e]);
+      if (sizeof(T) == 4)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) err[e] = 0.0f;
+      if (certain >= v0 && certain < v0 + VEC) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+          if (v0 + e == certain) w[e] = positive(w[e] - 1.0f);
+      }
     }
-    if (v0 + e == certain) {
-      const float d = x - 1.0f;
-      return d > 0.0f ? d : 0.0f;
-    }
-    return x;
   }
-  __device__ void load(int vec, float (&a)[VEC], float (&b)[VEC]) const {
+  __device__ void load(int vec, Vec<T>& a, Vec<T>& b) const {
     const int v0 = vec * VEC - lead;
-    load_vec(p, v0, V, true, a);
-    if (q) load_vec(q, v0, V, q_aligned, b);
+    a = load_vec(p, v0, V, true);
+    if (q) b = load_vec(q, v0, V, q_aligned);
   }
 };
 
@@ -173,7 +213,7 @@ __device__ __forceinline__ uint64_t arg_key(float v, int i) {
 }
 
 template <class T>
-__global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a, int cs) {
+__global__ void __launch_bounds__(THREADS, 4) verify_kernel(VerifyArgs a, int cs) {
   constexpr int VEC = 16 / sizeof(T);
   __shared__ Pair s_block[WARPS][BLOCKS], s_warp[WARPS], s_cta[2];  // sums (the CTA's: two passes)
   __shared__ uint64_t s_best[2][WARPS + 1];   // first maxima, by the row's parity
@@ -205,17 +245,17 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a, int cs
       int at = -1;
 #pragma unroll 1
       for (int k0 = first + lane; k0 < last; k0 += 32 * 2) {
-        float f[2][VEC];
+        Vec<T> f[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          if (k0 + 32 * u < last) load_vec(p, (k0 + 32 * u) * VEC - d.lead, V, true, f[u]);
+          if (k0 + 32 * u < last) f[u] = load_vec(p, (k0 + 32 * u) * VEC - d.lead, V, true);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int v0 = (k0 + 32 * u) * VEC - d.lead;
           if (k0 + 32 * u >= last) break;
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {  // (in a lane indices rise)
-            const float x = f[u][e] == f[u][e] ? f[u][e] : -INFINITY;
+            const float y = f[u][e], x = y == y ? y : -INFINITY;
             if (v0 + e >= 0 && v0 + e < V && (at < 0 || x > top)) top = x, at = v0 + e;
           }
         }
@@ -278,16 +318,17 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a, int cs
       const int nv = (d.vectors() + runs - 1) / runs, first = run * nv;
       const int last = min(first + nv, d.vectors());
       // rounds of a vector per lane, `per` of them a block
-      const int rounds = max(0, (last - first + 31) / 32), per = (rounds + BLOCKS - 1) / BLOCKS;
+      constexpr int U = 4;  // (loaded at a time)
+      const int rounds = max(1, (last - first + 31) / 32);
+      const int per = ((rounds + BLOCKS - 1) / BLOCKS + U - 1) / U * U;
       Pair mine;
       int blk = 0;
 #pragma unroll 1
       for (int q = 0; q < rounds; q += per, ++blk) {
         Sum2 sum;
-        constexpr int U = 2;
 #pragma unroll 1
         for (int i = q; i < min(q + per, rounds); i += U) {
-          float fa[U][VEC], fb[U][VEC];
+          Vec<T> fa[U], fb[U];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const int k = first + (i + u) * 32 + lane;
@@ -297,12 +338,12 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a, int cs
           for (int u = 0; u < U; ++u) {
             const int k = first + (i + u) * 32 + lane;
             if (i + u < q + per && k < last) {
+              float w[VEC], err[VEC];
+              d.weights(fa[u], fb[u], k * VEC - d.lead, w, err);
 #pragma unroll
-              for (int e = 0; e < VEC; ++e) {
-                float err;
-                const float w = d.weight(fa[u], fb[u], k * VEC - d.lead, e, err);
-                sum.add(w);
-                sum.e += err;
+              for (int e = 0; e < VEC; e += 2) {
+                sum.add(w[e], w[e + 1]);
+                if (sizeof(T) == 4) sum.error(err[e], err[e + 1]);
               }
             }
           }
@@ -348,20 +389,27 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a, int cs
 #pragma unroll 1
           for (int i = bl * per; i < min((bl + 1) * per, rounds) && found < 0; ++i) {  // in order
             const int k = first + i * 32 + lane, v0 = k * VEC - d.lead;
-            float fa[VEC], fb[VEC], wt[VEC], err[VEC];
+            Vec<T> fa, fb;
+            float wt[VEC], err[VEC];
             Sum2 sum;
             if (k < last) d.load(k, fa, fb);
+            if (k < last) {
+              d.weights(fa, fb, v0, wt, err);
+            } else {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              err[e] = wt[e] = 0.0f;
-              if (k < last) wt[e] = d.weight(fa, fb, v0, e, err[e]);
-              sum.add(wt[e]);
-              sum.e += err[e];
+              for (int e = 0; e < VEC; ++e) wt[e] = err[e] = 0.0f;
             }
-            const Pair run_incl = warp_scan(sum.pair());
+#pragma unroll
+            for (int e = 0; e < VEC; e += 2) {
+              sum.add(wt[e], wt[e + 1]);
+              if (sizeof(T) == 4) sum.error(err[e], err[e + 1]);
+            }
+            const Pair own_sum = sum.pair();
+            const float own_w = own_sum.h;
+            const Pair run_incl = warp_scan(own_sum);
             // the first lane that passes the goal looks for the element
-            const uint32_t m = __ballot_sync(0xffffffffu, sum.s > 0.0f && run_incl.value() > goal);
-            const uint32_t n = __ballot_sync(0xffffffffu, sum.s > 0.0f);
+            const uint32_t m = __ballot_sync(0xffffffffu, own_w > 0.0f && run_incl.value() > goal);
+            const uint32_t n = __ballot_sync(0xffffffffu, own_w > 0.0f);
             const int pick = m ? __ffs(m) - 1 : n ? 31 - __clz(n) : -1;
             if (pick >= 0) {
               double at = shfl_before(run_incl).value();
@@ -369,7 +417,7 @@ __global__ void __launch_bounds__(THREADS, 2) verify_kernel(VerifyArgs a, int cs
 #pragma unroll
               for (int e = 0; e < VEC; ++e) {
                 if (wt[e] > 0.0f && at <= goal) hit = v0 + e;  // the last that begins by the goal
-                at += (double)wt[e] + (double)err[e];
+                at += sizeof(T) == 4 ? (double)wt[e] + (double)err[e] : (double)wt[e];
               }
               hit = __shfl_sync(0xffffffffu, hit, pick);
               if (m) found = hit;
