@@ -8,6 +8,9 @@ dtype, shape, stride or device raises ValueError, what the library refuses raise
 from __future__ import annotations
 
 import ctypes as C
+import struct
+
+import torch
 
 import moe_decode_layer_mxfp8_gb300 as _m
 
@@ -50,6 +53,11 @@ class VerifyArgs(C.Structure):
                 ("greedy", C.c_void_p), ("accepted", C.c_void_p), ("tokens", C.c_void_p)]
 
 
+# The same structures packed at once: setting ctypes fields one by one took most of a call.
+_ATTEND = struct.Struct("@PPqqPPPiiiiiifPqqqPPq")
+_EVICT = struct.Struct("@PPqqPPPqiiiiPiPqqqPiPqqq")
+_VERIFY = struct.Struct("@PPqqiiiiPPPPPPP")
+
 CACHE_EXPORTS = ["mono_cache_build", "mono_cache_free", "mono_cache_status", "mono_cache_attend",
                  "mono_cache_evict", "mono_verify_drafts"]
 
@@ -61,50 +69,71 @@ def _lib() -> C.CDLL:
         L.mono_cache_free.argtypes = [C.c_void_p]
         L.mono_cache_free.restype = None
         L.mono_cache_status.argtypes = [C.c_void_p, C.c_int]
-        L.mono_cache_attend.argtypes = [C.c_void_p, C.POINTER(AttendArgs), C.c_void_p]
-        L.mono_cache_evict.argtypes = [C.c_void_p, C.POINTER(EvictArgs), C.c_void_p]
-        L.mono_verify_drafts.argtypes = [C.POINTER(VerifyArgs), C.c_void_p]
+        L.mono_cache_attend.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
+        L.mono_cache_evict.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
+        L.mono_verify_drafts.argtypes = [C.c_void_p, C.c_void_p]
         L._mono_cache_ready = True
     return L
 
 
-def _check(t, name, dtypes, shape, device, inner=True):
-    """A CUDA tensor of one of the dtypes and of the shape (None: any size), its last dimension
-    contiguous, on `device`.  Returns its data pointer."""
-    names = [str(d).replace("torch.", "") for d in dtypes]
+def _bad(t, name, dtypes, shape, device, packed):
+    """What is wrong with a tensor that failed the checks below."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} is not a tensor")
     if t.dtype not in dtypes:
-        raise ValueError(f"{name} is {t.dtype}, not {' or '.join(names)}")
-    if t.dim() != len(shape) or any(w is not None and s != w for s, w in zip(t.shape, shape)):
+        names = " or ".join(str(d).replace("torch.", "") for d in dtypes)
+        raise ValueError(f"{name} is {t.dtype}, not {names}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not cuda:{device}")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not "
                          f"({', '.join('*' if w is None else str(w) for w in shape)})")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not {device}")
-    if inner and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} is not contiguous in its last dimension")
-    if t.dim() > 1 and any(s > 1 and st <= 0 for s, st in zip(t.shape, t.stride())):
-        raise ValueError(f"{name} is broadcast")
+    raise ValueError(f"{name} is not contiguous" + ("" if packed else " in its last dimension, or is "
+                     f"broadcast: strides {t.stride()}"))
+
+
+def _vec(t, name, dtype, n, device):
+    """Address of a contiguous vector of n elements."""
+    if t.dtype is not dtype or t.get_device() != device or t.shape != (n,) or not t.is_contiguous():
+        _bad(t, name, (dtype,), (n,), device, True)
     return t.data_ptr()
 
 
-def _packed(t, name, dtypes, shape, device):
-    """_check of a tensor that must be contiguous."""
-    p = _check(t, name, dtypes, shape, device)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
-    return p
+def _mat(t, name, dtypes, rows, cols, device):
+    """(address, row stride) of a [rows, cols] matrix (None: any) with contiguous rows."""
+    shape, stride = t.shape, t.stride()
+    if (t.dtype not in dtypes or t.get_device() != device or len(shape) != 2
+            or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols)
+            or (shape[1] > 1 and stride[1] != 1) or (shape[0] > 1 and stride[0] < shape[1])):
+        _bad(t, name, dtypes, (rows, cols), device, False)
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1]
 
 
-def _row_stride(t):
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _table(t, name, rows, device):
+    if (t.dtype is not torch.int32 or t.get_device() != device or t.dim() != 2
+            or (rows is not None and t.shape[0] != rows) or not t.is_contiguous()):
+        _bad(t, name, (torch.int32,), (rows, None), device, True)
+    return t.data_ptr()
 
 
-def _stream_of(stream, device):
-    import torch
+_BF16, _F32 = (torch.bfloat16,), (torch.float32,)
+_PROBS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _call(name, device, stream, *args):
+    """Calls the library with `device` current, on `stream` or torch's current one."""
     if stream is None:
         stream = torch.cuda.current_stream(device)
-    if stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, not {device}")
-    return C.c_void_p(stream.cuda_stream)
+    elif stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, not cuda:{device}")
+    fn = getattr(_lib(), name)
+    if torch.cuda.current_device() == device:
+        rc = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream.cuda_stream)
+    if rc != _m.MONO_OK:
+        raise _m.MonoError(rc, name)
 
 
 class Cache:
@@ -114,7 +143,6 @@ class Cache:
     order them on the GPU."""
 
     def __init__(self, spec: dict, max_rows: int, max_requests: int):
-        import torch
         self.spec = {k: int(spec[k]) for k in ("n_q_heads", "head_dim", "kv_dim", "block_size",
                                                "kv_record_bytes")}
         self._h = C.c_void_p()
@@ -124,17 +152,19 @@ class Cache:
         if rc != _m.MONO_OK:
             raise _m.MonoError(rc, "mono_cache_build")
         self.device = torch.device("cuda", torch.cuda.current_device())
+        self._dev = self.device.index
+        self._width = self.spec["n_q_heads"] * self.spec["head_dim"]
 
     def _view(self, t, name):
-        import torch
-        if t.dim() != 3 or t.dtype != torch.uint8 or t.device != self.device:
+        if t.dim() != 3 or t.dtype is not torch.uint8 or t.get_device() != self._dev:
             raise ValueError(f"{name} is a uint8 [blocks, block_size, record] view on {self.device}")
-        if t.shape[1] != self.spec["block_size"] or t.shape[2] < self.spec["kv_record_bytes"] \
-                or t.stride(2) != 1:
+        shape, stride = t.shape, t.stride()
+        if (shape[1] != self.spec["block_size"] or shape[2] < self.spec["kv_record_bytes"]
+                or stride[2] != 1):
             raise ValueError(f"{name}: pages of {self.spec['block_size']} records of "
                              f"{self.spec['kv_record_bytes']} contiguous bytes expected, got shape "
-                             f"{tuple(t.shape)}, strides {t.stride()}")
-        return t.data_ptr(), t.stride(0), t.stride(1), t.shape[0]
+                             f"{tuple(shape)}, strides {stride}")
+        return t.data_ptr(), stride[0], stride[1], shape[0]
 
     def attend(self, q, o, positions, row_req, block_table, kv_cache, *, window=0, sinks=0,
                causal=True, scale=None, lse=None, weights=None, stream=None) -> None:
@@ -143,29 +173,27 @@ class Cache:
         ``window`` tokens and the first ``sinks``; ``lse`` (f32 [rows, n_q_heads]) gets the
         log-sum-exp of the scores, ``weights`` (f32 [n_req, tokens]) each token's attention weight
         added."""
-        import torch
-        s, dev = self.spec, self.device
-        rows, n_req, width = q.shape[0], block_table.shape[0], s["n_q_heads"] * s["head_dim"]
-        i32 = (torch.int32,)
-        a = AttendArgs(
-            q=_check(q, "q", (torch.bfloat16,), (rows, width), dev),
-            o=_check(o, "o", (torch.bfloat16,), (rows, width), dev),
-            q_stride=_row_stride(q), o_stride=_row_stride(o),
-            positions=_packed(positions, "positions", i32, (rows,), dev),
-            row_req=_packed(row_req, "row_req", i32, (rows,), dev),
-            block_table=_packed(block_table, "block_table", i32, (None, None), dev),
-            max_blocks=block_table.shape[1], n_req=n_req, rows=rows, window=window, sinks=sinks,
-            causal=int(bool(causal)), scale=0.0 if scale is None else float(scale))
-        if scale is not None and not scale > 0:
+        dev, i32 = self._dev, torch.int32
+        rows, (n_req, max_blocks) = q.shape[0], block_table.shape
+        if scale is None:
+            scale = 0.0
+        elif not scale > 0:
             raise ValueError("scale must be positive")
-        a.kv_cache, a.kv_stride_block, a.kv_stride_tok, a.kv_num_blocks = self._view(kv_cache,
-                                                                                    "kv_cache")
+        qp, qs = _mat(q, "q", _BF16, rows, self._width, dev)
+        op, os = _mat(o, "o", _BF16, rows, self._width, dev)
+        heads = self.spec["n_q_heads"]
+        lp = 0
         if lse is not None:
-            a.lse = _packed(lse, "lse", (torch.float32,), (rows, s["n_q_heads"]), dev)
-        if weights is not None:
-            a.weights = _check(weights, "weights", (torch.float32,), (n_req, None), dev)
-            a.weights_stride = _row_stride(weights)
-        self._call("mono_cache_attend", a, stream)
+            lp, ls = _mat(lse, "lse", _F32, rows, heads, dev)
+            if ls != heads:
+                _bad(lse, "lse", _F32, (rows, heads), dev, True)
+        wp, ws = (0, 0) if weights is None else _mat(weights, "weights", _F32, n_req, None, dev)
+        args = _ATTEND.pack(qp, op, qs, os, _vec(positions, "positions", i32, rows, dev),
+                            _vec(row_req, "row_req", i32, rows, dev),
+                            _table(block_table, "block_table", None, dev), max_blocks, n_req, rows,
+                            window, sinks, 1 if causal else 0, scale,
+                            *self._view(kv_cache, "kv_cache"), lp, wp, ws)
+        self._call("mono_cache_attend", args, stream)
 
     def evict(self, weights, lengths, block_table, kv_cache, kept, new_lengths, *, budget,
               sinks=0, recent=0, weights_out=None, dst_table=None, dst_cache=None,
@@ -175,44 +203,31 @@ class Cache:
         weights, in order, to the front of its pages, or to those of ``dst_table`` (in
         ``dst_cache``).  kept (int32 [n_req, >= budget]) gets the old slots, new_lengths the
         counts."""
-        import torch
-        dev, f32, i32 = self.device, (torch.float32,), (torch.int32,)
-        n_req = block_table.shape[0]
-        a = EvictArgs(
-            weights=_check(weights, "weights", f32, (n_req, None), dev),
-            weights_stride=_row_stride(weights),
-            lengths=_packed(lengths, "lengths", i32, (n_req,), dev),
-            new_lengths=_packed(new_lengths, "new_lengths", i32, (n_req,), dev),
-            kept=_check(kept, "kept", i32, (n_req, None), dev),
-            budget=budget, sinks=sinks, recent=recent, n_req=n_req,
-            block_table=_packed(block_table, "block_table", i32, (None, None), dev),
-            max_blocks=block_table.shape[1])
+        dev, i32 = self._dev, torch.int32
+        n_req, max_blocks = block_table.shape
+        wp, ws = _mat(weights, "weights", _F32, n_req, None, dev)
+        kp, ks = _mat(kept, "kept", (i32,), n_req, None, dev)
         if kept.shape[1] < budget:
             raise ValueError(f"kept holds {kept.shape[1]} slots a request, the budget is {budget}")
-        a.kept_stride = _row_stride(kept)
-        a.kv_cache, a.kv_stride_block, a.kv_stride_tok, a.kv_num_blocks = self._view(kv_cache,
-                                                                                    "kv_cache")
-        if weights_out is not None:
-            a.weights_out = _check(weights_out, "weights_out", f32, (n_req, None), dev)
-            a.weights_out_stride = _row_stride(weights_out)
-        if dst_table is not None:
-            a.dst_table = _packed(dst_table, "dst_table", i32, (n_req, None), dev)
-            a.dst_max_blocks = dst_table.shape[1]
+        vp, vs = (0, 0) if weights_out is None else _mat(weights_out, "weights_out", _F32, n_req, None,
+                                                          dev)
+        tp, tb = (0, 0) if dst_table is None else (_table(dst_table, "dst_table", n_req, dev),
+                                                   dst_table.shape[1])
+        dst = (0, 0, 0, 0)
         if dst_cache is not None:
             if dst_table is None:
                 raise ValueError("dst_cache needs a dst_table")
-            a.dst_cache, a.dst_stride_block, a.dst_stride_tok, a.dst_num_blocks = self._view(
-                dst_cache, "dst_cache")
-        self._call("mono_cache_evict", a, stream)
+            dst = self._view(dst_cache, "dst_cache")
+        args = _EVICT.pack(wp, vp, ws, vs, _vec(lengths, "lengths", i32, n_req, dev),
+                           _vec(new_lengths, "new_lengths", i32, n_req, dev), kp, ks, budget, sinks,
+                           recent, n_req, _table(block_table, "block_table", None, dev), max_blocks,
+                           *self._view(kv_cache, "kv_cache"), tp, tb, *dst)
+        self._call("mono_cache_evict", args, stream)
 
     def _call(self, name, args, stream):
-        import torch
         if not self._h:
             raise ValueError("the Cache is closed")
-        with torch.cuda.device(self.device):
-            rc = getattr(_lib(), name)(self._h, C.byref(args), _stream_of(stream, self.device))
-        if rc != _m.MONO_OK:
-            raise _m.MonoError(rc, name)
+        _call(name, self._dev, stream, self._h, args)
 
     def status(self, clear: bool = False) -> int:
         """The handle's MONO_STATUS_* bits (waits for the device)."""
@@ -240,27 +255,19 @@ def verify_drafts(target, draft, draft_tokens, row_start, u, r, accepted, tokens
     [rows, vocab] in f32, bf16 or f16; u [rows] and r [n_req] are uniform random numbers;
     ``greedy`` marks requests that take the target's maximum.  accepted [n_req] gets the number of
     accepted drafts, tokens [rows] the accepted drafts, the drawn token and -1 behind it."""
-    import torch
-    dev = target.device
-    if dev.type != "cuda":
+    dev = target.get_device()
+    if dev < 0:
         raise ValueError("target is not a CUDA tensor")
-    dtypes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-    i32, f32 = (torch.int32,), (torch.float32,)
-    rows, n_req = target.shape[0], row_start.shape[0] - 1
-    a = VerifyArgs(
-        target=_check(target, "target", tuple(dtypes), (rows, None), dev),
-        target_stride=_row_stride(target), dtype=dtypes[target.dtype], vocab=target.shape[1],
-        rows=rows, n_req=n_req, row_start=_packed(row_start, "row_start", i32, (None,), dev),
-        draft_tokens=_packed(draft_tokens, "draft_tokens", i32, (rows,), dev),
-        u=_packed(u, "u", f32, (rows,), dev), r=_packed(r, "r", f32, (n_req,), dev),
-        accepted=_packed(accepted, "accepted", i32, (n_req,), dev),
-        tokens=_packed(tokens, "tokens", i32, (rows,), dev))
-    if draft is not None:
-        a.draft = _check(draft, "draft", (target.dtype,), tuple(target.shape), dev)
-        a.draft_stride = _row_stride(draft)
-    if greedy is not None:
-        a.greedy = _packed(greedy, "greedy", i32, (n_req,), dev)
-    with torch.cuda.device(dev):
-        rc = _lib().mono_verify_drafts(C.byref(a), _stream_of(stream, dev))
-    if rc != _m.MONO_OK:
-        raise _m.MonoError(rc, "mono_verify_drafts")
+    i32, f32 = torch.int32, torch.float32
+    tp, ts = _mat(target, "target", _PROBS, None, None, dev)
+    rows, vocab = target.shape
+    n_req = row_start.shape[0] - 1
+    dp, ds = (0, 0) if draft is None else _mat(draft, "draft", (target.dtype,), rows, vocab, dev)
+    args = _VERIFY.pack(tp, dp, ts, ds, _PROBS[target.dtype], vocab, rows, n_req,
+                        _vec(row_start, "row_start", i32, n_req + 1, dev),
+                        _vec(draft_tokens, "draft_tokens", i32, rows, dev),
+                        _vec(u, "u", f32, rows, dev), _vec(r, "r", f32, n_req, dev),
+                        0 if greedy is None else _vec(greedy, "greedy", i32, n_req, dev),
+                        _vec(accepted, "accepted", i32, n_req, dev),
+                        _vec(tokens, "tokens", i32, rows, dev))
+    _call("mono_verify_drafts", dev, stream, args)

@@ -47,6 +47,12 @@ def test_struct_layout_matches_header(tmp_path):
     for _, s in structs:
         want += [C.sizeof(s)] + [getattr(s, f[0]).offset for f in s._fields_]
     assert [int(v) for v in got] == want
+    # the binding packs them at once: the same sizes and places
+    for (_, s), packed in zip(structs[1:], (mc._ATTEND, mc._EVICT, mc._VERIFY)):
+        assert packed.size == C.sizeof(s)
+        vals = list(range(1, len(s._fields_) + 1))
+        a = s.from_buffer_copy(packed.pack(*vals))
+        assert [getattr(a, f[0]) for f in s._fields_] == vals
 
 
 @pytest.mark.parametrize("change,code", [
