@@ -1,0 +1,256 @@
+// What the kernels of the attention over the cache share: how a step's work is cut into pieces,
+// found alike by every CTA, and how the pieces are joined.
+#pragma once
+
+#include <algorithm>
+
+#include "cache_kernels.h"
+
+namespace mono {
+namespace attend {
+
+constexpr int MAX_REQ = 512;
+constexpr float UNSET = -1.0e30f;  // the reference m_q of a query that has seen no token
+// log2 of a weight times its token's scale: at most TOP, and m_q puts the largest of the tile that
+// moves it at BASE; scales below 2^LEAST (and zeros) count as that
+constexpr float TOP = 15.0f, BASE = 6.0f, LEAST = -90.0f;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+// How a kernel deals the work out: a tile of `tile` tokens, row groups of rows_per rows (cols query
+// columns at most, `heads` per row in a full 128-byte chunk of the record), teams of CTAs.
+struct Shape {
+  int tile, cols, heads, rows_per, chunks, teams;
+};
+inline Shape shape_of(const AttendArgs& a, int tile, int cols, int teams) {
+  Shape s;
+  s.tile = tile;
+  s.cols = cols;
+  s.heads = a.n_q / (a.kv_dim / a.head_dim) * (a.head_dim == 64 && a.kv_dim > 64 ? 2 : 1);
+  s.rows_per = std::min(16, cols / s.heads);
+  s.chunks = (a.kv_dim + 127) / 128;
+  s.teams = teams;
+  return s;
+}
+
+// The step as every CTA derives it: per request its rows' largest and smallest position, and
+// the units (tiles times row groups) of all requests before it.
+struct Plan {
+  int* pre;  // [n_req + 1]
+  int *pmax, *pmin;
+};
+
+// What the rows of a request see, in tiles: [0, head) and [body, body + tiles - head).
+struct Span {
+  int hi, lo, head, body, tiles, tile;
+  __device__ int token(int i) const { return (i < head ? i : body + i - head) * tile; }
+};
+
+__device__ __forceinline__ Span span_of(const AttendArgs& a, const Shape& sh, int pmax, int pmin) {
+  const int TT = sh.tile;  // (a power of two)
+  Span s;
+  s.tile = TT;
+  s.hi = pmax;
+  const int first = a.causal ? pmin : pmax;
+  s.lo = a.window > 0 ? max(0, first - a.window + 1) : 0;
+  const long long cap = (long long)a.kv.max_blocks * a.kv.block_size;  // fits 31 bits
+  const int last = min(pmax, (int)cap - 1);
+  const int lo = min(s.lo, (int)cap);
+  const int shift = __ffs(TT) - 1;
+  const int b0 = lo >> shift, b1 = last >= lo ? (last >> shift) + 1 : b0;
+  s.head = min((min(min(a.sinks, s.lo), (int)cap) + TT - 1) >> shift, b0);
+  s.body = b0;
+  s.tiles = s.head + b1 - b0;
+  return s;
+}
+
+// The cut: W units over the teams, no team (of those that get any) more than one unit above
+// another.
+struct Cut {
+  int teams, each, more;  // team k starts at each * k + min(k, more)
+  __device__ Cut(int W, int n) : teams(min(n, W)) {
+    each = teams ? W / teams : 0;
+    more = W - each * teams;
+  }
+  __device__ int start(int k) const { return each * k + min(k, more); }
+  __device__ int size(int k) const { return k < teams ? each + (k < more ? 1 : 0) : 0; }
+  __device__ int team_of(int g) const {
+    const int big = (each + 1) * more;
+    return g < big ? g / (each + 1) : more + (g - big) / each;
+  }
+};
+
+// One piece of work of a team: tiles [t0, t0 + n) of a row group of a request.
+struct Job {
+  int b, group, t0, n;
+  Span span;
+};
+
+// The items of a team in order, from the place that the plan found for its first unit.
+struct Jobs {
+  int b, group, t0, left;
+};
+__device__ __forceinline__ bool next_job(const AttendArgs& a, const Shape& sh, const Plan& p, Jobs& w, Job& it) {
+  if (w.left <= 0) return false;
+  it.b = w.b;
+  it.group = w.group;
+  it.t0 = w.t0;
+  it.span = span_of(a, sh, p.pmax[w.b], p.pmin[w.b]);
+  it.n = min(it.span.tiles - w.t0, w.left);
+  w.left -= it.n;
+  w.t0 = 0;
+  ++w.group;
+  if (w.left > 0 && p.pre[w.b] + w.group * it.span.tiles >= p.pre[w.b + 1]) {
+    w.group = 0;
+    do ++w.b;
+    while (p.pre[w.b + 1] <= p.pre[w.b]);  // (units are left, so there is such a request)
+  }
+  return true;
+}
+
+// Where row r's results are: its request's and group's units [g0, g0 + tiles) and its place in
+// the group; tiles 0: nothing to see.
+struct RowInfo {
+  int g0, tiles, place;
+};
+
+__device__ __forceinline__ float log2_of(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Fills the plan in shared memory and finds the team's first item (every thread of the block calls
+// it; the results are behind the caller's next barrier).  Waits for the kernels before.
+template <int NT>
+__device__ __forceinline__ void derive_plan(const AttendArgs& a, const Shape& sh, const Plan& plan,
+                                            int team, bool live, Jobs* start, int* total) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+#pragma unroll 1
+  for (int b = tid; b < a.n_req; b += NT) {
+    plan.pmax[b] = -1;
+    plan.pmin[b] = 0x7FFFFFFF;
+    plan.pre[b + 1] = 0;  // rows so far
+  }
+  pdl_trigger();
+  pdl_wait();
+  __syncthreads();
+#pragma unroll 1
+  for (int r = tid; r < a.rows; r += NT) {
+    const int p = a.positions[r], b = a.row_req[r];
+    if (p < 0) continue;
+    if (b < 0 || b >= a.n_req) {
+      if (blockIdx.x == 0) atomicOr(a.status, ST_UNMAPPED_PAGE);
+      continue;
+    }
+    atomicMax(&plan.pmax[b], p);
+    atomicMin(&plan.pmin[b], p);
+    atomicAdd(&plan.pre[b + 1], 1);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int W = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.n_req; b0 += 32) {
+      const int b = b0 + lane;
+      const int n = b < a.n_req ? plan.pre[b + 1] : 0;
+      int u = 0;
+      if (n > 0) {
+        u = (n + sh.rows_per - 1) / sh.rows_per * span_of(a, sh, plan.pmax[b], plan.pmin[b]).tiles;
+        if (plan.pmax[b] >= (long long)a.kv.max_blocks * a.kv.block_size && blockIdx.x == 0)
+          atomicOr(a.status, ST_UNMAPPED_PAGE);
+      }
+#pragma unroll 1
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, u, o);
+        if (lane >= o) u += y;
+      }
+      if (b < a.n_req) plan.pre[b + 1] = W + u;
+      W += __shfl_sync(0xffffffffu, u, 31);
+    }
+    __syncwarp();
+    if (lane == 0) {  // the team's first unit
+      plan.pre[0] = 0;
+      const Cut cut(W, sh.teams);
+      const int w0 = cut.start(team);
+      Jobs w = {0, 0, 0, live ? cut.size(team) : 0};
+      if (w.left > 0) {
+        int hi = a.n_req;  // the last request that starts by w0
+#pragma unroll 1
+        while (hi - w.b > 1) {
+          const int mid = (w.b + hi) >> 1;
+          if (plan.pre[mid] <= w0) w.b = mid; else hi = mid;
+        }
+        const int u = w0 - (w.b ? plan.pre[w.b] : 0);
+        const int tiles = span_of(a, sh, plan.pmax[w.b], plan.pmin[w.b]).tiles;
+        w.group = u / tiles;
+        w.t0 = u - w.group * tiles;
+      }
+      *start = w;
+      if (blockIdx.x == 0) *total = W;
+    }
+  }
+}
+
+// Row r's place, by a whole warp.
+__device__ __forceinline__ RowInfo row_info(const AttendArgs& a, const Shape& sh, const Plan& plan,
+                                            int r) {
+  const int b = a.row_req[r], lane = threadIdx.x & 31;
+  RowInfo info = {0, 0, 0};
+  if (a.positions[r] >= 0 && b >= 0 && b < a.n_req) {
+    int rank = 0;
+#pragma unroll 1
+    for (int i = lane; i < r; i += 32) rank += a.row_req[i] == b && a.positions[i] >= 0;
+    rank = __reduce_add_sync(0xffffffffu, rank);
+    const Span s = span_of(a, sh, plan.pmax[b], plan.pmin[b]);
+    const int group = rank / sh.rows_per;
+    info = {plan.pre[b] + group * s.tiles, s.tiles, rank - group * sh.rows_per};
+  }
+  return info;
+}
+
+// The rows of group `group` of request b, in row order, by a whole warp: their number.
+__device__ __forceinline__ int group_rows(const AttendArgs& a, const Shape& sh, int b, int group,
+                                          int* rows, int* pos) {
+  const int first = group * sh.rows_per, lane = threadIdx.x & 31;
+  int seen = 0, n = 0;
+#pragma unroll 1
+  for (int r0 = 0; r0 < a.rows && n < sh.rows_per; r0 += 32) {
+    const int r = r0 + lane;
+    const int q = r < a.rows ? a.row_req[r] : -1, p0 = r < a.rows ? a.positions[r] : -1;
+    const int p = q == b ? p0 : -1;
+    const uint32_t m = __ballot_sync(0xffffffffu, p >= 0);
+    const int rank = seen + __popc(m & ((1u << lane) - 1)) - first;
+    if (p >= 0 && rank >= 0 && rank < sh.rows_per) rows[rank] = r, pos[rank] = p;
+    seen += __popc(m);
+    n = max(0, min(sh.rows_per, seen - first));
+  }
+  return n;
+}
+
+// A piece in the workspace: [team][2 slots][chunk][column]: m, l, two words of padding, O.
+constexpr int PART_LD = 128 + 4;
+struct Pieces {
+  float* part;
+  RowInfo* rows;  // [rows]
+  int* total;     // units of the step
+};
+
+cudaError_t launch_join(const Launch&, const AttendArgs&, const Shape&, const Pieces&);
+// The records as a tensor map (k_attend.cu); false where it cannot be one.
+bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int width, int run, int box);
+
+}  // namespace attend
+
+// The kernel for many query columns (k_attend.cu) and the one for few (k_attend_few.cu).
+cudaError_t attend_tc_prepare();
+cudaError_t launch_attend_tc(const Launch&, const AttendArgs&, const attend::Pieces&, int sms);
+cudaError_t attend_few_prepare();
+bool attend_few_fits(const AttendArgs&);
+cudaError_t launch_attend_few(const Launch&, const AttendArgs&, const attend::Pieces&, int sms);
+cudaError_t launch_attend_weights(const Launch&, const AttendArgs&, const attend::Pieces&, int sms);
+
+}  // namespace mono

@@ -33,24 +33,20 @@
 // Every mbarrier wait is bounded; a wait that runs out is reported, and from then on every role
 // runs its loop without waiting, copying or issuing, so that the barriers among warps still
 // complete and TMEM is freed.
-#include <cudaTypedefs.h>
-
-#include <algorithm>
-
-#include "cache_kernels.h"
+#include "attend_plan.cuh"
 #include "tc_common.cuh"
 
 namespace mono {
 namespace {
 
 using namespace tc;
+using namespace attend;
 
 constexpr int TT = 128;        // tokens per tile
 constexpr int NQ = 96;         // query columns at most
 constexpr int MERGE = 64;      // up to here both terms of the queries are columns of one MMA
 constexpr int GROUP = 16;      // rows of a group at most
 constexpr int ST = 5;          // tiles in the ring
-constexpr int MAX_REQ = 512;
 constexpr int THREADS = 24 * 32;
 constexpr int SOFT_WARPS = 16, SOFT = SOFT_WARPS * 32, GROUPS = SOFT_WARPS / 4;
 constexpr int WIDE_WARP = 16, WIDE_WARPS = 4, S_WARP = 20, O_WARP = 21;
@@ -58,12 +54,6 @@ constexpr int LOAD_WARP = 22, LOAD_WARPS = 2;
 // registers a thread: softmax warps take what the others give up (in all, the launch's)
 constexpr int REGS = 80, SOFT_REGS = 88, OTHER_REGS = 64;
 static_assert(SOFT_REGS * SOFT + OTHER_REGS * 256 == REGS * THREADS, "register split");
-// log2 of a weight times its token's scale: at most TOP, and m_q puts the largest of the tile that
-// moves it at BASE; scales below 2^LEAST (and zeros) count as that in the choice of m_q
-constexpr float TOP = 15.0f, BASE = 6.0f, LEAST = -90.0f;
-constexpr float UNSET = -1.0e30f;  // m_q of a query that has seen no token
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-
 constexpr int K_TILE = TT * 128, V_TILE = 2 * K_TILE;
 constexpr int K_OFF = 0;
 constexpr int V_OFF = K_OFF + ST * K_TILE;  // widened tiles [2]: dimensions 0..63, then 64..127
@@ -88,122 +78,16 @@ constexpr uint32_t S_IDESC = (1u << 23) | ((uint32_t)(TT >> 4) << 24);
 // kind::f16: f16 x f16, f32 accumulators, both MN-major.
 constexpr uint32_t O_IDESC = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(TT >> 4) << 24);
 
-// The step as every CTA derives it: per request its rows' largest and smallest position, and
-// the units (tiles times row groups) of all requests before it.
-struct Plan {
-  int* pre;  // [n_req + 1]
-  int *pmax, *pmin;
-};
-
-// What the rows of a request see, in tiles: [0, head) and [body, body + tiles - head).
-struct Span {
-  int hi, lo, head, body, tiles;
-  __device__ int token(int i) const { return (i < head ? i : body + i - head) * TT; }
-};
-
-struct Shape {
-  int width;     // bytes of the chunk: 128, or 64 in the last of an odd number of 64-wide slices
-  int heads;     // heads per row in a full chunk
-  int rows_per;  // rows of a group
-  int chunks, teams;
-};
-
-__device__ __forceinline__ Shape shape_of(const AttendArgs& a, int grid) {
-  Shape s;
-  const int hpg = a.n_q / (a.kv_dim / a.head_dim);
-  s.heads = hpg * (a.head_dim == 64 && a.kv_dim > 64 ? 2 : 1);
-  s.rows_per = min(GROUP, NQ / s.heads);
-  s.chunks = (a.kv_dim + 127) / 128;
-  s.teams = grid / s.chunks;
-  s.width = 128;
-  return s;
-}
-
-__device__ __forceinline__ Span span_of(const AttendArgs& a, int pmax, int pmin) {
-  Span s;
-  s.hi = pmax;
-  const int first = a.causal ? pmin : pmax;
-  s.lo = a.window > 0 ? max(0, first - a.window + 1) : 0;
-  const long long cap = (long long)a.kv.max_blocks * a.kv.block_size;  // fits 31 bits
-  const int last = min(pmax, (int)cap - 1);
-  const int lo = min(s.lo, (int)cap);
-  const int b0 = lo / TT, b1 = last >= lo ? last / TT + 1 : b0;
-  s.head = min((min(min(a.sinks, s.lo), (int)cap) + TT - 1) / TT, b0);
-  s.body = b0;
-  s.tiles = s.head + b1 - b0;
-  return s;
-}
-
-// The cut: W units over the teams, no team (of those that get any) more than one unit above
-// another.
-struct Cut {
-  int teams, each, more;  // team k starts at each * k + min(k, more)
-  __device__ Cut(int W, int n) : teams(min(n, W)) {
-    each = teams ? W / teams : 0;
-    more = W - each * teams;
-  }
-  __device__ int start(int k) const { return each * k + min(k, more); }
-  __device__ int size(int k) const { return k < teams ? each + (k < more ? 1 : 0) : 0; }
-  __device__ int team_of(int g) const {
-    const int big = (each + 1) * more;
-    return g < big ? g / (each + 1) : more + (g - big) / each;
-  }
-};
-
-// One piece of work of a team: tiles [t0, t0 + n) of a row group of a request.
-struct Item {
-  int b, group, t0, n;
-  Span span;
-};
-
-// The items of a team in order, from the place that the plan found for its first unit.
-struct Items {
-  int b, group, t0, left;
-};
-__device__ __forceinline__ bool next_item(const AttendArgs& a, const Plan& p, Items& w, Item& it) {
-  if (w.left <= 0) return false;
-  it.b = w.b;
-  it.group = w.group;
-  it.t0 = w.t0;
-  it.span = span_of(a, p.pmax[w.b], p.pmin[w.b]);
-  it.n = min(it.span.tiles - w.t0, w.left);
-  w.left -= it.n;
-  w.t0 = 0;
-  ++w.group;
-  if (w.left > 0 && p.pre[w.b] + w.group * it.span.tiles >= p.pre[w.b + 1]) {
-    w.group = 0;
-    do ++w.b;
-    while (p.pre[w.b + 1] <= p.pre[w.b]);  // (units are left, so there is such a request)
-  }
-  return true;
-}
-
-// Where row r's results are: its request's and group's units [g0, g0 + tiles) and its place in
-// the group; tiles 0: nothing to see.
-struct RowInfo {
-  int g0, tiles, place;
-};
-
 struct Args {
   CUtensorMap codes, scales;  // the cache as [pages][tokens][bytes], boxes of box tokens
   int box;                    // 0: no maps
   AttendArgs a;
-  float* part;     // [teams][2 slots][chunks][NQ][128 + 2]: O, then m and l
-  RowInfo* rows;   // [rows]
-  int* total;      // units of the step
+  Shape sh;
+  float* part;    // workspace (Pieces)
+  RowInfo* rows;
+  int* total;
 };
-constexpr int PART_LD = 128 + 4;
 
-__device__ __forceinline__ float log2_of(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // Two f32 as f16, the first in the low half.
 __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
   uint32_t r;
@@ -298,7 +182,7 @@ struct Shared {
   int slice[NQ], group_row[GROUP], group_pos[GROUP];
   uint32_t tmem;
   int cols, nrows, abort;
-  Items start;
+  Jobs start;
 };
 static_assert(SMEM_BYTES + sizeof(Shared) <= 227 * 1024, "shared memory");
 
@@ -505,7 +389,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   plan.pmax = plan.pre + MAX_REQ + 4;
   plan.pmin = plan.pmax + MAX_REQ;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const Shape sh = shape_of(a, gridDim.x);
+  const Shape& sh = ar.sh;
   const int team = blockIdx.x / sh.chunks, chunk = blockIdx.x - team * sh.chunks;
   const int chunk_bytes = min(128, a.kv_dim - 128 * chunk);
 
@@ -525,83 +409,19 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   if (tid < 2 * IMG / 4) reinterpret_cast<uint32_t*>(sm + QIMG_OFF)[tid] = 0x7F7F7F7Fu;
   fence_proxy_async_shared();
 
-  // ---------------------------------------------------------------------------- the cut
-#pragma unroll 1
-  for (int b = tid; b < a.n_req; b += THREADS) {
-    plan.pmax[b] = -1;
-    plan.pmin[b] = 0x7FFFFFFF;
-    plan.pre[b + 1] = 0;  // rows so far
-  }
-  pdl_trigger();
-  pdl_wait();
-  __syncthreads();
-#pragma unroll 1
-  for (int r = tid; r < a.rows; r += THREADS) {
-    const int p = a.positions[r], b = a.row_req[r];
-    if (p < 0) continue;
-    if (b < 0 || b >= a.n_req) {
-      if (blockIdx.x == 0) atomicOr(a.status, ST_UNMAPPED_PAGE);
-      continue;
-    }
-    atomicMax(&plan.pmax[b], p);
-    atomicMin(&plan.pmin[b], p);
-    atomicAdd(&plan.pre[b + 1], 1);
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int W = 0;
-#pragma unroll 1
-    for (int b0 = 0; b0 < a.n_req; b0 += 32) {
-      const int b = b0 + lane;
-      const int n = b < a.n_req ? plan.pre[b + 1] : 0;
-      int u = 0;
-      if (n > 0) {
-        u = (n + sh.rows_per - 1) / sh.rows_per * span_of(a, plan.pmax[b], plan.pmin[b]).tiles;
-        if (plan.pmax[b] >= (long long)a.kv.max_blocks * a.kv.block_size && blockIdx.x == 0)
-          atomicOr(a.status, ST_UNMAPPED_PAGE);
-      }
-#pragma unroll 1
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, u, o);
-        if (lane >= o) u += y;
-      }
-      if (b < a.n_req) plan.pre[b + 1] = W + u;
-      W += __shfl_sync(0xffffffffu, u, 31);
-    }
-    __syncwarp();
-    if (lane == 0) {  // the team's first unit
-      plan.pre[0] = 0;
-      const Cut cut(W, sh.teams);
-      const int w0 = cut.start(team);
-      Items w = {0, 0, 0, team < sh.teams ? cut.size(team) : 0};
-      if (w.left > 0) {
-        int hi = a.n_req;  // the last request that starts by w0
-#pragma unroll 1
-        while (hi - w.b > 1) {
-          const int mid = (w.b + hi) >> 1;
-          if (plan.pre[mid] <= w0) w.b = mid; else hi = mid;
-        }
-        const int u = w0 - (w.b ? plan.pre[w.b] : 0);
-        const int tiles = span_of(a, plan.pmax[w.b], plan.pmin[w.b]).tiles;
-        w.group = u / tiles;
-        w.t0 = u - w.group * tiles;
-      }
-      ss.start = w;
-      if (blockIdx.x == 0) *ar.total = W;
-    }
-  }
+  derive_plan<THREADS>(a, sh, plan, team, team < sh.teams, &ss.start, ar.total);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ss.tmem;
-  Items items = ss.start;
-  Item im;
+  Jobs items = ss.start;
+  Job im;
 
   if (warp >= LOAD_WARP) {
     // ------------------------------------------------------- loads: a warp takes every other tile
     regs_down<OTHER_REGS>();
     int ni = warp - LOAD_WARP;
-    bool more = next_item(a, plan, items, im);
+    bool more = next_job(a, sh, plan, items, im);
     // a lane per box of the next tile (of a token each without maps, four times): its page, on its
     // way while the tile before is loaded, and its first token's place in it
     const int box = ar.box ? ar.box : 1, bs = a.kv.block_size;
@@ -609,7 +429,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     int page[4], row[4], t0 = 0;
     auto locate = [&]() {
 #pragma unroll 1
-      while (more && ni >= im.n) ni -= im.n, more = next_item(a, plan, items, im);
+      while (more && ni >= im.n) ni -= im.n, more = next_job(a, sh, plan, items, im);
       if (!more) return;
       t0 = im.span.token(im.t0 + ni);
 #pragma unroll
@@ -750,7 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     if (elect_one()) tc_cp_img(tmem + SF_ONE, sm + ONE_OFF);
     __syncwarp();
 #pragma unroll 1
-    for (int item = 0; next_item(a, plan, items, im); ++item) {
+    for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
       wait(&ss.q_full, item & 1, a.status, abort);
       const Deal deal(ss.cols);
       const bool merged = deal.merged();
@@ -789,23 +609,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     // first, where the second kernel finds the rows' results
 #pragma unroll 1
     for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
-      const int b = a.row_req[r];
-      RowInfo info = {0, 0, 0};
-      if (a.positions[r] >= 0 && b >= 0 && b < a.n_req) {
-        int rank = 0;
-#pragma unroll 1
-        for (int i = lane; i < r; i += 32) rank += a.row_req[i] == b && a.positions[i] >= 0;
-        rank = __reduce_add_sync(0xffffffffu, rank);
-        const Span s = span_of(a, plan.pmax[b], plan.pmin[b]);
-        const int group = rank / sh.rows_per;
-        info = {plan.pre[b] + group * s.tiles, s.tiles, rank - group * sh.rows_per};
-      }
+      const RowInfo info = row_info(a, sh, plan, r);
       if (lane == 0) ar.rows[r] = info;
     }
     int it = 0;
     uint32_t ph = 0;
 #pragma unroll 1
-    for (int item = 0; next_item(a, plan, items, im); ++item) {
+    for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
       wait(&ss.q_full, item & 1, a.status, abort);
       const Deal deal(ss.cols);
       const uint32_t idesc = O_IDESC | ((uint32_t)(deal.nqp >> 3) << 17);
@@ -844,24 +654,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     w.to_log2 = a.scale * LOG2E;
     w.tmem = tmem + ((uint32_t)(32 * quad) << 16);
 #pragma unroll 1
-    while (next_item(a, plan, items, im)) {
+    while (next_job(a, sh, plan, items, im)) {
       // ---- the group's rows and queries
       bar_sync<SOFT>(1);  // the previous item's columns are no longer in use
       if (warp == 0) {
-        const int first = im.group * sh.rows_per;
-        int seen = 0, n = 0;
-#pragma unroll 1
-        for (int r0 = 0; r0 < a.rows && n < sh.rows_per; r0 += 32) {
-          const int r = r0 + lane;
-          const int q = r < a.rows ? a.row_req[r] : -1, p0 = r < a.rows ? a.positions[r] : -1;
-          const int p = q == im.b ? p0 : -1;
-          const uint32_t m = __ballot_sync(0xffffffffu, p >= 0);
-          const int rank = seen + __popc(m & ((1u << lane) - 1)) - first;
-          if (p >= 0 && rank >= 0 && rank < sh.rows_per)
-            ss.group_row[rank] = r, ss.group_pos[rank] = p;
-          seen += __popc(m);
-          n = max(0, min(sh.rows_per, seen - first));
-        }
+        const int n = group_rows(a, sh, im.b, im.group, ss.group_row, ss.group_pos);
         const int cols = (n * cheads + 15) & ~15;
         if (lane == 0) ss.cols = cols == 80 ? 96 : cols, ss.nrows = n;
       }
@@ -1046,144 +843,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   }
 }
 
-// Joins the pieces of a (row, head): a warp each, 4 dimensions a lane.  Rows that one piece
-// holds are done; pad rows and rows that see nothing get zeros.
-constexpr int JOIN_WARPS = 4;
-__global__ void __launch_bounds__(JOIN_WARPS * 32) attend_join_kernel(const Args ar, int grid) {
-  const AttendArgs& a = ar.a;
-  pdl_trigger();
-  pdl_wait();
-  const int r = blockIdx.x, h = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (h >= a.n_q) return;
-  const Shape sh = shape_of(a, grid);
-  const RowInfo info = ar.rows[r];
-  const int d = 4 * lane & (a.head_dim - 1);
-  __nv_bfloat16* o = a.o + r * a.o_stride + (long long)h * a.head_dim + d;
-  if (info.tiles == 0) {
-    *reinterpret_cast<uint2*>(o) = make_uint2(0u, 0u);
-    if (lane == 0) a.lse[(long long)r * a.n_q + h] = -INFINITY;
-    return;
-  }
-  const Cut cut(*ar.total, sh.teams);
-  const int k0 = cut.team_of(info.g0), k1 = cut.team_of(info.g0 + info.tiles - 1);
-  if (k0 == k1) return;  // whole in one team
-  const int chunk = h / sh.heads, hpg = a.n_q / (a.kv_dim / a.head_dim);
-  const int cheads = hpg * (min(128, a.kv_dim - 128 * chunk) > a.head_dim ? 2 : 1);
-  const int c = info.place * cheads + (h - chunk * sh.heads);
-  auto piece = [&](int k) {
-    const int slot = cut.start(k) > info.g0 ? 0 : 1;  // began before this team, or in it
-    return ar.part + (((size_t)(k * 2 + slot) * sh.chunks + chunk) * NQ + c) * PART_LD;
-  };
-  float M = UNSET;
-#pragma unroll 1
-  for (int k = k0 + lane; k <= k1; k += 32) M = fmaxf(M, piece(k)[0]);
-  M = warp_max(M);
-  float4 num = {0.0f, 0.0f, 0.0f, 0.0f};
-  float den = 0.0f;
-  // 64 wide: the upper half warp takes every other piece
-  const int first = a.head_dim == 64 ? lane >> 4 : 0, step = a.head_dim == 64 ? 2 : 1;
-#pragma unroll 2
-  for (int k = k0 + first; k <= k1; k += step) {
-    const float* p = piece(k);
-    const float f = ex2(p[0] - M);
-    const float4 x = *reinterpret_cast<const float4*>(p + 4 + d);
-    den = fmaf(f, p[1], den);
-    num.x = fmaf(f, x.x, num.x), num.y = fmaf(f, x.y, num.y);
-    num.z = fmaf(f, x.z, num.z), num.w = fmaf(f, x.w, num.w);
-  }
-  if (a.head_dim == 64) {
-    den += __shfl_xor_sync(0xffffffffu, den, 16);
-    num.x += __shfl_xor_sync(0xffffffffu, num.x, 16), num.y += __shfl_xor_sync(0xffffffffu, num.y, 16);
-    num.z += __shfl_xor_sync(0xffffffffu, num.z, 16), num.w += __shfl_xor_sync(0xffffffffu, num.w, 16);
-  }
-  const float inv = den == 0.0f ? 0.0f : 1.0f / den;
-  if (den == 0.0f) num = {0.0f, 0.0f, 0.0f, 0.0f};
-  *reinterpret_cast<uint2*>(o) =
-      make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
-  if (lane == 0)
-    a.lse[(long long)r * a.n_q + h] = den == 0.0f ? -INFINITY : (log2f(den) + M) * LN2;
-}
-
-// weights[b][t] += sum over b's rows and heads of exp(s - lse): a thread per token, rows and
-// heads in order.
-template <int DH>
-__global__ void __launch_bounds__(TT) attend_weights_kernel(AttendArgs a, int tiles) {
-  pdl_wait();
-  const int b = blockIdx.y, G = a.kv_dim / DH, hpg = a.n_q / G;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const long long t = (long long)tile * TT + threadIdx.x;
-    float w = 0.0f;
-    bool any = false;
-    for (int r = 0; r < a.rows; ++r) {
-      if (a.row_req[r] != b || a.positions[r] < 0) continue;
-      int hi = a.positions[r];
-      if (!a.causal)
-        for (int i = 0; i < a.rows; ++i)
-          if (a.row_req[i] == b) hi = max(hi, a.positions[i]);
-      const int lo = a.window > 0 ? max(0, hi - a.window + 1) : 0;
-      if (t > hi || (t < lo && t >= a.sinks)) continue;
-      const long long off = record_offset(a.kv, b, (int)t);
-      if (off < 0) continue;
-      any = true;
-      const float sc = *reinterpret_cast<const float*>(a.kv.base + off + a.kv_dim) * a.scale;
-      for (int h = 0; h < a.n_q; ++h) {
-        float d = 0.0f;
-        for (int i = 0; i < DH; ++i) {
-          uint32_t f[2];
-          e4m3x4_to_f16x4(a.kv.base[off + (h / hpg) * DH + i], f);
-          d = fmaf(__half2float(__ushort_as_half((unsigned short)(f[0] & 0xFFFF))),
-                   __bfloat162float(a.q[r * a.q_stride + h * DH + i]), d);
-        }
-        w += expf(d * sc - a.lse[(size_t)r * a.n_q + h]);
-      }
-    }
-    if (any && t < a.weights_stride) a.weights[b * a.weights_stride + t] += w;
-  }
-}
-
-// The records as a 3D byte tensor [pages][tokens][width], boxes of run (128: swizzled, bytes beyond
-// width read as 0) x box tokens; false where its strides are beyond a tensor map's.
-bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int width, int run, int box) {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  if (!encode) {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || !fn) {
-      (void)cudaGetLastError();
-      return false;
-    }
-    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
-  if (kv.stride_block >= (1ll << 40) || kv.stride_tok >= (1ll << 40)) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)kv.block_size, (cuuint64_t)kv.num_blocks};
-  const cuuint64_t strides[2] = {(cuuint64_t)kv.stride_tok, (cuuint64_t)kv.stride_block};
-  const cuuint32_t boxes[3] = {(cuuint32_t)run, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
-  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(kv.base), dims, strides,
-                boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                run == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-struct Layout {
-  size_t rows, total, part, bytes;
-};
-Layout layout(int max_rows, int sms) {
-  Layout l;
-  l.total = 0;
-  l.rows = 256;
-  l.part = l.rows + ((size_t)max_rows * sizeof(RowInfo) + 255) / 256 * 256;
-  l.bytes = l.part + (size_t)sms * 2 * NQ * PART_LD * sizeof(float);
-  return l;
-}
-
 }  // namespace
 
-size_t attend_workspace_bytes(int max_rows, int sms) { return layout(max_rows, sms).bytes; }
-
-cudaError_t attend_prepare() {
+cudaError_t attend_tc_prepare() {
   // the roles' register split adds up to what a block launches with
   cudaFuncAttributes f;
   cudaError_t e = cudaFuncGetAttributes(&f, attend_kernel);
@@ -1192,29 +854,19 @@ cudaError_t attend_prepare() {
   return cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
 }
 
-cudaError_t launch_attend(const Launch& L, const AttendArgs& a, uint8_t* ws, int max_rows, int sms) {
-  const Layout l = layout(max_rows, sms);
-  Args ar = {{}, {}, 0, a, reinterpret_cast<float*>(ws + l.part), reinterpret_cast<RowInfo*>(ws + l.rows),
-             reinterpret_cast<int*>(ws + l.total)};
+cudaError_t launch_attend_tc(const Launch& L, const AttendArgs& a, const attend::Pieces& ws, int sms) {
+  const int chunks = (a.kv_dim + 127) / 128;
+  Args ar = {{}, {}, 0, a, shape_of(a, TT, NQ, sms / chunks), ws.part, ws.rows, ws.total};
   // boxes of whole runs of a page, 8 rows (a swizzle atom) or more, that tiles are made of
   const int bs = a.kv.block_size;
-  if (bs % 8 == 0 && a.kv.num_blocks <= INT32_MAX) {
+  if (bs % 8 == 0) {
     const int box = std::min(bs & -bs, TT);
     if (encode_cache_map(&ar.codes, a.kv, a.kv_dim, 128, box) &&
         encode_cache_map(&ar.scales, a.kv, a.kv_dim + 16, 16, box))
       ar.box = box;
   }
-  cudaError_t e = launch_ex(L, dim3(sms), dim3(THREADS), SMEM_BYTES, attend_kernel, ar);
-  if (e == cudaSuccess)
-    e = launch_ex(L, dim3(a.rows, (a.n_q + JOIN_WARPS - 1) / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0,
-                  attend_join_kernel, ar, sms);
-  const long long cap = (long long)a.kv.max_blocks * a.kv.block_size;
-  const int tiles = (int)((cap + TT - 1) / TT);
-  if (e == cudaSuccess && a.weights)
-    e = launch_ex(L, dim3(min(tiles, 1024), a.n_req), dim3(TT), 0,
-                  a.head_dim == 128 ? attend_weights_kernel<128> : attend_weights_kernel<64>, a,
-                  tiles);
-  return e;
+  const cudaError_t e = launch_ex(L, dim3(sms), dim3(THREADS), SMEM_BYTES, attend_kernel, ar);
+  return e == cudaSuccess ? attend::launch_join(L, a, ar.sh, ws) : e;
 }
 
 }  // namespace mono

@@ -1,0 +1,137 @@
+// The attention over the cache: which kernel runs, and the join of its pieces.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "attend_plan.cuh"
+
+namespace mono {
+namespace attend {
+namespace {
+
+// Joins the pieces of a (row, head): a warp each, 4 dimensions a lane.  Rows that one piece
+// holds are done; pad rows and rows that see nothing get zeros.
+constexpr int JOIN_WARPS = 4;
+__global__ void __launch_bounds__(JOIN_WARPS * 32) attend_join_kernel(const AttendArgs a, const Shape sh, const Pieces ar) {
+  pdl_trigger();
+  pdl_wait();
+  const int r = blockIdx.x, h = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (h >= a.n_q) return;
+  const RowInfo info = ar.rows[r];
+  const int d = 4 * lane & (a.head_dim - 1);
+  __nv_bfloat16* o = a.o + r * a.o_stride + (long long)h * a.head_dim + d;
+  if (info.tiles == 0) {
+    *reinterpret_cast<uint2*>(o) = make_uint2(0u, 0u);
+    if (lane == 0) a.lse[(long long)r * a.n_q + h] = -INFINITY;
+    return;
+  }
+  const Cut cut(*ar.total, sh.teams);
+  const int k0 = cut.team_of(info.g0), k1 = cut.team_of(info.g0 + info.tiles - 1);
+  if (k0 == k1) return;  // whole in one team
+  const int chunk = h / sh.heads, hpg = a.n_q / (a.kv_dim / a.head_dim);
+  const int cheads = hpg * (min(128, a.kv_dim - 128 * chunk) > a.head_dim ? 2 : 1);
+  const int c = info.place * cheads + (h - chunk * sh.heads);
+  auto piece = [&](int k) {
+    const int slot = cut.start(k) > info.g0 ? 0 : 1;  // began before this team, or in it
+    return ar.part + (((size_t)(k * 2 + slot) * sh.chunks + chunk) * sh.cols + c) * PART_LD;
+  };
+  float M = UNSET;
+#pragma unroll 1
+  for (int k = k0 + lane; k <= k1; k += 32) M = fmaxf(M, piece(k)[0]);
+  M = warp_max(M);
+  float4 num = {0.0f, 0.0f, 0.0f, 0.0f};
+  float den = 0.0f;
+  // 64 wide: the upper half warp takes every other piece
+  const int first = a.head_dim == 64 ? lane >> 4 : 0, step = a.head_dim == 64 ? 2 : 1;
+#pragma unroll 2
+  for (int k = k0 + first; k <= k1; k += step) {
+    const float* p = piece(k);
+    const float f = ex2(p[0] - M);
+    const float4 x = *reinterpret_cast<const float4*>(p + 4 + d);
+    den = fmaf(f, p[1], den);
+    num.x = fmaf(f, x.x, num.x), num.y = fmaf(f, x.y, num.y);
+    num.z = fmaf(f, x.z, num.z), num.w = fmaf(f, x.w, num.w);
+  }
+  if (a.head_dim == 64) {
+    den += __shfl_xor_sync(0xffffffffu, den, 16);
+    num.x += __shfl_xor_sync(0xffffffffu, num.x, 16), num.y += __shfl_xor_sync(0xffffffffu, num.y, 16);
+    num.z += __shfl_xor_sync(0xffffffffu, num.z, 16), num.w += __shfl_xor_sync(0xffffffffu, num.w, 16);
+  }
+  const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+  if (den == 0.0f) num = {0.0f, 0.0f, 0.0f, 0.0f};
+  *reinterpret_cast<uint2*>(o) =
+      make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
+  if (lane == 0)
+    a.lse[(long long)r * a.n_q + h] = den == 0.0f ? -INFINITY : (log2f(den) + M) * LN2;
+}
+
+}  // namespace
+
+// The records as a 3D byte tensor [pages][tokens][width], boxes of run (128: swizzled, bytes beyond
+// width read as 0) x box tokens; false where its strides are beyond a tensor map's.
+bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int width, int run, int box) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      fn = nullptr;
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }();
+  if (!encode || kv.num_blocks > INT32_MAX) return false;
+  if (kv.stride_block >= (1ll << 40) || kv.stride_tok >= (1ll << 40)) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)kv.block_size, (cuuint64_t)kv.num_blocks};
+  const cuuint64_t strides[2] = {(cuuint64_t)kv.stride_tok, (cuuint64_t)kv.stride_block};
+  const cuuint32_t boxes[3] = {(cuuint32_t)run, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(kv.base), dims, strides,
+                boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                run == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+
+cudaError_t launch_join(const Launch& L, const AttendArgs& a, const Shape& sh, const Pieces& ws) {
+  return launch_ex(L, dim3(a.rows, (a.n_q + JOIN_WARPS - 1) / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0,
+                   attend_join_kernel, a, sh, ws);
+}
+
+}  // namespace attend
+
+namespace {
+struct Layout {
+  size_t rows, total, part, bytes;
+};
+Layout layout(int max_rows, int sms) {
+  Layout l;
+  l.total = 0;
+  l.rows = 256;
+  l.part = l.rows + ((size_t)max_rows * sizeof(attend::RowInfo) + 255) / 256 * 256;
+  // pieces: two per team and chunk, of 96 columns and a team per `chunks` SMs, or of 16 columns
+  // and a team per SM with at most 8 chunks
+  l.bytes = l.part + (size_t)sms * 2 * 128 * attend::PART_LD * sizeof(float);
+  return l;
+}
+}  // namespace
+
+size_t attend_workspace_bytes(int max_rows, int sms) { return layout(max_rows, sms).bytes; }
+
+cudaError_t attend_prepare() {
+  cudaError_t e = attend_tc_prepare();
+  return e == cudaSuccess ? attend_few_prepare() : e;
+}
+
+cudaError_t launch_attend(const Launch& L, const AttendArgs& a, uint8_t* base, int max_rows, int sms) {
+  const Layout l = layout(max_rows, sms);
+  const attend::Pieces ws = {reinterpret_cast<float*>(base + l.part),
+                             reinterpret_cast<attend::RowInfo*>(base + l.rows),
+                             reinterpret_cast<int*>(base + l.total)};
+  cudaError_t e = attend_few_fits(a) ? launch_attend_few(L, a, ws, sms) : launch_attend_tc(L, a, ws, sms);
+  if (e == cudaSuccess && a.weights) e = launch_attend_weights(L, a, ws, sms);
+  return e;
+}
+
+}  // namespace mono
