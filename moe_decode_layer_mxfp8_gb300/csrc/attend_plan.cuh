@@ -123,6 +123,15 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Codes with the NaN ones as zeros.
+__device__ __forceinline__ uint32_t without_nan(uint32_t v) {
+  const uint32_t nan = (((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
+  return v & ~(nan * 0xFFu);
+}
+__device__ __forceinline__ uint4 without_nan(uint4 v) {
+  return make_uint4(without_nan(v.x), without_nan(v.y), without_nan(v.z), without_nan(v.w));
+}
+
 // Fills the plan in shared memory and finds the team's first item (every thread of the block calls
 // it; the results are behind the caller's next barrier).  Waits for the kernels before.
 template <int NT>

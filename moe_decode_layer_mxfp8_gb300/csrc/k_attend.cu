@@ -369,14 +369,6 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
   for (int c = 0; c < C; ++c) scratch[32 * c] = l[c];
 }
 
-__device__ __forceinline__ uint32_t without_nan(uint32_t v) {
-  const uint32_t nan = (((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
-  return v & ~(nan * 0xFFu);
-}
-__device__ __forceinline__ uint4 without_nan(uint4 v) {
-  return make_uint4(without_nan(v.x), without_nan(v.y), without_nan(v.z), without_nan(v.w));
-}
-
 __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constant__ Args ar) {
   const AttendArgs& a = ar.a;
   extern __shared__ uint8_t smem_raw[];
