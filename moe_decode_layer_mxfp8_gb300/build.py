@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmono_layer.so")
 SOURCES = ["k_gemm.cu", "k_expert_tc.cu", "k_dense_tc.cu", "k_norm.cu", "k_attn.cu", "k_route.cu", "mono_layer.cu",
-           "noalloc.cu", "k_attend.cu", "k_attend_few.cu", "k_attend_join.cu", "k_evict.cu", "k_verify.cu", "cache_ops.cu"]
+           "noalloc.cu", "k_attend.cu", "k_attend_weights.cu", "k_attend_join.cu", "k_evict.cu", "k_verify.cu", "cache_ops.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

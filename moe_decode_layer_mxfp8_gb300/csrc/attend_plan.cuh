@@ -10,6 +10,7 @@ namespace mono {
 namespace attend {
 
 constexpr int MAX_REQ = 512;
+constexpr int MAX_COLS = 96;  // query columns of a row group at most
 constexpr float UNSET = -1.0e30f;  // the reference m_q of a query that has seen no token
 // log2 of a weight times its token's scale: at most TOP, and m_q puts the largest of the tile that
 // moves it at BASE; scales below 2^LEAST (and zeros) count as that
@@ -249,17 +250,15 @@ struct Pieces {
 };
 
 cudaError_t launch_join(const Launch&, const AttendArgs&, const Shape&, const Pieces&);
-// The records as a tensor map (k_attend.cu); false where it cannot be one.
+// The records as a tensor map (k_attend_join.cu); false where it cannot be one.
 bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int width, int run, int box);
 
 }  // namespace attend
 
-// The kernel for many query columns (k_attend.cu) and the one for few (k_attend_few.cu).
+// The attention's kernel (k_attend.cu) and the gathering of its weights (k_attend_weights.cu).
 cudaError_t attend_tc_prepare();
 cudaError_t launch_attend_tc(const Launch&, const AttendArgs&, const attend::Pieces&, int sms);
-cudaError_t attend_few_prepare();
-bool attend_few_fits(const AttendArgs&);
-cudaError_t launch_attend_few(const Launch&, const AttendArgs&, const attend::Pieces&, int sms);
+cudaError_t attend_weights_prepare();
 cudaError_t launch_attend_weights(const Launch&, const AttendArgs&, const attend::Pieces&, int sms);
 
 }  // namespace mono

@@ -1,4 +1,4 @@
-// The attention over the cache: which kernel runs, and the join of its pieces.
+// The attention over the cache: its launches, and the join of its pieces.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -110,9 +110,8 @@ Layout layout(int max_rows, int sms) {
   l.total = 0;
   l.rows = 256;
   l.part = l.rows + ((size_t)max_rows * sizeof(attend::RowInfo) + 255) / 256 * 256;
-  // pieces: two per team and chunk, of 96 columns and a team per `chunks` SMs, or of 16 columns
-  // and a team per SM with at most 8 chunks
-  l.bytes = l.part + (size_t)sms * 2 * 128 * attend::PART_LD * sizeof(float);
+  // pieces: two per team and chunk, a team per `chunks` SMs
+  l.bytes = l.part + (size_t)sms * 2 * attend::MAX_COLS * attend::PART_LD * sizeof(float);
   return l;
 }
 }  // namespace
@@ -121,7 +120,7 @@ size_t attend_workspace_bytes(int max_rows, int sms) { return layout(max_rows, s
 
 cudaError_t attend_prepare() {
   cudaError_t e = attend_tc_prepare();
-  return e == cudaSuccess ? attend_few_prepare() : e;
+  return e == cudaSuccess ? attend_weights_prepare() : e;
 }
 
 cudaError_t launch_attend(const Launch& L, const AttendArgs& a, uint8_t* base, int max_rows, int sms) {
@@ -129,7 +128,7 @@ cudaError_t launch_attend(const Launch& L, const AttendArgs& a, uint8_t* base, i
   const attend::Pieces ws = {reinterpret_cast<float*>(base + l.part),
                              reinterpret_cast<attend::RowInfo*>(base + l.rows),
                              reinterpret_cast<int*>(base + l.total)};
-  cudaError_t e = attend_few_fits(a) ? launch_attend_few(L, a, ws, sms) : launch_attend_tc(L, a, ws, sms);
+  cudaError_t e = launch_attend_tc(L, a, ws, sms);
   if (e == cudaSuccess && a.weights) e = launch_attend_weights(L, a, ws, sms);
   return e;
 }
