@@ -10,11 +10,11 @@ namespace mono {
 namespace attend {
 
 constexpr int MAX_REQ = 512;
-constexpr int MAX_COLS = 96;  // query columns of a row group at most
+constexpr int MAX_COLS = 64;  // query columns of a row group at most
 constexpr float UNSET = -1.0e30f;  // the reference m_q of a query that has seen no token
-// log2 of a weight times its token's scale: at most TOP, and m_q puts the largest of the tile that
-// moves it at BASE; scales below 2^LEAST (and zeros) count as that
-constexpr float TOP = 15.0f, BASE = 6.0f, LEAST = -90.0f;
+// log2 of a weight times its token's scale: below 1, and m_q puts the largest of the tile that moves
+// it at BASE or just below; scales below 2^LEAST (and zeros) count as that
+constexpr float BASE = -30.0f, LEAST = -60.0f;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 // How a kernel deals the work out: a tile of `tile` tokens, row groups of rows_per rows (cols query
@@ -38,6 +38,8 @@ inline Shape shape_of(const AttendArgs& a, int tile, int cols, int teams) {
 struct Plan {
   int* pre;  // [n_req + 1]
   int *pmax, *pmin;
+  int* pos;    // [rows] the rows' positions, -1 for those that see nothing, and
+  short* req;  // their requests; both may be null
 };
 
 // What the rows of a request see, in tiles: [0, head) and [body, body + tiles - head).
@@ -151,6 +153,8 @@ __device__ __forceinline__ void derive_plan(const AttendArgs& a, const Shape& sh
 #pragma unroll 1
   for (int r = tid; r < a.rows; r += NT) {
     const int p = a.positions[r], b = a.row_req[r];
+    const bool live = p >= 0 && b >= 0 && b < a.n_req;
+    if (plan.pos) plan.pos[r] = live ? p : -1, plan.req[r] = (short)(live ? b : -1);
     if (p < 0) continue;
     if (b < 0 || b >= a.n_req) {
       if (blockIdx.x == 0) atomicOr(a.status, ST_UNMAPPED_PAGE);
@@ -208,12 +212,12 @@ __device__ __forceinline__ void derive_plan(const AttendArgs& a, const Shape& sh
 // Row r's place, by a whole warp.
 __device__ __forceinline__ RowInfo row_info(const AttendArgs& a, const Shape& sh, const Plan& plan,
                                             int r) {
-  const int b = a.row_req[r], lane = threadIdx.x & 31;
+  const int b = plan.req[r], lane = threadIdx.x & 31;
   RowInfo info = {0, 0, 0};
-  if (a.positions[r] >= 0 && b >= 0 && b < a.n_req) {
+  if (b >= 0) {
     int rank = 0;
 #pragma unroll 1
-    for (int i = lane; i < r; i += 32) rank += a.row_req[i] == b && a.positions[i] >= 0;
+    for (int i = lane; i < r; i += 32) rank += plan.req[i] == b;
     rank = __reduce_add_sync(0xffffffffu, rank);
     const Span s = span_of(a, sh, plan.pmax[b], plan.pmin[b]);
     const int group = rank / sh.rows_per;
@@ -223,18 +227,17 @@ __device__ __forceinline__ RowInfo row_info(const AttendArgs& a, const Shape& sh
 }
 
 // The rows of group `group` of request b, in row order, by a whole warp: their number.
-__device__ __forceinline__ int group_rows(const AttendArgs& a, const Shape& sh, int b, int group,
-                                          int* rows, int* pos) {
+__device__ __forceinline__ int group_rows(const AttendArgs& a, const Shape& sh, const Plan& plan, int b,
+                                          int group, int* rows, int* pos) {
   const int first = group * sh.rows_per, lane = threadIdx.x & 31;
   int seen = 0, n = 0;
 #pragma unroll 1
   for (int r0 = 0; r0 < a.rows && n < sh.rows_per; r0 += 32) {
     const int r = r0 + lane;
-    const int q = r < a.rows ? a.row_req[r] : -1, p0 = r < a.rows ? a.positions[r] : -1;
-    const int p = q == b ? p0 : -1;
-    const uint32_t m = __ballot_sync(0xffffffffu, p >= 0);
+    const bool in = r < a.rows && plan.req[r] == b;
+    const uint32_t m = __ballot_sync(0xffffffffu, in);
     const int rank = seen + __popc(m & ((1u << lane) - 1)) - first;
-    if (p >= 0 && rank >= 0 && rank < sh.rows_per) rows[rank] = r, pos[rank] = p;
+    if (in && rank >= 0 && rank < sh.rows_per) rows[rank] = r, pos[rank] = plan.pos[r];
     seen += __popc(m);
     n = max(0, min(sh.rows_per, seen - first));
   }

@@ -386,6 +386,12 @@ __device__ __forceinline__ void mul2(float& x, float& y, float a) {
       : "+f"(x), "+f"(y)
       : "f"(a));
 }
+__device__ __forceinline__ void mul2(float& x, float& y, float ax, float ay) {
+  asm("{\n .reg .b64 s, m;\n mov.b64 s, {%0, %1};\n mov.b64 m, {%2, %3};\n"
+      " mul.rn.f32x2 s, s, m;\n mov.b64 {%0, %1}, s;\n}"
+      : "+f"(x), "+f"(y)
+      : "f"(ax), "f"(ay));
+}
 // 8 bf16 values in a 16-byte word <-> 8 floats
 __device__ __forceinline__ void bf16x8_to_f32(const uint4 v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};

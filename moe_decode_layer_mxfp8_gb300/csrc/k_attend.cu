@@ -7,15 +7,12 @@
 // A 128-byte run of a record (a chunk: one 128-wide latent slice, or two 64-wide ones) and 128
 // tokens make a tile.  Tokens are the M of the first product, dimensions that of the second, and
 // queries the N of both: the heads that share a latent slice, times the rows of a request that
-// share its context (1 to 96 columns, no padding beyond 16), so the cache is read once for all of
-// them.  The first product takes the e4m3 tile as it lies in the cache (kind::mxf8f6f4); a bf16
-// query is the exact sum of two e4m3 terms under one power-of-two scale per 32 dimensions.  The
-// second takes P scale_t in f16 (the one rounding between the scores and o: 11 bits) and the tile
-// widened to f16, which is exact.  m_q is chosen so that the largest P scale_t is about 2^6: what
-// f16 cannot hold lies 2^-31 below it.  (Weights as two e4m3 terms under block scales would spare
-// the widening, but cost each weight three times the instructions: 270 us against
-// 145 at 48 rows over 8 contexts of 1K..64K when both were young; weights in bf16 took three
-// instructions per two codes to widen the tile, f16 takes one.)
+// share its context (1 to 64 columns, padded to 16).  Both products take the e4m3 tile as it lies
+// in the cache (kind::mxf8f6f4; the second one transposed), so a tile is read into shared memory
+// once and never rewritten.  A bf16 query is the exact sum of two e4m3 terms under one power-of-two
+// scale per 32 dimensions; P scale_t is two e4m3 terms (together 8 bits, the one rounding between
+// scores and o) under a power-of-two scale per column and 32 tokens.  The terms are columns of one
+// MMA, added when accumulators are read.
 // O stays in TMEM over a whole run of tiles: m_q, an integer, moves only when a weight passes it
 // by far (then O is rescaled, exactly).
 //
@@ -25,11 +22,15 @@
 // A pair that falls into one piece is finished there; pieces of the others leave (O, m, l) in
 // the workspace, which a second kernel joins.
 //
-// Roles: warps 0-7 softmax (TMEM lane quadrant = warp % 4: one token per thread; warp / 4: half
-// of the columns), 8-11 widening, 12 the first product's MMAs, 13 the second's, 14 and 15 loads
-// (every other tile each: TMA boxes through the page table, or cp.async for page sizes that are no
-// multiple of 8).  What runs once per launch or item is kept short,
-// in rolled loops: its instructions come from L2 or further away.
+// Roles: warps 0-15 softmax, a token per thread (TMEM lane quadrant = warp % 4) and 16 columns per
+// group of four warps: with 16 columns the groups take every fourth tile each, with 32 two groups
+// share every other tile, with more the groups share all tiles.  Warps 16 and 17 make the next
+// item's queries while the current one runs, 18 and 19 issue the first product's MMAs, 20 and 21
+// the second's, 22 and 23 load (every other tile each: TMA boxes through the page table, or cp.async
+// for page sizes that are no multiple of 8).  A wait for a barrier that is complete still costs a
+// warp 100 to 300 cycles, an MMA's issue some 60: hence two warps for each product, and one wait per
+// tile in the softmax.  What runs once per launch or item is kept short, in rolled loops: its
+// instructions come from L2 or further away.
 // Every mbarrier wait is bounded; a wait that runs out is reported, and from then on every role
 // runs its loop without waiting, copying or issuing, so that the barriers among warps still
 // complete and TMEM is freed.
@@ -43,40 +44,37 @@ using namespace tc;
 using namespace attend;
 
 constexpr int TT = 128;        // tokens per tile
-constexpr int NQ = 96;         // query columns at most
-constexpr int MERGE = 64;      // up to here both terms of the queries are columns of one MMA
+constexpr int NQ = MAX_COLS;   // query columns at most
 constexpr int GROUP = 16;      // rows of a group at most
-constexpr int ST = 5;          // tiles in the ring
+constexpr int ST = 8;          // tiles in the ring
+constexpr int C = 16;          // columns of a softmax warp
+constexpr int Q_TWICE = 32;    // items of up to so many columns have their queries made ahead
 constexpr int THREADS = 24 * 32;
 constexpr int SOFT_WARPS = 16, SOFT = SOFT_WARPS * 32, GROUPS = SOFT_WARPS / 4;
-constexpr int WIDE_WARP = 16, WIDE_WARPS = 4, S_WARP = 20, O_WARP = 21;
+constexpr int PREP_WARP = 16, PREP = 2 * 32, S_WARP = 18, O_WARP = 20, MMA_WARPS = 2;
 constexpr int LOAD_WARP = 22, LOAD_WARPS = 2;
-// registers a thread: softmax warps take what the others give up (in all, the launch's)
-constexpr int REGS = 80, SOFT_REGS = 88, OTHER_REGS = 64;
-static_assert(SOFT_REGS * SOFT + OTHER_REGS * 256 == REGS * THREADS, "register split");
-constexpr int K_TILE = TT * 128, V_TILE = 2 * K_TILE;
+constexpr int MAX_ROWS = 1024;
+constexpr int K_TILE = TT * 128, IMG = 512, SLOTS = 8;
 constexpr int K_OFF = 0;
-constexpr int V_OFF = K_OFF + ST * K_TILE;  // widened tiles [2]: dimensions 0..63, then 64..127
-constexpr int P_OFF = V_OFF + 2 * V_TILE;   // weights: columns 0..63, then 64..95
-constexpr int Q_OFF = P_OFF + V_TILE;       // hi rows, then lo rows
-constexpr int IMG = 512;
-constexpr int QIMG_OFF = Q_OFF + 2 * NQ * 128;
-constexpr int ONE_OFF = QIMG_OFF + IMG;
+constexpr int P_OFF = K_OFF + ST * K_TILE;      // weights [2]: tokens x (streams x (hi, lo) columns)
+constexpr int Q_OFF = P_OFF + 2 * K_TILE;       // queries: hi rows, then lo rows; [2] up to Q_TWICE columns
+constexpr int PIMG_OFF = Q_OFF + K_TILE;    // scale images of the weights [SLOTS],
+constexpr int QIMG_OFF = PIMG_OFF + SLOTS * IMG;  // of the queries [2],
+constexpr int ONE_OFF = QIMG_OFF + 2 * IMG;       // and of ones
 constexpr int SC_OFF = ONE_OFF + IMG;  // the 16 bytes behind the codes, scale first [ST][128]
 constexpr int PLAN_OFF = SC_OFF + ST * TT * 16;
-constexpr int SMEM_BYTES = PLAN_OFF + (3 * MAX_REQ + 4) * 4 + 1024;
-static_assert(V_OFF % 1024 == 0 && P_OFF % 1024 == 0 && Q_OFF % 1024 == 0 && (NQ * 128) % 1024 == 0,
-              "swizzle atoms");
-constexpr int CMAX = NQ / GROUPS;  // columns of a softmax warp at most
-static_assert(SOFT_WARPS * CMAX * 32 * 4 <= V_TILE + 2 * NQ * 128, "the sums' scratch");
+constexpr int SMEM_BYTES = PLAN_OFF + (3 * MAX_REQ + 4) * 4 + MAX_ROWS * 6 + 1024;
+static_assert(PREP == NQ, "a thread per column");
+static_assert(P_OFF % 1024 == 0 && Q_OFF % 1024 == 0 && 2 * NQ * 128 <= K_TILE, "swizzle atoms");
 
-// TMEM columns
-constexpr int S_COL = 0, O_COL = 256, SF_ONE = 384, SF_Q = 388;
-// Instruction descriptors, M = 128; N, and the scale-byte selectors, are or-ed in.
-// kind::mxf8f6f4: e4m3 x e4m3, E8M0 scales, both K-major.
-constexpr uint32_t S_IDESC = (1u << 23) | ((uint32_t)(TT >> 4) << 24);
-// kind::f16: f16 x f16, f32 accumulators, both MN-major.
-constexpr uint32_t O_IDESC = (1u << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(TT >> 4) << 24);
+// TMEM columns: scores by slot, O by stream, scales
+// (ones for even and odd tiles, the queries' twice for each)
+constexpr int S_COL = 0, O_COL = 256, SF_ONE = 384, SF_Q = 392, SF_P = 408;
+static_assert(SF_P + 4 * SLOTS <= 512, "TMEM");
+// Instruction descriptor: kind::mxf8f6f4, e4m3 x e4m3, E8M0 scales, M = 128; N, and the scale-byte
+// selectors, are or-ed in.  The first product's operands are K-major, the second's MN-major.
+constexpr uint32_t IDESC = (1u << 23) | ((uint32_t)(TT >> 4) << 24);
+constexpr uint32_t TRANS = (1u << 15) | (1u << 16);
 
 struct Args {
   CUtensorMap codes, scales;  // the cache as [pages][tokens][bytes], boxes of box tokens
@@ -94,25 +92,16 @@ __device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// Matrix descriptor as desc_sw128, MN-major with `lbo` bytes between 128-byte runs along MN.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
-  return (desc_sw128(saddr) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(lbo >> 4) << 16);
-}
-__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred q;\n setp.ne.b32 q, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-template <int REGS>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-template <int REGS>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+// Four values, as two pairs of f16, as a word of e4m3 codes and one of the codes of what is left.
+__device__ __forceinline__ void hilo_x4(const float* v, uint32_t& hi, uint32_t& lo) {
+  asm("{\n .reg .b16 h0, h1, l0, l1;\n .reg .b32 f0, f1;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 h0, %2;\n cvt.rn.satfinite.e4m3x2.f16x2 h1, %3;\n"
+      " cvt.rn.f16x2.e4m3x2 f0, h0;\n cvt.rn.f16x2.e4m3x2 f1, h1;\n"
+      " sub.rn.f16x2 f0, %2, f0;\n sub.rn.f16x2 f1, %3, f1;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 l0, f0;\n cvt.rn.satfinite.e4m3x2.f16x2 l1, f1;\n"
+      " mov.b32 %0, {h0, h1};\n mov.b32 %1, {l0, l1};\n}"
+      : "=r"(hi), "=r"(lo)
+      : "r"(f16x2_of(v[0], v[1])), "r"(f16x2_of(v[2], v[3])));
 }
 template <int N>
 __device__ __forceinline__ void bar_sync(int id) {
@@ -147,22 +136,23 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status
 }
 // How an item's columns are dealt out (see the head of the file).
 struct Deal {
-  int nqp, streams, bufs;  // columns; streams of softmax groups; score buffers
-  __device__ explicit Deal(int cols) : nqp(cols), streams(cols <= 16 ? 4 : cols <= 48 ? 2 : 1) {
-    bufs = streams == 4 ? 4 : 2;
-  }
-  __device__ bool merged() const { return nqp <= MERGE; }
-  __device__ uint32_t s_col(int it) const { return S_COL + (256 / bufs) * (it & (bufs - 1)); }
-  __device__ int flat(int stream) const { return streams == 4 ? 16 * stream : 48 * stream; }
-  __device__ int slot(int it) const { return it & (bufs - 1); }
-  // parity of buffer slot(i)'s phase of an item's tile i, and the phases that an item of n tiles
+  int nqp, lg, streams, bufs;  // columns; 2^lg streams of softmax groups; slots of scores, weights
+  __device__ explicit Deal(int cols)
+      : nqp(cols), lg(cols <= 16 ? 2 : cols <= 32 ? 1 : 0), streams(1 << lg), bufs(2 << lg) {}
+  __device__ int slot(int i) const { return i & (bufs - 1); }
+  __device__ int stream(int i) const { return i & (streams - 1); }
+  __device__ uint32_t s_col(int i) const { return S_COL + (slot(i) << (7 - lg)); }
+  __device__ uint32_t o_col(int stream) const { return O_COL + 2 * nqp * stream; }
+  // where tile i's weights begin: their buffer, and the stream's place in its 128-byte rows
+  __device__ int p_buf(int i) const { return slot(i) >= streams ? K_TILE : 0; }
+  __device__ int p_byte(int stream) const { return 2 * nqp * stream; }
+  __device__ int q_byte(int item) const { return nqp <= Q_TWICE ? (item & 1) * (K_TILE / 2) : 0; }
+  // parity of slot(i)'s phase of an item's tile i, and the phases that an item of n tiles
   // leaves (ph: the slots' parities at its start, a bit each)
-  __device__ uint32_t parity(uint32_t ph, int i) const { return ((ph >> slot(i)) ^ (i / bufs)) & 1; }
+  __device__ uint32_t parity(uint32_t ph, int i) const { return ((ph >> slot(i)) ^ (i >> (lg + 1))) & 1; }
   __device__ void advance(uint32_t& ph, int n) const {
-    for (int b = 0; b < bufs; ++b) ph ^= (uint32_t)((n + bufs - 1 - b) / bufs & 1) << b;
+    for (int b = 0; b < bufs; ++b) ph ^= (uint32_t)((n + bufs - 1 - b) >> (lg + 1) & 1) << b;
   }
-  // where stream k's weights lie in the rows of the weights' buffer
-  __device__ int p_off(int stream) const { return streams == 4 ? 32 * stream : K_TILE * stream; }
 };
 
 // A maximum over the warp, every lane gets it (floats as ordered integers).
@@ -173,15 +163,23 @@ __device__ __forceinline__ float warp_max_any(float v) {
   return __int_as_float(i < 0 ? i ^ 0x7FFFFFFF : i);
 }
 
+// What the softmax needs of an item beside its span, made with the item's queries.
+struct Meta {
+  int cols, nrows;
+  int row[GROUP], pos[GROUP];
+  long long query[NQ], out[NQ];  // where a column's queries are, and where its first value goes
+  int slice[NQ];                 // -1: padding
+};
 struct Shared {
-  uint64_t full[ST], k_free[ST], s_full[4], p_full[4], pv_done[4], v_full[2], v_free[2], q_full, drain;
-  float neg_m[NQ], fac[NQ], red[SOFT_WARPS][CMAX];  // m and its change: [stream][column]
-  uint32_t valid[ST][4], mask[ST];  // tokens that are there; whether some row masks some token
-  long long out[NQ];  // where a column's first value goes: o or the workspace
-  float fin[NQ][4];   // a column's factor for each stream's O
-  int slice[NQ], group_row[GROUP], group_pos[GROUP];
+  uint64_t full[ST], k_free[ST], s_full[SLOTS], p_full[SLOTS], pv_done[SLOTS];
+  uint64_t q_full[2], q_free[2], o_free, drain;
+  float neg_m[NQ], fac[NQ], red[SOFT_WARPS][C];  // m and its change: [stream][column]
+  uint32_t most[SOFT_WARPS][C];  // the warp's columns' largest weights
+  uint32_t valid[ST][4];  // tokens that are there
+  float fin[4][NQ];   // a column's factor for each stream's O
+  Meta meta[2];
   uint32_t tmem;
-  int cols, nrows, abort;
+  int abort;
   Jobs start;
 };
 static_assert(SMEM_BYTES + sizeof(Shared) <= 227 * 1024, "shared memory");
@@ -190,50 +188,41 @@ static_assert(SMEM_BYTES + sizeof(Shared) <= 227 * 1024, "shared memory");
 struct Soft {
   Span span;
   int t0, n, it;      // the item's first tile and tile count, the ring's next tile
-  int c0, col, flat;  // this group's first column; of its stream's set: in TMEM and in m
+  int clear, clears;  // tiles [clear, clear + clears) of the item are every row's to see
+  int c0, flat;       // this group's first column, of all and of all streams' m
   int first, stride;  // the group's tiles
-  int nrows, cheads;  // the item's rows and the heads (columns) of each
-  int min_hi, max_lo; // tokens that every row sees: [max_lo, min_hi] and the sinks
+  int arrive;         // arrivals of each warp at a tile's weights (SOFT_WARPS from all of them)
+  int cheads;         // columns of a row
   float to_log2;
   uint32_t tmem;      // with the warp's lane quadrant
-  uint32_t p_row;     // the thread's row of its stream's weights, and their first 16-byte piece
-  uint32_t p_chunk;
-  uint32_t ph;        // the buffers' barriers' phases at the item's start
+  uint32_t ph;        // the slots' barriers' phases at the item's start
 };
 
-// The softmax of a group's C columns over its tiles of an item, a token per thread; leaves the
-// thread's share of every column's sum, in units of 2^m, in the scratch.
-template <int C>
+// The softmax of a group's columns over its tiles of an item, a token per thread; leaves the
+// thread's share of every column's sum, in units of 2^m.
 __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, const Deal& deal,
-                                           Shared& sh, uint8_t* sm) {
+                                           const Meta& meta, Shared& sh, uint8_t* sm, float (&l)[C]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, group = warp >> 2, tok = 32 * quad + lane;
-  const bool merged = deal.merged();
   volatile int* abort = &sh.abort;
-  float l[C], s[C];
-#pragma unroll
-  for (int c = 0; c < C; ++c) l[c] = 0.0f;
+  float s[C];
 #pragma unroll 1
   for (int i = w.first; i < w.n; i += w.stride) {
     const int it = w.it + i, st = it % ST, b = deal.slot(i);
-    const int t0 = w.span.token(w.t0 + i), t = t0 + tok;
-    wait(&sh.full[st], (it / ST) & 1, a.status, abort);
+    wait(&sh.s_full[b], deal.parity(w.ph, i), a.status, abort);  // (so the tile is there)
     const float raw = reinterpret_cast<const float*>(sm + SC_OFF)[(st * TT + tok) * 4];
     const uint32_t ok = sh.valid[st][quad];
     const bool fin = fabsf(raw) <= 3.0e38f;
     const float ct = fin ? raw * w.to_log2 : __int_as_float(0x7FC00000);
-    const float sc = fin ? raw : 0.0f;
-    const float lsc = sc > 0.0f ? fmaxf(log2_of(sc), LEAST) : LEAST;
-    __syncwarp();
-    if (lane < w.stride) mbar_arrive(&sh.k_free[st]);  // (as many arrivals whoever takes the tile)
-    // some of the tile's tokens are not every row's to see
-    const bool part = ok != 0xffffffffu || t0 + TT - 1 > w.min_hi ||
-                      (t0 < w.max_lo && t0 + TT > a.sinks);
+    const float sc = fin ? raw : 0.0f, size = fabsf(sc), up = 64.0f * sc;
+    // some of the tile's tokens may not be every row's to see
+    const bool part = ok != 0xffffffffu || (uint32_t)(i - w.clear) >= (uint32_t)w.clears;
     uint32_t see = 0xffffffffu;
     if (__builtin_expect(part, 0)) {  // the group's columns that see the token
+      const int t = w.span.token(w.t0 + i) + tok;
 #pragma unroll 1
-      for (int j = 0; j < w.nrows; ++j) {
-        const int hi = a.causal ? sh.group_pos[j] : w.span.hi;
+      for (int j = 0; j < meta.nrows; ++j) {
+        const int hi = a.causal ? meta.pos[j] : w.span.hi;
         const int lo = a.window > 0 ? max(0, hi - a.window + 1) : 0;
         if (((ok >> lane) & 1) && t <= hi && (t >= lo || t < a.sinks)) continue;
         // columns [c, c + cheads) of the item, from this group's first on
@@ -242,32 +231,90 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
         see &= ~((1u << y) - (1u << x));
       }
     }
-    wait(&sh.s_full[b], deal.parity(w.ph, i), a.status, abort);
-    const uint32_t scol = w.tmem + deal.s_col(i) + w.c0;
-    // weights; a second round where some query's m has to move (always in an item's first tile)
+    if (__builtin_expect(part && w.c0 == 0, 0)) {
+      // NaN codes that some row must not see would reach it as 0 * NaN (rows that do see the token
+      // are NaN by their scores); the first product has read the tile
+      uint8_t* k = sm + K_OFF + st * K_TILE + tok * 128;
 #pragma unroll 1
-    for (bool moved = false;; moved = true) {
+      for (int e = 0; e < 8; ++e) {
+        uint4* at = reinterpret_cast<uint4*>(k + (((e + lane) & 7) << 4));
+        *at = without_nan(*at);
+      }
+    }
+    const uint32_t scol = w.tmem + deal.s_col(i) + w.c0;
+    uint32_t mb[C];
+    // weights; m moves ahead of an item's first tile, and where a weight asks for it
+    bool move = i == w.first, moved = false;
+#pragma unroll 1
+    for (;;) {
       tc_fence_after();
-#pragma unroll
-      for (int g = 0; g < C; g += 8) tc_ld8(scol + g, s + g);
-      if (merged) {
-#pragma unroll
+      if (__builtin_expect(move, 0)) {
+        // the columns' largest weights times scales of the tile
+        const float lsc = sc != 0.0f ? fmaxf(log2_of(size), LEAST) : LEAST;
+#pragma unroll 1
         for (int g = 0; g < C; g += 8) {
-          float x[8];
-          tc_ld8(scol + deal.nqp + g, x);
+          float x[8], y[8], mine = 0.0f;
+          tc_ld8(scol + g, x);
+          tc_ld8(scol + deal.nqp + g, y);
           tc_wait_ld();
           tc_loaded(x);
-          tc_loaded(s + g);
+          tc_loaded(y);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s[g + e] += x[e];
+          for (int e = 0; e < 8; ++e) {
+            float v = fmaf(x[e] + y[e], ct, lsc);
+            if (!(v > -INFINITY) || !((see >> (g + e)) & 1)) v = -INFINITY;
+            const float m = warp_max_any(v);
+            if (lane == e) mine = m;
+          }
+          if (lane < 8) sh.red[warp][g + lane] = mine;
         }
-      } else {
-        tc_wait_ld();
+        bar_sync<128>(6 + group);
+        if (quad == 0 && lane < C) {
+          const float(*r)[C] = sh.red + 4 * group;
+          const float m = fmaxf(fmaxf(r[0][lane], r[1][lane]), fmaxf(r[2][lane], r[3][lane]));
+          const float old = -sh.neg_m[w.flat + lane];
+          float f = 1.0f;
+          if (m - old > BASE) {
+            const float now = fminf(ceilf(m) - BASE, 3.0e38f);
+            f = old == UNSET ? 0.0f : ex2(old - now);
+            sh.neg_m[w.flat + lane] = -now;
+          }
+          sh.fac[w.flat + lane] = f;
+        }
+        bar_sync<128>(6 + group);
+        if (i >= w.stride) {
 #pragma unroll
-        for (int g = 0; g < C; g += 8) tc_loaded(s + g);
+          for (int c = 0; c < C; ++c) l[c] *= sh.fac[w.flat + c];
+          const int pi = i - w.stride;  // the group's tile before: its product is in O
+          wait(&sh.pv_done[deal.slot(pi)], deal.parity(w.ph, pi), a.status, abort);
+          tc_fence_after();
+#pragma unroll 1
+          for (int g = 0; g < 2 * C; g += 8) {  // both terms'
+            float x[8];
+            const uint32_t oc = w.tmem + deal.o_col(w.first) + w.c0 + (g & C ? deal.nqp : 0) + (g & (C - 1));
+            tc_ld8(oc, x);
+            tc_wait_ld();
+            tc_loaded(x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= sh.fac[w.flat + (g & (C - 1)) + e];
+            tc_st8(oc, x);
+          }
+          tc_wait_st();
+        }
+        moved = true;
+      }
+#pragma unroll
+      for (int g = 0; g < C; g += 8) {
+        float x[8];
+        tc_ld8(scol + g, s + g);
+        tc_ld8(scol + deal.nqp + g, x);
+        tc_wait_ld();
+        tc_loaded(x);
+        tc_loaded(s + g);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) add2(s[g + e], s[g + e + 1], x[e], x[e + 1]);
       }
       const float4* nm = reinterpret_cast<const float4*>(sh.neg_m + w.flat);
-      float top = -INFINITY;
 #pragma unroll
       for (int c = 0; c < C; c += 4) {
         const float4 m = nm[c / 4];
@@ -279,94 +326,56 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
         for (int c = 0; c < C; ++c)
           if (!((see >> c) & 1)) s[c] = -INFINITY;
       }
+      // the largest weights times scales of the warp's tokens, as bits; 2 and more (or NaN) asks
+      // for a larger m
+      uint32_t any = 0;
 #pragma unroll
-      for (int c = 0; c < C; ++c) top = fmaxf(top, s[c]);
-      if (__builtin_expect(!bar_any(2 + group, !moved && top + lsc > TOP), 1)) break;
-      // the columns' largest weights times scales of the tile
-#pragma unroll 1
-      for (int g = 0; g < C; g += 8) {
-        float x[8], y[8], mine = 0.0f;
-        tc_ld8(scol + g, x);
-        if (merged) tc_ld8(scol + deal.nqp + g, y);
-        tc_wait_ld();
-        tc_loaded(x);
-        if (merged) tc_loaded(y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float v = fmaf(merged ? x[e] + y[e] : x[e], ct, lsc);
-          if (!(v > -INFINITY) || !((see >> (g + e)) & 1)) v = -INFINITY;
-          const float m = warp_max_any(v);
-          if (lane == e) mine = m;
-        }
-        if (lane < 8) sh.red[warp][g + lane] = mine;
+      for (int c = 0; c < C; ++c) {
+        s[c] = ex2(s[c]);
+        mb[c] = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaf(s[c], size, 0x1p-118f)));
+        any |= mb[c];
       }
-      bar_sync<128>(6 + group);
-      if (quad == 0 && lane < C) {
-        const float(*r)[CMAX] = sh.red + 4 * group;
-        const float m = fmaxf(fmaxf(r[0][lane], r[1][lane]), fmaxf(r[2][lane], r[3][lane]));
-        const float old = -sh.neg_m[w.flat + lane];
-        float f = 1.0f;
-        if (m - old > BASE) {
-          const float now = fminf(ceilf(m) - BASE, 3.0e38f);
-          f = old == UNSET ? 0.0f : ex2(old - now);
-          sh.neg_m[w.flat + lane] = -now;
-        }
-        sh.fac[w.flat + lane] = f;
-      }
-      bar_sync<128>(6 + group);
-#pragma unroll
-      for (int c = 0; c < C; ++c) l[c] *= sh.fac[w.flat + c];
-      if (i >= w.stride) {
-        const int pi = i - w.stride;  // the group's tile before: its product is in O
-        wait(&sh.pv_done[deal.slot(pi)], deal.parity(w.ph, pi), a.status, abort);
-        tc_fence_after();
-#pragma unroll 1
-        for (int g = 0; g < C; g += 8) {
-          float x[8];
-          const uint32_t oc = w.tmem + O_COL + w.col + g;
-          tc_ld8(oc, x);
-          tc_wait_ld();
-          tc_loaded(x);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] *= sh.fac[w.flat + g + e];
-          tc_st8(oc, x);
-        }
-        tc_wait_st();
-      }
+      if (moved) break;  // (alike in the group's warps)
+      move = bar_any(2 + group, any >> 30);
+      if (__builtin_expect(!move, 1)) break;
     }
-    // weights times scales, rows of 128 bytes per token; the buffer's last reader has finished
-    if (i >= w.stride) {
-      const int pi = i - w.stride;
-      wait(&sh.pv_done[deal.slot(pi)], deal.parity(w.ph, pi), a.status, abort);
-    }
+    // weights times scales as two e4m3 terms, 16 + 16 bytes of the token's row; a column's largest
+    // of the warp's tokens is in [2^7, 2^8)
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int g = 0; g < C; g += 8) {
-      uint32_t o[4];
+    for (int g = 0; g < C; g += 4) {
+      float y[4];
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        float p0 = ex2(s[g + e]), p1 = ex2(s[g + e + 1]);
-        add2(l[g + e], l[g + e + 1], p0, p1);
-        mul2(p0, p1, sc);
-        o[e / 2] = f16x2_of(p0, p1);
+      for (int e = 0; e < 4; e += 2) {
+        const int c = g + e;
+        y[e] = __uint_as_float(~mb[c] & 0x7F800000u);  // 2 / the largest's power of two
+        y[e + 1] = __uint_as_float(~mb[c + 1] & 0x7F800000u);
+        mul2(y[e], y[e + 1], up);
+        mul2(y[e], y[e + 1], s[c], s[c + 1]);
+        add2(l[c], l[c + 1], s[c], s[c + 1]);
       }
-      const int col = w.c0 + g;
-      *reinterpret_cast<uint4*>(sm + w.p_row + (col >> 6) * K_TILE +
-                                (((w.p_chunk + ((col & 63) >> 3)) ^ (tok & 7)) << 4)) =
-          make_uint4(o[0], o[1], o[2], o[3]);
+      hilo_x4(y, hi[g / 4], lo[g / 4]);
+    }
+    if (lane == 0) {
+#pragma unroll
+      for (int g = 0; g < C; g += 4)
+        *reinterpret_cast<uint4*>(&sh.most[warp][g]) = make_uint4(mb[g], mb[g + 1], mb[g + 2], mb[g + 3]);
+    }
+    uint8_t* prow = sm + P_OFF + deal.p_buf(i) + tok * 128;
+    const int ch = (deal.p_byte(w.first) + w.c0) >> 4, cl = ch + (deal.nqp >> 4);
+    *reinterpret_cast<uint4*>(prow + ((ch ^ (tok & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(prow + ((cl ^ (tok & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    __syncwarp();
+    {
+      const int n = w.c0 + (lane & 15) + (lane >> 4) * deal.nqp;
+      sm[PIMG_OFF + b * IMG + (n & 31) * 16 + (n >> 5) * 4 + quad] =
+          (uint8_t)((sh.most[warp][lane & 15] >> 23) - 7);
     }
     fence_proxy_async_shared();
     tc_fence_before();
     __syncwarp();
-    if (lane < w.stride) mbar_arrive(&sh.p_full[b]);
+    if (lane < w.arrive) mbar_arrive(&sh.p_full[b]);
   }
-  // every product of the item is done: the weights' and the queries' buffers are scratch
-#pragma unroll 1
-  for (int i = max(0, w.n - deal.bufs); i < w.n; ++i)
-    wait(&sh.pv_done[deal.slot(i)], deal.parity(w.ph, i), a.status, abort);
-  tc_fence_after();
-  float* scratch = reinterpret_cast<float*>(sm + P_OFF) + warp * CMAX * 32 + lane;
-#pragma unroll
-  for (int c = 0; c < C; ++c) scratch[32 * c] = l[c];
 }
 
 __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constant__ Args ar) {
@@ -380,25 +389,32 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   plan.pre = reinterpret_cast<int*>(sm + PLAN_OFF);
   plan.pmax = plan.pre + MAX_REQ + 4;
   plan.pmin = plan.pmax + MAX_REQ;
+  plan.pos = plan.pmin + MAX_REQ;
+  plan.req = reinterpret_cast<short*>(plan.pos + MAX_ROWS);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Shape& sh = ar.sh;
   const int team = blockIdx.x / sh.chunks, chunk = blockIdx.x - team * sh.chunks;
   const int chunk_bytes = min(128, a.kv_dim - 128 * chunk);
 
   if (tid == 0) {
-    // a tile is free when the first product, the widening and the softmax warps have read it
-    for (int s = 0; s < ST; ++s)
-      mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], 1 + WIDE_WARPS + SOFT_WARPS);
-    for (int s = 0; s < 4; ++s)
+    // (a tile is free when its second product is done)
+    for (int s = 0; s < ST; ++s) mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], 1);
+    for (int s = 0; s < SLOTS; ++s)
       mbar_init(&ss.s_full[s], 1), mbar_init(&ss.pv_done[s], 1), mbar_init(&ss.p_full[s], SOFT_WARPS);
-    for (int s = 0; s < 2; ++s) mbar_init(&ss.v_full[s], WIDE_WARPS), mbar_init(&ss.v_free[s], 1);
-    mbar_init(&ss.q_full, SOFT_WARPS);
-    mbar_init(&ss.drain, 2);
+    // an item's queries are free when all that read them or wait for them are done
+    for (int s = 0; s < 2; ++s)
+      mbar_init(&ss.q_full[s], PREP / 32), mbar_init(&ss.q_free[s], 2 * MMA_WARPS + SOFT_WARPS);
+    mbar_init(&ss.o_free, SOFT_WARPS);
+    mbar_init(&ss.drain, 2 * MMA_WARPS);
     ss.abort = 0;
     fence_mbar_init();
   }
   if (warp == S_WARP) tmem_alloc<512>(&ss.tmem);
-  if (tid < 2 * IMG / 4) reinterpret_cast<uint32_t*>(sm + QIMG_OFF)[tid] = 0x7F7F7F7Fu;
+  for (int i = tid; i < (SLOTS + 3) * IMG / 4; i += THREADS)
+    reinterpret_cast<uint32_t*>(sm + PIMG_OFF)[i] = 0x7F7F7F7Fu;
+  if (!ar.box && chunk_bytes < 128)  // (the bytes that nothing else writes)
+    for (int i = tid; i < ST * K_TILE / 16; i += THREADS)
+      *reinterpret_cast<uint4*>(sm + K_OFF + 16 * i) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_shared();
 
   derive_plan<THREADS>(a, sh, plan, team, team < sh.teams, &ss.start, ar.total);
@@ -411,7 +427,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 
   if (warp >= LOAD_WARP) {
     // ------------------------------------------------------- loads: a warp takes every other tile
-    regs_down<OTHER_REGS>();
     int ni = warp - LOAD_WARP;
     bool more = next_job(a, sh, plan, items, im);
     // a lane per box of the next tile (of a token each without maps, four times): its page, on its
@@ -442,12 +457,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       if (row[q] >= 0 && !m) atomicOr(a.status, ST_UNMAPPED_PAGE);
       return m;
     };
-    auto masks = [&](uint32_t there) {  // for some row of the request
-      const int first = a.causal ? plan.pmin[im.b] : im.span.hi;
-      const int last_lo = a.window > 0 ? max(0, im.span.hi - a.window + 1) : 0;
-      return (uint32_t)(there != 0xffffffffu || t0 + TT - 1 > first ||
-                        (t0 < last_lo && t0 + TT > a.sinks));
-    };
     locate();
 #pragma unroll 1
     for (int it = warp - LOAD_WARP; more; it += LOAD_WARPS) {
@@ -456,11 +465,14 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       if (it >= ST) go = wait(&ss.k_free[s], ((it / ST) - 1) & 1, a.status, abort);
       uint8_t* st = sm + K_OFF + s * K_TILE;
       uint8_t* sc = sm + SC_OFF + s * TT * 16;
-      uint32_t there = 0xffffffffu;
       if (ar.box) {
         // boxes with a token to see; their other tokens, and what the rest of the slot holds, are
         // masked
         const bool m = mapped(0);
+        if (m && go) {
+          tma_load_3d(st + ((lane * 128) << shift), &ar.codes, 128 * chunk, row[0], page[0], &ss.full[s]);
+          tma_load_3d(sc + ((lane * 16) << shift), &ar.scales, a.kv_dim, row[0], page[0], &ss.full[s]);
+        }
         const uint32_t have = __ballot_sync(0xffffffffu, m);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -469,16 +481,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                            (t >= im.span.lo || t < a.sinks);
           const uint32_t w = __ballot_sync(0xffffffffu, see);
           if (lane == q) ss.valid[s][q] = w;
-          there &= w;
         }
-        if (lane == 0) ss.mask[s] = masks(there);
         __syncwarp();
+        // (bytes that land before they are expected wait for this arrival all the same)
         if (lane == 0) mbar_arrive_expect_tx(&ss.full[s], go ? __popc(have) * box * (128 + 16) : 0);
         __syncwarp();
-        if (m && go) {
-          tma_load_3d(st + ((lane * 128) << shift), &ar.codes, 128 * chunk, row[0], page[0], &ss.full[s]);
-          tma_load_3d(sc + ((lane * 16) << shift), &ar.scales, a.kv_dim, row[0], page[0], &ss.full[s]);
-        }
       } else {
         const int piece = lane & 7;
         const bool in_chunk = go && 16 * piece < chunk_bytes;
@@ -491,7 +498,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           const long long off = m ? pg * a.kv.stride_block + rw * a.kv.stride_tok : 0;
           const uint32_t w = __ballot_sync(0xffffffffu, m);
           if (lane == 0) ss.valid[s][q] = w;
-          there &= w;
 #pragma unroll 1
           for (int e = 0; e < 8; ++e) {
             const int k = 4 * e + (lane >> 3), r = 32 * q + k;
@@ -502,7 +508,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           }
           if (go && m) cp_async16(sc + (32 * q + lane) * 16, a.kv.base + off + a.kv_dim, 16);
         }
-        if (lane == 0) ss.mask[s] = masks(there);
         cp_async_wait_all();
         fence_proxy_async_shared();
         __syncwarp();
@@ -511,96 +516,137 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       ni += LOAD_WARPS;
       locate();
     }
-  } else if (warp >= WIDE_WARP && warp < WIDE_WARP + WIDE_WARPS) {
-    // ------------------------------------------------------------ widening: 32 tokens of every tile
-    regs_down<OTHER_REGS>();
-    const int lw = warp - WIDE_WARP, piece = lane & 7, r4 = lane >> 3;
-    const int total = items.left;
+  } else if (warp >= PREP_WARP && warp < PREP_WARP + PREP / 32) {
+    // -------------------------------------------------------- the items' rows and queries
+    const int hpg = a.n_q / (a.kv_dim / a.head_dim);
+    const int cheads = hpg * (chunk_bytes > a.head_dim ? 2 : 1);  // heads per row of this chunk
+    const int dshift = a.head_dim == 64 ? 6 : 7, ptid = tid - 32 * PREP_WARP;
+    bool before = false;  // the item before had more than Q_TWICE columns
 #pragma unroll 1
-    for (int it = 0; it < total; ++it) {
-      const int s = it % ST, b = it & 1;
-      wait(&ss.full[s], (it / ST) & 1, a.status, abort);
-      if (it >= 2) wait(&ss.v_free[b], ((it >> 1) - 1) & 1, a.status, abort);
-      const bool mask = ss.mask[s] != 0;
-      const uint8_t* src = sm + K_OFF + s * K_TILE + 32 * lw * 128;
-      uint8_t* dst = sm + V_OFF + b * V_TILE + (piece >> 2) * K_TILE + 32 * lw * 128;
+    for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
+      const int qb = item & 1;
+      if (item >= 2) wait(&ss.q_free[qb], ((item >> 1) - 1) & 1, a.status, abort);
+      Meta& meta = ss.meta[qb];
+      if (warp == PREP_WARP) {
+        const int n = group_rows(a, sh, plan, im.b, im.group, meta.row, meta.pos);
+        if (lane == 0) meta.cols = (n * cheads + 15) & ~15, meta.nrows = n;
+      }
+      bar_sync<PREP>(1);
+      const int nqp = meta.cols, nq = meta.nrows * cheads;
+      {  // a column per thread: its head of the chunk, and where its queries and its results are
+        const bool whole = im.n == im.span.tiles;  // nobody else has tiles of this group
+        const int slot = (team * 2 + (im.t0 > 0 ? 0 : 1)) * sh.chunks + chunk;
+        const int j = ptid / cheads, h = ptid - j * cheads;
+        const int at = (chunk * sh.heads + h) * a.head_dim, r = ptid < nq ? meta.row[j] : 0;
+        meta.slice[ptid] = ptid < nq ? (h >= hpg ? 1 : 0) : -1;
+        meta.query[ptid] = r * a.q_stride + at;
+        meta.out[ptid] = whole ? r * a.o_stride + at : (long long)(slot * NQ + ptid) * PART_LD + 4;
+      }
+      const bool once = nqp > Q_TWICE;  // (the one buffer that both halves are)
+      if (item > 0 && (once || before)) wait(&ss.q_free[qb ^ 1], ((item - 1) >> 1) & 1, a.status, abort);
+      before = once;
+      bar_sync<PREP>(1);
+      // queries as two e4m3 terms, rows of 128 bytes: hi in row c, lo in row nqp + c; a thread
+      // takes 8 dimensions, the next ones on their way meanwhile
+      const int d = (ptid & 15) * 8, sl = d >> dshift, o = d >> 4;
+      const __nv_bfloat16* q = a.q + (d - (sl << dshift));
+      auto fetch = [&](int c) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (c < nq && meta.slice[c] == sl) x = __ldg(reinterpret_cast<const uint4*>(q + meta.query[c]));
+        return x;
+      };
+      uint4 next = fetch(ptid >> 4);
+      uint8_t* to = sm + Q_OFF + (once ? 0 : qb * (K_TILE / 2)) + (d & 8);
+      uint8_t* img = sm + QIMG_OFF + qb * IMG + (d >> 5);
+#pragma unroll 1
+      for (int c = ptid >> 4; c < nqp; c += PREP / 16) {
+        float v[8];
+        bf16x8_to_f32(next, v);
+        next = fetch(c + PREP / 16);
+        float m = 0.0f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint4 v[4];
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        if (__builtin_expect(isinf(m), 0)) {  // (the codes have no infinity)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = 16 * h + 4 * e + r4;
-          v[e] = lds128(src + row * 128 + ((piece ^ (row & 7)) << 4));
+          for (int e = 0; e < 8; ++e)
+            if (isinf(v[e])) v[e] = __int_as_float(0x7FC00000);
         }
+        const uint32_t code = e4m3_block_code(m);
+        const float inv = e8m0_inverse(code);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // a NaN code that some row must not see would reach it as 0 * NaN (rows that do see the
-          // token are NaN by their scores)
-          if (__builtin_expect(mask, 0)) v[e] = without_nan(v[e]);
-          const int row = 16 * h + 4 * e + r4, c = 2 * (piece & 3);
-          uint4 x, y;
-          uint32_t f[2];
-          e4m3x4_to_f16x4(v[e].x, f), x.x = f[0], x.y = f[1];
-          e4m3x4_to_f16x4(v[e].y, f), x.z = f[0], x.w = f[1];
-          e4m3x4_to_f16x4(v[e].z, f), y.x = f[0], y.y = f[1];
-          e4m3x4_to_f16x4(v[e].w, f), y.z = f[0], y.w = f[1];
-          *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = x;
-          *reinterpret_cast<uint4*>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) = y;
+        for (int e = 0; e < 8; e += 2) mul2(v[e], v[e + 1], inv);
+        uint32_t hw[2], lw[2];
+        hilo_x4(v, hw[0], lw[0]);
+        hilo_x4(v + 4, hw[1], lw[1]);
+        const int rl = nqp + c;
+        *reinterpret_cast<uint2*>(to + c * 128 + ((o ^ (c & 7)) << 4)) = make_uint2(hw[0], hw[1]);
+        *reinterpret_cast<uint2*>(to + rl * 128 + ((o ^ (rl & 7)) << 4)) = make_uint2(lw[0], lw[1]);
+        if ((d & 31) == 0) {
+          img[(c & 31) * 16 + (c >> 5) * 4] = (uint8_t)code;
+          img[(rl & 31) * 16 + (rl >> 5) * 4] = (uint8_t)code;
         }
       }
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ss.v_full[b]), mbar_arrive(&ss.k_free[s]);
+      if (lane == 0) mbar_arrive(&ss.q_full[qb]);
     }
-  } else if (warp == S_WARP) {
-    // ------------------------------------------------------------- the first product's MMAs
-    regs_down<OTHER_REGS>();
-    const uint32_t k0 = smem_u32(sm + K_OFF);
-    const uint64_t q0 = desc_sw128(smem_u32(sm + Q_OFF));
+  } else if (warp >= S_WARP && warp < S_WARP + MMA_WARPS) {
+    // ------------------------------- the first product's MMAs: a warp issues every other tile's
+    const int mine = warp - S_WARP;
+    const uint64_t k0 = desc_sw128(smem_u32(sm + K_OFF)), q0 = desc_sw128(smem_u32(sm + Q_OFF));
+    const uint32_t sf0 = tmem + SF_Q + 8 * mine, ones = tmem + SF_ONE + 4 * mine;
     int it = 0;
     uint32_t ph = 0;
-    if (elect_one()) tc_cp_img(tmem + SF_ONE, sm + ONE_OFF);
+    if (elect_one()) tc_cp_img(ones, sm + ONE_OFF);
     __syncwarp();
 #pragma unroll 1
     for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
-      wait(&ss.q_full, item & 1, a.status, abort);
-      const Deal deal(ss.cols);
-      const bool merged = deal.merged();
-      const uint32_t idesc = S_IDESC | ((uint32_t)((merged ? 2 * deal.nqp : deal.nqp) >> 3) << 17);
+      const int qb = item & 1;
+      wait(&ss.q_full[qb], (item >> 1) & 1, a.status, abort);
+      const Deal deal(ss.meta[qb].cols);
+      const uint32_t idesc = IDESC | ((uint32_t)(2 * deal.nqp >> 3) << 17);
+      const uint32_t sf = sf0 + 4 * qb;
+      const uint64_t qd = q0 + (deal.q_byte(item) >> 4);
+      if (elect_one()) tc_cp_img(sf, sm + QIMG_OFF + qb * IMG);
+      __syncwarp();
 #pragma unroll 1
-      for (int i = 0; i < im.n; ++i) {
+      for (int i = mine; i < im.n; i += MMA_WARPS) {
         const int st = (it + i) % ST, b = deal.slot(i);
         bool ok = wait(&ss.full[st], ((it + i) / ST) & 1, a.status, abort);
-        if (i >= deal.bufs) ok &= wait(&ss.p_full[b], deal.parity(ph, i - deal.bufs), a.status, abort);
+        // the slot's scores and weights are no longer in use
+        if (i >= deal.bufs)
+          ok &= wait(&ss.pv_done[b], deal.parity(ph, i - deal.bufs), a.status, abort);
         if (ok && elect_one()) {
           tc_fence_after();
-          if (i == 0) tc_cp_img(tmem + SF_Q, sm + QIMG_OFF);
-          const uint64_t kd = desc_sw128(k0 + st * K_TILE);
-#pragma unroll 1
-          for (int term = 0; term < (merged ? 1 : 2); ++term)
+          const uint64_t kd = k0 + st * (K_TILE / 16);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma_mxf8(tmem + deal.s_col(i), kd + 2 * k, q0 + term * (NQ * 128 / 16) + 2 * k,
-                          idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), tmem + SF_ONE,
-                          tmem + SF_Q, term > 0 || k > 0);
+          for (int k = 0; k < 4; ++k)
+            tc_mma_mxf8(tmem + deal.s_col(i), kd + 2 * k, qd + 2 * k,
+                        idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), ones, sf, k > 0);
           tc_commit(&ss.s_full[b]);
-          tc_commit(&ss.k_free[st]);
         }
         __syncwarp();
       }
+      if (elect_one()) tc_commit(&ss.q_free[qb]);
+#pragma unroll 1
+      for (int i = max(0, im.n - MMA_WARPS); i < im.n; ++i)  // all are done when each warp's last is
+        wait(&ss.pv_done[deal.slot(i)], deal.parity(ph, i), a.status, abort);
+      bar_sync<32 * MMA_WARPS>(11);  // (neither runs ahead of the phases that the other waits for)
       it += im.n;
       deal.advance(ph, im.n);
     }
     if (elect_one()) tc_commit(&ss.drain);  // (what was issued has completed at this arrival)
     __syncwarp();
-  } else if (warp == O_WARP) {
-    // ------------------------------------------------------------ the second product's MMAs
-    regs_down<OTHER_REGS>();
-    const uint64_t v0 = desc_mn(smem_u32(sm + V_OFF), K_TILE);
-    const uint64_t p0 = desc_mn(smem_u32(sm + P_OFF), K_TILE);
+  } else if (warp >= O_WARP && warp < O_WARP + MMA_WARPS) {
+    // ------------- the second product's MMAs: a warp issues every other tile's, so that it has its
+    // own streams' O; the first one all where there is one stream
+    const int mine = warp - O_WARP;
+    const uint64_t k0 = desc_sw128(smem_u32(sm + K_OFF)), p0 = desc_sw128(smem_u32(sm + P_OFF));
     // first, where the second kernel finds the rows' results
 #pragma unroll 1
-    for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    for (int r = blockIdx.x + mine * gridDim.x; r < a.rows; r += MMA_WARPS * gridDim.x) {
       const RowInfo info = row_info(a, sh, plan, r);
       if (lane == 0) ar.rows[r] = info;
     }
@@ -608,33 +654,42 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     uint32_t ph = 0;
 #pragma unroll 1
     for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
-      wait(&ss.q_full, item & 1, a.status, abort);
-      const Deal deal(ss.cols);
-      const uint32_t idesc = O_IDESC | ((uint32_t)(deal.nqp >> 3) << 17);
+      wait(&ss.q_full[item & 1], (item >> 1) & 1, a.status, abort);
+      const Deal deal(ss.meta[item & 1].cols);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ss.q_free[item & 1]);
+      const int step = deal.streams == 1 ? 1 : MMA_WARPS;
+      const int first = mine < step ? mine : im.n;
+      // (only where this warp has tiles: it may miss phases of other items)
+      if (item > 0 && first < im.n) wait(&ss.o_free, (item - 1) & 1, a.status, abort);
+      const uint32_t idesc = IDESC | TRANS | ((uint32_t)(2 * deal.nqp >> 3) << 17);
 #pragma unroll 1
-      for (int i = 0; i < im.n; ++i, ++it) {
-        const int b = deal.slot(i), v = it & 1, stream = i & (deal.streams - 1);
-        bool ok = wait(&ss.p_full[b], deal.parity(ph, i), a.status, abort);
-        ok &= wait(&ss.v_full[v], (it >> 1) & 1, a.status, abort);
+      for (int i = first; i < im.n; i += step) {
+        const int b = deal.slot(i), stream = deal.stream(i), st = (it + i) % ST;
+        const bool ok = wait(&ss.p_full[b], deal.parity(ph, i), a.status, abort);
         if (ok && elect_one()) {
           tc_fence_after();
-          const uint64_t pd = p0 + (deal.p_off(stream) >> 4);
+          const uint32_t sf = tmem + SF_P + 4 * b, ones = tmem + SF_ONE + 4 * (i & 1);
+          tc_cp_img(sf, sm + PIMG_OFF + b * IMG);
+          const uint64_t kd = k0 + st * (K_TILE / 16);
+          const uint64_t pd = p0 + ((deal.p_buf(i) + deal.p_byte(stream)) >> 4);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)  // 16 tokens each
-            tc_mma_f16(tmem + O_COL + deal.flat(stream), v0 + v * (V_TILE / 16) + k * (2048 / 16),
-                     pd + k * (2048 / 16), idesc, i >= deal.streams || k > 0);
+          for (int k = 0; k < 4; ++k)  // 32 tokens each
+            tc_mma_mxf8(tmem + deal.o_col(stream), kd + k * (4096 / 16), pd + k * (4096 / 16),
+                        idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), ones, sf,
+                        i >= deal.streams || k > 0);
           tc_commit(&ss.pv_done[b]);
-          tc_commit(&ss.v_free[v]);
+          tc_commit(&ss.k_free[st]);
         }
         __syncwarp();
       }
+      it += im.n;
       deal.advance(ph, im.n);
     }
     if (elect_one()) tc_commit(&ss.drain);
     __syncwarp();
   } else {
     // ---------------------------------------------------------------------------- softmax
-    regs_up<SOFT_REGS>();
     const int quad = warp & 3, group = warp >> 2;
     const int hpg = a.n_q / (a.kv_dim / a.head_dim);
     const int cheads = hpg * (chunk_bytes > a.head_dim ? 2 : 1);  // heads per row of this chunk
@@ -646,184 +701,124 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     w.to_log2 = a.scale * LOG2E;
     w.tmem = tmem + ((uint32_t)(32 * quad) << 16);
 #pragma unroll 1
-    while (next_job(a, sh, plan, items, im)) {
-      // ---- the group's rows and queries
-      bar_sync<SOFT>(1);  // the previous item's columns are no longer in use
-      if (warp == 0) {
-        const int n = group_rows(a, sh, im.b, im.group, ss.group_row, ss.group_pos);
-        const int cols = (n * cheads + 15) & ~15;
-        if (lane == 0) ss.cols = cols == 80 ? 96 : cols, ss.nrows = n;
-      }
-      bar_sync<SOFT>(1);
-      const int nrows = ss.nrows, nq = nrows * cheads;
-      const Deal deal(ss.cols);
-      const int nqp = deal.nqp;
-      const bool merged = deal.merged();
-      const bool whole = im.n == im.span.tiles;  // nobody else has tiles of this group
-      const long long slot = (long long)(team * 2 + (im.t0 > 0 ? 0 : 1)) * sh.chunks + chunk;
-      if (tid < NQ) {
-        ss.neg_m[tid] = -UNSET;
-        const int j = tid / cheads, h = tid - j * cheads, sl = h / hpg;
-        const long long head = (long long)chunk * sh.heads + h;
-        ss.slice[tid] = tid < nq ? sl : -1;
-        if (tid < nq)
-          ss.out[tid] = whole ? ss.group_row[j] * a.o_stride + head * a.head_dim
-                              : (slot * NQ + tid) * PART_LD + 4;
-      }
-      // queries as two e4m3 terms, rows of 128 bytes: hi in row c, lo in row nqp + c (merged)
-      // or NQ + c
-#pragma unroll 1
-      for (int i = tid; i < nqp * 16; i += SOFT) {  // first copied as they are, all at once
-        const int c = i >> 4, d = (i & 15) * 8;
-        const int j = c / cheads, h = c - j * cheads, sl = h / hpg;
-        const bool in = c < nq && (d >> dshift) == sl;
-        cp_async16(sm + P_OFF + i * 16,
-                   a.q + (in ? ss.group_row[j] * a.q_stride +
-                                   ((long long)chunk * sh.heads + h) * a.head_dim + (d - (sl << dshift))
-                             : 0),
-                   in ? 16 : 0);
-      }
-      cp_async_wait_all();
-      // (every lane takes part in the blocks' maxima)
-#pragma unroll 1
-      for (int i = tid; i < ((nqp * 16 + SOFT - 1) & ~(SOFT - 1)); i += SOFT) {
-        const bool live = i < nqp * 16;
-        const int c = live ? i >> 4 : 0, d = (i & 15) * 8;
-        float v[8];
-        bf16x8_to_f32(live ? lds128(sm + P_OFF + i * 16) : make_uint4(0, 0, 0, 0), v);
-        float m = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (isinf(v[e])) v[e] = __int_as_float(0x7FC00000);  // (the codes have no infinity)
-          m = fmaxf(m, fabsf(v[e]));
-        }
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const uint32_t code = e4m3_block_code(m);
-        const float inv = e8m0_inverse(code);
-        uint32_t hw[2] = {0, 0}, lw[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          uint32_t hb, lb;
-          e4m3_hilo(v[e] * inv, hb, lb);
-          hw[e >> 2] |= hb << (8 * (e & 3));
-          lw[e >> 2] |= lb << (8 * (e & 3));
-        }
-        const int rl = (merged ? nqp : NQ) + c;
-        const int o = (d >> 4), x = d & 8;
-        if (!live) continue;
-        *reinterpret_cast<uint2*>(sm + Q_OFF + c * 128 + ((o ^ (c & 7)) << 4) + x) =
-            make_uint2(hw[0], hw[1]);
-        *reinterpret_cast<uint2*>(sm + Q_OFF + rl * 128 + ((o ^ (rl & 7)) << 4) + x) =
-            make_uint2(lw[0], lw[1]);
-        if ((d & 31) == 0) {
-          sm[QIMG_OFF + (c & 31) * 16 + (c >> 5) * 4 + (d >> 5)] = (uint8_t)code;
-          if (merged) sm[QIMG_OFF + (rl & 31) * 16 + (rl >> 5) * 4 + (d >> 5)] = (uint8_t)code;
-        }
-      }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ss.q_full);
-      w.min_hi = 0x7FFFFFFF;
-      w.max_lo = 0;
-#pragma unroll 1
-      for (int j = 0; j < nrows; ++j) {
-        const int hi = a.causal ? ss.group_pos[j] : im.span.hi;
-        w.min_hi = min(w.min_hi, hi);
-        w.max_lo = max(w.max_lo, a.window > 0 ? max(0, hi - a.window + 1) : 0);
-      }
-      bar_sync<SOFT>(1);  // (the staged queries have been read: weights may take their place)
+    for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
+      wait(&ss.q_full[item & 1], (item >> 1) & 1, a.status, abort);
+      const Meta& meta = ss.meta[item & 1];
+      const Deal deal(meta.cols);
+      const int nqp = deal.nqp, nq = meta.nrows * cheads;
+      const bool whole = im.n == im.span.tiles;
       w.span = im.span;
       w.t0 = im.t0;
       w.n = im.n;
-      w.nrows = nrows;
-      const int stream = group & (deal.streams - 1), cols = nqp * deal.streams / GROUPS;
-      w.first = stream;
+      w.first = group & (deal.streams - 1);
       w.stride = deal.streams;
-      w.c0 = group / deal.streams * cols;
-      w.flat = deal.flat(stream) + w.c0;
-      w.col = w.flat;
-      w.p_row = P_OFF + (32 * quad + lane) * 128 + (deal.streams == 2 ? K_TILE * stream : 0);
-      w.p_chunk = deal.streams == 4 ? 2 * stream : 0;
-      if (cols == 16)
-        soft_tiles<16>(a, w, deal, ss, sm);
-      else
-        soft_tiles<24>(a, w, deal, ss, sm);
+      w.c0 = (group >> deal.lg) * C;
+      w.flat = nqp * w.first + w.c0;
+      w.arrive = deal.streams + (nqp == 48 && group == 0 ? 1 : 0);  // (the fourth group is idle)
+      {
+        // tiles whose tokens all rows see (those of the sinks, where there is a window, aside)
+        const int r = lane < meta.nrows ? lane : 0;
+        const int hi = a.causal ? meta.pos[r] : im.span.hi;
+        const int lo = __reduce_max_sync(0xffffffffu, a.window > 0 ? max(0, hi - a.window + 1) : 0);
+        const int end = (__reduce_min_sync(0xffffffffu, hi) + 1) / TT;  // of the tiles as tokens go
+        const int to = im.span.head - im.span.body - im.t0;  // from there to the item's
+        const int from = max((lo + TT - 1) / TT, im.span.body);
+        w.clear = lo == 0 ? -im.t0 : from + to;
+        w.clears = max(0, (lo == 0 ? end : end - from));
+      }
+      float l[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) l[c] = 0.0f;
+      if (w.c0 < nqp) {
+        if (quad == 0 && lane < C) ss.neg_m[w.flat + lane] = -UNSET;
+        bar_sync<128>(6 + group);
+        soft_tiles(a, w, deal, meta, ss, sm, l);
+      }
+      // every product of the item is done when each issuing warp's last is
+#pragma unroll 1
+      for (int i = max(0, w.n - MMA_WARPS); i < w.n; ++i)
+        wait(&ss.pv_done[deal.slot(i)], deal.parity(w.ph, i), a.status, abort);
+      tc_fence_after();
       w.it += im.n;
       deal.advance(w.ph, im.n);
 
       // ---- the item's result: the columns' sums over the tokens, then O
-      const float* scratch = reinterpret_cast<const float*>(sm + P_OFF);
-      __syncwarp();
-      if (lane < cols) {  // this warp's share of each
-        float v = 0.0f;
-#pragma unroll 4
-        for (int k = 0; k < 32; ++k) v += scratch[(warp * CMAX + lane) * 32 + ((k + lane) & 31)];
-        ss.red[warp][lane] = v;
+      // (halving: a lane ends with column lane % 16 of both half warps)
+#pragma unroll
+      for (int x = C / 2; x > 0; x >>= 1) {
+#pragma unroll
+        for (int c = 0; c < x; ++c) {
+          const bool up = lane & x;
+          const float give = up ? l[c] : l[c + x], keep = up ? l[c + x] : l[c];
+          l[c] = keep + __shfl_xor_sync(0xffffffffu, give, x);
+        }
       }
-      bar_sync<SOFT>(1);
+      l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
+      if (lane < C) ss.red[warp][lane] = l[0];
+      bar_sync<SOFT>(10);
       if (tid < nq) {
         // the streams' sums and O in the largest m (one stream: as they are)
         float m = UNSET, lt = 0.0f;
 #pragma unroll 1
-        for (int k = 0; k < min(deal.streams, im.n); ++k) m = fmaxf(m, -ss.neg_m[deal.flat(k) + tid]);
+        for (int k = 0; k < min(deal.streams, im.n); ++k) m = fmaxf(m, -ss.neg_m[nqp * k + tid]);
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
           float f = 0.0f;
           if (k < min(deal.streams, im.n)) {
-            const int g = k + tid / cols * deal.streams, c = tid % cols;
-            const float(*r)[CMAX] = ss.red + 4 * g;
-            const float mk = -ss.neg_m[deal.flat(k) + tid];
+            const int g = k + (tid / C << deal.lg), c = tid % C;
+            const float(*r)[C] = ss.red + 4 * g;
+            const float mk = -ss.neg_m[nqp * k + tid];
             const float lk = (r[0][c] + r[1][c]) + (r[2][c] + r[3][c]);
             f = lk != lk ? 1.0f : mk == UNSET ? 0.0f : ex2(mk - m);  // (a NaN stays one)
             if (f != 0.0f) lt = fmaf(lk, f, lt);
           }
-          ss.fin[tid][k] = f;
+          ss.fin[k][tid] = f;
         }
         const float up = !whole ? 1.0f : lt == 0.0f ? 0.0f : 1.0f / lt;
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) ss.fin[tid][k] *= up;
+        for (int k = 0; k < 4; ++k) ss.fin[k][tid] *= up;
         if (whole) {
           const int j = tid / cheads;
-          a.lse[(long long)ss.group_row[j] * a.n_q + chunk * sh.heads + tid - j * cheads] =
+          a.lse[(long long)meta.row[j] * a.n_q + chunk * sh.heads + tid - j * cheads] =
               lt == 0.0f ? -INFINITY : (log2f(lt) + m) * LN2;
         } else {
-          ar.part[ss.out[tid] - 4] = m;
-          ar.part[ss.out[tid] - 3] = lt;
+          ar.part[meta.out[tid] - 4] = m;
+          ar.part[meta.out[tid] - 3] = lt;
         }
       }
-      bar_sync<SOFT>(1);
+      bar_sync<SOFT>(10);
       const int d = 32 * quad + lane;  // this thread's dimension of the chunk
       const int sl = d >> dshift, dl = d - (sl << dshift);
 #pragma unroll 1
-      for (int c8 = 8 * group; c8 < nqp; c8 += 8 * GROUPS) {
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+      for (int c4 = 4 * group; c4 < nqp; c4 += 4 * GROUPS) {
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
         for (int k = 0; k < min(deal.streams, im.n); ++k) {
-          float x[8];
-          tc_ld8(w.tmem + O_COL + deal.flat(k) + c8, x);
+          float x[4], y[4];
+          tc_ld4(w.tmem + deal.o_col(k) + c4, x);
+          tc_ld4(w.tmem + deal.o_col(k) + nqp + c4, y);
           tc_wait_ld();
-          tc_loaded(x);
+          tc_loaded4(x);
+          tc_loaded4(y);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float f = ss.fin[c8 + e][k];
-            if (f != 0.0f) v[e] = fmaf(x[e], f, v[e]);
+          for (int e = 0; e < 4; ++e) {
+            const float f = ss.fin[k][c4 + e];
+            if (f != 0.0f) v[e] = fmaf(x[e] + y[e], f, v[e]);
           }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const long long at = ss.out[c8 + e] + dl;
-          const bool mine = ss.slice[c8 + e] == sl;
-          if (whole) {
-            if (mine) a.o[at] = __float2bfloat16_rn(v[e]);
-          } else {
-            if (mine) ar.part[at] = v[e];
-          }
+        for (int e = 0; e < 4; ++e) {
+          if (meta.slice[c4 + e] != sl) continue;
+          const long long at = meta.out[c4 + e] + dl;
+          if (whole)
+            a.o[at] = __float2bfloat16_rn(v[e]);
+          else
+            ar.part[at] = v[e];
         }
       }
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ss.o_free), mbar_arrive(&ss.q_free[item & 1]);
     }
   }
   tc_fence_before();
@@ -838,11 +833,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 }  // namespace
 
 cudaError_t attend_tc_prepare() {
-  // the roles' register split adds up to what a block launches with
-  cudaFuncAttributes f;
-  cudaError_t e = cudaFuncGetAttributes(&f, attend_kernel);
-  if (e == cudaSuccess && f.numRegs != REGS) e = cudaErrorInvalidConfiguration;
-  if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
 }
 

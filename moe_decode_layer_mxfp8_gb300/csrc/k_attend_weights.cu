@@ -62,6 +62,8 @@ __global__ void __launch_bounds__(THREADS, 2) attend_weights_kernel(const Attend
   plan.pre = reinterpret_cast<int*>(sm);
   plan.pmax = plan.pre + MAX_REQ + 4;
   plan.pmin = plan.pmax + MAX_REQ;
+  plan.pos = nullptr;
+  plan.req = nullptr;
   __half* sq = reinterpret_cast<__half*>(sm + PLAN_BYTES);
   constexpr int QLD = DH + 8, STEPS = DH / 16, PIECES = DH / 64;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, i4 = lane >> 2, j4 = lane & 3;
