@@ -10,11 +10,8 @@ namespace mono {
 namespace attend {
 
 constexpr int MAX_REQ = 512;
-constexpr int MAX_COLS = 64;  // query columns of a row group at most
+constexpr int MAX_COLS = 96;  // query columns of a row group at most
 constexpr float UNSET = -1.0e30f;  // the reference m_q of a query that has seen no token
-// log2 of a weight times its token's scale: below 1, and m_q puts the largest of the tile that moves
-// it at BASE or just below; scales below 2^LEAST (and zeros) count as that
-constexpr float BASE = -30.0f, LEAST = -60.0f;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 // How a kernel deals the work out: a tile of `tile` tokens, row groups of rows_per rows (cols query

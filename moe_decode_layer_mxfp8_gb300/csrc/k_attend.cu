@@ -44,37 +44,60 @@ using namespace tc;
 using namespace attend;
 
 constexpr int TT = 128;        // tokens per tile
-constexpr int NQ = MAX_COLS;   // query columns at most
 constexpr int GROUP = 16;      // rows of a group at most
-constexpr int ST = 8;          // tiles in the ring
-constexpr int C = 16;          // columns of a softmax warp
-constexpr int Q_TWICE = 32;    // items of up to so many columns have their queries made ahead
 constexpr int THREADS = 24 * 32;
 constexpr int SOFT_WARPS = 16, SOFT = SOFT_WARPS * 32, GROUPS = SOFT_WARPS / 4;
-constexpr int PREP_WARP = 16, PREP = 2 * 32, S_WARP = 18, O_WARP = 20, MMA_WARPS = 2;
-constexpr int LOAD_WARP = 22, LOAD_WARPS = 2;
+constexpr int Q_TWICE = 32;    // items of up to so many columns have their queries made ahead
 constexpr int MAX_ROWS = 1024;
-constexpr int K_TILE = TT * 128, IMG = 512, SLOTS = 8;
-constexpr int K_OFF = 0;
-constexpr int P_OFF = K_OFF + ST * K_TILE;      // weights [2]: tokens x (streams x (hi, lo) columns)
-constexpr int Q_OFF = P_OFF + 2 * K_TILE;       // queries: hi rows, then lo rows; [2] up to Q_TWICE columns
-constexpr int PIMG_OFF = Q_OFF + K_TILE;    // scale images of the weights [SLOTS],
-constexpr int QIMG_OFF = PIMG_OFF + SLOTS * IMG;  // of the queries [2],
-constexpr int ONE_OFF = QIMG_OFF + 2 * IMG;       // and of ones
-constexpr int SC_OFF = ONE_OFF + IMG;  // the 16 bytes behind the codes, scale first [ST][128]
-constexpr int PLAN_OFF = SC_OFF + ST * TT * 16;
-constexpr int SMEM_BYTES = PLAN_OFF + (3 * MAX_REQ + 4) * 4 + MAX_ROWS * 6 + 1024;
-static_assert(PREP == NQ, "a thread per column");
-static_assert(P_OFF % 1024 == 0 && Q_OFF % 1024 == 0 && 2 * NQ * 128 <= K_TILE, "swizzle atoms");
+constexpr int WIDE_FROM = 32;  // the wide form where requests have more columns on average
+constexpr int K_TILE = TT * 128, V_TILE = 2 * K_TILE, IMG = 512, SLOTS = 8;
 
-// TMEM columns: scores by slot, O by stream, scales
-// (ones for even and odd tiles, the queries' twice for each)
-constexpr int S_COL = 0, O_COL = 256, SF_ONE = 384, SF_Q = 392, SF_P = 408;
-static_assert(SF_P + 4 * SLOTS <= 512, "TMEM");
-// Instruction descriptor: kind::mxf8f6f4, e4m3 x e4m3, E8M0 scales, M = 128; N, and the scale-byte
-// selectors, are or-ed in.  The first product's operands are K-major, the second's MN-major.
+// What the two forms differ in (see the head of the file).
+template <bool WIDE>
+struct Form {
+  static constexpr int NQ = WIDE ? 96 : 64;  // query columns at most
+  static constexpr int CMAX = WIDE ? 24 : 16;  // columns of a softmax warp at most
+  static constexpr int ST = WIDE ? 3 : 8;    // tiles in the ring
+  // the roles' first warps
+  static constexpr int PREP_WARP = SOFT_WARPS, PREP = (WIDE ? 4 : 2) * 32;
+  static constexpr int MMA_WARPS = WIDE ? 1 : 2, S_WARP = PREP_WARP + PREP / 32,
+                       O_WARP = S_WARP + MMA_WARPS, LOAD_WARP = O_WARP + MMA_WARPS, LOAD_WARPS = 2;
+  static_assert(32 * (LOAD_WARP + LOAD_WARPS) == THREADS && PREP >= NQ, "roles");
+  // shared memory
+  static constexpr int K_OFF = 0;
+  static constexpr int V_OFF = K_OFF + ST * K_TILE;  // widened tiles [2]: dimensions 0..63, then 64..127
+  // weights [2]: tokens x (streams x columns) of 128 bytes; then those of columns from 64, of both
+  static constexpr int P_OFF = V_OFF + (WIDE ? 2 * V_TILE : 0);
+  // queries: hi rows, then lo rows; [2] up to Q_TWICE columns
+  static constexpr int Q_OFF = P_OFF + (WIDE ? 3 : 2) * K_TILE, Q_BYTES = 2 * NQ * 128;
+  static constexpr int PIMG_OFF = Q_OFF + Q_BYTES;   // scale images of the weights [SLOTS],
+  static constexpr int QIMG = WIDE ? 2 * IMG : IMG;
+  static constexpr int QIMG_OFF = PIMG_OFF + (WIDE ? 0 : SLOTS * IMG);  // of the queries [2],
+  static constexpr int ONE_OFF = QIMG_OFF + 2 * QIMG;                   // and of ones
+  static constexpr int SC_OFF = ONE_OFF + IMG;  // the 16 bytes behind the codes, scale first [ST][128]
+  static constexpr int PLAN_OFF = SC_OFF + ST * TT * 16;
+  static constexpr int SMEM_BYTES = PLAN_OFF + (3 * MAX_REQ + 4) * 4 + MAX_ROWS * 6 + 1024;
+  static_assert(P_OFF % 1024 == 0 && Q_OFF % 1024 == 0 && Q_BYTES / 2 % 1024 == 0, "swizzle atoms");
+  // TMEM columns: scores by slot, O by stream, scales (ones and the queries' per issuing warp)
+  static constexpr int S_COL = 0, O_COL = WIDE ? 384 : 256, SF_ONE = O_COL + (WIDE ? 96 : 128),
+                       SF_Q = SF_ONE + 4 * MMA_WARPS, SF_P = SF_Q + 8 * MMA_WARPS;
+  static_assert(SF_P + (WIDE ? 0 : 4 * SLOTS) <= 512, "TMEM");
+  // log2 of a weight times its token's scale: m puts the largest of the tile that moves it at BASE
+  // or just below, and moves again when one passes 2^15 (narrow: 2); scales below 2^LEAST (and zeros)
+  // count as that
+  static constexpr float BASE = WIDE ? 6.0f : -30.0f, LEAST = WIDE ? -90.0f : -60.0f;
+};
+// registers a thread in the wide form: softmax warps take what the others give up (in all, the
+// launch's)
+constexpr int REGS = 80, SOFT_REGS = 88, OTHER_REGS = 64;
+static_assert(SOFT_REGS * SOFT + OTHER_REGS * (THREADS - SOFT) == REGS * THREADS, "register split");
+
+// Instruction descriptors, M = 128; N, and the scale-byte selectors, are or-ed in.
+// kind::mxf8f6f4: e4m3 x e4m3, E8M0 scales, K-major, or (TRANS) MN-major.
 constexpr uint32_t IDESC = (1u << 23) | ((uint32_t)(TT >> 4) << 24);
 constexpr uint32_t TRANS = (1u << 15) | (1u << 16);
+// kind::f16: f16 x f16, f32 accumulators, both MN-major.
+constexpr uint32_t F16_IDESC = (1u << 4) | TRANS | ((uint32_t)(TT >> 4) << 24);
 
 struct Args {
   CUtensorMap codes, scales;  // the cache as [pages][tokens][bytes], boxes of box tokens
@@ -102,6 +125,26 @@ __device__ __forceinline__ void hilo_x4(const float* v, uint32_t& hi, uint32_t& 
       " mov.b32 %0, {h0, h1};\n mov.b32 %1, {l0, l1};\n}"
       : "=r"(hi), "=r"(lo)
       : "r"(f16x2_of(v[0], v[1])), "r"(f16x2_of(v[2], v[3])));
+}
+// Matrix descriptor as desc_sw128, MN-major with `lbo` bytes between 128-byte runs along MN.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
+  return (desc_sw128(saddr) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(lbo >> 4) << 16);
+}
+__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+template <int REGS>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 template <int N>
 __device__ __forceinline__ void bar_sync(int id) {
@@ -135,18 +178,22 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status
   return __all_sync(0xffffffffu, polls != ~0u);
 }
 // How an item's columns are dealt out (see the head of the file).
+template <bool WIDE>
 struct Deal {
   int nqp, lg, streams, bufs;  // columns; 2^lg streams of softmax groups; slots of scores, weights
   __device__ explicit Deal(int cols)
       : nqp(cols), lg(cols <= 16 ? 2 : cols <= 32 ? 1 : 0), streams(1 << lg), bufs(2 << lg) {}
   __device__ int slot(int i) const { return i & (bufs - 1); }
   __device__ int stream(int i) const { return i & (streams - 1); }
-  __device__ uint32_t s_col(int i) const { return S_COL + (slot(i) << (7 - lg)); }
-  __device__ uint32_t o_col(int stream) const { return O_COL + 2 * nqp * stream; }
+  __device__ uint32_t s_col(int i) const {
+    return Form<WIDE>::S_COL + (WIDE && lg == 0 ? 2 * Form<WIDE>::NQ * slot(i) : slot(i) << (7 - lg));
+  }
+  // a stream's columns of O: both terms' of the weights in the narrow form
+  __device__ uint32_t o_col(int stream) const { return Form<WIDE>::O_COL + (WIDE ? 1 : 2) * nqp * stream; }
   // where tile i's weights begin: their buffer, and the stream's place in its 128-byte rows
-  __device__ int p_buf(int i) const { return slot(i) >= streams ? K_TILE : 0; }
+  __device__ bool p_odd(int i) const { return slot(i) >= streams; }
   __device__ int p_byte(int stream) const { return 2 * nqp * stream; }
-  __device__ int q_byte(int item) const { return nqp <= Q_TWICE ? (item & 1) * (K_TILE / 2) : 0; }
+  __device__ int q_byte(int item) const { return nqp <= Q_TWICE ? (item & 1) * (Form<WIDE>::Q_BYTES / 2) : 0; }
   // parity of slot(i)'s phase of an item's tile i, and the phases that an item of n tiles
   // leaves (ph: the slots' parities at its start, a bit each)
   __device__ uint32_t parity(uint32_t ph, int i) const { return ((ph >> slot(i)) ^ (i >> (lg + 1))) & 1; }
@@ -164,31 +211,52 @@ __device__ __forceinline__ float warp_max_any(float v) {
 }
 
 // What the softmax needs of an item beside its span, made with the item's queries.
+template <bool WIDE>
 struct Meta {
+  static constexpr int NQ = Form<WIDE>::NQ;
   int cols, nrows;
   int row[GROUP], pos[GROUP];
   long long query[NQ], out[NQ];  // where a column's queries are, and where its first value goes
   int slice[NQ];                 // -1: padding
 };
+template <bool WIDE>
 struct Shared {
-  uint64_t full[ST], k_free[ST], s_full[SLOTS], p_full[SLOTS], pv_done[SLOTS];
-  uint64_t q_full[2], q_free[2], o_free, drain;
-  float neg_m[NQ], fac[NQ], red[SOFT_WARPS][C];  // m and its change: [stream][column]
-  uint32_t most[SOFT_WARPS][C];  // the warp's columns' largest weights
+  static constexpr int NQ = Form<WIDE>::NQ, ST = Form<WIDE>::ST, CMAX = Form<WIDE>::CMAX;
+  uint64_t full[ST], k_free[ST], s_full[SLOTS], p_full[SLOTS], pv_done[SLOTS], v_full[2], v_free[2];
+  uint64_t q_full[2], q_free[2], m_free[2], o_free, drain;
+  float neg_m[NQ], fac[NQ], red[SOFT_WARPS][CMAX];  // m and its change: [stream][column]
+  uint32_t most[SOFT_WARPS][CMAX];  // the warp's columns' largest weights
   uint32_t valid[ST][4];  // tokens that are there
-  float fin[4][NQ];   // a column's factor for each stream's O
-  Meta meta[2];
+  float fin[4][NQ];       // a column's factor for each stream's O
+  Meta<WIDE> meta[2];
   uint32_t tmem;
   int abort;
   Jobs start;
 };
-static_assert(SMEM_BYTES + sizeof(Shared) <= 227 * 1024, "shared memory");
+static_assert(Form<false>::SMEM_BYTES + sizeof(Shared<false>) <= 227 * 1024, "shared memory");
+static_assert(Form<true>::SMEM_BYTES + sizeof(Shared<true>) <= 227 * 1024, "shared memory");
+
+// The tiles [first, first + n) of an item that all its rows see whole (those of the sinks aside, where
+// there is a window); by a whole warp.
+struct Clear {
+  int first, n;
+  __device__ bool has(int i) const { return (uint32_t)(i - first) < (uint32_t)n; }
+};
+template <class M>
+__device__ __forceinline__ Clear clear_tiles(const AttendArgs& a, const Job& im, const M& meta) {
+  const int lane = threadIdx.x & 31, hi = a.causal ? meta.pos[lane < meta.nrows ? lane : 0] : im.span.hi;
+  const int lo = __reduce_max_sync(0xffffffffu, a.window > 0 ? max(0, hi - a.window + 1) : 0);
+  const int end = (__reduce_min_sync(0xffffffffu, hi) + 1) / TT;  // in tiles as tokens go
+  if (lo == 0) return {-im.t0, max(0, end)};
+  const int from = max((lo + TT - 1) / TT, im.span.body);
+  return {from + im.span.head - im.span.body - im.t0, max(0, end - from)};
+}
 
 // What a softmax warp knows of its item.
 struct Soft {
   Span span;
   int t0, n, it;      // the item's first tile and tile count, the ring's next tile
-  int clear, clears;  // tiles [clear, clear + clears) of the item are every row's to see
+  Clear clear;
   int c0, flat;       // this group's first column, of all and of all streams' m
   int first, stride;  // the group's tiles
   int arrive;         // arrivals of each warp at a tile's weights (SOFT_WARPS from all of them)
@@ -200,23 +268,31 @@ struct Soft {
 
 // The softmax of a group's columns over its tiles of an item, a token per thread; leaves the
 // thread's share of every column's sum, in units of 2^m.
-__device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, const Deal& deal,
-                                           const Meta& meta, Shared& sh, uint8_t* sm, float (&l)[C]) {
+template <bool WIDE, int C>
+__device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, const Deal<WIDE>& deal,
+                                           const Meta<WIDE>& meta, Shared<WIDE>& sh, uint8_t* sm,
+                                           float* l) {
+  using F = Form<WIDE>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3, group = warp >> 2, tok = 32 * quad + lane;
   volatile int* abort = &sh.abort;
   float s[C];
 #pragma unroll 1
   for (int i = w.first; i < w.n; i += w.stride) {
-    const int it = w.it + i, st = it % ST, b = deal.slot(i);
+    const int st = (w.it + i) % F::ST, b = deal.slot(i);
     wait(&sh.s_full[b], deal.parity(w.ph, i), a.status, abort);  // (so the tile is there)
-    const float raw = reinterpret_cast<const float*>(sm + SC_OFF)[(st * TT + tok) * 4];
+    const float raw = reinterpret_cast<const float*>(sm + F::SC_OFF)[(st * TT + tok) * 4];
     const uint32_t ok = sh.valid[st][quad];
     const bool fin = fabsf(raw) <= 3.0e38f;
     const float ct = fin ? raw * w.to_log2 : __int_as_float(0x7FC00000);
-    const float sc = fin ? raw : 0.0f, size = fabsf(sc), up = 64.0f * sc;
+    const float sc = fin ? raw : 0.0f, size = fabsf(sc);
+    const float lsc = sc != 0.0f ? fmaxf(log2_of(size), F::LEAST) : F::LEAST;
+    if (WIDE) {  // (as many arrivals whoever takes the tile)
+      __syncwarp();
+      if (lane < w.arrive) mbar_arrive(&sh.k_free[st]);
+    }
     // some of the tile's tokens may not be every row's to see
-    const bool part = ok != 0xffffffffu || (uint32_t)(i - w.clear) >= (uint32_t)w.clears;
+    const bool part = ok != 0xffffffffu || !w.clear.has(i);
     uint32_t see = 0xffffffffu;
     if (__builtin_expect(part, 0)) {  // the group's columns that see the token
       const int t = w.span.token(w.t0 + i) + tok;
@@ -231,10 +307,10 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
         see &= ~((1u << y) - (1u << x));
       }
     }
-    if (__builtin_expect(part && w.c0 == 0, 0)) {
+    if (!WIDE && __builtin_expect(part && w.c0 == 0, 0)) {
       // NaN codes that some row must not see would reach it as 0 * NaN (rows that do see the token
       // are NaN by their scores); the first product has read the tile
-      uint8_t* k = sm + K_OFF + st * K_TILE + tok * 128;
+      uint8_t* k = sm + F::K_OFF + st * K_TILE + tok * 128;
 #pragma unroll 1
       for (int e = 0; e < 8; ++e) {
         uint4* at = reinterpret_cast<uint4*>(k + (((e + lane) & 7) << 4));
@@ -250,7 +326,6 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
       tc_fence_after();
       if (__builtin_expect(move, 0)) {
         // the columns' largest weights times scales of the tile
-        const float lsc = sc != 0.0f ? fmaxf(log2_of(size), LEAST) : LEAST;
 #pragma unroll 1
         for (int g = 0; g < C; g += 8) {
           float x[8], y[8], mine = 0.0f;
@@ -270,12 +345,12 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
         }
         bar_sync<128>(6 + group);
         if (quad == 0 && lane < C) {
-          const float(*r)[C] = sh.red + 4 * group;
+          const float(*r)[F::CMAX] = sh.red + 4 * group;
           const float m = fmaxf(fmaxf(r[0][lane], r[1][lane]), fmaxf(r[2][lane], r[3][lane]));
           const float old = -sh.neg_m[w.flat + lane];
           float f = 1.0f;
-          if (m - old > BASE) {
-            const float now = fminf(ceilf(m) - BASE, 3.0e38f);
+          if (m - old > F::BASE) {
+            const float now = fminf(ceilf(m) - F::BASE, 3.0e38f);
             f = old == UNSET ? 0.0f : ex2(old - now);
             sh.neg_m[w.flat + lane] = -now;
           }
@@ -289,14 +364,15 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
           wait(&sh.pv_done[deal.slot(pi)], deal.parity(w.ph, pi), a.status, abort);
           tc_fence_after();
 #pragma unroll 1
-          for (int g = 0; g < 2 * C; g += 8) {  // both terms'
+          for (int g0 = 0; g0 < (WIDE ? C : 2 * C); g0 += 8) {  // (both terms')
             float x[8];
-            const uint32_t oc = w.tmem + deal.o_col(w.first) + w.c0 + (g & C ? deal.nqp : 0) + (g & (C - 1));
+            const int g = g0 < C ? g0 : g0 - C;
+            const uint32_t oc = w.tmem + deal.o_col(w.first) + w.c0 + g + (g0 < C ? 0 : deal.nqp);
             tc_ld8(oc, x);
             tc_wait_ld();
             tc_loaded(x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= sh.fac[w.flat + (g & (C - 1)) + e];
+            for (int e = 0; e < 8; ++e) x[e] *= sh.fac[w.flat + g + e];
             tc_st8(oc, x);
           }
           tc_wait_st();
@@ -326,50 +402,79 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
         for (int c = 0; c < C; ++c)
           if (!((see >> c) & 1)) s[c] = -INFINITY;
       }
-      // the largest weights times scales of the warp's tokens, as bits; 2 and more (or NaN) asks
-      // for a larger m
-      uint32_t any = 0;
+      uint32_t ask;
+      if constexpr (WIDE) {
+        float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        s[c] = ex2(s[c]);
-        mb[c] = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaf(s[c], size, 0x1p-118f)));
-        any |= mb[c];
+        for (int c = 0; c < C; ++c) top = fmaxf(top, s[c]);
+        ask = top + lsc > 15.0f;
+      } else {
+        // the largest weights times scales of the warp's tokens, as bits; 2 and more (or NaN) asks
+        // for a larger m
+        uint32_t any = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          s[c] = ex2(s[c]);
+          mb[c] = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaf(s[c], size, 0x1p-118f)));
+          any |= mb[c];
+        }
+        ask = any >> 30;
       }
       if (moved) break;  // (alike in the group's warps)
-      move = bar_any(2 + group, any >> 30);
+      move = bar_any(2 + group, ask);
       if (__builtin_expect(!move, 1)) break;
     }
-    // weights times scales as two e4m3 terms, 16 + 16 bytes of the token's row; a column's largest
-    // of the warp's tokens is in [2^7, 2^8)
-    uint32_t hi[4], lo[4];
+    uint8_t* prow = sm + F::P_OFF + tok * 128;
+    if constexpr (WIDE) {
+      // weights times scales
 #pragma unroll
-    for (int g = 0; g < C; g += 4) {
-      float y[4];
+      for (int g = 0; g < C; g += 8) {
+        uint32_t o[4];
 #pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const int c = g + e;
-        y[e] = __uint_as_float(~mb[c] & 0x7F800000u);  // 2 / the largest's power of two
-        y[e + 1] = __uint_as_float(~mb[c + 1] & 0x7F800000u);
-        mul2(y[e], y[e + 1], up);
-        mul2(y[e], y[e + 1], s[c], s[c + 1]);
-        add2(l[c], l[c + 1], s[c], s[c + 1]);
+        for (int e = 0; e < 8; e += 2) {
+          float p0 = ex2(s[g + e]), p1 = ex2(s[g + e + 1]);
+          add2(l[g + e], l[g + e + 1], p0, p1);
+          mul2(p0, p1, sc);
+          o[e / 2] = f16x2_of(p0, p1);
+        }
+        const int col = w.c0 + g, run = col >> 6, odd = deal.p_odd(i);
+        const int ch = (deal.p_byte(w.first) + 2 * (col & 63) + (run & odd) * 64) >> 4;
+        *reinterpret_cast<uint4*>(prow + (run ? 2 : odd) * K_TILE + ((ch ^ (tok & 7)) << 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
       }
-      hilo_x4(y, hi[g / 4], lo[g / 4]);
-    }
-    if (lane == 0) {
+    } else {
+      // weights times scales as two e4m3 terms, 16 + 16 bytes of the token's row; a column's largest
+      // of the warp's tokens is in [2^7, 2^8)
+      const float up = 64.0f * sc;
+      uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int g = 0; g < C; g += 4)
-        *reinterpret_cast<uint4*>(&sh.most[warp][g]) = make_uint4(mb[g], mb[g + 1], mb[g + 2], mb[g + 3]);
-    }
-    uint8_t* prow = sm + P_OFF + deal.p_buf(i) + tok * 128;
-    const int ch = (deal.p_byte(w.first) + w.c0) >> 4, cl = ch + (deal.nqp >> 4);
-    *reinterpret_cast<uint4*>(prow + ((ch ^ (tok & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(prow + ((cl ^ (tok & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    __syncwarp();
-    {
-      const int n = w.c0 + (lane & 15) + (lane >> 4) * deal.nqp;
-      sm[PIMG_OFF + b * IMG + (n & 31) * 16 + (n >> 5) * 4 + quad] =
-          (uint8_t)((sh.most[warp][lane & 15] >> 23) - 7);
+      for (int g = 0; g < C; g += 4) {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const int c = g + e;
+          y[e] = __uint_as_float(~mb[c] & 0x7F800000u);  // 2 / the largest's power of two
+          y[e + 1] = __uint_as_float(~mb[c + 1] & 0x7F800000u);
+          mul2(y[e], y[e + 1], up);
+          mul2(y[e], y[e + 1], s[c], s[c + 1]);
+          add2(l[c], l[c + 1], s[c], s[c + 1]);
+        }
+        hilo_x4(y, hi[g / 4], lo[g / 4]);
+      }
+      if (lane == 0) {
+#pragma unroll
+        for (int g = 0; g < C; g += 4)
+          *reinterpret_cast<uint4*>(&sh.most[warp][g]) = make_uint4(mb[g], mb[g + 1], mb[g + 2], mb[g + 3]);
+      }
+      const int ch = (deal.p_byte(w.first) + w.c0) >> 4, cl = ch + (deal.nqp >> 4);
+      *reinterpret_cast<uint4*>(prow + deal.p_odd(i) * K_TILE + ((ch ^ (tok & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(prow + deal.p_odd(i) * K_TILE + ((cl ^ (tok & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      __syncwarp();
+      {
+        const int n = w.c0 + (lane & 15) + (lane >> 4) * deal.nqp;
+        sm[F::PIMG_OFF + b * IMG + (n & 31) * 16 + (n >> 5) * 4 + quad] =
+            (uint8_t)((sh.most[warp][lane & 15] >> 23) - 7);
+      }
     }
     fence_proxy_async_shared();
     tc_fence_before();
@@ -378,15 +483,38 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
   }
 }
 
+// Sums of N columns over the warp's lanes: lane k gets column k % N's.
+template <int N>
+__device__ __forceinline__ float column_sums(float* l) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int x = N / 2; x > 0; x >>= 1) {
+#pragma unroll
+    for (int c = 0; c < x; ++c) {
+      const bool up = lane & x;
+      const float give = up ? l[c] : l[c + x], keep = up ? l[c + x] : l[c];
+      l[c] = keep + __shfl_xor_sync(0xffffffffu, give, x);
+    }
+  }
+#pragma unroll
+  for (int x = N; x < 32; x <<= 1) l[0] += __shfl_xor_sync(0xffffffffu, l[0], x);
+  return l[0];
+}
+
+template <bool WIDE>
 __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constant__ Args ar) {
+  using F = Form<WIDE>;
+  constexpr int NQ = F::NQ, ST = F::ST, PREP_WARP = F::PREP_WARP, PREP = F::PREP, S_WARP = F::S_WARP,
+                O_WARP = F::O_WARP, MMA_WARPS = F::MMA_WARPS, LOAD_WARP = F::LOAD_WARP,
+                LOAD_WARPS = F::LOAD_WARPS;
   const AttendArgs& a = ar.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                            ~uintptr_t(1023));
-  __shared__ __align__(16) Shared ss;
+  __shared__ __align__(16) Shared<WIDE> ss;
   volatile int* abort = &ss.abort;
   Plan plan;
-  plan.pre = reinterpret_cast<int*>(sm + PLAN_OFF);
+  plan.pre = reinterpret_cast<int*>(sm + F::PLAN_OFF);
   plan.pmax = plan.pre + MAX_REQ + 4;
   plan.pmin = plan.pmax + MAX_REQ;
   plan.pos = plan.pmin + MAX_REQ;
@@ -397,24 +525,29 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   const int chunk_bytes = min(128, a.kv_dim - 128 * chunk);
 
   if (tid == 0) {
-    // (a tile is free when its second product is done)
-    for (int s = 0; s < ST; ++s) mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], 1);
+    // a tile is free when its second product is done, or in the wide form when the first product,
+    // the widening and the softmax warps have read it
+    for (int s = 0; s < ST; ++s)
+      mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], WIDE ? 1 + PREP / 32 + SOFT_WARPS : 1);
+    for (int s = 0; s < 2; ++s) mbar_init(&ss.v_full[s], PREP / 32), mbar_init(&ss.v_free[s], 1);
     for (int s = 0; s < SLOTS; ++s)
       mbar_init(&ss.s_full[s], 1), mbar_init(&ss.pv_done[s], 1), mbar_init(&ss.p_full[s], SOFT_WARPS);
-    // an item's queries are free when all that read them or wait for them are done
+    // an item's queries are free with its first products, the rest of what was made with them when
+    // all that read it or wait for it are done
     for (int s = 0; s < 2; ++s)
-      mbar_init(&ss.q_full[s], PREP / 32), mbar_init(&ss.q_free[s], 2 * MMA_WARPS + SOFT_WARPS);
+      mbar_init(&ss.q_full[s], PREP / 32), mbar_init(&ss.q_free[s], MMA_WARPS),
+          mbar_init(&ss.m_free[s], MMA_WARPS + SOFT_WARPS);
     mbar_init(&ss.o_free, SOFT_WARPS);
     mbar_init(&ss.drain, 2 * MMA_WARPS);
     ss.abort = 0;
     fence_mbar_init();
   }
   if (warp == S_WARP) tmem_alloc<512>(&ss.tmem);
-  for (int i = tid; i < (SLOTS + 3) * IMG / 4; i += THREADS)
-    reinterpret_cast<uint32_t*>(sm + PIMG_OFF)[i] = 0x7F7F7F7Fu;
+  for (int i = tid; i < (F::SC_OFF - F::PIMG_OFF) / 4; i += THREADS)
+    reinterpret_cast<uint32_t*>(sm + F::PIMG_OFF)[i] = 0x7F7F7F7Fu;
   if (!ar.box && chunk_bytes < 128)  // (the bytes that nothing else writes)
     for (int i = tid; i < ST * K_TILE / 16; i += THREADS)
-      *reinterpret_cast<uint4*>(sm + K_OFF + 16 * i) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(sm + F::K_OFF + 16 * i) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_shared();
 
   derive_plan<THREADS>(a, sh, plan, team, team < sh.teams, &ss.start, ar.total);
@@ -425,271 +558,336 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   Jobs items = ss.start;
   Job im;
 
-  if (warp >= LOAD_WARP) {
-    // ------------------------------------------------------- loads: a warp takes every other tile
-    int ni = warp - LOAD_WARP;
-    bool more = next_job(a, sh, plan, items, im);
-    // a lane per box of the next tile (of a token each without maps, four times): its page, on its
-    // way while the tile before is loaded, and its first token's place in it
-    const int box = ar.box ? ar.box : 1, bs = a.kv.block_size;
-    const int shift = __ffs(box) - 1, boxes = TT >> shift;
-    int page[4], row[4], t0 = 0;
-    auto locate = [&]() {
+  if (warp >= SOFT_WARPS) {
+    if constexpr (WIDE) regs_down<OTHER_REGS>();
+    if (warp >= LOAD_WARP) {
+      // ------------------------------------------------------- loads: a warp takes every other tile
+      int ni = warp - LOAD_WARP;
+      bool more = next_job(a, sh, plan, items, im);
+      // a lane per box of the next tile (of a token each without maps, four times): its page, on its
+      // way while the tile before is loaded, and its first token's place in it
+      const int box = ar.box ? ar.box : 1, bs = a.kv.block_size;
+      const int shift = __ffs(box) - 1, boxes = TT >> shift;
+      int page[4], row[4], t0 = 0;
+      auto locate = [&]() {
 #pragma unroll 1
-      while (more && ni >= im.n) ni -= im.n, more = next_job(a, sh, plan, items, im);
-      if (!more) return;
-      t0 = im.span.token(im.t0 + ni);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (32 * q >= boxes) break;
-        const int t = t0 + ((32 * q + lane) << shift), lb = t / bs;
-        page[q] = -1;
-        row[q] = t - lb * bs;
-        if (32 * q + lane < boxes && lb < a.kv.max_blocks && t <= im.span.hi &&
-            (t + box > im.span.lo || t < a.sinks))
-          page[q] = __ldg(a.kv.table + (size_t)im.b * a.kv.max_blocks + lb);
-        else
-          row[q] = -1;
-      }
-    };
-    auto mapped = [&](int q) {
-      const bool m = page[q] >= 0 && page[q] < a.kv.num_blocks;
-      if (row[q] >= 0 && !m) atomicOr(a.status, ST_UNMAPPED_PAGE);
-      return m;
-    };
-    locate();
-#pragma unroll 1
-    for (int it = warp - LOAD_WARP; more; it += LOAD_WARPS) {
-      const int s = it % ST;
-      bool go = true;
-      if (it >= ST) go = wait(&ss.k_free[s], ((it / ST) - 1) & 1, a.status, abort);
-      uint8_t* st = sm + K_OFF + s * K_TILE;
-      uint8_t* sc = sm + SC_OFF + s * TT * 16;
-      if (ar.box) {
-        // boxes with a token to see; their other tokens, and what the rest of the slot holds, are
-        // masked
-        const bool m = mapped(0);
-        if (m && go) {
-          tma_load_3d(st + ((lane * 128) << shift), &ar.codes, 128 * chunk, row[0], page[0], &ss.full[s]);
-          tma_load_3d(sc + ((lane * 16) << shift), &ar.scales, a.kv_dim, row[0], page[0], &ss.full[s]);
-        }
-        const uint32_t have = __ballot_sync(0xffffffffu, m);
+        while (more && ni >= im.n) ni -= im.n, more = next_job(a, sh, plan, items, im);
+        if (!more) return;
+        t0 = im.span.token(im.t0 + ni);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int t = t0 + 32 * q + lane;
-          const bool see = ((have >> ((32 * q + lane) >> shift)) & 1) && t <= im.span.hi &&
-                           (t >= im.span.lo || t < a.sinks);
-          const uint32_t w = __ballot_sync(0xffffffffu, see);
-          if (lane == q) ss.valid[s][q] = w;
+          if (32 * q >= boxes) break;
+          const int t = t0 + ((32 * q + lane) << shift), lb = t / bs;
+          page[q] = -1;
+          row[q] = t - lb * bs;
+          if (32 * q + lane < boxes && lb < a.kv.max_blocks && t <= im.span.hi &&
+              (t + box > im.span.lo || t < a.sinks))
+            page[q] = __ldg(a.kv.table + (size_t)im.b * a.kv.max_blocks + lb);
+          else
+            row[q] = -1;
         }
-        __syncwarp();
-        // (bytes that land before they are expected wait for this arrival all the same)
-        if (lane == 0) mbar_arrive_expect_tx(&ss.full[s], go ? __popc(have) * box * (128 + 16) : 0);
-        __syncwarp();
-      } else {
-        const int piece = lane & 7;
-        const bool in_chunk = go && 16 * piece < chunk_bytes;
+      };
+      auto mapped = [&](int q) {
+        const bool m = page[q] >= 0 && page[q] < a.kv.num_blocks;
+        if (row[q] >= 0 && !m) atomicOr(a.status, ST_UNMAPPED_PAGE);
+        return m;
+      };
+      locate();
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          const int pg = q == 0 ? page[0] : q == 1 ? page[1] : q == 2 ? page[2] : page[3];
-          const int rw = q == 0 ? row[0] : q == 1 ? row[1] : q == 2 ? row[2] : row[3];
-          const bool m = pg >= 0 && pg < a.kv.num_blocks;
-          if (rw >= 0 && !m) atomicOr(a.status, ST_UNMAPPED_PAGE);
-          const long long off = m ? pg * a.kv.stride_block + rw * a.kv.stride_tok : 0;
-          const uint32_t w = __ballot_sync(0xffffffffu, m);
-          if (lane == 0) ss.valid[s][q] = w;
-#pragma unroll 1
-          for (int e = 0; e < 8; ++e) {
-            const int k = 4 * e + (lane >> 3), r = 32 * q + k;
-            const long long ro = __shfl_sync(0xffffffffu, off, k);
-            if (in_chunk && ((w >> k) & 1))
-              cp_async16(st + r * 128 + ((piece ^ (r & 7)) << 4), a.kv.base + ro + 128 * chunk + 16 * piece,
-                         16);
+      for (int it = warp - LOAD_WARP; more; it += LOAD_WARPS) {
+        const int s = it % ST;
+        bool go = true;
+        if (it >= ST) go = wait(&ss.k_free[s], ((it / ST) - 1) & 1, a.status, abort);
+        uint8_t* st = sm + F::K_OFF + s * K_TILE;
+        uint8_t* sc = sm + F::SC_OFF + s * TT * 16;
+        if (ar.box) {
+          // boxes with a token to see; their other tokens, and what the rest of the slot holds, are
+          // masked
+          const bool m = mapped(0);
+          if (m && go) {
+            tma_load_3d(st + ((lane * 128) << shift), &ar.codes, 128 * chunk, row[0], page[0], &ss.full[s]);
+            tma_load_3d(sc + ((lane * 16) << shift), &ar.scales, a.kv_dim, row[0], page[0], &ss.full[s]);
           }
-          if (go && m) cp_async16(sc + (32 * q + lane) * 16, a.kv.base + off + a.kv_dim, 16);
+          const uint32_t have = __ballot_sync(0xffffffffu, m);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int t = t0 + 32 * q + lane;
+            const bool see = ((have >> ((32 * q + lane) >> shift)) & 1) && t <= im.span.hi &&
+                             (t >= im.span.lo || t < a.sinks);
+            const uint32_t w = __ballot_sync(0xffffffffu, see);
+            if (lane == q) ss.valid[s][q] = w;
+          }
+          __syncwarp();
+          // (bytes that land before they are expected wait for this arrival all the same)
+          if (lane == 0) mbar_arrive_expect_tx(&ss.full[s], go ? __popc(have) * box * (128 + 16) : 0);
+          __syncwarp();
+        } else {
+          const int piece = lane & 7;
+          const bool in_chunk = go && 16 * piece < chunk_bytes;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            const int pg = q == 0 ? page[0] : q == 1 ? page[1] : q == 2 ? page[2] : page[3];
+            const int rw = q == 0 ? row[0] : q == 1 ? row[1] : q == 2 ? row[2] : row[3];
+            const bool m = pg >= 0 && pg < a.kv.num_blocks;
+            if (rw >= 0 && !m) atomicOr(a.status, ST_UNMAPPED_PAGE);
+            const long long off = m ? pg * a.kv.stride_block + rw * a.kv.stride_tok : 0;
+            const uint32_t w = __ballot_sync(0xffffffffu, m);
+            if (lane == 0) ss.valid[s][q] = w;
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {
+              const int k = 4 * e + (lane >> 3), r = 32 * q + k;
+              const long long ro = __shfl_sync(0xffffffffu, off, k);
+              if (in_chunk && ((w >> k) & 1))
+                cp_async16(st + r * 128 + ((piece ^ (r & 7)) << 4), a.kv.base + ro + 128 * chunk + 16 * piece,
+                           16);
+            }
+            if (go && m) cp_async16(sc + (32 * q + lane) * 16, a.kv.base + off + a.kv_dim, 16);
+          }
+          cp_async_wait_all();
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ss.full[s]);
         }
-        cp_async_wait_all();
+        ni += LOAD_WARPS;
+        locate();
+      }
+    } else if (warp >= PREP_WARP && warp < PREP_WARP + PREP / 32) {
+      // ---------------------- the items' rows and queries, and in the wide form the tiles' widening
+      const int hpg = a.n_q / (a.kv_dim / a.head_dim);
+      const int cheads = hpg * (chunk_bytes > a.head_dim ? 2 : 1);  // heads per row of this chunk
+      const int dshift = a.head_dim == 64 ? 6 : 7, ptid = tid - 32 * PREP_WARP;
+      int it = 0;
+      bool before = false;  // the item before had more than Q_TWICE columns
+#pragma unroll 1
+      for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
+        const int qb = item & 1;
+        if (item >= 2) {
+          wait(&ss.q_free[qb], ((item >> 1) - 1) & 1, a.status, abort);
+          wait(&ss.m_free[qb], ((item >> 1) - 1) & 1, a.status, abort);
+        }
+        Meta<WIDE>& meta = ss.meta[qb];
+        if (warp == PREP_WARP) {
+          const int n = group_rows(a, sh, plan, im.b, im.group, meta.row, meta.pos);
+          if (lane == 0) meta.cols = (n * cheads + 15) & ~15, meta.nrows = n;
+        }
+        bar_sync<PREP>(1);
+        const int nqp = meta.cols, nq = meta.nrows * cheads;
+        if (ptid < NQ) {  // a column per thread: its head of the chunk, and where its queries and its results are
+          const bool whole = im.n == im.span.tiles;  // nobody else has tiles of this group
+          const int slot = (team * 2 + (im.t0 > 0 ? 0 : 1)) * sh.chunks + chunk;
+          const int j = ptid / cheads, h = ptid - j * cheads;
+          const int at = (chunk * sh.heads + h) * a.head_dim, r = ptid < nq ? meta.row[j] : 0;
+          meta.slice[ptid] = ptid < nq ? (h >= hpg ? 1 : 0) : -1;
+          meta.query[ptid] = r * a.q_stride + at;
+          meta.out[ptid] = whole ? r * a.o_stride + at : (long long)(slot * NQ + ptid) * PART_LD + 4;
+        }
+        const bool once = nqp > Q_TWICE;  // (the one buffer that both halves are)
+        if (item > 0 && (once || before)) wait(&ss.q_free[qb ^ 1], ((item - 1) >> 1) & 1, a.status, abort);
+        before = once;
+        bar_sync<PREP>(1);
+        // queries as two e4m3 terms, rows of 128 bytes: hi in row c, lo in row nqp + c; a thread
+        // takes 8 dimensions, the next ones on their way meanwhile
+        const int d = (ptid & 15) * 8, sl = d >> dshift, o = d >> 4;
+        const __nv_bfloat16* q = a.q + (d - (sl << dshift));
+        auto fetch = [&](int c) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (c < nq && meta.slice[c] == sl) x = __ldg(reinterpret_cast<const uint4*>(q + meta.query[c]));
+          return x;
+        };
+        uint4 next = fetch(ptid >> 4);
+        uint8_t* to = sm + F::Q_OFF + (once ? 0 : qb * (F::Q_BYTES / 2)) + (d & 8);
+        uint8_t* img = sm + F::QIMG_OFF + qb * F::QIMG + (d >> 5);
+#pragma unroll 1
+        for (int c = ptid >> 4; c < nqp; c += PREP / 16) {
+          float v[8];
+          bf16x8_to_f32(next, v);
+          next = fetch(c + PREP / 16);
+          float m = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          if (__builtin_expect(isinf(m), 0)) {  // (the codes have no infinity)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (isinf(v[e])) v[e] = __int_as_float(0x7FC00000);
+          }
+          const uint32_t code = e4m3_block_code(m);
+          const float inv = e8m0_inverse(code);
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) mul2(v[e], v[e + 1], inv);
+          uint32_t hw[2], lw[2];
+          hilo_x4(v, hw[0], lw[0]);
+          hilo_x4(v + 4, hw[1], lw[1]);
+          const int rl = nqp + c;
+          *reinterpret_cast<uint2*>(to + c * 128 + ((o ^ (c & 7)) << 4)) = make_uint2(hw[0], hw[1]);
+          *reinterpret_cast<uint2*>(to + rl * 128 + ((o ^ (rl & 7)) << 4)) = make_uint2(lw[0], lw[1]);
+          if ((d & 31) == 0) {
+            img[(c & 31) * 16 + (c >> 5) * 4] = (uint8_t)code;
+            img[(rl >> 7) * IMG + (rl & 31) * 16 + (rl >> 5 & 3) * 4] = (uint8_t)code;
+          }
+        }
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ss.full[s]);
-      }
-      ni += LOAD_WARPS;
-      locate();
-    }
-  } else if (warp >= PREP_WARP && warp < PREP_WARP + PREP / 32) {
-    // -------------------------------------------------------- the items' rows and queries
-    const int hpg = a.n_q / (a.kv_dim / a.head_dim);
-    const int cheads = hpg * (chunk_bytes > a.head_dim ? 2 : 1);  // heads per row of this chunk
-    const int dshift = a.head_dim == 64 ? 6 : 7, ptid = tid - 32 * PREP_WARP;
-    bool before = false;  // the item before had more than Q_TWICE columns
+        if (lane == 0) mbar_arrive(&ss.q_full[qb]);
+        if constexpr (WIDE) {  // a warp widens 32 tokens of every tile
+          const Clear clear = clear_tiles(a, im, meta);
+          const int lw = warp - PREP_WARP, piece = lane & 7, r4 = lane >> 3;
 #pragma unroll 1
-    for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
-      const int qb = item & 1;
-      if (item >= 2) wait(&ss.q_free[qb], ((item >> 1) - 1) & 1, a.status, abort);
-      Meta& meta = ss.meta[qb];
-      if (warp == PREP_WARP) {
-        const int n = group_rows(a, sh, plan, im.b, im.group, meta.row, meta.pos);
-        if (lane == 0) meta.cols = (n * cheads + 15) & ~15, meta.nrows = n;
-      }
-      bar_sync<PREP>(1);
-      const int nqp = meta.cols, nq = meta.nrows * cheads;
-      {  // a column per thread: its head of the chunk, and where its queries and its results are
-        const bool whole = im.n == im.span.tiles;  // nobody else has tiles of this group
-        const int slot = (team * 2 + (im.t0 > 0 ? 0 : 1)) * sh.chunks + chunk;
-        const int j = ptid / cheads, h = ptid - j * cheads;
-        const int at = (chunk * sh.heads + h) * a.head_dim, r = ptid < nq ? meta.row[j] : 0;
-        meta.slice[ptid] = ptid < nq ? (h >= hpg ? 1 : 0) : -1;
-        meta.query[ptid] = r * a.q_stride + at;
-        meta.out[ptid] = whole ? r * a.o_stride + at : (long long)(slot * NQ + ptid) * PART_LD + 4;
-      }
-      const bool once = nqp > Q_TWICE;  // (the one buffer that both halves are)
-      if (item > 0 && (once || before)) wait(&ss.q_free[qb ^ 1], ((item - 1) >> 1) & 1, a.status, abort);
-      before = once;
-      bar_sync<PREP>(1);
-      // queries as two e4m3 terms, rows of 128 bytes: hi in row c, lo in row nqp + c; a thread
-      // takes 8 dimensions, the next ones on their way meanwhile
-      const int d = (ptid & 15) * 8, sl = d >> dshift, o = d >> 4;
-      const __nv_bfloat16* q = a.q + (d - (sl << dshift));
-      auto fetch = [&](int c) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (c < nq && meta.slice[c] == sl) x = __ldg(reinterpret_cast<const uint4*>(q + meta.query[c]));
-        return x;
-      };
-      uint4 next = fetch(ptid >> 4);
-      uint8_t* to = sm + Q_OFF + (once ? 0 : qb * (K_TILE / 2)) + (d & 8);
-      uint8_t* img = sm + QIMG_OFF + qb * IMG + (d >> 5);
-#pragma unroll 1
-      for (int c = ptid >> 4; c < nqp; c += PREP / 16) {
-        float v[8];
-        bf16x8_to_f32(next, v);
-        next = fetch(c + PREP / 16);
-        float m = 0.0f;
+          for (int i = 0; i < im.n; ++i, ++it) {
+            const int s = it % ST, b = it & 1;
+            wait(&ss.full[s], (it / ST) & 1, a.status, abort);
+            if (it >= 2) wait(&ss.v_free[b], ((it >> 1) - 1) & 1, a.status, abort);
+            const bool part = ss.valid[s][lw] != 0xffffffffu || !clear.has(i);
+            const uint8_t* src = sm + F::K_OFF + s * K_TILE + 32 * lw * 128;
+            uint8_t* dst = sm + F::V_OFF + b * V_TILE + (piece >> 2) * K_TILE + 32 * lw * 128;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        if (__builtin_expect(isinf(m), 0)) {  // (the codes have no infinity)
+            for (int h = 0; h < 2; ++h) {
+              uint4 v[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (isinf(v[e])) v[e] = __int_as_float(0x7FC00000);
-        }
-        const uint32_t code = e4m3_block_code(m);
-        const float inv = e8m0_inverse(code);
+              for (int e = 0; e < 4; ++e) {
+                const int row = 16 * h + 4 * e + r4;
+                v[e] = lds128(src + row * 128 + ((piece ^ (row & 7)) << 4));
+              }
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) mul2(v[e], v[e + 1], inv);
-        uint32_t hw[2], lw[2];
-        hilo_x4(v, hw[0], lw[0]);
-        hilo_x4(v + 4, hw[1], lw[1]);
-        const int rl = nqp + c;
-        *reinterpret_cast<uint2*>(to + c * 128 + ((o ^ (c & 7)) << 4)) = make_uint2(hw[0], hw[1]);
-        *reinterpret_cast<uint2*>(to + rl * 128 + ((o ^ (rl & 7)) << 4)) = make_uint2(lw[0], lw[1]);
-        if ((d & 31) == 0) {
-          img[(c & 31) * 16 + (c >> 5) * 4] = (uint8_t)code;
-          img[(rl & 31) * 16 + (rl >> 5) * 4] = (uint8_t)code;
+              for (int e = 0; e < 4; ++e) {
+                // a NaN code that some row must not see would reach it as 0 * NaN (rows that do see
+                // the token are NaN by their scores)
+                if (__builtin_expect(part, 0)) v[e] = without_nan(v[e]);
+                const int row = 16 * h + 4 * e + r4, c = 2 * (piece & 3);
+                uint4 x, y;
+                uint32_t f[2];
+                e4m3x4_to_f16x4(v[e].x, f), x.x = f[0], x.y = f[1];
+                e4m3x4_to_f16x4(v[e].y, f), x.z = f[0], x.w = f[1];
+                e4m3x4_to_f16x4(v[e].z, f), y.x = f[0], y.y = f[1];
+                e4m3x4_to_f16x4(v[e].w, f), y.z = f[0], y.w = f[1];
+                *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = x;
+                *reinterpret_cast<uint4*>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) = y;
+              }
+            }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ss.v_full[b]), mbar_arrive(&ss.k_free[s]);
+          }
         }
       }
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ss.q_full[qb]);
-    }
-  } else if (warp >= S_WARP && warp < S_WARP + MMA_WARPS) {
-    // ------------------------------- the first product's MMAs: a warp issues every other tile's
-    const int mine = warp - S_WARP;
-    const uint64_t k0 = desc_sw128(smem_u32(sm + K_OFF)), q0 = desc_sw128(smem_u32(sm + Q_OFF));
-    const uint32_t sf0 = tmem + SF_Q + 8 * mine, ones = tmem + SF_ONE + 4 * mine;
-    int it = 0;
-    uint32_t ph = 0;
-    if (elect_one()) tc_cp_img(ones, sm + ONE_OFF);
-    __syncwarp();
-#pragma unroll 1
-    for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
-      const int qb = item & 1;
-      wait(&ss.q_full[qb], (item >> 1) & 1, a.status, abort);
-      const Deal deal(ss.meta[qb].cols);
-      const uint32_t idesc = IDESC | ((uint32_t)(2 * deal.nqp >> 3) << 17);
-      const uint32_t sf = sf0 + 4 * qb;
-      const uint64_t qd = q0 + (deal.q_byte(item) >> 4);
-      if (elect_one()) tc_cp_img(sf, sm + QIMG_OFF + qb * IMG);
+    } else if (warp >= S_WARP && warp < S_WARP + MMA_WARPS) {
+      // ------------------ the first product's MMAs (two warps: each issues every other tile's)
+      const int mine = warp - S_WARP;
+      const uint64_t k0 = desc_sw128(smem_u32(sm + F::K_OFF)), q0 = desc_sw128(smem_u32(sm + F::Q_OFF));
+      const uint32_t sf = tmem + F::SF_Q + 8 * mine, ones = tmem + F::SF_ONE + 4 * mine;
+      int it = 0;
+      uint32_t ph = 0;
+      if (elect_one()) tc_cp_img(ones, sm + F::ONE_OFF);
       __syncwarp();
 #pragma unroll 1
-      for (int i = mine; i < im.n; i += MMA_WARPS) {
-        const int st = (it + i) % ST, b = deal.slot(i);
-        bool ok = wait(&ss.full[st], ((it + i) / ST) & 1, a.status, abort);
-        // the slot's scores and weights are no longer in use
-        if (i >= deal.bufs)
-          ok &= wait(&ss.pv_done[b], deal.parity(ph, i - deal.bufs), a.status, abort);
-        if (ok && elect_one()) {
-          tc_fence_after();
-          const uint64_t kd = k0 + st * (K_TILE / 16);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            tc_mma_mxf8(tmem + deal.s_col(i), kd + 2 * k, qd + 2 * k,
-                        idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), ones, sf, k > 0);
-          tc_commit(&ss.s_full[b]);
+      for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
+        const int qb = item & 1;
+        wait(&ss.q_full[qb], (item >> 1) & 1, a.status, abort);
+        const Deal<WIDE> deal(ss.meta[qb].cols);
+        const uint32_t idesc = IDESC | ((uint32_t)(2 * deal.nqp >> 3) << 17);
+        const uint64_t qd = q0 + (deal.q_byte(item) >> 4);
+        if (elect_one()) {
+          const uint8_t* img = sm + F::QIMG_OFF + qb * F::QIMG;
+          tc_cp_img(sf, img);
+          if (WIDE && 2 * deal.nqp > 128) tc_cp_img(sf + 4, img + IMG);
         }
         __syncwarp();
-      }
-      if (elect_one()) tc_commit(&ss.q_free[qb]);
 #pragma unroll 1
-      for (int i = max(0, im.n - MMA_WARPS); i < im.n; ++i)  // all are done when each warp's last is
-        wait(&ss.pv_done[deal.slot(i)], deal.parity(ph, i), a.status, abort);
-      bar_sync<32 * MMA_WARPS>(11);  // (neither runs ahead of the phases that the other waits for)
-      it += im.n;
-      deal.advance(ph, im.n);
-    }
-    if (elect_one()) tc_commit(&ss.drain);  // (what was issued has completed at this arrival)
-    __syncwarp();
-  } else if (warp >= O_WARP && warp < O_WARP + MMA_WARPS) {
-    // ------------- the second product's MMAs: a warp issues every other tile's, so that it has its
-    // own streams' O; the first one all where there is one stream
-    const int mine = warp - O_WARP;
-    const uint64_t k0 = desc_sw128(smem_u32(sm + K_OFF)), p0 = desc_sw128(smem_u32(sm + P_OFF));
-    // first, where the second kernel finds the rows' results
-#pragma unroll 1
-    for (int r = blockIdx.x + mine * gridDim.x; r < a.rows; r += MMA_WARPS * gridDim.x) {
-      const RowInfo info = row_info(a, sh, plan, r);
-      if (lane == 0) ar.rows[r] = info;
-    }
-    int it = 0;
-    uint32_t ph = 0;
-#pragma unroll 1
-    for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
-      wait(&ss.q_full[item & 1], (item >> 1) & 1, a.status, abort);
-      const Deal deal(ss.meta[item & 1].cols);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ss.q_free[item & 1]);
-      const int step = deal.streams == 1 ? 1 : MMA_WARPS;
-      const int first = mine < step ? mine : im.n;
-      // (only where this warp has tiles: it may miss phases of other items)
-      if (item > 0 && first < im.n) wait(&ss.o_free, (item - 1) & 1, a.status, abort);
-      const uint32_t idesc = IDESC | TRANS | ((uint32_t)(2 * deal.nqp >> 3) << 17);
-#pragma unroll 1
-      for (int i = first; i < im.n; i += step) {
-        const int b = deal.slot(i), stream = deal.stream(i), st = (it + i) % ST;
-        const bool ok = wait(&ss.p_full[b], deal.parity(ph, i), a.status, abort);
-        if (ok && elect_one()) {
-          tc_fence_after();
-          const uint32_t sf = tmem + SF_P + 4 * b, ones = tmem + SF_ONE + 4 * (i & 1);
-          tc_cp_img(sf, sm + PIMG_OFF + b * IMG);
-          const uint64_t kd = k0 + st * (K_TILE / 16);
-          const uint64_t pd = p0 + ((deal.p_buf(i) + deal.p_byte(stream)) >> 4);
+        for (int i = mine; i < im.n; i += MMA_WARPS) {
+          const int st = (it + i) % ST, b = deal.slot(i);
+          bool ok = wait(&ss.full[st], ((it + i) / ST) & 1, a.status, abort);
+          // the slot's scores and weights are no longer in use
+          if (i >= deal.bufs)
+            ok &= wait(&ss.pv_done[b], deal.parity(ph, i - deal.bufs), a.status, abort);
+          if (ok && elect_one()) {
+            tc_fence_after();
+            const uint64_t kd = k0 + st * (K_TILE / 16);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)  // 32 tokens each
-            tc_mma_mxf8(tmem + deal.o_col(stream), kd + k * (4096 / 16), pd + k * (4096 / 16),
-                        idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), ones, sf,
-                        i >= deal.streams || k > 0);
-          tc_commit(&ss.pv_done[b]);
-          tc_commit(&ss.k_free[st]);
+            for (int k = 0; k < 4; ++k)
+              tc_mma_mxf8(tmem + deal.s_col(i), kd + 2 * k, qd + 2 * k,
+                          idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), ones, sf, k > 0);
+            tc_commit(&ss.s_full[b]);
+            if (WIDE) tc_commit(&ss.k_free[st]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (elect_one()) tc_commit(&ss.q_free[qb]);
+#pragma unroll 1
+        for (int i = max(0, im.n - MMA_WARPS); i < im.n; ++i)  // all are done when each warp's last is
+          wait(&ss.pv_done[deal.slot(i)], deal.parity(ph, i), a.status, abort);
+        if (MMA_WARPS > 1) bar_sync<32 * MMA_WARPS>(11);  // (neither runs ahead of the phases that the other waits for)
+        it += im.n;
+        deal.advance(ph, im.n);
       }
-      it += im.n;
-      deal.advance(ph, im.n);
+      if (elect_one()) tc_commit(&ss.drain);  // (what was issued has completed at this arrival)
+      __syncwarp();
+    } else if (warp >= O_WARP && warp < O_WARP + MMA_WARPS) {
+      // ------------- the second product's MMAs (two warps: each issues every other tile's, so that it
+      // has its own streams' O; the first one all where there is one stream)
+      const int mine = warp - O_WARP;
+      const uint64_t k0 = desc_sw128(smem_u32(sm + F::K_OFF)), v0 = desc_mn(smem_u32(sm + F::V_OFF), K_TILE);
+      // first, where the second kernel finds the rows' results
+#pragma unroll 1
+      for (int r = blockIdx.x + mine * gridDim.x; r < a.rows; r += MMA_WARPS * gridDim.x) {
+        const RowInfo info = row_info(a, sh, plan, r);
+        if (lane == 0) ar.rows[r] = info;
+      }
+      int it = 0;
+      uint32_t ph = 0;
+#pragma unroll 1
+      for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
+        wait(&ss.q_full[item & 1], (item >> 1) & 1, a.status, abort);
+        const Deal<WIDE> deal(ss.meta[item & 1].cols);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ss.m_free[item & 1]);
+        const int step = deal.streams == 1 ? 1 : MMA_WARPS;
+        const int first = mine < step ? mine : im.n;
+        // (only where this warp has tiles: it may miss phases of other items)
+        if (item > 0 && first < im.n) wait(&ss.o_free, (item - 1) & 1, a.status, abort);
+        const uint32_t idesc = WIDE ? F16_IDESC | ((uint32_t)(deal.nqp >> 3) << 17)
+                                    : IDESC | TRANS | ((uint32_t)(2 * deal.nqp >> 3) << 17);
+#pragma unroll 1
+        for (int i = first; i < im.n; i += step) {
+          const int b = deal.slot(i), stream = deal.stream(i), st = (it + i) % ST;
+          bool ok = wait(&ss.p_full[b], deal.parity(ph, i), a.status, abort);
+          if (WIDE) ok &= wait(&ss.v_full[(it + i) & 1], ((it + i) >> 1) & 1, a.status, abort);
+          if (ok && elect_one()) {
+            tc_fence_after();
+            const int odd = deal.p_odd(i);
+            const uint32_t p = smem_u32(sm + F::P_OFF) + odd * K_TILE + deal.p_byte(stream);
+            const uint32_t oc = tmem + deal.o_col(stream);
+            if constexpr (WIDE) {
+              const uint64_t vd = v0 + ((it + i) & 1) * (V_TILE / 16);
+              // (columns from 64: behind both buffers, the second one's 64 bytes further)
+              const uint64_t pd = desc_mn(p, (2 - odd) * K_TILE + 64 * odd);
+#pragma unroll
+              for (int k = 0; k < 8; ++k)  // 16 tokens each
+                tc_mma_f16(oc, vd + k * (2048 / 16), pd + k * (2048 / 16), idesc, i >= deal.streams || k > 0);
+            } else {
+              const uint32_t sf = tmem + F::SF_P + 4 * b, ones = tmem + F::SF_ONE + 4 * (i & 1);
+              tc_cp_img(sf, sm + F::PIMG_OFF + b * IMG);
+              const uint64_t kd = k0 + st * (K_TILE / 16), pd = desc_sw128(p);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)  // 32 tokens each
+                tc_mma_mxf8(oc, kd + k * (4096 / 16), pd + k * (4096 / 16),
+                            idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), ones, sf,
+                            i >= deal.streams || k > 0);
+            }
+            tc_commit(&ss.pv_done[b]);
+            tc_commit(WIDE ? &ss.v_free[(it + i) & 1] : &ss.k_free[st]);
+          }
+          __syncwarp();
+        }
+        it += im.n;
+        deal.advance(ph, im.n);
+      }
+      if (elect_one()) tc_commit(&ss.drain);
+      __syncwarp();
     }
-    if (elect_one()) tc_commit(&ss.drain);
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------------------- softmax
+    if constexpr (WIDE) regs_up<SOFT_REGS>();
     const int quad = warp & 3, group = warp >> 2;
     const int hpg = a.n_q / (a.kv_dim / a.head_dim);
     const int cheads = hpg * (chunk_bytes > a.head_dim ? 2 : 1);  // heads per row of this chunk
@@ -703,8 +901,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 #pragma unroll 1
     for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
       wait(&ss.q_full[item & 1], (item >> 1) & 1, a.status, abort);
-      const Meta& meta = ss.meta[item & 1];
-      const Deal deal(meta.cols);
+      const Meta<WIDE>& meta = ss.meta[item & 1];
+      const Deal<WIDE> deal(meta.cols);
       const int nqp = deal.nqp, nq = meta.nrows * cheads;
       const bool whole = im.n == im.span.tiles;
       w.span = im.span;
@@ -712,27 +910,21 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       w.n = im.n;
       w.first = group & (deal.streams - 1);
       w.stride = deal.streams;
-      w.c0 = (group >> deal.lg) * C;
+      const int share = WIDE && nqp > 64 ? 24 : 16;  // columns of a group
+      w.c0 = (group >> deal.lg) * share;
       w.flat = nqp * w.first + w.c0;
       w.arrive = deal.streams + (nqp == 48 && group == 0 ? 1 : 0);  // (the fourth group is idle)
-      {
-        // tiles whose tokens all rows see (those of the sinks, where there is a window, aside)
-        const int r = lane < meta.nrows ? lane : 0;
-        const int hi = a.causal ? meta.pos[r] : im.span.hi;
-        const int lo = __reduce_max_sync(0xffffffffu, a.window > 0 ? max(0, hi - a.window + 1) : 0);
-        const int end = (__reduce_min_sync(0xffffffffu, hi) + 1) / TT;  // of the tiles as tokens go
-        const int to = im.span.head - im.span.body - im.t0;  // from there to the item's
-        const int from = max((lo + TT - 1) / TT, im.span.body);
-        w.clear = lo == 0 ? -im.t0 : from + to;
-        w.clears = max(0, (lo == 0 ? end : end - from));
-      }
-      float l[C];
+      w.clear = clear_tiles(a, im, meta);
+      float l[F::CMAX];
 #pragma unroll
-      for (int c = 0; c < C; ++c) l[c] = 0.0f;
+      for (int c = 0; c < F::CMAX; ++c) l[c] = 0.0f;
       if (w.c0 < nqp) {
-        if (quad == 0 && lane < C) ss.neg_m[w.flat + lane] = -UNSET;
+        if (quad == 0 && lane < share) ss.neg_m[w.flat + lane] = -UNSET;
         bar_sync<128>(6 + group);
-        soft_tiles(a, w, deal, meta, ss, sm, l);
+        if (share == 16)
+          soft_tiles<WIDE, 16>(a, w, deal, meta, ss, sm, l);
+        else
+          soft_tiles<WIDE, F::CMAX>(a, w, deal, meta, ss, sm, l);
       }
       // every product of the item is done when each issuing warp's last is
 #pragma unroll 1
@@ -743,18 +935,14 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       deal.advance(w.ph, im.n);
 
       // ---- the item's result: the columns' sums over the tokens, then O
-      // (halving: a lane ends with column lane % 16 of both half warps)
-#pragma unroll
-      for (int x = C / 2; x > 0; x >>= 1) {
-#pragma unroll
-        for (int c = 0; c < x; ++c) {
-          const bool up = lane & x;
-          const float give = up ? l[c] : l[c + x], keep = up ? l[c + x] : l[c];
-          l[c] = keep + __shfl_xor_sync(0xffffffffu, give, x);
-        }
+      {
+        const float v = column_sums<16>(l);
+        if (lane < 16) ss.red[warp][lane] = v;
       }
-      l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
-      if (lane < C) ss.red[warp][lane] = l[0];
+      if constexpr (WIDE) {
+        const float v = column_sums<8>(l + 16);
+        if (lane < 8) ss.red[warp][16 + lane] = v;
+      }
       bar_sync<SOFT>(10);
       if (tid < nq) {
         // the streams' sums and O in the largest m (one stream: as they are)
@@ -765,8 +953,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         for (int k = 0; k < 4; ++k) {
           float f = 0.0f;
           if (k < min(deal.streams, im.n)) {
-            const int g = k + (tid / C << deal.lg), c = tid % C;
-            const float(*r)[C] = ss.red + 4 * g;
+            const int g = k + (tid / share << deal.lg), c = tid % share;
+            const float(*r)[F::CMAX] = ss.red + 4 * g;
             const float mk = -ss.neg_m[nqp * k + tid];
             const float lk = (r[0][c] + r[1][c]) + (r[2][c] + r[3][c]);
             f = lk != lk ? 1.0f : mk == UNSET ? 0.0f : ex2(mk - m);  // (a NaN stays one)
@@ -794,12 +982,12 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
         for (int k = 0; k < min(deal.streams, im.n); ++k) {
-          float x[4], y[4];
+          float x[4], y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           tc_ld4(w.tmem + deal.o_col(k) + c4, x);
-          tc_ld4(w.tmem + deal.o_col(k) + nqp + c4, y);
+          if (!WIDE) tc_ld4(w.tmem + deal.o_col(k) + nqp + c4, y);
           tc_wait_ld();
           tc_loaded4(x);
-          tc_loaded4(y);
+          if (!WIDE) tc_loaded4(y);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float f = ss.fin[k][c4 + e];
@@ -818,7 +1006,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ss.o_free), mbar_arrive(&ss.q_free[item & 1]);
+      if (lane == 0) mbar_arrive(&ss.o_free), mbar_arrive(&ss.m_free[item & 1]);
     }
   }
   tc_fence_before();
@@ -833,12 +1021,25 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 }  // namespace
 
 cudaError_t attend_tc_prepare() {
-  return cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  // the wide form's register split adds up to what a block launches with
+  cudaFuncAttributes f;
+  cudaError_t e = cudaFuncGetAttributes(&f, attend_kernel<true>);
+  if (e == cudaSuccess && f.numRegs != REGS) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(attend_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Form<true>::SMEM_BYTES);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(attend_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Form<false>::SMEM_BYTES);
+  return e;
 }
 
 cudaError_t launch_attend_tc(const Launch& L, const AttendArgs& a, const attend::Pieces& ws, int sms) {
   const int chunks = (a.kv_dim + 127) / 128;
-  Args ar = {{}, {}, 0, a, shape_of(a, TT, NQ, sms / chunks), ws.part, ws.rows, ws.total};
+  const Shape narrow = shape_of(a, TT, Form<false>::NQ, sms / chunks);
+  const bool wide = (a.rows + a.n_req - 1) / a.n_req * narrow.heads > WIDE_FROM;
+  Args ar = {{}, {}, 0, a, wide ? shape_of(a, TT, Form<true>::NQ, sms / chunks) : narrow, ws.part, ws.rows,
+             ws.total};
   // boxes of whole runs of a page, 8 rows (a swizzle atom) or more, that tiles are made of
   const int bs = a.kv.block_size;
   if (bs % 8 == 0) {
@@ -847,7 +1048,9 @@ cudaError_t launch_attend_tc(const Launch& L, const AttendArgs& a, const attend:
         encode_cache_map(&ar.scales, a.kv, a.kv_dim + 16, 16, box))
       ar.box = box;
   }
-  const cudaError_t e = launch_ex(L, dim3(sms), dim3(THREADS), SMEM_BYTES, attend_kernel, ar);
+  const cudaError_t e =
+      wide ? launch_ex(L, dim3(sms), dim3(THREADS), Form<true>::SMEM_BYTES, attend_kernel<true>, ar)
+           : launch_ex(L, dim3(sms), dim3(THREADS), Form<false>::SMEM_BYTES, attend_kernel<false>, ar);
   return e == cudaSuccess ? attend::launch_join(L, a, ar.sh, ws) : e;
 }
 
