@@ -71,21 +71,20 @@ struct Form {
   // queries: hi rows, then lo rows; [2] up to Q_TWICE columns
   static constexpr int Q_OFF = P_OFF + (WIDE ? 3 : 2) * K_TILE, Q_BYTES = 2 * NQ * 128;
   static constexpr int PIMG_OFF = Q_OFF + Q_BYTES;   // scale images of the weights [SLOTS],
-  static constexpr int QIMG = WIDE ? 2 * IMG : IMG;
   static constexpr int QIMG_OFF = PIMG_OFF + (WIDE ? 0 : SLOTS * IMG);  // of the queries [2],
-  static constexpr int ONE_OFF = QIMG_OFF + 2 * QIMG;                   // and of ones
+  static constexpr int ONE_OFF = QIMG_OFF + 2 * IMG;                   // and of ones
   static constexpr int SC_OFF = ONE_OFF + IMG;  // the 16 bytes behind the codes, scale first [ST][128]
   static constexpr int PLAN_OFF = SC_OFF + ST * TT * 16;
   static constexpr int SMEM_BYTES = PLAN_OFF + (3 * MAX_REQ + 4) * 4 + MAX_ROWS * 6 + 1024;
   static_assert(P_OFF % 1024 == 0 && Q_OFF % 1024 == 0 && Q_BYTES / 2 % 1024 == 0, "swizzle atoms");
   // TMEM columns: scores by slot, O by stream, scales (ones and the queries' per issuing warp)
-  static constexpr int S_COL = 0, O_COL = WIDE ? 384 : 256, SF_ONE = O_COL + (WIDE ? 96 : 128),
+  static constexpr int S_COL = 0, O_COL = 256, SF_ONE = O_COL + (WIDE ? 96 : 128),
                        SF_Q = SF_ONE + 4 * MMA_WARPS, SF_P = SF_Q + 8 * MMA_WARPS;
   static_assert(SF_P + (WIDE ? 0 : 4 * SLOTS) <= 512, "TMEM");
   // log2 of a weight times its token's scale: m puts the largest of the tile that moves it at BASE
   // or just below, and moves again when one passes 2^15 (narrow: 2); scales below 2^LEAST (and zeros)
   // count as that
-  static constexpr float BASE = WIDE ? 6.0f : -30.0f, LEAST = WIDE ? -90.0f : -60.0f;
+  static constexpr float BASE = WIDE ? 0.0f : -30.0f, LEAST = WIDE ? -90.0f : -60.0f;
 };
 // registers a thread in the wide form: softmax warps take what the others give up (in all, the
 // launch's)
@@ -186,7 +185,7 @@ struct Deal {
   __device__ int slot(int i) const { return i & (bufs - 1); }
   __device__ int stream(int i) const { return i & (streams - 1); }
   __device__ uint32_t s_col(int i) const {
-    return Form<WIDE>::S_COL + (WIDE && lg == 0 ? 2 * Form<WIDE>::NQ * slot(i) : slot(i) << (7 - lg));
+    return Form<WIDE>::S_COL + (slot(i) << (7 - lg));
   }
   // a stream's columns of O: both terms' of the weights in the narrow form
   __device__ uint32_t o_col(int stream) const { return Form<WIDE>::O_COL + (WIDE ? 1 : 2) * nqp * stream; }
@@ -202,32 +201,27 @@ struct Deal {
   }
 };
 
-// A maximum over the warp, every lane gets it (floats as ordered integers).
-__device__ __forceinline__ float warp_max_any(float v) {
-  int i = __float_as_int(v);
-  i = i < 0 ? i ^ 0x7FFFFFFF : i;
-  i = __reduce_max_sync(0xffffffffu, i);
-  return __int_as_float(i < 0 ? i ^ 0x7FFFFFFF : i);
-}
-
 // What the softmax needs of an item beside its span, made with the item's queries.
 template <bool WIDE>
 struct Meta {
   static constexpr int NQ = Form<WIDE>::NQ;
   int cols, nrows;
   int row[GROUP], pos[GROUP];
-  long long query[NQ], out[NQ];  // where a column's queries are, and where its first value goes
-  int slice[NQ];                 // -1: padding
+  // where a column's queries are, where its first value goes, and its slice (-1: padding)
+  long long query[NQ];
+  alignas(16) long long out[NQ];
+  alignas(16) int slice[NQ];
 };
 template <bool WIDE>
 struct Shared {
   static constexpr int NQ = Form<WIDE>::NQ, ST = Form<WIDE>::ST, CMAX = Form<WIDE>::CMAX;
   uint64_t full[ST], k_free[ST], s_full[SLOTS], p_full[SLOTS], pv_done[SLOTS], v_full[2], v_free[2];
   uint64_t q_full[2], q_free[2], m_free[2], o_free, drain;
-  float neg_m[NQ], fac[NQ], red[SOFT_WARPS][CMAX];  // m and its change: [stream][column]
+  alignas(16) float neg_m[NQ];
+  float fac[NQ], red[SOFT_WARPS][CMAX];  // m and its change: [stream][column]
   uint32_t most[SOFT_WARPS][CMAX];  // the warp's columns' largest weights
   uint32_t valid[ST][4];  // tokens that are there
-  float fin[4][NQ];       // a column's factor for each stream's O
+  alignas(16) float fin[4][NQ];  // a column's factor for each stream's O
   Meta<WIDE> meta[2];
   uint32_t tmem;
   int abort;
@@ -252,6 +246,27 @@ __device__ __forceinline__ Clear clear_tiles(const AttendArgs& a, const Job& im,
   return {from + im.span.head - im.span.body - im.t0, max(0, end - from)};
 }
 
+// Sums, or maxima, of N columns over the warp's lanes: lane k gets column k % N's.
+template <int N, bool MAX>
+__device__ __forceinline__ float over_lanes(float* l) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int x = N / 2; x > 0; x >>= 1) {
+#pragma unroll
+    for (int c = 0; c < x; ++c) {
+      const bool up = lane & x;
+      const float give = up ? l[c] : l[c + x], keep = up ? l[c + x] : l[c];
+      const float got = __shfl_xor_sync(0xffffffffu, give, x);
+      l[c] = MAX ? fmaxf(keep, got) : keep + got;
+    }
+  }
+#pragma unroll
+  for (int x = N; x < 32; x <<= 1) {
+    const float got = __shfl_xor_sync(0xffffffffu, l[0], x);
+    l[0] = MAX ? fmaxf(l[0], got) : l[0] + got;
+  }
+  return l[0];
+}
 // What a softmax warp knows of its item.
 struct Soft {
   Span span;
@@ -328,20 +343,19 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
         // the columns' largest weights times scales of the tile
 #pragma unroll 1
         for (int g = 0; g < C; g += 8) {
-          float x[8], y[8], mine = 0.0f;
+          float x[8], y[8];
           tc_ld8(scol + g, x);
-          tc_ld8(scol + deal.nqp + g, y);
+          if (!WIDE) tc_ld8(scol + deal.nqp + g, y);
           tc_wait_ld();
           tc_loaded(x);
-          tc_loaded(y);
+          if (!WIDE) tc_loaded(y);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            float v = fmaf(x[e] + y[e], ct, lsc);
-            if (!(v > -INFINITY) || !((see >> (g + e)) & 1)) v = -INFINITY;
-            const float m = warp_max_any(v);
-            if (lane == e) mine = m;
+            x[e] = fmaf(WIDE ? x[e] : x[e] + y[e], ct, lsc);
+            if (!((see >> (g + e)) & 1)) x[e] = -INFINITY;
           }
-          if (lane < 8) sh.red[warp][g + lane] = mine;
+          const float v = over_lanes<8, true>(x);
+          if (lane < 8) sh.red[warp][g + lane] = v;
         }
         bar_sync<128>(6 + group);
         if (quad == 0 && lane < C) {
@@ -379,16 +393,21 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
         }
         moved = true;
       }
+      float x[WIDE ? 1 : C];
 #pragma unroll
       for (int g = 0; g < C; g += 8) {
-        float x[8];
         tc_ld8(scol + g, s + g);
-        tc_ld8(scol + deal.nqp + g, x);
-        tc_wait_ld();
-        tc_loaded(x);
-        tc_loaded(s + g);
+        if (!WIDE) tc_ld8(scol + deal.nqp + g, x + g);
+      }
+      tc_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) add2(s[g + e], s[g + e + 1], x[e], x[e + 1]);
+      for (int g = 0; g < C; g += 8) {
+        tc_loaded(s + g);
+        if constexpr (!WIDE) {
+          tc_loaded(x + g);
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) add2(s[g + e], s[g + e + 1], x[g + e], x[g + e + 1]);
+        }
       }
       const float4* nm = reinterpret_cast<const float4*>(sh.neg_m + w.flat);
 #pragma unroll
@@ -481,24 +500,6 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
     __syncwarp();
     if (lane < w.arrive) mbar_arrive(&sh.p_full[b]);
   }
-}
-
-// Sums of N columns over the warp's lanes: lane k gets column k % N's.
-template <int N>
-__device__ __forceinline__ float column_sums(float* l) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int x = N / 2; x > 0; x >>= 1) {
-#pragma unroll
-    for (int c = 0; c < x; ++c) {
-      const bool up = lane & x;
-      const float give = up ? l[c] : l[c + x], keep = up ? l[c + x] : l[c];
-      l[c] = keep + __shfl_xor_sync(0xffffffffu, give, x);
-    }
-  }
-#pragma unroll
-  for (int x = N; x < 32; x <<= 1) l[0] += __shfl_xor_sync(0xffffffffu, l[0], x);
-  return l[0];
 }
 
 template <bool WIDE>
@@ -685,23 +686,27 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         if (item > 0 && (once || before)) wait(&ss.q_free[qb ^ 1], ((item - 1) >> 1) & 1, a.status, abort);
         before = once;
         bar_sync<PREP>(1);
-        // queries as two e4m3 terms, rows of 128 bytes: hi in row c, lo in row nqp + c; a thread
-        // takes 8 dimensions, the next ones on their way meanwhile
+        // queries as two e4m3 terms, rows of 128 bytes: hi in row c, lo in row nqp + c.  A thread takes
+        // 8 dimensions of every so-manieth column; their 16 bytes are copied to where its codes go
         const int d = (ptid & 15) * 8, sl = d >> dshift, o = d >> 4;
         const __nv_bfloat16* q = a.q + (d - (sl << dshift));
-        auto fetch = [&](int c) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (c < nq && meta.slice[c] == sl) x = __ldg(reinterpret_cast<const uint4*>(q + meta.query[c]));
-          return x;
-        };
-        uint4 next = fetch(ptid >> 4);
         uint8_t* to = sm + F::Q_OFF + (once ? 0 : qb * (F::Q_BYTES / 2)) + (d & 8);
-        uint8_t* img = sm + F::QIMG_OFF + qb * F::QIMG + (d >> 5);
+        uint8_t* img = sm + F::QIMG_OFF + qb * IMG + (d >> 5);
+        auto place = [&](int r) { return to + r * 128 + ((o ^ (r & 7)) << 4); };
 #pragma unroll 1
         for (int c = ptid >> 4; c < nqp; c += PREP / 16) {
+          const bool in = c < nq && meta.slice[c] == sl;
+          const __nv_bfloat16* from = in ? q + meta.query[c] : a.q;
+          cp_async8(place(c), from, in ? 8 : 0);
+          cp_async8(place(nqp + c), from + (in ? 4 : 0), in ? 8 : 0);
+        }
+        cp_async_wait_all();
+#pragma unroll 1
+        for (int c = ptid >> 4; c < nqp; c += PREP / 16) {
+          uint2* hi = reinterpret_cast<uint2*>(place(c));
+          uint2* lo = reinterpret_cast<uint2*>(place(nqp + c));
           float v[8];
-          bf16x8_to_f32(next, v);
-          next = fetch(c + PREP / 16);
+          bf16x8_to_f32(make_uint4(hi->x, hi->y, lo->x, lo->y), v);
           float m = 0.0f;
 #pragma unroll
           for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
@@ -719,12 +724,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           uint32_t hw[2], lw[2];
           hilo_x4(v, hw[0], lw[0]);
           hilo_x4(v + 4, hw[1], lw[1]);
-          const int rl = nqp + c;
-          *reinterpret_cast<uint2*>(to + c * 128 + ((o ^ (c & 7)) << 4)) = make_uint2(hw[0], hw[1]);
-          *reinterpret_cast<uint2*>(to + rl * 128 + ((o ^ (rl & 7)) << 4)) = make_uint2(lw[0], lw[1]);
+          *hi = make_uint2(hw[0], hw[1]);
+          *lo = make_uint2(lw[0], lw[1]);
           if ((d & 31) == 0) {
             img[(c & 31) * 16 + (c >> 5) * 4] = (uint8_t)code;
-            img[(rl >> 7) * IMG + (rl & 31) * 16 + (rl >> 5 & 3) * 4] = (uint8_t)code;
+            if (!WIDE) img[((nqp + c) & 31) * 16 + ((nqp + c) >> 5) * 4] = (uint8_t)code;
           }
         }
         fence_proxy_async_shared();
@@ -785,12 +789,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         const int qb = item & 1;
         wait(&ss.q_full[qb], (item >> 1) & 1, a.status, abort);
         const Deal<WIDE> deal(ss.meta[qb].cols);
-        const uint32_t idesc = IDESC | ((uint32_t)(2 * deal.nqp >> 3) << 17);
+        // the queries' terms: two columns of the scores each, or added up (wide)
+      const int n = WIDE ? deal.nqp : 2 * deal.nqp;
+      const uint32_t idesc = IDESC | ((uint32_t)(n >> 3) << 17);
         const uint64_t qd = q0 + (deal.q_byte(item) >> 4);
         if (elect_one()) {
-          const uint8_t* img = sm + F::QIMG_OFF + qb * F::QIMG;
+          const uint8_t* img = sm + F::QIMG_OFF + qb * IMG;
           tc_cp_img(sf, img);
-          if (WIDE && 2 * deal.nqp > 128) tc_cp_img(sf + 4, img + IMG);
         }
         __syncwarp();
 #pragma unroll 1
@@ -804,9 +809,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             tc_fence_after();
             const uint64_t kd = k0 + st * (K_TILE / 16);
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              tc_mma_mxf8(tmem + deal.s_col(i), kd + 2 * k, qd + 2 * k,
-                          idesc | ((uint32_t)k << 4) | ((uint32_t)k << 29), ones, sf, k > 0);
+            for (int k = 0; k < (WIDE ? 8 : 4); ++k)
+              tc_mma_mxf8(tmem + deal.s_col(i), kd + 2 * (k & 3), qd + 2 * (k & 3) + (k >> 2) * (n * 128 / 16),
+                          idesc | ((uint32_t)(k & 3) << 4) | ((uint32_t)(k & 3) << 29), ones, sf, k > 0);
             tc_commit(&ss.s_full[b]);
             if (WIDE) tc_commit(&ss.k_free[st]);
           }
@@ -936,42 +941,44 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 
       // ---- the item's result: the columns' sums over the tokens, then O
       {
-        const float v = column_sums<16>(l);
+        const float v = over_lanes<16, false>(l);
         if (lane < 16) ss.red[warp][lane] = v;
       }
       if constexpr (WIDE) {
-        const float v = column_sums<8>(l + 16);
+        const float v = over_lanes<8, false>(l + 16);
         if (lane < 8) ss.red[warp][16 + lane] = v;
       }
       bar_sync<SOFT>(10);
-      if (tid < nq) {
-        // the streams' sums and O in the largest m (one stream: as they are)
-        float m = UNSET, lt = 0.0f;
-#pragma unroll 1
-        for (int k = 0; k < min(deal.streams, im.n); ++k) m = fmaxf(m, -ss.neg_m[nqp * k + tid]);
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          float f = 0.0f;
-          if (k < min(deal.streams, im.n)) {
-            const int g = k + (tid / share << deal.lg), c = tid % share;
-            const float(*r)[F::CMAX] = ss.red + 4 * g;
-            const float mk = -ss.neg_m[nqp * k + tid];
-            const float lk = (r[0][c] + r[1][c]) + (r[2][c] + r[3][c]);
-            f = lk != lk ? 1.0f : mk == UNSET ? 0.0f : ex2(mk - m);  // (a NaN stays one)
-            if (f != 0.0f) lt = fmaf(lk, f, lt);
-          }
-          ss.fin[k][tid] = f;
+      if (warp < ((nq << deal.lg) + 31) / 32) {
+        // the streams' sums and O in the largest m (one stream: as they are); a lane per column and
+        // stream
+        const int c = tid >> deal.lg, k = tid & (deal.streams - 1);
+        const bool live = c < nq && k < im.n;
+        float mk = UNSET, lk = 0.0f;
+        if (live) {
+          const int g = k + (c / share << deal.lg), at = c % share;
+          const float(*r)[F::CMAX] = ss.red + 4 * g;
+          mk = -ss.neg_m[nqp * k + c];
+          lk = (r[0][at] + r[1][at]) + (r[2][at] + r[3][at]);
         }
-        const float up = !whole ? 1.0f : lt == 0.0f ? 0.0f : 1.0f / lt;
+        float m = mk;
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) ss.fin[k][tid] *= up;
-        if (whole) {
-          const int j = tid / cheads;
-          a.lse[(long long)meta.row[j] * a.n_q + chunk * sh.heads + tid - j * cheads] =
-              lt == 0.0f ? -INFINITY : (log2f(lt) + m) * LN2;
-        } else {
-          ar.part[meta.out[tid] - 4] = m;
-          ar.part[meta.out[tid] - 3] = lt;
+        for (int x = 1; x < deal.streams; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        float f = lk != lk ? 1.0f : mk == UNSET ? 0.0f : ex2(mk - m);  // (a NaN stays one)
+        float lt = f != 0.0f ? lk * f : 0.0f;
+#pragma unroll 1
+        for (int x = 1; x < deal.streams; x <<= 1) lt += __shfl_xor_sync(0xffffffffu, lt, x);
+        if (whole) f = lt == 0.0f ? 0.0f : f / lt;
+        if (live) ss.fin[k][c] = f;
+        if (live && k == 0) {
+          if (whole) {
+            const int j = c / cheads;
+            a.lse[(long long)meta.row[j] * a.n_q + chunk * sh.heads + c - j * cheads] =
+                lt == 0.0f ? -INFINITY : (log2f(lt) + m) * LN2;
+          } else {
+            ar.part[meta.out[c] - 4] = m;
+            ar.part[meta.out[c] - 3] = lt;
+          }
         }
       }
       bar_sync<SOFT>(10);
@@ -985,23 +992,30 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           float x[4], y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           tc_ld4(w.tmem + deal.o_col(k) + c4, x);
           if (!WIDE) tc_ld4(w.tmem + deal.o_col(k) + nqp + c4, y);
+          const float4 f = *reinterpret_cast<const float4*>(&ss.fin[k][c4]);
           tc_wait_ld();
           tc_loaded4(x);
           if (!WIDE) tc_loaded4(y);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float f = ss.fin[k][c4 + e];
-            if (f != 0.0f) v[e] = fmaf(x[e] + y[e], f, v[e]);
-          }
+          if (f.x != 0.0f) v[0] = fmaf(x[0] + y[0], f.x, v[0]);
+          if (f.y != 0.0f) v[1] = fmaf(x[1] + y[1], f.y, v[1]);
+          if (f.z != 0.0f) v[2] = fmaf(x[2] + y[2], f.z, v[2]);
+          if (f.w != 0.0f) v[3] = fmaf(x[3] + y[3], f.w, v[3]);
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (meta.slice[c4 + e] != sl) continue;
-          const long long at = meta.out[c4 + e] + dl;
-          if (whole)
-            a.o[at] = __float2bfloat16_rn(v[e]);
-          else
-            ar.part[at] = v[e];
+        const int4 mine = *reinterpret_cast<const int4*>(&meta.slice[c4]);
+        const longlong2 a0 = *reinterpret_cast<const longlong2*>(&meta.out[c4]);
+        const longlong2 a1 = *reinterpret_cast<const longlong2*>(&meta.out[c4 + 2]);
+        if (whole) {
+          __nv_bfloat16* to = a.o + dl;
+          if (mine.x == sl) to[a0.x] = __float2bfloat16_rn(v[0]);
+          if (mine.y == sl) to[a0.y] = __float2bfloat16_rn(v[1]);
+          if (mine.z == sl) to[a1.x] = __float2bfloat16_rn(v[2]);
+          if (mine.w == sl) to[a1.y] = __float2bfloat16_rn(v[3]);
+        } else {
+          float* to = ar.part + dl;
+          if (mine.x == sl) to[a0.x] = v[0];
+          if (mine.y == sl) to[a0.y] = v[1];
+          if (mine.z == sl) to[a1.x] = v[2];
+          if (mine.w == sl) to[a1.y] = v[3];
         }
       }
       tc_fence_before();
