@@ -36,7 +36,8 @@ struct Plan {
   int* pre;  // [n_req + 1]
   int *pmax, *pmin;
   int* pos;    // [rows] the rows' positions, -1 for those that see nothing, and
-  short* req;  // their requests; both may be null
+  short* req;  // their requests
+  short* cnt;  // [n_req] rows that see something; may be null
 };
 
 // What the rows of a request see, in tiles: [0, head) and [body, body + tiles - head).
@@ -151,7 +152,7 @@ __device__ __forceinline__ void derive_plan(const AttendArgs& a, const Shape& sh
   for (int r = tid; r < a.rows; r += NT) {
     const int p = a.positions[r], b = a.row_req[r];
     const bool live = p >= 0 && b >= 0 && b < a.n_req;
-    if (plan.pos) plan.pos[r] = live ? p : -1, plan.req[r] = (short)(live ? b : -1);
+    plan.pos[r] = live ? p : -1, plan.req[r] = (short)(live ? b : -1);
     if (p < 0) continue;
     if (b < 0 || b >= a.n_req) {
       if (blockIdx.x == 0) atomicOr(a.status, ST_UNMAPPED_PAGE);
@@ -169,6 +170,7 @@ __device__ __forceinline__ void derive_plan(const AttendArgs& a, const Shape& sh
       const int b = b0 + lane;
       const int n = b < a.n_req ? plan.pre[b + 1] : 0;
       int u = 0;
+      if (plan.cnt && b < a.n_req) plan.cnt[b] = (short)n;
       if (n > 0) {
         u = (n + sh.rows_per - 1) / sh.rows_per * span_of(a, sh, plan.pmax[b], plan.pmin[b]).tiles;
         if (plan.pmax[b] >= (long long)a.kv.max_blocks * a.kv.block_size && blockIdx.x == 0)
@@ -201,7 +203,7 @@ __device__ __forceinline__ void derive_plan(const AttendArgs& a, const Shape& sh
         w.t0 = u - w.group * tiles;
       }
       *start = w;
-      if (blockIdx.x == 0) *total = W;
+      if (blockIdx.x == 0 && total) *total = W;
     }
   }
 }
@@ -250,8 +252,9 @@ struct Pieces {
 };
 
 cudaError_t launch_join(const Launch&, const AttendArgs&, const Shape&, const Pieces&);
-// The records as a tensor map (k_attend_join.cu); false where it cannot be one.
-bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int width, int run, int box);
+// The records' codes and the 16 bytes behind them as tensor maps with boxes of whole runs of a page, 8
+// rows (a swizzle atom) or more, that tiles are made of: the box's tokens; 0 where they cannot be maps.
+int encode_cache_maps(CUtensorMap* codes, CUtensorMap* scales, const AttendArgs& a);
 
 }  // namespace attend
 
@@ -259,6 +262,6 @@ bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int width, int run, i
 cudaError_t attend_tc_prepare();
 cudaError_t launch_attend_tc(const Launch&, const AttendArgs&, const attend::Pieces&, int sms);
 cudaError_t attend_weights_prepare();
-cudaError_t launch_attend_weights(const Launch&, const AttendArgs&, const attend::Pieces&, int sms);
+cudaError_t launch_attend_weights(const Launch&, const AttendArgs&, int sms);
 
 }  // namespace mono

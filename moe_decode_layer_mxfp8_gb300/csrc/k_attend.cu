@@ -34,8 +34,7 @@
 // Every mbarrier wait is bounded; a wait that runs out is reported, and from then on every role
 // runs its loop without waiting, copying or issuing, so that the barriers among warps still
 // complete and TMEM is freed.
-#include "attend_plan.cuh"
-#include "tc_common.cuh"
+#include "attend_tc.cuh"
 
 namespace mono {
 namespace {
@@ -43,14 +42,11 @@ namespace {
 using namespace tc;
 using namespace attend;
 
-constexpr int TT = 128;        // tokens per tile
-constexpr int GROUP = 16;      // rows of a group at most
 constexpr int THREADS = 24 * 32;
 constexpr int SOFT_WARPS = 16, SOFT = SOFT_WARPS * 32, GROUPS = SOFT_WARPS / 4;
 constexpr int Q_TWICE = 32;    // items of up to so many columns have their queries made ahead
-constexpr int MAX_ROWS = 1024;
 constexpr int WIDE_FROM = 32;  // the wide form where requests have more columns on average
-constexpr int K_TILE = TT * 128, V_TILE = 2 * K_TILE, IMG = 512, SLOTS = 8;
+constexpr int V_TILE = 2 * K_TILE, SLOTS = 8;
 
 // What the two forms differ in (see the head of the file).
 template <bool WIDE>
@@ -91,10 +87,7 @@ struct Form {
 constexpr int REGS = 80, SOFT_REGS = 88, OTHER_REGS = 64;
 static_assert(SOFT_REGS * SOFT + OTHER_REGS * (THREADS - SOFT) == REGS * THREADS, "register split");
 
-// Instruction descriptors, M = 128; N, and the scale-byte selectors, are or-ed in.
-// kind::mxf8f6f4: e4m3 x e4m3, E8M0 scales, K-major, or (TRANS) MN-major.
-constexpr uint32_t IDESC = (1u << 23) | ((uint32_t)(TT >> 4) << 24);
-constexpr uint32_t TRANS = (1u << 15) | (1u << 16);
+// Instruction descriptor, M = 128; N is or-ed in.
 // kind::f16: f16 x f16, f32 accumulators, both MN-major.
 constexpr uint32_t F16_IDESC = (1u << 4) | TRANS | ((uint32_t)(TT >> 4) << 24);
 
@@ -108,23 +101,6 @@ struct Args {
   int* total;
 };
 
-// Two f32 as f16, the first in the low half.
-__device__ __forceinline__ uint32_t f16x2_of(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// Four values, as two pairs of f16, as a word of e4m3 codes and one of the codes of what is left.
-__device__ __forceinline__ void hilo_x4(const float* v, uint32_t& hi, uint32_t& lo) {
-  asm("{\n .reg .b16 h0, h1, l0, l1;\n .reg .b32 f0, f1;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 h0, %2;\n cvt.rn.satfinite.e4m3x2.f16x2 h1, %3;\n"
-      " cvt.rn.f16x2.e4m3x2 f0, h0;\n cvt.rn.f16x2.e4m3x2 f1, h1;\n"
-      " sub.rn.f16x2 f0, %2, f0;\n sub.rn.f16x2 f1, %3, f1;\n"
-      " cvt.rn.satfinite.e4m3x2.f16x2 l0, f0;\n cvt.rn.satfinite.e4m3x2.f16x2 l1, f1;\n"
-      " mov.b32 %0, {h0, h1};\n mov.b32 %1, {l0, l1};\n}"
-      : "=r"(hi), "=r"(lo)
-      : "r"(f16x2_of(v[0], v[1])), "r"(f16x2_of(v[2], v[3])));
-}
 // Matrix descriptor as desc_sw128, MN-major with `lbo` bytes between 128-byte runs along MN.
 __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo) {
   return (desc_sw128(saddr) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(lbo >> 4) << 16);
@@ -144,37 +120,6 @@ __device__ __forceinline__ void regs_up() {
 template <int REGS>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
-}
-template <int N>
-__device__ __forceinline__ void bar_sync(int id) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(N) : "memory");
-}
-// Barrier among 128 threads that also tells whether any of them brought a true value.
-__device__ __forceinline__ bool bar_any(int id, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, 128, p;\n"
-      " selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(r)
-      : "r"((uint32_t)v), "r"(id)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// A wait for an mbarrier phase by a whole warp, in few instructions: some 10^7 polls (a good part
-// of a second) at most, none once another wait has run out.  False if it ran out.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
-  uint32_t polls = 0;
-#pragma unroll 1
-  while (!mbar_try_wait(bar, parity)) {
-    if (*abort || ++polls == (1u << 23)) {
-      atomicOr(status, ST_WAIT_TIMEOUT);
-      *abort = 1;
-      polls = ~0u;
-      break;
-    }
-  }
-  return __all_sync(0xffffffffu, polls != ~0u);
 }
 // How an item's columns are dealt out (see the head of the file).
 template <bool WIDE>
@@ -229,22 +174,6 @@ struct Shared {
 };
 static_assert(Form<false>::SMEM_BYTES + sizeof(Shared<false>) <= 227 * 1024, "shared memory");
 static_assert(Form<true>::SMEM_BYTES + sizeof(Shared<true>) <= 227 * 1024, "shared memory");
-
-// The tiles [first, first + n) of an item that all its rows see whole (those of the sinks aside, where
-// there is a window); by a whole warp.
-struct Clear {
-  int first, n;
-  __device__ bool has(int i) const { return (uint32_t)(i - first) < (uint32_t)n; }
-};
-template <class M>
-__device__ __forceinline__ Clear clear_tiles(const AttendArgs& a, const Job& im, const M& meta) {
-  const int lane = threadIdx.x & 31, hi = a.causal ? meta.pos[lane < meta.nrows ? lane : 0] : im.span.hi;
-  const int lo = __reduce_max_sync(0xffffffffu, a.window > 0 ? max(0, hi - a.window + 1) : 0);
-  const int end = (__reduce_min_sync(0xffffffffu, hi) + 1) / TT;  // in tiles as tokens go
-  if (lo == 0) return {-im.t0, max(0, end)};
-  const int from = max((lo + TT - 1) / TT, im.span.body);
-  return {from + im.span.head - im.span.body - im.t0, max(0, end - from)};
-}
 
 // Sums, or maxima, of N columns over the warp's lanes: lane k gets column k % N's.
 template <int N, bool MAX>
@@ -520,6 +449,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   plan.pmin = plan.pmax + MAX_REQ;
   plan.pos = plan.pmin + MAX_REQ;
   plan.req = reinterpret_cast<short*>(plan.pos + MAX_ROWS);
+  plan.cnt = nullptr;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Shape& sh = ar.sh;
   const int team = blockIdx.x / sh.chunks, chunk = blockIdx.x - team * sh.chunks;
@@ -546,9 +476,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   if (warp == S_WARP) tmem_alloc<512>(&ss.tmem);
   for (int i = tid; i < (F::SC_OFF - F::PIMG_OFF) / 4; i += THREADS)
     reinterpret_cast<uint32_t*>(sm + F::PIMG_OFF)[i] = 0x7F7F7F7Fu;
-  if (!ar.box && chunk_bytes < 128)  // (the bytes that nothing else writes)
-    for (int i = tid; i < ST * K_TILE / 16; i += THREADS)
-      *reinterpret_cast<uint4*>(sm + F::K_OFF + 16 * i) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_shared();
 
   derive_plan<THREADS>(a, sh, plan, team, team < sh.teams, &ss.start, ar.total);
@@ -565,33 +492,11 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       // ------------------------------------------------------- loads: a warp takes every other tile
       int ni = warp - LOAD_WARP;
       bool more = next_job(a, sh, plan, items, im);
-      // a lane per box of the next tile (of a token each without maps, four times): its page, on its
-      // way while the tile before is loaded, and its first token's place in it
-      const int box = ar.box ? ar.box : 1, bs = a.kv.block_size;
-      const int shift = __ffs(box) - 1, boxes = TT >> shift;
-      int page[4], row[4], t0 = 0;
+      TileLoader tile(ar.box);
       auto locate = [&]() {
 #pragma unroll 1
         while (more && ni >= im.n) ni -= im.n, more = next_job(a, sh, plan, items, im);
-        if (!more) return;
-        t0 = im.span.token(im.t0 + ni);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (32 * q >= boxes) break;
-          const int t = t0 + ((32 * q + lane) << shift), lb = t / bs;
-          page[q] = -1;
-          row[q] = t - lb * bs;
-          if (32 * q + lane < boxes && lb < a.kv.max_blocks && t <= im.span.hi &&
-              (t + box > im.span.lo || t < a.sinks))
-            page[q] = __ldg(a.kv.table + (size_t)im.b * a.kv.max_blocks + lb);
-          else
-            row[q] = -1;
-        }
-      };
-      auto mapped = [&](int q) {
-        const bool m = page[q] >= 0 && page[q] < a.kv.num_blocks;
-        if (row[q] >= 0 && !m) atomicOr(a.status, ST_UNMAPPED_PAGE);
-        return m;
+        if (more) tile.locate(a, im, ni);
       };
       locate();
 #pragma unroll 1
@@ -599,56 +504,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         const int s = it % ST;
         bool go = true;
         if (it >= ST) go = wait(&ss.k_free[s], ((it / ST) - 1) & 1, a.status, abort);
-        uint8_t* st = sm + F::K_OFF + s * K_TILE;
-        uint8_t* sc = sm + F::SC_OFF + s * TT * 16;
-        if (ar.box) {
-          // boxes with a token to see; their other tokens, and what the rest of the slot holds, are
-          // masked
-          const bool m = mapped(0);
-          if (m && go) {
-            tma_load_3d(st + ((lane * 128) << shift), &ar.codes, 128 * chunk, row[0], page[0], &ss.full[s]);
-            tma_load_3d(sc + ((lane * 16) << shift), &ar.scales, a.kv_dim, row[0], page[0], &ss.full[s]);
-          }
-          const uint32_t have = __ballot_sync(0xffffffffu, m);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int t = t0 + 32 * q + lane;
-            const bool see = ((have >> ((32 * q + lane) >> shift)) & 1) && t <= im.span.hi &&
-                             (t >= im.span.lo || t < a.sinks);
-            const uint32_t w = __ballot_sync(0xffffffffu, see);
-            if (lane == q) ss.valid[s][q] = w;
-          }
-          __syncwarp();
-          // (bytes that land before they are expected wait for this arrival all the same)
-          if (lane == 0) mbar_arrive_expect_tx(&ss.full[s], go ? __popc(have) * box * (128 + 16) : 0);
-          __syncwarp();
-        } else {
-          const int piece = lane & 7;
-          const bool in_chunk = go && 16 * piece < chunk_bytes;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            const int pg = q == 0 ? page[0] : q == 1 ? page[1] : q == 2 ? page[2] : page[3];
-            const int rw = q == 0 ? row[0] : q == 1 ? row[1] : q == 2 ? row[2] : row[3];
-            const bool m = pg >= 0 && pg < a.kv.num_blocks;
-            if (rw >= 0 && !m) atomicOr(a.status, ST_UNMAPPED_PAGE);
-            const long long off = m ? pg * a.kv.stride_block + rw * a.kv.stride_tok : 0;
-            const uint32_t w = __ballot_sync(0xffffffffu, m);
-            if (lane == 0) ss.valid[s][q] = w;
-#pragma unroll 1
-            for (int e = 0; e < 8; ++e) {
-              const int k = 4 * e + (lane >> 3), r = 32 * q + k;
-              const long long ro = __shfl_sync(0xffffffffu, off, k);
-              if (in_chunk && ((w >> k) & 1))
-                cp_async16(st + r * 128 + ((piece ^ (r & 7)) << 4), a.kv.base + ro + 128 * chunk + 16 * piece,
-                           16);
-            }
-            if (go && m) cp_async16(sc + (32 * q + lane) * 16, a.kv.base + off + a.kv_dim, 16);
-          }
-          cp_async_wait_all();
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ss.full[s]);
-        }
+        tile.load(a, im, ar.codes, ar.scales, chunk, sm + F::K_OFF + s * K_TILE, sm + F::SC_OFF + s * TT * 16,
+                  ss.valid[s], &ss.full[s], go);
         ni += LOAD_WARPS;
         locate();
       }
@@ -705,27 +562,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         for (int c = ptid >> 4; c < nqp; c += PREP / 16) {
           uint2* hi = reinterpret_cast<uint2*>(place(c));
           uint2* lo = reinterpret_cast<uint2*>(place(nqp + c));
-          float v[8];
-          bf16x8_to_f32(make_uint4(hi->x, hi->y, lo->x, lo->y), v);
-          float m = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          if (__builtin_expect(isinf(m), 0)) {  // (the codes have no infinity)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (isinf(v[e])) v[e] = __int_as_float(0x7FC00000);
-          }
-          const uint32_t code = e4m3_block_code(m);
-          const float inv = e8m0_inverse(code);
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) mul2(v[e], v[e + 1], inv);
-          uint32_t hw[2], lw[2];
-          hilo_x4(v, hw[0], lw[0]);
-          hilo_x4(v + 4, hw[1], lw[1]);
-          *hi = make_uint2(hw[0], hw[1]);
-          *lo = make_uint2(lw[0], lw[1]);
+          const uint32_t code = split_query(make_uint4(hi->x, hi->y, lo->x, lo->y), *hi, *lo);
           if ((d & 31) == 0) {
             img[(c & 31) * 16 + (c >> 5) * 4] = (uint8_t)code;
             if (!WIDE) img[((nqp + c) & 31) * 16 + ((nqp + c) >> 5) * 4] = (uint8_t)code;
@@ -1054,14 +891,7 @@ cudaError_t launch_attend_tc(const Launch& L, const AttendArgs& a, const attend:
   const bool wide = (a.rows + a.n_req - 1) / a.n_req * narrow.heads > WIDE_FROM;
   Args ar = {{}, {}, 0, a, wide ? shape_of(a, TT, Form<true>::NQ, sms / chunks) : narrow, ws.part, ws.rows,
              ws.total};
-  // boxes of whole runs of a page, 8 rows (a swizzle atom) or more, that tiles are made of
-  const int bs = a.kv.block_size;
-  if (bs % 8 == 0) {
-    const int box = std::min(bs & -bs, TT);
-    if (encode_cache_map(&ar.codes, a.kv, a.kv_dim, 128, box) &&
-        encode_cache_map(&ar.scales, a.kv, a.kv_dim + 16, 16, box))
-      ar.box = box;
-  }
+  ar.box = encode_cache_maps(&ar.codes, &ar.scales, a);
   const cudaError_t e =
       wide ? launch_ex(L, dim3(sms), dim3(THREADS), Form<true>::SMEM_BYTES, attend_kernel<true>, ar)
            : launch_ex(L, dim3(sms), dim3(THREADS), Form<false>::SMEM_BYTES, attend_kernel<false>, ar);

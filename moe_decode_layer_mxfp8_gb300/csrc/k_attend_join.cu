@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attend_join_kernel(const Atte
 
 // The records as a 3D byte tensor [pages][tokens][width], boxes of run (128: swizzled, bytes beyond
 // width read as 0) x box tokens; false where its strides are beyond a tensor map's.
-bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int width, int run, int box) {
+static bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int width, int run, int box) {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -93,6 +93,15 @@ bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int width, int run, i
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+int encode_cache_maps(CUtensorMap* codes, CUtensorMap* scales, const AttendArgs& a) {
+  const int bs = a.kv.block_size;
+  if (bs % 8) return 0;
+  const int box = std::min(bs & -bs, 128);
+  return encode_cache_map(codes, a.kv, a.kv_dim, 128, box) &&
+                 encode_cache_map(scales, a.kv, a.kv_dim + 16, 16, box)
+             ? box
+             : 0;
+}
 
 cudaError_t launch_join(const Launch& L, const AttendArgs& a, const Shape& sh, const Pieces& ws) {
   return launch_ex(L, dim3(a.rows, (a.n_q + JOIN_WARPS - 1) / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0,
@@ -129,7 +138,7 @@ cudaError_t launch_attend(const Launch& L, const AttendArgs& a, uint8_t* base, i
                              reinterpret_cast<attend::RowInfo*>(base + l.rows),
                              reinterpret_cast<int*>(base + l.total)};
   cudaError_t e = launch_attend_tc(L, a, ws, sms);
-  if (e == cudaSuccess && a.weights) e = launch_attend_weights(L, a, ws, sms);
+  if (e == cudaSuccess && a.weights) e = launch_attend_weights(L, a, sms);
   return e;
 }
 
