@@ -119,6 +119,31 @@ struct Vec {
     if (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(h));
     return __uint_as_float((uint32_t)h << 16);
   }
+  // The largest of the elements from v0 on that lie in [0, V), a NaN as -infinity.
+  __device__ float largest(int v0, int V) const {
+    float m;
+    if (v0 < 0 || v0 + VEC > V) {
+      m = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        if (v0 + e >= 0 && v0 + e < V) m = fmaxf(m, (*this)[e]);
+    } else if (sizeof(T) == 4) {
+      m = fmaxf(fmaxf((*this)[0], (*this)[1]), fmaxf((*this)[2], (*this)[3]));
+    } else {
+      Vec w = *this;
+      w.x.x = max2(max2(x.x, x.y), max2(x.z, x.w));
+      m = fmaxf(w[0], w[1]);
+    }
+    return m == m ? m : -INFINITY;
+  }
+  __device__ static uint32_t max2(uint32_t a, uint32_t b) {  // (a NaN loses)
+    uint32_t r;
+    if (std::is_same<T, __half>::value)
+      asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
 };
 // Elements outside [0, V) are 0.
 template <class T>
@@ -241,23 +266,30 @@ __global__ void __launch_bounds__(THREADS, 4) verify_kernel(VerifyArgs a, int cs
       const Draw<T> d(p, nullptr, V, -1);
       const int nv = (d.vectors() + runs - 1) / runs, first = run * nv;
       const int last = min(first + nv, d.vectors());
-      float top = 0.0f;
+      // a lane's first largest vector, kept as it was loaded
+      constexpr int U = 4;  // (loaded at a time)
+      float top = -INFINITY;
       int at = -1;
+      Vec<T> kept = {};
 #pragma unroll 1
-      for (int k0 = first + lane; k0 < last; k0 += 32 * 2) {
-        Vec<T> f[2];
+      for (int k0 = first + lane; k0 < last; k0 += 32 * U) {
+        Vec<T> f[U];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < U; ++u)
           if (k0 + 32 * u < last) f[u] = load_vec(p, (k0 + 32 * u) * VEC - d.lead, V, true);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int v0 = (k0 + 32 * u) * VEC - d.lead;
+        for (int u = 0; u < U; ++u) {
           if (k0 + 32 * u >= last) break;
+          const float m = f[u].largest((k0 + 32 * u) * VEC - d.lead, V);
+          if (at < 0 || m > top) top = m, at = k0 + 32 * u, kept = f[u];
+        }
+      }
+      const int v0 = at * VEC - d.lead;
+      if (at >= 0) {
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {  // (in a lane indices rise)
-            const float y = f[u][e], x = y == y ? y : -INFINITY;
-            if (v0 + e >= 0 && v0 + e < V && (at < 0 || x > top)) top = x, at = v0 + e;
-          }
+        for (int e = VEC - 1; e >= 0; --e) {
+          const float y = kept[e];
+          if (v0 + e >= 0 && v0 + e < V && ((y != y && top == -INFINITY) || y == top)) at = v0 + e;
         }
       }
       uint64_t best = at >= 0 ? arg_key(top, at) : 0;
@@ -340,10 +372,15 @@ __global__ void __launch_bounds__(THREADS, 4) verify_kernel(VerifyArgs a, int cs
             if (i + u < q + per && k < last) {
               float w[VEC], err[VEC];
               d.weights(fa[u], fb[u], k * VEC - d.lead, w, err);
+              if (sizeof(T) == 4) {
 #pragma unroll
-              for (int e = 0; e < VEC; e += 2) {
-                sum.add(w[e], w[e + 1]);
-                if (sizeof(T) == 4) sum.error(err[e], err[e + 1]);
+                for (int e = 0; e < VEC; e += 2) sum.add(w[e], w[e + 1]), sum.error(err[e], err[e + 1]);
+              } else {
+                // four 16-bit numbers' sum in f32 is exact while they lie within 13 binades, and else
+                // off by 2^-24 of itself: nothing that moves a draw among 10^5 tokens
+#pragma unroll
+                for (int e = 2; e < VEC; e += 2) add2(w[0], w[1], w[e], w[e + 1]);
+                sum.add(w[0], w[1]);
               }
             }
           }
