@@ -10,9 +10,9 @@
 // their sums through distributed shared memory, and the one warp whose run holds the threshold
 // finds the block and reads it again, in order.  A request whose residual is empty takes a second
 // pass over p.
-// The tests multiply two f32 in f64 (exact).  Sums decide which token is drawn, so they are
-// carried as pairs of f32 (error-free additions, and p - q as a pair): FP64 adds run at a 64th of
-// the FP32 rate here, and a search in f64 took 40 us of a CTA's 45.
+// Sums decide which token is drawn, so they are carried as pairs of f32 (error-free additions and
+// products, and p - q as a pair): FP64 runs at a 64th of the FP32 rate here, and a search in f64 took
+// 40 us of a CTA's 45.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -24,7 +24,7 @@ namespace {
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int MAX_CS = 16;
-constexpr int BLOCKS = 32;  // of a warp's run
+constexpr int BLOCKS = 8;  // of a warp's run
 
 __device__ __forceinline__ float as_f32(float v) { return v; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -34,7 +34,12 @@ __device__ __forceinline__ float positive(float v) { return v > 0.0f ? v : 0.0f;
 // A number as h + l, |l| at most half a unit of h's last place.
 struct Pair {
   float h = 0.0f, l = 0.0f;
-  __device__ double value() const { return (double)h + (double)l; }
+  __device__ Pair operator-() const {
+    Pair r;
+    r.h = -h, r.l = -l;
+    return r;
+  }
+  __device__ bool operator<=(Pair b) const { return h < b.h || (h == b.h && l <= b.l); }
 };
 __device__ __forceinline__ Pair operator+(Pair a, Pair b) {
   const float s = a.h + b.h, v = s - a.h;
@@ -42,6 +47,19 @@ __device__ __forceinline__ Pair operator+(Pair a, Pair b) {
   Pair r;
   r.h = s + e;
   r.l = e - (r.h - s);
+  return r;
+}
+__device__ __forceinline__ Pair operator*(float r, Pair a) {
+  const float s = r * a.h, e = fmaf(r, a.h, -s) + r * a.l;
+  Pair p;
+  p.h = s + e;
+  p.l = e - (p.h - s);
+  return p;
+}
+__device__ __forceinline__ Pair shfl(Pair a, int from) {
+  Pair r;
+  r.h = __shfl_sync(0xffffffffu, a.h, from);
+  r.l = __shfl_sync(0xffffffffu, a.l, from);
   return r;
 }
 __device__ __forceinline__ Pair shfl_xor(Pair a, int o) {
@@ -214,11 +232,17 @@ struct Draw {  // what a token is drawn from
   }
 };
 
+// x y < z, exactly.
+__device__ __forceinline__ bool product_below(float x, float y, float z) {
+  const float s = x * y;
+  if (!(s > 1.0e-30f && s < 1.0e30f)) return (double)x * (double)y < (double)z;
+  return s < z || (s == z && fmaf(x, y, -s) < 0.0f);
+}
 // The last lane of those below n whose weight is positive and whose prefix is at most x.
-__device__ __forceinline__ int lane_of(Pair before, Pair own, int n, double x) {
+__device__ __forceinline__ int lane_of(Pair before, Pair own, int n, Pair x) {
   const int lane = threadIdx.x & 31;
   const bool some = lane < n && own.h > 0.0f;
-  const uint32_t below = __ballot_sync(0xffffffffu, some && before.value() <= x);
+  const uint32_t below = __ballot_sync(0xffffffffu, some && before <= x);
   const uint32_t any = __ballot_sync(0xffffffffu, some);
   return below ? 31 - __clz(below) : __ffs(any) - 1;
 }
@@ -240,7 +264,8 @@ __device__ __forceinline__ uint64_t arg_key(float v, int i) {
 template <class T>
 __global__ void __launch_bounds__(THREADS, 4) verify_kernel(VerifyArgs a, int cs) {
   constexpr int VEC = 16 / sizeof(T);
-  __shared__ Pair s_block[WARPS][BLOCKS], s_warp[WARPS], s_cta[2];  // sums (the CTA's: two passes)
+  // sums: of the lanes' shares of blocks, of warps' runs, of the CTA's (for two passes)
+  __shared__ Pair s_block[WARPS][BLOCKS][32], s_warp[WARPS], s_cta[2];
   __shared__ uint64_t s_best[2][WARPS + 1];   // first maxima, by the row's parity
   __shared__ int s_row, s_tok;
   pdl_trigger();
@@ -325,7 +350,7 @@ __global__ void __launch_bounds__(THREADS, 4) verify_kernel(VerifyArgs a, int cs
           if (x >= 0 && x < V) {
             const float px = positive(as_f32(tp[(long long)k * a.target_stride + x]));
             const float qx = dp ? positive(as_f32(dp[(long long)k * a.draft_stride + x])) : 1.0f;
-            falls = !((double)a.u[k] * (double)qx < (double)px);
+            falls = !product_below(a.u[k], qx, px);
           }
         }
         const uint32_t m = __ballot_sync(0xffffffffu, falls);
@@ -341,7 +366,7 @@ __global__ void __launch_bounds__(THREADS, 4) verify_kernel(VerifyArgs a, int cs
     const T* p = tp + (long long)j * a.target_stride;
     const int x = a.draft_tokens[j];
     // (in [0, 1), whatever comes)
-    const double r = fmin(fmax((double)a.r[b], 0.0), 1.0 - 1.0 / 16777216.0);
+    const float r = fminf(fmaxf(a.r[b], 0.0f), 1.0f - 1.0f / 16777216.0f);
     int pass = j == r1 - 1 ? 1 : 0;  // 0: the residual, 1: the row itself
 #pragma unroll 1
     for (;; ++pass) {
@@ -385,12 +410,12 @@ __global__ void __launch_bounds__(THREADS, 4) verify_kernel(VerifyArgs a, int cs
             }
           }
         }
-        Pair t = sum.pair();
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t = t + shfl_xor(t, o);
-        if (lane == 0) s_block[warp][blk] = t;
+        const Pair t = sum.pair();
+        s_block[warp][blk][lane] = t;
         mine = mine + t;
       }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mine = mine + shfl_xor(mine, o);
       if (lane == 0) s_warp[warp] = mine;
       __syncthreads();
       Pair own = lane < WARPS ? s_warp[lane] : Pair(), incl = warp_scan(own);
@@ -404,34 +429,47 @@ __global__ void __launch_bounds__(THREADS, 4) verify_kernel(VerifyArgs a, int cs
         cta.l = __uint_as_float((uint32_t)(v >> 32));
       }
       const Pair to = warp_scan(cta);
-      const double total = __shfl_sync(0xffffffffu, to.value(), 31);
-      const bool sound = total > 0.0 && total < 1.0e300;  // (else there is nothing to draw from)
+      const Pair total = shfl(to, 31);
+      const bool sound = total.h > 0.0f && total.h <= 3.4e38f;  // (else there is nothing to draw from)
       if (!sound && pass == 0) continue;
-      const double want = r * total;
+      const Pair want = r * total;
       const int owner = sound ? lane_of(shfl_before(to), cta, cs, want) : 0;
       writer = owner == rank;
       if (tid == 0) s_tok = -1;
       __syncthreads();
       if (sound && writer) {
-        const double in_cta = want - __shfl_sync(0xffffffffu, shfl_before(to).value(), owner);
+        const Pair in_cta = want + -shfl(shfl_before(to), owner);
         const Pair before = shfl_before(incl);
         const int w = lane_of(before, own, WARPS, in_cta);
         if (warp == w) {
-          const double in_warp = in_cta - __shfl_sync(0xffffffffu, before.value(), w);
-          own = lane < blk ? s_block[warp][lane] : Pair();
+          const Pair in_warp = in_cta + -shfl(before, w);
+          // the blocks' sums, four lanes each, then a lane each
+          static_assert(BLOCKS * 4 == 32, "a quarter of a block's lanes per lane");
+          own = Pair();
+          if (lane / 4 < blk)
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) own = own + s_block[warp][lane / 4][(lane & 3) * 8 + i];
+          own = own + shfl_xor(own, 1);
+          own = own + shfl_xor(own, 2);
+          own = shfl(own, lane * 4 & 31);
+          if (lane >= blk) own = Pair();
           const Pair b0 = shfl_before(warp_scan(own));
           const int bl = lane_of(b0, own, blk, in_warp);
-          double goal = in_warp - __shfl_sync(0xffffffffu, b0.value(), bl);
-          int found = -1, fallback = -1;
-#pragma unroll 1
-          for (int i = bl * per; i < min((bl + 1) * per, rounds) && found < 0; ++i) {  // in order
-            const int k = first + i * 32 + lane, v0 = k * VEC - d.lead;
+          Pair goal = in_warp + -shfl(b0, bl);
+          // the round that passes the goal, in order; or else (should roundings leave the sum at the
+          // threshold) the block's last with a weight
+          int at = -1, i = bl * per;
+          bool found = false;
+          const int end = min((bl + 1) * per, rounds);
+          Pair incl_run;
+          float wt[VEC], err[VEC];
+          auto weigh = [&](int i) {
+            const int k = first + i * 32 + lane;
             Vec<T> fa, fb;
-            float wt[VEC], err[VEC];
             Sum2 sum;
-            if (k < last) d.load(k, fa, fb);
             if (k < last) {
-              d.weights(fa, fb, v0, wt, err);
+              d.load(k, fa, fb);
+              d.weights(fa, fb, k * VEC - d.lead, wt, err);
             } else {
 #pragma unroll
               for (int e = 0; e < VEC; ++e) wt[e] = err[e] = 0.0f;
@@ -441,29 +479,45 @@ __global__ void __launch_bounds__(THREADS, 4) verify_kernel(VerifyArgs a, int cs
               sum.add(wt[e], wt[e + 1]);
               if (sizeof(T) == 4) sum.error(err[e], err[e + 1]);
             }
-            const Pair own_sum = sum.pair();
-            const float own_w = own_sum.h;
-            const Pair run_incl = warp_scan(own_sum);
-            // the first lane that passes the goal looks for the element
-            const uint32_t m = __ballot_sync(0xffffffffu, own_w > 0.0f && run_incl.value() > goal);
-            const uint32_t n = __ballot_sync(0xffffffffu, own_w > 0.0f);
-            const int pick = m ? __ffs(m) - 1 : n ? 31 - __clz(n) : -1;
-            if (pick >= 0) {
-              double at = shfl_before(run_incl).value();
-              int hit = -1;
-#pragma unroll
-              for (int e = 0; e < VEC; ++e) {
-                if (wt[e] > 0.0f && at <= goal) hit = v0 + e;  // the last that begins by the goal
-                at += sizeof(T) == 4 ? (double)wt[e] + (double)err[e] : (double)wt[e];
-              }
-              hit = __shfl_sync(0xffffffffu, hit, pick);
-              if (m) found = hit;
-              fallback = hit;
+            return sum.pair();
+          };
+          int pick = -1;
+#pragma unroll 1
+          for (bool again = false;;) {
+            const Pair share = weigh(i);
+            incl_run = warp_scan(share);
+            const uint32_t some = __ballot_sync(0xffffffffu, share.h > 0.0f);
+            const uint32_t past = __ballot_sync(0xffffffffu, share.h > 0.0f && !(incl_run <= goal));
+            if (again) {
+              pick = some ? 31 - __clz(some) : -1;
+              break;
             }
-            goal -= __shfl_sync(0xffffffffu, run_incl.value(), 31);
+            if (past) {
+              found = true;
+              pick = __ffs(past) - 1;
+              break;
+            }
+            if (some) at = i;
+            if (++i < end) {
+              goal = goal + -shfl(incl_run, 31);
+              continue;
+            }
+            if (at < 0) break;
+            again = true;
+            i = at;
           }
-          // (the block's last weight, should roundings leave the sum at the threshold)
-          if (lane == 0) s_tok = found >= 0 ? found : fallback;
+          // the last element that begins by the goal (of all, without one)
+          Pair begin = shfl_before(incl_run);
+          int hit = -1;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            if (wt[e] > 0.0f && (!found || begin <= goal)) hit = (first + i * 32 + lane) * VEC - d.lead + e;
+            Pair x;
+            x.h = wt[e], x.l = sizeof(T) == 4 ? err[e] : 0.0f;
+            begin = begin + x;
+          }
+          hit = __shfl_sync(0xffffffffu, hit, max(pick, 0));
+          if (lane == 0) s_tok = pick >= 0 ? hit : -1;
         }
       }
       __syncthreads();
