@@ -262,7 +262,7 @@ __device__ __forceinline__ uint64_t arg_key(float v, int i) {
 }
 
 template <class T>
-__global__ void __launch_bounds__(THREADS, 4) verify_kernel(VerifyArgs a, int cs) {
+__global__ void __launch_bounds__(THREADS, 3) verify_kernel(VerifyArgs a, int cs) {
   constexpr int VEC = 16 / sizeof(T);
   // sums: of the lanes' shares of blocks, of warps' runs, of the CTA's (for two passes)
   __shared__ Pair s_block[WARPS][BLOCKS][32], s_warp[WARPS], s_cta[2];
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(THREADS, 4) verify_kernel(VerifyArgs a, int cs
       const int nv = (d.vectors() + runs - 1) / runs, first = run * nv;
       const int last = min(first + nv, d.vectors());
       // a lane's first largest vector, kept as it was loaded
-      constexpr int U = 4;  // (loaded at a time)
+      constexpr int U = 8;  // (loaded at a time)
       float top = -INFINITY;
       int at = -1;
       Vec<T> kept = {};
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(THREADS, 4) verify_kernel(VerifyArgs a, int cs
       const int nv = (d.vectors() + runs - 1) / runs, first = run * nv;
       const int last = min(first + nv, d.vectors());
       // rounds of a vector per lane, `per` of them a block
-      constexpr int U = 4;  // (loaded at a time)
+      constexpr int U = sizeof(T) == 4 ? 2 : 4;  // (loaded at a time)
       const int rounds = max(1, (last - first + 31) / 32);
       const int per = ((rounds + BLOCKS - 1) / BLOCKS + U - 1) / U * U;
       Pair mine;
@@ -536,10 +536,10 @@ __global__ void __launch_bounds__(THREADS, 4) verify_kernel(VerifyArgs a, int cs
 
 template <class T>
 cudaError_t launch(const Launch& L, const VerifyArgs& a, int sms) {
-  // as many CTAs a request as give the GPU four each, at least one vector a lane
+  // as many CTAs a request as give the GPU three each, at least one vector a lane
   int cs = 1;
   const int vectors = (a.vocab + Row<T>::VEC - 1) / Row<T>::VEC;
-  while (cs < MAX_CS && (long long)a.n_req * cs * 2 <= 4 * sms && cs * 2 * THREADS <= vectors) cs *= 2;
+  while (cs < MAX_CS && (long long)a.n_req * cs * 2 <= 3 * sms && cs * 2 * THREADS <= vectors) cs *= 2;
   cudaError_t e = cudaSuccess;
   if (cs > 8) e = cudaFuncSetAttribute(verify_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
