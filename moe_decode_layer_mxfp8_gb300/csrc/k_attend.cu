@@ -34,6 +34,8 @@
 // Every mbarrier wait is bounded; a wait that runs out is reported, and from then on every role
 // runs its loop without waiting, copying or issuing, so that the barriers among warps still
 // complete and TMEM is freed.
+#include <type_traits>
+
 #include "attend_tc.cuh"
 
 namespace mono {
@@ -486,12 +488,72 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   Jobs items = ss.start;
   Job im;
 
+  // An item's rows and queries, by N threads (t: 0..N - 1, whole warps); before: the last item's one
+  // buffer of queries has to be free.
+  const int hpg = a.n_q / (a.kv_dim / a.head_dim);
+  const int cheads = hpg * (chunk_bytes > a.head_dim ? 2 : 1);  // heads per row of this chunk
+  const int dshift = a.head_dim == 64 ? 6 : 7;
+  auto prepare = [&](auto threads, int item, int t, bool before) {
+    constexpr int N = decltype(threads)::value, BAR = N == PREP ? 1 : 12;
+    const int qb = item & 1;
+    Meta<WIDE>& meta = ss.meta[qb];
+    if (t < 32) {
+      const int n = group_rows(a, sh, plan, im.b, im.group, meta.row, meta.pos);
+      if (lane == 0) meta.cols = (n * cheads + 15) & ~15, meta.nrows = n;
+    }
+    bar_sync<N>(BAR);
+    const int nqp = meta.cols, nq = meta.nrows * cheads;
+    if (t < NQ) {  // a column per thread: its head of the chunk, and where its queries and its results are
+      const bool whole = im.n == im.span.tiles;  // nobody else has tiles of this group
+      const int slot = (team * 2 + (im.t0 > 0 ? 0 : 1)) * sh.chunks + chunk;
+      const int j = t / cheads, h = t - j * cheads;
+      const int at = (chunk * sh.heads + h) * a.head_dim, r = t < nq ? meta.row[j] : 0;
+      meta.slice[t] = t < nq ? (h >= hpg ? 1 : 0) : -1;
+      meta.query[t] = r * a.q_stride + at;
+      meta.out[t] = whole ? r * a.o_stride + at : (long long)(slot * NQ + t) * PART_LD + 4;
+    }
+    const bool once = nqp > Q_TWICE;  // (the one buffer that both halves are)
+    if (item > 0 && (once || before)) wait(&ss.q_free[qb ^ 1], ((item - 1) >> 1) & 1, a.status, abort);
+    bar_sync<N>(BAR);
+    // queries as two e4m3 terms, rows of 128 bytes: hi in row c, lo in row nqp + c.  A thread takes
+    // 8 dimensions of every so-manieth column; their 16 bytes are copied to where its codes go
+    const int d = (t & 15) * 8, sl = d >> dshift, o = d >> 4;
+    const __nv_bfloat16* q = a.q + (d - (sl << dshift));
+    uint8_t* to = sm + F::Q_OFF + (once ? 0 : qb * (F::Q_BYTES / 2)) + (d & 8);
+    uint8_t* img = sm + F::QIMG_OFF + qb * IMG + (d >> 5);
+    auto place = [&](int r) { return to + r * 128 + ((o ^ (r & 7)) << 4); };
+#pragma unroll 1
+    for (int c = t >> 4; c < nqp; c += N / 16) {
+      const bool in = c < nq && meta.slice[c] == sl;
+      const __nv_bfloat16* from = in ? q + meta.query[c] : a.q;
+      cp_async8(place(c), from, in ? 8 : 0);
+      cp_async8(place(nqp + c), from + (in ? 4 : 0), in ? 8 : 0);
+    }
+    cp_async_wait_all();
+#pragma unroll 1
+    for (int c = t >> 4; c < nqp; c += N / 16) {
+      uint2* hi = reinterpret_cast<uint2*>(place(c));
+      uint2* lo = reinterpret_cast<uint2*>(place(nqp + c));
+      const uint32_t code = split_query(make_uint4(hi->x, hi->y, lo->x, lo->y), *hi, *lo);
+      if ((d & 31) == 0) {
+        img[(c & 31) * 16 + (c >> 5) * 4] = (uint8_t)code;
+        if (!WIDE) img[((nqp + c) & 31) * 16 + ((nqp + c) >> 5) * 4] = (uint8_t)code;
+      }
+    }
+    fence_proxy_async_shared();
+  };
+  bool more = next_job(a, sh, plan, items, im);
+  // the first item's by all but the loading warps, then by their own warps, ahead of their use
+  if (more && warp < LOAD_WARP) {
+    prepare(std::integral_constant<int, 32 * LOAD_WARP>(), 0, tid, false);
+    bar_sync<32 * LOAD_WARP>(12);
+  }
+
   if (warp >= SOFT_WARPS) {
     if constexpr (WIDE) regs_down<OTHER_REGS>();
     if (warp >= LOAD_WARP) {
       // ------------------------------------------------------- loads: a warp takes every other tile
       int ni = warp - LOAD_WARP;
-      bool more = next_job(a, sh, plan, items, im);
       TileLoader tile(ar.box);
       auto locate = [&]() {
 #pragma unroll 1
@@ -511,66 +573,21 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       }
     } else if (warp >= PREP_WARP && warp < PREP_WARP + PREP / 32) {
       // ---------------------- the items' rows and queries, and in the wide form the tiles' widening
-      const int hpg = a.n_q / (a.kv_dim / a.head_dim);
-      const int cheads = hpg * (chunk_bytes > a.head_dim ? 2 : 1);  // heads per row of this chunk
-      const int dshift = a.head_dim == 64 ? 6 : 7, ptid = tid - 32 * PREP_WARP;
+      const int ptid = tid - 32 * PREP_WARP;
       int it = 0;
       bool before = false;  // the item before had more than Q_TWICE columns
 #pragma unroll 1
-      for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
+      for (int item = 0; more; ++item, more = next_job(a, sh, plan, items, im)) {
         const int qb = item & 1;
         if (item >= 2) {
           wait(&ss.q_free[qb], ((item >> 1) - 1) & 1, a.status, abort);
           wait(&ss.m_free[qb], ((item >> 1) - 1) & 1, a.status, abort);
         }
-        Meta<WIDE>& meta = ss.meta[qb];
-        if (warp == PREP_WARP) {
-          const int n = group_rows(a, sh, plan, im.b, im.group, meta.row, meta.pos);
-          if (lane == 0) meta.cols = (n * cheads + 15) & ~15, meta.nrows = n;
-        }
-        bar_sync<PREP>(1);
-        const int nqp = meta.cols, nq = meta.nrows * cheads;
-        if (ptid < NQ) {  // a column per thread: its head of the chunk, and where its queries and its results are
-          const bool whole = im.n == im.span.tiles;  // nobody else has tiles of this group
-          const int slot = (team * 2 + (im.t0 > 0 ? 0 : 1)) * sh.chunks + chunk;
-          const int j = ptid / cheads, h = ptid - j * cheads;
-          const int at = (chunk * sh.heads + h) * a.head_dim, r = ptid < nq ? meta.row[j] : 0;
-          meta.slice[ptid] = ptid < nq ? (h >= hpg ? 1 : 0) : -1;
-          meta.query[ptid] = r * a.q_stride + at;
-          meta.out[ptid] = whole ? r * a.o_stride + at : (long long)(slot * NQ + ptid) * PART_LD + 4;
-        }
-        const bool once = nqp > Q_TWICE;  // (the one buffer that both halves are)
-        if (item > 0 && (once || before)) wait(&ss.q_free[qb ^ 1], ((item - 1) >> 1) & 1, a.status, abort);
-        before = once;
-        bar_sync<PREP>(1);
-        // queries as two e4m3 terms, rows of 128 bytes: hi in row c, lo in row nqp + c.  A thread takes
-        // 8 dimensions of every so-manieth column; their 16 bytes are copied to where its codes go
-        const int d = (ptid & 15) * 8, sl = d >> dshift, o = d >> 4;
-        const __nv_bfloat16* q = a.q + (d - (sl << dshift));
-        uint8_t* to = sm + F::Q_OFF + (once ? 0 : qb * (F::Q_BYTES / 2)) + (d & 8);
-        uint8_t* img = sm + F::QIMG_OFF + qb * IMG + (d >> 5);
-        auto place = [&](int r) { return to + r * 128 + ((o ^ (r & 7)) << 4); };
-#pragma unroll 1
-        for (int c = ptid >> 4; c < nqp; c += PREP / 16) {
-          const bool in = c < nq && meta.slice[c] == sl;
-          const __nv_bfloat16* from = in ? q + meta.query[c] : a.q;
-          cp_async8(place(c), from, in ? 8 : 0);
-          cp_async8(place(nqp + c), from + (in ? 4 : 0), in ? 8 : 0);
-        }
-        cp_async_wait_all();
-#pragma unroll 1
-        for (int c = ptid >> 4; c < nqp; c += PREP / 16) {
-          uint2* hi = reinterpret_cast<uint2*>(place(c));
-          uint2* lo = reinterpret_cast<uint2*>(place(nqp + c));
-          const uint32_t code = split_query(make_uint4(hi->x, hi->y, lo->x, lo->y), *hi, *lo);
-          if ((d & 31) == 0) {
-            img[(c & 31) * 16 + (c >> 5) * 4] = (uint8_t)code;
-            if (!WIDE) img[((nqp + c) & 31) * 16 + ((nqp + c) >> 5) * 4] = (uint8_t)code;
-          }
-        }
-        fence_proxy_async_shared();
+        if (item > 0) prepare(std::integral_constant<int, PREP>(), item, ptid, before);
+        before = ss.meta[qb].cols > Q_TWICE;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ss.q_full[qb]);
+        const Meta<WIDE>& meta = ss.meta[qb];
         if constexpr (WIDE) {  // a warp widens 32 tokens of every tile
           const Clear clear = clear_tiles(a, im, meta);
           const int lw = warp - PREP_WARP, piece = lane & 7, r4 = lane >> 3;
@@ -622,7 +639,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       if (elect_one()) tc_cp_img(ones, sm + F::ONE_OFF);
       __syncwarp();
 #pragma unroll 1
-      for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
+      for (int item = 0; more; ++item, more = next_job(a, sh, plan, items, im)) {
         const int qb = item & 1;
         wait(&ss.q_full[qb], (item >> 1) & 1, a.status, abort);
         const Deal<WIDE> deal(ss.meta[qb].cols);
@@ -678,7 +695,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       int it = 0;
       uint32_t ph = 0;
 #pragma unroll 1
-      for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
+      for (int item = 0; more; ++item, more = next_job(a, sh, plan, items, im)) {
         wait(&ss.q_full[item & 1], (item >> 1) & 1, a.status, abort);
         const Deal<WIDE> deal(ss.meta[item & 1].cols);
         __syncwarp();
@@ -731,9 +748,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     // ---------------------------------------------------------------------------- softmax
     if constexpr (WIDE) regs_up<SOFT_REGS>();
     const int quad = warp & 3, group = warp >> 2;
-    const int hpg = a.n_q / (a.kv_dim / a.head_dim);
-    const int cheads = hpg * (chunk_bytes > a.head_dim ? 2 : 1);  // heads per row of this chunk
-    const int dshift = a.head_dim == 64 ? 6 : 7;
     Soft w;
     w.it = 0;
     w.ph = 0;
@@ -741,7 +755,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     w.to_log2 = a.scale * LOG2E;
     w.tmem = tmem + ((uint32_t)(32 * quad) << 16);
 #pragma unroll 1
-    for (int item = 0; next_job(a, sh, plan, items, im); ++item) {
+    for (int item = 0; more; ++item, more = next_job(a, sh, plan, items, im)) {
       wait(&ss.q_full[item & 1], (item >> 1) & 1, a.status, abort);
       const Meta<WIDE>& meta = ss.meta[item & 1];
       const Deal<WIDE> deal(meta.cols);
