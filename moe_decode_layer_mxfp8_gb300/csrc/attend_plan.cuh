@@ -15,11 +15,12 @@ constexpr float UNSET = -1.0e30f;  // the reference m_q of a query that has seen
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 // How a kernel deals the work out: a tile of `tile` tokens, row groups of rows_per rows (cols query
-// columns at most, `heads` per row in a full 128-byte chunk of the record), teams of CTAs.
+// columns at most, `heads` per row in a full 128-byte chunk of the record), teams of CTAs; beginning
+// another group costs a team as much as `extra` tiles.
 struct Shape {
-  int tile, cols, heads, rows_per, chunks, teams;
+  int tile, cols, heads, rows_per, chunks, teams, extra;
 };
-inline Shape shape_of(const AttendArgs& a, int tile, int cols, int teams) {
+inline Shape shape_of(const AttendArgs& a, int tile, int cols, int teams, int extra) {
   Shape s;
   s.tile = tile;
   s.cols = cols;
@@ -27,11 +28,12 @@ inline Shape shape_of(const AttendArgs& a, int tile, int cols, int teams) {
   s.rows_per = std::min(16, cols / s.heads);
   s.chunks = (a.kv_dim + 127) / 128;
   s.teams = teams;
+  s.extra = extra;
   return s;
 }
 
 // The step as every CTA derives it: per request its rows' largest and smallest position, and
-// the units (tiles times row groups) of all requests before it.
+// the units (its row groups times the extra and their tiles) of all requests before it.
 struct Plan {
   int* pre;  // [n_req + 1]
   int *pmax, *pmin;
@@ -64,7 +66,8 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const Shape& sh, in
   return s;
 }
 
-// The cut: W units over the teams, no team (of those that get any) more than one unit above
+// The cut: a line of W units, the first group's extra left out, over the teams, no team (of those that
+// get any) more than one unit above
 // another.
 struct Cut {
   int teams, each, more;  // team k starts at each * k + min(k, more)
@@ -88,30 +91,35 @@ struct Job {
 
 // The items of a team in order, from the place that the plan found for its first unit.
 struct Jobs {
-  int b, group, t0, left;
+  int b, group, at, left;  // at: the unit of the group
 };
 __device__ __forceinline__ bool next_job(const AttendArgs& a, const Shape& sh, const Plan& p, Jobs& w, Job& it) {
-  if (w.left <= 0) return false;
-  it.b = w.b;
-  it.group = w.group;
-  it.t0 = w.t0;
-  it.span = span_of(a, sh, p.pmax[w.b], p.pmin[w.b]);
-  it.n = min(it.span.tiles - w.t0, w.left);
-  w.left -= it.n;
-  w.t0 = 0;
-  ++w.group;
-  if (w.left > 0 && p.pre[w.b] + w.group * it.span.tiles >= p.pre[w.b + 1]) {
-    w.group = 0;
-    do ++w.b;
-    while (p.pre[w.b + 1] <= p.pre[w.b]);  // (units are left, so there is such a request)
+  it.n = 0;
+#pragma unroll 1
+  while (w.left > 0 && it.n <= 0) {
+    it.b = w.b;
+    it.group = w.group;
+    it.span = span_of(a, sh, p.pmax[w.b], p.pmin[w.b]);
+    const int units = it.span.tiles + sh.extra, n = min(units - w.at, w.left);
+    it.t0 = max(0, w.at - sh.extra);
+    it.n = w.at + n - sh.extra - it.t0;  // (none where only the extra is this team's)
+    w.left -= n;
+    w.at = 0;
+    ++w.group;
+    if (w.left > 0 && p.pre[w.b] + w.group * units >= p.pre[w.b + 1]) {
+      w.group = 0;
+      do ++w.b;
+      while (p.pre[w.b + 1] <= p.pre[w.b]);  // (units are left, so there is such a request)
+    }
   }
-  return true;
+  return it.n > 0;
 }
 
-// Where row r's results are: its request's and group's units [g0, g0 + tiles) and its place in
-// the group; tiles 0: nothing to see.
+// Where row r's results are: in the pieces of teams [k0, k1] (one: whole, and done), at its place in
+// the group; k0 -1: nothing to see.  A team's first slot is for a group that began before it, its
+// second for one that begins in it.
 struct RowInfo {
-  int g0, tiles, place;
+  int k0, k1, place;
 };
 
 __device__ __forceinline__ float log2_of(float x) {
@@ -137,7 +145,7 @@ __device__ __forceinline__ uint4 without_nan(uint4 v) {
 // it; the results are behind the caller's next barrier).  Waits for the kernels before.
 template <int NT>
 __device__ __forceinline__ void derive_plan(const AttendArgs& a, const Shape& sh, const Plan& plan,
-                                            int team, bool live, Jobs* start, int* total) {
+                                            int team, bool live, Jobs* start) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 #pragma unroll 1
   for (int b = tid; b < a.n_req; b += NT) {
@@ -172,7 +180,8 @@ __device__ __forceinline__ void derive_plan(const AttendArgs& a, const Shape& sh
       int u = 0;
       if (plan.cnt && b < a.n_req) plan.cnt[b] = (short)n;
       if (n > 0) {
-        u = (n + sh.rows_per - 1) / sh.rows_per * span_of(a, sh, plan.pmax[b], plan.pmin[b]).tiles;
+        const int tiles = span_of(a, sh, plan.pmax[b], plan.pmin[b]).tiles;
+        if (tiles > 0) u = (n + sh.rows_per - 1) / sh.rows_per * (tiles + sh.extra);
         if (plan.pmax[b] >= (long long)a.kv.max_blocks * a.kv.block_size && blockIdx.x == 0)
           atomicOr(a.status, ST_UNMAPPED_PAGE);
       }
@@ -187,8 +196,8 @@ __device__ __forceinline__ void derive_plan(const AttendArgs& a, const Shape& sh
     __syncwarp();
     if (lane == 0) {  // the team's first unit
       plan.pre[0] = 0;
-      const Cut cut(W, sh.teams);
-      const int w0 = cut.start(team);
+      const Cut cut(max(0, W - sh.extra), sh.teams);
+      const int w0 = cut.start(team) + sh.extra;
       Jobs w = {0, 0, 0, live ? cut.size(team) : 0};
       if (w.left > 0) {
         int hi = a.n_req;  // the last request that starts by w0
@@ -198,12 +207,11 @@ __device__ __forceinline__ void derive_plan(const AttendArgs& a, const Shape& sh
           if (plan.pre[mid] <= w0) w.b = mid; else hi = mid;
         }
         const int u = w0 - (w.b ? plan.pre[w.b] : 0);
-        const int tiles = span_of(a, sh, plan.pmax[w.b], plan.pmin[w.b]).tiles;
-        w.group = u / tiles;
-        w.t0 = u - w.group * tiles;
+        const int units = span_of(a, sh, plan.pmax[w.b], plan.pmin[w.b]).tiles + sh.extra;
+        w.group = u / units;
+        w.at = u - w.group * units;
       }
       *start = w;
-      if (blockIdx.x == 0 && total) *total = W;
     }
   }
 }
@@ -212,15 +220,19 @@ __device__ __forceinline__ void derive_plan(const AttendArgs& a, const Shape& sh
 __device__ __forceinline__ RowInfo row_info(const AttendArgs& a, const Shape& sh, const Plan& plan,
                                             int r) {
   const int b = plan.req[r], lane = threadIdx.x & 31;
-  RowInfo info = {0, 0, 0};
+  RowInfo info = {-1, -1, 0};
   if (b >= 0) {
     int rank = 0;
 #pragma unroll 1
     for (int i = lane; i < r; i += 32) rank += plan.req[i] == b;
     rank = __reduce_add_sync(0xffffffffu, rank);
-    const Span s = span_of(a, sh, plan.pmax[b], plan.pmin[b]);
+    const int tiles = span_of(a, sh, plan.pmax[b], plan.pmin[b]).tiles;
     const int group = rank / sh.rows_per;
-    info = {plan.pre[b] + group * s.tiles, s.tiles, rank - group * sh.rows_per};
+    if (tiles > 0) {
+      const Cut cut(plan.pre[a.n_req] - sh.extra, sh.teams);
+      const int g0 = plan.pre[b] + group * (tiles + sh.extra);  // (in the cut: without the first extra)
+      info = {cut.team_of(g0), cut.team_of(g0 + tiles - 1), rank - group * sh.rows_per};
+    }
   }
   return info;
 }
@@ -248,7 +260,6 @@ constexpr int PART_LD = 128 + 4;
 struct Pieces {
   float* part;
   RowInfo* rows;  // [rows]
-  int* total;     // units of the step
 };
 
 cudaError_t launch_join(const Launch&, const AttendArgs&, const Shape&, const Pieces&);

@@ -56,6 +56,7 @@ struct Form {
   static constexpr int NQ = WIDE ? 96 : 64;  // query columns at most
   static constexpr int CMAX = WIDE ? 24 : 16;  // columns of a softmax warp at most
   static constexpr int ST = WIDE ? 3 : 8;    // tiles in the ring
+  static constexpr int EXTRA = WIDE ? 5 : 10;  // what an item costs beside its tiles, in tiles
   // the roles' first warps
   static constexpr int PREP_WARP = SOFT_WARPS, PREP = (WIDE ? 4 : 2) * 32;
   static constexpr int MMA_WARPS = WIDE ? 1 : 2, S_WARP = PREP_WARP + PREP / 32,
@@ -100,7 +101,6 @@ struct Args {
   Shape sh;
   float* part;    // workspace (Pieces)
   RowInfo* rows;
-  int* total;
 };
 
 // Matrix descriptor as desc_sw128, MN-major with `lbo` bytes between 128-byte runs along MN.
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     reinterpret_cast<uint32_t*>(sm + F::PIMG_OFF)[i] = 0x7F7F7F7Fu;
   fence_proxy_async_shared();
 
-  derive_plan<THREADS>(a, sh, plan, team, team < sh.teams, &ss.start, ar.total);
+  derive_plan<THREADS>(a, sh, plan, team, team < sh.teams, &ss.start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -901,10 +901,10 @@ cudaError_t attend_tc_prepare() {
 
 cudaError_t launch_attend_tc(const Launch& L, const AttendArgs& a, const attend::Pieces& ws, int sms) {
   const int chunks = (a.kv_dim + 127) / 128;
-  const Shape narrow = shape_of(a, TT, Form<false>::NQ, sms / chunks);
+  const Shape narrow = shape_of(a, TT, Form<false>::NQ, sms / chunks, Form<false>::EXTRA);
   const bool wide = (a.rows + a.n_req - 1) / a.n_req * narrow.heads > WIDE_FROM;
-  Args ar = {{}, {}, 0, a, wide ? shape_of(a, TT, Form<true>::NQ, sms / chunks) : narrow, ws.part, ws.rows,
-             ws.total};
+  Args ar = {{}, {}, 0, a, wide ? shape_of(a, TT, Form<true>::NQ, sms / chunks, Form<true>::EXTRA) : narrow,
+             ws.part, ws.rows};
   ar.box = encode_cache_maps(&ar.codes, &ar.scales, a);
   const cudaError_t e =
       wide ? launch_ex(L, dim3(sms), dim3(THREADS), Form<true>::SMEM_BYTES, attend_kernel<true>, ar)

@@ -9,51 +9,62 @@ namespace mono {
 namespace attend {
 namespace {
 
-// Joins the pieces of a (row, head): a warp each, 4 dimensions a lane.  Rows that one piece
-// holds are done; pad rows and rows that see nothing get zeros.
-constexpr int JOIN_WARPS = 4;
+// Joins the pieces of a (row, head): a warp each, 4 dimensions a lane (64 wide: the half warps take
+// every other piece).  Rows that one piece holds are done; pad rows and rows that see nothing get
+// zeros.  Bound by latency: a lane per piece fetches m and l while the first pieces' O is on its way.
+constexpr int JOIN_WARPS = 4, AHEAD = 4;
 __global__ void __launch_bounds__(JOIN_WARPS * 32) attend_join_kernel(const AttendArgs a, const Shape sh, const Pieces ar) {
+  const int r = blockIdx.x, h = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int chunk = h / sh.heads, hpg = a.n_q / (a.kv_dim / a.head_dim);
+  const int cheads = hpg * (min(128, a.kv_dim - 128 * chunk) > a.head_dim ? 2 : 1);
+  const int d = 4 * lane & (a.head_dim - 1), step = 128 / a.head_dim, first = lane * 4 / a.head_dim;
+  __nv_bfloat16* o = a.o + r * a.o_stride + (long long)h * a.head_dim + d;
+  const size_t team = (size_t)2 * sh.chunks * sh.cols * PART_LD;  // from a team's pieces to the next's
   pdl_trigger();
   pdl_wait();
-  const int r = blockIdx.x, h = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (h >= a.n_q) return;
   const RowInfo info = ar.rows[r];
-  const int d = 4 * lane & (a.head_dim - 1);
-  __nv_bfloat16* o = a.o + r * a.o_stride + (long long)h * a.head_dim + d;
-  if (info.tiles == 0) {
+  if (info.k0 < 0) {
     *reinterpret_cast<uint2*>(o) = make_uint2(0u, 0u);
     if (lane == 0) a.lse[(long long)r * a.n_q + h] = -INFINITY;
     return;
   }
-  const Cut cut(*ar.total, sh.teams);
-  const int k0 = cut.team_of(info.g0), k1 = cut.team_of(info.g0 + info.tiles - 1);
-  if (k0 == k1) return;  // whole in one team
-  const int chunk = h / sh.heads, hpg = a.n_q / (a.kv_dim / a.head_dim);
-  const int cheads = hpg * (min(128, a.kv_dim - 128 * chunk) > a.head_dim ? 2 : 1);
-  const int c = info.place * cheads + (h - chunk * sh.heads);
-  auto piece = [&](int k) {
-    const int slot = cut.start(k) > info.g0 ? 0 : 1;  // began before this team, or in it
-    return ar.part + (((size_t)(k * 2 + slot) * sh.chunks + chunk) * sh.cols + c) * PART_LD;
-  };
-  float M = UNSET;
-#pragma unroll 1
-  for (int k = k0 + lane; k <= k1; k += 32) M = fmaxf(M, piece(k)[0]);
-  M = warp_max(M);
+  if (info.k0 == info.k1) return;  // whole in one team
+  const int c = info.place * cheads + (h - chunk * sh.heads), n = info.k1 - info.k0 + 1;
+  // piece i: team k0 + i's first slot, but the first piece its second
+  const float* base = ar.part + info.k0 * team + ((size_t)chunk * sh.cols + c) * PART_LD;
+  auto piece = [&](int i) { return base + i * team + (i == 0 ? (size_t)sh.chunks * sh.cols * PART_LD : 0); };
+  auto fetch = [&](int i) { return *reinterpret_cast<const float4*>(piece(i) + 4 + d); };
+  float m = UNSET, den = 0.0f;
   float4 num = {0.0f, 0.0f, 0.0f, 0.0f};
-  float den = 0.0f;
-  // 64 wide: the upper half warp takes every other piece
-  const int first = a.head_dim == 64 ? lane >> 4 : 0, step = a.head_dim == 64 ? 2 : 1;
-#pragma unroll 2
-  for (int k = k0 + first; k <= k1; k += step) {
-    const float* p = piece(k);
-    const float f = ex2(p[0] - M);
-    const float4 x = *reinterpret_cast<const float4*>(p + 4 + d);
-    den = fmaf(f, p[1], den);
-    num.x = fmaf(f, x.x, num.x), num.y = fmaf(f, x.y, num.y);
-    num.z = fmaf(f, x.z, num.z), num.w = fmaf(f, x.w, num.w);
+#pragma unroll 1
+  for (int b = 0; b < n; b += 32) {
+    const int in = min(32, n - b);
+    float2 ml = {UNSET, 0.0f};
+    if (lane < in) ml = *reinterpret_cast<const float2*>(piece(b + lane));
+    float4 x[AHEAD];
+#pragma unroll
+    for (int e = 0; e < AHEAD; ++e)
+      if (first + step * e < in) x[e] = fetch(b + first + step * e);
+    const float to = fmaxf(m, warp_max(ml.x)), f = ex2(ml.x - to), old = ex2(m - to);
+    m = to;
+    den = fmaf(den, old, warp_sum(f * ml.y));
+    num.x *= old, num.y *= old, num.z *= old, num.w *= old;
+#pragma unroll 1
+    for (int i = 0; i < in; i += step * AHEAD) {
+#pragma unroll
+      for (int e = 0; e < AHEAD; ++e) {
+        const int at = i + first + step * e;
+        const float g = __shfl_sync(0xffffffffu, f, at & 31);
+        if (at < in) {
+          num.x = fmaf(g, x[e].x, num.x), num.y = fmaf(g, x[e].y, num.y);
+          num.z = fmaf(g, x[e].z, num.z), num.w = fmaf(g, x[e].w, num.w);
+        }
+        if (at + step * AHEAD < in) x[e] = fetch(b + at + step * AHEAD);
+      }
+    }
   }
   if (a.head_dim == 64) {
-    den += __shfl_xor_sync(0xffffffffu, den, 16);
     num.x += __shfl_xor_sync(0xffffffffu, num.x, 16), num.y += __shfl_xor_sync(0xffffffffu, num.y, 16);
     num.z += __shfl_xor_sync(0xffffffffu, num.z, 16), num.w += __shfl_xor_sync(0xffffffffu, num.w, 16);
   }
@@ -62,7 +73,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attend_join_kernel(const Atte
   *reinterpret_cast<uint2*>(o) =
       make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));
   if (lane == 0)
-    a.lse[(long long)r * a.n_q + h] = den == 0.0f ? -INFINITY : (log2f(den) + M) * LN2;
+    a.lse[(long long)r * a.n_q + h] = den == 0.0f ? -INFINITY : (log2f(den) + m) * LN2;
 }
 
 }  // namespace
@@ -112,12 +123,11 @@ cudaError_t launch_join(const Launch& L, const AttendArgs& a, const Shape& sh, c
 
 namespace {
 struct Layout {
-  size_t rows, total, part, bytes;
+  size_t rows, part, bytes;
 };
 Layout layout(int max_rows, int sms) {
   Layout l;
-  l.total = 0;
-  l.rows = 256;
+  l.rows = 0;
   l.part = l.rows + ((size_t)max_rows * sizeof(attend::RowInfo) + 255) / 256 * 256;
   // pieces: two per team and chunk, a team per `chunks` SMs
   l.bytes = l.part + (size_t)sms * 2 * attend::MAX_COLS * attend::PART_LD * sizeof(float);
@@ -135,8 +145,7 @@ cudaError_t attend_prepare() {
 cudaError_t launch_attend(const Launch& L, const AttendArgs& a, uint8_t* base, int max_rows, int sms) {
   const Layout l = layout(max_rows, sms);
   const attend::Pieces ws = {reinterpret_cast<float*>(base + l.part),
-                             reinterpret_cast<attend::RowInfo*>(base + l.rows),
-                             reinterpret_cast<int*>(base + l.total)};
+                             reinterpret_cast<attend::RowInfo*>(base + l.rows)};
   cudaError_t e = launch_attend_tc(L, a, ws, sms);
   if (e == cudaSuccess && a.weights) e = launch_attend_weights(L, a, sms);
   return e;

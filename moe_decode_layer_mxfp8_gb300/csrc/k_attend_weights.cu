@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_weights_kernel(const __grid
   for (int i = tid; i < (CHUNKS + 1) * IMG / 4; i += THREADS)
     reinterpret_cast<uint32_t*>(sm + QIMG_OFF)[i] = 0x7F7F7F7Fu;
   fence_proxy_async_shared();
-  derive_plan<THREADS>(a, sh, plan, blockIdx.x, true, &ss.start, nullptr);
+  derive_plan<THREADS>(a, sh, plan, blockIdx.x, true, &ss.start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -312,7 +312,7 @@ cudaError_t attend_weights_prepare() {
 }
 
 cudaError_t launch_attend_weights(const Launch& L, const AttendArgs& a, int sms) {
-  Args ar = {{}, {}, 0, 0, 0, a, shape_of(a, TT, NQ, sms)};
+  Args ar = {{}, {}, 0, 0, 0, a, shape_of(a, TT, NQ, sms, 4)};
   ar.sh.rows_per = MAX_ROWS;  // a unit is a tile with all its request's rows
   ar.pad = (ar.sh.heads + 15) & ~15;
   // rows of a pass: as many as requests have on average, while columns and queries fit
