@@ -76,8 +76,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_weights_kernel(const __grid
   const AttendArgs& a = ar.a;
   const Shape& sh = ar.sh;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~uintptr_t(1023));
+  uint8_t* sm = smem_raw + (-smem_u32(smem_raw) & 1023);  // (still a shared pointer to the compiler)
   __shared__ __align__(16) Shared ss;
   volatile int* abort = &ss.abort;
   Plan plan;
