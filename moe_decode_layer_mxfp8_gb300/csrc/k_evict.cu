@@ -9,9 +9,9 @@
 //
 // Move (a CTA per 64 kept tokens, in order): the records go through registers, 16 bytes a lane,
 // every load of a chunk in flight at once.  Within the same pages a chunk is written only after
-// the chunks that read from its slots have loaded theirs: kept slots rise, so these are the
-// chunks from the one whose sources reach its first slot on (the selection leaves that place
-// behind) up to itself.  Chunks are handed out in order, so a chunk waits only for chunks that
+// the chunks that read from its slots have loaded theirs: kept slots rise, so these are the one or
+// two whose sources lie between its first slot and the next chunk's (the selection leaves those places
+// behind).  Chunks are handed out in order, so a chunk waits only for chunks that
 // have begun, and those publish their loads before they wait.  Weights move the same way.
 // Bound by HBM: each kept record is read once and written once.
 #include <algorithm>
@@ -232,6 +232,13 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(EvictArgs a, W
   const int i0 = chunk * CHUNK, count = min(CHUNK, n - i0);
   if (count <= 0) return;
   const bool still = a.in_place && n == len;  // everything stays where it is
+  // the chunks ahead of this one that read from the slots that it writes
+  int first = 0, end = 0;
+  if (ordered && n < len) {
+    const int* from = ws.from + (size_t)b * chunks + chunk;
+    first = from[0] / CHUNK;
+    end = min(chunk, (chunk + 1 < chunks && i0 + CHUNK < len ? from[1] + CHUNK - 1 : n + CHUNK - 1) / CHUNK);
+  }
   if (tid < count) {
     const int from = a.kept[b * a.kept_stride + i0 + tid];
     s_kept[tid] = from;
@@ -259,8 +266,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(EvictArgs a, W
     __threadfence();  // this thread's loads have been performed
     __syncthreads();
     if (tid == 0) st_release(const_cast<int*>(loaded) + chunk, 1);
-    const int first = ws.from[(size_t)b * chunks + chunk] / CHUNK;
-    for (int c = first + tid; c < chunk; c += MOVE_THREADS) wait_loaded(loaded + c, a.status);
+    for (int c = first + tid; c < end; c += MOVE_THREADS) wait_loaded(loaded + c, a.status);
     __syncthreads();
   }
 #pragma unroll
