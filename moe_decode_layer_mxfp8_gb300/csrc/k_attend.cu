@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   tc_fence_after();
   const uint32_t tmem = ss.tmem;
   Jobs items = ss.start;
-  Job im;
+  Job im = {};
 
   // An item's rows and queries, by N threads (t: 0..N - 1, whole warps); before: the last item's one
   // buffer of queries has to be free.
