@@ -59,7 +59,7 @@ int mono_cache_status(mono_cache_t *h, int clear);
  * weights, if given, gathers every cached token's attention weight: weights[b][t] += the sum
  * over b's rows and all heads of w[t], for t < weights_stride.  The order of that sum is fixed.
  *
- * Limits: max_blocks * block_size below 2^31, and times rows below 2^38.
+ * Limits: max_blocks * block_size below 2^31; its tiles of 128 tokens, and 16 more, times rows too.
  *
  * One handle's calls share its workspace: they must be ordered on the GPU (one stream, or
  * events between streams; graphs captured from one handle must not run at the same time).

@@ -60,7 +60,7 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const Shape& sh, in
   const int lo = min(s.lo, (int)cap);
   const int shift = __ffs(TT) - 1;
   const int b0 = lo >> shift, b1 = last >= lo ? (last >> shift) + 1 : b0;
-  s.head = min((min(min(a.sinks, s.lo), (int)cap) + TT - 1) >> shift, b0);
+  s.head = min((int)(((uint32_t)min(min(a.sinks, s.lo), (int)cap) + TT - 1) >> shift), b0);
   s.body = b0;
   s.tiles = s.head + b1 - b0;
   return s;

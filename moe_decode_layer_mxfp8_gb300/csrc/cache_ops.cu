@@ -145,8 +145,8 @@ int mono_cache_attend(mono_cache_t* h, const mono_attend_args* a, void* stream) 
     return MONO_ERR_BAD_ALIGNMENT;
   TRY(check_view(s, a->kv_cache, a->kv_stride_block, a->kv_stride_tok, a->kv_num_blocks,
                  a->max_blocks));
-  // (work is counted in 32 bits: tiles of 128 tokens over all rows)
-  if (((int64_t)a->max_blocks * s.block_size + 127) / 128 * a->rows > INT32_MAX)
+  // (work is counted in 32 bits: tiles of 128 tokens, and some more, over all rows)
+  if ((((int64_t)a->max_blocks * s.block_size + 127) / 128 + 16) * a->rows > INT32_MAX)
     return MONO_ERR_INVALID_ARG;
   TRY(check_device(h));
   AttendArgs k = {};

@@ -907,3 +907,42 @@ def test_a_serving_step_end_to_end():
     target, draft, tok, starts, u, r = make_verify(counts, 2000, torch.float32, seed=60)
     check_verify(m, target, draft, tok, starts, u, r)
     layer.close(), h.close()
+
+
+def test_attend_work_limit():
+    """The work of a step is counted in 32 bits: (tiles of 128 tokens + 16) * rows < 2^31."""
+    m = _m()
+    rows, blocks = 1024, (2 ** 21 - 17) * 8  # of 16 tokens
+    table = torch.full((1, blocks + 8), -1, dtype=torch.int32, device="cuda")
+    table[0, 0] = 0
+    pool = torch.zeros((1, 16, 80), dtype=torch.uint8, device="cuda")
+    h = m.Cache(TINY, max_rows=rows, max_requests=1)
+    q = torch.zeros((rows, 256), dtype=torch.bfloat16, device="cuda")
+    o = torch.full_like(q, float("nan"))
+    pos = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    with pytest.raises(m.MonoError):
+        h.attend(q, o, pos, pos, table, pool)
+    h.attend(q, o, pos, pos, table[:, :blocks].contiguous(), pool)
+    torch.cuda.synchronize()
+    assert h.status() == 0 and not o.any()
+    h.close()
+
+
+@pytest.mark.parametrize("rows", [1, 6], ids=["narrow", "wide"])
+def test_attend_negative_token_scales(rows):
+    """A record is its codes times its scale, whatever the scale's sign."""
+    m = _m()
+    L = 700
+    table, cache = make_cache(FULL, [L], seed=rows)
+    rng = np.random.default_rng(3)
+    for t in rng.choice(L, 300, replace=False):
+        rec = cache[table[0, t // 128], t % 128]
+        rec[512:516] = (-rec[512:516].view(np.float32)).view(np.uint8)
+    q = make_q(FULL, rows, 4)
+    pos = list(range(L - rows, L))
+    w0 = torch.zeros((1, L))
+    o, lse, w, st = run_attend(m, FULL, q, pos, [0] * rows, table, cache, weights=w0)
+    eo, tol, el, ltol, ew, wtol = co.attend(FULL, q.double().numpy(), pos, [0] * rows, table, cache,
+                                            n_weights=L)
+    assert st == 0 and (np.abs(o - eo) <= tol).all() and (np.abs(lse - el) <= ltol).all()
+    assert (np.abs(w - ew) <= wtol + 2.0 ** -24 * (rows * 64 + 2) * ew).all()
