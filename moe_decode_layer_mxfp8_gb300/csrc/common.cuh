@@ -367,31 +367,6 @@ __device__ __forceinline__ float block_max(float v, float* red) {
   return warp_max(t);
 }
 
-// Arithmetic on pairs of f32, one instruction for both.
-__device__ __forceinline__ void fma2(float& x, float& y, float a, float bx, float by) {  // x = x a + bx
-  asm("{\n .reg .b64 s, m, b;\n mov.b64 s, {%0, %1};\n mov.b64 m, {%2, %2};\n mov.b64 b, {%3, %4};\n"
-      " fma.rn.f32x2 s, s, m, b;\n mov.b64 {%0, %1}, s;\n}"
-      : "+f"(x), "+f"(y)
-      : "f"(a), "f"(bx), "f"(by));
-}
-__device__ __forceinline__ void add2(float& x, float& y, float bx, float by) {
-  asm("{\n .reg .b64 s, b;\n mov.b64 s, {%0, %1};\n mov.b64 b, {%2, %3};\n"
-      " add.rn.f32x2 s, s, b;\n mov.b64 {%0, %1}, s;\n}"
-      : "+f"(x), "+f"(y)
-      : "f"(bx), "f"(by));
-}
-__device__ __forceinline__ void mul2(float& x, float& y, float a) {
-  asm("{\n .reg .b64 s, m;\n mov.b64 s, {%0, %1};\n mov.b64 m, {%2, %2};\n"
-      " mul.rn.f32x2 s, s, m;\n mov.b64 {%0, %1}, s;\n}"
-      : "+f"(x), "+f"(y)
-      : "f"(a));
-}
-__device__ __forceinline__ void mul2(float& x, float& y, float ax, float ay) {
-  asm("{\n .reg .b64 s, m;\n mov.b64 s, {%0, %1};\n mov.b64 m, {%2, %3};\n"
-      " mul.rn.f32x2 s, s, m;\n mov.b64 {%0, %1}, s;\n}"
-      : "+f"(x), "+f"(y)
-      : "f"(ax), "f"(ay));
-}
 // 8 bf16 values in a 16-byte word <-> 8 floats
 __device__ __forceinline__ void bf16x8_to_f32(const uint4 v, float (&f)[8]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};

@@ -7,30 +7,45 @@
 // A 128-byte run of a record (a chunk: one 128-wide latent slice, or two 64-wide ones) and 128
 // tokens make a tile.  Tokens are the M of the first product, dimensions that of the second, and
 // queries the N of both: the heads that share a latent slice, times the rows of a request that
-// share its context (1 to 64 columns, padded to 16).  Both products take the e4m3 tile as it lies
-// in the cache (kind::mxf8f6f4; the second one transposed), so a tile is read into shared memory
-// once and never rewritten.  A bf16 query is the exact sum of two e4m3 terms under one power-of-two
-// scale per 32 dimensions; P scale_t is two e4m3 terms (together 8 bits, the one rounding between
-// scores and o) under a power-of-two scale per column and 32 tokens.  The terms are columns of one
-// MMA, added when accumulators are read.
-// O stays in TMEM over a whole run of tiles: m_q, an integer, moves only when a weight passes it
-// by far (then O is rescaled, exactly).
+// share its context (1 to 96 columns, padded to 16), so the cache is read once for all of them.
+// The first product takes the e4m3 tile as it lies in the cache (kind::mxf8f6f4); a bf16 query is
+// the exact sum of two e4m3 terms under one power-of-two scale per 32 dimensions.  The second one
+// has two forms:
+//   narrow: the same tile, transposed, against P scale_t as two e4m3 terms (together 8 bits, the
+//     one rounding between scores and o) under a power-of-two scale per column and 32 tokens: the
+//     tile is never rewritten, a weight costs some 14 instructions.  Both products' terms are
+//     columns of one MMA, added when accumulators are read.
+//   wide: the tile widened to f16 (exact) against P scale_t in f16 (11 bits): widening costs
+//     shared-memory bandwidth and four warps, but a weight only some 6 instructions.
+// Requests of up to 32 columns on average take the narrow form.  Measured over 8 contexts of
+// 1K..64K tokens, 16 heads a slice, rows of a request 1 / 2 / 3 / 4: narrow 40 / 57 / 86 / 96 us,
+// wide 68 / 72 / 77 / 81 us.
+// O stays in TMEM over a whole run of tiles: m_q, an integer, is set by the run's first tile and
+// moves only when a weight passes it by far (then O is rescaled, exactly).
 //
 // Work: the tiles of all (request, group of rows) pairs in one line, cut evenly into as many
 // pieces as there are teams; a team is one CTA per chunk, so that the CTAs that read the same
 // records run side by side.  Every CTA derives the cut from the step's positions and requests.
-// A pair that falls into one piece is finished there; pieces of the others leave (O, m, l) in
-// the workspace, which a second kernel joins.
+// Beginning another pair costs a team as much as ten tiles (five in the wide form), and the cut
+// counts it so: without that 8 rows over 8 contexts took 45 us instead of 41, windows of 4K tokens
+// for 48 rows 36 instead of 31.  A pair that falls into one piece is finished there; pieces of the
+// others leave (O, m, l) in the workspace, which a second kernel joins.
 //
 // Roles: warps 0-15 softmax, a token per thread (TMEM lane quadrant = warp % 4) and 16 columns per
-// group of four warps: with 16 columns the groups take every fourth tile each, with 32 two groups
-// share every other tile, with more the groups share all tiles.  Warps 16 and 17 make the next
-// item's queries while the current one runs, 18 and 19 issue the first product's MMAs, 20 and 21
-// the second's, 22 and 23 load (every other tile each: TMA boxes through the page table, or cp.async
-// for page sizes that are no multiple of 8).  A wait for a barrier that is complete still costs a
-// warp 100 to 300 cycles, an MMA's issue some 60: hence two warps for each product, and one wait per
-// tile in the softmax.  What runs once per launch or item is kept short, in rolled loops: its
-// instructions come from L2 or further away.
+// group of four warps (24 where there are more than 64): with 16 columns the groups take every
+// fourth tile each, with 32 two groups share every other tile, with more the groups share all
+// tiles.  Then come the warps that make the next item's queries while the current one runs (in the
+// wide form they widen tiles too), those that issue the first product's MMAs, the second's, and two
+// that load (every other tile each: TMA boxes through the page table, or cp.async for page sizes
+// that are no multiple of 8).  A wait for a barrier that is complete still costs a warp 100 to 300
+// cycles, an MMA's issue some 60: hence two warps for each product in the narrow form, whose tiles
+// take 700 cycles, and one wait per tile in the softmax.  What runs once per launch or item is kept
+// short, in rolled loops: its instructions come from L2 or further away.
+//
+// Measured: 8 rows over 8 contexts of 1K..64K 39 us, of which 31 are the tiles' (137 MB; copy: 20 us),
+// the rest launches, the cut and the join; bound by HBM while tiles run, by the first tile's latency
+// before.  48 rows 96 us, bound by the softmax warps' latencies (2850 cycles a tile, 0.6 instructions
+// a cycle; its MMAs take 1250).  One row over 777 tokens 12 us: launches and latencies.
 // Every mbarrier wait is bounded; a wait that runs out is reported, and from then on every role
 // runs its loop without waiting, copying or issuing, so that the barriers among warps still
 // complete and TMEM is freed.
@@ -47,7 +62,7 @@ using namespace attend;
 constexpr int THREADS = 24 * 32;
 constexpr int SOFT_WARPS = 16, SOFT = SOFT_WARPS * 32, GROUPS = SOFT_WARPS / 4;
 constexpr int Q_TWICE = 32;    // items of up to so many columns have their queries made ahead
-constexpr int WIDE_FROM = 32;  // the wide form where requests have more columns on average
+constexpr int WIDE_FROM = 32;  // the wide form where requests have more columns on average (see above)
 constexpr int V_TILE = 2 * K_TILE, SLOTS = 8;
 
 // What the two forms differ in (see the head of the file).

@@ -4,12 +4,14 @@
 //   w = max(p - q, 0), else from w = p in the last row: the smallest v with
 //   sum_{i <= v} w_i > r sum_i w_i
 //
-// Bound by reading the one row pair that the token is drawn from; small ones by latencies.  A
-// request is a cluster of up to 16 CTAs, each with a run of the vocabulary, cut once more into a
-// run per warp and that into blocks: one pass sums the blocks (16-byte loads), the CTAs exchange
-// their sums through distributed shared memory, and the one warp whose run holds the threshold
-// finds the block and reads it again, in order.  A request whose residual is empty takes a second
-// pass over p.
+// A request is a cluster of up to 16 CTAs, each with a run of the vocabulary, cut once more into a
+// run per warp and that into blocks: one pass sums the lanes' shares of the blocks (16-byte loads),
+// the CTAs exchange their sums through distributed shared memory, and the one warp whose run holds
+// the threshold finds the block and reads it again, in order.  A request whose residual is empty
+// takes a second pass over p.
+// Bound by reading the one row pair that the token is drawn from; small ones by latencies.
+// Measured: 192 requests of 3 drafts, 100003 bf16 entries, a quarter of them greedy 29 us (77 MB; copy:
+// 11 us), 8 of 5 drafts, 131072 f32 entries 10.5 us, 4 of 2 table drafts, 32000 f16 entries 7.2 us.
 // Sums decide which token is drawn, so they are carried as pairs of f32 (error-free additions and
 // products, and p - q as a pair): FP64 runs at a 64th of the FP32 rate here, and a search in f64 took
 // 40 us of a CTA's 45.
@@ -18,6 +20,7 @@
 #include <type_traits>
 
 #include "cache_kernels.h"
+#include "f32x2.cuh"
 
 namespace mono {
 namespace {

@@ -60,36 +60,6 @@ __device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 __device__ __forceinline__ void tc_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-// Eight columns of the warp's lane quadrant, TMEM -> registers and back.  Loaded registers are
-// to be used only behind tc_wait_ld and tc_loaded (which keeps the compiler from moving a use
-// ahead of the wait).
-__device__ __forceinline__ void tc_ld8(uint32_t taddr, float* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]),
-                 "=f"(r[6]), "=f"(r[7])
-               : "r"(taddr));
-}
-__device__ __forceinline__ void tc_loaded(float* r) {
-  asm volatile(""
-               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]),
-                 "+f"(r[7]));
-}
-__device__ __forceinline__ void tc_ld4(uint32_t taddr, float* r) {  // four columns
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3])
-               : "r"(taddr));
-}
-__device__ __forceinline__ void tc_loaded4(float* r) {
-  asm volatile("" : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]));
-}
-__device__ __forceinline__ void tc_st8(uint32_t taddr, const float* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-               "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
-               : "memory");
-}
-__device__ __forceinline__ void tc_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
 // True in one lane of the (converged) warp: the thread that issues the tensor-core work.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
