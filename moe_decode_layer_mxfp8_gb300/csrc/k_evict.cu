@@ -219,8 +219,11 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(EvictArgs a, W
   const int tid = threadIdx.x;
   if (tid == 0) s_ticket = atomicAdd(ws.ticket, 1);
   __syncthreads();
-  const int chunk = s_ticket / a.n_req, b = s_ticket - chunk * a.n_req;
-  const int n = a.new_lengths[b], len = ws.old_len[b];
+  const int chunk = s_ticket / a.n_req, b = s_ticket - chunk * a.n_req, i0 = chunk * CHUNK;
+  // (all that a chunk looks up first, at once: kept is written up to the budget)
+  const int* from = ws.from + (size_t)b * chunks + min(chunk, chunks - 1);
+  const int n = a.new_lengths[b], len = ws.old_len[b], from0 = from[0], from1 = from[chunk + 1 < chunks ? 1 : 0];
+  const int slot = tid < CHUNK && i0 + tid < a.budget ? a.kept[b * a.kept_stride + i0 + tid] : -1;
   const int* loaded = ws.loaded + (size_t)b * chunks;
   float* wo = a.weights_out + b * a.weights_out_stride;
   const long long wcap = a.weights_out_stride;
@@ -231,20 +234,18 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(EvictArgs a, W
     for (long long i = n + tid; i < min((long long)len, wcap); i += MOVE_THREADS) wo[i] = 0.0f;
     return;
   }
-  const int i0 = chunk * CHUNK, count = min(CHUNK, n - i0);
+  const int count = min(CHUNK, n - i0);
   if (count <= 0) return;
   const bool still = a.in_place && n == len;  // everything stays where it is
   // the chunks ahead of this one that read from the slots that it writes
   int first = 0, end = 0;
   if (ordered && n < len) {
-    const int* from = ws.from + (size_t)b * chunks + chunk;
-    first = from[0] / CHUNK;
-    end = min(chunk, (chunk + 1 < chunks && i0 + CHUNK < len ? from[1] + CHUNK - 1 : n + CHUNK - 1) / CHUNK);
+    first = from0 / CHUNK;
+    end = min(chunk, (chunk + 1 < chunks && i0 + CHUNK < len ? from1 + CHUNK - 1 : n + CHUNK - 1) / CHUNK);
   }
   if (tid < count) {
-    const int from = a.kept[b * a.kept_stride + i0 + tid];
-    s_kept[tid] = from;
-    const long long so = record_offset(a.src, b, from), d = record_offset(a.dst, b, i0 + tid);
+    s_kept[tid] = slot;
+    const long long so = record_offset(a.src, b, slot), d = record_offset(a.dst, b, i0 + tid);
     if (!still && (so < 0 || d < 0)) atomicOr(a.status, ST_UNMAPPED_PAGE);
     s_src[tid] = so < 0 || d < 0 || still ? -1 : so;
     s_dst[tid] = d;
