@@ -114,10 +114,15 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(EvictArgs a, Work
       }
       if (cs > 1) cluster_sync_all(); else __syncthreads();
       if (tid < 256) {
-        int n = hist[pass][tid];
         const uint32_t at = smem_u32(&hist[pass][tid]);
-        for (int k = 0; k < cs; ++k)
-          if (k != rank) n += ld_dsmem_i32(mapa_shared(at, k));
+        int v[MAX_CS], n = hist[pass][tid];
+        if (cs > 1) {
+#pragma unroll
+          for (int k = 0; k < MAX_CS; ++k)  // (all on their way at once)
+            v[k] = k < cs && k != rank ? ld_dsmem_i32(mapa_shared(at, k)) : 0;
+#pragma unroll
+          for (int k = 0; k < MAX_CS; ++k) n += v[k];
+        }
         s_tot[tid] = n;
       }
       __syncthreads();
@@ -167,12 +172,13 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(EvictArgs a, Work
   if (tid == 0) s_cnt = sum;
   if (cs > 1) {
     cluster_sync_all();
-    for (int k = 0; k < rank; ++k) {
-      uint64_t v;
+    uint64_t v = 0;  // a lane per CTA ahead of this one
+    if ((tid & 31) < rank)
       asm volatile("ld.shared::cluster.u64 %0, [%1];"
-                   : "=l"(v) : "r"(mapa_shared(smem_u32(&s_cnt), k)) : "memory");
-      at += v;
-    }
+                   : "=l"(v) : "r"(mapa_shared(smem_u32(&s_cnt), tid & 31)) : "memory");
+#pragma unroll
+    for (int o = MAX_CS / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    at += __shfl_sync(0xffffffffu, v, 0);
   }
   int sure = (int)(at >> 32), equal = (int)(at & 0xffffffffu);  // before this thread's slots
   for (int t = u0; t < u1; ++t) {
