@@ -14,8 +14,8 @@
 // places behind).  Chunks are handed out in order, so a chunk waits only for chunks that have begun,
 // and those publish their loads before they wait.  Weights move the same way.
 // Bound by HBM and the chain of lookups ahead of a chunk's loads: each kept record is read once and
-// written once.  Measured: 8 caches of 33K..64K tokens of 528 bytes cut to 32K, 67 us, of which the
-// selection takes 17 and the move 47 (274 MB; copy: 40 us).
+// written once.  Measured: 8 caches of 33K..64K tokens of 528 bytes cut to 32K, 64 us, of which the
+// selection takes 16 and the move 47 (274 MB; copy: 40 us); 3 of up to 5K tokens 13 us, latencies.
 #include <algorithm>
 
 #include "cache_kernels.h"
@@ -71,7 +71,8 @@ struct Work {
   int* from;     // [n_req][chunks]: kept tokens below the chunk's first slot
 };
 
-__global__ void __launch_bounds__(THREADS) evict_select_kernel(EvictArgs a, Work ws, int cs, int chunks) {
+// (two CTAs an SM: with one, clusters of 16 wait for one another's places)
+__global__ void __launch_bounds__(THREADS, 2) evict_select_kernel(EvictArgs a, Work ws, int cs, int chunks) {
   extern __shared__ float s_w[];  // the run's weights
   __shared__ int hist[4][256];
   __shared__ int s_tot[256], s_digit, s_need;
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(EvictArgs a, Work
 #pragma unroll 1
     for (int pass = 0; pass < 4 && need > 0; ++pass) {
       const int shift = 24 - 8 * pass;
+#pragma unroll 4
       for (int t = max(t0, lo) + tid; t < min(t1, hi); t += THREADS) {
         const uint32_t k = weight_key(cached ? s_w[t - t0] : w[t]);
         if ((k & mask) == key) atomicAdd(&hist[pass][(k >> shift) & 255], 1);
@@ -129,9 +131,9 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(EvictArgs a, Work
       if (tid < 32) {
         // the digit whose tokens, with those of the larger ones, first reach `need`: eight digits
         // a lane, from the largest down
-        int n = 0;
+        int n = 0, v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) n += s_tot[255 - 8 * tid - e];
+        for (int e = 0; e < 8; ++e) v[e] = s_tot[255 - 8 * tid - e], n += v[e];
         int incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -141,8 +143,9 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(EvictArgs a, Work
         const uint32_t m = __ballot_sync(0xffffffffu, incl >= need);
         if (tid == __ffs(m) - 1) {
           int left = need - (incl - n), d = 255 - 8 * tid;
-#pragma unroll 1
-          for (int e = 0; e < 7 && s_tot[d] < left; ++e) left -= s_tot[d--];
+#pragma unroll
+          for (int e = 0; e < 7; ++e)
+            if (d == 255 - 8 * tid - e && v[e] < left) left -= v[e], --d;
           s_digit = d;
           s_need = left;
         }
@@ -163,6 +166,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(EvictArgs a, Work
     return k > key ? 1 : k == key ? 2 : 0;
   };
   uint64_t mine = 0;
+#pragma unroll 4
   for (int t = u0; t < u1; ++t) {
     const int s = state(t);
     mine += s == 1 ? 1ull << 32 : s == 2 ? 1ull : 0ull;
