@@ -86,13 +86,13 @@ __device__ __forceinline__ bool bar_any(int id, bool v) {
   return r != 0;
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// A wait for an mbarrier phase by a whole warp, in few instructions: some 10^7 polls (a good part
-// of a second) at most, none once another wait has run out.  False if it ran out.
+// A wait for an mbarrier phase by a whole warp, in few instructions: some 10^6 polls (a second or
+// two) at most, none once another wait has run out.  False if it ran out.
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
   uint32_t polls = 0;
 #pragma unroll 1
   while (!mbar_try_wait(bar, parity)) {
-    if (*abort || ++polls == (1u << 23)) {
+    if (*abort || ++polls == (1u << 20)) {
       atomicOr(status, ST_WAIT_TIMEOUT);
       *abort = 1;
       polls = ~0u;

@@ -513,7 +513,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     Meta<WIDE>& meta = ss.meta[qb];
     if (t < 32) {
       const int n = group_rows(a, sh, plan, im.b, im.group, meta.row, meta.pos);
-      if (lane == 0) meta.cols = (n * cheads + 15) & ~15, meta.nrows = n;
+      const int cols = (n * cheads + 15) & ~15;
+      if (lane == 0) meta.cols = cols == 80 ? 96 : cols, meta.nrows = n;  // (four groups' columns)
     }
     bar_sync<N>(BAR);
     const int nqp = meta.cols, nq = meta.nrows * cheads;

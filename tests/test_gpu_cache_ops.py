@@ -946,3 +946,105 @@ def test_attend_negative_token_scales(rows):
                                             n_weights=L)
     assert st == 0 and (np.abs(o - eo) <= tol).all() and (np.abs(lse - el) <= ltol).all()
     assert (np.abs(w - ew) <= wtol + 2.0 ** -24 * (rows * 64 + 2) * ew).all()
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 6, 7])
+@pytest.mark.parametrize("window", [0, 200])
+def test_attend_rows_per_request(n, window):
+    """Every number of query columns: 16 heads a slice times n rows, as one group or two."""
+    check_attend(_m(), FULL, [700, 130], [n, n], seed=70 + n, window=window, sinks=2 * (window > 0))
+
+
+BIG = dict(n_q_heads=256, head_dim=64, kv_dim=1024, block_size=32, kv_record_bytes=1040)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4])
+def test_attend_widest_records(rows):
+    check_attend(_m(), BIG, [300, 45], [rows, 1], seed=80 + rows)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 6], ids=["narrow", "narrow2", "wide"])
+@pytest.mark.parametrize("down", [False, True], ids=["rising", "falling"])
+def test_attend_scores_that_rise_by_orders(rows, down):
+    """Values, and with them scores, that grow along the context: the running reference has to move
+    many times, and by more than an exponential can hold."""
+    m = _m()
+    L = 2000
+    table, cache = make_cache(FULL, [L], seed=90 + rows)
+    for t in range(L):
+        rec = cache[table[0, t // 128], t % 128]
+        x = (L - 1 - t if down else t) / L
+        rec[512:516] = (rec[512:516].view(np.float32) * np.float32(0.02 * 3000.0 ** x)).view(np.uint8)
+    q = make_q(FULL, rows, 5)
+    pos = list(range(L - rows, L))
+    o, lse, w, st = run_attend(m, FULL, q, pos, [0] * rows, table, cache, weights=torch.zeros((1, L)))
+    eo, tol, el, ltol, ew, wtol = co.attend(FULL, q.double().numpy(), pos, [0] * rows, table, cache,
+                                            n_weights=L)
+    assert st == 0 and (np.abs(o - eo) <= tol).all() and (np.abs(lse - el) <= ltol).all()
+    # (each of the rows * 64 weights that a token's sum is of is an f32: below 2^-126 it may be 0)
+    assert (np.abs(w - ew) <= wtol + 2.0 ** -24 * (rows * 64 + 2) * ew + rows * 64 * 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("rows", [1, 6], ids=["narrow", "wide"])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attend_nan_records_outside_the_view(rows, causal):
+    """NaN codes and scales in every token that no row sees, and behind the rows that are ahead of
+    them: window, first tokens, later rows' tokens."""
+    m = _m()
+    L, W, S = 900, 300, 3
+    table, cache = make_cache(FULL, [L], seed=95)
+    pos = list(range(L - 30, L - 30 + rows))
+    hi = pos[-1]
+    first = (pos[0] if causal else hi) - W + 1
+    for t in range(L):
+        if not (t <= hi and (t >= first or t < S)):
+            cache[table[0, t // 128], t % 128] = 0x7F
+    q = make_q(FULL, rows, 6)
+    kw = dict(window=W, sinks=S, causal=causal)
+    o, lse, w, st = run_attend(m, FULL, q, pos, [0] * rows, table, cache, weights=torch.zeros((1, L)),
+                               **kw)
+    eo, tol, el, ltol, ew, wtol = co.attend(FULL, q.double().numpy(), pos, [0] * rows, table, cache, W,
+                                            S, causal, n_weights=L)
+    assert st == 0 and (np.abs(o - eo) <= tol).all() and (np.abs(lse - el) <= ltol).all()
+    assert (np.abs(w - ew) <= wtol + 2.0 ** -24 * (rows * 64 + 2) * ew).all()
+    # a later row's token that holds NaN reaches the rows that see it, and no other
+    if rows > 1 and causal:
+        t = pos[3]
+        cache[table[0, t // 128], t % 128, :512] = 0x7F
+        o, _, _, st = run_attend(m, FULL, q, pos, [0] * rows, table, cache, **kw)
+        assert st == 0 and np.isnan(o[3:]).all() and (np.abs(o[:3] - eo[:3]) <= tol[:3]).all()
+
+
+def test_attend_largest_step():
+    """1024 rows of 512 requests, in any order, some of them pad rows."""
+    rng = np.random.default_rng(7)
+    lengths = rng.integers(2, 40, 512).tolist()
+    check_attend(_m(), TINY, lengths, [2] * 511 + [1], seed=97, pads=(5,), shuffle=True)
+
+
+def test_two_caches_at_once():
+    """Two handles on two streams give what each gives alone."""
+    m = _m()
+    dev = torch.device("cuda")
+    sets = []
+    for k, (spec, n) in enumerate([(FULL, 1), (FULL, 6), (WIDE, 3)]):
+        lengths = [3000 + 501 * k, 700]
+        table, cache = make_cache(spec, lengths, seed=98 + k)
+        pos = [p for L in lengths for p in range(L - n, L)]
+        req = [b for b in range(2) for _ in range(n)]
+        q = make_q(spec, 2 * n, 98 + k).to(dev)
+        args = (torch.tensor(pos, dtype=torch.int32, device=dev),
+                torch.tensor(req, dtype=torch.int32, device=dev),
+                torch.from_numpy(table).to(dev), torch.from_numpy(cache).to(dev))
+        h = m.Cache(spec, max_rows=2 * n, max_requests=2)
+        alone = torch.empty_like(q)
+        h.attend(q, alone, *args)
+        sets.append((h, q, args, alone, torch.cuda.Stream(), [torch.empty_like(q) for _ in range(20)]))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for h, q, args, _, s, outs in sets:
+            h.attend(q, outs[i], *args, stream=s)
+    torch.cuda.synchronize()
+    for h, _, _, alone, _, outs in sets:
+        assert h.status() == 0 and all(torch.equal(alone, x) for x in outs)
+        h.close()
