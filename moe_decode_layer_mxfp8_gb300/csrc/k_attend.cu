@@ -97,8 +97,8 @@ struct Form {
   static_assert(SF_P + (WIDE ? 0 : 4 * SLOTS) <= 512, "TMEM");
   // log2 of a weight times its token's scale: m puts the largest of the tile that moves it at BASE
   // or just below, and moves again when one passes 2^15 (narrow: 2); scales below 2^LEAST (and zeros)
-  // count as that
-  static constexpr float BASE = WIDE ? 0.0f : -30.0f, LEAST = WIDE ? -90.0f : -60.0f;
+  // count as that.  (What f16 cannot hold lies 2^-31 below that largest; narrow blocks have scales.)
+  static constexpr float BASE = WIDE ? 6.0f : -30.0f, LEAST = WIDE ? -90.0f : -60.0f;
 };
 // registers a thread in the wide form: softmax warps take what the others give up (in all, the
 // launch's)
@@ -114,7 +114,7 @@ struct Args {
   int box;                    // 0: no maps
   AttendArgs a;
   Shape sh;
-  float* part;    // workspace (Pieces)
+  float* part;  // workspace (Pieces)
   RowInfo* rows;
 };
 
@@ -432,8 +432,9 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
           *reinterpret_cast<uint4*>(&sh.most[warp][g]) = make_uint4(mb[g], mb[g + 1], mb[g + 2], mb[g + 3]);
       }
       const int ch = (deal.p_byte(w.first) + w.c0) >> 4, cl = ch + (deal.nqp >> 4);
-      *reinterpret_cast<uint4*>(prow + deal.p_odd(i) * K_TILE + ((ch ^ (tok & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(prow + deal.p_odd(i) * K_TILE + ((cl ^ (tok & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      prow += deal.p_odd(i) * K_TILE;
+      *reinterpret_cast<uint4*>(prow + ((ch ^ (tok & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(prow + ((cl ^ (tok & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       __syncwarp();
       {
         const int n = w.c0 + (lane & 15) + (lane >> 4) * deal.nqp;

@@ -14,7 +14,8 @@ namespace {
 // zeros.  Bound by latency (2 to 4.5 us): a lane per piece fetches m and l while the first pieces' O is
 // on its way.  (Joined by the team that brings the last piece, 48 rows took 9 us longer.)
 constexpr int JOIN_WARPS = 4, AHEAD = 4;
-__global__ void __launch_bounds__(JOIN_WARPS * 32) attend_join_kernel(const AttendArgs a, const Shape sh, const Pieces ar) {
+__global__ void __launch_bounds__(JOIN_WARPS * 32) attend_join_kernel(const AttendArgs a, const Shape sh,
+                                                                      const Pieces ar) {
   const int r = blockIdx.x, h = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int chunk = h / sh.heads, hpg = a.n_q / (a.kv_dim / a.head_dim);
   const int cheads = hpg * (min(128, a.kv_dim - 128 * chunk) > a.head_dim ? 2 : 1);
