@@ -14,8 +14,8 @@
 // places behind).  Chunks are handed out in order, so a chunk waits only for chunks that have begun,
 // and those publish their loads before they wait.  Weights move the same way.
 // Bound by HBM and the chain of lookups ahead of a chunk's loads: each kept record is read once and
-// written once.  Measured: 8 caches of 33K..64K tokens of 528 bytes cut to 32K, 64 us, of which the
-// selection takes 16 and the move 47 (274 MB; copy: 40 us); 3 of up to 5K tokens 13 us, latencies.
+// written once.  Measured: 8 caches of 33K..64K tokens of 528 bytes cut to 32K, 62 us, of which the
+// selection takes 14 and the move 47 (274 MB; copy: 40 us); 3 of up to 5K tokens 12 us, latencies.
 #include <algorithm>
 
 #include "cache_kernels.h"
@@ -75,7 +75,7 @@ struct Work {
 __global__ void __launch_bounds__(THREADS, 2) evict_select_kernel(EvictArgs a, Work ws, int cs, int chunks) {
   extern __shared__ float s_w[];  // the run's weights
   __shared__ int hist[4][256];
-  __shared__ int s_tot[256], s_digit, s_need;
+  __shared__ int s_tot[256], s_digit, s_need, s_last;
   __shared__ uint64_t warp_sums[WARPS], s_cnt;
   pdl_trigger();
   pdl_wait();
@@ -148,12 +148,14 @@ __global__ void __launch_bounds__(THREADS, 2) evict_select_kernel(EvictArgs a, W
             if (d == 255 - 8 * tid - e && v[e] < left) left -= v[e], --d;
           s_digit = d;
           s_need = left;
+          s_last = s_tot[d] == left;  // all of the digit's stay: its lower bits need no look
         }
       }
       __syncthreads();
       key |= (uint32_t)s_digit << shift;
       need = s_need;
       mask |= 255u << shift;
+      if (s_last) break;  // (alike in the cluster)
     }
   }
   // how many of this thread's slots stay for sure, and how many are equal to the threshold
