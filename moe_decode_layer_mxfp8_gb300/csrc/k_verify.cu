@@ -10,7 +10,7 @@
 // the threshold finds the block and reads it again, in order.  A request whose residual is empty
 // takes a second pass over p.
 // Bound by reading the one row pair that the token is drawn from; small ones by latencies.
-// Measured: 192 requests of 3 drafts, 100003 bf16 entries, a quarter of them greedy 29 us (77 MB; copy:
+// Measured: 192 requests of 3 drafts, 100003 bf16 entries, a quarter of them greedy 28.5 us (77 MB; copy:
 // 11 us), 8 of 5 drafts, 131072 f32 entries 10.5 us, 4 of 2 table drafts, 32000 f16 entries 7.2 us.
 // Sums decide which token is drawn, so they are carried as pairs of f32 (error-free additions and
 // products, and p - q as a pair): FP64 runs at a 64th of the FP32 rate here, and a search in f64 took
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(THREADS, 3) verify_kernel(VerifyArgs a, int cs
       const int nv = (d.vectors() + runs - 1) / runs, first = run * nv;
       const int last = min(first + nv, d.vectors());
       // a lane's first largest vector, kept as it was loaded
-      constexpr int U = 8;  // (loaded at a time)
+      constexpr int U = 10;  // (loaded at a time)
       float top = -INFINITY;
       int at = -1;
       Vec<T> kept = {};
