@@ -691,7 +691,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 #pragma unroll 1
         for (int i = max(0, im.n - MMA_WARPS); i < im.n; ++i)  // all are done when each warp's last is
           wait(&ss.pv_done[deal.slot(i)], deal.parity(ph, i), a.status, abort);
-        if (MMA_WARPS > 1) bar_sync<32 * MMA_WARPS>(11);  // (neither runs ahead of the phases that the other waits for)
+        // (neither runs ahead of the phases that the other waits for)
+        if (MMA_WARPS > 1) bar_sync<32 * MMA_WARPS>(11);
         it += im.n;
         deal.advance(ph, im.n);
       }
