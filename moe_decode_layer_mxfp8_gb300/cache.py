@@ -120,8 +120,10 @@ _BF16, _F32 = (torch.bfloat16,), (torch.float32,)
 _PROBS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
-# (what torch.cuda.current_stream and current_device ask, without their wrappers: 2 us of a call)
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# What torch.cuda.current_stream and current_device ask, without their wrappers (2 us of a call); not
+# in a torch built without CUDA.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _call(name, device, stream, *args):
