@@ -36,7 +36,7 @@
 // fourth tile each, with 32 two groups share every other tile, with more the groups share all
 // tiles.  Then come the warps that make the next item's queries while the current one runs (in the
 // wide form they widen tiles too), those that issue the first product's MMAs, the second's, and two
-// that load (every other tile each: TMA boxes through the page table, or cp.async for page sizes
+// that load (every other slot of the ring each: TMA boxes through the page table, or cp.async for page sizes
 // that are no multiple of 8).  A wait for a barrier that is complete still costs a warp 100 to 300
 // cycles, an MMA's issue some 60: hence two warps for each product in the narrow form, whose tiles
 // take 700 cycles, and one wait per tile in the softmax.  What runs once per launch or item is kept
@@ -568,8 +568,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   if (warp >= SOFT_WARPS) {
     if constexpr (WIDE) regs_down<OTHER_REGS>();
     if (warp >= LOAD_WARP) {
-      // ------------------------------------------------------- loads: a warp takes every other tile
-      int ni = warp - LOAD_WARP;
+      // ---------------------- loads: each slot of the ring has one loading warp (every other slot's:
+      // a wait by parity is for the phase that is meant only where the waiter saw the one before)
+      const int lw = warp - LOAD_WARP;
+      int ni = lw;
       TileLoader tile(ar.box);
       auto locate = [&]() {
 #pragma unroll 1
@@ -578,13 +580,15 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       };
       locate();
 #pragma unroll 1
-      for (int it = warp - LOAD_WARP; more; it += LOAD_WARPS) {
+      for (int it = lw; more;) {
         const int s = it % ST;
         bool go = true;
         if (it >= ST) go = wait(&ss.k_free[s], ((it / ST) - 1) & 1, a.status, abort);
         tile.load(a, im, ar.codes, ar.scales, chunk, sm + F::K_OFF + s * K_TILE, sm + F::SC_OFF + s * TT * 16,
                   ss.valid[s], &ss.full[s], go);
-        ni += LOAD_WARPS;
+        const int step = ST % LOAD_WARPS == 0 || s + LOAD_WARPS < ST ? LOAD_WARPS : ST - s + lw;
+        it += step;
+        ni += step;
         locate();
       }
     } else if (warp >= PREP_WARP && warp < PREP_WARP + PREP / 32) {
