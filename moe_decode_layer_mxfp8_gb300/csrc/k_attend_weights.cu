@@ -114,7 +114,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_weights_kernel(const __grid
   auto passes = [&](const Job& j) { return (plan.cnt[j.b] + ar.pass - 1) / ar.pass; };
 
   if (warp >= LOAD_WARP) {
-    // ------------------------------------------------------- loads: a warp takes every fourth tile
+    // ---------------- loads: each slot of the ring has one loading warp (a wait by parity is for the
+    // phase that is meant only where the waiter saw the one before)
     int it = 0;
     TileLoader tile(ar.box);
 #pragma unroll 1
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_weights_kernel(const __grid
       for (int p = passes(im); p > 0; --p) {
 #pragma unroll 1
         for (Walk w(im.n, chunks); w.more(); w.next(), ++it) {
-          if (it % LOAD_WARPS != warp - LOAD_WARP) continue;
+          if (it % ST % LOAD_WARPS != warp - LOAD_WARP) continue;
           const int s = it % ST;
           tile.locate(a, im, w.at());
           bool go = true;

@@ -80,6 +80,120 @@ class Machine:
         return kind == "tell" or (bar.phase > k if kind == "sync" else (bar.phase & 1) != (k & 1))
 
 
+# ------------------------------------------------------------------ the gathering of weights
+WEIGHTS = "k_attend_weights.cu"
+
+
+def weights_model(items, chunks, lg, by_slot, both, seed):
+    """items: (tiles, passes) each; by_slot: a slot of the ring has one loading warp; both: either MMA
+    warp waits for every tile and gives it back."""
+    ST, LOADERS, MMAS = (constant(n, WEIGHTS) for n in ("ST", "LOAD_WARPS", "S_WARPS"))
+    GROUPS = 4
+    m = Machine(seed)
+    full, k_free = [Bar(2) for _ in range(ST)], [Bar(1 + (MMAS if both else 1)) for _ in range(ST)]
+    s_full, s_free = [Bar(2) for _ in range(2 * GROUPS)], [Bar(1) for _ in range(2 * GROUPS)]
+    holds = [None] * ST  # the tile whose codes, scales and bits a slot holds
+    q_full, mma_sync, soft_sync = Bar(GROUPS), Bar(MMAS), Bar(GROUPS)
+
+    def walk(n):  # (place in a row, chunk, first tile of the row, its width)
+        for i in range(0, n, GROUPS):
+            width = min(GROUPS, n - i)
+            for c in range(chunks):
+                for tile in range(width):
+                    yield tile, c, i, width
+
+    def loader(w):
+        it = 0
+        for n, passes in items:
+            for _ in range(passes):
+                for _ in walk(n):
+                    s = it % ST
+                    if (s if by_slot else it) % LOADERS == w:
+                        if it >= ST:
+                            yield "wait", k_free[s], it // ST - 1
+
+                        def land(s=s, it=it):
+                            holds[s] = it
+                            full[s].arrive()
+                        yield land
+                        full[s].arrive()
+                        yield 0
+                    it += 1
+
+    def mma(w):
+        it, done, used = 0, 0, [0] * GROUPS
+        for n, passes in items:
+            for _ in range(passes):
+                yield "wait", q_full, done
+                done += 1
+                mma_sync.arrive()
+                yield "sync", mma_sync, done - 1
+                for tile, _, _, _ in walk(n):
+                    st = it % ST
+                    if both or tile & 1 == w:
+                        yield "wait", full[st], it // ST
+                    if tile & 1 != w:
+                        if both:
+                            k_free[st].arrive()
+                    else:
+                        assert holds[st] == it, "a product of another tile"
+                        k = used[tile]
+                        used[tile] += 1
+                        b = tile + (k & lg) * GROUPS
+                        if k >> lg:
+                            yield "wait", s_free[b], (k >> lg) - 1
+                        s_full[b].arrive()
+
+                        def done_(b=b, st=st):
+                            s_full[b].arrive()
+                            k_free[st].arrive()
+                        yield done_
+                        yield 0
+                    it += 1
+
+    def soft(g):
+        it, k, done = 0, 0, 0
+        for n, passes in items:
+            for _ in range(passes):
+                soft_sync.arrive()
+                yield "sync", soft_sync, done
+                done += 1
+                q_full.arrive()
+                for i in range(0, n, GROUPS):
+                    width = min(GROUPS, n - i)
+                    for c in range(chunks):
+                        if g < width:
+                            b, at = g + (k & lg) * GROUPS, it + c * width + g
+                            yield "wait", s_full[b], k >> lg
+                            assert holds[at % ST] == at, "the bits of another tile"
+                            k_free[at % ST].arrive()
+                            yield 0
+                            s_free[b].arrive()
+                            k += 1
+                    it += chunks * width
+
+    for w in range(LOADERS):
+        m.add(loader(w))
+    for w in range(MMAS):
+        m.add(mma(w))
+    for g in range(GROUPS):
+        m.add(soft(g))
+    m.run()
+
+
+def run_weights(chunks, lg, by_slot, both):
+    for seed in range(60):
+        rng = random.Random(seed)
+        weights_model([(rng.choice([1, 2, 3, 4, 5, 7, 9]), rng.choice([1, 1, 2, 3])) for _ in range(3)],
+                      chunks, lg, by_slot, both, seed)
+
+
+@pytest.mark.parametrize("lg", [0, 1])
+@pytest.mark.parametrize("chunks", [1, 2, 4, 8])
+def test_weights_tiles_are_loaded_into_free_slots(chunks, lg):
+    run_weights(chunks, lg, has(WEIGHTS, "it % ST % LOAD_WARPS"), True)
+
+
 # ------------------------------------------------------------------------------ the attention
 def attend_model(wide, items, seed):
     """items: (tiles, columns) each.  A softmax group's four warps are one role (they meet at every

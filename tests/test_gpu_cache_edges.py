@@ -52,3 +52,11 @@ def repeats(m, spec, lengths, rows_per, seed, times=40, weights=False, **kw):
 def test_attend_groups_of_few_columns_among_wide_ones(rows):
     """Requests of 6 rows (96 columns) with remainders of 16 and 32 columns, many tiles each."""
     repeats(_m(), FULL, [2900 + 777 * i for i in range(len(rows))], rows, seed=sum(rows))
+
+
+@pytest.mark.parametrize("spec,lengths,rows", [
+    (FULL, [3000 + 128 * i for i in range(8)], [1] * 8), (WIDE, [2111, 6400, 900], [5, 1, 3]),
+    (BIG, [4700, 1300], [1, 2]), (TINY, [9000] * 12, [2] * 12)], ids=["full", "wide", "big", "tiny"])
+def test_attend_weights_over_many_tiles(spec, lengths, rows):
+    """One to eight chunks a tile, runs of tiles of every remainder by four."""
+    repeats(_m(), spec, lengths, rows, seed=len(lengths), weights=True)
