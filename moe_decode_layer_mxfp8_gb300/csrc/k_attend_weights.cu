@@ -92,8 +92,9 @@ __global__ void __launch_bounds__(THREADS, 1) attend_weights_kernel(const __grid
   const int chunks = sh.chunks, cols = ar.pad * ar.pass, tail = a.kv_dim - 128 * (chunks - 1);
   const int lg = cols <= 16 ? 1 : 0;  // 2^lg slots of scores a group
   if (tid == 0) {
-    // a tile is free when the product and a group's warps have read it
-    for (int s = 0; s < ST; ++s) mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], 1 + 4);
+    // a tile is free when the product and a group's warps have read it, and the other issuing warp has
+    // seen it
+    for (int s = 0; s < ST; ++s) mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], S_WARPS + 4);
     for (int s = 0; s < 2 * GROUPS; ++s) mbar_init(&ss.s_full[s], 1), mbar_init(&ss.s_free[s], 4);
     mbar_init(&ss.q_full, SOFT_WARPS);
     mbar_init(&ss.drain, S_WARPS);
@@ -157,11 +158,16 @@ __global__ void __launch_bounds__(THREADS, 1) attend_weights_kernel(const __grid
         __syncwarp();
 #pragma unroll 1
         for (Walk w(im.n, chunks); w.more(); w.next(), ++it) {
-          if ((w.tile & 1) != mine) continue;
           const int st = it % ST, hi = w.tile >> 1;
+          // (the other warp's tiles too, and before they may go: a wait by parity is for the phase that
+          // is meant only where the waiter saw the one before)
+          bool ok = wait(&ss.full[st], (it / ST) & 1, a.status, abort);
+          if ((w.tile & 1) != mine) {
+            if (lane == 0) mbar_arrive(&ss.k_free[st]);
+            continue;
+          }
           const uint32_t k = hi ? used[1]++ : used[0]++;
           const int b = w.tile + (k & lg) * GROUPS;  // the group's slot
-          bool ok = wait(&ss.full[st], (it / ST) & 1, a.status, abort);
           if ((k >> lg) > 0) ok &= wait(&ss.s_free[b], ((k >> lg) - 1) & 1, a.status, abort);
           if (ok && elect_one()) {
             tc_fence_after();

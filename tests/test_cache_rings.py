@@ -194,6 +194,12 @@ def test_weights_tiles_are_loaded_into_free_slots(chunks, lg):
     run_weights(chunks, lg, has(WEIGHTS, "it % ST % LOAD_WARPS"), True)
 
 
+@pytest.mark.parametrize("lg", [0, 1])
+@pytest.mark.parametrize("chunks", [1, 2, 4, 8])
+def test_weights_products_wait_for_their_own_tiles(chunks, lg):
+    run_weights(chunks, lg, True, has(WEIGHTS, "mbar_init(&ss.k_free[s], S_WARPS + 4)"))
+
+
 # ------------------------------------------------------------------------------ the attention
 def attend_model(wide, items, seed):
     """items: (tiles, columns) each.  A softmax group's four warps are one role (they meet at every
