@@ -241,7 +241,7 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
 #pragma unroll 1
   for (int i = w.first; i < w.n; i += w.stride) {
     const int st = (w.it + i) % F::ST, b = deal.slot(i);
-    wait(&sh.s_full[b], deal.parity(w.ph, i), a.status, abort);  // (so the tile is there)
+    wait(&sh.s_full[b], deal.parity(w.ph, i), a.status, abort);  // (and the tile's scales)
     const float raw = reinterpret_cast<const float*>(sm + F::SC_OFF)[(st * TT + tok) * 4];
     const uint32_t ok = sh.valid[st][quad];
     const bool fin = fabsf(raw) <= 3.0e38f;
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], WIDE ? 1 + PREP / 32 + SOFT_WARPS : 1);
     for (int s = 0; s < 2; ++s) mbar_init(&ss.v_full[s], PREP / 32), mbar_init(&ss.v_free[s], 1);
     for (int s = 0; s < SLOTS; ++s)
-      mbar_init(&ss.s_full[s], 1), mbar_init(&ss.pv_done[s], 1), mbar_init(&ss.p_full[s], SOFT_WARPS);
+      mbar_init(&ss.s_full[s], 2), mbar_init(&ss.pv_done[s], 1), mbar_init(&ss.p_full[s], SOFT_WARPS);
     // an item's queries are free with its first products, the rest of what was made with them when
     // all that read it or wait for it are done
     for (int s = 0; s < 2; ++s)
@@ -688,6 +688,10 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
                           idesc | ((uint32_t)(k & 3) << 4) | ((uint32_t)(k & 3) << 29), ones, sf, k > 0);
             tc_commit(&ss.s_full[b]);
             if (WIDE) tc_commit(&ss.k_free[st]);
+            // This thread has waited for the copies, and its arrival here (a release; the commit's is
+            // none) passes what they wrote on to the softmax warps, which read the scales and, to
+            // clear masked codes, the tile behind this barrier alone.
+            mbar_arrive(&ss.s_full[b]);
           }
           __syncwarp();
         }
@@ -803,7 +807,8 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         else
           soft_tiles<WIDE, F::CMAX>(a, w, deal, meta, ss, sm, l);
       }
-      // every product of the item is done when each issuing warp's last is
+      // every product of the item is done when each issuing warp's last is (a group that has no part in
+      // a tile may pass its barrier a phase early; the barrier below holds it until those that have are here)
 #pragma unroll 1
       for (int i = max(0, w.n - MMA_WARPS); i < w.n; ++i)
         wait(&ss.pv_done[deal.slot(i)], deal.parity(w.ph, i), a.status, abort);
@@ -854,6 +859,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         }
       }
       bar_sync<SOFT>(10);
+      tc_fence_after();
       const int d = 32 * quad + lane;  // this thread's dimension of the chunk
       const int sl = d >> dshift, dl = d - (sl << dshift);
 #pragma unroll 1

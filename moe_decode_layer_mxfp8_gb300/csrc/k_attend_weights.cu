@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_weights_kernel(const __grid
     // a tile is free when the product and a group's warps have read it, and the other issuing warp has
     // seen it
     for (int s = 0; s < ST; ++s) mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], S_WARPS + 4);
-    for (int s = 0; s < 2 * GROUPS; ++s) mbar_init(&ss.s_full[s], 1), mbar_init(&ss.s_free[s], 4);
+    for (int s = 0; s < 2 * GROUPS; ++s) mbar_init(&ss.s_full[s], 2), mbar_init(&ss.s_free[s], 4);
     mbar_init(&ss.q_full, SOFT_WARPS);
     mbar_init(&ss.drain, S_WARPS);
     ss.abort = 0;
@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_weights_kernel(const __grid
                           sf + 4 * w.chunk, e > 0);
             tc_commit(&ss.s_full[b]);
             tc_commit(&ss.k_free[st]);
+            mbar_arrive(&ss.s_full[b]);  // (see k_attend.cu)
           }
           __syncwarp();
         }
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_weights_kernel(const __grid
           for (int chunk = 0; chunk < chunks; ++chunk, ++k) {
             const uint32_t at = it + chunk * width + group, st = at % ST;
             const int b = group + (k & lg) * GROUPS;
-            wait(&ss.s_full[b], (k >> lg) & 1, a.status, abort);  // (so the tile is there)
+            wait(&ss.s_full[b], (k >> lg) & 1, a.status, abort);  // (and the tile's scales)
             if (chunk == 0) {
               const float raw = reinterpret_cast<const float*>(sm + SC_OFF)[(st * TT + tok) * 4];
               const uint32_t ok = ss.valid[st][quad];

@@ -5,7 +5,9 @@ A wait for a barrier's phase is by parity: it passes as soon as the barrier's cu
 other one, so it means the phase that was meant only where the waiter knows that the phase before has
 completed.  The model's roles wait and arrive as the kernels' do (ring sizes and warp counts are read
 from the sources); the scheduler holds back some roles, copies and products for long, and every wait
-that passes is checked against the phase that it was meant for."""
+that passes is checked against the phase that it was meant for.  What a copy has written is visible to
+those that waited for it, or for a thread that had and then arrived; the arrival of a product's commit
+says nothing of the copies before it."""
 import os
 import random
 import re
@@ -30,9 +32,11 @@ def has(file, text):
 
 class Bar:
     def __init__(self, count):
-        self.count, self.pending, self.phase = count, 0, 0
+        self.count, self.pending, self.phase, self.carries = count, 0, 0, set()
 
-    def arrive(self, n=1):
+    def arrive(self, n=1, landed=()):
+        self.carries |= Machine.known
+        self.carries.update(landed)
         self.pending += n
         assert self.pending <= self.count, "more arrivals than a phase has"
         if self.pending == self.count:
@@ -40,6 +44,8 @@ class Bar:
 
 
 class Machine:
+    known = set()  # tiles whose copies the running role knows to have landed
+
     """Roles are generators of ("wait", bar, k): for phase k, by parity; ("sync", bar, k): exactly;
     ("tell", bar, k): nothing passes, k has to be complete; and of functions to call later, in the
     issuing role's order."""
@@ -55,17 +61,20 @@ class Machine:
         lazy = rng.choice([0.02, 0.3, 1.0])
         weight = {r: rng.choice([0.02, 0.3, 1.0]) for r in self.roles}
         at, queue = dict.fromkeys(self.roles), {r: [] for r in self.roles}
+        known = {r: set() for r in self.roles}
         while at or any(queue.values()):
             can = [(weight[r], r, None) for r, op in at.items() if op is None or self.passes(*op)]
             can += [(lazy, None, q) for q in queue.values() if q]
             assert can, "every role waits"
             _, r, q = rng.choices(can, [c[0] for c in can])[0]
+            Machine.known = set() if q else known[r]
             if q:
                 q.pop(0)()
                 continue
             if at[r] is not None:
                 kind, bar, k = at[r]
                 assert bar.phase > k, "a wait passed ahead of its phase"
+                known[r] |= bar.carries
             op = next(r, None)
             while callable(op):
                 queue[r].append(op)
@@ -82,6 +91,7 @@ class Machine:
 
 # ------------------------------------------------------------------ the gathering of weights
 WEIGHTS = "k_attend_weights.cu"
+TOLD = "mbar_arrive(&ss.s_full[b])"  # the issuing thread arrives for scores, beside their commit
 
 
 def weights_model(items, chunks, lg, by_slot, both, seed):
@@ -89,9 +99,10 @@ def weights_model(items, chunks, lg, by_slot, both, seed):
     warp waits for every tile and gives it back."""
     ST, LOADERS, MMAS = (constant(n, WEIGHTS) for n in ("ST", "LOAD_WARPS", "S_WARPS"))
     GROUPS = 4
+    told = has(WEIGHTS, TOLD)
     m = Machine(seed)
     full, k_free = [Bar(2) for _ in range(ST)], [Bar(1 + (MMAS if both else 1)) for _ in range(ST)]
-    s_full, s_free = [Bar(2) for _ in range(2 * GROUPS)], [Bar(1) for _ in range(2 * GROUPS)]
+    s_full, s_free = [Bar(1 + told) for _ in range(2 * GROUPS)], [Bar(1) for _ in range(2 * GROUPS)]
     holds = [None] * ST  # the tile whose codes, scales and bits a slot holds
     q_full, mma_sync, soft_sync = Bar(GROUPS), Bar(MMAS), Bar(GROUPS)
 
@@ -114,7 +125,7 @@ def weights_model(items, chunks, lg, by_slot, both, seed):
 
                         def land(s=s, it=it):
                             holds[s] = it
-                            full[s].arrive()
+                            full[s].arrive(landed=[it])
                         yield land
                         full[s].arrive()
                         yield 0
@@ -142,7 +153,8 @@ def weights_model(items, chunks, lg, by_slot, both, seed):
                         b = tile + (k & lg) * GROUPS
                         if k >> lg:
                             yield "wait", s_free[b], (k >> lg) - 1
-                        s_full[b].arrive()
+                        if told:
+                            s_full[b].arrive()
 
                         def done_(b=b, st=st):
                             s_full[b].arrive()
@@ -165,7 +177,7 @@ def weights_model(items, chunks, lg, by_slot, both, seed):
                         if g < width:
                             b, at = g + (k & lg) * GROUPS, it + c * width + g
                             yield "wait", s_full[b], k >> lg
-                            assert holds[at % ST] == at, "the bits of another tile"
+                            assert holds[at % ST] == at and at in m.known, "the bits of another tile"
                             k_free[at % ST].arrive()
                             yield 0
                             s_free[b].arrive()
@@ -207,11 +219,12 @@ def attend_model(wide, items, seed):
     F, which = "k_attend.cu", 1 if wide else 2
     ST, MMAS = constant("ST", F, which), constant("MMA_WARPS", F, which)
     LOADERS, GROUPS = 2, 4
+    told = has(F, TOLD)
     by_slot = has(F, "each slot of the ring has one loading warp")
     m = Machine(seed)
     full = [Bar(2) for _ in range(ST)]
     k_free = [Bar(2 + 4 if wide else 1) for _ in range(ST)]
-    s_full, pv_done, p_full = ([Bar(c) for _ in range(8)] for c in (2, 1, 4))
+    s_full, pv_done, p_full = ([Bar(c) for _ in range(8)] for c in (1 + told, 1, 4))
     v_full, v_free = [Bar(1), Bar(1)], [Bar(1), Bar(1)]
     q_full, q_free = [Bar(1), Bar(1)], [Bar(MMAS), Bar(MMAS)]
     m_free = [Bar(MMAS + GROUPS), Bar(MMAS + GROUPS)]
@@ -249,7 +262,7 @@ def attend_model(wide, items, seed):
 
             def land(s=s, it=it):
                 holds[s] = it
-                full[s].arrive()
+                full[s].arrive(landed=[it])
             yield land
             full[s].arrive()
             yield 0
@@ -289,7 +302,8 @@ def attend_model(wide, items, seed):
                 assert holds[st] == it + i, "a product of another tile"
                 if i >= d.bufs:
                     yield "wait", pv_done[b], ph.of(d, i - d.bufs)
-                s_full[b].arrive()
+                if told:
+                    s_full[b].arrive()
 
                 def done(b=b, st=st):
                     s_full[b].arrive()
@@ -342,7 +356,7 @@ def attend_model(wide, items, seed):
                 for i in range(stream, n, d.streams):
                     b, st = d.slot(i), (it + i) % ST
                     yield "wait", s_full[b], ph.of(d, i)
-                    assert holds[st] == it + i, "the bits of another tile"
+                    assert holds[st] == it + i and it + i in m.known, "the bits of another tile"
                     arrive = d.streams + (1 if cols == 48 and g == 0 else 0)
                     if wide:
                         k_free[st].arrive(arrive)
