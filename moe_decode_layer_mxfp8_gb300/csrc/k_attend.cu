@@ -96,7 +96,7 @@ struct Form {
                        SF_Q = SF_ONE + 4 * MMA_WARPS, SF_P = SF_Q + 8 * MMA_WARPS;
   static_assert(SF_P + (WIDE ? 0 : 4 * SLOTS) <= 512, "TMEM");
   // log2 of a weight times its token's scale: m puts the largest of the tile that moves it at BASE
-  // or just below, and moves again when one passes 2^15 (narrow: 2); scales below 2^LEAST (and zeros)
+  // or just below, and moves again when one passes 2^15 (narrow: 2^7); scales below 2^LEAST (and zeros)
   // count as that.  (What f16 cannot hold lies 2^-31 below that largest; narrow blocks have scales.)
   static constexpr float BASE = WIDE ? 6.0f : -30.0f, LEAST = WIDE ? -90.0f : -60.0f;
 };
@@ -181,7 +181,7 @@ struct Shared {
   uint64_t q_full[2], q_free[2], m_free[2], o_free, drain;
   alignas(16) float neg_m[NQ];
   float fac[NQ], red[SOFT_WARPS][CMAX];  // m and its change: [stream][column]
-  uint32_t most[SOFT_WARPS][CMAX];  // the warp's columns' largest weights
+  uint32_t most[SOFT_WARPS][CMAX];  // the warp's columns' largest weights (mb)
   uint32_t valid[ST][4];  // tokens that are there
   alignas(16) float fin[4][NQ];  // a column's factor for each stream's O
   Meta<WIDE> meta[2];
@@ -244,9 +244,11 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
     wait(&sh.s_full[b], deal.parity(w.ph, i), a.status, abort);  // (and the tile's scales)
     const float raw = reinterpret_cast<const float*>(sm + F::SC_OFF)[(st * TT + tok) * 4];
     const uint32_t ok = sh.valid[st][quad];
-    const bool fin = fabsf(raw) <= 3.0e38f;
+    // (a token that is not there has whatever was left in its place: no scale)
+    const bool fin = ((ok >> lane) & 1) && fabsf(raw) <= 3.0e38f;
     const float ct = fin ? raw * w.to_log2 : __int_as_float(0x7FC00000);
     const float sc = fin ? raw : 0.0f, size = fabsf(sc);
+    const float size64 = size * 0x1p-6f;
     const float lsc = sc != 0.0f ? fmaxf(log2_of(size), F::LEAST) : F::LEAST;
     if (WIDE) {  // (as many arrivals whoever takes the tile)
       __syncwarp();
@@ -374,13 +376,13 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
         for (int c = 0; c < C; ++c) top = fmaxf(top, s[c]);
         ask = top + lsc > 15.0f;
       } else {
-        // the largest weights times scales of the warp's tokens, as bits; 2 and more (or NaN) asks
-        // for a larger m
+        // the largest weights times scales of the warp's tokens, over 2^6, as bits; 2 and more (or
+        // NaN) asks for a larger m
         uint32_t any = 0;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
           s[c] = ex2(s[c]);
-          mb[c] = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaf(s[c], size, 0x1p-118f)));
+          mb[c] = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaf(s[c], size64, 0x1p-124f)));
           any |= mb[c];
         }
         ask = any >> 30;
@@ -409,8 +411,8 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
       }
     } else {
       // weights times scales as two e4m3 terms, 16 + 16 bytes of the token's row; a column's largest
-      // of the warp's tokens is in [2^7, 2^8)
-      const float up = 64.0f * sc;
+      // of the warp's tokens is in [2^7, 2^8).  The weight meets its scale first: a weight of 0 stays
+      // 0 whatever the scale, where the block's factor, 2^125 at most, times a scale may be infinite
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int g = 0; g < C; g += 4) {
@@ -418,10 +420,10 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
           const int c = g + e;
-          y[e] = __uint_as_float(~mb[c] & 0x7F800000u);  // 2 / the largest's power of two
-          y[e + 1] = __uint_as_float(~mb[c + 1] & 0x7F800000u);
-          mul2(y[e], y[e + 1], up);
-          mul2(y[e], y[e + 1], s[c], s[c + 1]);
+          y[e] = s[c], y[e + 1] = s[c + 1];
+          mul2(y[e], y[e + 1], sc);
+          // 2 / the power of two of mb
+          mul2(y[e], y[e + 1], __uint_as_float(~mb[c] & 0x7F800000u), __uint_as_float(~mb[c + 1] & 0x7F800000u));
           add2(l[c], l[c + 1], s[c], s[c + 1]);
         }
         hilo_x4(y, hi[g / 4], lo[g / 4]);
@@ -439,7 +441,7 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
       {
         const int n = w.c0 + (lane & 15) + (lane >> 4) * deal.nqp;
         sm[F::PIMG_OFF + b * IMG + (n & 31) * 16 + (n >> 5) * 4 + quad] =
-            (uint8_t)((sh.most[warp][lane & 15] >> 23) - 7);
+            (uint8_t)((sh.most[warp][lane & 15] >> 23) - 1);
       }
     }
     fence_proxy_async_shared();

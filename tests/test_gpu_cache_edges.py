@@ -6,8 +6,7 @@ import pytest
 import torch
 
 from tests import cache_oracle as co
-from tests.test_gpu_cache_ops import (BIG, FULL, ODD, TINY, WIDE, _m, check_attend, make_cache, make_q,
-                                      run_attend)
+from tests.test_gpu_cache_ops import (BIG, FULL, ODD, TINY, WIDE, _m, make_cache, make_q, run_attend)
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +59,91 @@ def test_attend_groups_of_few_columns_among_wide_ones(rows):
 def test_attend_weights_over_many_tiles(spec, lengths, rows):
     """One to eight chunks a tile, runs of tiles of every remainder by four."""
     repeats(_m(), spec, lengths, rows, seed=len(lengths), weights=True)
+
+
+def fill_unseen(spec, table, cache, seen, scale, rng):
+    """Ordinary codes under a finite scale in every slot that holds no token of `seen` ((b, t) pairs)."""
+    kv, bs = spec["kv_dim"], spec["block_size"]
+    keep = np.zeros(cache.shape[:2], bool)
+    for b, t in seen:
+        keep[table[b, t // bs], t % bs] = True
+    cache[~keep, :kv] = rng.integers(0, 0x7F, (int((~keep).sum()), kv)) | rng.choice(
+        [0, 0x80], (int((~keep).sum()), kv)).astype(np.int64)
+    cache[~keep, kv:kv + 4] = np.frombuffer(np.float32(scale).tobytes(), np.uint8)
+
+
+SCALES = [8.0, -50.0, 1e4, 1e30, 2.9e38]
+
+
+@pytest.mark.parametrize("scale", SCALES)
+@pytest.mark.parametrize("spec", [FULL, TINY, ODD], ids=["pages128", "pages16", "pages7"])
+@pytest.mark.parametrize("rows", [1, 2, 6])
+def test_attend_finite_scales_outside_the_view(spec, rows, scale):
+    """Page tails, tokens outside the window and later tokens hold any finite scale: no row is to
+    notice."""
+    m = _m()
+    rng = np.random.default_rng(rows)
+    for L, window, sinks in ((rows, 0, 0), (100, 0, 0), (301, 0, 0), (900, 130, 3)):
+        table, cache = make_cache(spec, [L + 40], 200 + L)
+        pos = list(range(L - rows, L))
+        first = max(0, pos[0] - window + 1) if window else 0
+        fill_unseen(spec, table, cache, [(0, t) for t in range(L) if t >= first or t < sinks], scale, rng)
+        q = make_q(spec, rows, L)
+        o, lse, w, st = run_attend(m, spec, q, pos, [0] * rows, table, cache, window=window, sinks=sinks,
+                                   weights=torch.zeros((1, L)))
+        eo, tol, el, ltol, ew, wtol = co.attend(spec, q.double().numpy(), pos, [0] * rows, table, cache,
+                                                window, sinks, n_weights=L)
+        assert st == 0 and (np.abs(o - eo) <= tol).all() and (np.abs(lse - el) <= ltol).all()
+        assert (np.abs(w - ew) <= wtol + 2.0 ** -24 * (rows * spec["n_q_heads"] + 2) * ew).all()
+
+
+@pytest.mark.parametrize("scale", SCALES[:3])
+def test_attend_finite_scales_left_in_shared_memory(scale):
+    """Boxes of a tile that are not loaded keep what a call before left there."""
+    m = _m()
+    dev = torch.device("cuda")
+    n = 16 * 10240  # eight tiles and more for every SM
+    pool = torch.randint(0, 4, (n // 16, 16, 80), dtype=torch.uint8, device=dev)
+    pool[..., 64:68] = torch.tensor([scale], device=dev).view(torch.uint8)
+    pages = torch.arange(n // 16, dtype=torch.int32, device=dev)[None].contiguous()
+    h = m.Cache(TINY, 1, 1)
+    zero = torch.zeros(1, dtype=torch.int32, device=dev)
+    for L in (1, 17, 40, 1000):
+        table, cache = make_cache(TINY, [L], 300 + L)
+        q = make_q(TINY, 1, L)
+        big, out = q.to(dev), torch.empty_like(q, device=dev)
+        h.attend(big, out, zero + n - 1, zero, pages, pool)
+        o, lse, _, st = run_attend(m, TINY, q, [L - 1], [0], table, cache, handle=h)
+        eo, tol, el, ltol, _, _ = co.attend(TINY, q.double().numpy(), [L - 1], [0], table, cache)
+        assert st == 0 and (np.abs(o - eo) <= tol).all() and (np.abs(lse - el) <= ltol).all()
+    h.close()
+
+
+ONE = dict(n_q_heads=1, head_dim=64, kv_dim=64, block_size=16, kv_record_bytes=80)
+
+
+@pytest.mark.parametrize("scale", SCALES[:1] + [100.0, 1e4])
+def test_attend_blocks_far_below_the_reference(scale):
+    """Whole blocks of 32 tokens in view with large scales and scores too low to count: their weights
+    are zeros, whatever their values.  (Scores to -10^6: 2^-126 of the largest weight is the least that
+    an f32 holds, times at most 448 times the scale: nothing that the bound has not.)"""
+    m = _m()
+    L, low = 700, {*range(32, 64), *range(192, 256)}
+    table, cache = make_cache(ONE, [L], 31)
+    q = make_q(ONE, 1, 31)
+    away = np.where(q[0].float().numpy() > 0, 0xB8, 0x38).astype(np.uint8)  # -1 and 1
+    for t in low:
+        rec = cache[table[0, t // 16], t % 16]
+        rec[:64] = away
+        rec[64:68] = np.frombuffer(np.float32(scale).tobytes(), np.uint8)
+    o, lse, _, st = run_attend(m, ONE, q, [L - 1], [0], table, cache)
+    seen = [t for t in range(L) if t not in low]
+    rec = np.stack([cache[table[0, t // 16], t % 16] for t in seen])
+    k = co.E4M3[rec[:, :64]] * np.ascontiguousarray(rec[:, 64:68]).view(np.float32)
+    s = k @ q[0].double().numpy() / 8.0
+    w = np.exp(s - s.max())
+    eo = w / w.sum() @ k
+    es = 2.0 ** -16 * (np.abs(k) @ np.abs(q[0].double().numpy()) / 8.0).max()
+    tol = 2.0 ** -8 * np.abs(eo) + (2.0 ** -8 + 2 * es + 2.0 ** -12) * (w / w.sum() @ np.abs(k) + np.abs(eo))
+    assert st == 0 and (np.abs(o[0] - eo) <= tol).all()
+    assert abs(lse[0, 0] - (s.max() + np.log(w.sum()))) <= es + 2.0 ** -18 + 2.0 ** -20
