@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_weights_kernel(const __grid
               const uint32_t ok = ss.valid[st][quad];
               ct = fabsf(raw) <= 3.0e38f ? raw * to_log2 : __int_as_float(0x7FC00000);
               there = (ok >> lane) & 1;
-              see = there ? 0xffffffffu : 0u;
+              see = there ? (1u << nrows) - 1 : 0u;  // (no padding columns: a NaN score would count)
               if (__builtin_expect(!clear.has(i), 0)) {
 #pragma unroll 1
                 for (int j = 0; j < nrows; ++j) {

@@ -147,3 +147,29 @@ def test_attend_blocks_far_below_the_reference(scale):
     tol = 2.0 ** -8 * np.abs(eo) + (2.0 ** -8 + 2 * es + 2.0 ** -12) * (w / w.sum() @ np.abs(k) + np.abs(eo))
     assert st == 0 and (np.abs(o[0] - eo) <= tol).all()
     assert abs(lse[0, 0] - (s.max() + np.log(w.sum()))) <= es + 2.0 ** -18 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("bad", ["nan", "inf_scale"])
+def test_attend_weights_of_tokens_between_windows(bad):
+    """Rows of one request far apart, with windows that leave tokens between them to nobody: what
+    those hold reaches no weight, also where a pass has fewer rows than it could."""
+    m = _m()
+    dev = torch.device("cuda")
+    table, cache = make_cache(FULL, [1100, 700], 41)
+    pos, req = [1099, 10, 699, 650, 40], [0, 0, 1, 1, 1]
+    seen = {(b, t) for b, p in zip(req, pos) for t in range(p - 4, p + 1)}
+    for b, L in enumerate((1100, 700)):
+        for t in range(L):
+            if (b, t) not in seen:
+                rec = cache[table[b, t // 128], t % 128]
+                if bad == "nan":
+                    rec[:] = 0x7F
+                else:
+                    rec[512:516] = np.frombuffer(np.float32(np.inf).tobytes(), np.uint8)
+    q = make_q(FULL, 5, 41)
+    o, _, w, st = run_attend(m, FULL, q, pos, req, table, cache, window=5, weights=torch.ones((2, 1100)))
+    eo, tol, _, _, ew, wtol = co.attend(FULL, q.double().numpy(), pos, req, table, cache, 5,
+                                        n_weights=1100)
+    assert st == 0 and (np.abs(o - eo) <= tol).all()
+    assert (np.abs(w - 1 - ew) <= wtol + 2.0 ** -24 * (1 + (5 * 64 + 2) * ew)).all()
+    assert (w[ew == 0] == 1).all()
