@@ -38,8 +38,8 @@ typedef struct {
 int mono_cache_build(const mono_cache_spec *spec, mono_cache_t **out);
 /* Releases it.  NULL is accepted. */
 void mono_cache_free(mono_cache_t *h);
-/* Reads the handle's device status word (synchronously; MONO_STATUS_* bits, >= 0) or a
- * negative error code; clears the word when `clear` is non-zero. */
+/* Waits for all work on the handle's device, whatever its stream, and reads the handle's status word
+ * (MONO_STATUS_* bits, >= 0; or a negative error code); clears the word when `clear` is non-zero. */
 int mono_cache_status(mono_cache_t *h, int clear);
 
 /*

@@ -238,7 +238,9 @@ class Cache:
         _call(name, self._dev, stream, self._h, args)
 
     def status(self, clear: bool = False) -> int:
-        """The handle's MONO_STATUS_* bits (waits for the device)."""
+        """The handle's MONO_STATUS_* bits (waits for the device, all its streams)."""
+        if not self._h:
+            raise ValueError("the Cache is closed")
         rc = _lib().mono_cache_status(self._h, int(clear))
         if rc < 0:
             raise _m.MonoError(rc, "mono_cache_status")

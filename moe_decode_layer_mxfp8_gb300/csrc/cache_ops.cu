@@ -119,10 +119,15 @@ void mono_cache_free(mono_cache_t* h) {
 
 int mono_cache_status(mono_cache_t* h, int clear) {
   if (!h) return MONO_ERR_INVALID_ARG;
-  int v = 0;
-  cudaError_t e = cudaMemcpy(&v, h->status, sizeof(int), cudaMemcpyDeviceToHost);
+  int v = 0, dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev != h->device) e = cudaSetDevice(h->device);
+  // (a copy on the default stream does not wait for streams that do not block with it)
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpy(&v, h->status, sizeof(int), cudaMemcpyDeviceToHost);
   if (e == cudaSuccess && clear) e = cudaMemset(h->status, 0, sizeof(int));
   if (e == cudaSuccess && clear) e = cudaDeviceSynchronize();
+  if (dev >= 0 && dev != h->device) (void)cudaSetDevice(dev);
   return e == cudaSuccess ? v : cuda_code(e);
 }
 

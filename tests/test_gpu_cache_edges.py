@@ -173,3 +173,30 @@ def test_attend_weights_of_tokens_between_windows(bad):
     assert st == 0 and (np.abs(o - eo) <= tol).all()
     assert (np.abs(w - 1 - ew) <= wtol + 2.0 ** -24 * (1 + (5 * 64 + 2) * ew)).all()
     assert (w[ew == 0] == 1).all()
+
+
+def test_status_waits_for_every_stream():
+    """A call behind long work on a stream of torch's own: its status is there without a wait by the
+    caller, and a cleared word stays clear."""
+    m = _m()
+    dev = torch.device("cuda")
+    table, cache = make_cache(TINY, [300], 42)
+    table[0, 3] = -1
+    i32 = dict(dtype=torch.int32, device=dev)
+    q = make_q(TINY, 1, 42).to(dev)
+    args = (torch.empty_like(q), torch.tensor([299], **i32), torch.tensor([0], **i32),
+            torch.from_numpy(table).to(dev), torch.from_numpy(cache).to(dev))
+    h = m.Cache(TINY, 1, 1)
+    s, a = torch.cuda.Stream(), torch.randn((8192, 8192), device=dev)
+    torch.mm(a, a)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(s):
+            for _ in range(5):
+                torch.mm(a, a)
+            h.attend(q, *args)
+        assert h.status(clear=True) == 1
+        assert h.status() == 0
+    h.close()
+    with pytest.raises(ValueError):
+        h.status()
