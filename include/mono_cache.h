@@ -58,7 +58,7 @@ int mono_cache_status(mono_cache_t *h, int clear);
  * MONO_STATUS_WAIT_TIMEOUT; the step's outputs are then undefined.
  *
  * weights, if given, gathers every cached token's attention weight: weights[b][t] += the sum
- * over b's rows and all heads of w[t], for t < weights_stride.  The order of that sum is fixed.
+ * over b's rows and all heads of w[t], for t < weights_cols.  The order of that sum is fixed.
  *
  * Limits: max_blocks * block_size below 2^31; its tiles of 128 tokens, and 16 more, times rows too.
  *
@@ -80,8 +80,9 @@ typedef struct {
   const uint8_t *kv_cache;    /* [kv_num_blocks, block_size, record] view, as in mono_step_args */
   int64_t kv_stride_block, kv_stride_tok, kv_num_blocks;
   float *lse;                 /* optional [rows, n_q_heads]: ln sum_t exp(s[t]) */
-  float *weights;             /* optional [n_req, weights_stride], added to */
-  int64_t weights_stride;
+  float *weights;             /* optional [n_req, weights_cols], added to */
+  int64_t weights_stride;     /* elements between rows */
+  int64_t weights_cols;       /* <= weights_stride; 0: the stride */
 } mono_attend_args;
 
 int mono_cache_attend(mono_cache_t *h, const mono_attend_args *args, void *stream);
@@ -94,7 +95,7 @@ int mono_cache_attend(mono_cache_t *h, const mono_attend_args *args, void *strea
  * 0, 1, ... of the destination, their weights with them:
  *   kept[b][i] = old slot of the token now in slot i, -1 from new_lengths[b] up to budget
  *   weights_out[b][i] = weights[b][kept[b][i]], 0 from new_lengths[b] up to lengths[b]
- * (within weights_out's rows).  Positions of later steps continue at new_lengths[b].
+ * (within weights_out's columns).  Positions of later steps continue at new_lengths[b].
  * Destination: dst_table NULL moves the records within the request's own pages; a dst_table
  * names other pages, of dst_cache or, where that is NULL, of kv_cache, none of them a page
  * that a request still holds tokens in.  weights_out NULL, or equal to weights with the same
@@ -107,9 +108,9 @@ int mono_cache_attend(mono_cache_t *h, const mono_attend_args *args, void *strea
  * as mono_cache_attend's do.
  */
 typedef struct {
-  const float *weights;       /* [n_req, weights_stride] */
-  float *weights_out;         /* optional [n_req, weights_out_stride] */
-  int64_t weights_stride, weights_out_stride;
+  const float *weights;       /* [n_req, weights_cols] */
+  float *weights_out;         /* optional [n_req, weights_out_cols] */
+  int64_t weights_stride, weights_out_stride; /* elements between rows */
   const int32_t *lengths;     /* [n_req] */
   int32_t *new_lengths;       /* [n_req] */
   int32_t *kept;              /* [n_req, kept_stride] */
@@ -124,6 +125,7 @@ typedef struct {
   int32_t dst_max_blocks;
   uint8_t *dst_cache;         /* optional; the strides below are read only when it is given */
   int64_t dst_stride_block, dst_stride_tok, dst_num_blocks;
+  int64_t weights_cols, weights_out_cols; /* at most their strides; 0: the strides */
 } mono_evict_args;
 
 int mono_cache_evict(mono_cache_t *h, const mono_evict_args *args, void *stream);

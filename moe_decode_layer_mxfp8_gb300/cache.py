@@ -28,7 +28,7 @@ class AttendArgs(C.Structure):
                 ("causal", C.c_int32), ("scale", C.c_float), ("kv_cache", C.c_void_p),
                 ("kv_stride_block", C.c_int64), ("kv_stride_tok", C.c_int64),
                 ("kv_num_blocks", C.c_int64), ("lse", C.c_void_p), ("weights", C.c_void_p),
-                ("weights_stride", C.c_int64)]
+                ("weights_stride", C.c_int64), ("weights_cols", C.c_int64)]
 
 
 class EvictArgs(C.Structure):
@@ -42,7 +42,8 @@ class EvictArgs(C.Structure):
                 ("kv_num_blocks", C.c_int64), ("dst_table", C.c_void_p),
                 ("dst_max_blocks", C.c_int32), ("dst_cache", C.c_void_p),
                 ("dst_stride_block", C.c_int64), ("dst_stride_tok", C.c_int64),
-                ("dst_num_blocks", C.c_int64)]
+                ("dst_num_blocks", C.c_int64), ("weights_cols", C.c_int64),
+                ("weights_out_cols", C.c_int64)]
 
 
 class VerifyArgs(C.Structure):
@@ -54,8 +55,8 @@ class VerifyArgs(C.Structure):
 
 
 # The same structures packed at once: setting ctypes fields one by one took most of a call.
-_ATTEND = struct.Struct("@PPqqPPPiiiiiifPqqqPPq")
-_EVICT = struct.Struct("@PPqqPPPqiiiiPiPqqqPiPqqq")
+_ATTEND = struct.Struct("@PPqqPPPiiiiiifPqqqPPqq")
+_EVICT = struct.Struct("@PPqqPPPqiiiiPiPqqqPiPqqqqq")
 _VERIFY = struct.Struct("@PPqqiiiiPPPPPPP")
 
 CACHE_EXPORTS = ["mono_cache_build", "mono_cache_free", "mono_cache_status", "mono_cache_attend",
@@ -107,6 +108,14 @@ def _mat(t, name, dtypes, rows, cols, device):
             or (shape[1] > 1 and stride[1] != 1) or (shape[0] > 1 and stride[0] < shape[1])):
         _bad(t, name, dtypes, (rows, cols), device, False)
     return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1]
+
+
+def _weights(t, name, rows, device):
+    """(address, row stride, columns) of a f32 [rows, tokens] matrix."""
+    p, stride = _mat(t, name, _F32, rows, None, device)
+    if t.shape[1] == 0:
+        raise ValueError(f"{name} has no columns")
+    return p, stride, t.shape[1]
 
 
 def _table(t, name, rows, device):
@@ -195,12 +204,12 @@ class Cache:
             lp, ls = _mat(lse, "lse", _F32, rows, heads, dev)
             if ls != heads:
                 _bad(lse, "lse", _F32, (rows, heads), dev, True)
-        wp, ws = (0, 0) if weights is None else _mat(weights, "weights", _F32, n_req, None, dev)
+        wp, ws, wc = (0, 0, 0) if weights is None else _weights(weights, "weights", n_req, dev)
         args = _ATTEND.pack(qp, op, qs, os, _vec(positions, "positions", i32, rows, dev),
                             _vec(row_req, "row_req", i32, rows, dev),
                             _table(block_table, "block_table", None, dev), max_blocks, n_req, rows,
                             window, sinks, 1 if causal else 0, scale,
-                            *self._view(kv_cache, "kv_cache"), lp, wp, ws)
+                            *self._view(kv_cache, "kv_cache"), lp, wp, ws, wc)
         self._call("mono_cache_attend", args, stream)
 
     def evict(self, weights, lengths, block_table, kv_cache, kept, new_lengths, *, budget,
@@ -213,12 +222,11 @@ class Cache:
         counts."""
         dev, i32 = self._dev, torch.int32
         n_req, max_blocks = block_table.shape
-        wp, ws = _mat(weights, "weights", _F32, n_req, None, dev)
+        wp, ws, wc = _weights(weights, "weights", n_req, dev)
         kp, ks = _mat(kept, "kept", (i32,), n_req, None, dev)
         if kept.shape[1] < budget:
             raise ValueError(f"kept holds {kept.shape[1]} slots a request, the budget is {budget}")
-        vp, vs = (0, 0) if weights_out is None else _mat(weights_out, "weights_out", _F32, n_req, None,
-                                                          dev)
+        vp, vs, vc = (0, 0, 0) if weights_out is None else _weights(weights_out, "weights_out", n_req, dev)
         tp, tb = (0, 0) if dst_table is None else (_table(dst_table, "dst_table", n_req, dev),
                                                    dst_table.shape[1])
         dst = (0, 0, 0, 0)
@@ -229,7 +237,7 @@ class Cache:
         args = _EVICT.pack(wp, vp, ws, vs, _vec(lengths, "lengths", i32, n_req, dev),
                            _vec(new_lengths, "new_lengths", i32, n_req, dev), kp, ks, budget, sinks,
                            recent, n_req, _table(block_table, "block_table", None, dev), max_blocks,
-                           *self._view(kv_cache, "kv_cache"), tp, tb, *dst)
+                           *self._view(kv_cache, "kv_cache"), tp, tb, *dst, wc, vc)
         self._call("mono_cache_evict", args, stream)
 
     def _call(self, name, args, stream):

@@ -34,14 +34,14 @@ struct AttendArgs {
   float scale;
   float* lse;  // [rows, n_q] (the caller's, or the workspace's when only weights are asked for)
   float* weights;
-  long long weights_stride;
+  long long weights_stride, weights_cols;
   int* status;
 };
 
 struct EvictArgs {
   const float* weights;
   float* weights_out;
-  long long weights_stride, weights_out_stride;
+  long long weights_stride, weights_out_stride, weights_cols, weights_out_cols;
   const int* lengths;
   int* new_lengths;
   int* kept;

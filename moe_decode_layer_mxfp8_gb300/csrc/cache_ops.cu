@@ -56,6 +56,9 @@ int check_view(const mono_cache_spec& s, const void* base, int64_t stride_block,
   return MONO_OK;
 }
 
+// Rows of `cols` elements (0: stride) that lie `stride` apart.
+bool check_cols(int64_t stride, int64_t cols) { return stride >= 1 && cols >= 0 && cols <= stride; }
+
 int check_device(const mono_cache* h) {
   int dev = -1;
   const cudaError_t e = cudaGetDevice(&dev);
@@ -140,7 +143,7 @@ int mono_cache_attend(mono_cache_t* h, const mono_attend_args* a, void* stream) 
     return MONO_ERR_INVALID_ARG;
   if (a->window < 0 || a->sinks < 0 || !std::isfinite(a->scale) || a->scale < 0.0f)
     return MONO_ERR_INVALID_ARG;
-  if (a->weights && a->weights_stride < 1) return MONO_ERR_INVALID_ARG;
+  if (a->weights && !check_cols(a->weights_stride, a->weights_cols)) return MONO_ERR_INVALID_ARG;
   const int64_t width = (int64_t)s.n_q_heads * s.head_dim;
   const int64_t qs = a->q_stride ? a->q_stride : width, os = a->o_stride ? a->o_stride : width;
   if (qs < width || os < width) return MONO_ERR_INVALID_ARG;
@@ -175,6 +178,7 @@ int mono_cache_attend(mono_cache_t* h, const mono_attend_args* a, void* stream) 
   k.lse = a->lse ? a->lse : h->lse;
   k.weights = a->weights;
   k.weights_stride = a->weights_stride;
+  k.weights_cols = a->weights_cols ? a->weights_cols : a->weights_stride;
   k.status = h->status;
   return cuda_code(launch_attend(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k,
                                  h->attend_ws, s.max_rows, h->sms));
@@ -190,8 +194,10 @@ int mono_cache_evict(mono_cache_t* h, const mono_evict_args* a, void* stream) {
   if (a->budget < 1 || a->sinks < 0 || a->recent < 0 ||
       (int64_t)a->sinks + a->recent > a->budget || a->kept_stride < a->budget)
     return MONO_ERR_INVALID_ARG;
-  if (a->weights_stride < 1 || (a->weights_out && a->weights_out_stride < 1))
+  if (!check_cols(a->weights_stride, a->weights_cols) ||
+      (a->weights_out && !check_cols(a->weights_out_stride, a->weights_out_cols)))
     return MONO_ERR_INVALID_ARG;
+  const int64_t cols = a->weights_cols ? a->weights_cols : a->weights_stride;
   if (a->weights_out == a->weights && a->weights_out_stride != a->weights_stride)
     return MONO_ERR_INVALID_ARG;  // in place means row for row
   if (a->dst_cache && !a->dst_table) return MONO_ERR_INVALID_ARG;
@@ -221,13 +227,15 @@ int mono_cache_evict(mono_cache_t* h, const mono_evict_args* a, void* stream) {
                    a->dst_max_blocks));
   }
   if (!evict_fits(a->n_req, a->budget,
-                  std::min((int64_t)a->max_blocks * s.block_size, a->weights_stride)))
+                  std::min((int64_t)a->max_blocks * s.block_size, cols)))
     return MONO_ERR_TOO_MANY_ROWS;
   TRY(check_device(h));
   k.weights = a->weights;
   k.weights_out = a->weights_out ? a->weights_out : const_cast<float*>(a->weights);
   k.weights_stride = a->weights_stride;
   k.weights_out_stride = a->weights_out ? a->weights_out_stride : a->weights_stride;
+  k.weights_cols = cols;
+  k.weights_out_cols = !a->weights_out ? cols : a->weights_out_cols ? a->weights_out_cols : a->weights_out_stride;
   k.lengths = a->lengths;
   k.new_lengths = a->new_lengths;
   k.kept = a->kept;

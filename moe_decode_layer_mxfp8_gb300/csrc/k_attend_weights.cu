@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_weights_kernel(const __grid
                   if (!(t <= hi && (t >= lo || t < a.sinks))) see &= ~(1u << j);
                 }
               }
-              there = there && t < a.weights_stride;
+              there = there && t < a.weights_cols;
               if (there) old = a.weights[im.b * a.weights_stride + t];
             }
             __syncwarp();

@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(THREADS, 2) evict_select_kernel(EvictArgs a, W
   const float* w = a.weights + b * a.weights_stride;
   int* kept = a.kept + b * a.kept_stride;
   int len = max(0, a.lengths[b]);
-  const long long cap = min((long long)a.src.max_blocks * a.src.block_size, a.weights_stride);
+  const long long cap = min((long long)a.src.max_blocks * a.src.block_size, a.weights_cols);
   if (len > cap) {
     len = (int)cap;
     if (tid == 0 && rank == 0) atomicOr(a.status, ST_UNMAPPED_PAGE);
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(MOVE_THREADS) evict_move_kernel(EvictArgs a, W
   const int slot = tid < CHUNK && i0 + tid < a.budget ? a.kept[b * a.kept_stride + i0 + tid] : -1;
   const int* loaded = ws.loaded + (size_t)b * chunks;
   float* wo = a.weights_out + b * a.weights_out_stride;
-  const long long wcap = a.weights_out_stride;
+  const long long wcap = a.weights_out_cols;
   if (chunk == chunks) {  // the tail of the weights
     if (ordered && n < len)
       for (int c = tid; c < (n + CHUNK - 1) / CHUNK; c += MOVE_THREADS) wait_loaded(loaded + c, a.status);
@@ -324,7 +324,7 @@ cudaError_t launch_evict(const Launch& L, const EvictArgs& a, uint8_t* workspace
   ws.old_len = reinterpret_cast<int*>(workspace + 256);
   ws.loaded = ws.old_len + ((size_t)max_req * 4 + 255) / 256 * 64;
   ws.from = ws.loaded + EVICT_MAX_CHUNKS;
-  const long long cap = std::min((long long)a.src.max_blocks * a.src.block_size, a.weights_stride);
+  const long long cap = std::min((long long)a.src.max_blocks * a.src.block_size, a.weights_cols);
   const int chunks = chunks_of(a.budget, cap);
   // as many CTAs a request as fit two an SM, eight slots a thread at least
   int cs = 1;

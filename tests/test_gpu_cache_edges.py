@@ -200,3 +200,38 @@ def test_status_waits_for_every_stream():
     h.close()
     with pytest.raises(ValueError):
         h.status()
+
+
+def test_weights_in_views_of_wider_tensors():
+    """Columns before and behind a view of weights, in and out, are left as they were; the last row's
+    end is the storage's."""
+    m = _m()
+    dev = torch.device("cuda")
+    lengths = [200, 333]
+    table, cache = make_cache(TINY, lengths, 43)
+    q = make_q(TINY, 2, 43)
+    want, *_ = run_attend(m, TINY, q, [199, 332], [0, 1], table, cache, weights=torch.ones((2, 150)))[2:]
+    big = torch.full((2, 300), 7.0, device=dev)
+    view = big[:, 150:]
+    view.fill_(1.0)
+    h = m.Cache(TINY, 2, 2)
+    i32 = dict(dtype=torch.int32, device=dev)
+    t, c = torch.from_numpy(table).to(dev), torch.from_numpy(cache).to(dev)
+    h.attend(q.to(dev), torch.empty_like(q, device=dev), torch.tensor([199, 332], **i32),
+             torch.tensor([0, 1], **i32), t, c, weights=view)
+    assert h.status() == 0 and (big[:, :150] == 7).all()
+    assert np.array_equal(view.double().cpu().numpy(), want)
+    # an eviction of 150 columns' tokens into 40, of which 64 cannot be kept
+    w = view.cpu().numpy()
+    out = torch.full((2, 100), 5.0, device=dev)
+    ln, kept = torch.tensor([150, 150], **i32), torch.zeros((2, 64), **i32)
+    h.evict(view, ln, t, c, kept, ln, budget=64, sinks=2, recent=9, weights_out=out[:, 60:])
+    assert h.status() == 0 and ln.tolist() == [64, 64]
+    keep = co.evict(w, [150, 150], 64, 2, 9)
+    assert kept.tolist() == keep and (out[:, :60] == 5).all()
+    assert np.array_equal(out[:, 60:].cpu().numpy(), np.stack([w[b, k[:40]] for b, k in enumerate(keep)]))
+    # lengths beyond a view's columns are cut to them
+    ln = torch.tensor([199, 100], **i32)
+    h.evict(big[:, :120], ln, t, c, kept, ln, budget=64)
+    assert h.status(clear=True) == 1 and ln.tolist() == [64, 64] and kept.max() < 120
+    h.close()
