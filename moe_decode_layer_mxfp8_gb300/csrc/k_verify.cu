@@ -13,8 +13,9 @@
 // Measured: 192 requests of 3 drafts, 100003 bf16 entries, a quarter of them greedy 28.5 us (77 MB; copy:
 // 11 us), 8 of 5 drafts, 131072 f32 entries 10.5 us, 4 of 2 table drafts, 32000 f16 entries 7.2 us.
 // Sums decide which token is drawn, so they are carried as pairs of f32 (error-free additions and
-// products, and p - q as a pair): FP64 runs at a 64th of the FP32 rate here, and a search in f64 took
-// 40 us of a CTA's 45.
+// products, and p - q as a pair) for every type: with 10^5 tokens, what an f32 sum of a large entry and
+// three small ones loses can move as much as one draw in a thousand by a token.  FP64 runs at a 64th of
+// the FP32 rate here, and a search in f64 took 40 us of a CTA's 45.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -98,11 +99,11 @@ struct Sum2 {
     float t0 = s0, t1 = s1;
     add2(t0, t1, x0, x1);
     float b0 = t0, b1 = t1;  // what of x went into t
-    add2(b0, b1, -s0, -s1);
+    sub2(b0, b1, s0, s1);
     float a0 = t0, a1 = t1;  // what of s did
-    add2(a0, a1, -b0, -b1);
-    add2(s0, s1, -a0, -a1);
-    add2(x0, x1, -b0, -b1);
+    sub2(a0, a1, b0, b1);
+    sub2(s0, s1, a0, a1);
+    sub2(x0, x1, b0, b1);
     add2(e0, e1, s0, s1);
     add2(e0, e1, x0, x1);
     s0 = t0;
@@ -157,6 +158,40 @@ struct Vec {
     }
     return m == m ? m : -INFINITY;
   }
+  // Every element at least the other vector's (a NaN is less than all).
+  __device__ Vec above(const Vec& o) const {
+    Vec r;
+    if (sizeof(T) == 4) {
+      r.x = make_uint4(max1(x.x, o.x.x), max1(x.y, o.x.y), max1(x.z, o.x.z), max1(x.w, o.x.w));
+    } else {
+      r.x = make_uint4(max2(x.x, o.x.x), max2(x.y, o.x.y), max2(x.z, o.x.z), max2(x.w, o.x.w));
+    }
+    return r;
+  }
+  // Negative elements and NaN as 0, infinities as the largest number.
+  __device__ Vec counted() const {
+    Vec r;
+    if (sizeof(T) == 4) {
+      r.x = make_uint4(most1(max1(x.x, 0)), most1(max1(x.y, 0)), most1(max1(x.z, 0)), most1(max1(x.w, 0)));
+    } else {
+      r.x = make_uint4(most2(max2(x.x, 0)), most2(max2(x.y, 0)), most2(max2(x.z, 0)), most2(max2(x.w, 0)));
+    }
+    return r;
+  }
+  __device__ static uint32_t max1(uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }
+  __device__ static uint32_t most1(uint32_t a) {
+    return __float_as_uint(fminf(__uint_as_float(a), 3.402823466e38f));
+  }
+  __device__ static uint32_t most2(uint32_t a) {
+    uint32_t r;
+    if (std::is_same<T, __half>::value)
+      asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x7BFF7BFFu));
+    else
+      asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(0x7F7F7F7Fu));
+    return r;
+  }
   __device__ static uint32_t max2(uint32_t a, uint32_t b) {  // (a NaN loses)
     uint32_t r;
     if (std::is_same<T, __half>::value)
@@ -202,30 +237,41 @@ struct Draw {  // what a token is drawn from
     q_aligned = q && Row<T>(q).lead == lead;
   }
   __device__ int vectors() const { return (V + lead + VEC - 1) / VEC; }
-  // The weights of a loaded vector, in two f32: the differences and what rounding took off them
-  // (for 16-bit types nothing worth carrying: a rounding needs p beyond 2^16 q).
+  // The weights of a loaded vector, in two f32: what is counted of p - q, and what rounding took off
+  // it (the difference of x >= y >= 0: exactly (x - d) - y).
   __device__ void weights(const Vec<T>& a, const Vec<T>& b, int v0, float (&w)[VEC], float (&err)[VEC]) const {
     if (q) {
+      const Vec<T> y = b.counted(), x = a.above(y);  // (nothing for a negative or NaN p)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float x = a[e], y = positive(b[e]), d = x - y;
-        if (sizeof(T) == 4) {
-          const float t = x - d, r = (x - (d + t)) + (t - y);
-          err[e] = d > 0.0f ? r : 0.0f;
-        }
-        w[e] = positive(d);  // (nothing for a negative or NaN p)
+      for (int e = 0; e < VEC; e += 2) {
+        w[e] = x[e], w[e + 1] = x[e + 1];
+        sub2(w[e], w[e + 1], y[e], y[e + 1]);
+        err[e] = x[e], err[e + 1] = x[e + 1];
+        sub2(err[e], err[e + 1], w[e], w[e + 1]);
+        sub2(err[e], err[e + 1], y[e], y[e + 1]);
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) w[e] = positive(a[e]);
-      if (sizeof(T) == 4)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) err[e] = 0.0f;
+      for (int e = 0; e < VEC; ++e) w[e] = positive(a[e]), err[e] = 0.0f;
       if (certain >= v0 && certain < v0 + VEC) {
 #pragma unroll
-        for (int e = 0; e < VEC; ++e)
-          if (v0 + e == certain) w[e] = positive(w[e] - 1.0f);
+        for (int e = 0; e < VEC; ++e) {
+          if (v0 + e != certain) continue;
+          const float x = fmaxf(w[e], 1.0f);
+          w[e] = x - 1.0f;
+          err[e] = (x - w[e]) - 1.0f;
+        }
       }
+    }
+  }
+  // The same, added up.
+  __device__ void add(const Vec<T>& a, const Vec<T>& b, int v0, Sum2& sum) const {
+    float w[VEC], err[VEC];
+    weights(a, b, v0, w, err);
+#pragma unroll
+    for (int e = 0; e < VEC; e += 2) {
+      sum.add(w[e], w[e + 1]);
+      sum.error(err[e], err[e + 1]);
     }
   }
   __device__ void load(int vec, Vec<T>& a, Vec<T>& b) const {
@@ -378,9 +424,8 @@ __global__ void __launch_bounds__(THREADS, 3) verify_kernel(VerifyArgs a, int cs
       const int nv = (d.vectors() + runs - 1) / runs, first = run * nv;
       const int last = min(first + nv, d.vectors());
       // rounds of a vector per lane, `per` of them a block
-      // loaded at a time: f32 2 (8 requests of 131072 10.1 us; 4 at a time 11.1), 16 bits 4 (192 of 100003
-      // 22.5 us, all sampled; 2 at a time 24.4)
-      constexpr int U = sizeof(T) == 4 ? 2 : 4;
+      // loaded at a time (192 requests of 100003 bf16 entries 30.5 us; four at a time 31.6)
+      constexpr int U = 2;
       const int rounds = max(1, (last - first + 31) / 32);
       const int per = ((rounds + BLOCKS - 1) / BLOCKS + U - 1) / U * U;
       Pair mine;
@@ -400,18 +445,7 @@ __global__ void __launch_bounds__(THREADS, 3) verify_kernel(VerifyArgs a, int cs
           for (int u = 0; u < U; ++u) {
             const int k = first + (i + u) * 32 + lane;
             if (i + u < q + per && k < last) {
-              float w[VEC], err[VEC];
-              d.weights(fa[u], fb[u], k * VEC - d.lead, w, err);
-              if (sizeof(T) == 4) {
-#pragma unroll
-                for (int e = 0; e < VEC; e += 2) sum.add(w[e], w[e + 1]), sum.error(err[e], err[e + 1]);
-              } else {
-                // four 16-bit numbers' sum in f32 is exact while they lie within 13 binades, and else
-                // off by 2^-24 of itself: nothing that moves a draw among 10^5 tokens
-#pragma unroll
-                for (int e = 2; e < VEC; e += 2) add2(w[0], w[1], w[e], w[e + 1]);
-                sum.add(w[0], w[1]);
-              }
+              d.add(fa[u], fb[u], k * VEC - d.lead, sum);
             }
           }
         }
@@ -482,7 +516,7 @@ __global__ void __launch_bounds__(THREADS, 3) verify_kernel(VerifyArgs a, int cs
 #pragma unroll
             for (int e = 0; e < VEC; e += 2) {
               sum.add(wt[e], wt[e + 1]);
-              if (sizeof(T) == 4) sum.error(err[e], err[e + 1]);
+              sum.error(err[e], err[e + 1]);
             }
             return sum.pair();
           };
@@ -518,7 +552,7 @@ __global__ void __launch_bounds__(THREADS, 3) verify_kernel(VerifyArgs a, int cs
           for (int e = 0; e < VEC; ++e) {
             if (wt[e] > 0.0f && (!found || begin <= goal)) hit = (first + i * 32 + lane) * VEC - d.lead + e;
             Pair x;
-            x.h = wt[e], x.l = sizeof(T) == 4 ? err[e] : 0.0f;
+            x.h = wt[e], x.l = err[e];
             begin = begin + x;
           }
           hit = __shfl_sync(0xffffffffu, hit, max(pick, 0));

@@ -6,7 +6,8 @@ import pytest
 import torch
 
 from tests import cache_oracle as co
-from tests.test_gpu_cache_ops import (BIG, FULL, ODD, TINY, WIDE, _m, make_cache, make_q, run_attend)
+from tests.test_gpu_cache_ops import (BIG, FULL, ODD, TINY, WIDE, _m, check_verify, make_cache, make_q,
+                                      run_attend)
 
 pytestmark = pytest.mark.gpu
 
@@ -235,3 +236,48 @@ def test_weights_in_views_of_wider_tensors():
     h.evict(big[:, :120], ln, t, c, kept, ln, budget=64)
     assert h.status(clear=True) == 1 and ln.tolist() == [64, 64] and kept.max() < 120
     h.close()
+
+
+# -------------------------------------------------------------------------- verification
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("tiny", [2.0 ** -24, 3 * 2.0 ** -24])
+def test_verify_small_entries_beside_large_ones(dtype, tiny):
+    """Entries that an f32 sum with their neighbours would lose decide where a threshold falls."""
+    m = _m()
+    V = 4096
+    p = torch.zeros((2, V), dtype=torch.float64)
+    p[:, ::8] = 1.0
+    p[0, :V // 2].view(-1, 8)[:, [2, 4, 6]] = tiny
+    p[1, V // 2:].view(-1, 8)[:, [1, 3, 5, 7]] = tiny
+    assert torch.equal(p.to(dtype).double(), p)
+    rows = p.to(dtype).cuda().repeat_interleave(200, 0)
+    r = np.concatenate([np.arange(312, 512), np.arange(0, 200)]).astype(np.float32) / 512
+    check_verify(m, rows, None, [0] * 400, list(range(401)), np.zeros(400, np.float32), r)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_verify_residuals_of_unlike_sizes(dtype):
+    """p - q of a large p and a small q takes more bits than an f32 has."""
+    m = _m()
+    V, n = 4096, 200
+    p, q = torch.zeros((2 * n, V), dtype=torch.float64), torch.zeros((2 * n, V), dtype=torch.float64)
+    p[:, ::8] = 16.0
+    q[:, V // 2::8] = 2.0 ** -24 * 3  # (an f32 difference loses it)
+    tok = [1, 0] * n  # (p is 0 there: refused)
+    r = np.arange(312, 512).astype(np.float32) / 512
+    check_verify(m, p.to(dtype).cuda(), q.to(dtype).cuda(), tok, list(range(0, 2 * n + 1, 2)),
+                 np.full(2 * n, 0.5, np.float32), r)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_verify_infinite_draft_entries(dtype):
+    """An infinite q takes all of a finite p; the largest finite p stands against it."""
+    m = _m()
+    g = torch.Generator().manual_seed(61)
+    p, q = torch.rand((60, 999), generator=g), torch.rand((60, 999), generator=g)
+    q[:, ::3] = float("inf")
+    q[:, 1::5] = float("nan")
+    p[:, 4] = -float("inf")
+    r = torch.rand(30, generator=g).numpy()
+    check_verify(m, p.to(dtype).cuda(), q.to(dtype).cuda(), [0] * 60, list(range(0, 61, 2)),
+                 np.full(60, 0.999, np.float32), r)
