@@ -545,12 +545,13 @@ __global__ void __launch_bounds__(THREADS, 3) verify_kernel(VerifyArgs a, int cs
             again = true;
             i = at;
           }
-          // the last element that begins by the goal (of all, without one)
+          // the last element that begins by the goal (of all, without one).  Where the goal is a border,
+          // the sums of lanes without a weight may pass it by a rounding: then the lane's first
           Pair begin = shfl_before(incl_run);
           int hit = -1;
 #pragma unroll
           for (int e = 0; e < VEC; ++e) {
-            if (wt[e] > 0.0f && (!found || begin <= goal)) hit = (first + i * 32 + lane) * VEC - d.lead + e;
+            if (wt[e] > 0.0f && (!found || hit < 0 || begin <= goal)) hit = (first + i * 32 + lane) * VEC - d.lead + e;
             Pair x;
             x.h = wt[e], x.l = err[e];
             begin = begin + x;

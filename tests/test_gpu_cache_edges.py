@@ -7,7 +7,7 @@ import torch
 
 from tests import cache_oracle as co
 from tests.test_gpu_cache_ops import (BIG, FULL, ODD, TINY, WIDE, _m, check_verify, make_cache, make_q,
-                                      run_attend)
+                                      run_attend, run_verify)
 
 pytestmark = pytest.mark.gpu
 
@@ -281,3 +281,26 @@ def test_verify_infinite_draft_entries(dtype):
     r = torch.rand(30, generator=g).numpy()
     check_verify(m, p.to(dtype).cuda(), q.to(dtype).cuda(), [0] * 60, list(range(0, 61, 2)),
                  np.full(60, 0.999, np.float32), r)
+
+
+def test_verify_thresholds_on_a_border():
+    """Two copies of some entries with zeros between them, and a threshold at half their sum: the last
+    of the first copy or the first of the second, as roundings fall, but one of them.  (Entries span
+    30 binades: their sums take more bits than two f32 hold, and differ in their last ones by the order
+    of the additions.)"""
+    m = _m()
+    rng = np.random.default_rng(0)
+    n, V = 3000, 1024
+    p, ends = np.zeros((n, V), np.float32), []
+    for row in p:
+        few = rng.integers(3, 10)
+        room = rng.integers(few, 13)
+        vals = rng.random(few) * 2.0 ** rng.integers(-30, 0, few)
+        first = rng.permutation(room)[:few]
+        second = room + rng.integers(1, 4) + rng.permutation(16)[:few]
+        row[4 * first], row[4 * second] = vals, vals
+        ends.append((4 * first.max(), 4 * second.min()))
+    acc, out = run_verify(m, torch.from_numpy(p).cuda(), None, [0] * n, list(range(n + 1)),
+                          np.zeros(n, np.float32), np.full(n, 0.5, np.float32))
+    assert acc == [0] * n
+    assert all(x in e for x, e in zip(out, ends)), [(x, e) for x, e in zip(out, ends) if x not in e][:5]
