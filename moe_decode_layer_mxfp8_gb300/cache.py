@@ -125,7 +125,15 @@ def _table(t, name, rows, device):
     return t.data_ptr()
 
 
+def _pack(layout, *values):
+    try:
+        return layout.pack(*values)
+    except struct.error as e:
+        raise ValueError(f"an argument is not a 32-bit integer: {e}") from None
+
+
 _BF16, _F32 = (torch.bfloat16,), (torch.float32,)
+_LEAST, _MOST = 2.0 ** -149, (2.0 - 2.0 ** -23) * 2.0 ** 127  # an f32 above 0
 _PROBS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
@@ -194,8 +202,8 @@ class Cache:
         rows, (n_req, max_blocks) = q.shape[0], block_table.shape
         if scale is None:
             scale = 0.0
-        elif not scale > 0:
-            raise ValueError("scale must be positive")
+        elif not _LEAST <= scale <= _MOST:  # (0 is the library's default)
+            raise ValueError("scale must be positive, and an f32")
         qp, qs = _mat(q, "q", _BF16, rows, self._width, dev)
         op, os = _mat(o, "o", _BF16, rows, self._width, dev)
         heads = self.spec["n_q_heads"]
@@ -205,11 +213,11 @@ class Cache:
             if ls != heads:
                 _bad(lse, "lse", _F32, (rows, heads), dev, True)
         wp, ws, wc = (0, 0, 0) if weights is None else _weights(weights, "weights", n_req, dev)
-        args = _ATTEND.pack(qp, op, qs, os, _vec(positions, "positions", i32, rows, dev),
-                            _vec(row_req, "row_req", i32, rows, dev),
-                            _table(block_table, "block_table", None, dev), max_blocks, n_req, rows,
-                            window, sinks, 1 if causal else 0, scale,
-                            *self._view(kv_cache, "kv_cache"), lp, wp, ws, wc)
+        args = _pack(_ATTEND, qp, op, qs, os, _vec(positions, "positions", i32, rows, dev),
+                     _vec(row_req, "row_req", i32, rows, dev),
+                     _table(block_table, "block_table", None, dev), max_blocks, n_req, rows,
+                     window, sinks, 1 if causal else 0, scale,
+                     *self._view(kv_cache, "kv_cache"), lp, wp, ws, wc)
         self._call("mono_cache_attend", args, stream)
 
     def evict(self, weights, lengths, block_table, kv_cache, kept, new_lengths, *, budget,
@@ -234,10 +242,10 @@ class Cache:
             if dst_table is None:
                 raise ValueError("dst_cache needs a dst_table")
             dst = self._view(dst_cache, "dst_cache")
-        args = _EVICT.pack(wp, vp, ws, vs, _vec(lengths, "lengths", i32, n_req, dev),
-                           _vec(new_lengths, "new_lengths", i32, n_req, dev), kp, ks, budget, sinks,
-                           recent, n_req, _table(block_table, "block_table", None, dev), max_blocks,
-                           *self._view(kv_cache, "kv_cache"), tp, tb, *dst, wc, vc)
+        args = _pack(_EVICT, wp, vp, ws, vs, _vec(lengths, "lengths", i32, n_req, dev),
+                     _vec(new_lengths, "new_lengths", i32, n_req, dev), kp, ks, budget, sinks,
+                     recent, n_req, _table(block_table, "block_table", None, dev), max_blocks,
+                     *self._view(kv_cache, "kv_cache"), tp, tb, *dst, wc, vc)
         self._call("mono_cache_evict", args, stream)
 
     def _call(self, name, args, stream):
@@ -281,11 +289,11 @@ def verify_drafts(target, draft, draft_tokens, row_start, u, r, accepted, tokens
     rows, vocab = target.shape
     n_req = row_start.shape[0] - 1
     dp, ds = (0, 0) if draft is None else _mat(draft, "draft", (target.dtype,), rows, vocab, dev)
-    args = _VERIFY.pack(tp, dp, ts, ds, _PROBS[target.dtype], vocab, rows, n_req,
-                        _vec(row_start, "row_start", i32, n_req + 1, dev),
-                        _vec(draft_tokens, "draft_tokens", i32, rows, dev),
-                        _vec(u, "u", f32, rows, dev), _vec(r, "r", f32, n_req, dev),
-                        0 if greedy is None else _vec(greedy, "greedy", i32, n_req, dev),
-                        _vec(accepted, "accepted", i32, n_req, dev),
-                        _vec(tokens, "tokens", i32, rows, dev))
+    args = _pack(_VERIFY, tp, dp, ts, ds, _PROBS[target.dtype], vocab, rows, n_req,
+                 _vec(row_start, "row_start", i32, n_req + 1, dev),
+                 _vec(draft_tokens, "draft_tokens", i32, rows, dev),
+                 _vec(u, "u", f32, rows, dev), _vec(r, "r", f32, n_req, dev),
+                 0 if greedy is None else _vec(greedy, "greedy", i32, n_req, dev),
+                 _vec(accepted, "accepted", i32, n_req, dev),
+                 _vec(tokens, "tokens", i32, rows, dev))
     _call("mono_verify_drafts", dev, stream, args)

@@ -61,3 +61,21 @@ def test_weights_are_as_wide_as_their_view():
             call(**{name: big[:, 7:7]})
 
 
+
+
+def test_scales_that_an_f32_does_not_hold_are_refused():
+    """A scale that rounds to 0 would be the default one."""
+    for scale in (0.0, -1.0, 1e-50, 1e39, float("inf"), float("nan")):
+        with pytest.raises(ValueError):
+            attend(scale=scale)
+    assert attend(scale=2.0 ** -149).scale == 2.0 ** -149
+    assert attend().scale == 0.0 and attend(scale=0.25).scale == 0.25
+
+
+def test_integers_that_32_bits_do_not_hold_are_refused():
+    for bad in (2 ** 31, 1.5, None):
+        with pytest.raises(ValueError):
+            attend(window=bad)
+        with pytest.raises(ValueError):
+            evict(sinks=bad)
+    assert attend(window=2 ** 31 - 1).window == 2 ** 31 - 1
