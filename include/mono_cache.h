@@ -60,7 +60,8 @@ int mono_cache_status(mono_cache_t *h, int clear);
  * weights, if given, gathers every cached token's attention weight: weights[b][t] += the sum
  * over b's rows and all heads of w[t], for t < weights_cols.  The order of that sum is fixed.
  *
- * Limits: max_blocks * block_size below 2^31; its tiles of 128 tokens, and 16 more, times rows too.
+ * Limits: max_blocks * block_size at most 2^31 - 2^16; its tiles of 128 tokens, and 16 more, times rows
+ * below 2^31.
  *
  * One handle's calls share its workspace: they must be ordered on the GPU (one stream, or
  * events between streams; graphs captured from one handle must not run at the same time).
@@ -155,7 +156,7 @@ typedef struct {
   const void *draft;            /* optional [rows, vocab] */
   int64_t target_stride, draft_stride; /* elements between rows, >= vocab */
   int32_t dtype;                /* MONO_PROB_*, of both */
-  int32_t vocab, rows, n_req;
+  int32_t vocab, rows, n_req;   /* vocab at most 2^31 - 64 */
   const int32_t *row_start;     /* [n_req + 1] */
   const int32_t *draft_tokens;  /* [rows] */
   const float *u;               /* [rows], uniform in [0, 1) */

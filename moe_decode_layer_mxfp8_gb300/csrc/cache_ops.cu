@@ -47,8 +47,8 @@ int check_layout(const mono_cache_spec& s) {
 int check_view(const mono_cache_spec& s, const void* base, int64_t stride_block,
                int64_t stride_tok, int64_t num_blocks, int max_blocks) {
   if (num_blocks < 1 || max_blocks < 1) return MONO_ERR_INVALID_ARG;
-  // token indices are 32-bit
-  if ((int64_t)max_blocks * s.block_size > INT32_MAX) return MONO_ERR_INVALID_ARG;
+  // token indices are 32-bit, also those of the rest of a tile and of a cluster's threads behind the last
+  if ((int64_t)max_blocks * s.block_size > INT32_MAX - 65535) return MONO_ERR_INVALID_ARG;
   if (!aligned(base, 16) || stride_tok % 16 || stride_block % 16) return MONO_ERR_BAD_ALIGNMENT;
   if (stride_tok < s.kv_record_bytes || stride_tok > INT64_MAX / (1 << 20) ||
       stride_block < (int64_t)s.block_size * stride_tok)
@@ -256,6 +256,7 @@ int mono_verify_drafts(const mono_verify_args* a, void* stream) {
       !a->tokens)
     return MONO_ERR_INVALID_ARG;
   if (a->vocab < 1 || a->rows < 1 || a->n_req < 1) return MONO_ERR_INVALID_ARG;
+  if (a->vocab > INT32_MAX - 63) return MONO_ERR_INVALID_ARG;  // (indices run to the end of a vector)
   if (a->dtype < MONO_PROB_F32 || a->dtype > MONO_PROB_F16) return MONO_ERR_INVALID_ARG;
   if (a->target_stride < a->vocab || (a->draft && a->draft_stride < a->vocab))
     return MONO_ERR_INVALID_ARG;

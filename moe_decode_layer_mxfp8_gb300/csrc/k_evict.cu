@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(THREADS, 2) evict_select_kernel(EvictArgs a, W
     sure += s == 1;
     equal += s == 2;
   }
-  for (int i = total + rank * THREADS + tid; i < a.budget; i += cs * THREADS) kept[i] = -1;
+  for (long long i = total + rank * THREADS + tid; i < a.budget; i += cs * THREADS) kept[i] = -1;
   if (cs > 1) cluster_sync_all();  // every CTA has read the length, and its neighbours' counts
   if (rank == 0 && tid == 0) {
     ws.old_len[b] = len;

@@ -304,3 +304,47 @@ def test_verify_thresholds_on_a_border():
                           np.zeros(n, np.float32), np.full(n, 0.5, np.float32))
     assert acc == [0] * n
     assert all(x in e for x, e in zip(out, ends)), [(x, e) for x, e in zip(out, ends) if x not in e][:5]
+
+
+# -------------------------------------------------------------------------------- limits
+def test_tables_beyond_the_indices_are_refused():
+    m = _m()
+    spec = dict(TINY, block_size=65535)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pool = torch.zeros((1, 65535, 80), dtype=torch.uint8, device="cuda")
+    q = torch.zeros((1, 256), dtype=torch.bfloat16, device="cuda")
+    zero, w = torch.zeros(1, **i32), torch.zeros((1, 64), device="cuda")
+    h = m.Cache(spec, 1, 1)
+    table = torch.full((1, 32768), -1, **i32)
+    table[0, 0] = 0
+    for n, ok in ((32768, False), (32767, True)):  # 2^31 - 2^15; 2^31 - 2^16 - 2^15 + 1 tokens
+        t = table[:, :n].contiguous()
+        calls = [lambda: h.attend(q, torch.empty_like(q), zero, zero, t, pool),
+                 lambda: h.evict(w, zero, t, pool, torch.zeros((1, 8), **i32), zero.clone(), budget=8)]
+        for call in calls:
+            if ok:
+                call()
+            else:
+                with pytest.raises(m.MonoError) as e:
+                    call()
+                assert e.value.code == -1
+    # the last token that the table could hold lies on no page: nothing is read for it
+    o = torch.full_like(q, float("nan"))
+    h.attend(q, o, torch.full((1,), 32767 * 65535 - 1, **i32), zero, table[:, :32767].contiguous(), pool,
+             window=300)
+    assert h.status() == 1 and not o.any()
+    h.close()
+
+
+def test_the_largest_budget():
+    """kept is filled up to the budget, with indices that a 32-bit step would pass."""
+    m = _m()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    n = 2 ** 31 - 1
+    kept = torch.zeros((1, n), **i32)
+    h = m.Cache(TINY, 1, 1)
+    h.evict(torch.ones((1, 64), device="cuda"), torch.tensor([50], **i32), torch.arange(4, **i32)[None],
+            torch.zeros((4, 16, 80), dtype=torch.uint8, device="cuda"), kept, torch.zeros(1, **i32), budget=n)
+    assert h.status() == 0 and kept[0, :50].tolist() == list(range(50))
+    assert all(bool((kept[0, i:i + 2 ** 28] == -1).all()) for i in range(50, n, 2 ** 28))
+    h.close()
