@@ -416,17 +416,14 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int g = 0; g < C; g += 4) {
-        float y[4];
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          const int c = g + e;
-          y[e] = s[c], y[e + 1] = s[c + 1];
-          mul2(y[e], y[e + 1], sc);
-          // 2 / the power of two of mb
-          mul2(y[e], y[e + 1], __uint_as_float(~mb[c] & 0x7F800000u), __uint_as_float(~mb[c + 1] & 0x7F800000u));
+        for (int c = g; c < g + 4; c += 2) {
           add2(l[c], l[c + 1], s[c], s[c + 1]);
+          mul2(s[c], s[c + 1], sc);
+          // 2 / the power of two of mb
+          mul2(s[c], s[c + 1], __uint_as_float(~mb[c] & 0x7F800000u), __uint_as_float(~mb[c + 1] & 0x7F800000u));
         }
-        hilo_x4(y, hi[g / 4], lo[g / 4]);
+        hilo_x4(s + g, hi[g / 4], lo[g / 4]);
       }
       if (lane == 0) {
 #pragma unroll
