@@ -100,8 +100,8 @@ struct Form {
   // count as that.  (What f16 cannot hold lies 2^-31 below that largest; narrow blocks have scales.)
   static constexpr float BASE = WIDE ? 6.0f : -30.0f, LEAST = WIDE ? -90.0f : -60.0f;
 };
-// registers a thread in the wide form: softmax warps take what the others give up (in all, the
-// launch's)
+// registers a thread at launch; in the wide form softmax warps then take what the others give up (in
+// all, the launch's)
 constexpr int REGS = 80, SOFT_REGS = 88, OTHER_REGS = 64;
 static_assert(SOFT_REGS * SOFT + OTHER_REGS * (THREADS - SOFT) == REGS * THREADS, "register split");
 
@@ -449,7 +449,7 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
 }
 
 template <bool WIDE>
-__global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constant__ Args ar) {
+__global__ void __maxnreg__(REGS) attend_kernel(const __grid_constant__ Args ar) {
   using F = Form<WIDE>;
   constexpr int NQ = F::NQ, ST = F::ST, PREP_WARP = F::PREP_WARP, PREP = F::PREP, S_WARP = F::S_WARP,
                 O_WARP = F::O_WARP, MMA_WARPS = F::MMA_WARPS, LOAD_WARP = F::LOAD_WARP,
