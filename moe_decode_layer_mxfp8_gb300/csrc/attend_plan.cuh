@@ -12,6 +12,9 @@ namespace attend {
 constexpr int MAX_REQ = 512;
 constexpr int MAX_COLS = 96;  // query columns of a row group at most
 constexpr float UNSET = -1.0e30f;  // the reference m_q of a query that has seen no token
+// A reference beyond this makes its column NaN: rounded to an f32 it could miss the weight that it is
+// made for by more than 2^8, and f16 weights pass 2^16.
+constexpr float SCORE_MAX = 0x1p27f;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 // How a kernel deals the work out: a tile of `tile` tokens, row groups of rows_per rows (cols query

@@ -312,7 +312,7 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
           const float old = -sh.neg_m[w.flat + lane];
           float f = 1.0f;
           if (m - old > F::BASE) {
-            const float now = fminf(ceilf(m) - F::BASE, 3.0e38f);
+            const float now = fabsf(m) <= SCORE_MAX ? ceilf(m) - F::BASE : __int_as_float(0x7FC00000);
             f = old == UNSET ? 0.0f : ex2(old - now);
             sh.neg_m[w.flat + lane] = -now;
           }

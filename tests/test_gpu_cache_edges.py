@@ -348,3 +348,46 @@ def test_the_largest_budget():
     assert h.status() == 0 and kept[0, :50].tolist() == list(range(50))
     assert all(bool((kept[0, i:i + 2 ** 28] == -1).all()) for i in range(50, n, 2 ** 28))
     h.close()
+
+
+# ------------------------------------------------------------------------- ends of the range
+@pytest.mark.parametrize("rows", [1, 6], ids=["narrow", "wide"])
+@pytest.mark.parametrize("L", [200, 40000], ids=["one_piece", "pieces"])
+def test_attend_scores_beyond_f32(rows, L):
+    """A score that an f32 cannot hold makes its head NaN, not 0."""
+    m = _m()
+    dev = torch.device("cuda")
+    n = -(-L // 16)
+    pool = torch.full((n, 16, 80), 0x38, dtype=torch.uint8, device=dev)  # codes of 1.0
+    pool[..., 64:68] = torch.tensor([1.0], device=dev).view(torch.uint8)
+    q = torch.ones((rows, 256), dtype=torch.bfloat16)
+    q[:, 64:128] = 0.0
+    pos = [L - 1] * rows
+    table = np.arange(n, dtype=np.int32)[None]
+    o, lse, _, st = run_attend(m, TINY, q, pos, [0] * rows, table, pool, scale=1e38)
+    o = o.reshape(rows, 4, 64)
+    assert st == 0 and np.isnan(o[:, [0, 2, 3]]).all() and not np.isfinite(lse[:, [0, 2, 3]]).any()
+    # (the second head's scores are zeros)
+    assert (o[:, 1] == 1).all() and np.abs(lse[:, 1] - np.log(L)).max() <= 2.0 ** -18
+
+
+@pytest.mark.parametrize("rows", [1, 6], ids=["narrow", "wide"])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attend_scores_near_and_beyond_the_limit(rows, sign):
+    """One key's scores, all alike but for one token: at 2^25 the weights of the others are as they
+    should be, beyond 2^26 a head is NaN, never 0."""
+    m = _m()
+    dev = torch.device("cuda")
+    L = 900
+    n = -(-L // 16)
+    pool = torch.full((n, 16, 80), 0x38, dtype=torch.uint8, device=dev)
+    pool[..., 64:68] = torch.tensor([1.0], device=dev).view(torch.uint8)
+    q = torch.full((rows, 256), float(sign), dtype=torch.bfloat16)
+    table = np.arange(n, dtype=np.int32)[None]
+    for power, fine in ((10, True), (25, True), (28, False), (40, False), (90, False)):
+        o, lse, _, st = run_attend(m, TINY, q, [L - 1] * rows, [0] * rows, table, pool, scale=2.0 ** (power - 6))
+        assert st == 0
+        if fine:  # (a score is exact; its reference is a multiple of 2 there, o a sum of equal weights)
+            assert (o == 1).all() and np.abs(lse - sign * 2.0 ** power - np.log(L)).max() <= 2.0 ** (power - 22)
+        else:
+            assert np.isnan(o).all() and np.isnan(lse).all()
