@@ -52,7 +52,7 @@ int mono_cache_status(mono_cache_t *h, int clear);
  * with every sum in f32; o is rounded to bf16 once.  Rows with positions[r] < 0 (pad rows) and
  * rows that see no token give o = 0 and lse = -inf.  Tokens outside a row's view never reach
  * its result, whatever their records hold.  A NaN code of a token in view makes NaN the heads whose
- * slices lie in its 128-byte run of the record.
+ * slices lie in its 128-byte run of the record; a scale above 2^64 or NaN, all heads.
  * A head whose largest scores (of all tokens, or of a run of them) are beyond 2^26 in size is NaN.  Tokens of unmapped pages (table entries outside
  * [0, kv_num_blocks), logical pages >= max_blocks) and rows with row_req outside [0, n_req) are
  * left out and raise MONO_STATUS_UNMAPPED_PAGE.  A wait that runs out raises

@@ -12,6 +12,10 @@ namespace attend {
 constexpr int MAX_REQ = 512;
 constexpr int MAX_COLS = 96;  // query columns of a row group at most
 constexpr float UNSET = -1.0e30f;  // the reference m_q of a query that has seen no token
+// Token scales above this (and infinite ones) count as NaN.  The reference follows weights times scales,
+// so that a weight itself lies as far below 2^-30 as its scale lies above 1: beyond this scale, weights
+// that count would be lost to an f32, and their sum with them.
+constexpr float SCALE_MAX = 0x1p64f;
 // A reference beyond this makes its column NaN: rounded to an f32 it could miss the weight that it is
 // made for by more than 2^8, and f16 weights pass 2^16.
 constexpr float SCORE_MAX = 0x1p27f;

@@ -245,7 +245,7 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
     const float raw = reinterpret_cast<const float*>(sm + F::SC_OFF)[(st * TT + tok) * 4];
     const uint32_t ok = sh.valid[st][quad];
     // (a token that is not there has whatever was left in its place: no scale)
-    const bool fin = ((ok >> lane) & 1) && fabsf(raw) <= 3.0e38f;
+    const bool fin = ((ok >> lane) & 1) && fabsf(raw) <= SCALE_MAX;
     const float ct = fin ? raw * w.to_log2 : __int_as_float(0x7FC00000);
     const float sc = fin ? raw : 0.0f, size = fabsf(sc);
     const float size64 = size * 0x1p-6f;

@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_weights_kernel(const __grid
             if (chunk == 0) {
               const float raw = reinterpret_cast<const float*>(sm + SC_OFF)[(st * TT + tok) * 4];
               const uint32_t ok = ss.valid[st][quad];
-              ct = fabsf(raw) <= 3.0e38f ? raw * to_log2 : __int_as_float(0x7FC00000);
+              ct = fabsf(raw) <= SCALE_MAX ? raw * to_log2 : __int_as_float(0x7FC00000);
               there = (ok >> lane) & 1;
               see = there ? (1u << nrows) - 1 : 0u;  // (no padding columns: a NaN score would count)
               if (__builtin_expect(!clear.has(i), 0)) {

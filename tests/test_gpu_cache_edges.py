@@ -352,6 +352,33 @@ def test_the_largest_budget():
 
 # ------------------------------------------------------------------------- ends of the range
 @pytest.mark.parametrize("rows", [1, 6], ids=["narrow", "wide"])
+@pytest.mark.parametrize("exponent", [60, 63.9, 70, 100, 126])
+def test_attend_largest_scales(rows, exponent):
+    """Scales up to 2^64 count as they are; rows that see a larger one are NaN, the others as without
+    it (and NaN where their own scores are beyond 2^26)."""
+    m = _m()
+    L = 300
+    table, cache = make_cache(TINY, [L], 51)
+    rng = np.random.default_rng(51)
+    for t in range(L):
+        rec = cache[table[0, t // 16], t % 16]
+        s = np.float32(2.0 ** exponent * (1 if t == 294 else rng.uniform(0.5, 1) if exponent < 64 else 2.0 ** -90))
+        rec[64:68] = np.frombuffer(s.tobytes(), np.uint8)
+    q = make_q(TINY, rows, 51)
+    pos = [296 - i for i in range(rows)]
+    k = 0.125 * 2.0 ** -exponent if exponent < 64 else 0.125
+    args = dict(scale=k, weights=torch.zeros((1, L)))
+    o, lse, w, st = run_attend(m, TINY, q, pos, [0] * rows, table, cache, **args)
+    eo, tol, el, ltol, _, _ = co.attend(TINY, q.double().numpy(), pos, [0] * rows, table, cache, scale=k)
+    sees = np.array([p >= 294 and exponent >= 64 for p in pos])
+    far = np.abs(el) > 2.0 ** 26
+    assert np.isnan(lse[far]).all() and np.isnan(o.reshape(rows, 4, 64)[far]).all()
+    sees |= far.any(1)
+    assert st == 0 and np.isnan(o[sees]).all() and np.isnan(lse[sees]).all()
+    assert (np.abs(o - eo) <= tol)[~sees].all() and (np.abs(lse - el) <= ltol)[~sees].all()
+
+
+@pytest.mark.parametrize("rows", [1, 6], ids=["narrow", "wide"])
 @pytest.mark.parametrize("L", [200, 40000], ids=["one_piece", "pieces"])
 def test_attend_scores_beyond_f32(rows, L):
     """A score that an f32 cannot hold makes its head NaN, not 0."""
