@@ -202,7 +202,8 @@ struct TileLoader {
 };
 
 // Eight elements of a query (q: bf16) as two e4m3 terms under the power of two that four neighbouring
-// lanes' 32 elements share: its code.
+// lanes' 32 elements share: its code.  The largest element is in [2^7, 2^8) then, a code's least step
+// 2^-9, and eight bits from 2^-2 up are the two terms' eight; smaller elements are off by up to 2^-10.
 __device__ __forceinline__ uint32_t split_query(uint4 q, uint2& hi, uint2& lo) {
   float v[8];
   bf16x8_to_f32(q, v);

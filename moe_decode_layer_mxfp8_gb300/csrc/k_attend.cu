@@ -9,7 +9,8 @@
 // queries the N of both: the heads that share a latent slice, times the rows of a request that
 // share its context (1 to 96 columns, padded to 16), so the cache is read once for all of them.
 // The first product takes the e4m3 tile as it lies in the cache (kind::mxf8f6f4); a bf16 query is
-// the exact sum of two e4m3 terms under one power-of-two scale per 32 dimensions.  The second one
+// the sum of two e4m3 terms under one power-of-two scale per 32 dimensions: exactly, but for elements
+// below 2^-9 of the 32's largest, which are off by up to 2^-17 of it.  The second one
 // has two forms:
 //   narrow: the same tile, transposed, against P scale_t as two e4m3 terms (together 8 bits, the
 //     one rounding between scores and o) under a power-of-two scale per column and 32 tokens: the
@@ -17,9 +18,10 @@
 //     columns of one MMA, added when accumulators are read.
 //   wide: the tile widened to f16 (exact) against P scale_t in f16 (11 bits): widening costs
 //     shared-memory bandwidth and four warps, but a weight only some 6 instructions.
-// Requests of up to 32 columns on average take the narrow form.  Measured over 8 contexts of
-// 1K..64K tokens, 16 heads a slice, rows of a request 1 / 2 / 3 / 4: narrow 40 / 57 / 86 / 96 us,
-// wide 68 / 72 / 77 / 81 us.
+// Steps of up to 32 columns a request on average take the narrow form; the average is over the rows of
+// the block table (the host does not see which of them have rows).  Measured over 8 contexts of
+// 1K..64K tokens, 16 heads a slice, rows of a request 1 / 2 / 3 / 4: narrow 41 / 56 / 84 / 92 us,
+// wide 69 / 73 / 78 / 82 us.
 // O stays in TMEM over a whole run of tiles: m_q, an integer, is set by the run's first tile and
 // moves only when a weight passes it by far (then O is rescaled, exactly).
 //
@@ -36,16 +38,15 @@
 // fourth tile each, with 32 two groups share every other tile, with more the groups share all
 // tiles.  Then come the warps that make the next item's queries while the current one runs (in the
 // wide form they widen tiles too), those that issue the first product's MMAs, the second's, and two
-// that load (every other slot of the ring each: TMA boxes through the page table, or cp.async for page sizes
-// that are no multiple of 8).  A wait for a barrier that is complete still costs a warp 100 to 300
+// that load (every other slot of the ring each: TMA boxes through the page table, or cp.async for
+// page sizes that are no multiple of 8).  A wait for a barrier that is complete still costs a warp 100 to 300
 // cycles, an MMA's issue some 60: hence two warps for each product in the narrow form, whose tiles
 // take 700 cycles, and one wait per tile in the softmax.  What runs once per launch or item is kept
 // short, in rolled loops: its instructions come from L2 or further away.
 //
-// Measured: 8 rows over 8 contexts of 1K..64K 39 us, of which 31 are the tiles' (137 MB; copy: 20 us),
-// the rest launches, the cut and the join; bound by HBM while tiles run, by the first tile's latency
-// before.  48 rows 96 us, bound by the softmax warps' latencies (2850 cycles a tile, 0.6 instructions
-// a cycle; its MMAs take 1250).  One row over 777 tokens 12 us: launches and latencies.
+// Measured: 8 rows over 8 contexts of 1K..64K 41 us (137 MB; copy: 20 us), some 8 of them launches, the
+// cut and the join; bound by HBM while tiles run, by the first tile's latency before.  48 rows 97 us, bound by the softmax warps' latencies (2850 cycles a tile, 0.6 instructions
+// a cycle; its MMAs take 1250).  One row over 777 tokens 12.5 us: launches and latencies.
 // Every mbarrier wait is bounded; a wait that runs out is reported, and from then on every role
 // runs its loop without waiting, copying or issuing, so that the barriers among warps still
 // complete and TMEM is freed.
@@ -663,8 +664,8 @@ __global__ void __maxnreg__(REGS) attend_kernel(const __grid_constant__ Args ar)
         wait(&ss.q_full[qb], (item >> 1) & 1, a.status, abort);
         const Deal<WIDE> deal(ss.meta[qb].cols);
         // the queries' terms: two columns of the scores each, or added up (wide)
-      const int n = WIDE ? deal.nqp : 2 * deal.nqp;
-      const uint32_t idesc = IDESC | ((uint32_t)(n >> 3) << 17);
+        const int n = WIDE ? deal.nqp : 2 * deal.nqp;
+        const uint32_t idesc = IDESC | ((uint32_t)(n >> 3) << 17);
         const uint64_t qd = q0 + (deal.q_byte(item) >> 4);
         if (elect_one()) {
           const uint8_t* img = sm + F::QIMG_OFF + qb * IMG;

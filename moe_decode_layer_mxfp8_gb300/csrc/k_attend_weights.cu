@@ -9,7 +9,7 @@
 // token's sum stays in one register, in a fixed order, with one writer.  The four groups work on four
 // tiles at a time, whose chunks come in turn.  Requests with more rows than a pass holds are read once
 // per pass.
-// Measured: 8 rows over 8 contexts of 1K..32K tokens 22 us (71 MB; copy: 10 us), bound by HBM while
+// Measured: 8 rows over 8 contexts of 1K..32K tokens 27 us (71 MB; copy: 10 us), bound by HBM while
 // tiles run; m16n8k16 MMAs on codes widened in registers took 50.
 #include "attend_tc.cuh"
 

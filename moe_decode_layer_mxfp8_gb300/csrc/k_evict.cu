@@ -14,8 +14,9 @@
 // places behind).  Chunks are handed out in order, so a chunk waits only for chunks that have begun,
 // and those publish their loads before they wait.  Weights move the same way.
 // Bound by HBM and the chain of lookups ahead of a chunk's loads: each kept record is read once and
-// written once.  Measured: 8 caches of 33K..64K tokens of 528 bytes cut to 32K, 62 us, of which the
-// selection takes 14 and the move 47 (274 MB; copy: 40 us); 3 of up to 5K tokens 12 us, latencies.
+// written once.  Measured: 8 caches of 33K..64K tokens of 528 bytes cut to 32K on other pages, 63 us, of
+// which the selection takes 14 and the move 47 (274 MB; copy: 40 us); in place, with the waits among
+// chunks, 78 us.  3 of up to 5K tokens 12 us, latencies.
 #include <algorithm>
 
 #include "cache_kernels.h"

@@ -10,8 +10,8 @@
 // the threshold finds the block and reads it again, in order.  A request whose residual is empty
 // takes a second pass over p.
 // Bound by reading the one row pair that the token is drawn from; small ones by latencies.
-// Measured: 192 requests of 3 drafts, 100003 bf16 entries, a quarter of them greedy 28.5 us (77 MB; copy:
-// 11 us), 8 of 5 drafts, 131072 f32 entries 10.5 us, 4 of 2 table drafts, 32000 f16 entries 7.2 us.
+// Measured: 192 requests of 3 drafts, 100003 bf16 entries, a quarter of them greedy 30.5 us (77 MB; copy:
+// 11 us), 8 of 5 drafts, 131072 f32 entries 10.8 us, 4 of 2 table drafts, 32000 f16 entries 7.6 us.
 // Sums decide which token is drawn, so they are carried as pairs of f32 (error-free additions and
 // products, and p - q as a pair) for every type: with 10^5 tokens, what an f32 sum of a large entry and
 // three small ones loses can move as much as one draw in a thousand by a token.  FP64 runs at a 64th of

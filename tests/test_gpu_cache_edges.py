@@ -418,3 +418,20 @@ def test_attend_scores_near_and_beyond_the_limit(rows, sign):
             assert (o == 1).all() and np.abs(lse - sign * 2.0 ** power - np.log(L)).max() <= 2.0 ** (power - 22)
         else:
             assert np.isnan(o).all() and np.isnan(lse).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("draft", [True, False])
+def test_verify_infinite_target_entries(dtype, draft):
+    """An infinite entry leaves nothing to draw from, in a residual and in a last row."""
+    m = _m()
+    g = torch.Generator().manual_seed(62)
+    p, q = torch.rand((6, 999), generator=g), torch.rand((6, 999), generator=g)
+    p[:, 500] = float("inf")
+    q[0, 500] = float("inf")
+    tok = [0, 0, 500, 0, 0, 0]  # the first draft falls, the second request's stands
+    u = np.array([0.999999, 0, 0.5, 0, 0, 0], np.float32)
+    p[0, 0] = 0.0
+    acc, out = run_verify(m, p.to(dtype).cuda(), q.to(dtype).cuda() if draft else None, tok, [0, 2, 4, 6], u,
+                          np.full(3, 0.5, np.float32))
+    assert acc[:2] == [0, 1] and out[:4] == [-1, -1, 500, -1]
