@@ -64,7 +64,8 @@ int mono_cache_status(mono_cache_t *h, int clear);
  * a table of the step's requests alone lets the kernels group rows best.
  *
  * weights, if given, gathers every cached token's attention weight: weights[b][t] += the sum
- * over b's rows and all heads of w[t], for t < weights_cols.  The order of that sum is fixed.
+ * over b's rows and all heads of w[t], for t < weights_cols.  The order of that sum is fixed; it is added
+ * a few of b's rows at a time (three at 16 heads a slice), each addition rounded to f32.
  *
  * Limits: max_blocks * block_size at most 2^31 - 2^16; its tiles of 128 tokens, and 16 more, times rows
  * below 2^31.
