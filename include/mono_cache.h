@@ -49,16 +49,18 @@ int mono_cache_status(mono_cache_t *h, int clear);
  * those of the rows before it) must be in the cache already, as mono_layer_step's insert
  * leaves them.  Head h reads latent slice g = h / (n_q_heads / (kv_dim/head_dim)) as key and value:
  *   s[t] = scale * scale_t * (q_h . codes_t,g)     w = softmax(s)     o_h = sum_t w[t] scale_t codes_t,g
- * with every sum in f32.  o is rounded to bf16 once; before that w[t] scale_t is rounded to 8 bits, or
- * to 11 where rows / n_req times the heads of a 128-byte run of the record is above 32 (lse is of
- * weights as they are), and q's elements to 2^-17 of the largest of their 32.  Rows with positions[r] < 0 (pad rows) and
- * rows that see no token give o = 0 and lse = -inf.  Tokens outside a row's view never reach
- * its result, whatever their records hold.  A NaN code of a token in view makes NaN the heads whose
- * slices lie in its 128-byte run of the record; a scale above 2^64 or NaN, all heads.
- * A head whose largest scores (of all tokens, or of a run of them) are beyond 2^26 in size is NaN.  Tokens of unmapped pages (table entries outside
- * [0, kv_num_blocks), logical pages >= max_blocks) and rows with row_req outside [0, n_req) are
- * left out and raise MONO_STATUS_UNMAPPED_PAGE.  A wait that runs out raises
- * MONO_STATUS_WAIT_TIMEOUT; the step's outputs are then undefined.
+ * with every sum in f32.  o is rounded to bf16 once; before that w[t] scale_t is rounded to 8 bits (and
+ * to 2^-17 of the largest of 32 tokens), or to 11 where rows / n_req, rounded up, times the heads of a
+ * 128-byte run of the record is above 32 (lse is of weights as they are), and q's elements to 2^-17 of
+ * the largest of their 32.  Rows with
+ * positions[r] < 0 (pad rows) and rows that see no token give o = 0 and lse = -inf.  Tokens outside a
+ * row's view never reach its result, whatever their records hold.  A NaN code of a token in view makes
+ * NaN the heads whose slices lie in its 128-byte run of the record; a scale that is NaN or beyond 2^64 in
+ * size, all heads.  A head whose largest scores (of all tokens, or of a run of them) are beyond 2^26 in
+ * size is NaN.  Tokens of unmapped pages (table entries outside [0, kv_num_blocks), logical pages >=
+ * max_blocks) and rows with row_req outside [0, n_req) are left out and raise
+ * MONO_STATUS_UNMAPPED_PAGE.  A wait that runs out raises MONO_STATUS_WAIT_TIMEOUT; the step's outputs
+ * are then undefined.
  *
  * n_req is the number of rows of block_table; those that no row of the step belongs to cost little, but
  * a table of the step's requests alone lets the kernels group rows best.
@@ -152,11 +154,11 @@ int mono_cache_evict(mono_cache_t *h, const mono_evict_args *args, void *stream)
  *   accepted[b] = number of accepted drafts
  *   tokens[row] = accepted drafts, then the drawn token, then -1
  * Tests and sums are carried in enough bits (products exact, sums in two f32) that roundings
- * decide nothing in practice.  Rows need not be normalised;
- * negative and NaN entries count as 0 where a token is drawn, and a draw from zeros yields -1.  Drafted tokens
- * outside [0, vocab) are refused.  An infinite target entry leaves nothing to draw from (-1), an infinite
- * draft entry takes all of the target's.  Requests without rows get accepted[b] = 0; rows outside
- * every request keep their tokens; row_start entries are cut to [0, rows].
+ * decide nothing in practice.  Rows need not be normalised; negative and NaN entries count as 0
+ * where a token is drawn, and a draw from zeros yields -1.  An infinite target entry leaves nothing
+ * to draw from (-1), an infinite draft entry takes all of the target's.  Drafted tokens outside
+ * [0, vocab) are refused.  Requests without rows get accepted[b] = 0; rows outside every request
+ * keep their tokens; row_start entries are cut to [0, rows].
  */
 enum { MONO_PROB_F32 = 0, MONO_PROB_BF16 = 1, MONO_PROB_F16 = 2 };
 typedef struct {

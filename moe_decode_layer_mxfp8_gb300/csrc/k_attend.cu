@@ -39,14 +39,15 @@
 // tiles.  Then come the warps that make the next item's queries while the current one runs (in the
 // wide form they widen tiles too), those that issue the first product's MMAs, the second's, and two
 // that load (every other slot of the ring each: TMA boxes through the page table, or cp.async for
-// page sizes that are no multiple of 8).  A wait for a barrier that is complete still costs a warp 100 to 300
-// cycles, an MMA's issue some 60: hence two warps for each product in the narrow form, whose tiles
-// take 700 cycles, and one wait per tile in the softmax.  What runs once per launch or item is kept
+// page sizes that are no multiple of 8).  A wait for a barrier that is complete still costs a warp 100
+// to 300 cycles, an MMA's issue some 60: hence two warps for each product in the narrow form, whose
+// tiles take 700 cycles, and one wait per tile in the softmax.  What runs once per launch or item is kept
 // short, in rolled loops: its instructions come from L2 or further away.
 //
 // Measured: 8 rows over 8 contexts of 1K..64K 41 us (137 MB; copy: 20 us), some 8 of them launches, the
-// cut and the join; bound by HBM while tiles run, by the first tile's latency before.  48 rows 97 us, bound by the softmax warps' latencies (2850 cycles a tile, 0.6 instructions
-// a cycle; its MMAs take 1250).  One row over 777 tokens 12.5 us: launches and latencies.
+// cut and the join; bound by HBM while tiles run, by the first tile's latency before.  48 rows 97 us,
+// bound by the softmax warps' latencies (2850 cycles a tile, 0.6 instructions a cycle; its MMAs take
+// 1250).  One row over 777 tokens 12.5 us: launches and latencies.
 // Every mbarrier wait is bounded; a wait that runs out is reported, and from then on every role
 // runs its loop without waiting, copying or issuing, so that the barriers among warps still
 // complete and TMEM is freed.

@@ -218,9 +218,9 @@ def attend_model(wide, items, seed):
     tile), the warps that make queries and widen tiles another."""
     F, which = "k_attend.cu", 1 if wide else 2
     ST, MMAS = constant("ST", F, which), constant("MMA_WARPS", F, which)
-    LOADERS, GROUPS = 2, 4
+    LOADERS, GROUPS = constant("LOAD_WARPS", F), 4
     told = has(F, TOLD)
-    by_slot = has(F, "each slot of the ring has one loading warp")
+    by_slot = has(F, "s + LOAD_WARPS < ST ? LOAD_WARPS : ST - s + lw")
     m = Machine(seed)
     full = [Bar(2) for _ in range(ST)]
     k_free = [Bar(2 + 4 if wide else 1) for _ in range(ST)]
