@@ -208,7 +208,7 @@ __device__ __forceinline__ Vec<T> load_vec(const T* p, int v0, int V, bool align
   Vec<T> r;
   if (aligned && v0 >= 0 && v0 + VEC <= V) {
     r.x = __ldg(reinterpret_cast<const uint4*>(p + v0));
-  } else {  // a row's ends, or q out of step with p: rare, and short code
+  } else {  // a row's ends, or all of a q out of step with p (192 requests: 61 us instead of 30)
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll 1
     for (int e = 0; e < VEC; ++e) {
