@@ -2,7 +2,8 @@
  * mono_cache.h -- C ABI of the operators around the decode layer's paged KV cache, for one
  * GB300 (sm_103a): attention of a step's rows over their requests' whole cached context (or a
  * sliding window with first tokens that stay visible), eviction of the tokens that gathered
- * the least attention weight, and verification of drafted tokens.  They serve the layers
+ * the least attention weight, appending rows' latents with their rotary positions, and verification
+ * of drafted tokens.  They serve the layers
  * whose attention runs outside mono_layer_step (mono_ffn_step takes its output) and the
  * serving loop around a stack of layers; the same library and error codes (mono_layer.h).
  *
@@ -139,6 +140,75 @@ typedef struct {
 } mono_evict_args;
 
 int mono_cache_evict(mono_cache_t *h, const mono_evict_args *args, void *stream);
+
+/*
+ * Rotary positions.  A row at rotary position t turns every head (or latent slice) x of head_dim
+ * elements: of the pairs (x1, x2) of its dimensions [offset, offset + dim), which are neighbours
+ * (interleaved != 0) or the halves' elements i and i + dim / 2, pair i becomes
+ *   y1 = x1 cos_i - x2 sin_i     y2 = x2 cos_i + x1 sin_i
+ * with cos_i = table[t][i], sin_i = table[t][dim / 2 + i] (inverse != 0: -sin_i), products and sums
+ * rounded to f32 one by one, the result to its type.  dim is a multiple of 16 up to head_dim, offset
+ * one of 8.  A row whose t is outside [0, positions) is skipped and raises MONO_STATUS_POSITION.
+ */
+typedef struct {
+  const float *table;         /* [positions, dim], 16-byte aligned; NULL: no rotation */
+  int64_t stride;             /* elements between rows, a multiple of 4; 0: dim */
+  int64_t positions;          /* 1 .. 2^31 - 1 */
+  int32_t dim, offset;
+  int32_t interleaved, inverse;
+} mono_rope;
+
+/* Element types of the calls below. */
+enum { MONO_TYPE_F32 = 0, MONO_TYPE_BF16 = 1, MONO_TYPE_F16 = 2 };
+
+/*
+ * Appending to the cache, with the rotation on the way.  Row r's latent kv[r], its slices turned by
+ * rope_positions[r] (NULL: positions[r]; after an eviction the two differ), is stored as the record of
+ * slot positions[r] of request row_req[r], as mono_layer_step stores one: s = amax / 448 (1 where that
+ * is 0), codes = e4m3 of latent / s, to nearest even and saturating, then s; bytes behind them are left
+ * as they were.  The rotated latent is not rounded before.  q, if given, is turned by the same positions
+ * into q_out (which may be q), every head of it.  Rows with positions[r] < 0 (pad rows) write nothing.
+ * Rows with row_req outside [0, n_req) and rows of unmapped pages store no record (their queries
+ * are turned) and raise MONO_STATUS_UNMAPPED_PAGE.  A NaN of the latent is a NaN code and does not
+ * count in amax; a latent with an infinity gets an infinite scale.  Rows that name the same slot leave
+ * an undefined record there.  Any number of rows (at most 2^30) and requests: max_rows and max_req
+ * are no limits here, and no workspace is used.
+ */
+typedef struct {
+  const void *kv;             /* [rows, kv_dim], 16-byte aligned, not in the cache */
+  const void *q;              /* optional [rows, n_q_heads * head_dim]; needs a table */
+  void *q_out;                /* like q: q itself with its stride, or not overlapping it */
+  int64_t kv_stride, q_stride, q_out_stride; /* elements between rows, whole 16 bytes; 0: packed */
+  const int32_t *positions;   /* [rows], < 0 for a pad row */
+  const int32_t *rope_positions; /* optional [rows] */
+  const int32_t *row_req;     /* [rows] */
+  const int32_t *block_table; /* [n_req, max_blocks] */
+  uint8_t *kv_cache;          /* [kv_num_blocks, block_size, record] view, as in mono_step_args */
+  int64_t kv_stride_block, kv_stride_tok, kv_num_blocks;
+  mono_rope rope;
+  int32_t dtype;              /* MONO_TYPE_*, of kv, q and q_out */
+  int32_t rows, n_req, max_blocks;
+} mono_append_args;
+
+int mono_cache_append(mono_cache_t *h, const mono_append_args *args, void *stream);
+
+/*
+ * Rotation alone: heads of head_dim, x into out (which may be x).  The cached latents are values, too,
+ * so where they are rotated an attention's output is a sum of values turned by their own positions:
+ * turned back (inverse) by the row's position, it depends on the distances only.  Pad rows
+ * (positions[r] < 0) are left as they were.  At most 2^30 rows and 2^20 heads.
+ */
+typedef struct {
+  const void *x;              /* [rows, heads * head_dim], 16-byte aligned */
+  void *out;                  /* like x: x itself with its stride, or not overlapping it */
+  int64_t x_stride, out_stride; /* elements between rows, whole 16 bytes; 0: packed */
+  const int32_t *positions;   /* [rows] rotary positions, < 0 for a pad row */
+  mono_rope rope;
+  int32_t dtype;              /* MONO_TYPE_*, of x and out */
+  int32_t rows, heads;
+} mono_rotate_args;
+
+int mono_cache_rotate(mono_cache_t *h, const mono_rotate_args *args, void *stream);
 
 /*
  * Verification of drafted tokens.  Request b's rows are [row_start[b], row_start[b + 1]): one

@@ -54,9 +54,10 @@ enum {
   MONO_STATUS_UNMAPPED_PAGE = 1, /* a block-table entry was outside [0, kv_num_blocks) */
   MONO_STATUS_WAIT_TIMEOUT = 2,  /* a pipeline wait ran past its time budget */
   MONO_STATUS_BAD_ROUTE = 4,     /* routing metadata out of range */
-  MONO_STATUS_F16_RANGE = 8      /* an activation copied to f16 for the tensor cores was
+  MONO_STATUS_F16_RANGE = 8,     /* an activation copied to f16 for the tensor cores was
                                     beyond +-65504 and was saturated there (the step's
                                     result then differs from the unsaturated layer) */
+  MONO_STATUS_POSITION = 16      /* a rotary position was outside its table (mono_cache.h) */
 };
 
 /*

@@ -46,6 +46,28 @@ class EvictArgs(C.Structure):
                 ("weights_out_cols", C.c_int64)]
 
 
+class Rope(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("stride", C.c_int64), ("positions", C.c_int64),
+                ("dim", C.c_int32), ("offset", C.c_int32), ("interleaved", C.c_int32),
+                ("inverse", C.c_int32)]
+
+
+class AppendArgs(C.Structure):
+    _fields_ = [("kv", C.c_void_p), ("q", C.c_void_p), ("q_out", C.c_void_p),
+                ("kv_stride", C.c_int64), ("q_stride", C.c_int64), ("q_out_stride", C.c_int64),
+                ("positions", C.c_void_p), ("rope_positions", C.c_void_p), ("row_req", C.c_void_p),
+                ("block_table", C.c_void_p), ("kv_cache", C.c_void_p),
+                ("kv_stride_block", C.c_int64), ("kv_stride_tok", C.c_int64),
+                ("kv_num_blocks", C.c_int64), ("rope", Rope), ("dtype", C.c_int32),
+                ("rows", C.c_int32), ("n_req", C.c_int32), ("max_blocks", C.c_int32)]
+
+
+class RotateArgs(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("out", C.c_void_p), ("x_stride", C.c_int64),
+                ("out_stride", C.c_int64), ("positions", C.c_void_p), ("rope", Rope),
+                ("dtype", C.c_int32), ("rows", C.c_int32), ("heads", C.c_int32)]
+
+
 class VerifyArgs(C.Structure):
     _fields_ = [("target", C.c_void_p), ("draft", C.c_void_p), ("target_stride", C.c_int64),
                 ("draft_stride", C.c_int64), ("dtype", C.c_int32), ("vocab", C.c_int32),
@@ -57,10 +79,12 @@ class VerifyArgs(C.Structure):
 # The same structures packed at once: setting ctypes fields one by one took most of a call.
 _ATTEND = struct.Struct("@PPqqPPPiiiiiifPqqqPPqq")
 _EVICT = struct.Struct("@PPqqPPPqiiiiPiPqqqPiPqqqqq")
+_APPEND = struct.Struct("@PPPqqqPPPPPqqqPqqiiiiiiii")
+_ROTATE = struct.Struct("@PPqqPPqqiiiiiii4x")
 _VERIFY = struct.Struct("@PPqqiiiiPPPPPPP")
 
 CACHE_EXPORTS = ["mono_cache_build", "mono_cache_free", "mono_cache_status", "mono_cache_attend",
-                 "mono_cache_evict", "mono_verify_drafts"]
+                 "mono_cache_evict", "mono_cache_append", "mono_cache_rotate", "mono_verify_drafts"]
 
 
 def _lib() -> C.CDLL:
@@ -72,6 +96,8 @@ def _lib() -> C.CDLL:
         L.mono_cache_status.argtypes = [C.c_void_p, C.c_int]
         L.mono_cache_attend.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
         L.mono_cache_evict.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
+        L.mono_cache_append.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
+        L.mono_cache_rotate.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
         L.mono_verify_drafts.argtypes = [C.c_void_p, C.c_void_p]
         L._mono_cache_ready = True
     return L
@@ -247,6 +273,64 @@ class Cache:
                      recent, n_req, _table(block_table, "block_table", None, dev), max_blocks,
                      *self._view(kv_cache, "kv_cache"), tp, tb, *dst, wc, vc)
         self._call("mono_cache_evict", args, stream)
+
+    def _rope(self, rope, offset, interleaved, inverse):
+        """The fields of a rotation: ``rope`` is f32 [positions, dim]."""
+        p, stride = _mat(rope, "rope", _F32, None, None, self._dev)
+        positions, dim = rope.shape
+        if offset is None:
+            offset = self.spec["head_dim"] - dim
+        return p, stride, positions, dim, offset, 1 if interleaved else 0, 1 if inverse else 0
+
+    def append(self, kv, positions, row_req, block_table, kv_cache, *, rope=None, rope_offset=None,
+               interleaved=False, rope_positions=None, q=None, q_out=None, stream=None) -> None:
+        """Stores the rows' latents (kv: f32, bf16 or f16 [rows, kv_dim]) as records of the slots
+        ``positions`` (-1: a pad row) of their requests, each latent slice rotated by the row's
+        entry of ``rope`` (f32 [positions, dim]: cosines, then sines; None: no rotation) at
+        ``rope_positions`` (default: ``positions``).  The rotated dimensions of a head are the
+        last ones, or those from ``rope_offset`` on; pairs are halves of them, or neighbours
+        (``interleaved``).  ``q`` (like kv, [rows, n_q_heads * head_dim]) is rotated alike, into
+        ``q_out`` or in place.  Any number of rows and requests."""
+        dev, i32 = self._dev, torch.int32
+        rows, dtype = kv.shape[0], kv.dtype
+        n_req, max_blocks = block_table.shape
+        kp, ks = _mat(kv, "kv", _PROBS, rows, self.spec["kv_dim"], dev)
+        qp, qs, op, os = 0, 0, 0, 0
+        if q is not None:
+            if rope is None:
+                raise ValueError("q needs a rope table")
+            qp, qs = _mat(q, "q", (dtype,), rows, self._width, dev)
+            op, os = (qp, qs) if q_out is None else _mat(q_out, "q_out", (dtype,), rows, self._width, dev)
+        elif q_out is not None:
+            raise ValueError("q_out needs a q")
+        if rope is not None:
+            turn = self._rope(rope, rope_offset, interleaved, False)
+        elif rope_positions is not None or rope_offset is not None:
+            raise ValueError("rope_positions and rope_offset need a rope table")
+        else:
+            turn = (0, 0, 0, 0, 0, 0, 0)
+        args = _pack(_APPEND, kp, qp, op, ks, qs, os, _vec(positions, "positions", i32, rows, dev),
+                     0 if rope_positions is None else _vec(rope_positions, "rope_positions", i32, rows, dev),
+                     _vec(row_req, "row_req", i32, rows, dev),
+                     _table(block_table, "block_table", None, dev), *self._view(kv_cache, "kv_cache"),
+                     *turn, _PROBS[dtype], rows, n_req, max_blocks)
+        self._call("mono_cache_append", args, stream)
+
+    def rotate(self, x, out, positions, rope, *, rope_offset=None, interleaved=False, inverse=False,
+               stream=None) -> None:
+        """Rotates the heads of x (f32, bf16 or f16 [rows, heads * head_dim]) by their rows'
+        rotary ``positions`` (-1: a pad row, left as it is) into ``out``, which may be x;
+        ``inverse`` turns back.  ``rope``, ``rope_offset`` and ``interleaved`` as in append."""
+        dev, dh = self._dev, self.spec["head_dim"]
+        xp, xs = _mat(x, "x", _PROBS, None, None, dev)
+        rows, width = x.shape
+        if width % dh:
+            raise ValueError(f"x has rows of {width} elements, not of heads of {dh}")
+        op, os = _mat(out, "out", (x.dtype,), rows, width, dev)
+        args = _pack(_ROTATE, xp, op, xs, os, _vec(positions, "positions", torch.int32, rows, dev),
+                     *self._rope(rope, rope_offset, interleaved, inverse), _PROBS[x.dtype], rows,
+                     width // dh)
+        self._call("mono_cache_rotate", args, stream)
 
     def _call(self, name, args, stream):
         if not self._h:

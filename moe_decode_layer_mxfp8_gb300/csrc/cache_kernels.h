@@ -2,9 +2,14 @@
 // their kernels.
 #pragma once
 
+#include <cuda_fp8.h>
+
 #include "kernels.h"
 
 namespace mono {
+
+// Device status bit of the cache operators beside those of common.cuh (MONO_STATUS_POSITION).
+constexpr int ST_POSITION = 16;
 
 // The paged cache as the kernels see it: record of (request, token) through the block table.
 struct PagedView {
@@ -64,6 +69,32 @@ struct VerifyArgs {
   int *accepted, *tokens;
 };
 
+// A rotation by position: table [positions][stride], cos of dim / 2 angles, then their sines; the
+// dimensions [offset, offset + dim) of a head.  dim 0: none.
+struct Rope {
+  const float* table;
+  long long stride;
+  int positions, dim, offset, interleaved, inverse;
+};
+struct RotateArgs {
+  int rows, head_dim;
+  const int *positions, *rope_positions;
+  Rope rope;
+  // heads: x [rows, heads * head_dim] into out; x null: none
+  const void* x;
+  void* out;
+  long long x_stride, out_stride;
+  int heads;
+  // latents: kv [rows, kv_dim] into the cache (written, too); kv null: none
+  const void* kv;
+  long long kv_stride;
+  int kv_dim, n_req;
+  const int* row_req;
+  PagedView cache;
+  int* status;
+  unsigned kv_blocks;  // (the launch's)
+};
+
 size_t attend_workspace_bytes(int max_rows, int sms);
 cudaError_t attend_prepare();  // raises the dynamic shared-memory limit
 cudaError_t launch_attend(const Launch&, const AttendArgs&, uint8_t* workspace, int max_rows,
@@ -73,6 +104,7 @@ size_t evict_workspace_bytes(int max_req);
 bool evict_fits(int n_req, int budget, long long cap);
 cudaError_t evict_prepare();
 cudaError_t launch_evict(const Launch&, const EvictArgs&, uint8_t* workspace, int max_req, int sms);
+cudaError_t launch_rotate(const Launch&, const RotateArgs&, int dtype);  // dtype: MONO_TYPE_*
 cudaError_t launch_verify(const Launch&, const VerifyArgs&, int dtype, int sms);
 
 }  // namespace mono

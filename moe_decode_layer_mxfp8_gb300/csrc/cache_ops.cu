@@ -59,6 +59,32 @@ int check_view(const mono_cache_spec& s, const void* base, int64_t stride_block,
 // Rows of `cols` elements (0: stride) that lie `stride` apart.
 bool check_cols(int64_t stride, int64_t cols) { return stride >= 1 && cols >= 0 && cols <= stride; }
 
+constexpr int MAX_ROTATED = 1 << 30;      // rows of a rotating call
+constexpr int TYPE_BYTES[3] = {4, 2, 2};  // MONO_TYPE_*
+bool check_dtype(int dtype) { return dtype >= MONO_TYPE_F32 && dtype <= MONO_TYPE_F16; }
+
+// Rows of `width` elements that lie `stride` apart (0: packed), in whole 16 bytes.
+int check_rows(const void* p, int64_t width, int64_t* stride, int bytes) {
+  if (!*stride) *stride = width;
+  if (*stride < width) return MONO_ERR_INVALID_ARG;
+  return aligned(p, 16) && *stride * bytes % 16 == 0 ? MONO_OK : MONO_ERR_BAD_ALIGNMENT;
+}
+
+// A rotation of heads of head_dim elements.
+int check_rope(const mono_rope& r, int head_dim, Rope* out) {
+  if (!r.table) return MONO_ERR_INVALID_ARG;
+  if (r.dim < 16 || r.dim % 16 || r.dim > head_dim || r.offset < 0 || r.offset % 8 ||
+      r.offset > head_dim - r.dim)
+    return MONO_ERR_UNSUPPORTED_DIMS;
+  int64_t stride = r.stride;
+  const int rc = check_rows(r.table, r.dim, &stride, 4);
+  if (rc != MONO_OK) return rc;
+  if (r.positions < 1 || r.positions > INT32_MAX || stride > INT64_MAX / 4 / r.positions)
+    return MONO_ERR_INVALID_ARG;
+  *out = {r.table, stride, (int)r.positions, r.dim, r.offset, r.interleaved != 0, r.inverse != 0};
+  return MONO_OK;
+}
+
 int check_device(const mono_cache* h) {
   int dev = -1;
   const cudaError_t e = cudaGetDevice(&dev);
@@ -248,6 +274,78 @@ int mono_cache_evict(mono_cache_t* h, const mono_evict_args* a, void* stream) {
   k.status = h->status;
   return cuda_code(launch_evict(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k,
                                 h->evict_ws, s.max_req, h->sms));
+}
+
+int mono_cache_append(mono_cache_t* h, const mono_append_args* a, void* stream) {
+  if (!h || !a) return MONO_ERR_INVALID_ARG;
+  const mono_cache_spec& s = h->spec;
+  if (a->rows < 1 || a->n_req < 1 || !check_dtype(a->dtype)) return MONO_ERR_INVALID_ARG;
+  if (a->rows > MAX_ROTATED) return MONO_ERR_TOO_MANY_ROWS;
+  if (!a->kv || !a->positions || !a->row_req || !a->block_table || !a->kv_cache)
+    return MONO_ERR_INVALID_ARG;
+  if (!a->q != !a->q_out || (a->q && !a->rope.table)) return MONO_ERR_INVALID_ARG;
+  RotateArgs k = {};
+  int64_t ks = a->kv_stride, qs = a->q_stride, os = a->q_out_stride;
+  TRY(check_rows(a->kv, s.kv_dim, &ks, TYPE_BYTES[a->dtype]));
+  if (a->q) {
+    const int64_t width = (int64_t)s.n_q_heads * s.head_dim;
+    TRY(check_rows(a->q, width, &qs, TYPE_BYTES[a->dtype]));
+    TRY(check_rows(a->q_out, width, &os, TYPE_BYTES[a->dtype]));
+    if (a->q == a->q_out && qs != os) return MONO_ERR_INVALID_ARG;  // in place means row for row
+  }
+  if (!aligned(a->positions, 4) || !aligned(a->rope_positions, 4) || !aligned(a->row_req, 4) ||
+      !aligned(a->block_table, 4))
+    return MONO_ERR_BAD_ALIGNMENT;
+  if (a->rope.table) TRY(check_rope(a->rope, s.head_dim, &k.rope));
+  TRY(check_view(s, a->kv_cache, a->kv_stride_block, a->kv_stride_tok, a->kv_num_blocks,
+                 a->max_blocks));
+  TRY(check_device(h));
+  k.rows = a->rows;
+  k.head_dim = s.head_dim;
+  k.positions = a->positions;
+  k.rope_positions = a->rope_positions;
+  k.x = a->q;
+  k.out = a->q_out;
+  k.x_stride = qs;
+  k.out_stride = os;
+  k.heads = s.n_q_heads;
+  k.kv = a->kv;
+  k.kv_stride = ks;
+  k.kv_dim = s.kv_dim;
+  k.n_req = a->n_req;
+  k.row_req = a->row_req;
+  k.cache = {a->kv_cache, a->kv_stride_block, a->kv_stride_tok, a->kv_num_blocks,
+             a->block_table, a->max_blocks, s.block_size};
+  k.status = h->status;
+  return cuda_code(launch_rotate(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k, a->dtype));
+}
+
+int mono_cache_rotate(mono_cache_t* h, const mono_rotate_args* a, void* stream) {
+  if (!h || !a) return MONO_ERR_INVALID_ARG;
+  const mono_cache_spec& s = h->spec;
+  if (a->rows < 1 || a->heads < 1 || !check_dtype(a->dtype)) return MONO_ERR_INVALID_ARG;
+  if (a->rows > MAX_ROTATED) return MONO_ERR_TOO_MANY_ROWS;
+  if (a->heads > (1 << 20)) return MONO_ERR_UNSUPPORTED_DIMS;
+  if (!a->x || !a->out || !a->positions) return MONO_ERR_INVALID_ARG;
+  RotateArgs k = {};
+  int64_t xs = a->x_stride, os = a->out_stride;
+  const int64_t width = (int64_t)a->heads * s.head_dim;
+  TRY(check_rows(a->x, width, &xs, TYPE_BYTES[a->dtype]));
+  TRY(check_rows(a->out, width, &os, TYPE_BYTES[a->dtype]));
+  if (a->x == a->out && xs != os) return MONO_ERR_INVALID_ARG;
+  if (!aligned(a->positions, 4)) return MONO_ERR_BAD_ALIGNMENT;
+  TRY(check_rope(a->rope, s.head_dim, &k.rope));
+  TRY(check_device(h));
+  k.rows = a->rows;
+  k.head_dim = s.head_dim;
+  k.positions = a->positions;
+  k.x = a->x;
+  k.out = a->out;
+  k.x_stride = xs;
+  k.out_stride = os;
+  k.heads = a->heads;
+  k.status = h->status;
+  return cuda_code(launch_rotate(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k, a->dtype));
 }
 
 int mono_verify_drafts(const mono_verify_args* a, void* stream) {
