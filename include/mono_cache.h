@@ -1,7 +1,7 @@
 /*
  * mono_cache.h -- C ABI of the operators around the decode layer's paged KV cache, for one
  * GB300 (sm_103a): attention of a step's rows over their requests' whole cached context (or a
- * sliding window with first tokens that stay visible), eviction of the tokens that gathered
+ * sliding window with first tokens that stay visible, or prefixes that requests share), eviction of the tokens that gathered
  * the least attention weight, appending rows' latents with their rotary positions, and verification
  * of drafted tokens.  They serve the layers
  * whose attention runs outside mono_layer_step (mono_ffn_step takes its output) and the
@@ -97,6 +97,46 @@ typedef struct {
 } mono_attend_args;
 
 int mono_cache_attend(mono_cache_t *h, const mono_attend_args *args, void *stream);
+
+/*
+ * Attention of requests that share prefixes.  As mono_cache_attend without a window, but the first
+ * P = prefix_lengths[prefix_of[b]] tokens of request b are those of a prefix, at prefix_table's row
+ * prefix_of[b], and read once for all rows of all its requests; its own tokens, t >= P, are at
+ * block_table[b][t / block_size] as ever (entries that lie in the prefix alone are not read), so that
+ * both tables may be those of whole contexts.  prefix_of[b] = -1: no prefix; prefix_of NULL: prefix 0 for
+ * all.  Row r at position p sees t <= hi, hi as there; a row inside its prefix sees that much of it.
+ *
+ * Sums, refused and masked tokens, status bits, pad rows, lse and the handle's workspace are as in
+ * mono_cache_attend; o is rounded to bf16 once, w[t] scale_t to 11 bits (and to 2^-31 of the largest of a
+ * row's tile of 128 tokens that set its reference) before that, q's elements to 2^-24 of a head's
+ * largest.  A NaN code of a token in view makes NaN the heads of its slice.  Scores of heads whose
+ * largest is beyond 2^26 in size are NaN.  Rows of requests whose prefix_of is outside [-1, n_prefix) are
+ * left out, o = 0, and raise MONO_STATUS_UNMAPPED_PAGE.  A negative length counts as 0.
+ *
+ * Limits: n_prefix 1..128; 2 * rows * (kv_dim / head_dim) times the tiles of the longer table, and 5 more,
+ * below 2^31; both tables' max_blocks * block_size at most 2^31 - 2^16.
+ */
+typedef struct {
+  const void *q;              /* bf16 [rows, n_q_heads * head_dim], 16-byte aligned */
+  void *o;                    /* bf16 [rows, n_q_heads * head_dim], not overlapping q */
+  int64_t q_stride, o_stride; /* elements between rows, multiples of 8; 0: rows packed */
+  const int32_t *positions;   /* [rows], < 0 for a pad row */
+  const int32_t *row_req;     /* [rows] request of each row, in any order */
+  const int32_t *block_table; /* [n_req, max_blocks] */
+  const int32_t *prefix_table; /* [n_prefix, prefix_max_blocks], pages of the same cache */
+  const int32_t *prefix_lengths; /* [n_prefix] tokens */
+  const int32_t *prefix_of;   /* optional [n_req] */
+  int32_t max_blocks, n_req;
+  int32_t prefix_max_blocks, n_prefix;
+  int32_t rows;               /* 1 <= rows <= max_rows */
+  int32_t causal;
+  float scale;                /* 0: 1/sqrt(head_dim) */
+  const uint8_t *kv_cache;
+  int64_t kv_stride_block, kv_stride_tok, kv_num_blocks;
+  float *lse;                 /* optional [rows, n_q_heads] */
+} mono_shared_args;
+
+int mono_cache_attend_shared(mono_cache_t *h, const mono_shared_args *args, void *stream);
 
 /*
  * Eviction.  Request b holds lengths[b] tokens in slots 0, 1, ... of its pages.  If that is

@@ -31,6 +31,17 @@ class AttendArgs(C.Structure):
                 ("weights_stride", C.c_int64), ("weights_cols", C.c_int64)]
 
 
+class SharedArgs(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("o", C.c_void_p), ("q_stride", C.c_int64),
+                ("o_stride", C.c_int64), ("positions", C.c_void_p), ("row_req", C.c_void_p),
+                ("block_table", C.c_void_p), ("prefix_table", C.c_void_p),
+                ("prefix_lengths", C.c_void_p), ("prefix_of", C.c_void_p),
+                ("max_blocks", C.c_int32), ("n_req", C.c_int32), ("prefix_max_blocks", C.c_int32),
+                ("n_prefix", C.c_int32), ("rows", C.c_int32), ("causal", C.c_int32),
+                ("scale", C.c_float), ("kv_cache", C.c_void_p), ("kv_stride_block", C.c_int64),
+                ("kv_stride_tok", C.c_int64), ("kv_num_blocks", C.c_int64), ("lse", C.c_void_p)]
+
+
 class EvictArgs(C.Structure):
     _fields_ = [("weights", C.c_void_p), ("weights_out", C.c_void_p),
                 ("weights_stride", C.c_int64), ("weights_out_stride", C.c_int64),
@@ -78,13 +89,14 @@ class VerifyArgs(C.Structure):
 
 # The same structures packed at once: setting ctypes fields one by one took most of a call.
 _ATTEND = struct.Struct("@PPqqPPPiiiiiifPqqqPPqq")
+_SHARED = struct.Struct("@PPqqPPPPPPiiiiiifPqqqP")
 _EVICT = struct.Struct("@PPqqPPPqiiiiPiPqqqPiPqqqqq")
 _APPEND = struct.Struct("@PPPqqqPPPPPqqqPqqiiiiiiii")
 _ROTATE = struct.Struct("@PPqqPPqqiiiiiii4x")
 _VERIFY = struct.Struct("@PPqqiiiiPPPPPPP")
 
 CACHE_EXPORTS = ["mono_cache_build", "mono_cache_free", "mono_cache_status", "mono_cache_attend",
-                 "mono_cache_evict", "mono_cache_append", "mono_cache_rotate", "mono_verify_drafts"]
+                 "mono_cache_attend_shared", "mono_cache_evict", "mono_cache_append", "mono_cache_rotate", "mono_verify_drafts"]
 
 
 def _lib() -> C.CDLL:
@@ -95,6 +107,7 @@ def _lib() -> C.CDLL:
         L.mono_cache_free.restype = None
         L.mono_cache_status.argtypes = [C.c_void_p, C.c_int]
         L.mono_cache_attend.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
+        L.mono_cache_attend_shared.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
         L.mono_cache_evict.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
         L.mono_cache_append.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
         L.mono_cache_rotate.argtypes = [C.c_void_p, C.c_void_p, C.c_void_p]
@@ -245,6 +258,38 @@ class Cache:
                      window, sinks, 1 if causal else 0, scale,
                      *self._view(kv_cache, "kv_cache"), lp, wp, ws, wc)
         self._call("mono_cache_attend", args, stream)
+
+    def attend_shared(self, q, o, positions, row_req, block_table, kv_cache, prefix_table,
+                      prefix_lengths, *, prefix_of=None, causal=True, scale=None, lse=None,
+                      stream=None) -> None:
+        """Attention as ``attend``, where the first prefix_lengths[g] tokens (int32 [prefixes]) of a
+        request b with prefix_of[b] = g (int32 [n_req]; -1: none; None: 0 for all) are those of
+        row g of ``prefix_table`` (int32 [prefixes, blocks]), read once for all its requests;
+        tokens behind them are in ``block_table``, indexed by their place in the whole context."""
+        dev, i32 = self._dev, torch.int32
+        rows, (n_req, max_blocks) = q.shape[0], block_table.shape
+        n_prefix, prefix_blocks = prefix_table.shape
+        if scale is None:
+            scale = 0.0
+        elif not _LEAST <= scale <= _MOST:
+            raise ValueError("scale must be positive, and an f32")
+        qp, qs = _mat(q, "q", _BF16, rows, self._width, dev)
+        op, os = _mat(o, "o", _BF16, rows, self._width, dev)
+        heads = self.spec["n_q_heads"]
+        lp = 0
+        if lse is not None:
+            lp, ls = _mat(lse, "lse", _F32, rows, heads, dev)
+            if ls != heads:
+                _bad(lse, "lse", _F32, (rows, heads), dev, True)
+        args = _pack(_SHARED, qp, op, qs, os, _vec(positions, "positions", i32, rows, dev),
+                     _vec(row_req, "row_req", i32, rows, dev),
+                     _table(block_table, "block_table", None, dev),
+                     _table(prefix_table, "prefix_table", None, dev),
+                     _vec(prefix_lengths, "prefix_lengths", i32, n_prefix, dev),
+                     0 if prefix_of is None else _vec(prefix_of, "prefix_of", i32, n_req, dev),
+                     max_blocks, n_req, prefix_blocks, n_prefix, rows, 1 if causal else 0, scale,
+                     *self._view(kv_cache, "kv_cache"), lp)
+        self._call("mono_cache_attend_shared", args, stream)
 
     def evict(self, weights, lengths, block_table, kv_cache, kept, new_lengths, *, budget,
               sinks=0, recent=0, weights_out=None, dst_table=None, dst_cache=None,

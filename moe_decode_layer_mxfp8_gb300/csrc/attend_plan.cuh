@@ -273,6 +273,8 @@ cudaError_t launch_join(const Launch&, const AttendArgs&, const Shape&, const Pi
 // The records' codes and the 16 bytes behind them as tensor maps with boxes of whole runs of a page, 8
 // rows (a swizzle atom) or more, that tiles are made of: the box's tokens; 0 where they cannot be maps.
 int encode_cache_maps(CUtensorMap* codes, CUtensorMap* scales, const AttendArgs& a);
+// The same with boxes of one latent slice, as they lie.
+int encode_shared_maps(CUtensorMap* codes, CUtensorMap* scales, const SharedArgs& a);
 
 }  // namespace attend
 

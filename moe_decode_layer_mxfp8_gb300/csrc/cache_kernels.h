@@ -95,10 +95,31 @@ struct RotateArgs {
   unsigned kv_blocks;  // (the launch's)
 };
 
+struct SharedArgs {
+  const __nv_bfloat16* q;
+  __nv_bfloat16* o;
+  long long q_stride, o_stride;
+  const int *positions, *row_req;
+  PagedView kv;   // the requests' own tokens
+  PagedView pre;  // the prefixes' (the same cache)
+  const int *prefix_lengths, *prefix_of;
+  int rows, n_req, n_prefix;
+  int n_q, head_dim, kv_dim;
+  int causal;
+  float scale;
+  float* lse;
+  int* status;
+};
+
 size_t attend_workspace_bytes(int max_rows, int sms);
 cudaError_t attend_prepare();  // raises the dynamic shared-memory limit
 cudaError_t launch_attend(const Launch&, const AttendArgs&, uint8_t* workspace, int max_rows,
                           int sms);
+constexpr int MAX_PREFIX = 128;  // prefixes of a call
+size_t shared_workspace_bytes(int max_rows, int n_q, int head_dim, int sms);
+bool shared_fits(int rows, int slices, long long tokens);  // the work is counted in 32 bits
+cudaError_t shared_prepare();
+cudaError_t launch_attend_shared(const Launch&, const SharedArgs&, uint8_t* workspace, int max_rows, int sms);
 constexpr int EVICT_MAX_CHUNKS = 1 << 18;  // moves of 64 kept tokens that a call may have
 size_t evict_workspace_bytes(int max_req);
 bool evict_fits(int n_req, int budget, long long cap);

@@ -16,6 +16,7 @@ struct mono_cache {
   float* lse = nullptr;
   uint8_t* attend_ws = nullptr;
   uint8_t* evict_ws = nullptr;
+  uint8_t* shared_ws = nullptr;
   int sms = 0;
   int* status = nullptr;
 };
@@ -121,12 +122,16 @@ int mono_cache_build(const mono_cache_spec* spec, mono_cache_t** out) {
   const size_t lse = ((size_t)spec->max_rows * spec->n_q_heads * 4 + 255) / 256 * 256;
   const size_t part = attend_workspace_bytes(spec->max_rows, prop.multiProcessorCount);
   const size_t ev = (evict_workspace_bytes(spec->max_req) + 255) / 256 * 256;
-  const size_t bytes = 256 + lse + ev + part;
+  const size_t shared = shared_workspace_bytes(spec->max_rows, spec->n_q_heads, spec->head_dim,
+                                               prop.multiProcessorCount);
+  const size_t part_end = (part + 255) / 256 * 256;
+  const size_t bytes = 256 + lse + ev + part_end + shared;
   cudaError_t e = cudaMalloc(&h->arena, bytes);
   if (e == cudaSuccess) e = cudaMemset(h->arena, 0, bytes);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = attend_prepare();
   if (e == cudaSuccess) e = evict_prepare();
+  if (e == cudaSuccess) e = shared_prepare();
   if (e != cudaSuccess) {
     mono_cache_free(h);
     return cuda_code(e);
@@ -135,6 +140,7 @@ int mono_cache_build(const mono_cache_spec* spec, mono_cache_t** out) {
   h->lse = reinterpret_cast<float*>(h->arena + 256);
   h->evict_ws = h->arena + 256 + lse;
   h->attend_ws = h->evict_ws + ev;
+  h->shared_ws = h->attend_ws + part_end;
   h->sms = prop.multiProcessorCount;
   *out = h;
   return MONO_OK;
@@ -208,6 +214,60 @@ int mono_cache_attend(mono_cache_t* h, const mono_attend_args* a, void* stream) 
   k.status = h->status;
   return cuda_code(launch_attend(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k,
                                  h->attend_ws, s.max_rows, h->sms));
+}
+
+int mono_cache_attend_shared(mono_cache_t* h, const mono_shared_args* a, void* stream) {
+  if (!h || !a) return MONO_ERR_INVALID_ARG;
+  const mono_cache_spec& s = h->spec;
+  if (a->rows < 1 || a->n_req < 1 || a->n_prefix < 1) return MONO_ERR_INVALID_ARG;
+  if (a->rows > s.max_rows || a->n_req > s.max_req || a->n_prefix > MAX_PREFIX)
+    return MONO_ERR_TOO_MANY_ROWS;
+  if (!a->q || !a->o || !a->positions || !a->row_req || !a->block_table || !a->prefix_table ||
+      !a->prefix_lengths || !a->kv_cache)
+    return MONO_ERR_INVALID_ARG;
+  if (!std::isfinite(a->scale) || a->scale < 0.0f) return MONO_ERR_INVALID_ARG;
+  const int64_t width = (int64_t)s.n_q_heads * s.head_dim;
+  int64_t qs = a->q_stride, os = a->o_stride;
+  TRY(check_rows(a->q, width, &qs, 2));
+  TRY(check_rows(a->o, width, &os, 2));
+  if (!aligned(a->positions, 4) || !aligned(a->row_req, 4) || !aligned(a->block_table, 4) ||
+      !aligned(a->prefix_table, 4) || !aligned(a->prefix_lengths, 4) || !aligned(a->prefix_of, 4) ||
+      !aligned(a->lse, 4))
+    return MONO_ERR_BAD_ALIGNMENT;
+  TRY(check_view(s, a->kv_cache, a->kv_stride_block, a->kv_stride_tok, a->kv_num_blocks,
+                 a->max_blocks));
+  TRY(check_view(s, a->kv_cache, a->kv_stride_block, a->kv_stride_tok, a->kv_num_blocks,
+                 a->prefix_max_blocks));
+  if (!shared_fits(a->rows, s.kv_dim / s.head_dim,
+                   (int64_t)std::max(a->max_blocks, a->prefix_max_blocks) * s.block_size))
+    return MONO_ERR_INVALID_ARG;
+  TRY(check_device(h));
+  SharedArgs k = {};
+  k.q = static_cast<const __nv_bfloat16*>(a->q);
+  k.o = static_cast<__nv_bfloat16*>(a->o);
+  k.q_stride = qs;
+  k.o_stride = os;
+  k.positions = a->positions;
+  k.row_req = a->row_req;
+  k.kv = {a->kv_cache, a->kv_stride_block, a->kv_stride_tok, a->kv_num_blocks,
+          a->block_table, a->max_blocks, s.block_size};
+  k.pre = k.kv;
+  k.pre.table = a->prefix_table;
+  k.pre.max_blocks = a->prefix_max_blocks;
+  k.prefix_lengths = a->prefix_lengths;
+  k.prefix_of = a->prefix_of;
+  k.rows = a->rows;
+  k.n_req = a->n_req;
+  k.n_prefix = a->n_prefix;
+  k.n_q = s.n_q_heads;
+  k.head_dim = s.head_dim;
+  k.kv_dim = s.kv_dim;
+  k.causal = a->causal != 0;
+  k.scale = a->scale > 0.0f ? a->scale : 1.0f / sqrtf((float)s.head_dim);
+  k.lse = a->lse;
+  k.status = h->status;
+  return cuda_code(launch_attend_shared(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k,
+                                        h->shared_ws, s.max_rows, h->sms));
 }
 
 int mono_cache_evict(mono_cache_t* h, const mono_evict_args* a, void* stream) {

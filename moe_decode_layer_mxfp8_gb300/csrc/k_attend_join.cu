@@ -80,9 +80,9 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) attend_join_kernel(const Atte
 
 }  // namespace
 
-// The records as a 3D byte tensor [pages][tokens][width], boxes of run (128: swizzled, bytes beyond
-// width read as 0) x box tokens; false where its strides are beyond a tensor map's.
-static bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int width, int run, int box) {
+// The records as a 3D byte tensor [pages][tokens][width], boxes of run (bytes beyond width read as 0) x
+// box tokens; false where its strides are beyond a tensor map's.
+static bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int width, int run, int box, bool swizzle) {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -101,19 +101,28 @@ static bool encode_cache_map(CUtensorMap* m, const PagedView& kv, int width, int
   const cuuint32_t boxes[3] = {(cuuint32_t)run, (cuuint32_t)box, 1}, ones[3] = {1, 1, 1};
   return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(kv.base), dims, strides,
                 boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                run == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int encode_cache_maps(CUtensorMap* codes, CUtensorMap* scales, const AttendArgs& a) {
-  const int bs = a.kv.block_size;
+static int encode_maps(CUtensorMap* codes, CUtensorMap* scales, const PagedView& kv, int kv_dim, int run,
+                       bool swizzle) {
+  const int bs = kv.block_size;
   if (bs % 8) return 0;
   const int box = std::min(bs & -bs, 128);
-  return encode_cache_map(codes, a.kv, a.kv_dim, 128, box) &&
-                 encode_cache_map(scales, a.kv, a.kv_dim + 16, 16, box)
+  return encode_cache_map(codes, kv, kv_dim, run, box, swizzle) &&
+                 encode_cache_map(scales, kv, kv_dim + 16, 16, box, false)
              ? box
              : 0;
+}
+
+int encode_cache_maps(CUtensorMap* codes, CUtensorMap* scales, const AttendArgs& a) {
+  return encode_maps(codes, scales, a.kv, a.kv_dim, 128, true);
+}
+
+int encode_shared_maps(CUtensorMap* codes, CUtensorMap* scales, const SharedArgs& a) {
+  return encode_maps(codes, scales, a.kv, a.kv_dim, a.head_dim, false);
 }
 
 cudaError_t launch_join(const Launch& L, const AttendArgs& a, const Shape& sh, const Pieces& ws) {
