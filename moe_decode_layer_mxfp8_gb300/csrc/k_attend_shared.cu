@@ -14,14 +14,14 @@
 //
 // Work: groups (a prefix with its requests' rows; a request's own tokens with its rows), slices and
 // pairs of blocks make items; the tiles of all items lie in one line, cut evenly over the CTAs, every
-// CTA deriving the cut for itself.  A CTA has two streams of softmax: those of the two blocks of a pair
-// over the same tiles, or of one block over every other tile.  What a CTA has of an item leaves (O, m, l)
+// CTA deriving the cut for itself.  A CTA has two streams of softmax: those of two blocks over the same
+// tiles, of two slices of one block, or (where a slice is left alone) of every other tile.  What a CTA has of an item leaves (O, m, l)
 // in the workspace; a second kernel joins them.
 //
-// Roles: warps 0-3 and 4-7 softmax, a query per thread; 8-11 widen tiles; 12 issues MMAs; 13 loads; 14
-// makes the items' rows; 15 tells the join where pieces are.
-// Every mbarrier wait is bounded; a wait that runs out is reported, and from then on every role runs its
-// loop without waiting, copying or issuing.
+// Roles: warps 0-3 and 4-7 softmax, a query per thread; 8-15 widen tiles; 16 and 17 issue a stream's MMAs
+// each; 18 loads; 19 makes the items and their rows, and tells the join where pieces are.
+// Every wait is for an mbarrier, and bounded; one that runs out is reported and ends its role, and with it
+// the others' waits.  Copies and products on their way are waited for before the CTA ends.
 #include "attend_tc.cuh"
 
 namespace mono {
@@ -30,16 +30,18 @@ namespace {
 using namespace tc;
 using namespace attend;
 
-constexpr int THREADS = 512, SOFT = 256;
-constexpr int WIDEN_WARP = 8, MMA_WARP = 12, LOAD_WARP = 13, ROWS_WARP = 14;
+constexpr int WIDEN_WARPS = 8, WIDEN_TOKENS = TT / WIDEN_WARPS;
+constexpr int WIDEN_WARP = 8, MMA_WARP = WIDEN_WARP + WIDEN_WARPS, LOAD_WARP = MMA_WARP + 2, ROWS_WARP = LOAD_WARP + 1;
+constexpr int THREADS = 32 * (ROWS_WARP + 1), SOFT = 32 * WIDEN_WARP;
 constexpr int MAX_GROUPS = MAX_PREFIX + MAX_REQ;
 constexpr int BLOCK = 128;       // queries
 constexpr int EXTRA = 3;         // what an item costs a CTA beside its steps, in steps
 constexpr int HALF = TT * 128;   // bytes of 64 dimensions of a tile, or a block, in f16
+constexpr int JOBS = 4;          // items whose rows are made ahead
 constexpr float BASE = 6.0f, LEAST = -90.0f;  // log2 of the weights times scales that m puts at most; scales below
 constexpr uint32_t TOO_LARGE = 0x7800;        // f16 of 2^15
 // registers a thread at launch, and as the roles divide them
-constexpr int REGS = 128, SOFT_REGS = 192, OTHER_REGS = 64;
+constexpr int REGS = 96, SOFT_REGS = 144, OTHER_REGS = 64;
 static_assert(SOFT_REGS * SOFT + OTHER_REGS * (THREADS - SOFT) == REGS * THREADS, "register split");
 
 template <int DH>
@@ -50,9 +52,11 @@ struct Form {
   static constexpr int SC_OFF = K_OFF + ST * NARROW;      // the 16 bytes behind the codes [ST][TT]
   static constexpr int TOK_OFF = SC_OFF + ST * TT * 16;   // a_t, scale_t, log2 scale_t [NS][3][TT]
   static constexpr int PLAN_OFF = TOK_OFF + NS * 3 * TT * 4;
-  static constexpr int PLAN_BYTES = MAX_GROUPS * (4 + 4 + 4 + 2) + 16 + MAX_ROWS * 6 + MAX_REQ * 2;
+  static constexpr int PLAN_BYTES = (MAX_GROUPS + 4) * 4 + MAX_GROUPS * (4 + 4 + 2) + MAX_PREFIX * 4 + MAX_ROWS * 6 +
+                                    MAX_REQ * 2;
   static constexpr int SMEM_BYTES = PLAN_OFF + PLAN_BYTES + 1024;
   static constexpr int O_COL = 256;  // TMEM: scores (and weights) of stream u at 128 u, its O at O_COL + DH u
+  static constexpr int PART_LD = DH + 8;  // a piece: m, l, six words of padding, O
 };
 
 struct Args {
@@ -72,82 +76,93 @@ struct Plan {
   int* end;    // [groups] one behind the last token that a row sees
   int* first;  // [groups] the first
   short* cnt;  // [groups] rows
+  int* len;    // [n_prefix] tokens
   int* hi;     // [rows] a row's last token
   short* req;  // [rows] its request; -1: nothing to see
   short* pfx;  // [n_req] its prefix; -1: none, -2: bad
 };
 
-struct Item {  // of a group: a slice, and a pair of blocks (or the last one)
-  int g, slice, pair;
+// A group's items.  First those of two blocks: for every slice the pairs of blocks.  Then those of an odd
+// last block: of two slices each, and if a slice is left, one whose streams take every other tile.
+enum { TWO_BLOCKS, TWO_SLICES, TWO_TILES };
+struct Items {
+  int tiles, blocks, len, half;  // lengths in the line of an item, and of one of TWO_TILES
+  __device__ Items(const Args& ar, int tiles, int rows)
+      : tiles(tiles), blocks((rows + ar.rows_per - 1) / ar.rows_per), len(EXTRA + tiles), half(EXTRA + (tiles + 1) / 2) {}
+  __device__ int of_pairs(const Args& ar) const { return ar.slices * (blocks >> 1); }
+  __device__ int whole(const Args& ar) const { return of_pairs(ar) + (blocks & 1) * (ar.slices >> 1); }
+  __device__ int units(const Args& ar) const { return tiles ? whole(ar) * len + (blocks & ar.slices & 1) * half : 0; }
+  __device__ int count(const Args& ar) const { return whole(ar) + (blocks & ar.slices & 1); }
 };
-struct Shape2 {  // of a group's items
-  int tiles, blocks, whole, half;  // a pair's and a single block's lengths in the line
-  __device__ int slice_len() const { return (blocks >> 1) * whole + (blocks & 1) * half; }
-  __device__ bool pairs(int pair) const { return 2 * pair + 1 < blocks; }
-  __device__ int len(int pair) const { return pairs(pair) ? whole : half; }
-};
-__device__ __forceinline__ Shape2 shape_of_group(const Args& ar, const Plan& p, int g) {
-  Shape2 s = {0, 0, 0, 0};
+__device__ __forceinline__ Items items_of(const Args& ar, const Plan& p, int g) {
   const int n = p.cnt[g], lo = p.first[g], end = p.end[g];
-  if (n == 0 || end <= lo) return s;
-  s.tiles = ((end - 1) >> 7) - (lo >> 7) + 1;
-  s.blocks = (n + ar.rows_per - 1) / ar.rows_per;
-  s.whole = EXTRA + s.tiles;
-  s.half = EXTRA + (s.tiles + 1) / 2;
-  return s;
+  return Items(ar, n == 0 || end <= lo ? 0 : ((end - 1) >> 7) - (lo >> 7) + 1, n);
 }
 
-// A CTA's part of an item: steps [s0, s1), of one tile for both streams or of two.
+// A CTA's part of an item: the steps from s0 on, of a tile for each stream.
 struct Job {
-  Item at;
-  bool pairs;
-  int tile0, tiles, s0, n[2];  // the group's first tile and number; first step; the streams' tiles
-  __device__ int count() const { return pairs ? n[0] : n[0] + n[1]; }
-  // the i-th tile of the ring, and which it is for stream u's j-th
-  __device__ int token(int i) const { return (tile0 + (pairs ? s0 + i : 2 * s0 + i)) * TT; }
-  __device__ int ring(int u, int j) const { return pairs ? j : 2 * j + u; }
+  int g, mode, slice, block;  // of stream 0 (the other one: the next slice, or the next block)
+  int tile, n[2];             // stream 0's first tile; the streams' tiles
+  bool begins;                // the item's first step is here
+  int least;                  // the smallest of its rows' last tokens
+  alignas(16) short row[2 * BLOCK];  // its rows (-1: none), its blocks' one after another
+  // tiles of the ring, and stream u's j-th among them
+  __device__ int count() const { return mode == TWO_BLOCKS ? n[0] : n[0] + n[1]; }
+  __device__ int ring(int u, int j) const { return mode == TWO_BLOCKS ? j : 2 * j + u; }
+  // the ring's i-th
+  __device__ int token(int i) const { return (tile + (mode == TWO_SLICES ? i >> 1 : i)) * TT; }
+  __device__ int slice_of(int u) const { return slice + (mode == TWO_SLICES ? u : 0); }
 };
 struct Cursor {
-  Item at;
-  int unit, left;
+  int g, item, unit, left;
 };
+// The CTA's next part of an item, into job but for its rows.
 __device__ __forceinline__ bool next_job(const Args& ar, const Plan& p, Cursor& c, Job& job) {
   const int groups = ar.a.n_prefix + ar.a.n_req;
 #pragma unroll 1
   while (c.left > 0) {
-    const Shape2 s = shape_of_group(ar, p, c.at.g);
-    const int len = s.len(c.at.pair), n = min(len - c.unit, c.left);
-    job.at = c.at;
-    job.pairs = s.pairs(c.at.pair);
-    job.tile0 = p.first[c.at.g] >> 7;
-    job.tiles = s.tiles;
-    job.s0 = max(0, c.unit - EXTRA);
-    const int s1 = c.unit + n - EXTRA;
-    job.n[0] = s1 - job.s0;
-    job.n[1] = job.pairs ? job.n[0] : min(2 * s1, s.tiles) - 2 * job.s0 - job.n[0];
+    const Items it = items_of(ar, p, c.g);
+    const int of_pairs = it.of_pairs(ar), whole = it.whole(ar);
+    const int len = c.item < whole ? it.len : it.half, n = min(len - c.unit, c.left);
+    const int s0 = max(0, c.unit - EXTRA), s1 = c.unit + n - EXTRA;
+    job.g = c.g;
+    job.n[0] = job.n[1] = s1 - s0;
+    job.begins = s0 == 0;
+    job.tile = (p.first[c.g] >> 7) + s0;
+    if (c.item < of_pairs) {
+      const int pairs = it.blocks >> 1;
+      job.mode = TWO_BLOCKS;
+      job.slice = c.item / pairs;
+      job.block = 2 * (c.item - job.slice * pairs);
+    } else {
+      job.block = it.blocks - 1;
+      job.mode = c.item < whole ? TWO_SLICES : TWO_TILES;
+      job.slice = 2 * (c.item - of_pairs);  // (the last slice where it is alone)
+      if (job.mode == TWO_TILES) {
+        job.tile += s0;
+        job.n[1] = min(2 * s1, it.tiles) - 2 * s0 - job.n[0];
+      }
+    }
     c.left -= n;
     c.unit = 0;
-    if (++c.at.pair >= (s.blocks + 1) >> 1) {
-      c.at.pair = 0;
-      if (++c.at.slice >= ar.slices) {
-        c.at.slice = 0;
-        do ++c.at.g;
-        while (c.at.g < groups && p.pre[c.at.g + 1] <= p.pre[c.at.g]);
-      }
+    if (++c.item >= it.count(ar)) {
+      c.item = 0;
+      do ++c.g;
+      while (c.g < groups && p.pre[c.g + 1] <= p.pre[c.g]);
     }
     if (job.n[0] > 0) return true;
   }
+  job.n[0] = job.n[1] = 0;
   return false;
 }
 
 struct Shared {
   uint64_t full[4], k_free[4], v_full[5], v_free[5];
-  uint64_t s_full[2], p_full[2], o_full[2], q_full[2], m_full[2], m_free[2], drain;
+  uint64_t s_full[2], p_full[2], o_full[2], q_full[2], merge, j_full[JOBS], j_free[JOBS], drain;
   uint32_t valid[4][4];                // tokens that are there, of a narrow tile
   alignas(16) uint32_t see[5][4];      // and of a wide one
   int part[5];                         // not every row of the item sees all its tokens
-  short row[2][2 * BLOCK];             // an item's rows (-1: none), its blocks' one after another
-  int least[2];                        // the smallest of their last tokens
+  Job job[JOBS];
   float2 ml[2][BLOCK];
   uint32_t tmem;
   int abort;
@@ -175,15 +190,18 @@ __device__ __forceinline__ void loaded32(uint32_t (&r)[32]) {
                "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
                "+r"(r[31]));
 }
-__device__ __forceinline__ void st32(uint32_t taddr, const uint32_t* r) {
+__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+// 32 bytes at once
+__device__ __forceinline__ void st_global8(float* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 // f16 x f16, f32 accumulators; A in shared memory, or in TMEM
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -211,6 +229,23 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// A wait for an mbarrier phase by a whole warp, for a second at most, and not once another wait has run out.
+// False if it ran out.
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+    while (!(ok = mbar_try_wait(bar, parity)) && !*abort) {
+      if (globaltimer_ns() - t0 > 1000000000ull) {
+        atomicOr(status, ST_WAIT_TIMEOUT);
+        *abort = 1;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
 // Fills the plan (every thread of the block) and finds the CTA's first item; the results are behind the
 // caller's next barrier.  Waits for the kernels before.
 __device__ __forceinline__ void derive_plan(const Args& ar, const Plan& plan, Cursor* start) {
@@ -222,41 +257,47 @@ __device__ __forceinline__ void derive_plan(const Args& ar, const Plan& plan, Cu
   for (int g = tid; g < groups; g += THREADS) plan.end[g] = 0, plan.cnt[g] = 0, plan.first[g] = 0;
   pdl_trigger();
   pdl_wait();
-#pragma unroll 1
-  for (int b = tid; b < a.n_req; b += THREADS) {
-    int g = a.prefix_of ? a.prefix_of[b] : 0;
+  constexpr int ROWS = (MAX_ROWS + THREADS - 1) / THREADS;
+  int p[ROWS], b[ROWS];
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    const int r = tid + k * THREADS;
+    p[k] = -1, b[k] = -1;
+    if (r < a.rows) p[k] = min(a.positions[r], 0x7FFFFFFE), b[k] = a.row_req[r];
+  }
+  static_assert(MAX_REQ <= THREADS && MAX_PREFIX <= THREADS, "a request a thread");
+  int g = -1;
+  if (tid < a.n_req) {
+    g = a.prefix_of ? a.prefix_of[tid] : 0;
     if (g < -1 || g >= np) g = -2;
-    plan.pfx[b] = (short)g;
+    plan.pfx[tid] = (short)g;
   }
+  if (tid < np) plan.len[tid] = max(0, a.prefix_lengths[tid]);
   __syncthreads();
-#pragma unroll 1
-  for (int b = tid; b < a.n_req; b += THREADS) {
-    const int g = plan.pfx[b];
-    plan.first[np + b] = g >= 0 ? max(0, a.prefix_lengths[g]) : 0;
-  }
+  if (g >= 0) plan.first[np + tid] = plan.len[g];
   // a request's rows and their largest position
-#pragma unroll 1
-  for (int r = tid; r < a.rows; r += THREADS) {
-    const int p = min(a.positions[r], 0x7FFFFFFE), b = a.row_req[r];
-    const bool in = b >= 0 && b < a.n_req, live = p >= 0 && in && plan.pfx[b] >= -1;
-    if (p >= 0 && !live && tell) atomicOr(a.status, ST_UNMAPPED_PAGE);
-    plan.req[r] = (short)(live ? b : -1);
-    plan.hi[r] = live ? p : -1;
-    if (live) atomicMax(&plan.end[np + b], p + 1);
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    const int r = tid + k * THREADS;
+    const bool live = p[k] >= 0 && b[k] >= 0 && b[k] < a.n_req && plan.pfx[b[k]] >= -1;
+    if (p[k] >= 0 && !live && tell) atomicOr(a.status, ST_UNMAPPED_PAGE);
+    if (!live) b[k] = -1;
+    if (r < a.rows) plan.req[r] = (short)b[k];
+    if (live) atomicMax(&plan.end[np + b[k]], p[k] + 1);
   }
   __syncthreads();
-#pragma unroll 1
-  for (int r = tid; r < a.rows; r += THREADS) {
-    const int b = plan.req[r];
-    if (b < 0) continue;
-    const int hi = a.causal ? plan.hi[r] : plan.end[np + b] - 1, g = plan.pfx[b], len = plan.first[np + b];
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    const int r = tid + k * THREADS;
+    if (b[k] < 0) continue;
+    const int hi = a.causal ? p[k] : plan.end[np + b[k]] - 1, of = plan.pfx[b[k]], len = plan.first[np + b[k]];
     plan.hi[r] = hi;
     // (16-bit counters: the words that hold them)
-    auto count = [&](int k) { atomicAdd(reinterpret_cast<int*>(plan.cnt) + (k >> 1), k & 1 ? 1 << 16 : 1); };
-    count(np + b);
-    if (g >= 0) {
-      count(g);
-      atomicMax(&plan.end[g], min(min(hi + 1, len), pcap));
+    auto count = [&](int i) { atomicAdd(reinterpret_cast<int*>(plan.cnt) + (i >> 1), i & 1 ? 1 << 16 : 1); };
+    count(np + b[k]);
+    if (of >= 0) {
+      count(of);
+      atomicMax(&plan.end[of], min(min(hi + 1, len), pcap));
       if (min(hi + 1, len) > pcap && tell) atomicOr(a.status, ST_UNMAPPED_PAGE);
     }
     if (hi >= cap && hi >= len && tell) atomicOr(a.status, ST_UNMAPPED_PAGE);
@@ -266,53 +307,49 @@ __device__ __forceinline__ void derive_plan(const Args& ar, const Plan& plan, Cu
     int W = 0;
 #pragma unroll 1
     for (int g0 = 0; g0 < groups; g0 += 32) {
-      const int g = g0 + lane;
+      const int i = g0 + lane;
       int u = 0;
-      if (g < groups) {
-        if (g >= np) plan.end[g] = min(plan.end[g], cap);
-        u = shape_of_group(ar, plan, g).slice_len() * ar.slices;
+      if (i < groups) {
+        if (i >= np) plan.end[i] = min(plan.end[i], cap);
+        u = items_of(ar, plan, i).units(ar);
       }
 #pragma unroll 1
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, u, o);
         if (lane >= o) u += y;
       }
-      if (g < groups) plan.pre[g + 1] = W + u;
+      if (i < groups) plan.pre[i + 1] = W + u;
       W += __shfl_sync(0xffffffffu, u, 31);
     }
     __syncwarp();
     if (lane == 0) {
       plan.pre[0] = 0;
       const Cut cut(W, gridDim.x);
-      Cursor c = {{0, 0, 0}, 0, cut.size(blockIdx.x)};
+      Cursor c = {0, 0, 0, cut.size(blockIdx.x)};
       if (c.left > 0) {
         const int w0 = cut.start(blockIdx.x);
-        int lo = 0, hi = groups;  // the last group that starts by w0 (and is not empty: the next starts later)
+        int hi = groups;  // the last group that starts by w0 (and is not empty: the next starts later)
 #pragma unroll 1
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (plan.pre[mid] <= w0) lo = mid; else hi = mid;
+        while (hi - c.g > 1) {
+          const int mid = (c.g + hi) >> 1;
+          if (plan.pre[mid] <= w0) c.g = mid; else hi = mid;
         }
-        const Shape2 s = shape_of_group(ar, plan, lo);
-        int u = w0 - (lo ? plan.pre[lo] : 0);
-        c.at.g = lo;
-        c.at.slice = u / s.slice_len();
-        u -= c.at.slice * s.slice_len();
-        c.at.pair = min(u / s.whole, s.blocks >> 1);
-        c.unit = u - c.at.pair * s.whole;
+        const Items it = items_of(ar, plan, c.g);
+        const int u = w0 - (c.g ? plan.pre[c.g] : 0);
+        c.item = min(u / it.len, it.whole(ar));
+        c.unit = u - c.item * it.len;
       }
       *start = c;
     }
   }
 }
 
-// The rows of an item's blocks into `rows`, in row order, by a whole warp; returns the smallest of their
-// last tokens.
-__device__ __forceinline__ int item_rows(const Args& ar, const Plan& plan, const Job& job, short* rows) {
-  const int lane = threadIdx.x & 31, np = ar.a.n_prefix, g = job.at.g;
-  const int first = 2 * job.at.pair * ar.rows_per, most = (job.pairs ? 2 : 1) * ar.rows_per;
-#pragma unroll 1
-  for (int i = lane; i < 2 * BLOCK; i += 32) rows[i] = -1;
+// The rows of an item's blocks, in row order, by a whole warp, and the smallest of their last tokens.
+__device__ __forceinline__ void item_rows(const Args& ar, const Plan& plan, Job& job) {
+  const int lane = threadIdx.x & 31, np = ar.a.n_prefix, g = job.g;
+  const int first = job.block * ar.rows_per, most = (job.mode == TWO_BLOCKS ? 2 : 1) * ar.rows_per;
+#pragma unroll
+  for (int i = 0; i < 2 * BLOCK / 8; i += 32) reinterpret_cast<uint4*>(job.row)[i + lane] = make_uint4(~0u, ~0u, ~0u, ~0u);
   __syncwarp();
   int seen = 0, least = 0x7FFFFFFF;
 #pragma unroll 1
@@ -322,12 +359,13 @@ __device__ __forceinline__ int item_rows(const Args& ar, const Plan& plan, const
     const uint32_t m = __ballot_sync(0xffffffffu, in);
     const int rank = seen + __popc(m & ((1u << lane) - 1)) - first;
     if (in && rank >= 0 && rank < most) {
-      rows[rank < ar.rows_per ? rank : BLOCK + rank - ar.rows_per] = (short)r;
+      job.row[rank < ar.rows_per ? rank : BLOCK + rank - ar.rows_per] = (short)r;
       least = min(least, plan.hi[r]);
     }
     seen += __popc(m);
   }
-  return __reduce_min_sync(0xffffffffu, least);
+  least = __reduce_min_sync(0xffffffffu, least);
+  if (lane == 0) job.least = least;
 }
 
 // Loads narrow tiles, a warp: TMA boxes through the page table, or cp.async where there are no maps.
@@ -342,7 +380,7 @@ struct Loader {
     boxes = TT >> shift;
   }
   __device__ __forceinline__ void locate(const Args& ar, const Plan& plan, const Job& job, int i) {
-    const int lane = threadIdx.x & 31, np = ar.a.n_prefix, g = job.at.g, bs = ar.a.kv.block_size;
+    const int lane = threadIdx.x & 31, np = ar.a.n_prefix, g = job.g, bs = ar.a.kv.block_size;
     const PagedView& v = g < np ? ar.a.pre : ar.a.kv;
     const int* table = v.table + (size_t)(g < np ? g : g - np) * v.max_blocks;
     t0 = job.token(i);
@@ -360,13 +398,13 @@ struct Loader {
     }
   }
   __device__ __forceinline__ void load(const Args& ar, int slice, uint8_t* st, uint8_t* sc, uint32_t* valid,
-                                       uint64_t* full, bool go) {
+                                       uint64_t* full) {
     const SharedArgs& a = ar.a;
     const int lane = threadIdx.x & 31;
     if (box > 1) {
       const bool m = page[0] >= 0 && page[0] < a.kv.num_blocks;
       if (row[0] >= 0 && !m) atomicOr(a.status, ST_UNMAPPED_PAGE);
-      if (m && go) {
+      if (m) {
         tma_load_3d(st + ((lane * DH) << shift), &ar.codes, DH * slice, row[0], page[0], full);
         tma_load_3d(sc + ((lane * 16) << shift), &ar.scales, a.kv_dim, row[0], page[0], full);
       }
@@ -379,7 +417,7 @@ struct Loader {
         if (lane == q) valid[q] = w;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(full, go ? __popc(have) * box * (DH + 16) : 0);
+      if (lane == 0) mbar_arrive_expect_tx(full, __popc(have) * box * (DH + 16));
       __syncwarp();
     } else {
       constexpr int PIECES = DH / 16, ROWS = 32 / PIECES;
@@ -396,10 +434,10 @@ struct Loader {
         for (int e = 0; e < 32 / ROWS; ++e) {
           const int k = ROWS * e + lane / PIECES, piece = lane & (PIECES - 1);
           const long long ro = __shfl_sync(0xffffffffu, off, k);
-          if (go && ((w >> k) & 1))
+          if ((w >> k) & 1)
             cp_async16(st + (32 * q + k) * DH + 16 * piece, a.kv.base + ro + DH * slice + 16 * piece, 16);
         }
-        if (go && m) cp_async16(sc + (32 * q + lane) * 16, a.kv.base + off + a.kv_dim, 16);
+        if (m) cp_async16(sc + (32 * q + lane) * 16, a.kv.base + off + a.kv_dim, 16);
       }
       cp_async_wait_all();
       __syncwarp();
@@ -408,107 +446,19 @@ struct Loader {
   }
 };
 
-// What a softmax thread knows of its item and query.
-struct Soft {
-  uint32_t s_at, o_at;  // TMEM: the stream's scores and O, with the warp's lane quadrant
-  int hi;               // the row's last token
-  float factor;         // of the scores
-  bool scaled;          // some of the warp's factors are not 1
-  float m, l;
-};
-
-// The largest weight times scale (log2) of the thread's query in a tile.
-template <bool PART>
-__device__ __forceinline__ float tile_max(const Soft& w, const float* tok, const uint32_t* see, int t0) {
-  float top = -INFINITY;
+// Columns of the warp's lanes times a factor each: f32 (O), or packed f16 (weights).
+template <bool HALVES>
+__device__ __forceinline__ void scale_columns(uint32_t at, int columns, float f) {
+  const uint32_t f2 = f16x2_of(f, f);
 #pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    uint32_t s[32];
-    tc_ld32(w.s_at + 32 * c, s);
-    uint32_t sees = 0xffffffffu;
-    if (PART) {
-      const int n = w.hi - (t0 + 32 * c) + 1;
-      sees = see[c] & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1);
-    }
+  for (int c = 0; c < columns; c += 8) {
+    float x[8];
+    tc_ld8(at + c, x);
     tc_wait_ld();
-    loaded32(s);
+    tc_loaded(x);
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      float x = fmaf(__uint_as_float(s[e]) * w.factor, tok[32 * c + e], tok[2 * TT + 32 * c + e]);
-      if (PART && !((sees >> e) & 1)) x = -INFINITY;
-      top = fmaxf(top, x);
-    }
-  }
-  return top;
-}
-
-// The tile's weights times scales as packed f16, their sum (without scales), and the largest pair.
-template <bool PART>
-__device__ __forceinline__ void tile_weights(const Soft& w, const float* tok, const uint32_t* see, int t0,
-                                             uint32_t (&p)[64], float& l0, float& l1, uint32_t& top) {
-  uint32_t s[2][32];
-  tc_ld32(w.s_at, s[0]);
-  l0 = l1 = 0.0f;
-  top = 0;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    tc_wait_ld();
-    loaded32(s[c & 1]);
-    if (c < 3) tc_ld32(w.s_at + 32 * (c + 1), s[(c + 1) & 1]);
-    float* x = reinterpret_cast<float*>(s[c & 1]);
-    if (w.scaled) {
-#pragma unroll
-      for (int e = 0; e < 32; e += 2) mul2(x[e], x[e + 1], w.factor);
-    }
-#pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-      const float4 a = *reinterpret_cast<const float4*>(tok + 32 * c + e);
-      fma2t(x[e], x[e + 1], a.x, a.y, -w.m);
-      fma2t(x[e + 2], x[e + 3], a.z, a.w, -w.m);
-    }
-    if (PART) {
-      const int n = w.hi - (t0 + 32 * c) + 1;
-      const uint32_t sees = see[c] & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1);
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (!((sees >> e) & 1)) x[e] = -INFINITY;
-    }
-#pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-      const float4 sc = *reinterpret_cast<const float4*>(tok + TT + 32 * c + e);
-      float p0 = ex2(x[e]), p1 = ex2(x[e + 1]), p2 = ex2(x[e + 2]), p3 = ex2(x[e + 3]);
-      add2(l0, l1, p0, p1);
-      add2(l0, l1, p2, p3);
-      mul2(p0, p1, sc.x, sc.y);
-      mul2(p2, p3, sc.z, sc.w);
-      p[16 * c + e / 2] = f16x2_of(p0, p1);
-      p[16 * c + e / 2 + 1] = f16x2_of(p2, p3);
-      top = max_u16x2(top, max_u16x2(p[16 * c + e / 2], p[16 * c + e / 2 + 1]));
-    }
-  }
-}
-
-// Moves the query's reference to the tile's weights, and what was summed under the old one with it.
-template <int DH, bool PART>
-__device__ __forceinline__ void move_reference(Soft& w, const float* tok, const uint32_t* see, int t0, bool first) {
-  const float top = tile_max<PART>(w, tok, see, t0);
-  float f = 1.0f;
-  if (top - w.m > BASE) {
-    const float now = fabsf(top) <= SCORE_MAX ? ceilf(top) - BASE : __int_as_float(0x7FC00000);
-    f = w.m == UNSET ? 0.0f : ex2(w.m - now);
-    w.m = now;
-  }
-  if (first) return;
-  w.l *= f;
-#pragma unroll 1
-  for (int c = 0; c < DH; c += 32) {
-    uint32_t o[32];
-    tc_ld32(w.o_at + c, o);
-    tc_wait_ld();
-    loaded32(o);
-#pragma unroll
-    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-    st32(w.o_at + c, o);
+    for (int e = 0; e < 8; ++e) x[e] = HALVES ? __uint_as_float(hmul2(__float_as_uint(x[e]), f2)) : x[e] * f;
+    tc_st8(at + c, x);
   }
   tc_wait_st();
 }
@@ -526,22 +476,27 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
   plan.pre = reinterpret_cast<int*>(sm + F::PLAN_OFF);
   plan.end = plan.pre + MAX_GROUPS + 4;
   plan.first = plan.end + MAX_GROUPS;
-  plan.hi = plan.first + MAX_GROUPS;
+  plan.len = plan.first + MAX_GROUPS;
+  plan.hi = plan.len + MAX_PREFIX;
   plan.cnt = reinterpret_cast<short*>(plan.hi + MAX_ROWS);
   plan.req = plan.cnt + MAX_GROUPS;
   plan.pfx = plan.req + MAX_ROWS;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int s = 0; s < ST; ++s) mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], 4);
-    for (int s = 0; s < NS; ++s) mbar_init(&ss.v_full[s], 4), mbar_init(&ss.v_free[s], 1);
+    for (int s = 0; s < ST; ++s) mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], WIDEN_WARPS);
+    for (int s = 0; s < NS; ++s) mbar_init(&ss.v_full[s], WIDEN_WARPS), mbar_init(&ss.v_free[s], 2);
     for (int u = 0; u < 2; ++u) {
       mbar_init(&ss.s_full[u], 2), mbar_init(&ss.p_full[u], 4), mbar_init(&ss.o_full[u], 1);
-      mbar_init(&ss.q_full[u], 4), mbar_init(&ss.m_full[u], 1), mbar_init(&ss.m_free[u], 12);
+      mbar_init(&ss.q_full[u], 4);
     }
-    mbar_init(&ss.drain, 1);
+    // an item is read by the softmax, widening, issuing and loading warps
+    for (int k = 0; k < JOBS; ++k) mbar_init(&ss.j_full[k], 1), mbar_init(&ss.j_free[k], SOFT / 32 + WIDEN_WARPS + 3);
+    mbar_init(&ss.merge, SOFT / 32);
+    mbar_init(&ss.drain, 2);
     ss.abort = 0;
     fence_mbar_init();
+    if (ar.box) prefetch_tmap(&ar.codes), prefetch_tmap(&ar.scales);
   }
   if (warp == MMA_WARP) tmem_alloc<512>(&ss.tmem);
   derive_plan(ar, plan, &ss.start);
@@ -549,370 +504,460 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ss.tmem;
-  Cursor cur = ss.start;
-  Job job;
+
+  // The next item (null: there is none, or a wait ran out), and that it is no longer needed; by whole warps.
+  int item = 0;
+  auto next_item = [&]() -> const Job* {
+    const Job* job = &ss.job[item % JOBS];
+    if (!await(&ss.j_full[item % JOBS], (item / JOBS) & 1, a.status, abort)) return nullptr;
+    return job->n[0] > 0 ? job : nullptr;
+  };
+  auto item_done = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ss.j_free[item % JOBS]);
+    ++item;
+  };
 
   if (warp >= WIDEN_WARP) {
     regs_down<OTHER_REGS>();
-    if (warp < MMA_WARP) {
-      // -------------------------------------------- tiles from e4m3 to f16, 32 tokens a warp
-      constexpr int PIECES = DH / 16, ROWS = 32 / PIECES;  // of 16 codes; rows at a time
-      const int q = warp - WIDEN_WARP, piece = lane & (PIECES - 1), r0 = lane / PIECES;
+    if (warp < MMA_WARP) [&] {
+      // ------------------------------------------------------------- tiles from e4m3 to f16
+      constexpr int PIECES = DH / 16, ROWS = 32 / PIECES, N = WIDEN_TOKENS / ROWS;  // of 16 codes; rows at a time
+      const int t0 = WIDEN_TOKENS * (warp - WIDEN_WARP), piece = lane & (PIECES - 1), r0 = lane / PIECES;
       const float to_log2 = a.scale * LOG2E;
+      const int odd = (piece >> 2) & 1;  // (such lanes store the other half first: no bank twice)
       int it = 0;
 #pragma unroll 1
-      for (int item = 0; next_job(ar, plan, cur, job); ++item) {
-        wait(&ss.m_full[item & 1], (item >> 1) & 1, a.status, abort);
-        const int least = ss.least[item & 1];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ss.m_free[item & 1]);
-        const int n = job.count();
+      while (const Job* job = next_item()) {
+        const int n = job->count(), least = job->least;
 #pragma unroll 1
         for (int i = 0; i < n; ++i, ++it) {
           const int st = it % ST, s = it % NS;
-          wait(&ss.full[st], (it / ST) & 1, a.status, abort);
-          if (it >= NS) wait(&ss.v_free[s], (it / NS - 1) & 1, a.status, abort);
-          const uint32_t ok = ss.valid[st][q];
-          const bool late = least < job.token(i) + TT - 1;  // some row does not see the last token
-          const bool part = late || (ss.valid[st][0] & ss.valid[st][1] & ss.valid[st][2] & ss.valid[st][3]) != 0xffffffffu;
-          const uint8_t* src = sm + F::K_OFF + st * F::NARROW + 32 * q * DH;
-          uint8_t* dst = sm + F::V_OFF + s * F::WIDE + 32 * q * 128 + (piece >> 2) * HALF;
-          uint32_t nan = 0;  // tokens with NaN codes
+          if (!await(&ss.full[st], (it / ST) & 1, a.status, abort)) return;
+          const uint32_t ok = ss.valid[st][t0 >> 5];
+          // some row does not see all its tokens
+          const bool part = least < job->token(i) + TT - 1 ||
+                            (ss.valid[st][0] & ss.valid[st][1] & ss.valid[st][2] & ss.valid[st][3]) != 0xffffffffu;
+          uint4 v[N];
 #pragma unroll
-          for (int h = 0; h < 32; h += 4 * ROWS) {
-            uint4 v[4];
+          for (int e = 0; e < N; ++e) v[e] = lds128(sm + F::K_OFF + st * F::NARROW + (t0 + e * ROWS) * DH + lane * 16);
+          const float raw = lane < WIDEN_TOKENS
+                                ? *reinterpret_cast<const float*>(sm + F::SC_OFF + (st * TT + t0 + lane) * 16)
+                                : 0.0f;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ss.k_free[st]);
+          uint32_t nan = 0;
+          if (__builtin_expect(part, 0)) {
+            // a NaN code that some row must not see would reach it as 0 * NaN: it is a 0 here, and the
+            // token's factor is NaN
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = lds128(src + (h + e * ROWS) * DH + lane * 16);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // a NaN code that some row must not see would reach it as 0 * NaN: it is a 0 here, and the
-              // token's factor is NaN
-              if (__builtin_expect(part, 0)) {
-                const uint4 c = without_nan(v[e]);
-                const uint32_t bad =
-                    __ballot_sync(0xffffffffu, c.x != v[e].x || c.y != v[e].y || c.z != v[e].z || c.w != v[e].w);
+            for (int e = 0; e < N; ++e) {
+              const uint4 c = without_nan(v[e]);
+              const uint32_t bad =
+                  __ballot_sync(0xffffffffu, c.x != v[e].x || c.y != v[e].y || c.z != v[e].z || c.w != v[e].w);
+              v[e] = c;
 #pragma unroll 1
-                for (int k = 0; k < ROWS; ++k)
-                  if ((bad >> (k * PIECES)) & ((1u << PIECES) - 1)) nan |= 1u << (h + e * ROWS + k);
-                v[e] = c;
-              }
-              const int row = h + e * ROWS + r0, c = 2 * (piece & 3);
-              uint4 x, y;
-              uint32_t f[2];
-              e4m3x4_to_f16x4(v[e].x, f), x.x = f[0], x.y = f[1];
-              e4m3x4_to_f16x4(v[e].y, f), x.z = f[0], x.w = f[1];
-              e4m3x4_to_f16x4(v[e].z, f), y.x = f[0], y.y = f[1];
-              e4m3x4_to_f16x4(v[e].w, f), y.z = f[0], y.w = f[1];
-              *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = x;
-              *reinterpret_cast<uint4*>(dst + row * 128 + (((c + 1) ^ (row & 7)) << 4)) = y;
+              for (int k = 0; k < ROWS; ++k)
+                if ((bad >> (k * PIECES)) & ((1u << PIECES) - 1)) nan |= 1u << (e * ROWS + k);
             }
           }
-          {  // a token per lane
-            const float raw = *reinterpret_cast<const float*>(sm + F::SC_OFF + (st * TT + 32 * q + lane) * 16);
-            const bool fin = ((ok >> lane) & 1) && fabsf(raw) <= SCALE_MAX;
+          if (it >= NS && !await(&ss.v_free[s], (it / NS - 1) & 1, a.status, abort)) return;
+          uint8_t* dst = sm + F::V_OFF + s * F::WIDE + (piece >> 2) * HALF;
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const int row = t0 + e * ROWS + r0, c = 2 * (piece & 3) + odd;
+            uint4 x, y;
+            uint32_t f[2];
+            e4m3x4_to_f16x4(odd ? v[e].z : v[e].x, f), x.x = f[0], x.y = f[1];
+            e4m3x4_to_f16x4(odd ? v[e].w : v[e].y, f), x.z = f[0], x.w = f[1];
+            e4m3x4_to_f16x4(odd ? v[e].x : v[e].z, f), y.x = f[0], y.y = f[1];
+            e4m3x4_to_f16x4(odd ? v[e].y : v[e].w, f), y.z = f[0], y.w = f[1];
+            *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = x;
+            *reinterpret_cast<uint4*>(dst + row * 128 + (((c ^ 1) ^ (row & 7)) << 4)) = y;
+          }
+          if (lane < WIDEN_TOKENS) {  // a token a lane
+            const bool fin = ((ok >> ((t0 & 31) + lane)) & 1) && fabsf(raw) <= SCALE_MAX;
             const float sc = fin ? raw : 0.0f;
-            float* tok = reinterpret_cast<float*>(sm + F::TOK_OFF) + s * 3 * TT + 32 * q + lane;
+            float* tok = reinterpret_cast<float*>(sm + F::TOK_OFF) + s * 3 * TT + t0 + lane;
             tok[0] = fin && !((nan >> lane) & 1) ? raw * to_log2 : __int_as_float(0x7FC00000);
             tok[TT] = sc;
             tok[2 * TT] = sc != 0.0f ? fmaxf(log2_of(fabsf(sc)), LEAST) : LEAST;
-            if (lane == 0) ss.see[s][q] = ok;
-            if (q == 0 && lane == 0) ss.part[s] = part;
+          }
+          if (lane == 0) {
+            if ((t0 & 31) == 0) ss.see[s][t0 >> 5] = ok;
+            if (t0 == 0) ss.part[s] = part;
           }
           fence_proxy_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ss.v_full[s]), mbar_arrive(&ss.k_free[st]);
+          if (lane == 0) mbar_arrive(&ss.v_full[s]);
         }
+        item_done();
       }
-    } else if (warp == MMA_WARP) {
-      // ------------------------------------------------------------------------------- MMAs
+    }();
+    else if (warp < LOAD_WARP) {
+      // --------------------------------------------------------------- MMAs, a warp per stream
       constexpr uint32_t IS = (1u << 4) | ((uint32_t)(TT >> 3) << 17) | ((uint32_t)(BLOCK >> 4) << 24);
       constexpr uint32_t IO = (1u << 4) | (1u << 16) | ((uint32_t)(DH >> 3) << 17) | ((uint32_t)(BLOCK >> 4) << 24);
-      const uint64_t q0 = desc_sw128(smem_u32(sm + F::Q_OFF)), k0 = desc_sw128(smem_u32(sm + F::V_OFF)),
+      const int u = warp - MMA_WARP;
+      const uint64_t q0 = desc_sw128(smem_u32(sm + F::Q_OFF) + u * F::WIDE), k0 = desc_sw128(smem_u32(sm + F::V_OFF)),
                      v0 = desc_mn(smem_u32(sm + F::V_OFF), HALF);
-      int it = 0;              // the ring's tiles of the items before
-      uint32_t pc[2] = {0, 0};  // the streams' tiles so far
-      auto scores = [&](int u, int j) {
-        const int i = it + job.ring(u, j), s = i % NS;
-        bool ok = wait(&ss.v_full[s], (i / NS) & 1, a.status, abort);
-        if (ok && elect_one()) {
-          tc_fence_after();
-#pragma unroll
-          for (int k = 0; k < DH / 16; ++k)
-            mma_ss(tmem + 128 * u, q0 + u * (F::WIDE / 16) + (k >> 2) * (HALF / 16) + 2 * (k & 3),
-                   k0 + s * (F::WIDE / 16) + (k >> 2) * (HALF / 16) + 2 * (k & 3), IS, k > 0);
-          tc_commit(&ss.s_full[u]);
-          // (the commit is no release: this arrival passes on what the widening warps wrote)
-          mbar_arrive(&ss.s_full[u]);
+      const uint32_t sc = tmem + 128 * u, oc = tmem + F::O_COL + DH * u;
+      int it = 0, seen = 0;  // the ring's tiles of the items before, and those that this warp has waited for
+      uint32_t pc = 0;       // the stream's tiles so far
+      // Waits for the ring's tiles up to i, the other stream's too, and gives those back: a wait is by
+      // parity, so none may be missed, and no slot may go two tiles further before this warp has seen it.
+      auto see = [&](const Job& job, int i) {
+        bool ok = true;
+#pragma unroll 1
+        for (; ok && seen <= i; ++seen) {
+          ok = await(&ss.v_full[seen % NS], (seen / NS) & 1, a.status, abort);
+          if (job.mode != TWO_BLOCKS && ((seen - it) & 1) != u && lane == 0) mbar_arrive(&ss.v_free[seen % NS]);
         }
-        __syncwarp();
+        return ok;
       };
+      bool ok = true;
 #pragma unroll 1
-      for (int item = 0; next_job(ar, plan, cur, job); ++item) {
-#pragma unroll 1
-        for (int u = 0; u < 2; ++u) {
-          wait(&ss.q_full[u], item & 1, a.status, abort);
-          if ((u ? job.n[1] : job.n[0]) > 0) scores(u, 0);
-          else if (lane == 0) mbar_arrive(&ss.o_full[u]);
-          __syncwarp();
-        }
-#pragma unroll 1
-        for (int j = 0; j < job.n[0]; ++j) {
-#pragma unroll 1
-          for (int u = 0; u < 2; ++u) {
-            const int n = u ? job.n[1] : job.n[0];
-            if (j >= n) break;
-            const int s = (it + job.ring(u, j)) % NS;
-            const bool ok = wait(&ss.p_full[u], (u ? pc[1] : pc[0]) & 1, a.status, abort);
-            if (u) ++pc[1]; else ++pc[0];
-            if (ok && elect_one()) {
-              tc_fence_after();
+      while (ok) {
+        const Job* job = next_item();
+        if (!job) break;
+        const int n = u ? job->n[1] : job->n[0];
+        auto scores = [&](int j) {
+          const int i = it + job->ring(u, j);
+          ok = see(*job, i);
+          if (ok && elect_one()) {
+            tc_fence_after();
+            const uint64_t kd = k0 + (i % NS) * (F::WIDE / 16);
 #pragma unroll
-              for (int k = 0; k < TT / 16; ++k)
-                mma_ts(tmem + F::O_COL + DH * u, tmem + 128 * u + 8 * k, v0 + s * (F::WIDE / 16) + k * (2048 / 16), IO,
-                       j > 0 || k > 0);
-              if (!job.pairs || u == 1) tc_commit(&ss.v_free[s]);
-              if (j + 1 == n) tc_commit(&ss.o_full[u]);
-            }
-            __syncwarp();
-            if (j + 1 < n) scores(u, j + 1);
+            for (int k = 0; k < DH / 16; ++k)
+              mma_ss(sc, q0 + (k >> 2) * (HALF / 16) + 2 * (k & 3), kd + (k >> 2) * (HALF / 16) + 2 * (k & 3), IS, k > 0);
+            tc_commit(&ss.s_full[u]);
+            // (the commit is no release: this arrival passes on what the widening warps wrote)
+            mbar_arrive(&ss.s_full[u]);
           }
+          __syncwarp();
+        };
+        ok = await(&ss.q_full[u], item & 1, a.status, abort);
+        if (ok && n > 0) scores(0);
+        else if (lane == 0) mbar_arrive(&ss.o_full[u]);
+#pragma unroll 1
+        for (int j = 0; ok && j < n; ++j, ++pc) {
+          const int s = (it + job->ring(u, j)) % NS;
+          ok = await(&ss.p_full[u], pc & 1, a.status, abort);
+          if (ok && elect_one()) {
+            tc_fence_after();
+            const uint64_t vd = v0 + s * (F::WIDE / 16);
+#pragma unroll
+            for (int k = 0; k < TT / 16; ++k) mma_ts(oc, sc + 8 * k, vd + k * (2048 / 16), IO, j > 0 || k > 0);
+            tc_commit(&ss.v_free[s]);
+            if (j + 1 == n) tc_commit(&ss.o_full[u]);
+          }
+          __syncwarp();
+          if (ok && j + 1 < n) scores(j + 1);
         }
-        it += job.count();
+        ok = ok && see(*job, it + job->count() - 1);
+        it += job->count();
+        item_done();
       }
       if (elect_one()) tc_commit(&ss.drain);
       __syncwarp();
     } else if (warp == LOAD_WARP) {
       // ------------------------------------------------------------------------------ loads
       Loader<DH> tile(ar.box);
-      int it = 0;
-      bool more = next_job(ar, plan, cur, job);
-      int i = 0, n = more ? job.count() : 0;
-      if (more) tile.locate(ar, plan, job, 0);
-#pragma unroll 1
-      while (more) {
-        const int st = it % ST;
-        bool go = true;
-        if (it >= ST) go = wait(&ss.k_free[st], (it / ST - 1) & 1, a.status, abort);
-        tile.load(ar, job.at.slice, sm + F::K_OFF + st * F::NARROW, sm + F::SC_OFF + st * TT * 16, ss.valid[st],
-                  &ss.full[st], go);
-        ++it;
-        if (++i == n) {
-          more = next_job(ar, plan, cur, job);
+      int it = 0, i = 0, n = 0;
+      const Job* job = nullptr;
+      auto advance = [&]() {  // to the next tile, and looks its pages up
+        if (++i >= n) {
+          if (job) item_done();
+          job = next_item();
           i = 0;
-          n = more ? job.count() : 0;
+          n = job ? job->count() : 0;
         }
-        if (more) tile.locate(ar, plan, job, i);
-      }
-    } else if (warp == ROWS_WARP) {
-      // ------------------------------------------------------------------- the items' rows
+        if (job) tile.locate(ar, plan, *job, i);
+      };
+      advance();
 #pragma unroll 1
-      for (int item = 0; next_job(ar, plan, cur, job); ++item) {
-        const int b = item & 1;
-        if (item >= 2) wait(&ss.m_free[b], ((item >> 1) - 1) & 1, a.status, abort);
-        const int least = item_rows(ar, plan, job, ss.row[b]);
-        if (lane == 0) ss.least[b] = least;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ss.m_full[b]);
+      for (; job; ++it) {
+        const int st = it % ST;
+        if (it >= ST && !await(&ss.k_free[st], (it / ST - 1) & 1, a.status, abort)) break;
+        tile.load(ar, job->slice_of(i & 1), sm + F::K_OFF + st * F::NARROW, sm + F::SC_OFF + st * TT * 16, ss.valid[st],
+                  &ss.full[st]);
+        advance();
       }
+      // (what is on its way lands in this CTA's shared memory)
+#pragma unroll 1
+      for (int k = max(0, it - ST); k < it; ++k) mbar_wait(&ss.full[k % ST], (k / ST) & 1, a.status);
     } else {
-      // ------------------------- where the join finds a row's pieces: per kind of group, its first unit in
-      // the line, tiles, blocks and the row's rank (tiles 0: none)
+      // ------------------------------------------------------------------ the items and their rows
+      Cursor cur = ss.start;
+#pragma unroll 1
+      for (;; ++item) {
+        const int k = item % JOBS;
+        if (item >= JOBS && !await(&ss.j_free[k], (item / JOBS - 1) & 1, a.status, abort)) break;
+        Job& job = ss.job[k];
+        bool more = false;
+        if (lane == 0) more = next_job(ar, plan, cur, job);
+        more = __shfl_sync(0xffffffffu, more, 0);
+        if (more) item_rows(ar, plan, job);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ss.j_full[k]);
+        if (!more) break;
+      }
+      // where the join finds a row's pieces: per kind of group, its first unit in the line, tiles, rows and
+      // the row's rank (tiles 0: none)
 #pragma unroll 1
       for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        const int b = plan.req[r];
-        int rank[2] = {0, 0};
-        const int g = b < 0 ? -1 : plan.pfx[b];
+        const int b = plan.req[r], g = b < 0 ? -1 : plan.pfx[b];
+        int own = 0, pre = 0;
         if (b >= 0) {
 #pragma unroll 1
           for (int i = lane; i < r; i += 32) {
             const int c = plan.req[i];
-            rank[1] += c == b;
-            rank[0] += c >= 0 && plan.pfx[c] == g;
+            own += c == b;
+            pre += c >= 0 && plan.pfx[c] == g;
           }
         }
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-          const int n = __reduce_add_sync(0xffffffffu, k ? rank[1] : rank[0]);
-          const int at = b < 0 ? -1 : k ? a.n_prefix + b : g;
-          int4 v = {0, 0, 0, n};
-          if (at >= 0) {
-            const Shape2 s = shape_of_group(ar, plan, at);
-            v.x = plan.pre[at], v.y = s.tiles, v.z = s.blocks;
-          }
-          if (lane == 0) reinterpret_cast<int4*>(ar.info)[2 * r + k] = v;
+        own = __reduce_add_sync(0xffffffffu, own);
+        pre = __reduce_add_sync(0xffffffffu, pre);
+        if (lane < 2) {
+          const int at = b < 0 ? -1 : lane ? a.n_prefix + b : g;
+          int4 v = {0, 0, 0, lane ? own : pre};
+          if (at >= 0) v.x = plan.pre[at], v.y = items_of(ar, plan, at).tiles, v.z = plan.cnt[at];
+          reinterpret_cast<int4*>(ar.info)[2 * r + lane] = v;
         }
         if (lane == 0 && r == 0) ar.info[8 * a.rows] = plan.pre[a.n_prefix + a.n_req];
       }
     }
-  } else {
+  } else [&] {
     // ------------------------------------------------------------------------------- softmax
     regs_up<SOFT_REGS>();
     const int u = warp >> 2, quad = warp & 3, q = 32 * quad + lane;
-    Soft w;
-    w.s_at = tmem + 128 * u + ((uint32_t)(32 * quad) << 16);
-    w.o_at = tmem + F::O_COL + DH * u + ((uint32_t)(32 * quad) << 16);
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16), s_at = lanes + 128 * u, o_at = lanes + F::O_COL + DH * u;
     const int j_row = q / ar.hps, head = q - j_row * ar.hps;
     int it = 0;
-    uint32_t sc = 0;
+    uint32_t sc = 0, mc = 0;  // the stream's tiles, and phases of the merging barrier, so far
 #pragma unroll 1
-    for (int item = 0; next_job(ar, plan, cur, job); ++item) {
-      wait(&ss.m_full[item & 1], (item >> 1) & 1, a.status, abort);
-      const int row = j_row < ar.rows_per ? ss.row[item & 1][(job.pairs ? u * BLOCK : 0) + j_row] : -1;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ss.m_free[item & 1]);
-      w.hi = row >= 0 ? plan.hi[row] : -1;
-      w.m = UNSET;
-      w.l = 0.0f;
-      w.factor = 1.0f;
-      {  // the query
-        uint4 v[DH / 8];
-        if (row >= 0) {
-          const uint4* src = reinterpret_cast<const uint4*>(a.q + row * a.q_stride + (job.at.slice * ar.hps + head) * DH);
-#pragma unroll
-          for (int e = 0; e < DH / 8; ++e) v[e] = src[e];
-        } else {
-#pragma unroll
-          for (int e = 0; e < DH / 8; ++e) v[e] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        // its largest finite element, as bf16 bits
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < DH / 8; ++e) {
-          const uint32_t x[4] = {v[e].x & 0x7FFF7FFFu, v[e].y & 0x7FFF7FFFu, v[e].z & 0x7FFF7FFFu, v[e].w & 0x7FFF7FFFu};
-          top = max_u16x2(top, max_u16x2(max_u16x2(x[0], x[1]), max_u16x2(x[2], x[3])));
-        }
-        top = max(top >> 16, top & 0xFFFFu);
-        float up = 1.0f;
-        // (in f16's reach as it is: 2^-1 to 2^15; NaN and infinities make the row NaN either way)
-        if (top != 0 && top < 0x7F80u && (top < 0x3F00u || top >= 0x4700u)) {
-          const int e = max((int)(top >> 7), 1);  // the largest element is 2^(e - 127) or more: to 2^4, or as near as an f32 goes
-          const int k = min(max(131 - e, -126), 126);
-          up = __uint_as_float((uint32_t)(127 + k) << 23);
-          w.factor = __uint_as_float((uint32_t)(127 - k) << 23);
-        }
+    while (const Job* at = next_item()) {
+      const Job& job = *at;
+      const int n = u ? job.n[1] : job.n[0], mode = job.mode;
+      const int row = j_row < ar.rows_per ? job.row[(mode == TWO_BLOCKS ? u * BLOCK : 0) + j_row] : -1;
+      const int hi = row >= 0 ? plan.hi[row] : -1;
+      float factor = 1.0f;
+      {  // the query; most need no scaling, which is found out on the way
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + max(row, 0) * a.q_stride +
+                                                          (job.slice_of(u) * ar.hps + head) * DH);
         uint8_t* dst = sm + F::Q_OFF + u * F::WIDE + q * 128;
+        float up = 1.0f;
+        bool again = false;
+#pragma unroll 1
+        for (;;) {
+          uint32_t top = 0;  // the largest element, as bf16 bits
+#pragma unroll 1
+          for (int e0 = 0; e0 < DH / 8; e0 += 8) {
+            uint4 v[8];
 #pragma unroll
-        for (int e = 0; e < DH / 8; ++e) {
-          float f[8];
-          bf16x8_to_f32(v[e], f);
+            for (int e = 0; e < 8; ++e) v[e] = row >= 0 ? src[e0 + e] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] *= up;
-          if (__builtin_expect(top >= 0x7F80u, 0)) {
+            for (int e = 0; e < 8; ++e) {
+              float f[8];
+              bf16x8_to_f32(v[e], f);
+              top = max_u16x2(top, max_u16x2(max_u16x2(v[e].x & 0x7FFF7FFFu, v[e].y & 0x7FFF7FFFu),
+                                             max_u16x2(v[e].z & 0x7FFF7FFFu, v[e].w & 0x7FFF7FFFu)));
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (isinf(f[k])) f[k] = __int_as_float(0x7FC00000);
+              for (int k = 0; k < 8; k += 2) mul2(f[k], f[k + 1], up);
+              *reinterpret_cast<uint4*>(dst + (e0 >> 3) * HALF + ((e ^ (q & 7)) << 4)) =
+                  make_uint4(f16x2_of(f[0], f[1]), f16x2_of(f[2], f[3]), f16x2_of(f[4], f[5]), f16x2_of(f[6], f[7]));
+            }
           }
-          *reinterpret_cast<uint4*>(dst + (e >> 3) * HALF + (((e & 7) ^ (q & 7)) << 4)) =
-              make_uint4(f16x2_of(f[0], f[1]), f16x2_of(f[2], f[3]), f16x2_of(f[4], f[5]), f16x2_of(f[6], f[7]));
+          if (again) break;
+          top = max(top >> 16, top & 0xFFFFu);
+          // in f16's reach as it is: 2^-1 to 2^15
+          const bool far = top != 0 && (top < 0x3F00u || top >= 0x4700u);
+          again = __any_sync(0xffffffffu, far);
+          if (__builtin_expect(!again, 1)) break;
+          if (top >= 0x7F80u) {  // not finite: the query's weights are NaN
+            up = factor = __int_as_float(0x7FC00000);
+          } else if (far) {
+            // the largest element is in [2^(e - 127), 2^(e - 126)): to 2^4, or as near as an f32 goes
+            const int e = max((int)(top >> 7), 1), k = min(max(131 - e, -126), 126);
+            up = __uint_as_float((uint32_t)(127 + k) << 23);
+            factor = __uint_as_float((uint32_t)(127 - k) << 23);
+          }
         }
       }
-      w.scaled = __any_sync(0xffffffffu, w.factor != 1.0f);
+      const bool scaled = __any_sync(0xffffffffu, factor != 1.0f);
       const bool idle = !__any_sync(0xffffffffu, row >= 0);  // no queries in this warp
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ss.q_full[u]);
 
-      const int n = u ? job.n[1] : job.n[0];
+      float m = UNSET, l0 = 0.0f, l1 = 0.0f;
 #pragma unroll 1
       for (int j = 0; j < n; ++j, ++sc) {
-        const int i = job.ring(u, j), s = (it + i) % NS, t0 = job.token(i);
-        wait(&ss.s_full[u], sc & 1, a.status, abort);
+        const int i = job.ring(u, j), s = (it + i) % NS;
+        if (!await(&ss.s_full[u], sc & 1, a.status, abort)) return;
         if (!idle) {
-          tc_fence_after();
           const float* tok = reinterpret_cast<const float*>(sm + F::TOK_OFF) + s * 3 * TT;
-          const uint32_t* see = ss.see[s];
           const bool part = ss.part[s];
-          uint32_t p[64], top;
-          float l0, l1;
-          bool moved = false, move = j == 0;
+          tc_fence_after();
+          // 32 tokens at a time: their weights times scales, as packed f16, take their scores' place
 #pragma unroll 1
-          for (;;) {
-            if (move) {
-              if (part) move_reference<DH, true>(w, tok, see, t0, j == 0);
-              else move_reference<DH, false>(w, tok, see, t0, j == 0);
-              moved = true;
+          for (int c = 0; c < 4; ++c) {
+            uint32_t sees = 0xffffffffu;
+            if (__builtin_expect(part, 0)) {
+              const int k = hi - (job.token(i) + 32 * c) + 1;
+              sees = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1;
+              sees &= ss.see[s][c];
             }
-            if (part) tile_weights<true>(w, tok, see, t0, p, l0, l1, top);
-            else tile_weights<false>(w, tok, see, t0, p, l0, l1, top);
-            if (moved) break;
-            move = __any_sync(0xffffffffu, (top & 0xFFFFu) > TOO_LARGE || (top >> 16) > TOO_LARGE);
-            if (!move) break;
+            bool moved = false, move = j == 0 && c == 0;
+#pragma unroll 1
+            for (;;) {
+              uint32_t raw[32];
+              float* x = reinterpret_cast<float*>(raw);
+              tc_ld32(s_at + 32 * c, raw);
+              tc_wait_ld();
+              loaded32(raw);
+              if (__builtin_expect(scaled, 0)) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) mul2(x[e], x[e + 1], factor);
+              }
+              if (__builtin_expect(move, 0)) {
+                // the reference to the largest of these weights times scales, and what was summed under the
+                // old one with it
+                float top = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                  const float4 f = *reinterpret_cast<const float4*>(tok + 32 * c + e);
+                  const float4 g = *reinterpret_cast<const float4*>(tok + 2 * TT + 32 * c + e);
+                  const float y[4] = {fmaf(x[e], f.x, g.x), fmaf(x[e + 1], f.y, g.y), fmaf(x[e + 2], f.z, g.z),
+                                      fmaf(x[e + 3], f.w, g.w)};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    if ((sees >> (e + k)) & 1) top = fmaxf(top, y[k]);
+                }
+                float f = 1.0f;
+                if (top - m > BASE) {
+                  const float now = fabsf(top) <= SCORE_MAX ? ceilf(top) - BASE : __int_as_float(0x7FC00000);
+                  f = m == UNSET ? 0.0f : ex2(m - now);
+                  m = now;
+                }
+                l0 *= f;
+                l1 *= f;
+                if (j > 0) scale_columns<false>(o_at, DH, f);
+                tc_wait_st();
+                if (c > 0) scale_columns<true>(s_at, 16 * c, f);
+                moved = true;
+              }
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(tok + 32 * c + e);
+                fma2t(x[e], x[e + 1], f.x, f.y, -m);
+                fma2t(x[e + 2], x[e + 3], f.z, f.w, -m);
+              }
+              if (__builtin_expect(part, 0)) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((sees >> e) & 1)) x[e] = -INFINITY;
+              }
+              float k0 = 0.0f, k1 = 0.0f;
+              uint32_t p[16], top = 0;
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 g = *reinterpret_cast<const float4*>(tok + TT + 32 * c + e);
+                float p0 = ex2(x[e]), p1 = ex2(x[e + 1]), p2 = ex2(x[e + 2]), p3 = ex2(x[e + 3]);
+                add2(k0, k1, p0, p1);
+                add2(k0, k1, p2, p3);
+                mul2(p0, p1, g.x, g.y);
+                mul2(p2, p3, g.z, g.w);
+                p[e / 2] = f16x2_of(p0, p1);
+                p[e / 2 + 1] = f16x2_of(p2, p3);
+                top = max_u16x2(top, max_u16x2(p[e / 2], p[e / 2 + 1]));
+              }
+              if (!moved) {
+                move = __any_sync(0xffffffffu, (top & 0xFFFFu) > TOO_LARGE || (top >> 16) > TOO_LARGE);
+                if (__builtin_expect(move, 0)) continue;
+              }
+              add2(l0, l1, k0, k1);
+              st16(s_at + 16 * c, p);
+              break;
+            }
           }
-          w.l += l0 + l1;
-          st32(w.s_at, p);
-          st32(w.s_at + 32, p + 32);
           tc_wait_st();
           tc_fence_before();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ss.p_full[u]);
       }
-      wait(&ss.o_full[u], item & 1, a.status, abort);
+      if (!await(&ss.o_full[u], item & 1, a.status, abort)) return;
       tc_fence_after();
       it += job.count();
 
       // ---- the piece: where it goes, then O
       float* to = nullptr;
       if (row >= 0) {
-        const int kind = job.at.g < a.n_prefix ? 0 : 1;
-        const size_t k = job.s0 == 0 ? ((size_t)kind * ar.max_rows + row) * a.n_q + job.at.slice * ar.hps + head
-                                     : (size_t)blockIdx.x * (2 * BLOCK) + (job.pairs ? u * BLOCK : 0) + q;
-        to = (job.s0 == 0 ? ar.home : ar.over) + k * (DH + 4);
+        const int kind = job.g < a.n_prefix ? 0 : 1;
+        const size_t k = job.begins
+                             ? ((size_t)kind * ar.max_rows + row) * a.n_q + job.slice_of(u) * ar.hps + head
+                             : (size_t)blockIdx.x * (2 * BLOCK) + (mode == TWO_TILES ? 0 : u * BLOCK) + q;
+        to = (job.begins ? ar.home : ar.over) + k * F::PART_LD;
       }
-      if (job.pairs) {
-        if (to) *reinterpret_cast<float2*>(to) = make_float2(w.m, w.l);
+      float l = l0 + l1;
+      if (mode != TWO_TILES) {
+        if (!idle) {
+          if (to) *reinterpret_cast<float2*>(to) = make_float2(m, l);
 #pragma unroll 1
-        for (int c = 0; c < DH; c += 32) {
-          uint32_t o[32];
-          tc_ld32(w.o_at + c, o);
-          tc_wait_ld();
-          loaded32(o);
-          if (to)
+          for (int c = 0; c < DH; c += 32) {
+            uint32_t o[32];
+            tc_ld32(o_at + c, o);
+            tc_wait_ld();
+            loaded32(o);
+            if (to)
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(to + 4 + c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              for (int e = 0; e < 32; e += 8) st_global8(to + 8 + c + e, o + e);
+          }
         }
       } else {  // both streams' O in the larger m, half of the dimensions each
-        ss.ml[u][q] = make_float2(w.m, w.l);
-        bar_sync<SOFT>(1);
+        auto meet = [&] {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ss.merge);
+          return await(&ss.merge, mc++ & 1, a.status, abort);
+        };
+        ss.ml[u][q] = make_float2(m, l);
+        if (!meet()) return;
         const float2 x = ss.ml[0][q], y = ss.ml[1][q];
-        const float m = fmaxf(x.x, y.x);
+        m = fmaxf(x.x, y.x);
         // (a NaN stays one)
         const float fx = x.y != x.y ? 1.0f : x.x == UNSET ? 0.0f : ex2(x.x - m);
         const float fy = y.y != y.y ? 1.0f : y.x == UNSET ? 0.0f : ex2(y.x - m);
-        const float l = (fx != 0.0f ? x.y * fx : 0.0f) + (fy != 0.0f ? y.y * fy : 0.0f);
+        l = (fx != 0.0f ? x.y * fx : 0.0f) + (fy != 0.0f ? y.y * fy : 0.0f);
         if (to && u == 0) *reinterpret_cast<float2*>(to) = make_float2(m, l);
-        const uint32_t o0 = tmem + F::O_COL + ((uint32_t)(32 * quad) << 16);
 #pragma unroll 1
-        for (int c = u * (DH / 2); c < (u + 1) * (DH / 2); c += 32) {
-          uint32_t v[32], z[32];
-          tc_ld32(o0 + c, v);
-          tc_ld32(o0 + DH + c, z);
+        for (int c = u * (DH / 2); c < (u + 1) * (DH / 2); c += 8) {
+          float v[8], z[8];
+          tc_ld8(lanes + F::O_COL + c, v);
+          tc_ld8(lanes + F::O_COL + DH + c, z);
           tc_wait_ld();
-          loaded32(v);
-          loaded32(z);
+          tc_loaded(v);
+          tc_loaded(z);
+          uint32_t w[8];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float p0 = fx != 0.0f ? __uint_as_float(v[e]) * fx : 0.0f;
-            const float p1 = fy != 0.0f ? __uint_as_float(z[e]) * fy : 0.0f;
-            v[e] = __float_as_uint(p0 + p1);
+          for (int e = 0; e < 8; ++e) {
+            const float p0 = fx != 0.0f ? v[e] * fx : 0.0f, p1 = fy != 0.0f ? z[e] * fy : 0.0f;
+            w[e] = __float_as_uint(p0 + p1);
           }
-          if (to)
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(to + 4 + c + e) = make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          if (to) st_global8(to + 8 + c, w);
         }
         tc_fence_before();
-        bar_sync<SOFT>(1);  // (the next item's products go over both)
+        if (!meet()) return;  // (the next item's products go over both)
         tc_fence_after();
       }
       tc_fence_before();
+      item_done();
     }
-  }
+  }();
   tc_fence_before();
   __syncthreads();
   if (warp == MMA_WARP) {
-    (void)wait(&ss.drain, 0, a.status, abort);
+    mbar_wait(&ss.drain, 0, a.status);  // (whatever ran out before)
     tc_fence_after();
     tmem_dealloc<512>(tmem);
   }
@@ -925,7 +970,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_shared_kernel(const __gr
   const SharedArgs& a = ar.a;
   const int r = blockIdx.x, h = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int dh = a.head_dim, d = 4 * lane & (dh - 1), step = 128 / dh, own = lane * 4 / dh;
-  const int slice = h / ar.hps, ld = dh + 4;
+  const int slice = h / ar.hps, ld = dh + 8;
   pdl_trigger();
   pdl_wait();
   if (h >= a.n_q) return;
@@ -936,13 +981,21 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_shared_kernel(const __gr
     const int4 v = reinterpret_cast<const int4*>(ar.info)[2 * r + k];
     n[k] = 0, over[k] = 0;
     if (v.y == 0) continue;
-    Shape2 s = {v.y, v.z, EXTRA + v.y, EXTRA + (v.y + 1) / 2};
-    const int block = v.w / ar.rows_per, pair = block >> 1;
-    const int from = v.x + slice * s.slice_len() + pair * s.whole;
-    const int k0 = cut.team_of(from + EXTRA), k1 = cut.team_of(from + s.len(pair) - 1);
+    const Items it(ar, v.y, v.z);
+    const int block = v.w / ar.rows_per, of_pairs = it.of_pairs(ar), pairs = it.blocks >> 1;
+    int item, len = it.len, lane0 = 0;
+    if (block < 2 * pairs) {
+      item = slice * pairs + (block >> 1);
+      lane0 = (block & 1) * BLOCK;
+    } else {
+      item = of_pairs + (slice >> 1);
+      if (item < it.whole(ar)) lane0 = (slice & 1) * BLOCK;
+      else len = it.half;
+    }
+    const int from = v.x + item * it.len;
+    const int k0 = cut.team_of(from + EXTRA), k1 = cut.team_of(from + len - 1);
     n[k] = k1 - k0 + 1;
-    over[k] = (k0 + 1) * (2 * BLOCK) + (s.pairs(pair) ? (block & 1) * BLOCK : 0) + (v.w - block * ar.rows_per) * ar.hps +
-              (h - slice * ar.hps);
+    over[k] = (k0 + 1) * (2 * BLOCK) + lane0 + (v.w - block * ar.rows_per) * ar.hps + (h - slice * ar.hps);
   }
   const int all = n[0] + n[1];
   auto piece = [&](int i) -> const float* {
@@ -950,7 +1003,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_shared_kernel(const __gr
     return x == 0 ? ar.home + (((size_t)k * ar.max_rows + r) * a.n_q + h) * ld
                   : ar.over + ((size_t)over[k] + (size_t)(x - 1) * (2 * BLOCK)) * ld;
   };
-  auto fetch = [&](int i) { return *reinterpret_cast<const float4*>(piece(i) + 4 + d); };
+  auto fetch = [&](int i) { return *reinterpret_cast<const float4*>(piece(i) + 8 + d); };
   float m = UNSET, den = 0.0f;
   float4 num = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
@@ -1009,7 +1062,7 @@ struct Layout {
 };
 Layout layout(int max_rows, int n_q, int head_dim, int sms) {
   Layout l;
-  const size_t piece = (size_t)(head_dim + 4) * 4;
+  const size_t piece = (size_t)(head_dim + 8) * 4;  // (Form::PART_LD)
   l.info = 0;
   l.home = ((size_t)max_rows * 32 + 16 + 255) / 256 * 256;
   l.over = l.home + 2 * (size_t)max_rows * n_q * piece;

@@ -157,6 +157,18 @@ def test_long_prefix():
     check(WIDE, [20011], [0] * 3, [1, 40, 77], [1, 2, 3], seed=11)
 
 
+def test_many_steps_of_two_blocks():
+    """Some ten tiles a CTA and item: the rings go round."""
+    check(dict(TINY, n_q_heads=4), [12000], [0] * 16, [64 + i for i in range(16)], [64] * 16, seed=12)
+
+
+@pytest.mark.parametrize("layout,P", [("wide", 1500), ("tiny", 3000), ("odd", 1700), ("three", 900)])
+def test_many_steps_of_single_blocks(layout, P):
+    """Many prefixes with two rows each: two slices at once, or every other tile."""
+    n = 128 if layout in ("wide", "tiny") else 60
+    check(LAYOUTS[layout], [P - 3 * i for i in range(n)], list(range(n)), [2 + i % 3 for i in range(n)], [2] * n, seed=13)
+
+
 def test_without_any_prefix_and_with_empty_ones():
     check(WIDE, [64], [-1, -1], [300, 20], [3, 2], seed=3)
     check(WIDE, [0, 64], [0, 1], [300, 20], [3, 2], seed=4)
