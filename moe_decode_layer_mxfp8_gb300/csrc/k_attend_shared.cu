@@ -2,14 +2,14 @@
 // read once for the rows of all its requests, every request's own tokens for its rows.
 //
 //   S[q, t] = codes_t . q        (query q = one head of one row, token t)
-//   P[q, t] = 2^(a_t S - m_q) scale_t,  a_t = scale scale_t log2e     O[q, :] = sum_t P[q, t] codes_t
+//   P[q, t] = 2^(a_t S - m_q) a_t,  a_t = scale scale_t log2e         O[q, :] = sum_t P[q, t] codes_t
 //
 // Queries are the M of both products, 128 of them a block: the heads that read a latent slice, times as
 // many rows as fit.  Tokens are the N of the first product, 128 a tile, and its K operand is the V
 // operand of the second: the tile is widened from e4m3 to f16 (exact) once, and serves both.  A query
 // is f16 too, off by at most 2^-24 of its largest element (those out of f16's reach are scaled by a
 // power of two).  P is f16 (11 bits; the one rounding between scores and o) under m_q, an integer that
-// follows the weights times scales, so that the largest of the tile that set it is in (2^5, 2^6], and
+// follows them, so that the largest of the 64 tokens that set it is in (2^5, 2^6], and
 // moves when one passes 2^15; O is rescaled then, exactly.  P takes its scores' place in TMEM.
 //
 // Work: groups (a prefix with its requests' rows; a request's own tokens with its rows), slices and
@@ -18,8 +18,8 @@
 // tiles, of two slices of one block, or (where a slice is left alone) of every other tile.  What a CTA has of an item leaves (O, m, l)
 // in the workspace; a second kernel joins them.
 //
-// Roles: warps 0-3 and 4-7 softmax, a query per thread; 8-15 widen tiles; 16 and 17 issue a stream's MMAs
-// each; 18 loads; 19 makes the items and their rows, and tells the join where pieces are.
+// Roles: warps 0-7 and 8-15 softmax; 16-19 widen tiles; 20 and 21 issue a stream's MMAs each; 22 loads; 23
+// makes the items and their rows, and tells the join where pieces are.
 // Every wait is for an mbarrier, and bounded; one that runs out is reported and ends its role, and with it
 // the others' waits.  Copies and products on their way are waited for before the CTA ends.
 #include "attend_tc.cuh"
@@ -30,31 +30,48 @@ namespace {
 using namespace tc;
 using namespace attend;
 
-constexpr int WIDEN_WARPS = 8, WIDEN_TOKENS = TT / WIDEN_WARPS;
-constexpr int WIDEN_WARP = 8, MMA_WARP = WIDEN_WARP + WIDEN_WARPS, LOAD_WARP = MMA_WARP + 2, ROWS_WARP = LOAD_WARP + 1;
+constexpr int SOFT_WARPS = 16, STREAM_WARPS = SOFT_WARPS / 2, WIDEN_WARPS = 4, WIDEN_TOKENS = TT / WIDEN_WARPS;
+constexpr int WIDEN_WARP = SOFT_WARPS, MMA_WARP = WIDEN_WARP + WIDEN_WARPS, LOAD_WARP = MMA_WARP + 2, ROWS_WARP = LOAD_WARP + 1;
 constexpr int THREADS = 32 * (ROWS_WARP + 1), SOFT = 32 * WIDEN_WARP;
 constexpr int MAX_GROUPS = MAX_PREFIX + MAX_REQ;
 constexpr int BLOCK = 128;       // queries
 constexpr int EXTRA = 3;         // what an item costs a CTA beside its steps, in steps
 constexpr int HALF = TT * 128;   // bytes of 64 dimensions of a tile, or a block, in f16
 constexpr int JOBS = 4;          // items whose rows are made ahead
-constexpr float BASE = 6.0f, LEAST = -90.0f;  // log2 of the weights times scales that m puts at most; scales below
-constexpr uint32_t TOO_LARGE = 0x7800;        // f16 of 2^15
+constexpr float BASE = 6.0f, LEAST = -90.0f;  // log2 of the weights times a_t that m puts at most; a_t below
+constexpr float TOO_LARGE = 0x1p15f;           // m moves when a weight times a_t may be larger (f16 ends at 2^16)
+// queries are taken times 2^6: the largest element of most is then between 2^-1 and 2^15 (bf16 bits of the limits)
+constexpr float Q_SCALE = 64.0f;
+constexpr uint32_t Q_LOW = 0x3C00, Q_HIGH = 0x4400;
 // registers a thread at launch, and as the roles divide them
-constexpr int REGS = 96, SOFT_REGS = 144, OTHER_REGS = 64;
+constexpr int REGS = 80, SOFT_REGS = 88, OTHER_REGS = 64;
 static_assert(SOFT_REGS * SOFT + OTHER_REGS * (THREADS - SOFT) == REGS * THREADS, "register split");
+
+// The step as every CTA derives it.  Groups: prefixes, then requests.
+struct Plan {
+  int pre[MAX_GROUPS + 4];  // [groups + 1] the line's steps of all groups before
+  int end[MAX_GROUPS];      // one behind the last token that a row sees
+  int first[MAX_GROUPS];    // the first
+  int len[MAX_PREFIX];      // tokens of a prefix
+  int hi[MAX_ROWS];         // a row's last token
+  short cnt[MAX_GROUPS];    // rows
+  short req[MAX_ROWS];      // a row's request; -1: nothing to see
+  short pfx[MAX_REQ];       // a request's prefix; -1: none, -2: bad
+};
 
 template <int DH>
 struct Form {
   static constexpr int WIDE = DH / 64 * HALF, NARROW = TT * DH;  // a tile in f16, in e4m3
   static constexpr int NS = DH == 128 ? 3 : 5, ST = DH == 128 ? 2 : 4;  // rings of wide and narrow tiles
-  static constexpr int Q_OFF = 0, V_OFF = Q_OFF + 2 * WIDE, K_OFF = V_OFF + NS * WIDE;
+  // a stream's queries; its O goes through the same place, half of the dimensions at a time, in rows 16 bytes
+  // longer than they are (no bank twice)
+  static constexpr int Q_BYTES = WIDE + 16 * BLOCK, O_LD = 2 * DH + 16;
+  static_assert(Q_BYTES == BLOCK * O_LD, "O's rows");
+  static constexpr int Q_OFF = 0, V_OFF = Q_OFF + 2 * Q_BYTES, K_OFF = V_OFF + NS * WIDE;
   static constexpr int SC_OFF = K_OFF + ST * NARROW;      // the 16 bytes behind the codes [ST][TT]
-  static constexpr int TOK_OFF = SC_OFF + ST * TT * 16;   // a_t, scale_t, log2 scale_t [NS][3][TT]
-  static constexpr int PLAN_OFF = TOK_OFF + NS * 3 * TT * 4;
-  static constexpr int PLAN_BYTES = (MAX_GROUPS + 4) * 4 + MAX_GROUPS * (4 + 4 + 2) + MAX_PREFIX * 4 + MAX_ROWS * 6 +
-                                    MAX_REQ * 2;
-  static constexpr int SMEM_BYTES = PLAN_OFF + PLAN_BYTES + 1024;
+  static constexpr int TOK_OFF = SC_OFF + ST * TT * 16;   // a_t [NS][TT], in the order of token_slot
+  static constexpr int PLAN_OFF = TOK_OFF + NS * TT * 4;
+  static constexpr int SMEM_BYTES = PLAN_OFF + (int)sizeof(Plan) + 1024;
   static constexpr int O_COL = 256;  // TMEM: scores (and weights) of stream u at 128 u, its O at O_COL + DH u
   static constexpr int PART_LD = DH + 8;  // a piece: m, l, six words of padding, O
 };
@@ -70,17 +87,16 @@ struct Args {
   int max_rows;
 };
 
-// The step as every CTA derives it.  Groups: prefixes, then requests.
-struct Plan {
-  int* pre;    // [groups + 1] the line's steps of all groups before
-  int* end;    // [groups] one behind the last token that a row sees
-  int* first;  // [groups] the first
-  short* cnt;  // [groups] rows
-  int* len;    // [n_prefix] tokens
-  int* hi;     // [rows] a row's last token
-  short* req;  // [rows] its request; -1: nothing to see
-  short* pfx;  // [n_req] its prefix; -1: none, -2: bad
-};
+// (tokens behind what the requests' table holds are nobody's; a prefix's end was cut to its table)
+__device__ __forceinline__ int end_of(const SharedArgs& a, const Plan& p, int g) {
+  return g < a.n_prefix ? p.end[g] : min(p.end[g], a.kv.max_blocks * a.kv.block_size);
+}
+
+// A softmax lane has the tokens 8 k + 2 (lane & 3), and the next one, of a tile: where a token's factor is,
+// so that 16 bytes hold a lane's of two k.
+__device__ __forceinline__ int token_slot(int t) {
+  return (t >> 4) * 16 + ((t >> 1) & 3) * 4 + ((t >> 3) & 1) * 2 + (t & 1);
+}
 
 // A group's items.  First those of two blocks: for every slice the pairs of blocks.  Then those of an odd
 // last block: of two slices each, and if a slice is left, one whose streams take every other tile.
@@ -95,7 +111,7 @@ struct Items {
   __device__ int count(const Args& ar) const { return whole(ar) + (blocks & ar.slices & 1); }
 };
 __device__ __forceinline__ Items items_of(const Args& ar, const Plan& p, int g) {
-  const int n = p.cnt[g], lo = p.first[g], end = p.end[g];
+  const int n = p.cnt[g], lo = p.first[g], end = end_of(ar.a, p, g);
   return Items(ar, n == 0 || end <= lo ? 0 : ((end - 1) >> 7) - (lo >> 7) + 1, n);
 }
 
@@ -158,15 +174,15 @@ __device__ __forceinline__ bool next_job(const Args& ar, const Plan& p, Cursor& 
 
 struct Shared {
   uint64_t full[4], k_free[4], v_full[5], v_free[5];
-  uint64_t s_full[2], p_full[2], o_full[2], q_full[2], merge, j_full[JOBS], j_free[JOBS], drain;
+  uint64_t s_full[2], p_full[2], o_full[2], o_out[2], q_full[2], merge, j_full[JOBS], j_free[JOBS], drain;
   uint32_t valid[4][4];                // tokens that are there, of a narrow tile
   alignas(16) uint32_t see[5][4];      // and of a wide one
   int part[5];                         // not every row of the item sees all its tokens
+  alignas(16) float most[5][WIDEN_WARPS];  // its largest |a_t|, of a warp's tokens each
   Job job[JOBS];
   float2 ml[2][BLOCK];
   uint32_t tmem;
   int abort;
-  Cursor start;
 };
 static_assert(Form<128>::SMEM_BYTES + sizeof(Shared) <= 227 * 1024, "shared memory");
 static_assert(Form<64>::SMEM_BYTES + sizeof(Shared) <= 227 * 1024, "shared memory");
@@ -178,9 +194,10 @@ __device__ __forceinline__ void fma2t(float& x, float& y, float ax, float ay, fl
       : "+f"(x), "+f"(y)
       : "f"(ax), "f"(ay), "f"(b));
 }
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+// The larger magnitudes of two pairs of bf16 (with whatever sign).
+__device__ __forceinline__ uint32_t larger_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 __device__ __forceinline__ void loaded32(uint32_t (&r)[32]) {
@@ -190,12 +207,28 @@ __device__ __forceinline__ void loaded32(uint32_t (&r)[32]) {
                "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
                "+r"(r[31]));
 }
-__device__ __forceinline__ void st16(uint32_t taddr, const uint32_t* r) {
+// 16 rows x 32 columns: registers 4 k + 2 h + b are row lane / 4 + 8 h, column 8 k + 2 (lane & 3) + b.
+__device__ __forceinline__ void ld_rows(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void loaded16(uint32_t (&r)[16]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+               "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+// 16 rows x 16 columns of packed pairs: registers 2 k + h are row lane / 4 + 8 h, column 4 k + (lane & 3).
+__device__ __forceinline__ void st_rows(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// A bulk copy from shared to global memory, in a group with this thread's others until they are waited for.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
 }
 // 32 bytes at once
 __device__ __forceinline__ void st_global8(float* p, const uint32_t* r) {
@@ -246,11 +279,11 @@ __device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, int* statu
   return __all_sync(0xffffffffu, ok);
 }
 
-// Fills the plan (every thread of the block) and finds the CTA's first item; the results are behind the
-// caller's next barrier.  Waits for the kernels before.
-__device__ __forceinline__ void derive_plan(const Args& ar, const Plan& plan, Cursor* start) {
+// Fills the plan but for the line (every thread of the block); the results are behind the caller's next
+// barrier.  Waits for the kernels before.
+__device__ __forceinline__ void derive_plan(const Args& ar, Plan& plan) {
   const SharedArgs& a = ar.a;
-  const int tid = threadIdx.x, lane = tid & 31, np = a.n_prefix, groups = np + a.n_req;
+  const int tid = threadIdx.x, np = a.n_prefix, groups = np + a.n_req;
   const bool tell = blockIdx.x == 0;
   const int cap = a.kv.max_blocks * a.kv.block_size, pcap = a.pre.max_blocks * a.kv.block_size;  // (fit 31 bits)
 #pragma unroll 1
@@ -302,46 +335,42 @@ __device__ __forceinline__ void derive_plan(const Args& ar, const Plan& plan, Cu
     }
     if (hi >= cap && hi >= len && tell) atomicOr(a.status, ST_UNMAPPED_PAGE);
   }
-  __syncthreads();
-  if (tid < 32) {
-    int W = 0;
+}
+
+// Lays the groups out in the line and finds the CTA's first item; by a whole warp.
+__device__ __forceinline__ Cursor cut_line(const Args& ar, Plan& plan) {
+  const int lane = threadIdx.x & 31, groups = ar.a.n_prefix + ar.a.n_req;
+  int W = 0;
 #pragma unroll 1
-    for (int g0 = 0; g0 < groups; g0 += 32) {
-      const int i = g0 + lane;
-      int u = 0;
-      if (i < groups) {
-        if (i >= np) plan.end[i] = min(plan.end[i], cap);
-        u = items_of(ar, plan, i).units(ar);
-      }
+  for (int g0 = 0; g0 < groups; g0 += 32) {
+    const int i = g0 + lane;
+    int u = i < groups ? items_of(ar, plan, i).units(ar) : 0;
 #pragma unroll 1
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, u, o);
-        if (lane >= o) u += y;
-      }
-      if (i < groups) plan.pre[i + 1] = W + u;
-      W += __shfl_sync(0xffffffffu, u, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, u, o);
+      if (lane >= o) u += y;
     }
-    __syncwarp();
-    if (lane == 0) {
-      plan.pre[0] = 0;
-      const Cut cut(W, gridDim.x);
-      Cursor c = {0, 0, 0, cut.size(blockIdx.x)};
-      if (c.left > 0) {
-        const int w0 = cut.start(blockIdx.x);
-        int hi = groups;  // the last group that starts by w0 (and is not empty: the next starts later)
-#pragma unroll 1
-        while (hi - c.g > 1) {
-          const int mid = (c.g + hi) >> 1;
-          if (plan.pre[mid] <= w0) c.g = mid; else hi = mid;
-        }
-        const Items it = items_of(ar, plan, c.g);
-        const int u = w0 - (c.g ? plan.pre[c.g] : 0);
-        c.item = min(u / it.len, it.whole(ar));
-        c.unit = u - c.item * it.len;
-      }
-      *start = c;
-    }
+    if (i < groups) plan.pre[i + 1] = W + u;
+    W += __shfl_sync(0xffffffffu, u, 31);
   }
+  if (lane == 0) plan.pre[0] = 0;
+  __syncwarp();
+  const Cut cut(W, gridDim.x);
+  Cursor c = {0, 0, 0, cut.size(blockIdx.x)};
+  if (c.left > 0) {
+    const int w0 = cut.start(blockIdx.x);
+    int hi = groups;  // the last group that starts by w0 (and is not empty: the next starts later)
+#pragma unroll 1
+    while (hi - c.g > 1) {
+      const int mid = (c.g + hi) >> 1;
+      if (plan.pre[mid] <= w0) c.g = mid; else hi = mid;
+    }
+    const Items it = items_of(ar, plan, c.g);
+    const int u = w0 - plan.pre[c.g];
+    c.item = min(u / it.len, it.whole(ar));
+    c.unit = u - c.item * it.len;
+  }
+  return c;
 }
 
 // The rows of an item's blocks, in row order, by a whole warp, and the smallest of their last tokens.
@@ -385,7 +414,7 @@ struct Loader {
     const int* table = v.table + (size_t)(g < np ? g : g - np) * v.max_blocks;
     t0 = job.token(i);
     lo = plan.first[g];
-    end = plan.end[g];
+    end = end_of(ar.a, plan, g);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (32 * q >= boxes) break;
@@ -446,19 +475,23 @@ struct Loader {
   }
 };
 
-// Columns of the warp's lanes times a factor each: f32 (O), or packed f16 (weights).
+// 16 rows times the lane's two rows' factors: f32 columns (O), or packed f16 (weights).
 template <bool HALVES>
-__device__ __forceinline__ void scale_columns(uint32_t at, int columns, float f) {
-  const uint32_t f2 = f16x2_of(f, f);
+__device__ __forceinline__ void scale_rows(uint32_t at, int columns, const float (&f)[2]) {
 #pragma unroll 1
   for (int c = 0; c < columns; c += 8) {
-    float x[8];
-    tc_ld8(at + c, x);
+    uint32_t x[4];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "r"(at + c));
     tc_wait_ld();
-    tc_loaded(x);
+    asm volatile("" : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = HALVES ? __uint_as_float(hmul2(__float_as_uint(x[e]), f2)) : x[e] * f;
-    tc_st8(at + c, x);
+    for (int e = 0; e < 4; ++e)
+      x[e] = HALVES ? hmul2(x[e], f16x2_of(f[e >> 1], f[e >> 1])) : __float_as_uint(__uint_as_float(x[e]) * f[e >> 1]);
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + c), "r"(x[0]), "r"(x[1]),
+                 "r"(x[2]), "r"(x[3])
+                 : "memory");
   }
   tc_wait_st();
 }
@@ -472,34 +505,26 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
   uint8_t* sm = smem_raw + (-smem_u32(smem_raw) & 1023);
   __shared__ __align__(16) Shared ss;
   volatile int* abort = &ss.abort;
-  Plan plan;
-  plan.pre = reinterpret_cast<int*>(sm + F::PLAN_OFF);
-  plan.end = plan.pre + MAX_GROUPS + 4;
-  plan.first = plan.end + MAX_GROUPS;
-  plan.len = plan.first + MAX_GROUPS;
-  plan.hi = plan.len + MAX_PREFIX;
-  plan.cnt = reinterpret_cast<short*>(plan.hi + MAX_ROWS);
-  plan.req = plan.cnt + MAX_GROUPS;
-  plan.pfx = plan.req + MAX_ROWS;
+  Plan& plan = *reinterpret_cast<Plan*>(sm + F::PLAN_OFF);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], WIDEN_WARPS);
     for (int s = 0; s < NS; ++s) mbar_init(&ss.v_full[s], WIDEN_WARPS), mbar_init(&ss.v_free[s], 2);
     for (int u = 0; u < 2; ++u) {
-      mbar_init(&ss.s_full[u], 2), mbar_init(&ss.p_full[u], 4), mbar_init(&ss.o_full[u], 1);
-      mbar_init(&ss.q_full[u], 4);
+      mbar_init(&ss.s_full[u], 2), mbar_init(&ss.p_full[u], STREAM_WARPS), mbar_init(&ss.o_full[u], 1);
+      mbar_init(&ss.q_full[u], STREAM_WARPS), mbar_init(&ss.o_out[u], STREAM_WARPS);
     }
     // an item is read by the softmax, widening, issuing and loading warps
-    for (int k = 0; k < JOBS; ++k) mbar_init(&ss.j_full[k], 1), mbar_init(&ss.j_free[k], SOFT / 32 + WIDEN_WARPS + 3);
-    mbar_init(&ss.merge, SOFT / 32);
+    for (int k = 0; k < JOBS; ++k) mbar_init(&ss.j_full[k], 1), mbar_init(&ss.j_free[k], SOFT_WARPS + WIDEN_WARPS + 3);
+    mbar_init(&ss.merge, SOFT_WARPS);
     mbar_init(&ss.drain, 2);
     ss.abort = 0;
     fence_mbar_init();
     if (ar.box) prefetch_tmap(&ar.codes), prefetch_tmap(&ar.scales);
   }
   if (warp == MMA_WARP) tmem_alloc<512>(&ss.tmem);
-  derive_plan(ar, plan, &ss.start);
+  derive_plan(ar, plan);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -524,7 +549,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
       // ------------------------------------------------------------- tiles from e4m3 to f16
       constexpr int PIECES = DH / 16, ROWS = 32 / PIECES, N = WIDEN_TOKENS / ROWS;  // of 16 codes; rows at a time
       const int t0 = WIDEN_TOKENS * (warp - WIDEN_WARP), piece = lane & (PIECES - 1), r0 = lane / PIECES;
-      const float to_log2 = a.scale * LOG2E;
+      const float to_log2 = a.scale * (LOG2E / Q_SCALE);
       const int odd = (piece >> 2) & 1;  // (such lanes store the other half first: no bank twice)
       int it = 0;
 #pragma unroll 1
@@ -541,9 +566,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
           uint4 v[N];
 #pragma unroll
           for (int e = 0; e < N; ++e) v[e] = lds128(sm + F::K_OFF + st * F::NARROW + (t0 + e * ROWS) * DH + lane * 16);
-          const float raw = lane < WIDEN_TOKENS
-                                ? *reinterpret_cast<const float*>(sm + F::SC_OFF + (st * TT + t0 + lane) * 16)
-                                : 0.0f;
+          const float raw = *reinterpret_cast<const float*>(sm + F::SC_OFF + (st * TT + t0 + lane) * 16);
           __syncwarp();
           if (lane == 0) mbar_arrive(&ss.k_free[st]);
           uint32_t nan = 0;
@@ -575,16 +598,16 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
             *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = x;
             *reinterpret_cast<uint4*>(dst + row * 128 + (((c ^ 1) ^ (row & 7)) << 4)) = y;
           }
-          if (lane < WIDEN_TOKENS) {  // a token a lane
-            const bool fin = ((ok >> ((t0 & 31) + lane)) & 1) && fabsf(raw) <= SCALE_MAX;
-            const float sc = fin ? raw : 0.0f;
-            float* tok = reinterpret_cast<float*>(sm + F::TOK_OFF) + s * 3 * TT + t0 + lane;
-            tok[0] = fin && !((nan >> lane) & 1) ? raw * to_log2 : __int_as_float(0x7FC00000);
-            tok[TT] = sc;
-            tok[2 * TT] = sc != 0.0f ? fmaxf(log2_of(fabsf(sc)), LEAST) : LEAST;
+          {  // a token a lane
+            static_assert(WIDEN_TOKENS == 32, "a token a lane");
+            const bool fin = ((ok >> lane) & 1) && fabsf(raw) <= SCALE_MAX && !((nan >> lane) & 1);
+            const float f = raw * to_log2;
+            reinterpret_cast<float*>(sm + F::TOK_OFF)[s * TT + token_slot(t0 + lane)] = fin ? f : __int_as_float(0x7FC00000);
+            const uint32_t most = __reduce_max_sync(0xffffffffu, fin ? __float_as_uint(fabsf(f)) : 0u);
+            if (lane == 0) ss.most[s][warp - WIDEN_WARP] = __uint_as_float(most);
           }
           if (lane == 0) {
-            if ((t0 & 31) == 0) ss.see[s][t0 >> 5] = ok;
+            ss.see[s][t0 >> 5] = ok;
             if (t0 == 0) ss.part[s] = part;
           }
           fence_proxy_async_shared();
@@ -599,7 +622,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
       constexpr uint32_t IS = (1u << 4) | ((uint32_t)(TT >> 3) << 17) | ((uint32_t)(BLOCK >> 4) << 24);
       constexpr uint32_t IO = (1u << 4) | (1u << 16) | ((uint32_t)(DH >> 3) << 17) | ((uint32_t)(BLOCK >> 4) << 24);
       const int u = warp - MMA_WARP;
-      const uint64_t q0 = desc_sw128(smem_u32(sm + F::Q_OFF) + u * F::WIDE), k0 = desc_sw128(smem_u32(sm + F::V_OFF)),
+      const uint64_t q0 = desc_sw128(smem_u32(sm + F::Q_OFF) + u * F::Q_BYTES), k0 = desc_sw128(smem_u32(sm + F::V_OFF)),
                      v0 = desc_mn(smem_u32(sm + F::V_OFF), HALF);
       const uint32_t sc = tmem + 128 * u, oc = tmem + F::O_COL + DH * u;
       int it = 0, seen = 0;  // the ring's tiles of the items before, and those that this warp has waited for
@@ -688,7 +711,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
       for (int k = max(0, it - ST); k < it; ++k) mbar_wait(&ss.full[k % ST], (k / ST) & 1, a.status);
     } else {
       // ------------------------------------------------------------------ the items and their rows
-      Cursor cur = ss.start;
+      Cursor cur = cut_line(ar, plan);
 #pragma unroll 1
       for (;; ++item) {
         const int k = item % JOBS;
@@ -729,157 +752,229 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
     }
   } else [&] {
     // ------------------------------------------------------------------------------- softmax
+    // A warp has 16 rows of its lane quadrant; of their scores and weights a lane has the rows lane / 4 and lane
+    // / 4 + 8, and a quarter of the tokens (token_slot).  (With a row a lane, the loads of the tokens' factors
+    // took as long as both products; with 32 rows a warp, its chain of latencies took twice as long.)
     regs_up<SOFT_REGS>();
-    const int u = warp >> 2, quad = warp & 3, q = 32 * quad + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16), s_at = lanes + 128 * u, o_at = lanes + F::O_COL + DH * u;
-    const int j_row = q / ar.hps, head = q - j_row * ar.hps;
+    const int u = warp / STREAM_WARPS, quad = warp & 3, half = (warp >> 2) & 1;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16), rows16 = (uint32_t)(16 * half) << 16;
+    const uint32_t s_at = lanes + 128 * u + rows16, o_at = lanes + F::O_COL + DH * u;
+    const int q16 = 32 * quad + 16 * half;  // the warp's first query of the block
     int it = 0;
     uint32_t sc = 0, mc = 0;  // the stream's tiles, and phases of the merging barrier, so far
 #pragma unroll 1
     while (const Job* at = next_item()) {
       const Job& job = *at;
       const int n = u ? job.n[1] : job.n[0], mode = job.mode;
-      const int row = j_row < ar.rows_per ? job.row[(mode == TWO_BLOCKS ? u * BLOCK : 0) + j_row] : -1;
-      const int hi = row >= 0 ? plan.hi[row] : -1;
+      // query q's row and head of the slice; and where its piece goes (null: there is no such query)
+      auto row_of = [&](int q, int& head) -> int {
+        const int j = q / ar.hps;
+        head = q - j * ar.hps;
+        return j < ar.rows_per ? job.row[(mode == TWO_BLOCKS ? u * BLOCK : 0) + j] : -1;
+      };
+      auto piece_of = [&](int q) -> float* {
+        int head;
+        const int row = row_of(q, head);
+        if (row < 0) return nullptr;
+        const size_t k = job.begins ? ((size_t)(job.g < a.n_prefix ? 0 : ar.max_rows) + row) * a.n_q +
+                                          job.slice_of(u) * ar.hps + head
+                                    : (size_t)blockIdx.x * (2 * BLOCK) + (mode == TWO_TILES ? 0 : u * BLOCK) + q;
+        return (job.begins ? ar.home : ar.over) + k * F::PART_LD;
+      };
+      int head;
+      const int row = row_of(q16 + (lane & 15), head), hi = row >= 0 ? plan.hi[row] : -1;
+      const bool idle = !__any_sync(0xffffffffu, row >= 0);  // no queries in this warp
       float factor = 1.0f;
-      {  // the query; most need no scaling, which is found out on the way
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + max(row, 0) * a.q_stride +
-                                                          (job.slice_of(u) * ar.hps + head) * DH);
-        uint8_t* dst = sm + F::Q_OFF + u * F::WIDE + q * 128;
-        float up = 1.0f;
-        bool again = false;
+      // the stream's warps have the last item's O out of the queries' place
+      if (item > 0 && !await(&ss.o_out[u], (item - 1) & 1, a.status, abort)) return;
+      {  // the warp's queries, 16 bytes a lane; most need no scaling, which is found out on the way
+        constexpr int PIECES = DH / 8, ROWS = 32 / PIECES, N = 16 / ROWS;  // lanes of a query; queries at a time
+        const int piece = lane & (PIECES - 1), r0 = lane / PIECES;
+        const long long from = row >= 0 ? row * a.q_stride + (job.slice_of(u) * ar.hps + head) * DH : -1;
+        uint8_t* dst = sm + F::Q_OFF + u * F::Q_BYTES + q16 * 128 + (piece >> 3) * HALF;
+        float up = Q_SCALE;
+        uint32_t most = 0;  // the largest element of query lane & 15, as bf16 bits (where it is needed)
 #pragma unroll 1
-        for (;;) {
-          uint32_t top = 0;  // the largest element, as bf16 bits
-#pragma unroll 1
-          for (int e0 = 0; e0 < DH / 8; e0 += 8) {
-            uint4 v[8];
+        for (int pass = 0; pass < 3; ++pass) {  // as they are; their largest elements; scaled
+          uint4 v[N];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = row >= 0 ? src[e0 + e] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float f[8];
-              bf16x8_to_f32(v[e], f);
-              top = max_u16x2(top, max_u16x2(max_u16x2(v[e].x & 0x7FFF7FFFu, v[e].y & 0x7FFF7FFFu),
-                                             max_u16x2(v[e].z & 0x7FFF7FFFu, v[e].w & 0x7FFF7FFFu)));
-#pragma unroll
-              for (int k = 0; k < 8; k += 2) mul2(f[k], f[k + 1], up);
-              *reinterpret_cast<uint4*>(dst + (e0 >> 3) * HALF + ((e ^ (q & 7)) << 4)) =
-                  make_uint4(f16x2_of(f[0], f[1]), f16x2_of(f[2], f[3]), f16x2_of(f[4], f[5]), f16x2_of(f[6], f[7]));
-            }
+          for (int e = 0; e < N; ++e) {
+            const long long at = __shfl_sync(0xffffffffu, from, e * ROWS + r0);
+            v[e] = at >= 0 ? *reinterpret_cast<const uint4*>(a.q + at + piece * 8) : make_uint4(0u, 0u, 0u, 0u);
           }
-          if (again) break;
-          top = max(top >> 16, top & 0xFFFFu);
-          // in f16's reach as it is: 2^-1 to 2^15
-          const bool far = top != 0 && (top < 0x3F00u || top >= 0x4700u);
-          again = __any_sync(0xffffffffu, far);
-          if (__builtin_expect(!again, 1)) break;
-          if (top >= 0x7F80u) {  // not finite: the query's weights are NaN
-            up = factor = __int_as_float(0x7FC00000);
-          } else if (far) {
-            // the largest element is in [2^(e - 127), 2^(e - 126)): to 2^4, or as near as an f32 goes
-            const int e = max((int)(top >> 7), 1), k = min(max(131 - e, -126), 126);
-            up = __uint_as_float((uint32_t)(127 + k) << 23);
-            factor = __uint_as_float((uint32_t)(127 - k) << 23);
+          uint32_t fine = 0, high = 0;  // a bit per query: its largest element is Q_LOW or more; some are Q_HIGH or more
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            uint32_t top = larger_bf16x2(larger_bf16x2(v[e].x, v[e].y), larger_bf16x2(v[e].z, v[e].w)) & 0x7FFF7FFFu;
+            top = max(top >> 16, top & 0xFFFFu);
+            if (__builtin_expect(pass == 1, 0)) {
+#pragma unroll
+              for (int x = PIECES / 2; x > 0; x >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+              top = __shfl_sync(0xffffffffu, top, (lane & (ROWS - 1)) * PIECES);
+              if ((lane & 15) / ROWS == e) most = top;
+              continue;
+            }
+            const uint32_t b = __ballot_sync(0xffffffffu, top >= Q_LOW);
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+              if ((b >> (r * PIECES)) & ((1u << PIECES) - 1)) fine |= 1u << (e * ROWS + r);
+            high = max(high, top);
+            float f[8], by = up;
+            if (__builtin_expect(pass == 2, 0)) by = __shfl_sync(0xffffffffu, up, e * ROWS + r0);
+            bf16x8_to_f32(v[e], f);
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) mul2(f[k], f[k + 1], by);
+            const int r = e * ROWS + r0;
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) =
+                make_uint4(f16x2_of(f[0], f[1]), f16x2_of(f[2], f[3]), f16x2_of(f[4], f[5]), f16x2_of(f[6], f[7]));
+          }
+          if (pass == 0 &&
+              !__any_sync(0xffffffffu, high >= Q_HIGH || (row >= 0 && !((fine >> (lane & 15)) & 1))))
+            break;
+          if (pass == 1) {
+            if (most >= 0x7F80u) {  // not finite: the query's weights are NaN
+              up = factor = __int_as_float(0x7FC00000);
+            } else if (most != 0 && (most < Q_LOW || most >= Q_HIGH)) {
+              // the largest element is in [2^(e - 127), 2^(e - 126)): to 2^4, or as near as an f32 goes
+              const int e = max((int)(most >> 7), 1), k = min(max(131 - e, -120), 126);
+              up = __uint_as_float((uint32_t)(127 + k) << 23);
+              factor = __uint_as_float((uint32_t)(127 - k) << 23) * Q_SCALE;
+            }
           }
         }
       }
       const bool scaled = __any_sync(0xffffffffu, factor != 1.0f);
-      const bool idle = !__any_sync(0xffffffffu, row >= 0);  // no queries in this warp
       fence_proxy_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ss.q_full[u]);
 
-      float m = UNSET, l0 = 0.0f, l1 = 0.0f;
+      float m[2] = {UNSET, UNSET}, l[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll 1
       for (int j = 0; j < n; ++j, ++sc) {
         const int i = job.ring(u, j), s = (it + i) % NS;
         if (!await(&ss.s_full[u], sc & 1, a.status, abort)) return;
         if (!idle) {
-          const float* tok = reinterpret_cast<const float*>(sm + F::TOK_OFF) + s * 3 * TT;
-          const bool part = ss.part[s];
           tc_fence_after();
-          // 32 tokens at a time: their weights times scales, as packed f16, take their scores' place
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t sees = 0xffffffffu;
-            if (__builtin_expect(part, 0)) {
-              const int k = hi - (job.token(i) + 32 * c) + 1;
-              sees = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1;
-              sees &= ss.see[s][c];
-            }
+          const bool part = ss.part[s];
+          const float4 most4 = *reinterpret_cast<const float4*>(ss.most[s]);
+          const float most = fmaxf(fmaxf(most4.x, most4.y), fmaxf(most4.z, most4.w));
+          const float4* tok = reinterpret_cast<const float4*>(sm + F::TOK_OFF) + s * TT / 4 + (lane & 3);
+          // 32 tokens at a time: their weights times a_t, as packed f16, take the place of scores that were read
+          auto chunk = [&](uint32_t(&raw)[16], int c) {
+            float* x = reinterpret_cast<float*>(raw);
+            auto scale = [&] {
+              if (__builtin_expect(scaled, 0)) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const float f = __shfl_sync(0xffffffffu, factor, (lane >> 2) + 8 * r);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) mul2(x[4 * k + 2 * r], x[4 * k + 2 * r + 1], f);
+                }
+              }
+            };
+            scale();
+            // the tokens that row r sees: bits 8 k and the next
+            auto sees = [&](int r) -> uint32_t {
+              const int t = __shfl_sync(0xffffffffu, hi, (lane >> 2) + 8 * r) - (job.token(i) + c) + 1;
+              return (ss.see[s][c >> 5] & (t >= 32 ? ~0u : t <= 0 ? 0u : (1u << t) - 1)) >> (2 * (lane & 3));
+            };
             bool moved = false, move = j == 0 && c == 0;
 #pragma unroll 1
             for (;;) {
-              uint32_t raw[32];
-              float* x = reinterpret_cast<float*>(raw);
-              tc_ld32(s_at + 32 * c, raw);
-              tc_wait_ld();
-              loaded32(raw);
-              if (__builtin_expect(scaled, 0)) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) mul2(x[e], x[e + 1], factor);
-              }
               if (__builtin_expect(move, 0)) {
-                // the reference to the largest of these weights times scales, and what was summed under the
-                // old one with it
-                float top = -INFINITY;
+                // the references to the largest of these weights times a_t, and what was summed under the old
+                // ones with them
+                float f[2];
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                  const float4 f = *reinterpret_cast<const float4*>(tok + 32 * c + e);
-                  const float4 g = *reinterpret_cast<const float4*>(tok + 2 * TT + 32 * c + e);
-                  const float y[4] = {fmaf(x[e], f.x, g.x), fmaf(x[e + 1], f.y, g.y), fmaf(x[e + 2], f.z, g.z),
-                                      fmaf(x[e + 3], f.w, g.w)};
+                for (int r = 0; r < 2; ++r) {
+                  const uint32_t w = part ? sees(r) : ~0u;
+                  float top = -INFINITY;
 #pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    if ((sees >> (e + k)) & 1) top = fmaxf(top, y[k]);
+                  for (int k = 0; k < 4; ++k) {
+                    const float2 t = reinterpret_cast<const float2*>(tok + c / 4 + (k >> 1) * 4)[k & 1];
+                    const float y0 = fmaf(x[4 * k + 2 * r], t.x, fmaxf(log2_of(fabsf(t.x)), LEAST));
+                    const float y1 = fmaf(x[4 * k + 2 * r + 1], t.y, fmaxf(log2_of(fabsf(t.y)), LEAST));
+                    if ((w >> (8 * k)) & 1) top = fmaxf(top, y0);
+                    if ((w >> (8 * k)) & 2) top = fmaxf(top, y1);
+                  }
+                  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                  f[r] = 1.0f;
+                  if (top - m[r] > BASE) {
+                    const float now = fabsf(top) <= SCORE_MAX ? ceilf(top) - BASE : __int_as_float(0x7FC00000);
+                    f[r] = m[r] == UNSET ? 0.0f : ex2(m[r] - now);
+                    m[r] = now;
+                  }
+                  l[r][0] *= f[r];
+                  l[r][1] *= f[r];
                 }
-                float f = 1.0f;
-                if (top - m > BASE) {
-                  const float now = fabsf(top) <= SCORE_MAX ? ceilf(top) - BASE : __int_as_float(0x7FC00000);
-                  f = m == UNSET ? 0.0f : ex2(m - now);
-                  m = now;
-                }
-                l0 *= f;
-                l1 *= f;
-                if (j > 0) scale_columns<false>(o_at, DH, f);
+                if (j > 0) scale_rows<false>(o_at + rows16, DH, f);
                 tc_wait_st();
-                if (c > 0) scale_columns<true>(s_at, 16 * c, f);
+                if (c > 0) scale_rows<true>(s_at, c / 2, f);
                 moved = true;
               }
+              // (in passes over all of them: a branch a pair would cost more than what it skips)
+              float2 t[4];
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(tok + 32 * c + e);
-                fma2t(x[e], x[e + 1], f.x, f.y, -m);
-                fma2t(x[e + 2], x[e + 3], f.z, f.w, -m);
+              for (int k = 0; k < 4; k += 2) {
+                const float4 v = tok[c / 4 + 2 * k];
+                t[k] = make_float2(v.x, v.y), t[k + 1] = make_float2(v.z, v.w);
               }
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) fma2t(x[e], x[e + 1], t[e >> 2].x, t[e >> 2].y, -m[(e >> 1) & 1]);
               if (__builtin_expect(part, 0)) {
+                const uint32_t w[2] = {sees(0), sees(1)};
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((sees >> e) & 1)) x[e] = -INFINITY;
+                for (int e = 0; e < 16; ++e)
+                  if (!((w[(e >> 1) & 1] >> (8 * (e >> 2) + (e & 1))) & 1)) x[e] = -INFINITY;
               }
-              float k0 = 0.0f, k1 = 0.0f;
-              uint32_t p[16], top = 0;
+              float sum[2][2];
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 g = *reinterpret_cast<const float4*>(tok + TT + 32 * c + e);
-                float p0 = ex2(x[e]), p1 = ex2(x[e + 1]), p2 = ex2(x[e + 2]), p3 = ex2(x[e + 3]);
-                add2(k0, k1, p0, p1);
-                add2(k0, k1, p2, p3);
-                mul2(p0, p1, g.x, g.y);
-                mul2(p2, p3, g.z, g.w);
-                p[e / 2] = f16x2_of(p0, p1);
-                p[e / 2 + 1] = f16x2_of(p2, p3);
-                top = max_u16x2(top, max_u16x2(p[e / 2], p[e / 2 + 1]));
+              for (int e = 0; e < 16; e += 2) {
+                const int r = (e >> 1) & 1;
+                x[e] = ex2(x[e]), x[e + 1] = ex2(x[e + 1]);
+                if (e < 4) sum[r][0] = x[e], sum[r][1] = x[e + 1];
+                else add2(sum[r][0], sum[r][1], x[e], x[e + 1]);
+                mul2(x[e], x[e + 1], t[e >> 2].x, t[e >> 2].y);
               }
-              if (!moved) {
-                move = __any_sync(0xffffffffu, (top & 0xFFFFu) > TOO_LARGE || (top >> 16) > TOO_LARGE);
-                if (__builtin_expect(move, 0)) continue;
+              if (!moved) {  // (no weight is above its sum; infinity times 0 asks, too)
+                move = __any_sync(0xffffffffu, !(fmaxf(fmaxf(sum[0][0], sum[0][1]), fmaxf(sum[1][0], sum[1][1])) *
+                                                     most <= TOO_LARGE));
+                if (__builtin_expect(move, 0)) {
+                  ld_rows(s_at + c, raw);
+                  tc_wait_ld();
+                  loaded16(raw);
+                  scale();
+                  continue;
+                }
               }
-              add2(l0, l1, k0, k1);
-              st16(s_at + 16 * c, p);
+              if (__builtin_expect(part, 0)) {  // (a factor may be NaN)
+                const uint32_t w[2] = {sees(0), sees(1)};
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (!((w[(e >> 1) & 1] >> (8 * (e >> 2) + (e & 1))) & 1)) x[e] = 0.0f;
+              }
+              uint32_t p[8];
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) p[e / 2] = f16x2_of(x[e], x[e + 1]);
+              st_rows(s_at + c / 2, p);
+#pragma unroll
+              for (int r = 0; r < 2; ++r) add2(l[r][0], l[r][1], sum[r][0], sum[r][1]);
               break;
             }
+          };
+          uint32_t even[16], odd[16];
+          ld_rows(s_at, even);
+#pragma unroll 1
+          for (int c = 0; c < TT; c += 64) {  // (a chunk's scores are fetched while the one before is in hand)
+            tc_wait_ld();
+            loaded16(even);
+            ld_rows(s_at + c + 32, odd);
+            chunk(even, c);
+            tc_wait_ld();
+            loaded16(odd);
+            if (c == 0) ld_rows(s_at + 64, even);
+            chunk(odd, c + 32);
           }
           tc_wait_st();
           tc_fence_before();
@@ -891,47 +986,61 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
       tc_fence_after();
       it += job.count();
 
-      // ---- the piece: where it goes, then O
-      float* to = nullptr;
-      if (row >= 0) {
-        const int kind = job.g < a.n_prefix ? 0 : 1;
-        const size_t k = job.begins
-                             ? ((size_t)kind * ar.max_rows + row) * a.n_q + job.slice_of(u) * ar.hps + head
-                             : (size_t)blockIdx.x * (2 * BLOCK) + (mode == TWO_TILES ? 0 : u * BLOCK) + q;
-        to = (job.begins ? ar.home : ar.over) + k * F::PART_LD;
-      }
-      float l = l0 + l1;
-      if (mode != TWO_TILES) {
-        if (!idle) {
-          if (to) *reinterpret_cast<float2*>(to) = make_float2(m, l);
-#pragma unroll 1
-          for (int c = 0; c < DH; c += 32) {
-            uint32_t o[32];
-            tc_ld32(o_at + c, o);
-            tc_wait_ld();
-            loaded32(o);
-            if (to)
+      // ---- the piece: the references and sums of the rows, a lane each; then O
+      float m_row = UNSET, l_row = 0.0f;
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) st_global8(to + 8 + c + e, o + e);
+      for (int r = 0; r < 2; ++r) {
+        float t = l[r][0] + l[r][1];
+        t += __shfl_xor_sync(0xffffffffu, t, 1);
+        t += __shfl_xor_sync(0xffffffffu, t, 2);
+        const float from = __shfl_sync(0xffffffffu, m[r], (lane & 7) * 4);
+        t = __shfl_sync(0xffffffffu, t, (lane & 7) * 4);
+        if (((lane >> 3) & 1) == r) m_row = from, l_row = t;
+      }
+      const int q = 32 * quad + lane;  // of the quadrant's queries
+      if (mode != TWO_TILES) {
+        if (lane < 16 && row >= 0) *reinterpret_cast<float2*>(piece_of(q16 + lane)) = make_float2(m_row, l_row);
+        float* to = half == 0 ? piece_of(q) : nullptr;
+        if (__any_sync(0xffffffffu, to != nullptr)) {
+          // (a thread's row by a copy of its own: stored from registers, a row apart, they took 4500 cycles)
+          uint8_t* out = sm + F::Q_OFF + u * F::Q_BYTES + q * F::O_LD;
+#pragma unroll 1
+          for (int c = 0; c < DH; c += DH / 2) {
+            if (c > 0) bulk_wait_read();
+#pragma unroll
+            for (int d = 0; d < DH / 2; d += 32) {
+              uint32_t o[32];
+              tc_ld32(o_at + c + d, o);
+              tc_wait_ld();
+              loaded32(o);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<uint4*>(out + 4 * (d + e)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+            fence_proxy_async_shared();
+            if (to) bulk_store(to + 8 + c, out, 2 * DH), bulk_commit();
           }
+          bulk_wait_read();
         }
-      } else {  // both streams' O in the larger m, half of the dimensions each
+      } else {  // both streams' O in the larger m, a quarter of the dimensions a warp
         auto meet = [&] {
           __syncwarp();
           if (lane == 0) mbar_arrive(&ss.merge);
           return await(&ss.merge, mc++ & 1, a.status, abort);
         };
-        ss.ml[u][q] = make_float2(m, l);
+        if (lane < 16) ss.ml[u][q16 + lane] = make_float2(m_row, l_row);
         if (!meet()) return;
+        float* to = piece_of(q);
         const float2 x = ss.ml[0][q], y = ss.ml[1][q];
-        m = fmaxf(x.x, y.x);
+        m_row = fmaxf(x.x, y.x);
         // (a NaN stays one)
-        const float fx = x.y != x.y ? 1.0f : x.x == UNSET ? 0.0f : ex2(x.x - m);
-        const float fy = y.y != y.y ? 1.0f : y.x == UNSET ? 0.0f : ex2(y.x - m);
-        l = (fx != 0.0f ? x.y * fx : 0.0f) + (fy != 0.0f ? y.y * fy : 0.0f);
-        if (to && u == 0) *reinterpret_cast<float2*>(to) = make_float2(m, l);
+        const float fx = x.y != x.y ? 1.0f : x.x == UNSET ? 0.0f : ex2(x.x - m_row);
+        const float fy = y.y != y.y ? 1.0f : y.x == UNSET ? 0.0f : ex2(y.x - m_row);
+        l_row = (fx != 0.0f ? x.y * fx : 0.0f) + (fy != 0.0f ? y.y * fy : 0.0f);
+        if (to && u == 0 && half == 0) *reinterpret_cast<float2*>(to) = make_float2(m_row, l_row);
+        const int first = (2 * u + half) * (DH / 4);
 #pragma unroll 1
-        for (int c = u * (DH / 2); c < (u + 1) * (DH / 2); c += 8) {
+        for (int c = first; c < first + DH / 4; c += 8) {
           float v[8], z[8];
           tc_ld8(lanes + F::O_COL + c, v);
           tc_ld8(lanes + F::O_COL + DH + c, z);
@@ -951,9 +1060,12 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
         tc_fence_after();
       }
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ss.o_out[u]);
       item_done();
     }
   }();
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // (a softmax thread's rows)
   tc_fence_before();
   __syncthreads();
   if (warp == MMA_WARP) {
@@ -1039,7 +1151,8 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_shared_kernel(const __gr
     num.x += __shfl_xor_sync(0xffffffffu, num.x, 16), num.y += __shfl_xor_sync(0xffffffffu, num.y, 16);
     num.z += __shfl_xor_sync(0xffffffffu, num.z, 16), num.w += __shfl_xor_sync(0xffffffffu, num.w, 16);
   }
-  const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+  // (O was summed with a_t in the scales' place)
+  const float inv = den == 0.0f ? 0.0f : 1.0f / (den * (a.scale * (LOG2E / Q_SCALE)));
   if (den == 0.0f) num = {0.0f, 0.0f, 0.0f, 0.0f};
   *reinterpret_cast<uint2*>(a.o + r * a.o_stride + (long long)h * dh + d) =
       make_uint2(pack_bf16x2(num.x * inv, num.y * inv), pack_bf16x2(num.z * inv, num.w * inv));

@@ -18,10 +18,10 @@ def model(items, NS, ST, seed, gives_back=True, widen=2, quads=2):
     m = Machine(seed)
     full, k_free = [Bar(2) for _ in range(ST)], [Bar(widen) for _ in range(ST)]
     v_full, v_free = [Bar(widen) for _ in range(NS)], [Bar(2) for _ in range(NS)]
-    s_full, p_full, o_full, q_full = ([Bar(c) for _ in range(2)] for c in (2, quads, 1, quads))
+    s_full, p_full, o_full, q_full, o_out = ([Bar(c) for _ in range(2)] for c in (2, quads, 1, quads, quads))
     j_full, j_free = [Bar(1) for _ in range(JOBS)], [Bar(2 * quads + widen + 3) for _ in range(JOBS)]
     merge = Bar(2 * quads)
-    narrow, wide = [None] * ST, [None] * NS
+    narrow, wide, out = [None] * ST, [None] * NS, [0, 0]
 
     def count(mode, n):
         return n[0] if mode == TWO_BLOCKS else n[0] + n[1]
@@ -135,6 +135,9 @@ def model(items, NS, ST, seed, gives_back=True, widen=2, quads=2):
         at, sc, mc = [0], [0], [0]
 
         def role(item, mode, n):
+            if item:
+                yield "wait", o_out[u], item - 1
+            assert not out[u], "queries where O is on its way out"
             q_full[u].arrive()
             yield 0
             for j in range(n[u]):
@@ -145,12 +148,17 @@ def model(items, NS, ST, seed, gives_back=True, widen=2, quads=2):
                 p_full[u].arrive()
                 yield 0
             yield "wait", o_full[u], item
+            out[u] += 1
+            yield 0
+            out[u] -= 1
             at[0] += count(mode, n)
             if mode == TWO_TILES:
                 for _ in range(2):
                     merge.arrive()
                     yield "wait", merge, mc[0]
                     mc[0] += 1
+            o_out[u].arrive()
+            yield 0
         yield from jobs(role)
 
     m.add(rows())
