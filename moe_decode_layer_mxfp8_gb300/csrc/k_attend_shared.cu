@@ -18,8 +18,8 @@
 // tiles, of two slices of one block, or (where a slice is left alone) of every other tile.  What a CTA has of an item leaves (O, m, l)
 // in the workspace; a second kernel joins them.
 //
-// Roles: warps 0-7 and 8-15 softmax; 16-19 widen tiles; 20 and 21 issue a stream's MMAs each; 22 loads; 23
-// makes the items and their rows, and tells the join where pieces are.
+// Roles: warps 0-7 and 8-15 softmax; 16-19 widen tiles; 20 issues MMAs; 21 loads; 22 makes the items and their
+// rows, and tells the join where pieces are (23 makes the registers' split come out).
 // Every wait is for an mbarrier, and bounded; one that runs out is reported and ends its role, and with it
 // the others' waits.  Copies and products on their way are waited for before the CTA ends.
 #include "attend_tc.cuh"
@@ -31,8 +31,8 @@ using namespace tc;
 using namespace attend;
 
 constexpr int SOFT_WARPS = 16, STREAM_WARPS = SOFT_WARPS / 2, WIDEN_WARPS = 4, WIDEN_TOKENS = TT / WIDEN_WARPS;
-constexpr int WIDEN_WARP = SOFT_WARPS, MMA_WARP = WIDEN_WARP + WIDEN_WARPS, LOAD_WARP = MMA_WARP + 2, ROWS_WARP = LOAD_WARP + 1;
-constexpr int THREADS = 32 * (ROWS_WARP + 1), SOFT = 32 * WIDEN_WARP;
+constexpr int WIDEN_WARP = SOFT_WARPS, MMA_WARP = WIDEN_WARP + WIDEN_WARPS, LOAD_WARP = MMA_WARP + 1, ROWS_WARP = LOAD_WARP + 1;
+constexpr int THREADS = 32 * (ROWS_WARP + 2), SOFT = 32 * WIDEN_WARP;
 constexpr int MAX_GROUPS = MAX_PREFIX + MAX_REQ;
 constexpr int BLOCK = 128;       // queries
 constexpr int EXTRA = 3;         // what an item costs a CTA beside its steps, in steps
@@ -178,7 +178,7 @@ struct Shared {
   uint32_t valid[4][4];                // tokens that are there, of a narrow tile
   alignas(16) uint32_t see[5][4];      // and of a wide one
   int part[5];                         // not every row of the item sees all its tokens
-  alignas(16) float most[5][WIDEN_WARPS];  // its largest |a_t|, of a warp's tokens each
+  alignas(16) float most[5][WIDEN_WARPS];  // its largest |a_t| (NaN: one is), of a warp's tokens each
   Job job[JOBS];
   float2 ml[2][BLOCK];
   uint32_t tmem;
@@ -475,22 +475,20 @@ struct Loader {
   }
 };
 
-// 16 rows times the lane's two rows' factors: f32 columns (O), or packed f16 (weights).
-template <bool HALVES>
+// O of 16 rows times the lane's two rows' factors.
 __device__ __forceinline__ void scale_rows(uint32_t at, int columns, const float (&f)[2]) {
 #pragma unroll 1
   for (int c = 0; c < columns; c += 8) {
-    uint32_t x[4];
+    float x[4];
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
                  : "r"(at + c));
     tc_wait_ld();
-    asm volatile("" : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]));
+    tc_loaded4(x);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      x[e] = HALVES ? hmul2(x[e], f16x2_of(f[e >> 1], f[e >> 1])) : __float_as_uint(__uint_as_float(x[e]) * f[e >> 1]);
-    asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + c), "r"(x[0]), "r"(x[1]),
-                 "r"(x[2]), "r"(x[3])
+    for (int e = 0; e < 4; ++e) x[e] *= f[e >> 1];
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1,%2,%3,%4};" ::"r"(at + c), "f"(x[0]), "f"(x[1]),
+                 "f"(x[2]), "f"(x[3])
                  : "memory");
   }
   tc_wait_st();
@@ -510,15 +508,15 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
 
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], WIDEN_WARPS);
-    for (int s = 0; s < NS; ++s) mbar_init(&ss.v_full[s], WIDEN_WARPS), mbar_init(&ss.v_free[s], 2);
+    for (int s = 0; s < NS; ++s) mbar_init(&ss.v_full[s], WIDEN_WARPS), mbar_init(&ss.v_free[s], 1);
     for (int u = 0; u < 2; ++u) {
       mbar_init(&ss.s_full[u], 2), mbar_init(&ss.p_full[u], STREAM_WARPS), mbar_init(&ss.o_full[u], 1);
       mbar_init(&ss.q_full[u], STREAM_WARPS), mbar_init(&ss.o_out[u], STREAM_WARPS);
     }
     // an item is read by the softmax, widening, issuing and loading warps
-    for (int k = 0; k < JOBS; ++k) mbar_init(&ss.j_full[k], 1), mbar_init(&ss.j_free[k], SOFT_WARPS + WIDEN_WARPS + 3);
+    for (int k = 0; k < JOBS; ++k) mbar_init(&ss.j_full[k], 1), mbar_init(&ss.j_free[k], SOFT_WARPS + WIDEN_WARPS + 2);
     mbar_init(&ss.merge, SOFT_WARPS);
-    mbar_init(&ss.drain, 2);
+    mbar_init(&ss.drain, 1);
     ss.abort = 0;
     fence_mbar_init();
     if (ar.box) prefetch_tmap(&ar.codes), prefetch_tmap(&ar.scales);
@@ -600,10 +598,10 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
           }
           {  // a token a lane
             static_assert(WIDEN_TOKENS == 32, "a token a lane");
-            const bool fin = ((ok >> lane) & 1) && fabsf(raw) <= SCALE_MAX && !((nan >> lane) & 1);
-            const float f = raw * to_log2;
-            reinterpret_cast<float*>(sm + F::TOK_OFF)[s * TT + token_slot(t0 + lane)] = fin ? f : __int_as_float(0x7FC00000);
-            const uint32_t most = __reduce_max_sync(0xffffffffu, fin ? __float_as_uint(fabsf(f)) : 0u);
+            const bool there = (ok >> lane) & 1, fin = fabsf(raw) <= SCALE_MAX && !((nan >> lane) & 1);
+            const float f = !there ? 0.0f : fin ? raw * to_log2 : __int_as_float(0x7FC00000);
+            reinterpret_cast<float*>(sm + F::TOK_OFF)[s * TT + token_slot(t0 + lane)] = f;
+            const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(f)));  // (a NaN stays one)
             if (lane == 0) ss.most[s][warp - WIDEN_WARP] = __uint_as_float(most);
           }
           if (lane == 0) {
@@ -617,67 +615,66 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
         item_done();
       }
     }();
-    else if (warp < LOAD_WARP) {
-      // --------------------------------------------------------------- MMAs, a warp per stream
+    else if (warp == MMA_WARP) {
+      // ------------------------------------------- MMAs: a stream's second product, then its next first one, in
+      // turns, so that one stream's run while the other's softmax does.  (Issued by a warp per stream they
+      // mixed, both streams' scores came at once, and MMAs and softmax took turns.)
       constexpr uint32_t IS = (1u << 4) | ((uint32_t)(TT >> 3) << 17) | ((uint32_t)(BLOCK >> 4) << 24);
       constexpr uint32_t IO = (1u << 4) | (1u << 16) | ((uint32_t)(DH >> 3) << 17) | ((uint32_t)(BLOCK >> 4) << 24);
-      const int u = warp - MMA_WARP;
-      const uint64_t q0 = desc_sw128(smem_u32(sm + F::Q_OFF) + u * F::Q_BYTES), k0 = desc_sw128(smem_u32(sm + F::V_OFF)),
+      const uint64_t q0 = desc_sw128(smem_u32(sm + F::Q_OFF)), k0 = desc_sw128(smem_u32(sm + F::V_OFF)),
                      v0 = desc_mn(smem_u32(sm + F::V_OFF), HALF);
-      const uint32_t sc = tmem + 128 * u, oc = tmem + F::O_COL + DH * u;
-      int it = 0, seen = 0;  // the ring's tiles of the items before, and those that this warp has waited for
-      uint32_t pc = 0;       // the stream's tiles so far
-      // Waits for the ring's tiles up to i, the other stream's too, and gives those back: a wait is by
-      // parity, so none may be missed, and no slot may go two tiles further before this warp has seen it.
-      auto see = [&](const Job& job, int i) {
-        bool ok = true;
-#pragma unroll 1
-        for (; ok && seen <= i; ++seen) {
-          ok = await(&ss.v_full[seen % NS], (seen / NS) & 1, a.status, abort);
-          if (job.mode != TWO_BLOCKS && ((seen - it) & 1) != u && lane == 0) mbar_arrive(&ss.v_free[seen % NS]);
-        }
-        return ok;
-      };
+      int it = 0;              // the ring's tiles of the items before
+      uint32_t pc[2] = {0, 0};  // the streams' tiles so far
       bool ok = true;
 #pragma unroll 1
       while (ok) {
         const Job* job = next_item();
         if (!job) break;
-        const int n = u ? job->n[1] : job->n[0];
-        auto scores = [&](int j) {
+        auto scores = [&](int u, int j) {
           const int i = it + job->ring(u, j);
-          ok = see(*job, i);
+          ok = await(&ss.v_full[i % NS], (i / NS) & 1, a.status, abort);
           if (ok && elect_one()) {
             tc_fence_after();
-            const uint64_t kd = k0 + (i % NS) * (F::WIDE / 16);
+            const uint64_t qd = q0 + u * (F::Q_BYTES / 16), kd = k0 + (i % NS) * (F::WIDE / 16);
 #pragma unroll
             for (int k = 0; k < DH / 16; ++k)
-              mma_ss(sc, q0 + (k >> 2) * (HALF / 16) + 2 * (k & 3), kd + (k >> 2) * (HALF / 16) + 2 * (k & 3), IS, k > 0);
+              mma_ss(tmem + 128 * u, qd + (k >> 2) * (HALF / 16) + 2 * (k & 3), kd + (k >> 2) * (HALF / 16) + 2 * (k & 3),
+                     IS, k > 0);
             tc_commit(&ss.s_full[u]);
             // (the commit is no release: this arrival passes on what the widening warps wrote)
             mbar_arrive(&ss.s_full[u]);
           }
           __syncwarp();
         };
-        ok = await(&ss.q_full[u], item & 1, a.status, abort);
-        if (ok && n > 0) scores(0);
-        else if (lane == 0) mbar_arrive(&ss.o_full[u]);
 #pragma unroll 1
-        for (int j = 0; ok && j < n; ++j, ++pc) {
-          const int s = (it + job->ring(u, j)) % NS;
-          ok = await(&ss.p_full[u], pc & 1, a.status, abort);
-          if (ok && elect_one()) {
-            tc_fence_after();
-            const uint64_t vd = v0 + s * (F::WIDE / 16);
-#pragma unroll
-            for (int k = 0; k < TT / 16; ++k) mma_ts(oc, sc + 8 * k, vd + k * (2048 / 16), IO, j > 0 || k > 0);
-            tc_commit(&ss.v_free[s]);
-            if (j + 1 == n) tc_commit(&ss.o_full[u]);
-          }
+        for (int u = 0; ok && u < 2; ++u) {
+          ok = await(&ss.q_full[u], item & 1, a.status, abort);
+          if (ok && (u ? job->n[1] : job->n[0]) > 0) scores(u, 0);
+          else if (lane == 0) mbar_arrive(&ss.o_full[u]);
           __syncwarp();
-          if (ok && j + 1 < n) scores(j + 1);
         }
-        ok = ok && see(*job, it + job->count() - 1);
+#pragma unroll 1
+        for (int j = 0; ok && j < job->n[0]; ++j) {
+#pragma unroll 1
+          for (int u = 0; ok && u < 2; ++u) {
+            const int n = u ? job->n[1] : job->n[0];
+            if (j >= n) break;
+            const int s = (it + job->ring(u, j)) % NS;
+            ok = await(&ss.p_full[u], (u ? pc[1] : pc[0]) & 1, a.status, abort);
+            if (u) ++pc[1]; else ++pc[0];
+            if (ok && elect_one()) {
+              tc_fence_after();
+              const uint32_t oc = tmem + F::O_COL + DH * u, pcol = tmem + 128 * u;
+              const uint64_t vd = v0 + s * (F::WIDE / 16);
+#pragma unroll
+              for (int k = 0; k < TT / 16; ++k) mma_ts(oc, pcol + 8 * k, vd + k * (2048 / 16), IO, j > 0 || k > 0);
+              if (job->mode != TWO_BLOCKS || u == 1) tc_commit(&ss.v_free[s]);
+              if (j + 1 == n) tc_commit(&ss.o_full[u]);
+            }
+            __syncwarp();
+            if (ok && j + 1 < n) scores(u, j + 1);
+          }
+        }
         it += job->count();
         item_done();
       }
@@ -709,7 +706,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
       // (what is on its way lands in this CTA's shared memory)
 #pragma unroll 1
       for (int k = max(0, it - ST); k < it; ++k) mbar_wait(&ss.full[k % ST], (k / ST) & 1, a.status);
-    } else {
+    } else if (warp == ROWS_WARP) {
       // ------------------------------------------------------------------ the items and their rows
       Cursor cur = cut_line(ar, plan);
 #pragma unroll 1
@@ -858,124 +855,121 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
           const bool part = ss.part[s];
           const float4 most4 = *reinterpret_cast<const float4*>(ss.most[s]);
           const float most = fmaxf(fmaxf(most4.x, most4.y), fmaxf(most4.z, most4.w));
+          const bool bad = part && isnan((most4.x + most4.y) + (most4.z + most4.w));  // some factor is NaN
           const float4* tok = reinterpret_cast<const float4*>(sm + F::TOK_OFF) + s * TT / 4 + (lane & 3);
-          // 32 tokens at a time: their weights times a_t, as packed f16, take the place of scores that were read
-          auto chunk = [&](uint32_t(&raw)[16], int c) {
-            float* x = reinterpret_cast<float*>(raw);
-            auto scale = [&] {
-              if (__builtin_expect(scaled, 0)) {
+          auto scale = [&](float* x) {
+            if (__builtin_expect(scaled, 0)) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                  const float f = __shfl_sync(0xffffffffu, factor, (lane >> 2) + 8 * r);
+              for (int r = 0; r < 2; ++r) {
+                const float f = __shfl_sync(0xffffffffu, factor, (lane >> 2) + 8 * r);
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) mul2(x[4 * k + 2 * r], x[4 * k + 2 * r + 1], f);
-                }
+                for (int k = 0; k < 4; ++k) mul2(x[4 * k + 2 * r], x[4 * k + 2 * r + 1], f);
               }
-            };
-            scale();
-            // the tokens that row r sees: bits 8 k and the next
-            auto sees = [&](int r) -> uint32_t {
-              const int t = __shfl_sync(0xffffffffu, hi, (lane >> 2) + 8 * r) - (job.token(i) + c) + 1;
-              return (ss.see[s][c >> 5] & (t >= 32 ? ~0u : t <= 0 ? 0u : (1u << t) - 1)) >> (2 * (lane & 3));
-            };
-            bool moved = false, move = j == 0 && c == 0;
+            }
+          };
+          // of tokens 32 c on, those that row r sees: bits 8 k and the next
+          auto sees = [&](int r, int c) -> uint32_t {
+            const int t = __shfl_sync(0xffffffffu, hi, (lane >> 2) + 8 * r) - (job.token(i) + 32 * c) + 1;
+            return (ss.see[s][c] & (t >= 32 ? ~0u : t <= 0 ? 0u : (1u << t) - 1)) >> (2 * (lane & 3));
+          };
+          uint32_t p[4][8];  // weights times a_t, packed f16
+          float sum[2][2];
+          bool moved = false, move = j == 0;
 #pragma unroll 1
-            for (;;) {
-              if (__builtin_expect(move, 0)) {
-                // the references to the largest of these weights times a_t, and what was summed under the old
-                // ones with them
-                float f[2];
+          for (;;) {
+            if (__builtin_expect(move, 0)) {
+              // the references to the largest of the tile's weights times a_t, and what was summed under the old
+              // ones with them
+              float top[2] = {-INFINITY, -INFINITY}, f[2];
+#pragma unroll 1
+              for (int c = 0; c < 4; ++c) {
+                uint32_t raw[16];
+                float* x = reinterpret_cast<float*>(raw);
+                ld_rows(s_at + 32 * c, raw);
+                tc_wait_ld();
+                loaded16(raw);
+                scale(x);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                  const uint32_t w = part ? sees(r) : ~0u;
-                  float top = -INFINITY;
+                  const uint32_t w = part ? sees(r, c) : ~0u;
 #pragma unroll
                   for (int k = 0; k < 4; ++k) {
-                    const float2 t = reinterpret_cast<const float2*>(tok + c / 4 + (k >> 1) * 4)[k & 1];
+                    const float2 t = reinterpret_cast<const float2*>(tok + 8 * c + (k >> 1) * 4)[k & 1];
                     const float y0 = fmaf(x[4 * k + 2 * r], t.x, fmaxf(log2_of(fabsf(t.x)), LEAST));
                     const float y1 = fmaf(x[4 * k + 2 * r + 1], t.y, fmaxf(log2_of(fabsf(t.y)), LEAST));
-                    if ((w >> (8 * k)) & 1) top = fmaxf(top, y0);
-                    if ((w >> (8 * k)) & 2) top = fmaxf(top, y1);
+                    if ((w >> (8 * k)) & 1) top[r] = fmaxf(top[r], y0);
+                    if ((w >> (8 * k)) & 2) top[r] = fmaxf(top[r], y1);
                   }
-                  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                  f[r] = 1.0f;
-                  if (top - m[r] > BASE) {
-                    const float now = fabsf(top) <= SCORE_MAX ? ceilf(top) - BASE : __int_as_float(0x7FC00000);
-                    f[r] = m[r] == UNSET ? 0.0f : ex2(m[r] - now);
-                    m[r] = now;
-                  }
-                  l[r][0] *= f[r];
-                  l[r][1] *= f[r];
                 }
-                if (j > 0) scale_rows<false>(o_at + rows16, DH, f);
-                tc_wait_st();
-                if (c > 0) scale_rows<true>(s_at, c / 2, f);
-                moved = true;
               }
-              // (in passes over all of them: a branch a pair would cost more than what it skips)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+                f[r] = 1.0f;
+                if (top[r] - m[r] > BASE) {
+                  const float now = fabsf(top[r]) <= SCORE_MAX ? ceilf(top[r]) - BASE : __int_as_float(0x7FC00000);
+                  f[r] = m[r] == UNSET ? 0.0f : ex2(m[r] - now);
+                  m[r] = now;
+                }
+                l[r][0] *= f[r];
+                l[r][1] *= f[r];
+              }
+              if (j > 0) scale_rows(o_at + rows16, DH, f);
+              moved = true;
+            }
+            // 32 tokens at a time, in passes over all of them (a branch a pair would cost more than what it skips);
+            // the next ones' scores are fetched meanwhile
+            uint32_t raw[2][16];
+            ld_rows(s_at, raw[0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              float* x = reinterpret_cast<float*>(raw[c & 1]);
+              tc_wait_ld();
+              loaded16(raw[c & 1]);
+              if (c < 3) ld_rows(s_at + 32 * (c + 1), raw[(c + 1) & 1]);
+              scale(x);
               float2 t[4];
 #pragma unroll
               for (int k = 0; k < 4; k += 2) {
-                const float4 v = tok[c / 4 + 2 * k];
+                const float4 v = tok[8 * c + 2 * k];
                 t[k] = make_float2(v.x, v.y), t[k + 1] = make_float2(v.z, v.w);
               }
 #pragma unroll
               for (int e = 0; e < 16; e += 2) fma2t(x[e], x[e + 1], t[e >> 2].x, t[e >> 2].y, -m[(e >> 1) & 1]);
               if (__builtin_expect(part, 0)) {
-                const uint32_t w[2] = {sees(0), sees(1)};
+                const uint32_t w[2] = {sees(0, c), sees(1, c)};
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                   if (!((w[(e >> 1) & 1] >> (8 * (e >> 2) + (e & 1))) & 1)) x[e] = -INFINITY;
               }
-              float sum[2][2];
 #pragma unroll
               for (int e = 0; e < 16; e += 2) {
                 const int r = (e >> 1) & 1;
                 x[e] = ex2(x[e]), x[e + 1] = ex2(x[e + 1]);
-                if (e < 4) sum[r][0] = x[e], sum[r][1] = x[e + 1];
+                if (c == 0 && e < 4) sum[r][0] = x[e], sum[r][1] = x[e + 1];
                 else add2(sum[r][0], sum[r][1], x[e], x[e + 1]);
                 mul2(x[e], x[e + 1], t[e >> 2].x, t[e >> 2].y);
               }
-              if (!moved) {  // (no weight is above its sum; infinity times 0 asks, too)
-                move = __any_sync(0xffffffffu, !(fmaxf(fmaxf(sum[0][0], sum[0][1]), fmaxf(sum[1][0], sum[1][1])) *
-                                                     most <= TOO_LARGE));
-                if (__builtin_expect(move, 0)) {
-                  ld_rows(s_at + c, raw);
-                  tc_wait_ld();
-                  loaded16(raw);
-                  scale();
-                  continue;
-                }
-              }
-              if (__builtin_expect(part, 0)) {  // (a factor may be NaN)
-                const uint32_t w[2] = {sees(0), sees(1)};
+              if (__builtin_expect(bad, 0)) {
+                const uint32_t w[2] = {sees(0, c), sees(1, c)};
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                   if (!((w[(e >> 1) & 1] >> (8 * (e >> 2) + (e & 1))) & 1)) x[e] = 0.0f;
               }
-              uint32_t p[8];
 #pragma unroll
-              for (int e = 0; e < 16; e += 2) p[e / 2] = f16x2_of(x[e], x[e + 1]);
-              st_rows(s_at + c / 2, p);
-#pragma unroll
-              for (int r = 0; r < 2; ++r) add2(l[r][0], l[r][1], sum[r][0], sum[r][1]);
-              break;
+              for (int e = 0; e < 16; e += 2) p[c][e / 2] = f16x2_of(x[e], x[e + 1]);
             }
-          };
-          uint32_t even[16], odd[16];
-          ld_rows(s_at, even);
-#pragma unroll 1
-          for (int c = 0; c < TT; c += 64) {  // (a chunk's scores are fetched while the one before is in hand)
-            tc_wait_ld();
-            loaded16(even);
-            ld_rows(s_at + c + 32, odd);
-            chunk(even, c);
-            tc_wait_ld();
-            loaded16(odd);
-            if (c == 0) ld_rows(s_at + 64, even);
-            chunk(odd, c + 32);
+            // (no weight is above its sum; infinity times 0 asks, too)
+            if (moved) break;
+            move = __any_sync(0xffffffffu, !(fmaxf(fmaxf(sum[0][0], sum[0][1]), fmaxf(sum[1][0], sum[1][1])) * most <=
+                                             TOO_LARGE));
+            if (__builtin_expect(!move, 1)) break;
           }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) st_rows(s_at + 16 * c, p[c]);  // (in the scores' place)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) add2(l[r][0], l[r][1], sum[r][0], sum[r][1]);
           tc_wait_st();
           tc_fence_before();
         }

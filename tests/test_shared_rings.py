@@ -11,15 +11,16 @@ FILE = "k_attend_shared.cu"
 TWO_BLOCKS, TWO_SLICES, TWO_TILES = range(3)
 
 
-def model(items, NS, ST, seed, gives_back=True, widen=2, quads=2):
+def model(items, NS, ST, seed, early_free=False, widen=2, quads=2):
     """items: (mode, tiles of stream 0, of stream 1) each.  ``widen`` and ``quads`` warps stand for the
-    widening warps and a stream's softmax warps."""
+    widening warps and a stream's softmax warps; early_free: a tile is given back with the first stream's
+    product, a mistake."""
     JOBS = constant("JOBS", FILE)
     m = Machine(seed)
     full, k_free = [Bar(2) for _ in range(ST)], [Bar(widen) for _ in range(ST)]
-    v_full, v_free = [Bar(widen) for _ in range(NS)], [Bar(2) for _ in range(NS)]
+    v_full, v_free = [Bar(widen) for _ in range(NS)], [Bar(1) for _ in range(NS)]
     s_full, p_full, o_full, q_full, o_out = ([Bar(c) for _ in range(2)] for c in (2, quads, 1, quads, quads))
-    j_full, j_free = [Bar(1) for _ in range(JOBS)], [Bar(2 * quads + widen + 3) for _ in range(JOBS)]
+    j_full, j_free = [Bar(1) for _ in range(JOBS)], [Bar(2 * quads + widen + 2) for _ in range(JOBS)]
     merge = Bar(2 * quads)
     narrow, wide, out = [None] * ST, [None] * NS, [0, 0]
 
@@ -82,52 +83,44 @@ def model(items, NS, ST, seed, gives_back=True, widen=2, quads=2):
                 at[0] += 1
         yield from jobs(role)
 
-    def mma(u):
-        at, seen, pc = [0], [0], [0]
+    def mma():
+        at, pc = [0], [0, 0]
 
-        def see(mode, upto):
-            while seen[0] <= upto:
-                yield "wait", v_full[seen[0] % NS], seen[0] // NS
-                if mode != TWO_BLOCKS:
-                    if gives_back:
-                        if (seen[0] - at[0]) & 1 != u:
-                            v_free[seen[0] % NS].arrive()
-                            yield 0
-                seen[0] += 1
-
-        def scores(mode, j):
+        def scores(mode, u, j):
             i = at[0] + ring(mode, u, j)
-            yield from see(mode, i)
+            yield "wait", v_full[i % NS], i // NS
             assert wide[i % NS] == i, "scores of another tile"
             yield lambda: s_full[u].arrive()
             s_full[u].arrive()
             yield 0
 
         def role(item, mode, n):
-            yield "wait", q_full[u], item
-            if n[u]:
-                yield from scores(mode, 0)
-            else:
-                o_full[u].arrive()
-                yield 0
-            for j in range(n[u]):
-                i = at[0] + ring(mode, u, j)
-                yield "wait", p_full[u], pc[0]
-                pc[0] += 1
-                assert wide[i % NS] == i, "a product of another tile"
+            for u in range(2):
+                yield "wait", q_full[u], item
+                if n[u]:
+                    yield from scores(mode, u, 0)
+                else:
+                    o_full[u].arrive()
+                    yield 0
+            for j in range(n[0]):
+                for u in range(2):
+                    if j >= n[u]:
+                        break
+                    i = at[0] + ring(mode, u, j)
+                    yield "wait", p_full[u], pc[u]
+                    pc[u] += 1
+                    assert wide[i % NS] == i, "a product of another tile"
 
-                def done(i=i, last=j + 1 == n[u]):
-                    assert wide[i % NS] == i, "a tile that is written while it is read"
-                    v_free[i % NS].arrive()
-                    if not gives_back and mode != TWO_BLOCKS:
-                        v_free[i % NS].arrive()
-                    if last:
-                        o_full[u].arrive()
-                yield done
-                yield 0
-                if j + 1 < n[u]:
-                    yield from scores(mode, j + 1)
-            yield from see(mode, at[0] + count(mode, n) - 1)
+                    def done(i=i, u=u, free=mode != TWO_BLOCKS or u == 1 or early_free, last=j + 1 == n[u]):
+                        assert wide[i % NS] == i, "a tile that is written while it is read"
+                        if free and (not early_free or mode != TWO_BLOCKS or u == 0):
+                            v_free[i % NS].arrive()
+                        if last:
+                            o_full[u].arrive()
+                    yield done
+                    yield 0
+                    if j + 1 < n[u]:
+                        yield from scores(mode, u, j + 1)
             at[0] += count(mode, n)
         yield from jobs(role)
 
@@ -165,8 +158,8 @@ def model(items, NS, ST, seed, gives_back=True, widen=2, quads=2):
     m.add(loader())
     for w in range(widen):
         m.add(widener(w))
+    m.add(mma())
     for u in range(2):
-        m.add(mma(u))
         for _ in range(quads):
             m.add(soft(u))
     m.run()
@@ -186,14 +179,11 @@ def test_every_role_sees_its_phases(dh):
     text = "NS = DH == 128 ? %d : %d, ST = DH == 128 ? %d : %d"
     assert has(FILE, text % (3, 5, 2, 4)), "the rings' sizes"
     NS, ST = (3, 2) if dh == 128 else (5, 4)
-    # a warp that issues one stream's products gives the other's tiles back
-    back = has(FILE, "((seen - it) & 1) != u && lane == 0) mbar_arrive(&ss.v_free[seen % NS])")
     for seed in range(250):
-        model(some_items(random.Random(seed)), NS, ST, seed, back)
+        model(some_items(random.Random(seed)), NS, ST, seed)
 
 
-def test_the_model_finds_a_tile_that_goes_unseen():
-    """Without giving tiles back, a slot may go two tiles further before a stream's warp has seen it."""
+def test_the_model_finds_a_tile_that_is_given_back_too_early():
     with pytest.raises(AssertionError):
         for seed in range(250):
-            model(some_items(random.Random(seed)), 3, 2, seed, False)
+            model(some_items(random.Random(seed)), 3, 2, seed, early_free=True)
