@@ -63,17 +63,16 @@ template <int DH>
 struct Form {
   static constexpr int WIDE = DH / 64 * HALF, NARROW = TT * DH;  // a tile in f16, in e4m3
   static constexpr int NS = DH == 128 ? 3 : 5, ST = DH == 128 ? 2 : 4;  // rings of wide and narrow tiles
-  // a stream's queries; its O goes through the same place, half of the dimensions at a time, in rows 16 bytes
-  // longer than they are (no bank twice)
-  static constexpr int Q_BYTES = WIDE + 16 * BLOCK, O_LD = 2 * DH + 16;
-  static_assert(Q_BYTES == BLOCK * O_LD, "O's rows");
+  // a stream's queries; its pieces go through the same place, eight rows of a warp at a time
+  static constexpr int PART_LD = DH + 8;  // a piece: m, l, six words of padding, O
+  static constexpr int Q_BYTES = WIDE + 16 * BLOCK;
+  static_assert(Q_BYTES == 8 * 8 * PART_LD * 4, "eight rows a warp");
   static constexpr int Q_OFF = 0, V_OFF = Q_OFF + 2 * Q_BYTES, K_OFF = V_OFF + NS * WIDE;
   static constexpr int SC_OFF = K_OFF + ST * NARROW;      // the 16 bytes behind the codes [ST][TT]
   static constexpr int TOK_OFF = SC_OFF + ST * TT * 16;   // a_t [NS][TT], in the order of token_slot
   static constexpr int PLAN_OFF = TOK_OFF + NS * TT * 4;
   static constexpr int SMEM_BYTES = PLAN_OFF + (int)sizeof(Plan) + 1024;
   static constexpr int O_COL = 256;  // TMEM: scores (and weights) of stream u at 128 u, its O at O_COL + DH u
-  static constexpr int PART_LD = DH + 8;  // a piece: m, l, six words of padding, O
 };
 
 struct Args {
@@ -199,13 +198,6 @@ __device__ __forceinline__ uint32_t larger_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
-}
-__device__ __forceinline__ void loaded32(uint32_t (&r)[32]) {
-  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-               "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
-  asm volatile("" : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-               "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
-               "+r"(r[31]));
 }
 // 16 rows x 32 columns: registers 4 k + 2 h + b are row lane / 4 + 8 h, column 8 k + 2 (lane & 3) + b.
 __device__ __forceinline__ void ld_rows(uint32_t taddr, uint32_t (&r)[16]) {
@@ -784,25 +776,35 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
       float factor = 1.0f;
       // the stream's warps have the last item's O out of the queries' place
       if (item > 0 && !await(&ss.o_out[u], (item - 1) & 1, a.status, abort)) return;
-      {  // the warp's queries, 16 bytes a lane; most need no scaling, which is found out on the way
+      {  // the warp's queries, 16 bytes a lane: copied to where they go, then rewritten there as f16.  Most need no
+         // scaling, which is found out on the way.  (Rolled: this runs once an item.)
         constexpr int PIECES = DH / 8, ROWS = 32 / PIECES, N = 16 / ROWS;  // lanes of a query; queries at a time
         const int piece = lane & (PIECES - 1), r0 = lane / PIECES;
         const long long from = row >= 0 ? row * a.q_stride + (job.slice_of(u) * ar.hps + head) * DH : -1;
         uint8_t* dst = sm + F::Q_OFF + u * F::Q_BYTES + q16 * 128 + (piece >> 3) * HALF;
+        auto place = [&](int r) { return dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4); };
         float up = Q_SCALE;
         uint32_t most = 0;  // the largest element of query lane & 15, as bf16 bits (where it is needed)
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {  // as they are; their largest elements; scaled
-          uint4 v[N];
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const long long at = __shfl_sync(0xffffffffu, from, e * ROWS + r0);
-            v[e] = at >= 0 ? *reinterpret_cast<const uint4*>(a.q + at + piece * 8) : make_uint4(0u, 0u, 0u, 0u);
+          if (pass != 1) {
+#pragma unroll 1
+            for (int e = 0; e < N; ++e) {
+              const long long at = __shfl_sync(0xffffffffu, from, e * ROWS + r0);
+              cp_async16(place(e * ROWS + r0), a.q + (at >= 0 ? at + piece * 8 : 0), at >= 0 ? 16 : 0);
+            }
+            cp_async_wait_all();
           }
           uint32_t fine = 0, high = 0;  // a bit per query: its largest element is Q_LOW or more; some are Q_HIGH or more
-#pragma unroll
+#pragma unroll 1
           for (int e = 0; e < N; ++e) {
-            uint32_t top = larger_bf16x2(larger_bf16x2(v[e].x, v[e].y), larger_bf16x2(v[e].z, v[e].w)) & 0x7FFF7FFFu;
+            uint4* at = reinterpret_cast<uint4*>(place(e * ROWS + r0));
+            uint4 v = *at;
+            if (__builtin_expect(pass == 1, 0)) {
+              const long long src = __shfl_sync(0xffffffffu, from, e * ROWS + r0);
+              v = src >= 0 ? *reinterpret_cast<const uint4*>(a.q + src + piece * 8) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            uint32_t top = larger_bf16x2(larger_bf16x2(v.x, v.y), larger_bf16x2(v.z, v.w)) & 0x7FFF7FFFu;
             top = max(top >> 16, top & 0xFFFFu);
             if (__builtin_expect(pass == 1, 0)) {
 #pragma unroll
@@ -816,14 +818,12 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
             for (int r = 0; r < ROWS; ++r)
               if ((b >> (r * PIECES)) & ((1u << PIECES) - 1)) fine |= 1u << (e * ROWS + r);
             high = max(high, top);
-            float f[8], by = up;
-            if (__builtin_expect(pass == 2, 0)) by = __shfl_sync(0xffffffffu, up, e * ROWS + r0);
-            bf16x8_to_f32(v[e], f);
+            float f[8];
+            const float by = __shfl_sync(0xffffffffu, up, e * ROWS + r0);
+            bf16x8_to_f32(v, f);
 #pragma unroll
             for (int k = 0; k < 8; k += 2) mul2(f[k], f[k + 1], by);
-            const int r = e * ROWS + r0;
-            *reinterpret_cast<uint4*>(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4)) =
-                make_uint4(f16x2_of(f[0], f[1]), f16x2_of(f[2], f[3]), f16x2_of(f[4], f[5]), f16x2_of(f[6], f[7]));
+            *at = make_uint4(f16x2_of(f[0], f[1]), f16x2_of(f[2], f[3]), f16x2_of(f[4], f[5]), f16x2_of(f[6], f[7]));
           }
           if (pass == 0 &&
               !__any_sync(0xffffffffu, high >= Q_HIGH || (row >= 0 && !((fine >> (lane & 15)) & 1))))
@@ -857,119 +857,138 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
           const float most = fmaxf(fmaxf(most4.x, most4.y), fmaxf(most4.z, most4.w));
           const bool bad = part && isnan((most4.x + most4.y) + (most4.z + most4.w));  // some factor is NaN
           const float4* tok = reinterpret_cast<const float4*>(sm + F::TOK_OFF) + s * TT / 4 + (lane & 3);
-          auto scale = [&](float* x) {
-            if (__builtin_expect(scaled, 0)) {
+          // Exponents, weights, their sums and the weights times a_t, of 32 tokens.
+          auto factors = [&](int c, float2(&t)[4]) {
 #pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                const float f = __shfl_sync(0xffffffffu, factor, (lane >> 2) + 8 * r);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mul2(x[4 * k + 2 * r], x[4 * k + 2 * r + 1], f);
-              }
+            for (int k = 0; k < 4; k += 2) {
+              const float4 v = tok[8 * c + 2 * k];
+              t[k] = make_float2(v.x, v.y), t[k + 1] = make_float2(v.z, v.w);
             }
           };
-          // of tokens 32 c on, those that row r sees: bits 8 k and the next
-          auto sees = [&](int r, int c) -> uint32_t {
-            const int t = __shfl_sync(0xffffffffu, hi, (lane >> 2) + 8 * r) - (job.token(i) + 32 * c) + 1;
-            return (ss.see[s][c] & (t >= 32 ? ~0u : t <= 0 ? 0u : (1u << t) - 1)) >> (2 * (lane & 3));
+          auto exponents = [&](float* x, const float2(&t)[4]) {
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) fma2t(x[e], x[e + 1], t[e >> 2].x, t[e >> 2].y, -m[(e >> 1) & 1]);
           };
-          uint32_t p[4][8];  // weights times a_t, packed f16
-          float sum[2][2];
-          bool moved = false, move = j == 0;
-#pragma unroll 1
-          for (;;) {
-            if (__builtin_expect(move, 0)) {
-              // the references to the largest of the tile's weights times a_t, and what was summed under the old
-              // ones with them
-              float top[2] = {-INFINITY, -INFINITY}, f[2];
-#pragma unroll 1
-              for (int c = 0; c < 4; ++c) {
-                uint32_t raw[16];
-                float* x = reinterpret_cast<float*>(raw);
-                ld_rows(s_at + 32 * c, raw);
-                tc_wait_ld();
-                loaded16(raw);
-                scale(x);
+          auto weights = [&](float* x, const float2(&t)[4], float(&sum)[2][2]) {
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                  const uint32_t w = part ? sees(r, c) : ~0u;
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const float2 t = reinterpret_cast<const float2*>(tok + 8 * c + (k >> 1) * 4)[k & 1];
-                    const float y0 = fmaf(x[4 * k + 2 * r], t.x, fmaxf(log2_of(fabsf(t.x)), LEAST));
-                    const float y1 = fmaf(x[4 * k + 2 * r + 1], t.y, fmaxf(log2_of(fabsf(t.y)), LEAST));
-                    if ((w >> (8 * k)) & 1) top[r] = fmaxf(top[r], y0);
-                    if ((w >> (8 * k)) & 2) top[r] = fmaxf(top[r], y1);
-                  }
-                }
-              }
-#pragma unroll
-              for (int r = 0; r < 2; ++r) {
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-                f[r] = 1.0f;
-                if (top[r] - m[r] > BASE) {
-                  const float now = fabsf(top[r]) <= SCORE_MAX ? ceilf(top[r]) - BASE : __int_as_float(0x7FC00000);
-                  f[r] = m[r] == UNSET ? 0.0f : ex2(m[r] - now);
-                  m[r] = now;
-                }
-                l[r][0] *= f[r];
-                l[r][1] *= f[r];
-              }
-              if (j > 0) scale_rows(o_at + rows16, DH, f);
-              moved = true;
+            for (int e = 0; e < 16; e += 2) {
+              x[e] = ex2(x[e]), x[e + 1] = ex2(x[e + 1]);
+              add2(sum[(e >> 1) & 1][0], sum[(e >> 1) & 1][1], x[e], x[e + 1]);
+              mul2(x[e], x[e + 1], t[e >> 2].x, t[e >> 2].y);
             }
-            // 32 tokens at a time, in passes over all of them (a branch a pair would cost more than what it skips);
-            // the next ones' scores are fetched meanwhile
-            uint32_t raw[2][16];
+          };
+          // A tile that all rows see, under the references as they are.  (32 tokens at a time, the next ones'
+          // scores fetched meanwhile; the weights take the scores' place when none was too large.)
+          bool plain = j > 0 && !part && !scaled;
+          if (__builtin_expect(plain, 1)) {
+            uint32_t raw[2][16], p[4][8];
+            float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
             ld_rows(s_at, raw[0]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               float* x = reinterpret_cast<float*>(raw[c & 1]);
+              float2 t[4];
+              factors(c, t);
               tc_wait_ld();
               loaded16(raw[c & 1]);
               if (c < 3) ld_rows(s_at + 32 * (c + 1), raw[(c + 1) & 1]);
-              scale(x);
-              float2 t[4];
-#pragma unroll
-              for (int k = 0; k < 4; k += 2) {
-                const float4 v = tok[8 * c + 2 * k];
-                t[k] = make_float2(v.x, v.y), t[k + 1] = make_float2(v.z, v.w);
-              }
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) fma2t(x[e], x[e + 1], t[e >> 2].x, t[e >> 2].y, -m[(e >> 1) & 1]);
-              if (__builtin_expect(part, 0)) {
-                const uint32_t w[2] = {sees(0, c), sees(1, c)};
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (!((w[(e >> 1) & 1] >> (8 * (e >> 2) + (e & 1))) & 1)) x[e] = -INFINITY;
-              }
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const int r = (e >> 1) & 1;
-                x[e] = ex2(x[e]), x[e + 1] = ex2(x[e + 1]);
-                if (c == 0 && e < 4) sum[r][0] = x[e], sum[r][1] = x[e + 1];
-                else add2(sum[r][0], sum[r][1], x[e], x[e + 1]);
-                mul2(x[e], x[e + 1], t[e >> 2].x, t[e >> 2].y);
-              }
-              if (__builtin_expect(bad, 0)) {
-                const uint32_t w[2] = {sees(0, c), sees(1, c)};
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (!((w[(e >> 1) & 1] >> (8 * (e >> 2) + (e & 1))) & 1)) x[e] = 0.0f;
-              }
+              exponents(x, t);
+              weights(x, t, sum);
 #pragma unroll
               for (int e = 0; e < 16; e += 2) p[c][e / 2] = f16x2_of(x[e], x[e + 1]);
             }
             // (no weight is above its sum; infinity times 0 asks, too)
-            if (moved) break;
-            move = __any_sync(0xffffffffu, !(fmaxf(fmaxf(sum[0][0], sum[0][1]), fmaxf(sum[1][0], sum[1][1])) * most <=
-                                             TOO_LARGE));
-            if (__builtin_expect(!move, 1)) break;
+            plain = __all_sync(0xffffffffu, fmaxf(fmaxf(sum[0][0], sum[0][1]), fmaxf(sum[1][0], sum[1][1])) * most <=
+                                                TOO_LARGE);
+            if (__builtin_expect(plain, 1)) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c) st_rows(s_at + 16 * c, p[c]);
+#pragma unroll
+              for (int r = 0; r < 2; ++r) add2(l[r][0], l[r][1], sum[r][0], sum[r][1]);
+            }
           }
+          if (__builtin_expect(!plain, 0)) {
+            // Any tile: first the references to the largest of its weights times a_t (and what was summed under the
+            // old ones with them).  In rolled loops: most of this runs once an item, and is fetched for it.
+            float f[2] = {1.0f, 1.0f};
+            if (scaled) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) st_rows(s_at + 16 * c, p[c]);  // (in the scores' place)
+              for (int r = 0; r < 2; ++r) f[r] = __shfl_sync(0xffffffffu, factor, (lane >> 2) + 8 * r);
+            }
+            // of tokens 32 c on, those that row r sees: bits 8 k and the next
+            auto sees = [&](int r, int c) -> uint32_t {
+              const int t = __shfl_sync(0xffffffffu, hi, (lane >> 2) + 8 * r) - (job.token(i) + 32 * c) + 1;
+              return (ss.see[s][c] & (t >= 32 ? ~0u : t <= 0 ? 0u : (1u << t) - 1)) >> (2 * (lane & 3));
+            };
+            auto load = [&](int c, uint32_t(&raw)[16], uint32_t(&w)[2]) {
+              ld_rows(s_at + 32 * c, raw);
+              w[0] = w[1] = ~0u;
+              if (part) w[0] = sees(0, c), w[1] = sees(1, c);
+              tc_wait_ld();
+              loaded16(raw);
+              if (scaled) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) add2(l[r][0], l[r][1], sum[r][0], sum[r][1]);
+                for (int e = 0; e < 16; e += 2)
+                  mul2(reinterpret_cast<float*>(raw)[e], reinterpret_cast<float*>(raw)[e + 1], f[(e >> 1) & 1]);
+              }
+            };
+            auto hide = [&](float* x, const uint32_t(&w)[2], float to) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (!((w[(e >> 1) & 1] >> (8 * (e >> 2) + (e & 1))) & 1)) x[e] = to;
+            };
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t raw[16], w[2];
+              float* x = reinterpret_cast<float*>(raw);
+              float2 t[4];
+              factors(c, t);
+              load(c, raw, w);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float gx = fmaxf(log2_of(fabsf(t[k].x)), LEAST), gy = fmaxf(log2_of(fabsf(t[k].y)), LEAST);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  x[4 * k + 2 * r] = fmaf(x[4 * k + 2 * r], t[k].x, gx);
+                  x[4 * k + 2 * r + 1] = fmaf(x[4 * k + 2 * r + 1], t[k].y, gy);
+                }
+              }
+              if (part) hide(x, w, -INFINITY);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) top[(e >> 1) & 1] = fmaxf(top[(e >> 1) & 1], x[e]);
+            }
+            float by[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+              top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+              by[r] = 1.0f;
+              if (top[r] - m[r] > BASE) {
+                const float now = fabsf(top[r]) <= SCORE_MAX ? ceilf(top[r]) - BASE : __int_as_float(0x7FC00000);
+                by[r] = m[r] == UNSET ? 0.0f : ex2(m[r] - now);
+                m[r] = now;
+              }
+              l[r][0] *= by[r];
+              l[r][1] *= by[r];
+            }
+            if (j > 0 && __any_sync(0xffffffffu, by[0] != 1.0f || by[1] != 1.0f)) scale_rows(o_at + rows16, DH, by);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t raw[16], w[2], p[8];
+              float* x = reinterpret_cast<float*>(raw);
+              float2 t[4];
+              factors(c, t);
+              load(c, raw, w);
+              exponents(x, t);
+              if (part) hide(x, w, -INFINITY);
+              weights(x, t, l);
+              if (bad) hide(x, w, 0.0f);
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) p[e / 2] = f16x2_of(x[e], x[e + 1]);
+              st_rows(s_at + 16 * c, p);  // (over scores that were read)
+            }
+          }
           tc_wait_st();
           tc_fence_before();
         }
@@ -993,26 +1012,45 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
       }
       const int q = 32 * quad + lane;  // of the quadrant's queries
       if (mode != TWO_TILES) {
-        if (lane < 16 && row >= 0) *reinterpret_cast<float2*>(piece_of(q16 + lane)) = make_float2(m_row, l_row);
-        float* to = half == 0 ? piece_of(q) : nullptr;
-        if (__any_sync(0xffffffffu, to != nullptr)) {
-          // (a thread's row by a copy of its own: stored from registers, a row apart, they took 4500 cycles)
-          uint8_t* out = sm + F::Q_OFF + u * F::Q_BYTES + q * F::O_LD;
-#pragma unroll 1
-          for (int c = 0; c < DH; c += DH / 2) {
-            if (c > 0) bulk_wait_read();
+        if (!idle) {
+          // whole pieces through shared memory, eight rows at a time, by a copy for every run of them (stored from
+          // registers, or by a copy each, they took 4500 cycles)
+          float* to = piece_of(q16 + (lane & 15));
+          const long long prev = __shfl_up_sync(0xffffffffu, reinterpret_cast<long long>(to), 1);
+          const bool head_of_run = to && ((lane & 7) == 0 || prev + F::PART_LD * 4 != reinterpret_cast<long long>(to));
+          const uint32_t ends = __ballot_sync(0xffffffffu, head_of_run || !to);
+          uint8_t* out = sm + F::Q_OFF + u * F::Q_BYTES + (4 * half + quad) * (F::Q_BYTES / 8);
+          float* mine = reinterpret_cast<float*>(out) + (lane >> 2) * F::PART_LD + 2 * (lane & 3);
+          float2 later[DH / 8];
 #pragma unroll
-            for (int d = 0; d < DH / 2; d += 32) {
-              uint32_t o[32];
-              tc_ld32(o_at + c + d, o);
-              tc_wait_ld();
-              loaded32(o);
+          for (int c = 0; c < DH; c += 32) {
+            uint32_t o[16];
+            ld_rows(o_at + rows16 + c, o);
+            tc_wait_ld();
+            loaded16(o);
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<uint4*>(out + 4 * (d + e)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int k = 0; k < 4; ++k) {
+              *reinterpret_cast<uint2*>(mine + 8 + c + 8 * k) = make_uint2(o[4 * k], o[4 * k + 1]);
+              later[c / 8 + k] = make_float2(__uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
             }
+          }
+#pragma unroll 1
+          for (int r = 0; r < 2; ++r) {
+            if (r > 0) {
+              bulk_wait_read();
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < DH / 8; ++k) *reinterpret_cast<float2*>(mine + 8 + 8 * k) = later[k];
+            }
+            if (lane >> 3 == r)
+              *reinterpret_cast<float2*>(reinterpret_cast<float*>(out) + (lane & 7) * F::PART_LD) = make_float2(m_row, l_row);
             fence_proxy_async_shared();
-            if (to) bulk_store(to + 8 + c, out, 2 * DH), bulk_commit();
+            __syncwarp();
+            if (lane >> 3 == r && head_of_run) {
+              const int first = lane & 7, n = __ffs((ends >> (lane + 1) | 1u << (7 - first)));
+              bulk_store(to, reinterpret_cast<float*>(out) + first * F::PART_LD, n * F::PART_LD * 4);
+            }
+            bulk_commit();
           }
           bulk_wait_read();
         }
