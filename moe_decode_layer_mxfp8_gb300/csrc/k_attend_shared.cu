@@ -22,6 +22,8 @@
 // rows, and tells the join where pieces are (23 makes the registers' split come out).
 // Every wait is for an mbarrier, and bounded; one that runs out is reported and ends its role, and with it
 // the others' waits.  Copies and products on their way are waited for before the CTA ends.
+#include <cstddef>
+
 #include "attend_tc.cuh"
 
 namespace mono {
@@ -75,10 +77,24 @@ struct Form {
   static constexpr int O_COL = 256;  // TMEM: scores (and weights) of stream u at 128 u, its O at O_COL + DH u
 };
 
+// Division of numbers below 2^31 by one that the host knows: n mul / 2^shift, mul = 2^(31 + l) / d rounded up,
+// 2^l >= d (Granlund and Montgomery's theorem).
+struct Divisor {
+  uint32_t mul;
+  int shift;
+  static Divisor of(int d) {
+    int l = 0;
+    while ((1ll << l) < d) ++l;
+    return {(uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+  }
+  __device__ int operator()(int n) const { return (int)((uint64_t)(uint32_t)n * mul >> shift); }
+};
+
 struct Args {
   CUtensorMap codes, scales;
   int box;  // 0: no maps
   int slices, hps, rows_per;  // latent slices, heads of one, rows of a block
+  Divisor by_page, by_hps, by_rows;  // block_size, hps, rows_per
   SharedArgs a;
   float* home;   // pieces: [2][max_rows][n_q], of those that begin an item; prefixes', then own tokens'
   float* over;   // [CTAs][2 * BLOCK], of a CTA's item that began before it
@@ -103,7 +119,7 @@ enum { TWO_BLOCKS, TWO_SLICES, TWO_TILES };
 struct Items {
   int tiles, blocks, len, half;  // lengths in the line of an item, and of one of TWO_TILES
   __device__ Items(const Args& ar, int tiles, int rows)
-      : tiles(tiles), blocks((rows + ar.rows_per - 1) / ar.rows_per), len(EXTRA + tiles), half(EXTRA + (tiles + 1) / 2) {}
+      : tiles(tiles), blocks(ar.by_rows(rows + ar.rows_per - 1)), len(EXTRA + tiles), half(EXTRA + (tiles + 1) / 2) {}
   __device__ int of_pairs(const Args& ar) const { return ar.slices * (blocks >> 1); }
   __device__ int whole(const Args& ar) const { return of_pairs(ar) + (blocks & 1) * (ar.slices >> 1); }
   __device__ int units(const Args& ar) const { return tiles ? whole(ar) * len + (blocks & ar.slices & 1) * half : 0; }
@@ -172,8 +188,9 @@ __device__ __forceinline__ bool next_job(const Args& ar, const Plan& p, Cursor& 
 }
 
 struct Shared {
-  uint64_t full[4], k_free[4], v_full[5], v_free[5];
-  uint64_t s_full[2], p_full[2], o_full[2], o_out[2], q_full[2], merge, j_full[JOBS], j_free[JOBS], drain;
+  // barriers, and the arrivals that complete their phases
+  uint64_t full[4], k_free[4], v_full[5], v_free[5], s_full[2], p_full[2], o_full[2], o_out[2], q_full[2], merge, drain;
+  uint64_t j_full[JOBS], j_free[JOBS];
   uint32_t valid[4][4];                // tokens that are there, of a narrow tile
   alignas(16) uint32_t see[5][4];      // and of a wide one
   int part[5];                         // not every row of the item sees all its tokens
@@ -183,6 +200,16 @@ struct Shared {
   uint32_t tmem;
   int abort;
 };
+// (an item is read by the softmax, widening, issuing and loading warps)
+constexpr int BARRIERS = 30 + 2 * JOBS;
+__device__ __forceinline__ int arrivals(int i) {
+  if (i >= 30) return i < 30 + JOBS ? 1 : SOFT_WARPS + WIDEN_WARPS + 2;
+  if (i >= 28) return i < 29 ? SOFT_WARPS : 1;
+  if (i >= 20) return i == 22 || i == 23 ? 1 : STREAM_WARPS;
+  if (i >= 18) return 2;
+  return i < 4 || i >= 13 ? 1 : WIDEN_WARPS;
+}
+static_assert(offsetof(Shared, valid) == 8 * BARRIERS, "barriers");
 static_assert(Form<128>::SMEM_BYTES + sizeof(Shared) <= 227 * 1024, "shared memory");
 static_assert(Form<64>::SMEM_BYTES + sizeof(Shared) <= 227 * 1024, "shared memory");
 
@@ -222,12 +249,6 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t 
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                : "memory");
 }
-// 32 bytes at once
-__device__ __forceinline__ void st_global8(float* p, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
 // f16 x f16, f32 accumulators; A in shared memory, or in TMEM
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -252,23 +273,6 @@ __device__ __forceinline__ void regs_up() {
 template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// A wait for an mbarrier phase by a whole warp, for a second at most, and not once another wait has run out.
-// False if it ran out.
-__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!ok) {
-    const uint64_t t0 = globaltimer_ns();
-#pragma unroll 1
-    while (!(ok = mbar_try_wait(bar, parity)) && !*abort) {
-      if (globaltimer_ns() - t0 > 1000000000ull) {
-        atomicOr(status, ST_WAIT_TIMEOUT);
-        *abort = 1;
-      }
-    }
-  }
-  return __all_sync(0xffffffffu, ok);
 }
 
 // Fills the plan but for the line (every thread of the block); the results are behind the caller's next
@@ -327,24 +331,29 @@ __device__ __forceinline__ void derive_plan(const Args& ar, Plan& plan) {
     }
     if (hi >= cap && hi >= len && tell) atomicOr(a.status, ST_UNMAPPED_PAGE);
   }
+  __syncthreads();
+  if (tid < groups) plan.pre[tid + 1] = items_of(ar, plan, tid).units(ar);
+  static_assert(MAX_GROUPS <= THREADS, "a group a thread");
 }
 
-// Lays the groups out in the line and finds the CTA's first item; by a whole warp.
+// Lays the groups out in the line (pre[g + 1] holds what group g takes) and finds the CTA's first item; by a
+// whole warp.
 __device__ __forceinline__ Cursor cut_line(const Args& ar, Plan& plan) {
   const int lane = threadIdx.x & 31, groups = ar.a.n_prefix + ar.a.n_req;
-  int W = 0;
+  const int each = (groups + 31) >> 5, from = lane * each, to = min(from + each, groups);  // a lane's groups
+  int u = 0;
 #pragma unroll 1
-  for (int g0 = 0; g0 < groups; g0 += 32) {
-    const int i = g0 + lane;
-    int u = i < groups ? items_of(ar, plan, i).units(ar) : 0;
-#pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, u, o);
-      if (lane >= o) u += y;
-    }
-    if (i < groups) plan.pre[i + 1] = W + u;
-    W += __shfl_sync(0xffffffffu, u, 31);
+  for (int g = from; g < to; ++g) u += plan.pre[g + 1];
+  int W = u;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, W, o);
+    if (lane >= o) W += y;
   }
+  u = W - u;
+  W = __shfl_sync(0xffffffffu, W, 31);
+#pragma unroll 1
+  for (int g = from; g < to; ++g) u += plan.pre[g + 1], plan.pre[g + 1] = u;
   if (lane == 0) plan.pre[0] = 0;
   __syncwarp();
   const Cut cut(W, gridDim.x);
@@ -389,67 +398,66 @@ __device__ __forceinline__ void item_rows(const Args& ar, const Plan& plan, Job&
   if (lane == 0) job.least = least;
 }
 
-// Loads narrow tiles, a warp: TMA boxes through the page table, or cp.async where there are no maps.
-// A lane per box of the tile (of a token each without maps, four times), looked up ahead of the load.
+// Loads narrow tiles, a warp: TMA boxes through the page table, a lane each, looked up ahead of the load; or
+// cp.async, a token a lane, where there are no maps.
 template <int DH>
 struct Loader {
-  int box, shift, boxes, t0, lo, end;
-  int page[4], row[4];
+  int box, shift, t0, lo, end, page, row;
+  const int* table;
+  int max_blocks;
   __device__ explicit Loader(int b) {
     box = b ? b : 1;
     shift = __ffs(box) - 1;
-    boxes = TT >> shift;
+  }
+  // The page and the place in it of token t (page -1: not mapped; row -1: not needed).
+  __device__ __forceinline__ void look_up(const Args& ar, int t, bool needed) {
+    const int lb = ar.by_page(t);
+    page = row = -1;
+    if (needed && t < end && t + box > lo) {
+      row = t - lb * ar.a.kv.block_size;
+      if (lb < max_blocks) page = __ldg(table + lb);
+      if (page >= ar.a.kv.num_blocks) page = -1;
+    }
   }
   __device__ __forceinline__ void locate(const Args& ar, const Plan& plan, const Job& job, int i) {
-    const int lane = threadIdx.x & 31, np = ar.a.n_prefix, g = job.g, bs = ar.a.kv.block_size;
+    const int lane = threadIdx.x & 31, np = ar.a.n_prefix, g = job.g;
     const PagedView& v = g < np ? ar.a.pre : ar.a.kv;
-    const int* table = v.table + (size_t)(g < np ? g : g - np) * v.max_blocks;
+    max_blocks = v.max_blocks;
+    table = v.table + (size_t)(g < np ? g : g - np) * max_blocks;
     t0 = job.token(i);
     lo = plan.first[g];
     end = end_of(ar.a, plan, g);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (32 * q >= boxes) break;
-      const int t = t0 + ((32 * q + lane) << shift), lb = t / bs;
-      page[q] = row[q] = -1;
-      if (32 * q + lane < boxes && t < end && t + box > lo) {
-        row[q] = t - lb * bs;
-        if (lb < v.max_blocks) page[q] = __ldg(table + lb);
-      }
-    }
+    if (box > 1) look_up(ar, t0 + (lane << shift), lane < TT >> shift);
   }
   __device__ __forceinline__ void load(const Args& ar, int slice, uint8_t* st, uint8_t* sc, uint32_t* valid,
                                        uint64_t* full) {
     const SharedArgs& a = ar.a;
     const int lane = threadIdx.x & 31;
     if (box > 1) {
-      const bool m = page[0] >= 0 && page[0] < a.kv.num_blocks;
-      if (row[0] >= 0 && !m) atomicOr(a.status, ST_UNMAPPED_PAGE);
-      if (m) {
-        tma_load_3d(st + ((lane * DH) << shift), &ar.codes, DH * slice, row[0], page[0], full);
-        tma_load_3d(sc + ((lane * 16) << shift), &ar.scales, a.kv_dim, row[0], page[0], full);
+      if (page >= 0) {
+        tma_load_3d(st + ((lane * DH) << shift), &ar.codes, DH * slice, row, page, full);
+        tma_load_3d(sc + ((lane * 16) << shift), &ar.scales, a.kv_dim, row, page, full);
+      } else if (row >= 0) {
+        atomicOr(a.status, ST_UNMAPPED_PAGE);
       }
-      const uint32_t have = __ballot_sync(0xffffffffu, m);
-#pragma unroll
+      const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+#pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         const int t = t0 + 32 * q + lane;
-        const bool see = ((have >> ((32 * q + lane) >> shift)) & 1) && t >= lo && t < end;
-        const uint32_t w = __ballot_sync(0xffffffffu, see);
+        const uint32_t w =
+            __ballot_sync(0xffffffffu, ((have >> ((32 * q + lane) >> shift)) & 1) && t >= lo && t < end);
         if (lane == q) valid[q] = w;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_expect_tx(full, __popc(have) * box * (DH + 16));
-      __syncwarp();
     } else {
       constexpr int PIECES = DH / 16, ROWS = 32 / PIECES;
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
-        const int pg = q == 0 ? page[0] : q == 1 ? page[1] : q == 2 ? page[2] : page[3];
-        const int rw = q == 0 ? row[0] : q == 1 ? row[1] : q == 2 ? row[2] : row[3];
-        const bool m = pg >= 0 && pg < a.kv.num_blocks;
-        if (rw >= 0 && !m) atomicOr(a.status, ST_UNMAPPED_PAGE);
-        const long long off = m ? pg * a.kv.stride_block + rw * a.kv.stride_tok : 0;
-        const uint32_t w = __ballot_sync(0xffffffffu, m);
+        look_up(ar, t0 + 32 * q + lane, true);
+        if (row >= 0 && page < 0) atomicOr(a.status, ST_UNMAPPED_PAGE);
+        const long long off = page * a.kv.stride_block + row * a.kv.stride_tok;
+        const uint32_t w = __ballot_sync(0xffffffffu, page >= 0);
         if (lane == 0) valid[q] = w;
 #pragma unroll 1
         for (int e = 0; e < 32 / ROWS; ++e) {
@@ -458,12 +466,13 @@ struct Loader {
           if ((w >> k) & 1)
             cp_async16(st + (32 * q + k) * DH + 16 * piece, a.kv.base + ro + DH * slice + 16 * piece, 16);
         }
-        if (m) cp_async16(sc + (32 * q + lane) * 16, a.kv.base + off + a.kv_dim, 16);
+        if (page >= 0) cp_async16(sc + (32 * q + lane) * 16, a.kv.base + off + a.kv_dim, 16);
       }
       cp_async_wait_all();
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
     }
+    __syncwarp();
   }
 };
 
@@ -498,19 +507,12 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
   Plan& plan = *reinterpret_cast<Plan*>(sm + F::PLAN_OFF);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  if (tid == 0) {
-    for (int s = 0; s < ST; ++s) mbar_init(&ss.full[s], 1), mbar_init(&ss.k_free[s], WIDEN_WARPS);
-    for (int s = 0; s < NS; ++s) mbar_init(&ss.v_full[s], WIDEN_WARPS), mbar_init(&ss.v_free[s], 1);
-    for (int u = 0; u < 2; ++u) {
-      mbar_init(&ss.s_full[u], 2), mbar_init(&ss.p_full[u], STREAM_WARPS), mbar_init(&ss.o_full[u], 1);
-      mbar_init(&ss.q_full[u], STREAM_WARPS), mbar_init(&ss.o_out[u], STREAM_WARPS);
-    }
-    // an item is read by the softmax, widening, issuing and loading warps
-    for (int k = 0; k < JOBS; ++k) mbar_init(&ss.j_full[k], 1), mbar_init(&ss.j_free[k], SOFT_WARPS + WIDEN_WARPS + 2);
-    mbar_init(&ss.merge, SOFT_WARPS);
-    mbar_init(&ss.drain, 1);
-    ss.abort = 0;
+  if (tid < BARRIERS) {
+    mbar_init(ss.full + tid, arrivals(tid));
     fence_mbar_init();
+  }
+  if (tid == 0) {
+    ss.abort = 0;
     if (ar.box) prefetch_tmap(&ar.codes), prefetch_tmap(&ar.scales);
   }
   if (warp == MMA_WARP) tmem_alloc<512>(&ss.tmem);
@@ -524,7 +526,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
   int item = 0;
   auto next_item = [&]() -> const Job* {
     const Job* job = &ss.job[item % JOBS];
-    if (!await(&ss.j_full[item % JOBS], (item / JOBS) & 1, a.status, abort)) return nullptr;
+    if (!wait(&ss.j_full[item % JOBS], (item / JOBS) & 1, a.status, abort)) return nullptr;
     return job->n[0] > 0 ? job : nullptr;
   };
   auto item_done = [&]() {
@@ -548,46 +550,49 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
 #pragma unroll 1
         for (int i = 0; i < n; ++i, ++it) {
           const int st = it % ST, s = it % NS;
-          if (!await(&ss.full[st], (it / ST) & 1, a.status, abort)) return;
+          if (!wait(&ss.full[st], (it / ST) & 1, a.status, abort)) return;
           const uint32_t ok = ss.valid[st][t0 >> 5];
           // some row does not see all its tokens
           const bool part = least < job->token(i) + TT - 1 ||
                             (ss.valid[st][0] & ss.valid[st][1] & ss.valid[st][2] & ss.valid[st][3]) != 0xffffffffu;
-          uint4 v[N];
-#pragma unroll
-          for (int e = 0; e < N; ++e) v[e] = lds128(sm + F::K_OFF + st * F::NARROW + (t0 + e * ROWS) * DH + lane * 16);
           const float raw = *reinterpret_cast<const float*>(sm + F::SC_OFF + (st * TT + t0 + lane) * 16);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ss.k_free[st]);
+          if (it >= NS && !wait(&ss.v_free[s], (it / NS - 1) & 1, a.status, abort)) return;
+          const uint8_t* src = sm + F::K_OFF + st * F::NARROW + t0 * DH + lane * 16;
+          uint8_t* dst = sm + F::V_OFF + s * F::WIDE + (piece >> 2) * HALF;
           uint32_t nan = 0;
-          if (__builtin_expect(part, 0)) {
-            // a NaN code that some row must not see would reach it as 0 * NaN: it is a 0 here, and the
-            // token's factor is NaN
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-              const uint4 c = without_nan(v[e]);
-              const uint32_t bad =
-                  __ballot_sync(0xffffffffu, c.x != v[e].x || c.y != v[e].y || c.z != v[e].z || c.w != v[e].w);
-              v[e] = c;
 #pragma unroll 1
-              for (int k = 0; k < ROWS; ++k)
-                if ((bad >> (k * PIECES)) & ((1u << PIECES) - 1)) nan |= 1u << (e * ROWS + k);
+          for (int e0 = 0; e0 < N; e0 += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = lds128(src + (e0 + e) * ROWS * DH);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (__builtin_expect(part, 0)) {
+                // a NaN code that some row must not see would reach it as 0 * NaN: it is a 0 here, and the
+                // token's factor is NaN
+                const uint4 c = without_nan(v[e]);
+                const uint32_t bad =
+                    __ballot_sync(0xffffffffu, c.x != v[e].x || c.y != v[e].y || c.z != v[e].z || c.w != v[e].w);
+                v[e] = c;
+                if (__builtin_expect(bad, 0)) {
+#pragma unroll 1
+                  for (int k = 0; k < ROWS; ++k)
+                    if ((bad >> (k * PIECES)) & ((1u << PIECES) - 1)) nan |= 1u << ((e0 + e) * ROWS + k);
+                }
+              }
+              const int row = t0 + (e0 + e) * ROWS + r0, c = 2 * (piece & 3) + odd;
+              uint4 x, y;
+              uint32_t f[2];
+              e4m3x4_to_f16x4(odd ? v[e].z : v[e].x, f), x.x = f[0], x.y = f[1];
+              e4m3x4_to_f16x4(odd ? v[e].w : v[e].y, f), x.z = f[0], x.w = f[1];
+              e4m3x4_to_f16x4(odd ? v[e].x : v[e].z, f), y.x = f[0], y.y = f[1];
+              e4m3x4_to_f16x4(odd ? v[e].y : v[e].w, f), y.z = f[0], y.w = f[1];
+              *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = x;
+              *reinterpret_cast<uint4*>(dst + row * 128 + (((c ^ 1) ^ (row & 7)) << 4)) = y;
             }
           }
-          if (it >= NS && !await(&ss.v_free[s], (it / NS - 1) & 1, a.status, abort)) return;
-          uint8_t* dst = sm + F::V_OFF + s * F::WIDE + (piece >> 2) * HALF;
-#pragma unroll
-          for (int e = 0; e < N; ++e) {
-            const int row = t0 + e * ROWS + r0, c = 2 * (piece & 3) + odd;
-            uint4 x, y;
-            uint32_t f[2];
-            e4m3x4_to_f16x4(odd ? v[e].z : v[e].x, f), x.x = f[0], x.y = f[1];
-            e4m3x4_to_f16x4(odd ? v[e].w : v[e].y, f), x.z = f[0], x.w = f[1];
-            e4m3x4_to_f16x4(odd ? v[e].x : v[e].z, f), y.x = f[0], y.y = f[1];
-            e4m3x4_to_f16x4(odd ? v[e].y : v[e].w, f), y.z = f[0], y.w = f[1];
-            *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = x;
-            *reinterpret_cast<uint4*>(dst + row * 128 + (((c ^ 1) ^ (row & 7)) << 4)) = y;
-          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ss.k_free[st]);
           {  // a token a lane
             static_assert(WIDEN_TOKENS == 32, "a token a lane");
             const bool there = (ok >> lane) & 1, fin = fabsf(raw) <= SCALE_MAX && !((nan >> lane) & 1);
@@ -616,55 +621,51 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
       const uint64_t q0 = desc_sw128(smem_u32(sm + F::Q_OFF)), k0 = desc_sw128(smem_u32(sm + F::V_OFF)),
                      v0 = desc_mn(smem_u32(sm + F::V_OFF), HALF);
       int it = 0;              // the ring's tiles of the items before
-      uint32_t pc[2] = {0, 0};  // the streams' tiles so far
+      uint32_t pc = 0;         // parities of the streams' tiles so far
       bool ok = true;
 #pragma unroll 1
       while (ok) {
         const Job* job = next_item();
         if (!job) break;
-        auto scores = [&](int u, int j) {
-          const int i = it + job->ring(u, j);
-          ok = await(&ss.v_full[i % NS], (i / NS) & 1, a.status, abort);
-          if (ok && elect_one()) {
-            tc_fence_after();
-            const uint64_t qd = q0 + u * (F::Q_BYTES / 16), kd = k0 + (i % NS) * (F::WIDE / 16);
-#pragma unroll
-            for (int k = 0; k < DH / 16; ++k)
-              mma_ss(tmem + 128 * u, qd + (k >> 2) * (HALF / 16) + 2 * (k & 3), kd + (k >> 2) * (HALF / 16) + 2 * (k & 3),
-                     IS, k > 0);
-            tc_commit(&ss.s_full[u]);
-            // (the commit is no release: this arrival passes on what the widening warps wrote)
-            mbar_arrive(&ss.s_full[u]);
-          }
-          __syncwarp();
-        };
 #pragma unroll 1
-        for (int u = 0; ok && u < 2; ++u) {
-          ok = await(&ss.q_full[u], item & 1, a.status, abort);
-          if (ok && (u ? job->n[1] : job->n[0]) > 0) scores(u, 0);
-          else if (lane == 0) mbar_arrive(&ss.o_full[u]);
-          __syncwarp();
-        }
-#pragma unroll 1
-        for (int j = 0; ok && j < job->n[0]; ++j) {
+        for (int j = -1; ok && j < job->n[0]; ++j) {
 #pragma unroll 1
           for (int u = 0; ok && u < 2; ++u) {
             const int n = u ? job->n[1] : job->n[0];
-            if (j >= n) break;
-            const int s = (it + job->ring(u, j)) % NS;
-            ok = await(&ss.p_full[u], (u ? pc[1] : pc[0]) & 1, a.status, abort);
-            if (u) ++pc[1]; else ++pc[0];
-            if (ok && elect_one()) {
-              tc_fence_after();
-              const uint32_t oc = tmem + F::O_COL + DH * u, pcol = tmem + 128 * u;
-              const uint64_t vd = v0 + s * (F::WIDE / 16);
-#pragma unroll
-              for (int k = 0; k < TT / 16; ++k) mma_ts(oc, pcol + 8 * k, vd + k * (2048 / 16), IO, j > 0 || k > 0);
-              if (job->mode != TWO_BLOCKS || u == 1) tc_commit(&ss.v_free[s]);
-              if (j + 1 == n) tc_commit(&ss.o_full[u]);
+            if (j < 0) {
+              ok = wait(&ss.q_full[u], item & 1, a.status, abort);
+              if (n == 0 && lane == 0) mbar_arrive(&ss.o_full[u]);
+            } else if (j < n) {
+              ok = wait(&ss.p_full[u], (pc >> u) & 1, a.status, abort);
+              pc ^= 1u << u;
+              if (ok && elect_one()) {
+                const int s = (it + job->ring(u, j)) % NS;
+                const uint32_t oc = tmem + F::O_COL + DH * u, pcol = tmem + 128 * u;
+                uint64_t vd = v0 + s * (F::WIDE / 16);
+                tc_fence_after();
+#pragma unroll 2
+                for (int k = 0; k < TT / 16; ++k, vd += 2048 / 16) mma_ts(oc, pcol + 8 * k, vd, IO, j > 0 || k > 0);
+                if (job->mode != TWO_BLOCKS || u == 1) tc_commit(&ss.v_free[s]);
+                if (j + 1 == n) tc_commit(&ss.o_full[u]);
+              }
             }
             __syncwarp();
-            if (ok && j + 1 < n) scores(u, j + 1);
+            if (!ok || j + 1 >= n) continue;
+            const int i = it + job->ring(u, j + 1);
+            ok = wait(&ss.v_full[i % NS], (i / NS) & 1, a.status, abort);
+            if (ok && elect_one()) {
+              tc_fence_after();
+              const uint64_t qd = q0 + u * (F::Q_BYTES / 16), kd = k0 + (i % NS) * (F::WIDE / 16);
+#pragma unroll 2
+              for (int k = 0; k < DH / 16; ++k) {
+                const int at = (k >> 2) * (HALF / 16) + 2 * (k & 3);
+                mma_ss(tmem + 128 * u, qd + at, kd + at, IS, k > 0);
+              }
+              tc_commit(&ss.s_full[u]);
+              // (the commit is no release: this arrival passes on what the widening warps wrote)
+              mbar_arrive(&ss.s_full[u]);
+            }
+            __syncwarp();
           }
         }
         it += job->count();
@@ -690,7 +691,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
 #pragma unroll 1
       for (; job; ++it) {
         const int st = it % ST;
-        if (it >= ST && !await(&ss.k_free[st], (it / ST - 1) & 1, a.status, abort)) break;
+        if (it >= ST && !wait(&ss.k_free[st], (it / ST - 1) & 1, a.status, abort)) break;
         tile.load(ar, job->slice_of(i & 1), sm + F::K_OFF + st * F::NARROW, sm + F::SC_OFF + st * TT * 16, ss.valid[st],
                   &ss.full[st]);
         advance();
@@ -704,7 +705,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
 #pragma unroll 1
       for (;; ++item) {
         const int k = item % JOBS;
-        if (item >= JOBS && !await(&ss.j_free[k], (item / JOBS - 1) & 1, a.status, abort)) break;
+        if (item >= JOBS && !wait(&ss.j_free[k], (item / JOBS - 1) & 1, a.status, abort)) break;
         Job& job = ss.job[k];
         bool more = false;
         if (lane == 0) more = next_job(ar, plan, cur, job);
@@ -755,88 +756,77 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
     while (const Job* at = next_item()) {
       const Job& job = *at;
       const int n = u ? job.n[1] : job.n[0], mode = job.mode;
-      // query q's row and head of the slice; and where its piece goes (null: there is no such query)
-      auto row_of = [&](int q, int& head) -> int {
-        const int j = q / ar.hps;
-        head = q - j * ar.hps;
-        return j < ar.rows_per ? job.row[(mode == TWO_BLOCKS ? u * BLOCK : 0) + j] : -1;
-      };
-      auto piece_of = [&](int q) -> float* {
-        int head;
-        const int row = row_of(q, head);
-        if (row < 0) return nullptr;
-        const size_t k = job.begins ? ((size_t)(job.g < a.n_prefix ? 0 : ar.max_rows) + row) * a.n_q +
-                                          job.slice_of(u) * ar.hps + head
-                                    : (size_t)blockIdx.x * (2 * BLOCK) + (mode == TWO_TILES ? 0 : u * BLOCK) + q;
-        return (job.begins ? ar.home : ar.over) + k * F::PART_LD;
-      };
-      int head;
-      const int row = row_of(q16 + (lane & 15), head), hi = row >= 0 ? plan.hi[row] : -1;
+      // the row and the head of query lane & 15, its row's last token, where its piece goes
+      const int ql = q16 + (lane & 15), jr = ar.by_hps(ql), head = job.slice_of(u) * ar.hps + ql - jr * ar.hps;
+      const int row = jr < ar.rows_per ? job.row[(mode == TWO_BLOCKS ? u * BLOCK : 0) + jr] : -1;
+      const int hi = row >= 0 ? plan.hi[row] : -1;
       const bool idle = !__any_sync(0xffffffffu, row >= 0);  // no queries in this warp
       float factor = 1.0f;
       // the stream's warps have the last item's O out of the queries' place
-      if (item > 0 && !await(&ss.o_out[u], (item - 1) & 1, a.status, abort)) return;
-      {  // the warp's queries, 16 bytes a lane: copied to where they go, then rewritten there as f16.  Most need no
-         // scaling, which is found out on the way.  (Rolled: this runs once an item.)
+      if (item > 0 && !wait(&ss.o_out[u], (item - 1) & 1, a.status, abort)) return;
+      {  // the warp's queries, 16 bytes a lane: copied to where they go, then rewritten there as f16
         constexpr int PIECES = DH / 8, ROWS = 32 / PIECES, N = 16 / ROWS;  // lanes of a query; queries at a time
         const int piece = lane & (PIECES - 1), r0 = lane / PIECES;
-        const long long from = row >= 0 ? row * a.q_stride + (job.slice_of(u) * ar.hps + head) * DH : -1;
+        const long long from = row >= 0 ? row * a.q_stride + head * DH : -1;
         uint8_t* dst = sm + F::Q_OFF + u * F::Q_BYTES + q16 * 128 + (piece >> 3) * HALF;
-        auto place = [&](int r) { return dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4); };
-        float up = Q_SCALE;
-        uint32_t most = 0;  // the largest element of query lane & 15, as bf16 bits (where it is needed)
-#pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {  // as they are; their largest elements; scaled
-          if (pass != 1) {
-#pragma unroll 1
-            for (int e = 0; e < N; ++e) {
-              const long long at = __shfl_sync(0xffffffffu, from, e * ROWS + r0);
-              cp_async16(place(e * ROWS + r0), a.q + (at >= 0 ? at + piece * 8 : 0), at >= 0 ? 16 : 0);
-            }
-            cp_async_wait_all();
-          }
-          uint32_t fine = 0, high = 0;  // a bit per query: its largest element is Q_LOW or more; some are Q_HIGH or more
+        auto place = [&](int e) {
+          const int r = e * ROWS + r0;
+          return reinterpret_cast<uint4*>(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4));
+        };
+        auto copy = [&](int e) {
+          const long long at = __shfl_sync(0xffffffffu, from, e * ROWS + r0);
+          cp_async16(place(e), a.q + (at >= 0 ? at + piece * 8 : 0), at >= 0 ? 16 : 0);
+        };
+        auto largest = [](const uint4& v) {  // as bf16 bits
+          const uint32_t t = larger_bf16x2(larger_bf16x2(v.x, v.y), larger_bf16x2(v.z, v.w)) & 0x7FFF7FFFu;
+          return max(t >> 16, t & 0xFFFFu);
+        };
+        auto rewrite = [&](uint4* at, const uint4& v, float by) {
+          float f[8];
+          bf16x8_to_f32(v, f);
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) mul2(f[k], f[k + 1], by);
+          *at = make_uint4(f16x2_of(f[0], f[1]), f16x2_of(f[2], f[3]), f16x2_of(f[4], f[5]), f16x2_of(f[6], f[7]));
+        };
+#pragma unroll 4
+        for (int e = 0; e < N; ++e) copy(e);
+        cp_async_wait_all();
+        uint32_t fine = 0, high = 0;  // a bit per e: its largest element here is Q_LOW or more; the largest of all
+#pragma unroll 2
+        for (int e = 0; e < N; ++e) {
+          const uint4 v = *place(e);
+          const uint32_t top = largest(v);
+          high = max(high, top);
+          fine |= (uint32_t)(top >= Q_LOW) << e;
+          rewrite(place(e), v, Q_SCALE);
+        }
+#pragma unroll
+        for (int x = PIECES / 2; x > 0; x >>= 1) fine |= __shfl_xor_sync(0xffffffffu, fine, x);
+        fine = __shfl_sync(0xffffffffu, fine, (lane & (ROWS - 1)) * PIECES);  // (query lane & 15's is its bit e)
+        if (__builtin_expect(__any_sync(0xffffffffu, high >= Q_HIGH ||
+                                                         (row >= 0 && !((fine >> ((lane & 15) / ROWS)) & 1))),
+                             0)) {
+          // some are out of f16's reach, or not finite, or zeros: again, scaled
 #pragma unroll 1
           for (int e = 0; e < N; ++e) {
-            uint4* at = reinterpret_cast<uint4*>(place(e * ROWS + r0));
-            uint4 v = *at;
-            if (__builtin_expect(pass == 1, 0)) {
-              const long long src = __shfl_sync(0xffffffffu, from, e * ROWS + r0);
-              v = src >= 0 ? *reinterpret_cast<const uint4*>(a.q + src + piece * 8) : make_uint4(0u, 0u, 0u, 0u);
-            }
-            uint32_t top = larger_bf16x2(larger_bf16x2(v.x, v.y), larger_bf16x2(v.z, v.w)) & 0x7FFF7FFFu;
-            top = max(top >> 16, top & 0xFFFFu);
-            if (__builtin_expect(pass == 1, 0)) {
-#pragma unroll
-              for (int x = PIECES / 2; x > 0; x >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
-              top = __shfl_sync(0xffffffffu, top, (lane & (ROWS - 1)) * PIECES);
-              if ((lane & 15) / ROWS == e) most = top;
-              continue;
-            }
-            const uint32_t b = __ballot_sync(0xffffffffu, top >= Q_LOW);
-#pragma unroll
-            for (int r = 0; r < ROWS; ++r)
-              if ((b >> (r * PIECES)) & ((1u << PIECES) - 1)) fine |= 1u << (e * ROWS + r);
-            high = max(high, top);
-            float f[8];
-            const float by = __shfl_sync(0xffffffffu, up, e * ROWS + r0);
-            bf16x8_to_f32(v, f);
-#pragma unroll
-            for (int k = 0; k < 8; k += 2) mul2(f[k], f[k + 1], by);
-            *at = make_uint4(f16x2_of(f[0], f[1]), f16x2_of(f[2], f[3]), f16x2_of(f[4], f[5]), f16x2_of(f[6], f[7]));
-          }
-          if (pass == 0 &&
-              !__any_sync(0xffffffffu, high >= Q_HIGH || (row >= 0 && !((fine >> (lane & 15)) & 1))))
-            break;
-          if (pass == 1) {
-            if (most >= 0x7F80u) {  // not finite: the query's weights are NaN
-              up = factor = __int_as_float(0x7FC00000);
-            } else if (most != 0 && (most < Q_LOW || most >= Q_HIGH)) {
-              // the largest element is in [2^(e - 127), 2^(e - 126)): to 2^4, or as near as an f32 goes
-              const int e = max((int)(most >> 7), 1), k = min(max(131 - e, -120), 126);
+            copy(e);
+            cp_async_wait_all();
+            const uint4 v = *place(e);
+            uint32_t top = largest(v);
+#pragma unroll 1
+            for (int x = PIECES / 2; x > 0; x >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+            float up = Q_SCALE, back = 1.0f;
+            if (top >= 0x7F80u) {  // not finite: the query's weights are NaN
+              up = back = __int_as_float(0x7FC00000);
+            } else if (top != 0 && (top < Q_LOW || top >= Q_HIGH)) {
+              // the largest element is in [2^(k - 127), 2^(k - 126)): to 2^4, or as near as an f32 goes
+              const int k = min(max(131 - max((int)(top >> 7), 1), -120), 126);
               up = __uint_as_float((uint32_t)(127 + k) << 23);
-              factor = __uint_as_float((uint32_t)(127 - k) << 23) * Q_SCALE;
+              back = __uint_as_float((uint32_t)(127 - k) << 23) * Q_SCALE;
             }
+            rewrite(place(e), v, up);
+            back = __shfl_sync(0xffffffffu, back, (lane & (ROWS - 1)) * PIECES);
+            if ((lane & 15) / ROWS == e) factor = back;
           }
         }
       }
@@ -849,7 +839,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
 #pragma unroll 1
       for (int j = 0; j < n; ++j, ++sc) {
         const int i = job.ring(u, j), s = (it + i) % NS;
-        if (!await(&ss.s_full[u], sc & 1, a.status, abort)) return;
+        if (!wait(&ss.s_full[u], sc & 1, a.status, abort)) return;
         if (!idle) {
           tc_fence_after();
           const bool part = ss.part[s];
@@ -877,13 +867,60 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
               mul2(x[e], x[e + 1], t[e >> 2].x, t[e >> 2].y);
             }
           };
-          // A tile that all rows see, under the references as they are.  (32 tokens at a time, the next ones'
+          // The references to the largest of some of the tile's weights times a_t (the first of them that is above
+          // by BASE), and what was summed under the old ones with them.
+          auto move = [&](float(&top)[2]) {
+            float by[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+              top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+              by[r] = 1.0f;
+              if (top[r] - m[r] > BASE) {
+                const float now = fabsf(top[r]) <= SCORE_MAX ? ceilf(top[r]) - BASE : __int_as_float(0x7FC00000);
+                by[r] = m[r] == UNSET ? 0.0f : ex2(m[r] - now);
+                m[r] = now;
+              }
+              l[r][0] *= by[r];
+              l[r][1] *= by[r];
+            }
+            if (j > 0 && __any_sync(0xffffffffu, by[0] != 1.0f || by[1] != 1.0f)) scale_rows(o_at + rows16, DH, by);
+          };
+          // log2 of weights times a_t, under no reference
+          auto logs = [&](float* x, const float2(&t)[4]) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float gx = fmaxf(log2_of(fabsf(t[k].x)), LEAST), gy = fmaxf(log2_of(fabsf(t[k].y)), LEAST);
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                x[4 * k + 2 * r] = fmaf(x[4 * k + 2 * r], t[k].x, gx);
+                x[4 * k + 2 * r + 1] = fmaf(x[4 * k + 2 * r + 1], t[k].y, gy);
+              }
+            }
+          };
+          auto largest = [&](const float* x, float(&top)[2]) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top[(e >> 1) & 1] = fmaxf(top[(e >> 1) & 1], x[e]);
+          };
+          // A tile that all rows see, under the references as they are (an item's first one: those that its first
+          // 32 tokens ask for).  (32 tokens at a time, the next ones'
           // scores fetched meanwhile; the weights take the scores' place when none was too large.)
-          bool plain = j > 0 && !part && !scaled;
+          bool plain = !part && !scaled;
           if (__builtin_expect(plain, 1)) {
             uint32_t raw[2][16], p[4][8];
             float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
             ld_rows(s_at, raw[0]);
+            if (__builtin_expect(j == 0, 0)) {
+              float2 t[4];
+              float top[2] = {-INFINITY, -INFINITY};
+              factors(0, t);
+              tc_wait_ld();
+              loaded16(raw[0]);
+              logs(reinterpret_cast<float*>(raw[0]), t);
+              largest(reinterpret_cast<float*>(raw[0]), top);
+              move(top);
+              ld_rows(s_at, raw[0]);
+            }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               float* x = reinterpret_cast<float*>(raw[c & 1]);
@@ -908,8 +945,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
             }
           }
           if (__builtin_expect(!plain, 0)) {
-            // Any tile: first the references to the largest of its weights times a_t (and what was summed under the
-            // old ones with them).  In rolled loops: most of this runs once an item, and is fetched for it.
+            // Any tile: first the references.
             float f[2] = {1.0f, 1.0f};
             if (scaled) {
 #pragma unroll
@@ -939,54 +975,24 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
             };
             float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t raw[16], w[2];
-              float* x = reinterpret_cast<float*>(raw);
-              float2 t[4];
-              factors(c, t);
-              load(c, raw, w);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float gx = fmaxf(log2_of(fabsf(t[k].x)), LEAST), gy = fmaxf(log2_of(fabsf(t[k].y)), LEAST);
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                  x[4 * k + 2 * r] = fmaf(x[4 * k + 2 * r], t[k].x, gx);
-                  x[4 * k + 2 * r + 1] = fmaf(x[4 * k + 2 * r + 1], t[k].y, gy);
-                }
-              }
-              if (part) hide(x, w, -INFINITY);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) top[(e >> 1) & 1] = fmaxf(top[(e >> 1) & 1], x[e]);
-            }
-            float by[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-              top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-              by[r] = 1.0f;
-              if (top[r] - m[r] > BASE) {
-                const float now = fabsf(top[r]) <= SCORE_MAX ? ceilf(top[r]) - BASE : __int_as_float(0x7FC00000);
-                by[r] = m[r] == UNSET ? 0.0f : ex2(m[r] - now);
-                m[r] = now;
-              }
-              l[r][0] *= by[r];
-              l[r][1] *= by[r];
-            }
-            if (j > 0 && __any_sync(0xffffffffu, by[0] != 1.0f || by[1] != 1.0f)) scale_rows(o_at + rows16, DH, by);
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 8; ++c) {  // the references; the weights
+              if (c == 4) move(top);
               uint32_t raw[16], w[2], p[8];
               float* x = reinterpret_cast<float*>(raw);
               float2 t[4];
-              factors(c, t);
-              load(c, raw, w);
-              exponents(x, t);
+              factors(c & 3, t);
+              load(c & 3, raw, w);
+              if (c < 4) logs(x, t); else exponents(x, t);
               if (part) hide(x, w, -INFINITY);
+              if (c < 4) {
+                largest(x, top);
+                continue;
+              }
               weights(x, t, l);
               if (bad) hide(x, w, 0.0f);
 #pragma unroll
               for (int e = 0; e < 16; e += 2) p[e / 2] = f16x2_of(x[e], x[e + 1]);
-              st_rows(s_at + 16 * c, p);  // (over scores that were read)
+              st_rows(s_at + 16 * (c & 3), p);  // (over scores that were read)
             }
           }
           tc_wait_st();
@@ -995,7 +1001,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
         __syncwarp();
         if (lane == 0) mbar_arrive(&ss.p_full[u]);
       }
-      if (!await(&ss.o_full[u], item & 1, a.status, abort)) return;
+      if (!wait(&ss.o_full[u], item & 1, a.status, abort)) return;
       tc_fence_after();
       it += job.count();
 
@@ -1010,14 +1016,19 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
         t = __shfl_sync(0xffffffffu, t, (lane & 7) * 4);
         if (((lane >> 3) & 1) == r) m_row = from, l_row = t;
       }
-      const int q = 32 * quad + lane;  // of the quadrant's queries
+      long long to = 0;  // where the piece goes (0: there is no such query)
+      if (row >= 0)
+        to = reinterpret_cast<long long>(
+            (job.begins ? ar.home : ar.over) +
+            (job.begins ? ((size_t)(job.g < a.n_prefix ? 0 : ar.max_rows) + row) * a.n_q + head
+                        : (size_t)blockIdx.x * (2 * BLOCK) + (mode == TWO_TILES ? 0 : u * BLOCK) + ql) *
+                F::PART_LD);
       if (mode != TWO_TILES) {
         if (!idle) {
           // whole pieces through shared memory, eight rows at a time, by a copy for every run of them (stored from
           // registers, or by a copy each, they took 4500 cycles)
-          float* to = piece_of(q16 + (lane & 15));
-          const long long prev = __shfl_up_sync(0xffffffffu, reinterpret_cast<long long>(to), 1);
-          const bool head_of_run = to && ((lane & 7) == 0 || prev + F::PART_LD * 4 != reinterpret_cast<long long>(to));
+          const long long prev = __shfl_up_sync(0xffffffffu, to, 1);
+          const bool head_of_run = to && ((lane & 7) == 0 || prev + F::PART_LD * 4 != to);
           const uint32_t ends = __ballot_sync(0xffffffffu, head_of_run || !to);
           uint8_t* out = sm + F::Q_OFF + u * F::Q_BYTES + (4 * half + quad) * (F::Q_BYTES / 8);
           float* mine = reinterpret_cast<float*>(out) + (lane >> 2) * F::PART_LD + 2 * (lane & 3);
@@ -1048,44 +1059,53 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
             __syncwarp();
             if (lane >> 3 == r && head_of_run) {
               const int first = lane & 7, n = __ffs((ends >> (lane + 1) | 1u << (7 - first)));
-              bulk_store(to, reinterpret_cast<float*>(out) + first * F::PART_LD, n * F::PART_LD * 4);
+              bulk_store(reinterpret_cast<void*>(to), reinterpret_cast<float*>(out) + first * F::PART_LD, n * F::PART_LD * 4);
             }
             bulk_commit();
           }
           bulk_wait_read();
         }
-      } else {  // both streams' O in the larger m, a quarter of the dimensions a warp
+      } else {  // both streams' O in the larger m, half of the dimensions a stream
         auto meet = [&] {
           __syncwarp();
           if (lane == 0) mbar_arrive(&ss.merge);
-          return await(&ss.merge, mc++ & 1, a.status, abort);
+          return wait(&ss.merge, mc++ & 1, a.status, abort);
         };
-        if (lane < 16) ss.ml[u][q16 + lane] = make_float2(m_row, l_row);
+        if (lane < 16) ss.ml[u][ql] = make_float2(m_row, l_row);
         if (!meet()) return;
-        float* to = piece_of(q);
-        const float2 x = ss.ml[0][q], y = ss.ml[1][q];
+        const float2 x = ss.ml[0][ql], y = ss.ml[1][ql];
         m_row = fmaxf(x.x, y.x);
         // (a NaN stays one)
         const float fx = x.y != x.y ? 1.0f : x.x == UNSET ? 0.0f : ex2(x.x - m_row);
         const float fy = y.y != y.y ? 1.0f : y.x == UNSET ? 0.0f : ex2(y.x - m_row);
         l_row = (fx != 0.0f ? x.y * fx : 0.0f) + (fy != 0.0f ? y.y * fy : 0.0f);
-        if (to && u == 0 && half == 0) *reinterpret_cast<float2*>(to) = make_float2(m_row, l_row);
-        const int first = (2 * u + half) * (DH / 4);
+        if (to && u == 0 && lane < 16) *reinterpret_cast<float2*>(to) = make_float2(m_row, l_row);
+        if (!idle) {
 #pragma unroll 1
-        for (int c = first; c < first + DH / 4; c += 8) {
-          float v[8], z[8];
-          tc_ld8(lanes + F::O_COL + c, v);
-          tc_ld8(lanes + F::O_COL + DH + c, z);
-          tc_wait_ld();
-          tc_loaded(v);
-          tc_loaded(z);
-          uint32_t w[8];
+          for (int c = u * (DH / 2); c < (u + 1) * (DH / 2); c += 32) {
+            uint32_t v[16], z[16];
+            ld_rows(o_at - DH * u + rows16 + c, v);
+            ld_rows(o_at - DH * u + rows16 + DH + c, z);
+            tc_wait_ld();
+            loaded16(v);
+            loaded16(z);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float p0 = fx != 0.0f ? v[e] * fx : 0.0f, p1 = fy != 0.0f ? z[e] * fy : 0.0f;
-            w[e] = __float_as_uint(p0 + p1);
+            for (int r = 0; r < 2; ++r) {
+              const int of = (lane >> 2) + 8 * r;
+              const float gx = __shfl_sync(0xffffffffu, fx, of), gy = __shfl_sync(0xffffffffu, fy, of);
+              float* at = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, to, of));
+              if (!at) continue;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float o[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+                  o[b] = (gx != 0.0f ? __uint_as_float(v[4 * k + 2 * r + b]) * gx : 0.0f) +
+                         (gy != 0.0f ? __uint_as_float(z[4 * k + 2 * r + b]) * gy : 0.0f);
+                *reinterpret_cast<float2*>(at + 8 + c + 8 * k + 2 * (lane & 3)) = make_float2(o[0], o[1]);
+              }
+            }
           }
-          if (to) st_global8(to + 8 + c, w);
         }
         tc_fence_before();
         if (!meet()) return;  // (the next item's products go over both)
@@ -1114,7 +1134,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_shared_kernel(const __gr
   const SharedArgs& a = ar.a;
   const int r = blockIdx.x, h = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int dh = a.head_dim, d = 4 * lane & (dh - 1), step = 128 / dh, own = lane * 4 / dh;
-  const int slice = h / ar.hps, ld = dh + 8;
+  const int slice = ar.by_hps(h), ld = dh + 8;
   pdl_trigger();
   pdl_wait();
   if (h >= a.n_q) return;
@@ -1126,7 +1146,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_shared_kernel(const __gr
     n[k] = 0, over[k] = 0;
     if (v.y == 0) continue;
     const Items it(ar, v.y, v.z);
-    const int block = v.w / ar.rows_per, of_pairs = it.of_pairs(ar), pairs = it.blocks >> 1;
+    const int block = ar.by_rows(v.w), of_pairs = it.of_pairs(ar), pairs = it.blocks >> 1;
     int item, len = it.len, lane0 = 0;
     if (block < 2 * pairs) {
       item = slice * pairs + (block >> 1);
@@ -1237,6 +1257,9 @@ cudaError_t launch_attend_shared(const Launch& L, const SharedArgs& a, uint8_t* 
   ar.slices = a.kv_dim / a.head_dim;
   ar.hps = a.n_q / ar.slices;
   ar.rows_per = BLOCK / ar.hps;
+  ar.by_page = Divisor::of(a.kv.block_size);
+  ar.by_hps = Divisor::of(ar.hps);
+  ar.by_rows = Divisor::of(ar.rows_per);
   ar.info = reinterpret_cast<int*>(ws + l.info);
   ar.home = reinterpret_cast<float*>(ws + l.home);
   ar.over = reinterpret_cast<float*>(ws + l.over);
