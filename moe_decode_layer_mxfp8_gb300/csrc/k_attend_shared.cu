@@ -37,7 +37,7 @@ constexpr int WIDEN_WARP = SOFT_WARPS, MMA_WARP = WIDEN_WARP + WIDEN_WARPS, LOAD
 constexpr int THREADS = 32 * (ROWS_WARP + 2), SOFT = 32 * WIDEN_WARP;
 constexpr int MAX_GROUPS = MAX_PREFIX + MAX_REQ;
 constexpr int BLOCK = 128;       // queries
-constexpr int EXTRA = 3;         // what an item costs a CTA beside its steps, in steps
+constexpr int EXTRA = 4;         // what an item costs a CTA beside its steps, in steps
 constexpr int HALF = TT * 128;   // bytes of 64 dimensions of a tile, or a block, in f16
 constexpr int JOBS = 4;          // items whose rows are made ahead
 constexpr float BASE = 6.0f, LEAST = -90.0f;  // log2 of the weights times a_t that m puts at most; a_t below
@@ -98,7 +98,7 @@ struct Args {
   SharedArgs a;
   float* home;   // pieces: [2][max_rows][n_q], of those that begin an item; prefixes', then own tokens'
   float* over;   // [CTAs][2 * BLOCK], of a CTA's item that began before it
-  int* info;     // [rows][8]
+  int* info;     // [rows][slices][2][2]: pieces, and the second one's place, of a prefix and of own tokens
   int max_rows;
 };
 
@@ -715,12 +715,13 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
         if (lane == 0) mbar_arrive(&ss.j_full[k]);
         if (!more) break;
       }
-      // where the join finds a row's pieces: per kind of group, its first unit in the line, tiles, rows and
-      // the row's rank (tiles 0: none)
+      // where the join finds the pieces of a row's queries in a slice: how many of its prefix's tokens, and of its
+      // own, and the place of the second of each
+      const Cut cut(plan.pre[a.n_prefix + a.n_req], gridDim.x);
 #pragma unroll 1
       for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const int b = plan.req[r], g = b < 0 ? -1 : plan.pfx[b];
-        int own = 0, pre = 0;
+        int own = 0, pre = 0;  // the row's rank among those of its groups
         if (b >= 0) {
 #pragma unroll 1
           for (int i = lane; i < r; i += 32) {
@@ -731,13 +732,30 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
         }
         own = __reduce_add_sync(0xffffffffu, own);
         pre = __reduce_add_sync(0xffffffffu, pre);
-        if (lane < 2) {
-          const int at = b < 0 ? -1 : lane ? a.n_prefix + b : g;
-          int4 v = {0, 0, 0, lane ? own : pre};
-          if (at >= 0) v.x = plan.pre[at], v.y = items_of(ar, plan, at).tiles, v.z = plan.cnt[at];
-          reinterpret_cast<int4*>(ar.info)[2 * r + lane] = v;
+#pragma unroll 1
+        for (int i = lane; i < 2 * ar.slices; i += 32) {
+          const int at = b < 0 ? -1 : i & 1 ? a.n_prefix + b : g, rank = i & 1 ? own : pre, slice = i >> 1;
+          int2 v = {0, 0};
+          if (at >= 0) {
+            const Items it = items_of(ar, plan, at);
+            const int block = ar.by_rows(rank), pairs = it.blocks >> 1;
+            int item, len = it.len, first = 0;
+            if (block < 2 * pairs) {
+              item = slice * pairs + (block >> 1);
+              first = (block & 1) * BLOCK;
+            } else {
+              item = it.of_pairs(ar) + (slice >> 1);
+              if (item < it.whole(ar)) first = (slice & 1) * BLOCK;
+              else len = it.half;
+            }
+            if (it.tiles) {
+              const int from = plan.pre[at] + item * it.len, k = cut.team_of(from + EXTRA);
+              v = make_int2(cut.team_of(from + len - 1) - k + 1,
+                            (k + 1) * (2 * BLOCK) + first + (rank - block * ar.rows_per) * ar.hps);
+            }
+          }
+          reinterpret_cast<int2*>(ar.info)[(size_t)r * 2 * ar.slices + i] = v;
         }
-        if (lane == 0 && r == 0) ar.info[8 * a.rows] = plan.pre[a.n_prefix + a.n_req];
       }
     }
   } else [&] {
@@ -1127,43 +1145,24 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
   }
 }
 
-// Joins the pieces of a (row, head), of its prefix and its own tokens: a warp each, 4 dimensions a lane
-// (64 wide: the half warps take every other piece).
-constexpr int JOIN_WARPS = 4, AHEAD = 4;
-__global__ void __launch_bounds__(JOIN_WARPS * 32) join_shared_kernel(const __grid_constant__ Args ar, int ctas) {
+// Joins the pieces of a (row, head), of its prefix and its own tokens: `team` warps each, which take them in
+// turn; 4 dimensions a lane (64 wide: the half warps take every other piece).
+constexpr int JOIN_WARPS = 4, MAX_TEAM = 8, AHEAD = 6, TEAM_WARPS = 32;
+__global__ void __launch_bounds__(MAX_TEAM * 32) join_shared_kernel(const __grid_constant__ Args ar, int team) {
+  __shared__ float2 ml_of[MAX_TEAM];
+  __shared__ float4 num_of[MAX_TEAM][32];
   const SharedArgs& a = ar.a;
-  const int r = blockIdx.x, h = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mate = warp & (team - 1);
+  const int r = blockIdx.x, h = (blockIdx.y * (blockDim.x >> 5) + warp) / team;
   const int dh = a.head_dim, d = 4 * lane & (dh - 1), step = 128 / dh, own = lane * 4 / dh;
   const int slice = ar.by_hps(h), ld = dh + 8;
   pdl_trigger();
   pdl_wait();
-  if (h >= a.n_q) return;
-  const Cut cut(ar.info[8 * a.rows], ctas);
-  int n[2], over[2];  // a kind's pieces; its second one's place
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int4 v = reinterpret_cast<const int4*>(ar.info)[2 * r + k];
-    n[k] = 0, over[k] = 0;
-    if (v.y == 0) continue;
-    const Items it(ar, v.y, v.z);
-    const int block = ar.by_rows(v.w), of_pairs = it.of_pairs(ar), pairs = it.blocks >> 1;
-    int item, len = it.len, lane0 = 0;
-    if (block < 2 * pairs) {
-      item = slice * pairs + (block >> 1);
-      lane0 = (block & 1) * BLOCK;
-    } else {
-      item = of_pairs + (slice >> 1);
-      if (item < it.whole(ar)) lane0 = (slice & 1) * BLOCK;
-      else len = it.half;
-    }
-    const int from = v.x + item * it.len;
-    const int k0 = cut.team_of(from + EXTRA), k1 = cut.team_of(from + len - 1);
-    n[k] = k1 - k0 + 1;
-    over[k] = (k0 + 1) * (2 * BLOCK) + lane0 + (v.w - block * ar.rows_per) * ar.hps + (h - slice * ar.hps);
-  }
-  const int all = n[0] + n[1];
-  auto piece = [&](int i) -> const float* {
-    const int k = i < n[0] ? 0 : 1, x = k ? i - n[0] : i;
+  const int4 info = h < a.n_q ? reinterpret_cast<const int4*>(ar.info)[r * ar.slices + slice] : make_int4(0, 0, 0, 0);
+  const int n[2] = {info.x, info.z}, in_slice = h - slice * ar.hps, over[2] = {info.y + in_slice, info.w + in_slice};
+  const int all = (n[0] + n[1] - mate + team - 1) / team;  // this warp's
+  auto piece = [&](int mine) -> const float* {
+    const int i = mine * team + mate, k = i < n[0] ? 0 : 1, x = k ? i - n[0] : i;
     return x == 0 ? ar.home + (((size_t)k * ar.max_rows + r) * a.n_q + h) * ld
                   : ar.over + ((size_t)over[k] + (size_t)(x - 1) * (2 * BLOCK)) * ld;
   };
@@ -1203,6 +1202,29 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) join_shared_kernel(const __gr
     num.x += __shfl_xor_sync(0xffffffffu, num.x, 16), num.y += __shfl_xor_sync(0xffffffffu, num.y, 16);
     num.z += __shfl_xor_sync(0xffffffffu, num.z, 16), num.w += __shfl_xor_sync(0xffffffffu, num.w, 16);
   }
+  if (team > 1) {
+    if (lane == 0) ml_of[warp] = make_float2(m, den);
+    num_of[warp][lane] = num;
+    __syncthreads();
+    if (mate != 0) return;
+    float to = m;
+#pragma unroll 1
+    for (int w = 1; w < team; ++w) to = fmaxf(to, ml_of[warp + w].x);
+    den = 0.0f;
+    num = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (int w = 0; w < team; ++w) {
+      const float2 ml = ml_of[warp + w];
+      const float4 x = num_of[warp + w][lane];
+      const float f = ml.y != ml.y ? 1.0f : ml.y == 0.0f ? 0.0f : ex2(ml.x - to);
+      if (f == 0.0f) continue;
+      den = fmaf(f, ml.y, den);
+      num.x = fmaf(f, x.x, num.x), num.y = fmaf(f, x.y, num.y);
+      num.z = fmaf(f, x.z, num.z), num.w = fmaf(f, x.w, num.w);
+    }
+    m = to;
+  }
+  if (h >= a.n_q) return;
   // (O was summed with a_t in the scales' place)
   const float inv = den == 0.0f ? 0.0f : 1.0f / (den * (a.scale * (LOG2E / Q_SCALE)));
   if (den == 0.0f) num = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -1229,7 +1251,7 @@ Layout layout(int max_rows, int n_q, int head_dim, int sms) {
   Layout l;
   const size_t piece = (size_t)(head_dim + 8) * 4;  // (Form::PART_LD)
   l.info = 0;
-  l.home = ((size_t)max_rows * 32 + 16 + 255) / 256 * 256;
+  l.home = ((size_t)max_rows * n_q * 16 + 255) / 256 * 256;  // (as many slices as heads at most)
   l.over = l.home + 2 * (size_t)max_rows * n_q * piece;
   l.bytes = l.over + (size_t)sms * 2 * BLOCK * piece;
   return l;
@@ -1268,9 +1290,12 @@ cudaError_t launch_attend_shared(const Launch& L, const SharedArgs& a, uint8_t* 
   cudaError_t e = a.head_dim == 128
                       ? launch_ex(L, dim3(sms), dim3(THREADS), Form<128>::SMEM_BYTES, attend_shared_kernel<128>, ar)
                       : launch_ex(L, dim3(sms), dim3(THREADS), Form<64>::SMEM_BYTES, attend_shared_kernel<64>, ar);
+  // Few queries have many pieces each: teams of warps, as many as the GPU holds at once.
+  int team = 1;
+  while (team < MAX_TEAM && 2LL * team * a.rows * a.n_q <= TEAM_WARPS * sms) team *= 2;
+  const int warps = team > JOIN_WARPS ? team : JOIN_WARPS;
   if (e == cudaSuccess)
-    e = launch_ex(L, dim3(a.rows, (a.n_q + JOIN_WARPS - 1) / JOIN_WARPS), dim3(JOIN_WARPS * 32), 0, join_shared_kernel,
-                  ar, sms);
+    e = launch_ex(L, dim3(a.rows, (a.n_q * team + warps - 1) / warps), dim3(warps * 32), 0, join_shared_kernel, ar, team);
   return e;
 }
 
