@@ -54,6 +54,7 @@ struct Plan {
   int pre[MAX_GROUPS + 4];  // [groups + 1] the line's steps of all groups before
   int end[MAX_GROUPS];      // one behind the last token that a row sees
   int first[MAX_GROUPS];    // the first
+  int tiles[MAX_GROUPS];    // from the one's to the other's
   int len[MAX_PREFIX];      // tokens of a prefix
   int hi[MAX_ROWS];         // a row's last token
   short cnt[MAX_GROUPS];    // rows
@@ -126,8 +127,7 @@ struct Items {
   __device__ int count(const Args& ar) const { return whole(ar) + (blocks & ar.slices & 1); }
 };
 __device__ __forceinline__ Items items_of(const Args& ar, const Plan& p, int g) {
-  const int n = p.cnt[g], lo = p.first[g], end = end_of(ar.a, p, g);
-  return Items(ar, n == 0 || end <= lo ? 0 : ((end - 1) >> 7) - (lo >> 7) + 1, n);
+  return Items(ar, p.tiles[g], p.cnt[g]);
 }
 
 // A CTA's part of an item: the steps from s0 on, of a tile for each stream.
@@ -286,13 +286,12 @@ __device__ __forceinline__ void derive_plan(const Args& ar, Plan& plan) {
   for (int g = tid; g < groups; g += THREADS) plan.end[g] = 0, plan.cnt[g] = 0, plan.first[g] = 0;
   pdl_trigger();
   pdl_wait();
-  constexpr int ROWS = (MAX_ROWS + THREADS - 1) / THREADS;
-  int p[ROWS], b[ROWS];
-#pragma unroll
-  for (int k = 0; k < ROWS; ++k) {
-    const int r = tid + k * THREADS;
-    p[k] = -1, b[k] = -1;
-    if (r < a.rows) p[k] = min(a.positions[r], 0x7FFFFFFE), b[k] = a.row_req[r];
+  // (loops that most steps run once are kept small: this code runs once, and comes from memory)
+#pragma unroll 1
+  for (int r = tid; r < a.rows; r += THREADS) {
+    const int p = a.positions[r], b = a.row_req[r];
+    plan.hi[r] = min(p, 0x7FFFFFFE);
+    plan.req[r] = (short)(b < 0 || b >= a.n_req ? -1 : b);
   }
   static_assert(MAX_REQ <= THREADS && MAX_PREFIX <= THREADS, "a request a thread");
   int g = -1;
@@ -305,34 +304,41 @@ __device__ __forceinline__ void derive_plan(const Args& ar, Plan& plan) {
   __syncthreads();
   if (g >= 0) plan.first[np + tid] = plan.len[g];
   // a request's rows and their largest position
-#pragma unroll
-  for (int k = 0; k < ROWS; ++k) {
-    const int r = tid + k * THREADS;
-    const bool live = p[k] >= 0 && b[k] >= 0 && b[k] < a.n_req && plan.pfx[b[k]] >= -1;
-    if (p[k] >= 0 && !live && tell) atomicOr(a.status, ST_UNMAPPED_PAGE);
-    if (!live) b[k] = -1;
-    if (r < a.rows) plan.req[r] = (short)b[k];
-    if (live) atomicMax(&plan.end[np + b[k]], p[k] + 1);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < ROWS; ++k) {
-    const int r = tid + k * THREADS;
-    if (b[k] < 0) continue;
-    const int hi = a.causal ? p[k] : plan.end[np + b[k]] - 1, of = plan.pfx[b[k]], len = plan.first[np + b[k]];
-    plan.hi[r] = hi;
-    // (16-bit counters: the words that hold them)
-    auto count = [&](int i) { atomicAdd(reinterpret_cast<int*>(plan.cnt) + (i >> 1), i & 1 ? 1 << 16 : 1); };
-    count(np + b[k]);
-    if (of >= 0) {
-      count(of);
-      atomicMax(&plan.end[of], min(min(hi + 1, len), pcap));
-      if (min(hi + 1, len) > pcap && tell) atomicOr(a.status, ST_UNMAPPED_PAGE);
+#pragma unroll 1
+  for (int r = tid; r < a.rows; r += THREADS) {
+    const int p = plan.hi[r], b = plan.req[r];
+    if (p >= 0 && b >= 0 && plan.pfx[b] >= -1) {
+      atomicMax(&plan.end[np + b], p + 1);
+    } else {
+      plan.req[r] = -1;
+      if (p >= 0 && tell) atomicOr(a.status, ST_UNMAPPED_PAGE);
     }
-    if (hi >= cap && hi >= len && tell) atomicOr(a.status, ST_UNMAPPED_PAGE);
   }
   __syncthreads();
-  if (tid < groups) plan.pre[tid + 1] = items_of(ar, plan, tid).units(ar);
+#pragma unroll 1
+  for (int r = tid; r < a.rows; r += THREADS) {
+    const int b = plan.req[r];
+    if (b < 0) continue;
+    const int hi = a.causal ? plan.hi[r] : plan.end[np + b] - 1, of = plan.pfx[b], len = plan.first[np + b];
+    plan.hi[r] = hi;
+    bool beyond = hi >= cap && hi >= len;
+    // (16-bit counters: the words that hold them)
+#pragma unroll 1
+    for (int i = np + b, k = 0; k < 2 && i >= 0; ++k, i = of)
+      atomicAdd(reinterpret_cast<int*>(plan.cnt) + (i >> 1), i & 1 ? 1 << 16 : 1);
+    if (of >= 0) {
+      const int end = min(hi + 1, len);
+      beyond |= end > pcap;
+      atomicMax(&plan.end[of], min(end, pcap));
+    }
+    if (beyond && tell) atomicOr(a.status, ST_UNMAPPED_PAGE);
+  }
+  __syncthreads();
+  if (tid < groups) {
+    const int lo = plan.first[tid], end = end_of(a, plan, tid);
+    plan.tiles[tid] = plan.cnt[tid] == 0 || end <= lo ? 0 : ((end - 1) >> 7) - (lo >> 7) + 1;
+    plan.pre[tid + 1] = items_of(ar, plan, tid).units(ar);
+  }
   static_assert(MAX_GROUPS <= THREADS, "a group a thread");
 }
 
@@ -505,7 +511,9 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
   __shared__ __align__(16) Shared ss;
   volatile int* abort = &ss.abort;
   Plan& plan = *reinterpret_cast<Plan*>(sm + F::PLAN_OFF);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the warp from one lane: the compiler then knows the roles to be whole warps, and leaves out a fifth of
+  // the code, that for lanes apart; 256 requests 152 -> 144 us)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (tid < BARRIERS) {
     mbar_init(ss.full + tid, arrivals(tid));
@@ -1159,25 +1167,34 @@ __global__ void __launch_bounds__(MAX_TEAM * 32) join_shared_kernel(const __grid
   pdl_trigger();
   pdl_wait();
   const int4 info = h < a.n_q ? reinterpret_cast<const int4*>(ar.info)[r * ar.slices + slice] : make_int4(0, 0, 0, 0);
-  const int n[2] = {info.x, info.z}, in_slice = h - slice * ar.hps, over[2] = {info.y + in_slice, info.w + in_slice};
-  const int all = (n[0] + n[1] - mate + team - 1) / team;  // this warp's
-  auto piece = [&](int mine) -> const float* {
-    const int i = mine * team + mate, k = i < n[0] ? 0 : 1, x = k ? i - n[0] : i;
-    return x == 0 ? ar.home + (((size_t)k * ar.max_rows + r) * a.n_q + h) * ld
-                  : ar.over + ((size_t)over[k] + (size_t)(x - 1) * (2 * BLOCK)) * ld;
-  };
-  auto fetch = [&](int i) { return *reinterpret_cast<const float4*>(piece(i) + 8 + d); };
+  // where the pieces are, in floats behind `home` (which `over` is behind): a kind's first one, its others
+  const int home = (r * a.n_q + h) * ld, next = 2 * BLOCK * ld;
+  const int over = (int)(ar.over - ar.home) + (h - slice * ar.hps) * ld;
+  // this warp's (from one lane, so that the compiler knows the loops to be the whole warp's)
+  const int all = __shfl_sync(0xffffffffu, (info.x + info.z - mate + team - 1) / team, 0);
   float m = UNSET, den = 0.0f;
   float4 num = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
   for (int b = 0; b < all; b += 32) {
     const int in = min(32, all - b);
+    int at = home;  // a piece a lane
     float2 ml = {UNSET, 0.0f};
-    if (lane < in) ml = *reinterpret_cast<const float2*>(piece(b + lane));
+    if (lane < in) {
+      int i = (b + lane) * team + mate;
+      const bool own_tokens = i >= info.x;
+      if (own_tokens) i -= info.x;
+      at = i == 0 ? home + (own_tokens ? ar.max_rows * a.n_q * ld : 0)
+                  : over + (own_tokens ? info.w : info.y) * ld + (i - 1) * next;
+      ml = *reinterpret_cast<const float2*>(ar.home + at);
+    }
     float4 x[AHEAD];
+    auto fetch = [&](int i) {  // (those behind the last: the last again, without a part)
 #pragma unroll
-    for (int e = 0; e < AHEAD; ++e)
-      if (own + step * e < in) x[e] = fetch(b + own + step * e);
+      for (int e = 0; e < AHEAD; ++e)
+        x[e] = *reinterpret_cast<const float4*>(
+            ar.home + __shfl_sync(0xffffffffu, at, min(i + own + step * e, in - 1)) + 8 + d);
+    };
+    fetch(0);
     const float to = fmaxf(m, warp_max(ml.x)), old = m == to ? 1.0f : ex2(m - to);
     // (a piece that saw nothing has no part; a NaN stays one)
     const float f = ml.y != ml.y ? 1.0f : ml.y == 0.0f ? 0.0f : ex2(ml.x - to);
@@ -1185,17 +1202,19 @@ __global__ void __launch_bounds__(MAX_TEAM * 32) join_shared_kernel(const __grid
     den = fmaf(den, old, warp_sum(f != 0.0f ? f * ml.y : 0.0f));
     num.x *= old, num.y *= old, num.z *= old, num.w *= old;
 #pragma unroll 1
-    for (int i = 0; i < in; i += step * AHEAD) {
+    for (int i = 0;;) {
 #pragma unroll
       for (int e = 0; e < AHEAD; ++e) {
-        const int at = i + own + step * e;
-        const float g = __shfl_sync(0xffffffffu, f, at & 31);
-        if (at < in && g != 0.0f) {
+        const int k = i + own + step * e;
+        float g = __shfl_sync(0xffffffffu, f, k & 31);
+        if (k < in && g != 0.0f) {
           num.x = fmaf(g, x[e].x, num.x), num.y = fmaf(g, x[e].y, num.y);
           num.z = fmaf(g, x[e].z, num.z), num.w = fmaf(g, x[e].w, num.w);
         }
-        if (at + step * AHEAD < in) x[e] = fetch(b + at + step * AHEAD);
       }
+      i += step * AHEAD;
+      if (i >= in) break;
+      fetch(i);
     }
   }
   if (dh == 64) {
