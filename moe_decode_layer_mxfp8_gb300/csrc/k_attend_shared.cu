@@ -22,6 +22,7 @@
 // rows, and tells the join where pieces are (23 makes the registers' split come out).
 // Every wait is for an mbarrier, and bounded; one that runs out is reported and ends its role, and with it
 // the others' waits.  Copies and products on their way are waited for before the CTA ends.
+#include <cfloat>
 #include <cstddef>
 
 #include "attend_tc.cuh"
@@ -237,6 +238,13 @@ __device__ __forceinline__ void ld_rows(uint32_t taddr, uint32_t (&r)[16]) {
 __device__ __forceinline__ void loaded16(uint32_t (&r)[16]) {
   asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+__device__ __forceinline__ void put_rows(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 // 16 rows x 16 columns of packed pairs: registers 2 k + h are row lane / 4 + 8 h, column 4 k + (lane & 3).
 __device__ __forceinline__ void st_rows(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -568,6 +576,23 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
           const uint8_t* src = sm + F::K_OFF + st * F::NARROW + t0 * DH + lane * 16;
           uint8_t* dst = sm + F::V_OFF + s * F::WIDE + (piece >> 2) * HALF;
           uint32_t nan = 0;
+          if (__builtin_expect(part, 0)) {
+            // a NaN code that some row must not see would reach it as 0 * NaN: it is a 0 then, and the token's
+            // factor is NaN
+#pragma unroll 1
+            for (int e = 0; e < N; ++e) {
+              uint4* at = reinterpret_cast<uint4*>(const_cast<uint8_t*>(src) + e * ROWS * DH);
+              const uint4 v = *at, c = without_nan(v);
+              const uint32_t bad = __ballot_sync(0xffffffffu, c.x != v.x || c.y != v.y || c.z != v.z || c.w != v.w);
+              if (__builtin_expect(bad, 0)) {
+                *at = c;
+#pragma unroll 1
+                for (int k = 0; k < ROWS; ++k)
+                  if ((bad >> (k * PIECES)) & ((1u << PIECES) - 1)) nan |= 1u << (e * ROWS + k);
+              }
+            }
+            fence_proxy_async_shared();  // (ahead of the next copy to this place)
+          }
 #pragma unroll 1
           for (int e0 = 0; e0 < N; e0 += 4) {
             uint4 v[4];
@@ -575,19 +600,6 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
             for (int e = 0; e < 4; ++e) v[e] = lds128(src + (e0 + e) * ROWS * DH);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if (__builtin_expect(part, 0)) {
-                // a NaN code that some row must not see would reach it as 0 * NaN: it is a 0 here, and the
-                // token's factor is NaN
-                const uint4 c = without_nan(v[e]);
-                const uint32_t bad =
-                    __ballot_sync(0xffffffffu, c.x != v[e].x || c.y != v[e].y || c.z != v[e].z || c.w != v[e].w);
-                v[e] = c;
-                if (__builtin_expect(bad, 0)) {
-#pragma unroll 1
-                  for (int k = 0; k < ROWS; ++k)
-                    if ((bad >> (k * PIECES)) & ((1u << PIECES) - 1)) nan |= 1u << ((e0 + e) * ROWS + k);
-                }
-              }
               const int row = t0 + (e0 + e) * ROWS + r0, c = 2 * (piece & 3) + odd;
               uint4 x, y;
               uint32_t f[2];
@@ -604,7 +616,8 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
           {  // a token a lane
             static_assert(WIDEN_TOKENS == 32, "a token a lane");
             const bool there = (ok >> lane) & 1, fin = fabsf(raw) <= SCALE_MAX && !((nan >> lane) & 1);
-            const float f = !there ? 0.0f : fin ? raw * to_log2 : __int_as_float(0x7FC00000);
+            float f = !there ? 0.0f : fin ? raw * to_log2 : __int_as_float(0x7FC00000);
+            if (f == 0.0f) f = FLT_MIN;  // (as good as 0, and infinity times it is infinity)
             reinterpret_cast<float*>(sm + F::TOK_OFF)[s * TT + token_slot(t0 + lane)] = f;
             const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(f)));  // (a NaN stays one)
             if (lane == 0) ss.most[s][warp - WIDEN_WARP] = __uint_as_float(most);
@@ -649,10 +662,10 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
               if (ok && elect_one()) {
                 const int s = (it + job->ring(u, j)) % NS;
                 const uint32_t oc = tmem + F::O_COL + DH * u, pcol = tmem + 128 * u;
-                uint64_t vd = v0 + s * (F::WIDE / 16);
+                const uint64_t vd = v0 + s * (F::WIDE / 16);
                 tc_fence_after();
-#pragma unroll 2
-                for (int k = 0; k < TT / 16; ++k, vd += 2048 / 16) mma_ts(oc, pcol + 8 * k, vd, IO, j > 0 || k > 0);
+#pragma unroll
+                for (int k = 0; k < TT / 16; ++k) mma_ts(oc, pcol + 8 * k, vd + k * (2048 / 16), IO, j > 0 || k > 0);
                 if (job->mode != TWO_BLOCKS || u == 1) tc_commit(&ss.v_free[s]);
                 if (j + 1 == n) tc_commit(&ss.o_full[u]);
               }
@@ -664,7 +677,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
             if (ok && elect_one()) {
               tc_fence_after();
               const uint64_t qd = q0 + u * (F::Q_BYTES / 16), kd = k0 + (i % NS) * (F::WIDE / 16);
-#pragma unroll 2
+#pragma unroll
               for (int k = 0; k < DH / 16; ++k) {
                 const int at = (k >> 2) * (HALF / 16) + 2 * (k & 3);
                 mma_ss(tmem + 128 * u, qd + at, kd + at, IS, k > 0);
@@ -683,26 +696,28 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
       __syncwarp();
     } else if (warp == LOAD_WARP) {
       // ------------------------------------------------------------------------------ loads
-      Loader<DH> tile(ar.box);
-      int it = 0, i = 0, n = 0;
+      // A tile's pages are looked up while the one before waits for its place.
+      Loader<DH> tile(ar.box), next(ar.box);
+      int it = -1, i = 0, n = 0, slice = 0;
       const Job* job = nullptr;
-      auto advance = [&]() {  // to the next tile, and looks its pages up
+#pragma unroll 1
+      for (;;) {
+        const int of = slice;
         if (++i >= n) {
           if (job) item_done();
           job = next_item();
           i = 0;
           n = job ? job->count() : 0;
         }
-        if (job) tile.locate(ar, plan, *job, i);
-      };
-      advance();
-#pragma unroll 1
-      for (; job; ++it) {
-        const int st = it % ST;
-        if (it >= ST && !wait(&ss.k_free[st], (it / ST - 1) & 1, a.status, abort)) break;
-        tile.load(ar, job->slice_of(i & 1), sm + F::K_OFF + st * F::NARROW, sm + F::SC_OFF + st * TT * 16, ss.valid[st],
-                  &ss.full[st]);
-        advance();
+        if (job) next.locate(ar, plan, *job, i), slice = job->slice_of(i & 1);
+        if (it >= 0) {
+          const int st = it % ST;
+          if (it >= ST && !wait(&ss.k_free[st], (it / ST - 1) & 1, a.status, abort)) break;
+          tile.load(ar, of, sm + F::K_OFF + st * F::NARROW, sm + F::SC_OFF + st * TT * 16, ss.valid[st], &ss.full[st]);
+        }
+        ++it;
+        if (!job) break;
+        tile = next;
       }
       // (what is on its way lands in this CTA's shared memory)
 #pragma unroll 1
@@ -928,10 +943,36 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
 #pragma unroll
             for (int e = 0; e < 16; ++e) top[(e >> 1) & 1] = fmaxf(top[(e >> 1) & 1], x[e]);
           };
-          // A tile that all rows see, under the references as they are (an item's first one: those that its first
-          // 32 tokens ask for).  (32 tokens at a time, the next ones'
-          // scores fetched meanwhile; the weights take the scores' place when none was too large.)
-          bool plain = !part && !scaled;
+          // of tokens 32 c on, those that row r sees
+          auto sees = [&](int r, int c) -> uint32_t {
+            const int t = __shfl_sync(0xffffffffu, hi, (lane >> 2) + 8 * r) - (job.token(i) + 32 * c) + 1;
+            return ss.see[s][c] & (t >= 32 ? ~0u : t <= 0 ? 0u : (1u << t) - 1);
+          };
+          auto seen = [&](const uint32_t(&w)[2], int e) { return (w[(e >> 1) & 1] >> (8 * (e >> 2) + 2 * (lane & 3) + (e & 1))) & 1; };
+          // Most tiles, under the references as they are (an item's first one: those that its first 32 tokens ask
+          // for, or all where some are hidden).  (32 tokens at a time, the next ones' scores fetched meanwhile; the
+          // weights take the scores' place when none was too large.)
+          bool plain = !scaled && !bad;
+          if (part && plain) {
+            // scores that their rows do not see: what makes their exponents -inf
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t w[2] = {sees(0, c), sees(1, c)};
+              if (__all_sync(0xffffffffu, (w[0] & w[1]) == ~0u)) continue;
+              uint32_t raw[16];
+              float2 t[4];
+              ld_rows(s_at + 32 * c, raw);
+              factors(c, t);
+              tc_wait_ld();
+              loaded16(raw);
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (!seen(w, e))
+                  raw[e] = 0xFF800000u ^ (__float_as_uint(e & 1 ? t[e >> 2].y : t[e >> 2].x) & 0x80000000u);
+              put_rows(s_at + 32 * c, raw);
+            }
+            tc_wait_st();
+          }
           if (__builtin_expect(plain, 1)) {
             uint32_t raw[2][16], p[4][8];
             float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
@@ -939,11 +980,16 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
             if (__builtin_expect(j == 0, 0)) {
               float2 t[4];
               float top[2] = {-INFINITY, -INFINITY};
-              factors(0, t);
-              tc_wait_ld();
-              loaded16(raw[0]);
-              logs(reinterpret_cast<float*>(raw[0]), t);
-              largest(reinterpret_cast<float*>(raw[0]), top);
+#pragma unroll 1
+              for (int c = part ? 3 : 0;; --c) {
+                if (part) ld_rows(s_at + 32 * c, raw[0]);
+                factors(c, t);
+                tc_wait_ld();
+                loaded16(raw[0]);
+                logs(reinterpret_cast<float*>(raw[0]), t);
+                largest(reinterpret_cast<float*>(raw[0]), top);
+                if (c == 0) break;
+              }
               move(top);
               ld_rows(s_at, raw[0]);
             }
@@ -977,11 +1023,6 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
 #pragma unroll
               for (int r = 0; r < 2; ++r) f[r] = __shfl_sync(0xffffffffu, factor, (lane >> 2) + 8 * r);
             }
-            // of tokens 32 c on, those that row r sees: bits 8 k and the next
-            auto sees = [&](int r, int c) -> uint32_t {
-              const int t = __shfl_sync(0xffffffffu, hi, (lane >> 2) + 8 * r) - (job.token(i) + 32 * c) + 1;
-              return (ss.see[s][c] & (t >= 32 ? ~0u : t <= 0 ? 0u : (1u << t) - 1)) >> (2 * (lane & 3));
-            };
             auto load = [&](int c, uint32_t(&raw)[16], uint32_t(&w)[2]) {
               ld_rows(s_at + 32 * c, raw);
               w[0] = w[1] = ~0u;
@@ -997,7 +1038,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
             auto hide = [&](float* x, const uint32_t(&w)[2], float to) {
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                if (!((w[(e >> 1) & 1] >> (8 * (e >> 2) + (e & 1))) & 1)) x[e] = to;
+                if (!seen(w, e)) x[e] = to;
             };
             float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll 1
