@@ -38,7 +38,7 @@ constexpr int WIDEN_WARP = SOFT_WARPS, MMA_WARP = WIDEN_WARP + WIDEN_WARPS, LOAD
 constexpr int THREADS = 32 * (ROWS_WARP + 2), SOFT = 32 * WIDEN_WARP;
 constexpr int MAX_GROUPS = MAX_PREFIX + MAX_REQ;
 constexpr int BLOCK = 128;       // queries
-constexpr int EXTRA = 4;         // what an item costs a CTA beside its steps, in steps
+constexpr int EXTRA = 3;         // what an item costs a CTA beside its steps, in steps
 constexpr int HALF = TT * 128;   // bytes of 64 dimensions of a tile, or a block, in f16
 constexpr int JOBS = 4;          // items whose rows are made ahead
 constexpr float BASE = 6.0f, LEAST = -90.0f;  // log2 of the weights times a_t that m puts at most; a_t below
@@ -805,7 +805,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
       float factor = 1.0f;
       // the stream's warps have the last item's O out of the queries' place
       if (item > 0 && !wait(&ss.o_out[u], (item - 1) & 1, a.status, abort)) return;
-      {  // the warp's queries, 16 bytes a lane: copied to where they go, then rewritten there as f16
+      {  // the warp's queries as f16, 16 bytes a lane
         constexpr int PIECES = DH / 8, ROWS = 32 / PIECES, N = 16 / ROWS;  // lanes of a query; queries at a time
         const int piece = lane & (PIECES - 1), r0 = lane / PIECES;
         const long long from = row >= 0 ? row * a.q_stride + head * DH : -1;
@@ -814,9 +814,9 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
           const int r = e * ROWS + r0;
           return reinterpret_cast<uint4*>(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4));
         };
-        auto copy = [&](int e) {
+        auto fetch = [&](int e) {
           const long long at = __shfl_sync(0xffffffffu, from, e * ROWS + r0);
-          cp_async16(place(e), a.q + (at >= 0 ? at + piece * 8 : 0), at >= 0 ? 16 : 0);
+          return at >= 0 ? *reinterpret_cast<const uint4*>(a.q + at + piece * 8) : make_uint4(0, 0, 0, 0);
         };
         auto largest = [](const uint4& v) {  // as bf16 bits
           const uint32_t t = larger_bf16x2(larger_bf16x2(v.x, v.y), larger_bf16x2(v.z, v.w)) & 0x7FFF7FFFu;
@@ -829,17 +829,16 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
           for (int k = 0; k < 8; k += 2) mul2(f[k], f[k + 1], by);
           *at = make_uint4(f16x2_of(f[0], f[1]), f16x2_of(f[2], f[3]), f16x2_of(f[4], f[5]), f16x2_of(f[6], f[7]));
         };
-#pragma unroll 4
-        for (int e = 0; e < N; ++e) copy(e);
-        cp_async_wait_all();
+        uint4 v[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = fetch(e);
         uint32_t fine = 0, high = 0;  // a bit per e: its largest element here is Q_LOW or more; the largest of all
-#pragma unroll 2
+#pragma unroll
         for (int e = 0; e < N; ++e) {
-          const uint4 v = *place(e);
-          const uint32_t top = largest(v);
+          const uint32_t top = largest(v[e]);
           high = max(high, top);
           fine |= (uint32_t)(top >= Q_LOW) << e;
-          rewrite(place(e), v, Q_SCALE);
+          rewrite(place(e), v[e], Q_SCALE);
         }
 #pragma unroll
         for (int x = PIECES / 2; x > 0; x >>= 1) fine |= __shfl_xor_sync(0xffffffffu, fine, x);
@@ -850,9 +849,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
           // some are out of f16's reach, or not finite, or zeros: again, scaled
 #pragma unroll 1
           for (int e = 0; e < N; ++e) {
-            copy(e);
-            cp_async_wait_all();
-            const uint4 v = *place(e);
+            const uint4 v = fetch(e);
             uint32_t top = largest(v);
 #pragma unroll 1
             for (int x = PIECES / 2; x > 0; x >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
