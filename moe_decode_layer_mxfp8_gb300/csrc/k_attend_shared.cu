@@ -214,6 +214,19 @@ static_assert(offsetof(Shared, valid) == 8 * BARRIERS, "barriers");
 static_assert(Form<128>::SMEM_BYTES + sizeof(Shared) <= 227 * 1024, "shared memory");
 static_assert(Form<64>::SMEM_BYTES + sizeof(Shared) <= 227 * 1024, "shared memory");
 
+// wait() by a thread alone
+__device__ __forceinline__ bool wait_alone(uint64_t* bar, uint32_t parity, int* status, volatile int* abort) {
+  uint32_t polls = 0;
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort || ++polls == (1u << 20)) {
+      atomicOr(status, ST_WAIT_TIMEOUT);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
 // x a + b, two tokens of a query
 __device__ __forceinline__ void fma2t(float& x, float& y, float ax, float ay, float b) {
   asm("{\n .reg .b64 s, m, b;\n mov.b64 s, {%0, %1};\n mov.b64 m, {%2, %3};\n mov.b64 b, {%4, %4};\n"
@@ -636,63 +649,70 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
     else if (warp == MMA_WARP) {
       // ------------------------------------------- MMAs: a stream's second product, then its next first one, in
       // turns, so that one stream's run while the other's softmax does.  (Issued by a warp per stream they
-      // mixed, both streams' scores came at once, and MMAs and softmax took turns.)
+      // mixed, both streams' scores came at once, and MMAs and softmax took turns.)  By one thread, in few
+      // instructions: between two turns the other warps' push these out of the instruction cache, and each 128
+      // bytes of them cost some 90 cycles again.
       constexpr uint32_t IS = (1u << 4) | ((uint32_t)(TT >> 3) << 17) | ((uint32_t)(BLOCK >> 4) << 24);
       constexpr uint32_t IO = (1u << 4) | (1u << 16) | ((uint32_t)(DH >> 3) << 17) | ((uint32_t)(BLOCK >> 4) << 24);
-      const uint64_t q0 = desc_sw128(smem_u32(sm + F::Q_OFF)), k0 = desc_sw128(smem_u32(sm + F::V_OFF)),
-                     v0 = desc_mn(smem_u32(sm + F::V_OFF), HALF);
-      int it = 0;              // the ring's tiles of the items before
-      uint32_t pc = 0;         // parities of the streams' tiles so far
-      bool ok = true;
+      if (elect_one()) {
+        const uint64_t q0 = desc_sw128(smem_u32(sm + F::Q_OFF)), k0 = desc_sw128(smem_u32(sm + F::V_OFF)),
+                       v0 = desc_mn(smem_u32(sm + F::V_OFF), HALF);
+        auto await = [&](uint64_t* bar, uint32_t parity) {
+          const bool there = wait_alone(bar, parity, a.status, abort);
+          tc_fence_after();
+          return there;
+        };
+        int s1 = 0, s2 = 0;           // the wide ring's places of the next first product, and second one
+        uint32_t phase = 0, pc = 0;   // parities: of s1's place, of the streams' tiles so far
+        bool ok = true;
 #pragma unroll 1
-      while (ok) {
-        const Job* job = next_item();
-        if (!job) break;
+        for (; ok; ++item) {
+          const Job* job = &ss.job[item % JOBS];
+          ok = await(&ss.j_full[item % JOBS], (item / JOBS) & 1);
+          if (!ok || job->n[0] <= 0) break;
+          const int n0 = job->n[0], n1 = job->n[1];
+          const bool both = job->mode == TWO_BLOCKS;  // streams' tiles are the same
 #pragma unroll 1
-        for (int j = -1; ok && j < job->n[0]; ++j) {
-#pragma unroll 1
-          for (int u = 0; ok && u < 2; ++u) {
-            const int n = u ? job->n[1] : job->n[0];
-            if (j < 0) {
-              ok = wait(&ss.q_full[u], item & 1, a.status, abort);
-              if (n == 0 && lane == 0) mbar_arrive(&ss.o_full[u]);
-            } else if (j < n) {
-              ok = wait(&ss.p_full[u], (pc >> u) & 1, a.status, abort);
+          for (int x = -2; x < 2 * n0; ++x) {  // stream x & 1
+            const int u = x & 1, n = u ? n1 : n0, left = n - (x >> 1);
+            const bool next = !both || u;  // (the last one that needs the place)
+            if (x >= 0 && left <= 0) continue;
+            ok = await(x < 0 ? &ss.q_full[u] : &ss.p_full[u], x < 0 ? item & 1 : (pc >> u) & 1);
+            if (!ok) break;
+            if (x >= 0) {
               pc ^= 1u << u;
-              if (ok && elect_one()) {
-                const int s = (it + job->ring(u, j)) % NS;
-                const uint32_t oc = tmem + F::O_COL + DH * u, pcol = tmem + 128 * u;
-                const uint64_t vd = v0 + s * (F::WIDE / 16);
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < TT / 16; ++k) mma_ts(oc, pcol + 8 * k, vd + k * (2048 / 16), IO, j > 0 || k > 0);
-                if (job->mode != TWO_BLOCKS || u == 1) tc_commit(&ss.v_free[s]);
-                if (j + 1 == n) tc_commit(&ss.o_full[u]);
+              uint64_t vd = v0 + s2 * (F::WIDE / 16);
+              uint32_t pcol = tmem + 128 * u, accumulate = x > 1;
+#pragma unroll 2
+              for (int k = 0; k < TT / 16; ++k, pcol += 8, vd += 2048 / 16, accumulate = 1)
+                mma_ts(tmem + F::O_COL + DH * u, pcol, vd, IO, accumulate);
+              if (next) {
+                tc_commit(&ss.v_free[s2]);
+                if (++s2 == NS) s2 = 0;
               }
+              if (left == 1) tc_commit(&ss.o_full[u]);
+            } else if (n == 0) {
+              mbar_arrive(&ss.o_full[u]);
             }
-            __syncwarp();
-            if (!ok || j + 1 >= n) continue;
-            const int i = it + job->ring(u, j + 1);
-            ok = wait(&ss.v_full[i % NS], (i / NS) & 1, a.status, abort);
-            if (ok && elect_one()) {
-              tc_fence_after();
-              const uint64_t qd = q0 + u * (F::Q_BYTES / 16), kd = k0 + (i % NS) * (F::WIDE / 16);
-#pragma unroll
-              for (int k = 0; k < DH / 16; ++k) {
-                const int at = (k >> 2) * (HALF / 16) + 2 * (k & 3);
-                mma_ss(tmem + 128 * u, qd + at, kd + at, IS, k > 0);
-              }
-              tc_commit(&ss.s_full[u]);
-              // (the commit is no release: this arrival passes on what the widening warps wrote)
-              mbar_arrive(&ss.s_full[u]);
+            if (left <= 1) continue;
+            ok = await(&ss.v_full[s1], phase);
+            if (!ok) break;
+            uint64_t qd = q0 + u * (F::Q_BYTES / 16), kd = k0 + s1 * (F::WIDE / 16);
+#pragma unroll 2
+            for (int k = 0; k < DH / 16; ++k) {
+              mma_ss(tmem + 128 * u, qd, kd, IS, k > 0);
+              const int on = k == 3 ? HALF / 16 - 6 : 2;
+              qd += on, kd += on;
             }
-            __syncwarp();
+            tc_commit(&ss.s_full[u]);
+            // (the commit is no release: this arrival passes on what the widening warps wrote)
+            mbar_arrive(&ss.s_full[u]);
+            if (next && ++s1 == NS) s1 = 0, phase ^= 1;
           }
+          if (ok) mbar_arrive(&ss.j_free[item % JOBS]);
         }
-        it += job->count();
-        item_done();
+        tc_commit(&ss.drain);
       }
-      if (elect_one()) tc_commit(&ss.drain);
       __syncwarp();
     } else if (warp == LOAD_WARP) {
       // ------------------------------------------------------------------------------ loads
