@@ -92,7 +92,9 @@ struct RotateArgs {
   const int* row_req;
   PagedView cache;
   int* status;
-  unsigned kv_blocks;  // (the launch's)
+  // the launch's: slots of heads that share a row; threads of a latent, CTAs of latents
+  int across, span;
+  unsigned kv_blocks;
 };
 
 struct SharedArgs {

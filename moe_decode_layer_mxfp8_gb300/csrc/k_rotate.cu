@@ -9,15 +9,24 @@
 // positions, scaled frequencies and several axes are the caller's.  A thread owns 8 neighbouring
 // dimensions of a head: neighbours pair up within them, halves with the lane that owns the others' 8
 // (rotated dimensions come in whole runs of 8).  It keeps its cosines and sines over all its heads of a
-// row.  A latent is a warp's, so that its largest element is one reduction away from its codes.
+// row: the fewer threads share a row, the fewer chains from a position to the table's row there are to
+// wait for, as long as the threads fill the GPU.  A latent has the threads of its runs: halving its part
+// of a warp, or whole warps, its largest element one reduction away from its codes.
+//
+// Bound by DRAM where steps are large, by latency (launch, position, table) where they are small.  Measured
+// in a graph: one request's token 2.5 us; 48 rows of 64 heads back 2.5; 20001 rows of 16 heads of 64, f16, 17.2
+// (5.0 TB/s of 6.8; a head a thread: 47); 23K prompt rows of 64 heads of 128 with their latents 148 (5.2
+// TB/s; 187 with CTAs of 256; twice as many loads in flight 157); 14K narrow f32 latents 5.3 (a warp each: 10).
 #include "cache_kernels.h"
 
 namespace mono {
 namespace {
 
-constexpr int THREADS = 256, WARPS = THREADS / 32;
-constexpr int AHEAD = 4;       // a thread's loads in flight
-constexpr int LATENT_RUNS = 4;  // runs of 8 that a lane has of a latent at most (1024 wide)
+constexpr int THREADS = 128, WARPS = THREADS / 32;
+constexpr int AHEAD = 4;  // a thread's loads in flight
+constexpr int PER = 8;    // heads of a thread where there are rows enough to fill the GPU
+constexpr long long MANY = 152 * 1024;
+static_assert(WARPS * 256 >= 1024, "the widest latent a CTA");
 
 template <typename T>
 struct Run;  // 8 elements as they lie
@@ -65,8 +74,8 @@ __device__ __forceinline__ void store_run(T* p, const Run<T>& v) {
   *reinterpret_cast<Run<T>*>(p) = v;
 }
 
-// What a thread knows of its 8 dimensions: whether they are rotated, with which lane's, and a
-// position's cosines and sines (interleaved: of its four pairs).
+// What a thread knows of its 8 dimensions: whether they are rotated, with which lane's, and a position's
+// cosines and sines, a sine's sign that of its product (y1 takes x2 times -sin).
 struct Turn {
   bool in, first;  // rotated; the first half of the pairs
   int partner;     // lane
@@ -76,43 +85,44 @@ struct Turn {
     in = i >= 0 && i < r.dim;  // (dim 0: no rotation)
     first = i < half;
     partner = !in || r.interleaved ? lane : first ? lane + half / 8 : lane - half / 8;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) c[k] = s[k] = 0.0f;
   }
   __device__ __forceinline__ void load(const Rope& r, int head_dim, int position) {
     const int half = r.dim / 2, i = ((threadIdx.x & 31) & (head_dim / 8 - 1)) * 8 - r.offset;
     if (!in) return;
-    const float* t = r.table + position * r.stride + (r.interleaved ? i / 2 : first ? i : i - half);
-    const int n = r.interleaved ? 1 : 2;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (k >= n) break;
-      const float4 x = __ldg(reinterpret_cast<const float4*>(t) + k);
-      const float4 y = __ldg(reinterpret_cast<const float4*>(t + half) + k);
-      c[4 * k] = x.x, c[4 * k + 1] = x.y, c[4 * k + 2] = x.z, c[4 * k + 3] = x.w;
-      s[4 * k] = y.x, s[4 * k + 1] = y.y, s[4 * k + 2] = y.z, s[4 * k + 3] = y.w;
-    }
-    if (r.inverse)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s[k] = -s[k];
-  }
-  // Every lane of the warp calls it (halves pair up across lanes).
-  __device__ __forceinline__ void apply(const Rope& r, float (&f)[8]) const {
+    const float4* t = reinterpret_cast<const float4*>(
+        r.table + position * r.stride + (r.interleaved ? i / 2 : first ? i : i - half));
+    const float4 x = __ldg(t), y = __ldg(t + half / 4);
+    const uint32_t turned = r.inverse ? 0x80000000u : 0u;
+    auto signed_by = [](float v, uint32_t sign) { return __uint_as_float(__float_as_uint(v) ^ sign); };
+    const float cx[4] = {x.x, x.y, x.z, x.w}, sx[4] = {y.x, y.y, y.z, y.w};
     if (r.interleaved) {
-      if (!in) return;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) c[k] = cx[k / 2], s[k] = signed_by(sx[k / 2], turned ^ (k & 1 ? 0u : 0x80000000u));
+    } else {
+      const float4 z = __ldg(t + 1), w = __ldg(t + half / 4 + 1);
+      const float cz[4] = {z.x, z.y, z.z, z.w}, sz[4] = {w.x, w.y, w.z, w.w};
+      const uint32_t sign = turned ^ (first ? 0x80000000u : 0u);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float a = f[2 * k], b = f[2 * k + 1];
-        f[2 * k] = __fsub_rn(__fmul_rn(a, c[k]), __fmul_rn(b, s[k]));
-        f[2 * k + 1] = __fadd_rn(__fmul_rn(b, c[k]), __fmul_rn(a, s[k]));
+        c[k] = cx[k], c[k + 4] = cz[k];
+        s[k] = signed_by(sx[k], sign), s[k + 4] = signed_by(sz[k], sign);
       }
-      return;
+    }
+  }
+  // Every lane of the warp calls it (halves pair up across lanes); the result is one where `in`.
+  __device__ __forceinline__ void apply(const Rope& r, float (&f)[8]) const {
+    float o[8];
+    if (r.interleaved) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = f[k ^ 1];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = __shfl_sync(0xffffffffu, f[k], partner);
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float o = __shfl_sync(0xffffffffu, f[k], partner);
-      if (!in) continue;
-      const float x = __fmul_rn(f[k], c[k]), y = __fmul_rn(o, s[k]);
-      f[k] = first ? __fsub_rn(x, y) : __fadd_rn(x, y);
-    }
+    for (int k = 0; k < 8; ++k) f[k] = __fadd_rn(__fmul_rn(f[k], c[k]), __fmul_rn(o[k], s[k]));
   }
 };
 
@@ -126,71 +136,69 @@ __device__ __forceinline__ int rope_position(const RotateArgs& a, int r, bool& o
   return p < 0 || outside ? -1 : t;
 }
 
-// Heads of rows, or latents where there are any (the first kv_blocks CTAs).  Heads: a thread's 8
-// dimensions of a slot of heads; as many rows a CTA as its threads hold.
-template <typename T>
+// Heads of rows, or latents where there are any (the first kv_blocks CTAs; without heads all, in fewer
+// registers).  Heads: a thread's 8 dimensions of a slot of heads; as many rows a CTA as its threads hold.
+template <typename T, bool HEADS>
 __global__ void __launch_bounds__(THREADS) rotate_kernel(const RotateArgs a) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the warp, and what loops depend on, from one lane: the compiler then knows the shuffles to be whole warps')
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int runs = a.head_dim / 8;
   Turn turn(a.rope, a.head_dim);
   pdl_trigger();
   pdl_wait();
   bool outside;
-  if (blockIdx.x < a.kv_blocks) {
-    // --------------------------------------------------------------------------- a latent per warp
-    const int r = blockIdx.x * WARPS + warp;
-    if (r >= a.rows) return;
-    const T* kv = static_cast<const T*>(a.kv) + r * a.kv_stride;
-    Run<T> v[LATENT_RUNS];
-#pragma unroll
-    for (int k = 0; k < LATENT_RUNS; ++k)
-      if ((lane + 32 * k) * 8 < a.kv_dim) v[k] = load_run(kv + (lane + 32 * k) * 8);
-    const int p = a.positions[r], t = rope_position(a, r, outside);
-    if (outside && lane == 0) atomicOr(a.status, ST_POSITION);
-    if (t < 0) return;
-    const int b = a.row_req[r];
-    const long long at = b < 0 || b >= a.n_req ? -1 : record_offset(a.cache, b, p);
-    turn.load(a.rope, a.head_dim, t);
-    float f[LATENT_RUNS][8], amax = 0.0f;
-#pragma unroll
-    for (int k = 0; k < LATENT_RUNS; ++k) {
-      if (32 * 8 * k >= a.kv_dim) break;
-      const bool live = (lane + 32 * k) * 8 < a.kv_dim;
-      if (live)
-        v[k].get(f[k]);
-      else
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[k][e] = 0.0f;
-      if (a.rope.dim > 0) turn.apply(a.rope, f[k]);
-      if (live)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[k][e]));
+  if (!HEADS || blockIdx.x < a.kv_blocks) {
+    // -------------------------------------------------------------------- latents, 8 elements a thread
+    __shared__ float largest[WARPS];
+    const int of = tid / a.span, i = (tid - of * a.span) * 8, r = blockIdx.x * (THREADS / a.span) + of;
+    const bool live = of < THREADS / a.span && r < a.rows && i < a.kv_dim;
+    Run<T> v;
+    if (live) v = load_run(static_cast<const T*>(a.kv) + r * a.kv_stride + i);
+    const int p = live ? a.positions[r] : -1, t = live ? rope_position(a, r, outside) : -1;
+    if (live && outside && i == 0) atomicOr(a.status, ST_POSITION);
+    const int b = live ? a.row_req[r] : -1;
+    const long long at = t < 0 || b < 0 || b >= a.n_req ? -1 : record_offset(a.cache, b, p);
+    if (t >= 0) turn.load(a.rope, a.head_dim, t);
+    float f[8] = {}, amax = 0.0f;
+    if (live) v.get(f);
+    if (a.rope.dim > 0) {
+      turn.apply(a.rope, f);
+      if (!turn.in && live) v.get(f);
     }
-    amax = warp_max(amax);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float x = __shfl_xor_sync(0xffffffffu, amax, o);
+      if (o < a.span) amax = fmaxf(amax, x);
+    }
+    if (a.span > 32) {
+      if (lane == 0) largest[warp] = amax;
+      __syncthreads();
+      if (t < 0) return;
+#pragma unroll 1
+      for (int w = 0; w < a.span / 32; ++w) amax = fmaxf(amax, largest[of * (a.span / 32) + w]);
+    }
+    if (t < 0) return;
     if (at < 0) {
-      if (lane == 0) atomicOr(a.status, ST_UNMAPPED_PAGE);
+      if (i == 0) atomicOr(a.status, ST_UNMAPPED_PAGE);
       return;
     }
     // (0 / 0 otherwise; the smallest f32 over 448 are 0 too)
     float s = amax / 448.0f;
     if (s == 0.0f) s = 1.0f;
     uint8_t* rec = const_cast<uint8_t*>(a.cache.base) + at;
+    uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < LATENT_RUNS; ++k) {
-      if ((lane + 32 * k) * 8 >= a.kv_dim) break;
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = __nv_cvt_float2_to_fp8x2(make_float2(f[k][2 * e] / s, f[k][2 * e + 1] / s),
-                                        __NV_SATFINITE, __NV_E4M3);
-      *reinterpret_cast<uint2*>(rec + (lane + 32 * k) * 8) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-    }
-    if (lane == 0) *reinterpret_cast<float*>(rec + a.kv_dim) = s;
+    for (int e = 0; e < 4; ++e)
+      w[e] = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * e] / s, f[2 * e + 1] / s), __NV_SATFINITE, __NV_E4M3);
+    *reinterpret_cast<uint2*>(rec + i) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    if (i == 0) *reinterpret_cast<float*>(rec + a.kv_dim) = s;
     return;
   }
   // ------------------------------------------------------------------------------------------ heads
   const int slot = tid / runs, slots = THREADS / runs;
-  const int across = min(a.heads, slots), rows = slots / across;  // slots of a row, rows of a CTA
+  const int across = a.across, rows = slots / across;  // slots of a row, rows of a CTA
   const int j = slot / across, h0 = slot - j * across;
   const long long r = (long long)(blockIdx.x - a.kv_blocks) * rows + j;
   const bool live = j < rows && r < a.rows;
@@ -210,36 +218,50 @@ __global__ void __launch_bounds__(THREADS) rotate_kernel(const RotateArgs a) {
   if (t >= 0) turn.load(a.rope, a.head_dim, t);
   const bool todo = move && t >= 0;
 #pragma unroll 1
-  for (int h = h0;; fetch(h)) {  // (as often in all lanes)
+  for (int k = 0;;) {  // (as often in all lanes)
 #pragma unroll
     for (int e = 0; e < AHEAD; ++e) {
-      if (h - h0 + e * across >= a.heads) break;
+      if (k + e * across >= a.heads) break;
+      const int h = h0 + k + e * across;
       float f[8] = {};
-      const bool mine = todo && h + e * across < a.heads;
+      const bool mine = todo && h < a.heads;
       if (mine) v[e].get(f);
       turn.apply(a.rope, f);
       if (!mine) continue;
       if (turn.in) v[e].set(f);
-      store_run(out + (h + e * across) * a.head_dim, v[e]);
+      store_run(out + h * a.head_dim, v[e]);
     }
-    h += across * AHEAD;
-    if (h - h0 >= a.heads) break;
+    k += across * AHEAD;
+    if (k >= a.heads) break;
+    fetch(h0 + k);
   }
 }
 
 template <typename T>
 cudaError_t launch(const Launch& L, const RotateArgs& a, unsigned grid) {
-  return launch_ex(L, dim3(grid), dim3(THREADS), 0, rotate_kernel<T>, a);
+  return launch_ex(L, dim3(grid), dim3(THREADS), 0, a.x ? rotate_kernel<T, true> : rotate_kernel<T, false>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_rotate(const Launch& L, const RotateArgs& args, int dtype) {
   RotateArgs a = args;
-  a.kv_blocks = a.kv ? (unsigned)((a.rows + WARPS - 1) / WARPS) : 0;
+  a.span = 32, a.kv_blocks = 0;
+  if (a.kv) {
+    // a latent's threads: whole warps, or the least part of one that halving leads to
+    if (a.kv_dim > 256) a.span = (a.kv_dim + 255) / 256 * 32;
+    while (a.span <= 32 && a.span > 1 && a.span / 2 * 8 >= a.kv_dim) a.span /= 2;
+    a.kv_blocks = (unsigned)((a.rows + THREADS / a.span - 1) / (THREADS / a.span));
+  }
   unsigned grid = a.kv_blocks;
   if (a.x) {
-    const int slots = THREADS / (a.head_dim / 8), rows = slots / (a.heads < slots ? a.heads : slots);
+    const int slots = THREADS / (a.head_dim / 8);
+    int across = a.heads < slots ? a.heads : slots;
+    while (across > 1 && (a.heads + across - 1) / across < PER &&
+           (long long)a.rows * across * (a.head_dim / 8) > MANY)
+      across /= 2;
+    a.across = across;
+    const int rows = slots / across;
     grid += (unsigned)((a.rows + rows - 1) / rows);
   }
   return dtype == 0 ? launch<float>(L, a, grid)
