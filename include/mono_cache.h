@@ -107,13 +107,13 @@ int mono_cache_attend(mono_cache_t *h, const mono_attend_args *args, void *strea
  * all.  Row r at position p sees t <= hi, hi as there; a row inside its prefix sees that much of it.
  *
  * Sums, refused and masked tokens, status bits, pad rows, lse and the handle's workspace are as in
- * mono_cache_attend; o is rounded to bf16 once, w[t] scale_t to 11 bits (and to 2^-31 of the largest of a
- * row's tile of 128 tokens that set its reference) before that, q's elements to 2^-24 of a head's
- * largest.  A NaN code of a token in view makes NaN the heads of its slice.  Scores of heads whose
+ * mono_cache_attend; o is rounded to bf16 once, w[t] scale_t to 11 bits before that (and to 2^-30 of the
+ * largest of the 32 to 128 tokens that set a row's reference), q's elements to 2^-24 of a head's
+ * largest; scale_t below 2^-64 in size lose bits of o.  A NaN code of a token in view makes NaN the heads of its slice.  Scores of heads whose
  * largest is beyond 2^26 in size are NaN.  Rows of requests whose prefix_of is outside [-1, n_prefix) are
  * left out, o = 0, and raise MONO_STATUS_UNMAPPED_PAGE.  A negative length counts as 0.
  *
- * Limits: n_prefix 1..128; 2 * rows * (kv_dim / head_dim) times the tiles of the longer table, and 5 more,
+ * Limits: n_prefix 1..128; 2 * rows * (kv_dim / head_dim) times the tiles of the longer table, and 4 more,
  * below 2^31; both tables' max_blocks * block_size at most 2^31 - 2^16.
  */
 typedef struct {
@@ -130,7 +130,7 @@ typedef struct {
   int32_t prefix_max_blocks, n_prefix;
   int32_t rows;               /* 1 <= rows <= max_rows */
   int32_t causal;
-  float scale;                /* 0: 1/sqrt(head_dim) */
+  float scale;                /* 2^-20 .. 2^20; 0: 1/sqrt(head_dim) */
   const uint8_t *kv_cache;
   int64_t kv_stride_block, kv_stride_tok, kv_num_blocks;
   float *lse;                 /* optional [rows, n_q_heads] */

@@ -271,8 +271,8 @@ class Cache:
         n_prefix, prefix_blocks = prefix_table.shape
         if scale is None:
             scale = 0.0
-        elif not _LEAST <= scale <= _MOST:
-            raise ValueError("scale must be positive, and an f32")
+        elif not 2.0 ** -20 <= scale <= 2.0 ** 20:
+            raise ValueError("scale must be in [2^-20, 2^20]")
         qp, qs = _mat(q, "q", _BF16, rows, self._width, dev)
         op, os = _mat(o, "o", _BF16, rows, self._width, dev)
         heads = self.spec["n_q_heads"]

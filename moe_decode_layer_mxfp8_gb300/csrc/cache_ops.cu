@@ -225,7 +225,8 @@ int mono_cache_attend_shared(mono_cache_t* h, const mono_shared_args* a, void* s
   if (!a->q || !a->o || !a->positions || !a->row_req || !a->block_table || !a->prefix_table ||
       !a->prefix_lengths || !a->kv_cache)
     return MONO_ERR_INVALID_ARG;
-  if (!std::isfinite(a->scale) || a->scale < 0.0f) return MONO_ERR_INVALID_ARG;
+  // (the tokens' factors hold it, 2^64 times as large or 2^-64; a NaN is refused)
+  if (a->scale != 0.0f && !(a->scale >= 0x1p-20f && a->scale <= 0x1p20f)) return MONO_ERR_INVALID_ARG;
   const int64_t width = (int64_t)s.n_q_heads * s.head_dim;
   int64_t qs = a->q_stride, os = a->o_stride;
   TRY(check_rows(a->q, width, &qs, 2));

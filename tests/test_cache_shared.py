@@ -74,7 +74,7 @@ def test_it_hands_over_what_it_was_given():
     dict(block_table=torch.zeros((2, 5), dtype=torch.int64)), dict(prefix_table=i32(3, 8)[:, :7]),
     dict(prefix_lengths=i32(2)), dict(prefix_of=i32(3)), dict(prefix_of=torch.zeros(2, dtype=torch.int64)),
     dict(lse=torch.zeros((3, 5))), dict(lse=torch.zeros((3, 8))[:, :4]), dict(scale=0.0), dict(scale=-1.0),
-    dict(scale=float("nan")), dict(scale=1e39), dict(kv_cache=torch.zeros((4, 15, 144), dtype=torch.uint8))])
+    dict(scale=float("nan")), dict(scale=1e39), dict(scale=2.0 ** 20.1), dict(scale=2.0 ** -20.1), dict(kv_cache=torch.zeros((4, 15, 144), dtype=torch.uint8))])
 def test_it_refuses(kw):
     with pytest.raises(ValueError):
         call(**kw)

@@ -274,6 +274,28 @@ def test_rotate_there_and_back(layout, heads):
     h.close()
 
 
+@pytest.mark.parametrize("layout,heads,rows", [("full", 5, 4001), ("full", 64, 1500), ("wide", 16, 1250),
+                                               ("wide", 7, 2777), ("wide", 131, 1300)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotate_many_rows(layout, heads, rows, inter):
+    """So many that a thread takes several heads, and a CTA several rows."""
+    m = _m()
+    spec = LAYOUTS[layout]
+    h = m.Cache(spec, 1, 1)
+    rng = np.random.default_rng(heads)
+    pos = rng.integers(-1, 300, rows)
+    tab = ro.table(300, 32)
+    x = torch.from_numpy(rng.standard_normal((rows, heads * spec["head_dim"])).astype(np.float32)).to(torch.float16)
+    xd, out = x.cuda(), torch.full(x.shape, 7.0, dtype=x.dtype, device="cuda")
+    h.rotate(xd, out, i32(pos), torch.from_numpy(tab).cuda(), rope_offset=16, interleaved=inter)
+    want = torch.from_numpy(ro.rotate(x.float().numpy(), tab, pos, spec["head_dim"], 16, inter, False,
+                                      dtype=np.float32)).to(x.dtype)
+    want[torch.from_numpy(pos) < 0] = 7.0
+    assert torch.equal(out.cpu(), want)
+    assert h.status() == 0
+    h.close()
+
+
 def test_rotate_positions_outside_the_table():
     m = _m()
     h = m.Cache(TINY, 1, 1)

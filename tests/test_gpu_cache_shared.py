@@ -247,6 +247,20 @@ def test_records_that_are_all_zeros():
     check(WIDE, [300], [0, 0], [77, 130], [3, 4], seed=2, edit=zeros)
 
 
+@pytest.mark.parametrize("scale", [2.0 ** -20, 2.0 ** 20])
+def test_the_least_and_the_largest_scale(scale):
+    """With queries that make the scores ordinary ones."""
+    def q(n):
+        return (make_q(FULL, n, 3).float() * (2.0 ** -4 / scale)).to(torch.bfloat16)
+    check(FULL, [260], [0, 0], [70, 5], [2, 3], seed=8, scale=scale, q=q)
+
+
+@pytest.mark.parametrize("n", [1, 13, 26, 52, 104])
+def test_pieces_joined_by_teams_of_every_size(n):
+    """Rows of 64 heads behind a prefix that the whole GPU shares: 8, 4, 2 and 1 warps a query."""
+    check(FULL, [9000], [0] * n, [1] * n, [1] * n, seed=n)
+
+
 def test_nan_codes_and_scales_reach_only_rows_and_heads_that_see_them():
     m = _m()
     kv = WIDE["kv_dim"]
@@ -483,7 +497,8 @@ def test_the_library_refuses():
             (dict(n_prefix=0), -1), (dict(n_prefix=129), -3), (dict(q=a + 8), -4), (dict(o=a + 2), -4),
             (dict(q_stride=1023), -1), (dict(o_stride=1028), -4), (dict(positions=a + 2), -4), (dict(lse=a + 2), -4),
             (dict(prefix_of=a + 1), -4), (dict(prefix_lengths=a + 2), -4), (dict(scale=-1.0), -1),
-            (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(max_blocks=0), -1),
+            (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(scale=2.0 ** 21), -1),
+            (dict(scale=2.0 ** -21), -1), (dict(max_blocks=0), -1),
             (dict(prefix_max_blocks=0), -1), (dict(max_blocks=2 ** 26), -1), (dict(prefix_max_blocks=2 ** 26), -1),
             (dict(kv_stride_tok=128), -5), (dict(kv_num_blocks=0), -1)]:
         args = mc.SharedArgs(**dict(good, **change))
