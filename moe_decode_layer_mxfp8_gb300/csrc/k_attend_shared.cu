@@ -296,9 +296,9 @@ __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Fills the plan but for the line (every thread of the block); the results are behind the caller's next
-// barrier.  Waits for the kernels before.
-__device__ __forceinline__ void derive_plan(const Args& ar, Plan& plan) {
+// Fills the plan (every thread of the block); the results are behind the caller's next barrier.  Waits for the
+// kernels before.  `sums`: an int per warp.
+__device__ __forceinline__ void derive_plan(const Args& ar, Plan& plan, int* sums) {
   const SharedArgs& a = ar.a;
   const int tid = threadIdx.x, np = a.n_prefix, groups = np + a.n_req;
   const bool tell = blockIdx.x == 0;
@@ -355,44 +355,42 @@ __device__ __forceinline__ void derive_plan(const Args& ar, Plan& plan) {
     if (beyond && tell) atomicOr(a.status, ST_UNMAPPED_PAGE);
   }
   __syncthreads();
+  // the groups' places in the line
+  int units = 0;
   if (tid < groups) {
     const int lo = plan.first[tid], end = end_of(a, plan, tid);
     plan.tiles[tid] = plan.cnt[tid] == 0 || end <= lo ? 0 : ((end - 1) >> 7) - (lo >> 7) + 1;
-    plan.pre[tid + 1] = items_of(ar, plan, tid).units(ar);
+    units = items_of(ar, plan, tid).units(ar);
   }
   static_assert(MAX_GROUPS <= THREADS, "a group a thread");
-}
-
-// Lays the groups out in the line (pre[g + 1] holds what group g takes) and finds the CTA's first item; by a
-// whole warp.
-__device__ __forceinline__ Cursor cut_line(const Args& ar, Plan& plan) {
-  const int lane = threadIdx.x & 31, groups = ar.a.n_prefix + ar.a.n_req;
-  const int each = (groups + 31) >> 5, from = lane * each, to = min(from + each, groups);  // a lane's groups
-  int u = 0;
-#pragma unroll 1
-  for (int g = from; g < to; ++g) u += plan.pre[g + 1];
-  int W = u;
+  int upto = units;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, W, o);
-    if (lane >= o) W += y;
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if ((tid & 31) >= o) upto += y;
   }
-  u = W - u;
-  W = __shfl_sync(0xffffffffu, W, 31);
+  if ((tid & 31) == 31) sums[tid >> 5] = upto;
+  __syncthreads();
+  if (tid < groups) {
 #pragma unroll 1
-  for (int g = from; g < to; ++g) u += plan.pre[g + 1], plan.pre[g + 1] = u;
-  if (lane == 0) plan.pre[0] = 0;
-  __syncwarp();
-  const Cut cut(W, gridDim.x);
+    for (int w = 0; w < tid >> 5; ++w) upto += sums[w];
+    plan.pre[tid + 1] = upto;
+  }
+  if (tid == 0) plan.pre[0] = 0;
+}
+
+// The CTA's first item, by a whole warp.
+__device__ __forceinline__ Cursor cut_line(const Args& ar, const Plan& plan) {
+  const int lane = threadIdx.x & 31, groups = ar.a.n_prefix + ar.a.n_req;
+  const Cut cut(plan.pre[groups], gridDim.x);
   Cursor c = {0, 0, 0, cut.size(blockIdx.x)};
   if (c.left > 0) {
-    const int w0 = cut.start(blockIdx.x);
-    int hi = groups;  // the last group that starts by w0 (and is not empty: the next starts later)
-#pragma unroll 1
-    while (hi - c.g > 1) {
-      const int mid = (c.g + hi) >> 1;
-      if (plan.pre[mid] <= w0) c.g = mid; else hi = mid;
-    }
+    // the last group that starts by w0 (and is not empty: the next starts later), a lane a run of groups, then a group
+    const int w0 = cut.start(blockIdx.x), each = (groups + 31) >> 5;
+    static_assert(MAX_GROUPS <= 32 * 32, "a run's groups are a warp's");
+    c.g = each * (__popc(__ballot_sync(0xffffffffu, lane * each < groups && plan.pre[min(lane * each, groups)] <= w0)) - 1);
+    const int g = c.g + lane;
+    c.g += __popc(__ballot_sync(0xffffffffu, lane < each && g < groups && plan.pre[min(g, groups)] <= w0)) - 1;
     const Items it = items_of(ar, plan, c.g);
     const int u = w0 - plan.pre[c.g];
     c.item = min(u / it.len, it.whole(ar));
@@ -409,17 +407,25 @@ __device__ __forceinline__ void item_rows(const Args& ar, const Plan& plan, Job&
   for (int i = 0; i < 2 * BLOCK / 8; i += 32) reinterpret_cast<uint4*>(job.row)[i + lane] = make_uint4(~0u, ~0u, ~0u, ~0u);
   __syncwarp();
   int seen = 0, least = 0x7FFFFFFF;
+  constexpr int AT_ONCE = 4;  // (a group's rows are anywhere: 256 rows, 32 at a time, took 1900 cycles)
 #pragma unroll 1
-  for (int r0 = 0; r0 < ar.a.rows && seen - first < most; r0 += 32) {
-    const int r = r0 + lane, b = r < ar.a.rows ? plan.req[r] : -1;
-    const bool in = b >= 0 && (g < np ? plan.pfx[b] == g : b == g - np);
-    const uint32_t m = __ballot_sync(0xffffffffu, in);
-    const int rank = seen + __popc(m & ((1u << lane) - 1)) - first;
-    if (in && rank >= 0 && rank < most) {
-      job.row[rank < ar.rows_per ? rank : BLOCK + rank - ar.rows_per] = (short)r;
-      least = min(least, plan.hi[r]);
+  for (int r0 = 0; r0 < ar.a.rows && seen - first < most; r0 += 32 * AT_ONCE) {
+    int b[AT_ONCE];
+    bool in[AT_ONCE];
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) b[k] = r0 + 32 * k + lane < ar.a.rows ? plan.req[r0 + 32 * k + lane] : -1;
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) in[k] = b[k] >= 0 && (g < np ? plan.pfx[b[k]] == g : b[k] == g - np);
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) {
+      const uint32_t m = __ballot_sync(0xffffffffu, in[k]);
+      const int r = r0 + 32 * k + lane, rank = seen + __popc(m & ((1u << lane) - 1)) - first;
+      if (in[k] && rank >= 0 && rank < most) {
+        job.row[rank < ar.rows_per ? rank : BLOCK + rank - ar.rows_per] = (short)r;
+        least = min(least, plan.hi[r]);
+      }
+      seen += __popc(m);
     }
-    seen += __popc(m);
   }
   least = __reduce_min_sync(0xffffffffu, least);
   if (lane == 0) job.least = least;
@@ -443,9 +449,10 @@ struct Loader {
     if (needed && t < end && t + box > lo) {
       row = t - lb * ar.a.kv.block_size;
       if (lb < max_blocks) page = __ldg(table + lb);
-      if (page >= ar.a.kv.num_blocks) page = -1;
     }
   }
+  // (asked where it is needed, so that nothing waits for a lookup before)
+  __device__ __forceinline__ bool mapped(const Args& ar) const { return page >= 0 && page < ar.a.kv.num_blocks; }
   __device__ __forceinline__ void locate(const Args& ar, const Plan& plan, const Job& job, int i) {
     const int lane = threadIdx.x & 31, np = ar.a.n_prefix, g = job.g;
     const PagedView& v = g < np ? ar.a.pre : ar.a.kv;
@@ -461,13 +468,14 @@ struct Loader {
     const SharedArgs& a = ar.a;
     const int lane = threadIdx.x & 31;
     if (box > 1) {
-      if (page >= 0) {
+      const bool there = mapped(ar);
+      if (there) {
         tma_load_3d(st + ((lane * DH) << shift), &ar.codes, DH * slice, row, page, full);
         tma_load_3d(sc + ((lane * 16) << shift), &ar.scales, a.kv_dim, row, page, full);
       } else if (row >= 0) {
         atomicOr(a.status, ST_UNMAPPED_PAGE);
       }
-      const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+      const uint32_t have = __ballot_sync(0xffffffffu, there);
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         const int t = t0 + 32 * q + lane;
@@ -482,9 +490,10 @@ struct Loader {
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         look_up(ar, t0 + 32 * q + lane, true);
-        if (row >= 0 && page < 0) atomicOr(a.status, ST_UNMAPPED_PAGE);
+        const bool there = mapped(ar);
+        if (row >= 0 && !there) atomicOr(a.status, ST_UNMAPPED_PAGE);
         const long long off = page * a.kv.stride_block + row * a.kv.stride_tok;
-        const uint32_t w = __ballot_sync(0xffffffffu, page >= 0);
+        const uint32_t w = __ballot_sync(0xffffffffu, there);
         if (lane == 0) valid[q] = w;
 #pragma unroll 1
         for (int e = 0; e < 32 / ROWS; ++e) {
@@ -493,7 +502,7 @@ struct Loader {
           if ((w >> k) & 1)
             cp_async16(st + (32 * q + k) * DH + 16 * piece, a.kv.base + ro + DH * slice + 16 * piece, 16);
         }
-        if (page >= 0) cp_async16(sc + (32 * q + lane) * 16, a.kv.base + off + a.kv_dim, 16);
+        if (there) cp_async16(sc + (32 * q + lane) * 16, a.kv.base + off + a.kv_dim, 16);
       }
       cp_async_wait_all();
       __syncwarp();
@@ -545,7 +554,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
     if (ar.box) prefetch_tmap(&ar.codes), prefetch_tmap(&ar.scales);
   }
   if (warp == MMA_WARP) tmem_alloc<512>(&ss.tmem);
-  derive_plan(ar, plan);
+  derive_plan(ar, plan, reinterpret_cast<int*>(ss.ml));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -589,7 +598,16 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
           const uint8_t* src = sm + F::K_OFF + st * F::NARROW + t0 * DH + lane * 16;
           uint8_t* dst = sm + F::V_OFF + s * F::WIDE + (piece >> 2) * HALF;
           uint32_t nan = 0;
-          if (__builtin_expect(part, 0)) {
+          bool check = false;
+          if (__builtin_expect(part && ok != 0, 0)) {
+#pragma unroll 4
+            for (int e = 0; e < N; ++e) {
+              const uint4 v = lds128(src + e * ROWS * DH), c = without_nan(v);
+              check |= c.x != v.x || c.y != v.y || c.z != v.z || c.w != v.w;
+            }
+            check = __any_sync(0xffffffffu, check);
+          }
+          if (__builtin_expect(check, 0)) {
             // a NaN code that some row must not see would reach it as 0 * NaN: it is a 0 then, and the token's
             // factor is NaN
 #pragma unroll 1
@@ -606,6 +624,14 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
             }
             fence_proxy_async_shared();  // (ahead of the next copy to this place)
           }
+          if (__builtin_expect(ok == 0, 0)) {  // no tokens: zeros
+#pragma unroll 1
+            for (int e = 0; e < N; ++e) {
+              const int row = t0 + e * ROWS + r0, c = 2 * (piece & 3) + odd;
+              *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(dst + row * 128 + (((c ^ 1) ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+            }
+          } else
 #pragma unroll 1
           for (int e0 = 0; e0 < N; e0 += 4) {
             uint4 v[4];
@@ -677,6 +703,8 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
             const int u = x & 1, n = u ? n1 : n0, left = n - (x >> 1);
             const bool next = !both || u;  // (the last one that needs the place)
             if (x >= 0 && left <= 0) continue;
+            // (streams of the same tiles: the next one, there long since, is seen ahead of the weights, for both)
+            if (both && !u && left > 1 && !(ok = await(&ss.v_full[s1], phase))) break;
             ok = await(x < 0 ? &ss.q_full[u] : &ss.p_full[u], x < 0 ? item & 1 : (pc >> u) & 1);
             if (!ok) break;
             if (x >= 0) {
@@ -695,8 +723,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
               mbar_arrive(&ss.o_full[u]);
             }
             if (left <= 1) continue;
-            ok = await(&ss.v_full[s1], phase);
-            if (!ok) break;
+            if (!both && !(ok = await(&ss.v_full[s1], phase))) break;
             uint64_t qd = q0 + u * (F::Q_BYTES / 16), kd = k0 + s1 * (F::WIDE / 16);
 #pragma unroll 2
             for (int k = 0; k < DH / 16; ++k) {
@@ -900,6 +927,8 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
         if (!wait(&ss.s_full[u], sc & 1, a.status, abort)) return;
         if (!idle) {
           tc_fence_after();
+          uint32_t raw[2][16];
+          ld_rows(s_at, raw[0]);
           const bool part = ss.part[s];
           const float4 most4 = *reinterpret_cast<const float4*>(ss.most[s]);
           const float most = fmaxf(fmaxf(most4.x, most4.y), fmaxf(most4.z, most4.w));
@@ -970,46 +999,45 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
           // for, or all where some are hidden).  (32 tokens at a time, the next ones' scores fetched meanwhile; the
           // weights take the scores' place when none was too large.)
           bool plain = !scaled && !bad;
-          if (part && plain) {
-            // scores that their rows do not see: what makes their exponents -inf
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t w[2] = {sees(0, c), sees(1, c)};
-              if (__all_sync(0xffffffffu, (w[0] & w[1]) == ~0u)) continue;
-              uint32_t raw[16];
-              float2 t[4];
-              ld_rows(s_at + 32 * c, raw);
-              factors(c, t);
-              tc_wait_ld();
-              loaded16(raw);
-#pragma unroll
-              for (int e = 0; e < 16; ++e)
-                if (!seen(w, e))
-                  raw[e] = 0xFF800000u ^ (__float_as_uint(e & 1 ? t[e >> 2].y : t[e >> 2].x) & 0x80000000u);
-              put_rows(s_at + 32 * c, raw);
-            }
-            tc_wait_st();
-          }
-          if (__builtin_expect(plain, 1)) {
-            uint32_t raw[2][16], p[4][8];
-            float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
-            ld_rows(s_at, raw[0]);
-            if (__builtin_expect(j == 0, 0)) {
-              float2 t[4];
+          if (__builtin_expect(!plain || part || j == 0, 0)) {
+            tc_wait_ld();
+            loaded16(raw[0]);
+            if (plain) {
+              // scores that their rows do not see: what makes their exponents -inf; an item's first references
               float top[2] = {-INFINITY, -INFINITY};
+              const int chunks = part ? 4 : 1;
 #pragma unroll 1
-              for (int c = part ? 3 : 0;; --c) {
-                if (part) ld_rows(s_at + 32 * c, raw[0]);
+              for (int c = 0; c < chunks; ++c) {
+                uint32_t w[2] = {~0u, ~0u};
+                if (part) w[0] = sees(0, c), w[1] = sees(1, c);
+                const bool all = __all_sync(0xffffffffu, (w[0] & w[1]) == ~0u);
+                if (all && j > 0) continue;
+                float2 t[4];
+                ld_rows(s_at + 32 * c, raw[0]);
                 factors(c, t);
                 tc_wait_ld();
                 loaded16(raw[0]);
-                logs(reinterpret_cast<float*>(raw[0]), t);
-                largest(reinterpret_cast<float*>(raw[0]), top);
-                if (c == 0) break;
+                if (!all) {
+                  const uint32_t mine[2] = {w[0] >> (2 * (lane & 3)), w[1] >> (2 * (lane & 3))};
+#pragma unroll
+                  for (int e = 0; e < 16; ++e)
+                    if (!(mine[(e >> 1) & 1] & (1u << (8 * (e >> 2) + (e & 1)))))
+                      raw[0][e] = 0xFF800000u ^ (__float_as_uint(e & 1 ? t[e >> 2].y : t[e >> 2].x) & 0x80000000u);
+                  put_rows(s_at + 32 * c, raw[0]);
+                }
+                if (j == 0) {
+                  logs(reinterpret_cast<float*>(raw[0]), t);
+                  largest(reinterpret_cast<float*>(raw[0]), top);
+                }
               }
-              move(top);
+              if (j == 0) move(top);
+              tc_wait_st();
               ld_rows(s_at, raw[0]);
             }
+          }
+          if (__builtin_expect(plain, 1)) {
+            uint32_t p[4][8];
+            float sum[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               float* x = reinterpret_cast<float*>(raw[c & 1]);

@@ -86,9 +86,10 @@ def model(items, NS, ST, seed, early_free=False, widen=2, quads=2):
     def mma():
         at, pc = [0], [0, 0]
 
-        def scores(mode, u, j):
+        def scores(mode, u, j, seen=False):
             i = at[0] + ring(mode, u, j)
-            yield "wait", v_full[i % NS], i // NS
+            if not seen:
+                yield "wait", v_full[i % NS], i // NS
             assert wide[i % NS] == i, "scores of another tile"
             yield lambda: s_full[u].arrive()
             s_full[u].arrive()
@@ -96,9 +97,12 @@ def model(items, NS, ST, seed, early_free=False, widen=2, quads=2):
 
         def role(item, mode, n):
             for u in range(2):
+                if mode == TWO_BLOCKS and u == 0 and n[0]:
+                    i = at[0]
+                    yield "wait", v_full[i % NS], i // NS
                 yield "wait", q_full[u], item
                 if n[u]:
-                    yield from scores(mode, u, 0)
+                    yield from scores(mode, u, 0, mode == TWO_BLOCKS)
                 else:
                     o_full[u].arrive()
                     yield 0
@@ -107,6 +111,8 @@ def model(items, NS, ST, seed, early_free=False, widen=2, quads=2):
                     if j >= n[u]:
                         break
                     i = at[0] + ring(mode, u, j)
+                    if mode == TWO_BLOCKS and u == 0 and j + 1 < n[u]:  # (for both streams)
+                        yield "wait", v_full[(i + 1) % NS], (i + 1) // NS
                     yield "wait", p_full[u], pc[u]
                     pc[u] += 1
                     assert wide[i % NS] == i, "a product of another tile"
@@ -120,7 +126,7 @@ def model(items, NS, ST, seed, early_free=False, widen=2, quads=2):
                     yield done
                     yield 0
                     if j + 1 < n[u]:
-                        yield from scores(mode, u, j + 1)
+                        yield from scores(mode, u, j + 1, mode == TWO_BLOCKS)
             at[0] += count(mode, n)
         yield from jobs(role)
 
