@@ -40,6 +40,7 @@ constexpr int MAX_GROUPS = MAX_PREFIX + MAX_REQ;
 constexpr int BLOCK = 128;       // queries
 constexpr int EXTRA = 3;         // what an item costs a CTA beside its steps, in steps
 constexpr int HALF = TT * 128;   // bytes of 64 dimensions of a tile, or a block, in f16
+constexpr int LONG = 16;         // tiles from which on a lone block's slices are an item each
 constexpr int JOBS = 4;          // items whose rows are made ahead
 constexpr float BASE = 6.0f, LEAST = -90.0f;  // log2 of the weights times a_t that m puts at most; a_t below
 constexpr float TOO_LARGE = 0x1p15f;           // m moves when a weight times a_t may be larger (f16 ends at 2^16)
@@ -116,16 +117,23 @@ __device__ __forceinline__ int token_slot(int t) {
 }
 
 // A group's items.  First those of two blocks: for every slice the pairs of blocks.  Then those of an odd
-// last block: of two slices each, and if a slice is left, one whose streams take every other tile.
+// last block: of two slices each, and if a slice is left, one whose streams take every other tile; in a long
+// group all slices are such items, since these have half as many pieces.
 enum { TWO_BLOCKS, TWO_SLICES, TWO_TILES };
 struct Items {
   int tiles, blocks, len, half;  // lengths in the line of an item, and of one of TWO_TILES
   __device__ Items(const Args& ar, int tiles, int rows)
       : tiles(tiles), blocks(ar.by_rows(rows + ar.rows_per - 1)), len(EXTRA + tiles), half(EXTRA + (tiles + 1) / 2) {}
   __device__ int of_pairs(const Args& ar) const { return ar.slices * (blocks >> 1); }
-  __device__ int whole(const Args& ar) const { return of_pairs(ar) + (blocks & 1) * (ar.slices >> 1); }
-  __device__ int units(const Args& ar) const { return tiles ? whole(ar) * len + (blocks & ar.slices & 1) * half : 0; }
-  __device__ int count(const Args& ar) const { return whole(ar) + (blocks & ar.slices & 1); }
+  // slices of a lone block that are two to an item
+  __device__ int joint(const Args& ar) const { return tiles < LONG ? ar.slices & ~1 : 0; }
+  __device__ int whole(const Args& ar) const { return of_pairs(ar) + (blocks & 1) * (joint(ar) >> 1); }
+  __device__ int count(const Args& ar) const { return whole(ar) + (blocks & 1) * (ar.slices - joint(ar)); }
+  __device__ int at(const Args& ar, int item) const {  // an item's place
+    const int n = whole(ar);
+    return min(item, n) * len + max(item - n, 0) * half;
+  }
+  __device__ int units(const Args& ar) const { return tiles ? at(ar, count(ar)) : 0; }
 };
 __device__ __forceinline__ Items items_of(const Args& ar, const Plan& p, int g) {
   return Items(ar, p.tiles[g], p.cnt[g]);
@@ -169,7 +177,7 @@ __device__ __forceinline__ bool next_job(const Args& ar, const Plan& p, Cursor& 
     } else {
       job.block = it.blocks - 1;
       job.mode = c.item < whole ? TWO_SLICES : TWO_TILES;
-      job.slice = 2 * (c.item - of_pairs);  // (the last slice where it is alone)
+      job.slice = c.item < whole ? 2 * (c.item - of_pairs) : it.joint(ar) + c.item - whole;
       if (job.mode == TWO_TILES) {
         job.tile += s0;
         job.n[1] = min(2 * s1, it.tiles) - 2 * s0 - job.n[0];
@@ -307,6 +315,10 @@ __device__ __forceinline__ void derive_plan(const Args& ar, Plan& plan, int* sum
   for (int g = tid; g < groups; g += THREADS) plan.end[g] = 0, plan.cnt[g] = 0, plan.first[g] = 0;
   pdl_trigger();
   pdl_wait();
+  static_assert(MAX_REQ <= THREADS && MAX_PREFIX <= THREADS, "a request a thread");
+  int g = -1, len = 0;  // (fetched ahead of the first use of any)
+  if (tid < a.n_req) g = a.prefix_of ? a.prefix_of[tid] : 0;
+  if (tid < np) len = a.prefix_lengths[tid];
   // (loops that most steps run once are kept small: this code runs once, and comes from memory)
 #pragma unroll 1
   for (int r = tid; r < a.rows; r += THREADS) {
@@ -314,14 +326,11 @@ __device__ __forceinline__ void derive_plan(const Args& ar, Plan& plan, int* sum
     plan.hi[r] = min(p, 0x7FFFFFFE);
     plan.req[r] = (short)(b < 0 || b >= a.n_req ? -1 : b);
   }
-  static_assert(MAX_REQ <= THREADS && MAX_PREFIX <= THREADS, "a request a thread");
-  int g = -1;
   if (tid < a.n_req) {
-    g = a.prefix_of ? a.prefix_of[tid] : 0;
     if (g < -1 || g >= np) g = -2;
     plan.pfx[tid] = (short)g;
   }
-  if (tid < np) plan.len[tid] = max(0, a.prefix_lengths[tid]);
+  if (tid < np) plan.len[tid] = max(0, len);
   __syncthreads();
   if (g >= 0) plan.first[np + tid] = plan.len[g];
   // a request's rows and their largest position
@@ -392,9 +401,9 @@ __device__ __forceinline__ Cursor cut_line(const Args& ar, const Plan& plan) {
     const int g = c.g + lane;
     c.g += __popc(__ballot_sync(0xffffffffu, lane < each && g < groups && plan.pre[min(g, groups)] <= w0)) - 1;
     const Items it = items_of(ar, plan, c.g);
-    const int u = w0 - plan.pre[c.g];
-    c.item = min(u / it.len, it.whole(ar));
-    c.unit = u - c.item * it.len;
+    const int u = w0 - plan.pre[c.g], whole = it.whole(ar), more = u - whole * it.len;
+    c.item = more < 0 ? u / it.len : whole + more / it.half;
+    c.unit = u - it.at(ar, c.item);
   }
   return c;
 }
@@ -814,12 +823,12 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
               item = slice * pairs + (block >> 1);
               first = (block & 1) * BLOCK;
             } else {
-              item = it.of_pairs(ar) + (slice >> 1);
-              if (item < it.whole(ar)) first = (slice & 1) * BLOCK;
-              else len = it.half;
+              const int joint = it.joint(ar);
+              if (slice < joint) item = it.of_pairs(ar) + (slice >> 1), first = (slice & 1) * BLOCK;
+              else item = it.whole(ar) + slice - joint, len = it.half;
             }
             if (it.tiles) {
-              const int from = plan.pre[at] + item * it.len, k = cut.team_of(from + EXTRA);
+              const int from = plan.pre[at] + it.at(ar, item), k = cut.team_of(from + EXTRA);
               v = make_int2(cut.team_of(from + len - 1) - k + 1,
                             (k + 1) * (2 * BLOCK) + first + (rank - block * ar.rows_per) * ar.hps);
             }
@@ -1025,7 +1034,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
                       raw[0][e] = 0xFF800000u ^ (__float_as_uint(e & 1 ? t[e >> 2].y : t[e >> 2].x) & 0x80000000u);
                   put_rows(s_at + 32 * c, raw[0]);
                 }
-                if (j == 0) {
+                if (j == 0 && __any_sync(0xffffffffu, w[0] | w[1])) {
                   logs(reinterpret_cast<float*>(raw[0]), t);
                   largest(reinterpret_cast<float*>(raw[0]), top);
                 }
@@ -1253,24 +1262,42 @@ __global__ void __launch_bounds__(MAX_TEAM * 32) join_shared_kernel(const __grid
   pdl_trigger();
   pdl_wait();
   const int4 info = h < a.n_q ? reinterpret_cast<const int4*>(ar.info)[r * ar.slices + slice] : make_int4(0, 0, 0, 0);
-  // where the pieces are, in floats behind `home` (which `over` is behind): a kind's first one, its others
-  const int home = (r * a.n_q + h) * ld, next = 2 * BLOCK * ld;
+  // where the pieces are, in floats behind `home` (which `over` is behind): the first ones, of its prefix and of
+  // its own tokens, and the others
+  const int home = (r * a.n_q + (h < a.n_q ? h : 0)) * ld, own_home = home + ar.max_rows * a.n_q * ld, next = 2 * BLOCK * ld;
   const int over = (int)(ar.over - ar.home) + (h - slice * ar.hps) * ld;
-  // this warp's (from one lane, so that the compiler knows the loops to be the whole warp's)
-  const int all = __shfl_sync(0xffffffffu, (info.x + info.z - mate + team - 1) / team, 0);
   float m = UNSET, den = 0.0f;
   float4 num = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto part_of = [&](const float2& ml) {  // (a piece that saw nothing has no part; a NaN stays one)
+    return ml.y != ml.y ? 1.0f : ml.y == 0.0f ? 0.0f : ex2(ml.x - m);
+  };
+  auto add = [&](float f, const float4& x) {
+    num.x = fmaf(f, x.x, num.x), num.y = fmaf(f, x.y, num.y);
+    num.z = fmaf(f, x.z, num.z), num.w = fmaf(f, x.w, num.w);
+  };
+  if (mate == 0) {  // the first ones, fetched before it is known that they are there
+    float2 p = *reinterpret_cast<const float2*>(ar.home + home), q = *reinterpret_cast<const float2*>(ar.home + own_home);
+    const float4 x = *reinterpret_cast<const float4*>(ar.home + home + 8 + d),
+                 y = *reinterpret_cast<const float4*>(ar.home + own_home + 8 + d);
+    if (info.x <= 0) p = {UNSET, 0.0f};
+    if (info.z <= 0) q = {UNSET, 0.0f};
+    m = fmaxf(p.x, q.x);
+    const float f = part_of(p), g = part_of(q);
+    den = (f != 0.0f ? f * p.y : 0.0f) + (g != 0.0f ? g * q.y : 0.0f);
+    if (f != 0.0f && own == 0) add(f, x);
+    if (g != 0.0f && own == step - 1) add(g, y);
+  }
+  // this warp's others (from one lane, so that the compiler knows the loops to be the whole warp's)
+  const int of_prefix = max(info.x - 1, 0);
+  const int all = __shfl_sync(0xffffffffu, (of_prefix + max(info.z - 1, 0) - mate + team - 1) / team, 0);
 #pragma unroll 1
   for (int b = 0; b < all; b += 32) {
     const int in = min(32, all - b);
     int at = home;  // a piece a lane
     float2 ml = {UNSET, 0.0f};
     if (lane < in) {
-      int i = (b + lane) * team + mate;
-      const bool own_tokens = i >= info.x;
-      if (own_tokens) i -= info.x;
-      at = i == 0 ? home + (own_tokens ? ar.max_rows * a.n_q * ld : 0)
-                  : over + (own_tokens ? info.w : info.y) * ld + (i - 1) * next;
+      const int i = (b + lane) * team + mate;
+      at = over + (i < of_prefix ? info.y * ld + i * next : info.w * ld + (i - of_prefix) * next);
       ml = *reinterpret_cast<const float2*>(ar.home + at);
     }
     float4 x[AHEAD];
@@ -1281,10 +1308,9 @@ __global__ void __launch_bounds__(MAX_TEAM * 32) join_shared_kernel(const __grid
             ar.home + __shfl_sync(0xffffffffu, at, min(i + own + step * e, in - 1)) + 8 + d);
     };
     fetch(0);
-    const float to = fmaxf(m, warp_max(ml.x)), old = m == to ? 1.0f : ex2(m - to);
-    // (a piece that saw nothing has no part; a NaN stays one)
-    const float f = ml.y != ml.y ? 1.0f : ml.y == 0.0f ? 0.0f : ex2(ml.x - to);
-    m = to;
+    const float old_m = m;
+    m = fmaxf(m, warp_max(ml.x));
+    const float old = old_m == m ? 1.0f : ex2(old_m - m), f = part_of(ml);
     den = fmaf(den, old, warp_sum(f != 0.0f ? f * ml.y : 0.0f));
     num.x *= old, num.y *= old, num.z *= old, num.w *= old;
 #pragma unroll 1
@@ -1292,11 +1318,8 @@ __global__ void __launch_bounds__(MAX_TEAM * 32) join_shared_kernel(const __grid
 #pragma unroll
       for (int e = 0; e < AHEAD; ++e) {
         const int k = i + own + step * e;
-        float g = __shfl_sync(0xffffffffu, f, k & 31);
-        if (k < in && g != 0.0f) {
-          num.x = fmaf(g, x[e].x, num.x), num.y = fmaf(g, x[e].y, num.y);
-          num.z = fmaf(g, x[e].z, num.z), num.w = fmaf(g, x[e].w, num.w);
-        }
+        const float g = __shfl_sync(0xffffffffu, f, k & 31);
+        if (k < in && g != 0.0f) add(g, x[e]);
       }
       i += step * AHEAD;
       if (i >= in) break;
