@@ -169,6 +169,18 @@ def test_many_steps_of_single_blocks(layout, P):
     check(LAYOUTS[layout], [P - 3 * i for i in range(n)], list(range(n)), [2 + i % 3 for i in range(n)], [2] * n, seed=13)
 
 
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("P", [14 * 128 + 1, 15 * 128 + 1, 16 * 128 - 1, 17 * 128 + 5])
+def test_lone_blocks_of_long_groups(layout, P):
+    """About as many tiles as decide how a lone block's slices are taken, of a prefix and of own tokens,
+    alone and behind a pair of blocks."""
+    spec = LAYOUTS[layout]
+    per = 128 // (spec["n_q_heads"] * spec["head_dim"] // spec["kv_dim"])  # rows a block
+    check(spec, [P], [0, -1], [3, P], [1, 1], seed=P)
+    if per <= 32:
+        check(spec, [P], [0], [2 * per + 40], [2 * per + 1], seed=P + 1)
+
+
 def test_without_any_prefix_and_with_empty_ones():
     check(WIDE, [64], [-1, -1], [300, 20], [3, 2], seed=3)
     check(WIDE, [0, 64], [0, 1], [300, 20], [3, 2], seed=4)
