@@ -97,7 +97,7 @@ struct Args {
   CUtensorMap codes, scales;
   int box;  // 0: no maps
   int slices, hps, rows_per;  // latent slices, heads of one, rows of a block
-  Divisor by_page, by_hps, by_rows;  // block_size, hps, rows_per
+  Divisor by_page, by_hps, by_rows, by_grid;  // block_size, hps, rows_per, CTAs
   SharedArgs a;
   float* home;   // pieces: [2][max_rows][n_q], of those that begin an item; prefixes', then own tokens'
   float* over;   // [CTAs][2 * BLOCK], of a CTA's item that began before it
@@ -388,10 +388,20 @@ __device__ __forceinline__ void derive_plan(const Args& ar, Plan& plan, int* sum
   if (tid == 0) plan.pre[0] = 0;
 }
 
+// The cut of a line of W.
+__device__ __forceinline__ Cut cut_of(const Args& ar, int W) {
+  const int n = gridDim.x;
+  Cut cut(min(W, 1), 1);
+  cut.teams = min(W, n);
+  cut.each = W >= n ? ar.by_grid(W) : min(W, 1);
+  cut.more = W - cut.each * cut.teams;
+  return cut;
+}
+
 // The CTA's first item, by a whole warp.
 __device__ __forceinline__ Cursor cut_line(const Args& ar, const Plan& plan) {
   const int lane = threadIdx.x & 31, groups = ar.a.n_prefix + ar.a.n_req;
-  const Cut cut(plan.pre[groups], gridDim.x);
+  const Cut cut = cut_of(ar, plan.pre[groups]);
   Cursor c = {0, 0, 0, cut.size(blockIdx.x)};
   if (c.left > 0) {
     // the last group that starts by w0 (and is not empty: the next starts later), a lane a run of groups, then a group
@@ -401,9 +411,10 @@ __device__ __forceinline__ Cursor cut_line(const Args& ar, const Plan& plan) {
     const int g = c.g + lane;
     c.g += __popc(__ballot_sync(0xffffffffu, lane < each && g < groups && plan.pre[min(g, groups)] <= w0)) - 1;
     const Items it = items_of(ar, plan, c.g);
-    const int u = w0 - plan.pre[c.g], whole = it.whole(ar), more = u - whole * it.len;
-    c.item = more < 0 ? u / it.len : whole + more / it.half;
-    c.unit = u - it.at(ar, c.item);
+    const int u = w0 - plan.pre[c.g], whole = it.whole(ar), more = u - whole * it.len, len = more < 0 ? it.len : it.half;
+    const int n = (more < 0 ? u : more) / len;
+    c.item = more < 0 ? n : whole + n;
+    c.unit = (more < 0 ? u : more) - n * len;
   }
   return c;
 }
@@ -796,7 +807,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
       }
       // where the join finds the pieces of a row's queries in a slice: how many of its prefix's tokens, and of its
       // own, and the place of the second of each
-      const Cut cut(plan.pre[a.n_prefix + a.n_req], gridDim.x);
+      const Cut cut = cut_of(ar, plan.pre[a.n_prefix + a.n_req]);
 #pragma unroll 1
       for (int r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const int b = plan.req[r], g = b < 0 ? -1 : plan.pfx[b];
@@ -1410,6 +1421,7 @@ cudaError_t launch_attend_shared(const Launch& L, const SharedArgs& a, uint8_t* 
   ar.by_page = Divisor::of(a.kv.block_size);
   ar.by_hps = Divisor::of(ar.hps);
   ar.by_rows = Divisor::of(ar.rows_per);
+  ar.by_grid = Divisor::of(sms);
   ar.info = reinterpret_cast<int*>(ws + l.info);
   ar.home = reinterpret_cast<float*>(ws + l.home);
   ar.over = reinterpret_cast<float*>(ws + l.over);
