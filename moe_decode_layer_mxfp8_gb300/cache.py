@@ -141,10 +141,14 @@ def _vec(t, name, dtype, n, device):
 
 def _mat(t, name, dtypes, rows, cols, device):
     """(address, row stride) of a [rows, cols] matrix (None: any) with contiguous rows."""
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     if (t.dtype not in dtypes or t.get_device() != device or len(shape) != 2
-            or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols)
-            or (shape[1] > 1 and stride[1] != 1) or (shape[0] > 1 and stride[0] < shape[1])):
+            or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols)):
+        _bad(t, name, dtypes, (rows, cols), device, False)
+    if t.is_contiguous():  # (most are, and their strides take twice as long to ask for)
+        return t.data_ptr(), shape[1]
+    stride = t.stride()
+    if (shape[1] > 1 and stride[1] != 1) or (shape[0] > 1 and stride[0] < shape[1]):
         _bad(t, name, dtypes, (rows, cols), device, False)
     return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1]
 
@@ -182,6 +186,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
+_functions = {}  # the library's, by name
+
+
 def _call(name, device, stream, *args):
     """Calls the library with `device` current, on `stream` or torch's current one."""
     if stream is None:
@@ -190,7 +197,7 @@ def _call(name, device, stream, *args):
         raise ValueError(f"the stream is on {stream.device}, not cuda:{device}")
     else:
         raw = stream.cuda_stream
-    fn = getattr(_lib(), name)
+    fn = _functions.get(name) or _functions.setdefault(name, getattr(_lib(), name))
     if _current_device() == device:
         rc = fn(*args, raw)
     else:
