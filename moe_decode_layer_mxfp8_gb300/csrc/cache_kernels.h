@@ -92,8 +92,8 @@ struct RotateArgs {
   const int* row_req;
   PagedView cache;
   int* status;
-  // the launch's: slots of heads that share a row; threads of a latent, CTAs of latents
-  int across, span;
+  // the launch's: slots of heads that share a row; threads of a latent, CTAs of latents, log2 of how far apart these are
+  int across, span, apart;
   unsigned kv_blocks;
 };
 
