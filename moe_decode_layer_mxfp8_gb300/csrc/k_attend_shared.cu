@@ -1261,14 +1261,14 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
 
 // Joins the pieces of a (row, head), of its prefix and its own tokens: `team` warps each, which take them in
 // turn; 4 dimensions a lane (64 wide: the half warps take every other piece).
-constexpr int JOIN_WARPS = 4, MAX_TEAM = 8, AHEAD = 6, TEAM_WARPS = 32;
-__global__ void __launch_bounds__(MAX_TEAM * 32) join_shared_kernel(const __grid_constant__ Args ar, int team) {
+constexpr int JOIN_WARPS = 4, MAX_TEAM = 8, AHEAD = 6, TEAM_WARPS = 32, FEW = 3;
+__global__ void __launch_bounds__(MAX_TEAM * 32) join_shared_kernel(const __grid_constant__ Args ar, int team_log2) {
   __shared__ float2 ml_of[MAX_TEAM];
   __shared__ float4 num_of[MAX_TEAM][32];
   const SharedArgs& a = ar.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mate = warp & (team - 1);
-  const int r = blockIdx.x, h = (blockIdx.y * (blockDim.x >> 5) + warp) / team;
-  const int dh = a.head_dim, d = 4 * lane & (dh - 1), step = 128 / dh, own = lane * 4 / dh;
+  const int team = 1 << team_log2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mate = warp & (team - 1);
+  const int r = blockIdx.x, h = (blockIdx.y * (blockDim.x >> 5) + warp) >> team_log2;
+  const int dh = a.head_dim, d = 4 * lane & (dh - 1), step = dh == 128 ? 1 : 2, own = dh == 128 ? 0 : lane >> 4;
   const int slice = ar.by_hps(h), ld = dh + 8;
   pdl_trigger();
   pdl_wait();
@@ -1300,15 +1300,41 @@ __global__ void __launch_bounds__(MAX_TEAM * 32) join_shared_kernel(const __grid
   }
   // this warp's others (from one lane, so that the compiler knows the loops to be the whole warp's)
   const int of_prefix = max(info.x - 1, 0);
-  const int all = __shfl_sync(0xffffffffu, (of_prefix + max(info.z - 1, 0) - mate + team - 1) / team, 0);
+  const int all = __shfl_sync(0xffffffffu, (of_prefix + max(info.z - 1, 0) - mate + team - 1) >> team_log2, 0);
+  auto place = [&](int i) { return over + (i < of_prefix ? info.y * ld + i * next : info.w * ld + (i - of_prefix) * next); };
+  if (all > 0 && all <= FEW) {
+    // (as most are where there are many to join: of 500 instructions a warp half went into the general way)
+    float2 ml[FEW];
+    float4 x[FEW];
+#pragma unroll
+    for (int e = 0; e < FEW; ++e) {
+      ml[e] = {UNSET, 0.0f};
+      if (e >= all) continue;
+      const float* at = ar.home + place((e << team_log2) + mate);
+      ml[e] = *reinterpret_cast<const float2*>(at);
+      if ((e & (step - 1)) == own) x[e] = *reinterpret_cast<const float4*>(at + 8 + d);
+    }
+    const float old_m = m;
+#pragma unroll
+    for (int e = 0; e < FEW; ++e) m = fmaxf(m, ml[e].x);
+    const float old = old_m == m ? 1.0f : ex2(old_m - m);
+    den *= old;
+    num.x *= old, num.y *= old, num.z *= old, num.w *= old;
+#pragma unroll
+    for (int e = 0; e < FEW; ++e) {
+      const float f = part_of(ml[e]);
+      if (e >= all || f == 0.0f) continue;
+      den = fmaf(f, ml[e].y, den);
+      if ((e & (step - 1)) == own) add(f, x[e]);
+    }
+  } else
 #pragma unroll 1
   for (int b = 0; b < all; b += 32) {
     const int in = min(32, all - b);
     int at = home;  // a piece a lane
     float2 ml = {UNSET, 0.0f};
     if (lane < in) {
-      const int i = (b + lane) * team + mate;
-      at = over + (i < of_prefix ? info.y * ld + i * next : info.w * ld + (i - of_prefix) * next);
+      at = place(((b + lane) << team_log2) + mate);
       ml = *reinterpret_cast<const float2*>(ar.home + at);
     }
     float4 x[AHEAD];
@@ -1431,11 +1457,11 @@ cudaError_t launch_attend_shared(const Launch& L, const SharedArgs& a, uint8_t* 
                       ? launch_ex(L, dim3(sms), dim3(THREADS), Form<128>::SMEM_BYTES, attend_shared_kernel<128>, ar)
                       : launch_ex(L, dim3(sms), dim3(THREADS), Form<64>::SMEM_BYTES, attend_shared_kernel<64>, ar);
   // Few queries have many pieces each: teams of warps, as many as the GPU holds at once.
-  int team = 1;
-  while (team < MAX_TEAM && 2LL * team * a.rows * a.n_q <= TEAM_WARPS * sms) team *= 2;
-  const int warps = team > JOIN_WARPS ? team : JOIN_WARPS;
+  int log2 = 0;
+  while ((1 << log2) < MAX_TEAM && (2LL << log2) * a.rows * a.n_q <= TEAM_WARPS * sms) ++log2;
+  const int team = 1 << log2, warps = team > JOIN_WARPS ? team : JOIN_WARPS;
   if (e == cudaSuccess)
-    e = launch_ex(L, dim3(a.rows, (a.n_q * team + warps - 1) / warps), dim3(warps * 32), 0, join_shared_kernel, ar, team);
+    e = launch_ex(L, dim3(a.rows, (a.n_q * team + warps - 1) / warps), dim3(warps * 32), 0, join_shared_kernel, ar, log2);
   return e;
 }
 
