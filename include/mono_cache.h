@@ -1,11 +1,11 @@
 /*
  * mono_cache.h -- C ABI of the operators around the decode layer's paged KV cache, for one
  * GB300 (sm_103a): attention of a step's rows over their requests' whole cached context (or a
- * sliding window with first tokens that stay visible, or prefixes that requests share), eviction of the tokens that gathered
- * the least attention weight, appending rows' latents with their rotary positions, and verification
- * of drafted tokens.  They serve the layers
- * whose attention runs outside mono_layer_step (mono_ffn_step takes its output) and the
- * serving loop around a stack of layers; the same library and error codes (mono_layer.h).
+ * sliding window with first tokens that stay visible, or prefixes that requests share), eviction
+ * of the tokens that gathered the least attention weight, appending rows' latents with their
+ * rotary positions, and verification of drafted tokens.  They serve the layers whose attention
+ * runs outside mono_layer_step (mono_ffn_step takes its output) and the serving loop around a
+ * stack of layers; the same library and error codes (mono_layer.h).
  *
  * Conventions are those of mono_layer.h: device pointers borrowed from the caller, negative
  * MONO_ERR_* codes and no aborts, arguments checked on the host before anything is enqueued,
@@ -99,22 +99,24 @@ typedef struct {
 int mono_cache_attend(mono_cache_t *h, const mono_attend_args *args, void *stream);
 
 /*
- * Attention of requests that share prefixes.  As mono_cache_attend without a window, but the first
- * P = prefix_lengths[prefix_of[b]] tokens of request b are those of a prefix, at prefix_table's row
- * prefix_of[b], and read once for all rows of all its requests; its own tokens, t >= P, are at
- * block_table[b][t / block_size] as ever (entries that lie in the prefix alone are not read), so that
- * both tables may be those of whole contexts.  prefix_of[b] = -1: no prefix; prefix_of NULL: prefix 0 for
- * all.  Row r at position p sees t <= hi, hi as there; a row inside its prefix sees that much of it.
+ * Attention of requests that share prefixes.  As mono_cache_attend without a window, but the
+ * first P = prefix_lengths[prefix_of[b]] tokens of request b are those of a prefix, at
+ * prefix_table's row prefix_of[b], and read once for all rows of all its requests; its own tokens,
+ * t >= P, are at block_table[b][t / block_size] as ever (entries that lie in the prefix alone are
+ * not read), so that both tables may be those of whole contexts.  prefix_of[b] = -1: no prefix;
+ * prefix_of NULL: prefix 0 for all.  Row r at position p sees t <= hi, hi as there; a row inside
+ * its prefix sees that much of it.
  *
  * Sums, refused and masked tokens, status bits, pad rows, lse and the handle's workspace are as in
- * mono_cache_attend; o is rounded to bf16 once, w[t] scale_t to 11 bits before that (and to 2^-30 of the
- * largest of the 32 to 128 tokens that set a row's reference), q's elements to 2^-24 of a head's
- * largest; scale_t below 2^-64 in size lose bits of o.  A NaN code of a token in view makes NaN the heads of its slice.  Scores of heads whose
- * largest is beyond 2^26 in size are NaN.  Rows of requests whose prefix_of is outside [-1, n_prefix) are
- * left out, o = 0, and raise MONO_STATUS_UNMAPPED_PAGE.  A negative length counts as 0.
+ * mono_cache_attend; o is rounded to bf16 once, w[t] scale_t to 11 bits before that (and to 2^-30
+ * of the largest of the 32 to 128 tokens that set a row's reference), q's elements to 2^-24 of a
+ * head's largest; scale_t below 2^-64 in size lose bits of o.  A NaN code of a token in view makes
+ * NaN the heads of its slice.  Scores of heads whose largest is beyond 2^26 in size are NaN.  Rows
+ * of requests whose prefix_of is outside [-1, n_prefix) are left out, o = 0, and raise
+ * MONO_STATUS_UNMAPPED_PAGE.  A negative length counts as 0.
  *
- * Limits: n_prefix 1..128; 2 * rows * (kv_dim / head_dim) times the tiles of the longer table, and 4 more,
- * below 2^31; both tables' max_blocks * block_size at most 2^31 - 2^16.
+ * Limits: n_prefix 1..128; 2 * rows * (kv_dim / head_dim) times the tiles (of 128 tokens) of the
+ * longer table, and 4 more, below 2^31; both tables' max_blocks * block_size at most 2^31 - 2^16.
  */
 typedef struct {
   const void *q;              /* bf16 [rows, n_q_heads * head_dim], 16-byte aligned */
@@ -202,17 +204,18 @@ typedef struct {
 enum { MONO_TYPE_F32 = 0, MONO_TYPE_BF16 = 1, MONO_TYPE_F16 = 2 };
 
 /*
- * Appending to the cache, with the rotation on the way.  Row r's latent kv[r], its slices turned by
- * rope_positions[r] (NULL: positions[r]; after an eviction the two differ), is stored as the record of
- * slot positions[r] of request row_req[r], as mono_layer_step stores one: s = amax / 448 (1 where that
- * is 0), codes = e4m3 of latent / s, to nearest even and saturating, then s; bytes behind them are left
- * as they were.  The rotated latent is not rounded before.  q, if given, is turned by the same positions
- * into q_out (which may be q), every head of it.  Rows with positions[r] < 0 (pad rows) write nothing.
- * Rows with row_req outside [0, n_req) and rows of unmapped pages store no record (their queries
- * are turned) and raise MONO_STATUS_UNMAPPED_PAGE.  A NaN of the latent is a NaN code and does not
- * count in amax; a latent with an infinity gets an infinite scale.  Rows that name the same slot leave
- * an undefined record there.  Any number of rows (at most 2^30) and requests: max_rows and max_req
- * are no limits here, and no workspace is used.
+ * Appending to the cache, with the rotation on the way.  Row r's latent kv[r], its slices turned
+ * by rope_positions[r] (NULL: positions[r]; after an eviction the two differ), is stored as the
+ * record of slot positions[r] of request row_req[r], as mono_layer_step stores one: s = amax / 448
+ * (1 where that is 0), codes = e4m3 of latent / s, to nearest even and saturating, then s; bytes
+ * behind them are left as they were.  The rotated latent is not rounded before.  q, if given, is
+ * turned by the same positions into q_out (which may be q), every head of it.  Rows with
+ * positions[r] < 0 (pad rows) write nothing.  Rows with row_req outside [0, n_req) and rows of
+ * unmapped pages store no record (their queries are turned) and raise MONO_STATUS_UNMAPPED_PAGE.
+ * A NaN of the latent is a NaN code and does not count in amax; a latent with an infinity gets an
+ * infinite scale.  Rows that name the same slot leave an undefined record there.  Any number of
+ * rows (at most 2^30) and requests: max_rows and max_req are no limits here, and no workspace is
+ * used.
  */
 typedef struct {
   const void *kv;             /* [rows, kv_dim], 16-byte aligned, not in the cache */

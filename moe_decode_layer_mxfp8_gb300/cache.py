@@ -1,5 +1,6 @@
 """Python binding of the cache operators' C ABI (include/mono_cache.h): attention over a paged
-fp8 cache, eviction by accumulated attention weight, verification of drafted tokens.
+fp8 cache (also behind prefixes that requests share), eviction by accumulated attention weight,
+appending and rotating by position, verification of drafted tokens.
 
 Argument marshalling and checks only; the operators run in the library's CUDA kernels.  Tensors
 must be CUDA tensors of one device and stay valid until the enqueued work has run.  A wrong
@@ -96,7 +97,8 @@ _ROTATE = struct.Struct("@PPqqPPqqiiiiiii4x")
 _VERIFY = struct.Struct("@PPqqiiiiPPPPPPP")
 
 CACHE_EXPORTS = ["mono_cache_build", "mono_cache_free", "mono_cache_status", "mono_cache_attend",
-                 "mono_cache_attend_shared", "mono_cache_evict", "mono_cache_append", "mono_cache_rotate", "mono_verify_drafts"]
+                 "mono_cache_attend_shared", "mono_cache_evict", "mono_cache_append",
+                 "mono_cache_rotate", "mono_verify_drafts"]
 
 
 def _lib() -> C.CDLL:
@@ -352,7 +354,9 @@ class Cache:
             if rope is None:
                 raise ValueError("q needs a rope table")
             qp, qs = _mat(q, "q", (dtype,), rows, self._width, dev)
-            op, os = (qp, qs) if q_out is None else _mat(q_out, "q_out", (dtype,), rows, self._width, dev)
+            op, os = qp, qs
+            if q_out is not None:
+                op, os = _mat(q_out, "q_out", (dtype,), rows, self._width, dev)
         elif q_out is not None:
             raise ValueError("q_out needs a q")
         if rope is not None:
@@ -361,11 +365,13 @@ class Cache:
             raise ValueError("rope_positions and rope_offset need a rope table")
         else:
             turn = (0, 0, 0, 0, 0, 0, 0)
+        rp = 0
+        if rope_positions is not None:
+            rp = _vec(rope_positions, "rope_positions", i32, rows, dev)
         args = _pack(_APPEND, kp, qp, op, ks, qs, os, _vec(positions, "positions", i32, rows, dev),
-                     0 if rope_positions is None else _vec(rope_positions, "rope_positions", i32, rows, dev),
-                     _vec(row_req, "row_req", i32, rows, dev),
-                     _table(block_table, "block_table", None, dev), *self._view(kv_cache, "kv_cache"),
-                     *turn, _PROBS[dtype], rows, n_req, max_blocks)
+                     rp, _vec(row_req, "row_req", i32, rows, dev),
+                     _table(block_table, "block_table", None, dev),
+                     *self._view(kv_cache, "kv_cache"), *turn, _PROBS[dtype], rows, n_req, max_blocks)
         self._call("mono_cache_append", args, stream)
 
     def rotate(self, x, out, positions, rope, *, rope_offset=None, interleaved=False, inverse=False,

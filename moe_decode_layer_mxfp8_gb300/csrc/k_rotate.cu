@@ -14,9 +14,11 @@
 // of a warp, or whole warps, its largest element one reduction away from its codes.
 //
 // Bound by DRAM where steps are large, by latency (launch, position, table) where they are small.  Measured
-// in a graph: one request's token 2.5 us; 48 rows of 64 heads back 2.5; 20001 rows of 16 heads of 64, f16, 17.2
-// (5.0 TB/s of 6.8; a head a thread: 47); 23K prompt rows of 64 heads of 128 with their latents 148 (5.2
-// TB/s; 187 with CTAs of 256; twice as many loads in flight 157); 14K narrow f32 latents 5.3 (a warp each: 10).
+// in a graph: one request's token 2.5 us; 48 rows of 64 heads 2.7, back 2.6; 20001 rows of 16 heads of 64,
+// f16, 15.6 (5.4 TB/s of 6.8; a head a thread: 47); 22K prompt rows of 64 heads of 128 with their latents 134
+// (5.7 TB/s; with CTAs of 256 threads 40 more, with twice as many loads in flight 10; latents by the
+// heads' threads need 72 registers: 7 more), without latents 6.6 TB/s; 14K narrow f32 latents 5.1 (a warp
+// each: 10).
 #include "cache_kernels.h"
 
 namespace mono {
