@@ -2,7 +2,9 @@
 
 Each .cu file compiles to an object in parallel with
 ``nvcc -gencode arch=compute_103a,code=sm_103a -O3 -lineinfo``; the objects link into a
-shared library with the CUDA runtime linked statically.  Run ``python -m
+shared library with the CUDA runtime linked statically.  Beside it args.cpp becomes the Python
+extension _args, which checks tensor arguments; without it (no headers of torch or Python) cache.py
+does the same, slower.  Run ``python -m
 moe_decode_layer_mxfp8_gb300.build`` or call ``build()``.
 """
 from __future__ import annotations
@@ -12,12 +14,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmono_layer.so")
+ARGS_LIB = os.path.join(HERE, "_args.so")
 SOURCES = ["k_gemm.cu", "k_expert_tc.cu", "k_dense_tc.cu", "k_norm.cu", "k_attn.cu", "k_route.cu", "mono_layer.cu",
            "noalloc.cu", "k_attend.cu", "k_attend_weights.cu", "k_attend_join.cu", "k_evict.cu", "k_verify.cu",
            "k_rotate.cu", "k_attend_shared.cu", "cache_ops.cu"]
@@ -48,6 +52,34 @@ def _stale(obj: str, src: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_args(force: bool = False) -> str | None:
+    """The extension of csrc/args.cpp; None where it cannot be built."""
+    src, stamp = os.path.join(CSRC, "args.cpp"), os.path.join(OUT_DIR, "args.torch")
+    try:
+        import torch
+        if (not force and os.path.exists(ARGS_LIB) and os.path.exists(stamp)
+                and os.path.getmtime(ARGS_LIB) >= os.path.getmtime(src)
+                and open(stamp).read() == torch.__version__):
+            return ARGS_LIB
+        root = os.path.dirname(torch.__file__)
+        inc, lib = os.path.join(root, "include"), os.path.join(root, "lib")
+        tmp = ARGS_LIB + f".tmp{os.getpid()}"
+        cmd = ["g++", "-O1", "-std=c++17", "-fPIC", "-shared", "-w", f'-DARGS_TORCH="{torch.__version__}"',
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", inc, "-isystem",
+               os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+               src, "-o", tmp, "-L" + lib, "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(r.stderr[-2000:])
+        os.replace(tmp, ARGS_LIB)
+        with open(stamp, "w") as f:
+            f.write(torch.__version__)
+        return ARGS_LIB
+    except Exception as e:  # (the operators work without it)
+        sys.stderr.write(f"args.cpp was not built: {e}\n")
+        return None
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) -> str:
     nvcc = _nvcc()
     os.makedirs(OUT_DIR, exist_ok=True)
@@ -64,7 +96,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, quiet: bool = True) 
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, r
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, len(jobs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
+        ex.submit(build_args, force)
         for src, r in ex.map(run, jobs):
             if r.returncode != 0:
                 raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stderr}")

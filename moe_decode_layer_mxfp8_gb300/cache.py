@@ -134,8 +134,23 @@ def _bad(t, name, dtypes, shape, device, packed):
                      f"broadcast: strides {t.stride()}"))
 
 
+def _native():
+    """The extension that makes the checks below in a tenth of their time, if it is there for this torch."""
+    try:
+        from . import _args
+    except ImportError:
+        return None
+    return _args if _args.TORCH == torch.__version__ else None
+
+
+_args = _native()
+
+
 def _vec(t, name, dtype, n, device):
     """Address of a contiguous vector of n elements."""
+    p = _args and _args.vec(t, dtype, n, device)
+    if p is not None:
+        return p
     if t.dtype is not dtype or t.get_device() != device or t.shape != (n,) or not t.is_contiguous():
         _bad(t, name, (dtype,), (n,), device, True)
     return t.data_ptr()
@@ -143,11 +158,14 @@ def _vec(t, name, dtype, n, device):
 
 def _mat(t, name, dtypes, rows, cols, device):
     """(address, row stride) of a [rows, cols] matrix (None: any) with contiguous rows."""
+    p = _args and _args.mat(t, dtypes, -1 if rows is None else rows, -1 if cols is None else cols, device)
+    if p is not None:
+        return p
     shape = t.shape
     if (t.dtype not in dtypes or t.get_device() != device or len(shape) != 2
             or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols)):
         _bad(t, name, dtypes, (rows, cols), device, False)
-    if t.is_contiguous():  # (most are, and their strides take twice as long to ask for)
+    if shape[1] and t.is_contiguous():  # (most are, and their strides take twice as long to ask for)
         return t.data_ptr(), shape[1]
     stride = t.stride()
     if (shape[1] > 1 and stride[1] != 1) or (shape[0] > 1 and stride[0] < shape[1]):
@@ -164,6 +182,9 @@ def _weights(t, name, rows, device):
 
 
 def _table(t, name, rows, device):
+    p = _args and _args.table(t, torch.int32, -1 if rows is None else rows, device)
+    if p is not None:
+        return p
     if (t.dtype is not torch.int32 or t.get_device() != device or t.dim() != 2
             or (rows is not None and t.shape[0] != rows) or not t.is_contiguous()):
         _bad(t, name, (torch.int32,), (rows, None), device, True)
@@ -180,6 +201,7 @@ def _pack(layout, *values):
 _BF16, _F32 = (torch.bfloat16,), (torch.float32,)
 _LEAST, _MOST = 2.0 ** -149, (2.0 - 2.0 ** -23) * 2.0 ** 127  # an f32 above 0
 _PROBS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_FLOATS = tuple(_PROBS)
 
 
 # What torch.cuda.current_stream and current_device ask, without their wrappers (2 us of a call); not
@@ -229,6 +251,10 @@ class Cache:
         self._width = self.spec["n_q_heads"] * self.spec["head_dim"]
 
     def _view(self, t, name):
+        block, record = self.spec["block_size"], self.spec["kv_record_bytes"]
+        p = _args and _args.view(t, torch.uint8, block, record, self._dev)
+        if p is not None:
+            return p
         if t.dim() != 3 or t.dtype is not torch.uint8 or t.get_device() != self._dev:
             raise ValueError(f"{name} is a uint8 [blocks, block_size, record] view on {self.device}")
         shape, stride = t.shape, t.stride()
@@ -348,7 +374,7 @@ class Cache:
         dev, i32 = self._dev, torch.int32
         rows, dtype = kv.shape[0], kv.dtype
         n_req, max_blocks = block_table.shape
-        kp, ks = _mat(kv, "kv", _PROBS, rows, self.spec["kv_dim"], dev)
+        kp, ks = _mat(kv, "kv", _FLOATS, rows, self.spec["kv_dim"], dev)
         qp, qs, op, os = 0, 0, 0, 0
         if q is not None:
             if rope is None:
@@ -380,7 +406,7 @@ class Cache:
         rotary ``positions`` (-1: a pad row, left as it is) into ``out``, which may be x;
         ``inverse`` turns back.  ``rope``, ``rope_offset`` and ``interleaved`` as in append."""
         dev, dh = self._dev, self.spec["head_dim"]
-        xp, xs = _mat(x, "x", _PROBS, None, None, dev)
+        xp, xs = _mat(x, "x", _FLOATS, None, None, dev)
         rows, width = x.shape
         if width % dh:
             raise ValueError(f"x has rows of {width} elements, not of heads of {dh}")
@@ -427,7 +453,7 @@ def verify_drafts(target, draft, draft_tokens, row_start, u, r, accepted, tokens
     if dev < 0:
         raise ValueError("target is not a CUDA tensor")
     i32, f32 = torch.int32, torch.float32
-    tp, ts = _mat(target, "target", _PROBS, None, None, dev)
+    tp, ts = _mat(target, "target", _FLOATS, None, None, dev)
     rows, vocab = target.shape
     n_req = row_start.shape[0] - 1
     dp, ds = (0, 0) if draft is None else _mat(draft, "draft", (target.dtype,), rows, vocab, dev)
