@@ -134,23 +134,8 @@ def _bad(t, name, dtypes, shape, device, packed):
                      f"broadcast: strides {t.stride()}"))
 
 
-def _native():
-    """The extension that makes the checks below in a tenth of their time, if it is there for this torch."""
-    try:
-        from . import _args
-    except ImportError:
-        return None
-    return _args if _args.TORCH == torch.__version__ else None
-
-
-_args = _native()
-
-
 def _vec(t, name, dtype, n, device):
     """Address of a contiguous vector of n elements."""
-    p = _args and _args.vec(t, dtype, n, device)
-    if p is not None:
-        return p
     if t.dtype is not dtype or t.get_device() != device or t.shape != (n,) or not t.is_contiguous():
         _bad(t, name, (dtype,), (n,), device, True)
     return t.data_ptr()
@@ -158,9 +143,6 @@ def _vec(t, name, dtype, n, device):
 
 def _mat(t, name, dtypes, rows, cols, device):
     """(address, row stride) of a [rows, cols] matrix (None: any) with contiguous rows."""
-    p = _args and _args.mat(t, dtypes, -1 if rows is None else rows, -1 if cols is None else cols, device)
-    if p is not None:
-        return p
     shape = t.shape
     if (t.dtype not in dtypes or t.get_device() != device or len(shape) != 2
             or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols)):
@@ -182,13 +164,41 @@ def _weights(t, name, rows, device):
 
 
 def _table(t, name, rows, device):
-    p = _args and _args.table(t, torch.int32, -1 if rows is None else rows, device)
-    if p is not None:
-        return p
     if (t.dtype is not torch.int32 or t.get_device() != device or t.dim() != 2
             or (rows is not None and t.shape[0] != rows) or not t.is_contiguous()):
         _bad(t, name, (torch.int32,), (rows, None), device, True)
     return t.data_ptr()
+
+
+def _pages(t, name, block_size, record, device):
+    """(address, strides of pages and of records, pages) of a cache."""
+    if t.dim() != 3 or t.dtype is not torch.uint8 or t.get_device() != device:
+        raise ValueError(f"{name} is a uint8 [blocks, block_size, record] view on cuda:{device}")
+    shape, stride = t.shape, t.stride()
+    if shape[1] != block_size or shape[2] < record or stride[2] != 1:
+        raise ValueError(f"{name}: pages of {block_size} records of {record} contiguous bytes expected, "
+                         f"got shape {tuple(shape)}, strides {stride}")
+    return t.data_ptr(), stride[0], stride[1], shape[0]
+
+
+_IN_PYTHON = _vec, _mat, _table, _pages
+
+
+def _native():
+    """The extension that makes these checks in a tenth of their time, if it is there for this torch."""
+    try:
+        from . import _args
+    except ImportError:
+        return None
+    if (_args.TORCH, getattr(_args, "INTERFACE", 0)) != (torch.__version__, 2):
+        return None
+    _args.otherwise(*_IN_PYTHON)
+    return _args
+
+
+_args = _native()
+if _args:
+    _vec, _mat, _table, _pages = _args.vec, _args.mat, _args.table, _args.pages
 
 
 def _pack(layout, *values):
@@ -251,19 +261,7 @@ class Cache:
         self._width = self.spec["n_q_heads"] * self.spec["head_dim"]
 
     def _view(self, t, name):
-        block, record = self.spec["block_size"], self.spec["kv_record_bytes"]
-        p = _args and _args.view(t, torch.uint8, block, record, self._dev)
-        if p is not None:
-            return p
-        if t.dim() != 3 or t.dtype is not torch.uint8 or t.get_device() != self._dev:
-            raise ValueError(f"{name} is a uint8 [blocks, block_size, record] view on {self.device}")
-        shape, stride = t.shape, t.stride()
-        if (shape[1] != self.spec["block_size"] or shape[2] < self.spec["kv_record_bytes"]
-                or stride[2] != 1):
-            raise ValueError(f"{name}: pages of {self.spec['block_size']} records of "
-                             f"{self.spec['kv_record_bytes']} contiguous bytes expected, got shape "
-                             f"{tuple(shape)}, strides {stride}")
-        return t.data_ptr(), stride[0], stride[1], shape[0]
+        return _pages(t, name, self.spec["block_size"], self.spec["kv_record_bytes"], self._dev)
 
     def attend(self, q, o, positions, row_req, block_table, kv_cache, *, window=0, sinks=0,
                causal=True, scale=None, lse=None, weights=None, stream=None) -> None:

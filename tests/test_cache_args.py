@@ -22,49 +22,56 @@ def tensors():
     yield from (None, 3, "x", [1, 2])
 
 
-class Layout:
-    spec, _dev, device, _view = dict(block_size=8, kv_record_bytes=80), -1, "cpu", mc.Cache._view
-
-
-CHECKS = {
-    "vec": lambda t: mc._vec(t, "t", I32, 6, -1),
-    "vec of one": lambda t: mc._vec(t, "t", I32, 1, -1),
-    "vec of none": lambda t: mc._vec(t, "t", I32, 0, -1),
-    "mat": lambda t: mc._mat(t, "t", (F32,), 6, 16, -1),
-    "mat of any": lambda t: mc._mat(t, "t", mc._FLOATS, None, None, -1),
-    "mat elsewhere": lambda t: mc._mat(t, "t", (F32,), 6, 16, 0),
-    "table": lambda t: mc._table(t, "t", None, -1),
-    "table of six": lambda t: mc._table(t, "t", 6, -1),
-    "view": lambda t: Layout()._view(t, "t"),
+CHECKS = {  # which check, and its arguments behind the tensor
+    "vec": (0, "t", I32, 6, -1),
+    "vec of one": (0, "t", I32, 1, -1),
+    "vec of none": (0, "t", I32, 0, -1),
+    "mat": (1, "t", (F32,), 6, 16, -1),
+    "mat of any": (1, "t", mc._FLOATS, None, None, -1),
+    "mat elsewhere": (1, "t", (F32,), 6, 16, 0),
+    "table": (2, "t", None, -1),
+    "table of six": (2, "t", 6, -1),
+    "pages": (3, "t", 8, 80, -1),
 }
 
 
 @pytest.mark.parametrize("check", CHECKS)
-def test_both_give_the_same(check, monkeypatch):
+def test_both_give_the_same(check):
     if mc._args is None:
         pytest.skip("the extension is not there")
+    which, *args = CHECKS[check]
 
-    def answer(t):
+    def answer(fn, t):
         try:
-            return CHECKS[check](t)
+            return fn(t, *args)
         except (ValueError, AttributeError) as e:
             return type(e), str(e)
 
     for t in tensors():
-        quick = answer(t)
-        with monkeypatch.context() as m:
-            m.setattr(mc, "_args", None)
-            assert quick == answer(t), t
+        assert answer((mc._vec, mc._mat, mc._table, mc._pages)[which], t) == answer(mc._IN_PYTHON[which], t), t
+
+
+def test_what_python_alone_accepts_is_accepted():
+    """What the extension does not know goes to the check in Python."""
+    if mc._args is None:
+        pytest.skip("the extension is not there")
+    seen = []
+    try:
+        mc._args.otherwise(*(lambda *a: seen.append(a) or 7 for _ in range(4)))
+        assert mc._vec("not a tensor", "t", I32, 6, -1) == 7 and seen == [("not a tensor", "t", I32, 6, -1)]
+    finally:
+        mc._args.otherwise(*mc._IN_PYTHON)
+    assert mc._vec is mc._args.vec
 
 
 def test_sizes_that_are_no_numbers():
     if mc._args is None:
         pytest.skip("the extension is not there")
     t = torch.zeros(6, dtype=I32)
-    for bad in (lambda: mc._args.vec(t, I32, 1.5, -1), lambda: mc._args.vec(t, I32, "6", -1), lambda: mc._args.vec(t, I32),
-                lambda: mc._args.mat(t, [F32], 6, 1, -1), lambda: mc._args.view(t, U8, 8, None, -1)):
+    for bad in (lambda: mc._vec(t, "t", I32, 1.5, -1), lambda: mc._vec(t, "t", I32, "6", -1), lambda: mc._vec(t, "t", I32),
+                lambda: mc._mat(t, "t", [F32], 6, 1, -1), lambda: mc._pages(t, "t", 8, "80", -1)):
         with pytest.raises(TypeError):
             bad()
     with pytest.raises(OverflowError):
-        mc._args.vec(t, I32, 2 ** 70, -1)
-    assert mc._args.vec(t, 5, 6, -1) is None and mc._args.vec(t, I32, 6, -1) == t.data_ptr()
+        mc._vec(t, "t", I32, 2 ** 70, -1)
+    assert mc._vec(t, "t", I32, 6, -1) == t.data_ptr()
