@@ -812,6 +812,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
         bool more = false;
         if (lane == 0) more = next_job(ar, plan, cur, job);
         more = __shfl_sync(0xffffffffu, more, 0);
+        __syncwarp();  // (the item that lane 0 wrote, to all lanes: a shuffle orders no memory)
         if (more) item_rows(ar, plan, job);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ss.j_full[k]);
