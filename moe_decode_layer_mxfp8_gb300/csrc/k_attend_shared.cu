@@ -1211,10 +1211,13 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
           bulk_wait_read();
         }
       } else {  // both streams' O in the larger m, half of the dimensions a stream
-        auto meet = [&] {
+        auto meet = [&] {  // (a stream's warps read the other one's O, and leave theirs to it)
+          tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&ss.merge);
-          return wait(&ss.merge, mc++ & 1, a.status, abort);
+          const bool met = wait(&ss.merge, mc++ & 1, a.status, abort);
+          tc_fence_after();
+          return met;
         };
         if (lane < 16) ss.ml[u][ql] = make_float2(m_row, l_row);
         if (!meet()) return;
@@ -1252,9 +1255,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
             }
           }
         }
-        tc_fence_before();
         if (!meet()) return;  // (the next item's products go over both)
-        tc_fence_after();
       }
       tc_fence_before();
       __syncwarp();

@@ -19,3 +19,12 @@ def test_an_items_fields_are_ordered_before_its_rows_are_made():
     barrier is."""
     steps = between("if (lane == 0) more = next_job(ar, plan, cur, job);", "item_rows(ar, plan, job)")
     assert "__syncwarp();" in steps
+
+
+def test_streams_that_meet_order_what_they_read_of_each_others_tensor_memory():
+    """The fence ahead of the arrival and the one behind the wait, whatever is read behind either meeting."""
+    steps = between("auto meet = ", "};")
+    at = [steps.index(x) for x in ("tc_fence_before();", "mbar_arrive(&ss.merge)", "wait(&ss.merge", "tc_fence_after();")]
+    assert at == sorted(at)
+    item = between("auto meet = ", "mbar_arrive(&ss.o_out[u])")
+    assert item.count("meet()") == 2 and item.index("meet()") < item.index("ld_rows(") < item.rindex("meet()")
