@@ -111,8 +111,9 @@ int mono_cache_attend(mono_cache_t *h, const mono_attend_args *args, void *strea
  * mono_cache_attend; o is rounded to bf16 once, w[t] scale_t to 11 bits before that (and to 2^-30
  * of the largest of the 32 to 128 tokens that set a row's reference), q's elements to 2^-24 of a
  * head's largest; scale_t below 2^-64 in size lose bits of o.  A NaN code of a token in view makes
- * NaN the heads of its slice.  Scores of heads whose largest is beyond 2^26 in size are NaN.  Rows
- * of requests whose prefix_of is outside [-1, n_prefix) are left out, o = 0, and raise
+ * NaN the heads of its slice.  A head whose largest score, of all tokens that its row sees, is beyond
+ * 2^27 ln 2 (2^26.5) in size is NaN; tokens that far below 0 weigh nothing beside others.  Rows of
+ * requests whose prefix_of is outside [-1, n_prefix) are left out, o = 0, and raise
  * MONO_STATUS_UNMAPPED_PAGE.  A negative length counts as 0.
  *
  * Limits: n_prefix 1..128; 2 * rows * (kv_dim / head_dim) times the tiles (of 128 tokens) of the
