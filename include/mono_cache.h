@@ -224,7 +224,7 @@ typedef struct {
   void *q_out;                /* like q: q itself with its stride, or not overlapping it */
   int64_t kv_stride, q_stride, q_out_stride; /* elements between rows, whole 16 bytes; 0: packed */
   const int32_t *positions;   /* [rows], < 0 for a pad row */
-  const int32_t *rope_positions; /* optional [rows] */
+  const int32_t *rope_positions; /* optional [rows]; not read without a table */
   const int32_t *row_req;     /* [rows] */
   const int32_t *block_table; /* [n_req, max_blocks] */
   uint8_t *kv_cache;          /* [kv_num_blocks, block_size, record] view, as in mono_step_args */

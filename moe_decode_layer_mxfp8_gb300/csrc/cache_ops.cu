@@ -364,7 +364,7 @@ int mono_cache_append(mono_cache_t* h, const mono_append_args* a, void* stream) 
   k.rows = a->rows;
   k.head_dim = s.head_dim;
   k.positions = a->positions;
-  k.rope_positions = a->rope_positions;
+  k.rope_positions = a->rope.table ? a->rope_positions : nullptr;
   k.x = a->q;
   k.out = a->q_out;
   k.x_stride = qs;
