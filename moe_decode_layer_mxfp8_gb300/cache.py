@@ -356,6 +356,8 @@ class Cache:
         """The fields of a rotation: ``rope`` is f32 [positions, dim]."""
         p, stride = _mat(rope, "rope", _F32, None, None, self._dev)
         positions, dim = rope.shape
+        if not p:  # (no address would mean no rotation)
+            raise ValueError(f"rope has no entries: shape {tuple(rope.shape)}")
         if offset is None:
             offset = self.spec["head_dim"] - dim
         return p, stride, positions, dim, offset, 1 if interleaved else 0, 1 if inverse else 0
