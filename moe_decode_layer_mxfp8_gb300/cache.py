@@ -341,11 +341,15 @@ class Cache:
         vp, vs, vc = (0, 0, 0) if weights_out is None else _weights(weights_out, "weights_out", n_req, dev)
         tp, tb = (0, 0) if dst_table is None else (_table(dst_table, "dst_table", n_req, dev),
                                                    dst_table.shape[1])
+        if dst_table is not None and not tp:  # (no address would mean in place)
+            raise ValueError("dst_table has no columns")
         dst = (0, 0, 0, 0)
         if dst_cache is not None:
             if dst_table is None:
                 raise ValueError("dst_cache needs a dst_table")
             dst = self._view(dst_cache, "dst_cache")
+            if not dst[0]:  # (no address would mean kv_cache)
+                raise ValueError("dst_cache has no pages")
         args = _pack(_EVICT, wp, vp, ws, vs, _vec(lengths, "lengths", i32, n_req, dev),
                      _vec(new_lengths, "new_lengths", i32, n_req, dev), kp, ks, budget, sinks,
                      recent, n_req, _table(block_table, "block_table", None, dev), max_blocks,
