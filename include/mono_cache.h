@@ -35,7 +35,11 @@ typedef struct {
   int32_t max_rows, max_req;
 } mono_cache_spec;
 
-/* Validates the layout and allocates the workspace on the current device. */
+/*
+ * Validates the layout and allocates the workspace on the current device: that of the operator that needs
+ * most, for the shared prefixes 8 * (head_dim + 8) bytes a row and head, and 1024 * (head_dim + 8) an SM
+ * (25 MB at 48 rows of 64 heads of 128, 95 MB at 1024).
+ */
 int mono_cache_build(const mono_cache_spec *spec, mono_cache_t **out);
 /* Releases it.  NULL is accepted. */
 void mono_cache_free(mono_cache_t *h);

@@ -14,9 +14,9 @@ struct mono_cache {
   int device = 0;
   uint8_t* arena = nullptr;
   float* lse = nullptr;
-  uint8_t* attend_ws = nullptr;
-  uint8_t* evict_ws = nullptr;
-  uint8_t* shared_ws = nullptr;
+  // What a call's kernels leave to each other, whichever the operator: a handle's calls follow one another on the
+  // GPU, every kernel waits for those before it ahead of its first access, and none reads what its call did not write.
+  uint8_t* workspace = nullptr;
   int sms = 0;
   int* status = nullptr;
 };
@@ -120,14 +120,13 @@ int mono_cache_build(const mono_cache_spec* spec, mono_cache_t** out) {
   h->spec = *spec;
   h->device = dev;
   const size_t lse = ((size_t)spec->max_rows * spec->n_q_heads * 4 + 255) / 256 * 256;
-  const size_t part = attend_workspace_bytes(spec->max_rows, prop.multiProcessorCount);
-  const size_t ev = (evict_workspace_bytes(spec->max_req) + 255) / 256 * 256;
-  const size_t shared = shared_workspace_bytes(spec->max_rows, spec->n_q_heads, spec->head_dim,
-                                               prop.multiProcessorCount);
-  const size_t part_end = (part + 255) / 256 * 256;
-  const size_t bytes = 256 + lse + ev + part_end + shared;
+  const size_t bytes = 256 + lse +
+                       std::max({attend_workspace_bytes(spec->max_rows, prop.multiProcessorCount),
+                                 evict_workspace_bytes(spec->max_req),
+                                 shared_workspace_bytes(spec->max_rows, spec->n_q_heads, spec->head_dim,
+                                                        prop.multiProcessorCount)});
   cudaError_t e = cudaMalloc(&h->arena, bytes);
-  if (e == cudaSuccess) e = cudaMemset(h->arena, 0, bytes);
+  if (e == cudaSuccess) e = cudaMemset(h->arena, 0, 256);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = attend_prepare();
   if (e == cudaSuccess) e = evict_prepare();
@@ -138,9 +137,7 @@ int mono_cache_build(const mono_cache_spec* spec, mono_cache_t** out) {
   }
   h->status = reinterpret_cast<int*>(h->arena);
   h->lse = reinterpret_cast<float*>(h->arena + 256);
-  h->evict_ws = h->arena + 256 + lse;
-  h->attend_ws = h->evict_ws + ev;
-  h->shared_ws = h->attend_ws + part_end;
+  h->workspace = h->arena + 256 + lse;
   h->sms = prop.multiProcessorCount;
   *out = h;
   return MONO_OK;
@@ -213,7 +210,7 @@ int mono_cache_attend(mono_cache_t* h, const mono_attend_args* a, void* stream) 
   k.weights_cols = a->weights_cols ? a->weights_cols : a->weights_stride;
   k.status = h->status;
   return cuda_code(launch_attend(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k,
-                                 h->attend_ws, s.max_rows, h->sms));
+                                 h->workspace, s.max_rows, h->sms));
 }
 
 int mono_cache_attend_shared(mono_cache_t* h, const mono_shared_args* a, void* stream) {
@@ -268,7 +265,7 @@ int mono_cache_attend_shared(mono_cache_t* h, const mono_shared_args* a, void* s
   k.lse = a->lse;
   k.status = h->status;
   return cuda_code(launch_attend_shared(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k,
-                                        h->shared_ws, s.max_rows, h->sms));
+                                        h->workspace, s.max_rows, h->sms));
 }
 
 int mono_cache_evict(mono_cache_t* h, const mono_evict_args* a, void* stream) {
@@ -334,7 +331,7 @@ int mono_cache_evict(mono_cache_t* h, const mono_evict_args* a, void* stream) {
   k.copy_bytes = (s.kv_dim + 4 + 15) / 16 * 16;
   k.status = h->status;
   return cuda_code(launch_evict(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k,
-                                h->evict_ws, s.max_req, h->sms));
+                                h->workspace, s.max_req, h->sms));
 }
 
 int mono_cache_append(mono_cache_t* h, const mono_append_args* a, void* stream) {

@@ -132,3 +132,39 @@ def test_rotary_positions_without_a_table_are_not_looked_at(lib):
         assert h.call("append", append_args(rope_positions=A + 64, rope=rope)) == 0
         assert lib.rotation_given() == 32 and lib.rope_positions_given() == A + 64
         assert h.call("append", append_args(rope_positions=A + 2)) == -4  # (a wrong one is still refused)
+
+
+def attend_args(**kw):
+    return mc.AttendArgs(**dict(dict(q=A, o=A, positions=A, row_req=A, block_table=A, max_blocks=5, n_req=2, rows=3, **VIEW), **kw))
+
+
+def shared_args():
+    return mc.SharedArgs(q=A, o=A, positions=A, row_req=A, block_table=A, prefix_table=A, prefix_lengths=A, max_blocks=5,
+                         n_req=2, prefix_max_blocks=3, n_prefix=1, rows=3, **VIEW)
+
+
+def evict_args():
+    return mc.EvictArgs(weights=A, lengths=A, new_lengths=A, kept=A, block_table=A, weights_stride=320, kept_stride=8, budget=8,
+                        n_req=2, max_blocks=5, **VIEW)
+
+
+@pytest.mark.parametrize("max_rows,n_q_heads", [(1, 4), (48, 16), (1024, 32)])
+def test_operators_that_follow_one_another_share_a_workspace(lib, max_rows, n_q_heads):
+    """A handle holds that of the largest, not all of them, and spends no time on its contents."""
+    shared = 5000000 + 1000 * max_rows
+    before = value(lib, "zeroed")
+    with Handle(lib, max_rows=max_rows, n_q_heads=n_q_heads) as h:
+        assert h.rc == 0
+        all_bytes, lse = value(lib, "allocated"), max_rows * n_q_heads * 4
+        assert shared + lse <= all_bytes <= shared + lse + 4096
+        assert value(lib, "zeroed") - before <= 4096
+        rows = min(3, max_rows)
+        for name, args in (("attend", attend_args(rows=rows)), ("attend_shared", shared_args()), ("evict", evict_args())):
+            args.rows = rows
+            assert h.call(name, args) == 0
+        arena = value(lib, "arena", C.c_void_p)
+        at = {value(lib, n, C.c_void_p) - arena for n in ("attend_at", "shared_at", "evict_at")}
+        # one place, 256-byte aligned in the arena, behind the status word and the attention's own log-sums
+        lse_at = value(lib, "lse_at", C.c_void_p) - arena
+        assert len(at) == 1 and lse_at >= 4 and min(at) >= lse_at + lse and min(at) % 256 == 0
+        assert min(at) + shared <= all_bytes
