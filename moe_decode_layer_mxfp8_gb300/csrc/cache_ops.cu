@@ -19,6 +19,7 @@ struct mono_cache {
   uint8_t* workspace = nullptr;
   int sms = 0;
   int* status = nullptr;
+  cudaError_t shared_ready = cudaSuccess;  // (the others do without that kernel)
 };
 
 namespace {
@@ -130,11 +131,12 @@ int mono_cache_build(const mono_cache_spec* spec, mono_cache_t** out) {
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = attend_prepare();
   if (e == cudaSuccess) e = evict_prepare();
-  if (e == cudaSuccess) e = shared_prepare();
   if (e != cudaSuccess) {
     mono_cache_free(h);
     return cuda_code(e);
   }
+  h->shared_ready = shared_prepare();
+  if (h->shared_ready != cudaSuccess) (void)cudaGetLastError();
   h->status = reinterpret_cast<int*>(h->arena);
   h->lse = reinterpret_cast<float*>(h->arena + 256);
   h->workspace = h->arena + 256 + lse;
@@ -240,6 +242,7 @@ int mono_cache_attend_shared(mono_cache_t* h, const mono_shared_args* a, void* s
                    (int64_t)std::max(a->max_blocks, a->prefix_max_blocks) * s.block_size))
     return MONO_ERR_INVALID_ARG;
   TRY(check_device(h));
+  if (h->shared_ready != cudaSuccess) return cuda_code(h->shared_ready);
   SharedArgs k = {};
   k.q = static_cast<const __nv_bfloat16*>(a->q);
   k.o = static_cast<__nv_bfloat16*>(a->o);

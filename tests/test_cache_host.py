@@ -168,3 +168,17 @@ def test_operators_that_follow_one_another_share_a_workspace(lib, max_rows, n_q_
         lse_at = value(lib, "lse_at", C.c_void_p) - arena
         assert len(at) == 1 and lse_at >= 4 and min(at) >= lse_at + lse and min(at) % 256 == 0
         assert min(at) + shared <= all_bytes
+
+
+def test_a_kernel_that_cannot_run_is_its_own_operators_business(lib):
+    C.c_int.in_dll(lib, "shared_error").value = 9
+    try:
+        with Handle(lib) as h:
+            assert h.rc == 0
+            assert h.call("attend", attend_args()) == 0 and h.call("evict", evict_args()) == 0
+            assert h.call("append", append_args()) == 0
+            assert h.call("attend_shared", shared_args()) == -7
+    finally:
+        C.c_int.in_dll(lib, "shared_error").value = 0
+    with Handle(lib) as h:
+        assert h.call("attend_shared", shared_args()) == 0
