@@ -21,7 +21,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmono_layer.so")
-ARGS_LIB = os.path.join(HERE, "_args.so")
+# (its name is for one interpreter: another one does not find it)
+ARGS_LIB = os.path.join(HERE, "_args" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["k_gemm.cu", "k_expert_tc.cu", "k_dense_tc.cu", "k_norm.cu", "k_attn.cu", "k_route.cu", "mono_layer.cu",
            "noalloc.cu", "k_attend.cu", "k_attend_weights.cu", "k_attend_join.cu", "k_evict.cu", "k_verify.cu",
            "k_rotate.cu", "k_attend_shared.cu", "cache_ops.cu"]
@@ -54,9 +55,12 @@ def _stale(obj: str, src: str) -> bool:
 
 def build_args(force: bool = False) -> str | None:
     """The extension of csrc/args.cpp; None where it cannot be built."""
-    src, stamp = os.path.join(CSRC, "args.cpp"), os.path.join(OUT_DIR, "args.torch")
+    src, stamp = os.path.join(CSRC, "args.cpp"), os.path.join(OUT_DIR, os.path.basename(ARGS_LIB) + ".torch")
     try:
         import torch
+        for_any = os.path.join(os.path.dirname(ARGS_LIB), "_args.so")  # (as it was named: any interpreter would load it)
+        if os.path.exists(for_any):
+            os.remove(for_any)
         if (not force and os.path.exists(ARGS_LIB) and os.path.exists(stamp)
                 and os.path.getmtime(ARGS_LIB) >= os.path.getmtime(src)
                 and open(stamp).read() == torch.__version__):
