@@ -127,7 +127,7 @@ size_t evict_workspace_bytes(int max_req);
 bool evict_fits(int n_req, int budget, long long cap);
 cudaError_t evict_prepare();
 cudaError_t launch_evict(const Launch&, const EvictArgs&, uint8_t* workspace, int max_req, int sms);
-cudaError_t launch_rotate(const Launch&, const RotateArgs&, int dtype);  // dtype: MONO_TYPE_*
+cudaError_t launch_rotate(const Launch&, const RotateArgs&, int dtype, int sms);  // dtype: MONO_TYPE_*
 cudaError_t launch_verify(const Launch&, const VerifyArgs&, int dtype, int sms);
 
 }  // namespace mono

@@ -378,7 +378,7 @@ int mono_cache_append(mono_cache_t* h, const mono_append_args* a, void* stream) 
   k.cache = {a->kv_cache, a->kv_stride_block, a->kv_stride_tok, a->kv_num_blocks,
              a->block_table, a->max_blocks, s.block_size};
   k.status = h->status;
-  return cuda_code(launch_rotate(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k, a->dtype));
+  return cuda_code(launch_rotate(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k, a->dtype, h->sms));
 }
 
 int mono_cache_rotate(mono_cache_t* h, const mono_rotate_args* a, void* stream) {
@@ -406,7 +406,7 @@ int mono_cache_rotate(mono_cache_t* h, const mono_rotate_args* a, void* stream) 
   k.out_stride = os;
   k.heads = a->heads;
   k.status = h->status;
-  return cuda_code(launch_rotate(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k, a->dtype));
+  return cuda_code(launch_rotate(Launch{reinterpret_cast<cudaStream_t>(stream), true}, k, a->dtype, h->sms));
 }
 
 int mono_verify_drafts(const mono_verify_args* a, void* stream) {

@@ -26,8 +26,8 @@ namespace {
 
 constexpr int THREADS = 128, WARPS = THREADS / 32;
 constexpr int AHEAD = 4;  // a thread's loads in flight
-constexpr int PER = 8;    // heads of a thread where there are rows enough to fill the GPU
-constexpr long long MANY = 152 * 1024;
+constexpr int PER = 8;    // heads of a thread where there are rows enough to fill the GPU,
+constexpr int FULL = 1024;  // which takes so many threads an SM
 static_assert(WARPS * 256 >= 1024, "the widest latent a CTA");
 
 template <typename T>
@@ -266,7 +266,7 @@ cudaError_t launch(const Launch& L, const RotateArgs& a, unsigned grid) {
 
 }  // namespace
 
-cudaError_t launch_rotate(const Launch& L, const RotateArgs& args, int dtype) {
+cudaError_t launch_rotate(const Launch& L, const RotateArgs& args, int dtype, int sms) {
   RotateArgs a = args;
   a.span = 32, a.kv_blocks = 0, a.apart = 0;
   if (a.kv) {
@@ -280,7 +280,7 @@ cudaError_t launch_rotate(const Launch& L, const RotateArgs& args, int dtype) {
     const int slots = THREADS / (a.head_dim / 8);
     int across = a.heads < slots ? a.heads : slots;
     while (across > 1 && (a.heads + across - 1) / across < PER &&
-           (long long)a.rows * across * (a.head_dim / 8) > MANY)
+           (long long)a.rows * across * (a.head_dim / 8) > (long long)FULL * sms)
       across /= 2;
     a.across = across;
     const int rows = slots / across;

@@ -17,6 +17,7 @@ using namespace mono;
 extern "C" {
 int shared_error;  // what the attention over shared prefixes says when it is prepared
 RotateArgs rotated;
+int rotated_sms;
 uint8_t *attend_at, *shared_at, *evict_at;
 const float* lse_at;
 cudaError_t cudaGetDeviceProperties(cudaDeviceProp* p, int) {
@@ -42,7 +43,7 @@ cudaError_t launch_attend(const Launch&, const AttendArgs& a, uint8_t* ws, int, 
 }
 cudaError_t launch_attend_shared(const Launch&, const SharedArgs&, uint8_t* ws, int, int) { shared_at = ws; return cudaSuccess; }
 cudaError_t launch_evict(const Launch&, const EvictArgs&, uint8_t* ws, int, int) { evict_at = ws; return cudaSuccess; }
-cudaError_t launch_rotate(const Launch&, const RotateArgs& a, int) { rotated = a; return cudaSuccess; }
+cudaError_t launch_rotate(const Launch&, const RotateArgs& a, int, int sms) { rotated = a, rotated_sms = sms; return cudaSuccess; }
 cudaError_t launch_verify(const Launch&, const VerifyArgs&, int, int) { return cudaSuccess; }
 }
 """
@@ -132,6 +133,15 @@ def test_rotary_positions_without_a_table_are_not_looked_at(lib):
         assert h.call("append", append_args(rope_positions=A + 64, rope=rope)) == 0
         assert lib.rotation_given() == 32 and lib.rope_positions_given() == A + 64
         assert h.call("append", append_args(rope_positions=A + 2)) == -4  # (a wrong one is still refused)
+
+
+def test_rotations_are_dealt_out_over_the_devices_sms(lib):
+    with Handle(lib) as h:
+        rope = dict(table=A, positions=9, dim=32, offset=32)
+        rot = mc.RotateArgs(x=A, out=A, positions=A, dtype=1, rows=3, heads=2, rope=mc.Rope(**rope))
+        for name, args in (("rotate", rot), ("append", append_args(rope=rope))):
+            C.c_int.in_dll(lib, "rotated_sms").value = 0
+            assert h.call(name, args) == 0 and value(lib, "rotated_sms", C.c_int) == 152
 
 
 def attend_args(**kw):
