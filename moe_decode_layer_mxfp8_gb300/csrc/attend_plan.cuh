@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cfloat>
 
 #include "cache_kernels.h"
 
@@ -11,7 +12,7 @@ namespace attend {
 
 constexpr int MAX_REQ = 512;
 constexpr int MAX_COLS = 96;  // query columns of a row group at most
-constexpr float UNSET = -1.0e30f;  // the reference m_q of a query that has seen no token
+constexpr float UNSET = -FLT_MAX;  // the reference m_q of a query that has seen no token, below every score
 // Token scales above this (and infinite ones) count as NaN.  The reference follows weights times scales,
 // so that a weight itself lies as far below 2^-30 as its scale lies above 1: beyond this scale, weights
 // that count would be lost to an f32, and their sum with them.

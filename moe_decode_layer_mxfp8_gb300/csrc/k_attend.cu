@@ -301,7 +301,8 @@ __device__ __forceinline__ void soft_tiles(const AttendArgs& a, const Soft& w, c
           if (!WIDE) tc_loaded(y);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            x[e] = fmaf(WIDE ? x[e] : x[e] + y[e], ct, lsc);
+            // (a score that an f32 does not hold, -inf, is not one that is not seen)
+            x[e] = fmaxf(fmaf(WIDE ? x[e] : x[e] + y[e], ct, lsc), -2.0f * SCORE_MAX);
             if (!((see >> (g + e)) & 1)) x[e] = -INFINITY;
           }
           const float v = over_lanes<8, true>(x);

@@ -59,7 +59,6 @@ constexpr float TOO_LARGE = 0x1p15f;           // m moves when a weight times a_
 // The least reference: tokens below it have no weight beside those that come later, and a head whose tokens are all
 // below it (as large as scores have to be for a NaN, and negative) is NaN.
 constexpr float LOWEST = -SCORE_MAX;
-constexpr float UNSEEN = -FLT_MAX;  // the reference of a query that has seen no token, below every score
 // queries are taken times 2^6: the largest element of most is then between 2^-1 and 2^15 (bf16 bits of the limits)
 constexpr float Q_SCALE = 64.0f;
 constexpr uint32_t Q_LOW = 0x3C00, Q_HIGH = 0x4400;
@@ -957,7 +956,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
       __syncwarp();
       if (lane == 0) mbar_arrive(&ss.q_full[u]);
 
-      float m[2] = {UNSEEN, UNSEEN}, l[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+      float m[2] = {UNSET, UNSET}, l[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll 1
       for (int j = 0; j < n; ++j, ++sc) {
         const int i = job.ring(u, j), s = (it + i) % NS;
@@ -1002,7 +1001,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
               by[r] = 1.0f;
               if (top[r] - m[r] > BASE) {
                 const float now = top[r] <= SCORE_MAX ? fmaxf(ceilf(top[r]) - BASE, LOWEST) : __int_as_float(0x7FC00000);
-                by[r] = m[r] == UNSEEN ? 0.0f : ex2(m[r] - now);
+                by[r] = m[r] == UNSET ? 0.0f : ex2(m[r] - now);
                 m[r] = now;
               }
               l[r][0] *= by[r];
@@ -1161,7 +1160,7 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
       it += job.count();
 
       // ---- the piece: the references and sums of the rows, a lane each; then O
-      float m_row = UNSEEN, l_row = 0.0f;
+      float m_row = UNSET, l_row = 0.0f;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         float t = l[r][0] + l[r][1];
@@ -1234,8 +1233,8 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
         const float2 x = ss.ml[0][ql], y = ss.ml[1][ql];
         m_row = fmaxf(x.x, y.x);
         // (a NaN stays one)
-        const float fx = x.y != x.y ? 1.0f : x.x == UNSEEN ? 0.0f : ex2(x.x - m_row);
-        const float fy = y.y != y.y ? 1.0f : y.x == UNSEEN ? 0.0f : ex2(y.x - m_row);
+        const float fx = x.y != x.y ? 1.0f : x.x == UNSET ? 0.0f : ex2(x.x - m_row);
+        const float fy = y.y != y.y ? 1.0f : y.x == UNSET ? 0.0f : ex2(y.x - m_row);
         l_row = (fx != 0.0f ? x.y * fx : 0.0f) + (fy != 0.0f ? y.y * fy : 0.0f);
         if (to && u == 0 && lane < 16) *reinterpret_cast<float2*>(to) = make_float2(m_row, l_row);
         if (!idle) {
@@ -1301,7 +1300,7 @@ __global__ void __launch_bounds__(MAX_TEAM * 32) join_shared_kernel(const __grid
   // its own tokens, and the others
   const int home = (r * a.n_q + (h < a.n_q ? h : 0)) * ld, own_home = home + ar.max_rows * a.n_q * ld, next = 2 * BLOCK * ld;
   const int over = (int)(ar.over - ar.home) + (h - slice * ar.hps) * ld;
-  float m = UNSEEN, den = 0.0f;
+  float m = UNSET, den = 0.0f;
   float4 num = {0.0f, 0.0f, 0.0f, 0.0f};
   auto part_of = [&](const float2& ml) {  // (a piece that saw nothing has no part; a NaN stays one)
     return ml.y != ml.y ? 1.0f : ml.y == 0.0f ? 0.0f : ex2(ml.x - m);
@@ -1314,8 +1313,8 @@ __global__ void __launch_bounds__(MAX_TEAM * 32) join_shared_kernel(const __grid
     float2 p = *reinterpret_cast<const float2*>(ar.home + home), q = *reinterpret_cast<const float2*>(ar.home + own_home);
     const float4 x = *reinterpret_cast<const float4*>(ar.home + home + 8 + d),
                  y = *reinterpret_cast<const float4*>(ar.home + own_home + 8 + d);
-    if (info.x <= 0) p = {UNSEEN, 0.0f};
-    if (info.z <= 0) q = {UNSEEN, 0.0f};
+    if (info.x <= 0) p = {UNSET, 0.0f};
+    if (info.z <= 0) q = {UNSET, 0.0f};
     m = fmaxf(p.x, q.x);
     const float f = part_of(p), g = part_of(q);
     den = (f != 0.0f ? f * p.y : 0.0f) + (g != 0.0f ? g * q.y : 0.0f);
@@ -1332,7 +1331,7 @@ __global__ void __launch_bounds__(MAX_TEAM * 32) join_shared_kernel(const __grid
     float4 x[FEW];
 #pragma unroll
     for (int e = 0; e < FEW; ++e) {
-      ml[e] = {UNSEEN, 0.0f};
+      ml[e] = {UNSET, 0.0f};
       if (e >= all) continue;
       const float* at = ar.home + place((e << team_log2) + mate);
       ml[e] = *reinterpret_cast<const float2*>(at);
@@ -1356,7 +1355,7 @@ __global__ void __launch_bounds__(MAX_TEAM * 32) join_shared_kernel(const __grid
   for (int b = 0; b < all; b += 32) {
     const int in = min(32, all - b);
     int at = home;  // a piece a lane
-    float2 ml = {UNSEEN, 0.0f};
+    float2 ml = {UNSET, 0.0f};
     if (lane < in) {
       at = place(((b + lane) << team_log2) + mate);
       ml = *reinterpret_cast<const float2*>(ar.home + at);
