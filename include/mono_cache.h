@@ -38,7 +38,7 @@ typedef struct {
 /*
  * Validates the layout and allocates the workspace on the current device: that of the operator that needs
  * most, for the shared prefixes 8 * (head_dim + 8) bytes a row and head, and 1024 * (head_dim + 8) an SM
- * (25 MB at 48 rows of 64 heads of 128, 95 MB at 1024).
+ * (25 MB at 48 rows of 64 heads of 128, 94 MB at 1024).
  */
 int mono_cache_build(const mono_cache_spec *spec, mono_cache_t **out);
 /* Releases it.  NULL is accepted. */
@@ -109,7 +109,8 @@ int mono_cache_attend(mono_cache_t *h, const mono_attend_args *args, void *strea
  * t >= P, are at block_table[b][t / block_size] as ever (entries that lie in the prefix alone are
  * not read), so that both tables may be those of whole contexts.  prefix_of[b] = -1: no prefix;
  * prefix_of NULL: prefix 0 for all.  Row r at position p sees t <= hi, hi as there; a row inside
- * its prefix sees that much of it.
+ * its prefix sees that much of it.  Faster than mono_cache_attend over whole contexts from some 1000
+ * shared tokens on, slower where little is shared and requests of a row or two hold many tokens of their own.
  *
  * Sums, refused and masked tokens, status bits, pad rows, lse and the handle's workspace are as in
  * mono_cache_attend; o is rounded to bf16 once, w[t] scale_t to 11 bits before that (and to 2^-30

@@ -185,7 +185,7 @@ _IN_PYTHON = _vec, _mat, _table, _pages
 
 
 def _native():
-    """The extension that makes these checks in a tenth of their time, if it is there for this torch."""
+    """The extension that makes these checks faster, if it is there for this torch."""
     try:
         from . import _args
     except ImportError:
@@ -298,7 +298,9 @@ class Cache:
         """Attention as ``attend``, where the first prefix_lengths[g] tokens (int32 [prefixes]) of a
         request b with prefix_of[b] = g (int32 [n_req]; -1: none; None: 0 for all) are those of
         row g of ``prefix_table`` (int32 [prefixes, blocks]), read once for all its requests;
-        tokens behind them are in ``block_table``, indexed by their place in the whole context."""
+        tokens behind them are in ``block_table``, indexed by their place in the whole context.
+        Worth it from some 1K shared tokens on; where little is shared and requests of a row or two
+        have many tokens of their own, ``attend`` is faster."""
         dev, i32 = self._dev, torch.int32
         rows, (n_req, max_blocks) = q.shape[0], block_table.shape
         n_prefix, prefix_blocks = prefix_table.shape

@@ -27,9 +27,13 @@
 // other stream's fill some), their barriers (700) and the softmax (1550); a step of two tiles takes 3150 to
 // 3600 cycles where the MMAs alone would take 2050.  An item costs some 6 us beside its tiles (queries 1.5,
 // first scores 0.7, first softmax 2, last product and piece 1.5), the plan and the first item 3, the join 2 to 8.
-// Measured in a graph, 64 heads of 128: one question behind 777 tokens 12.9 us; eight requests behind 32K
-// tokens 22 (a call per request's whole context: 38 by the other kernel), with five drafts each 54.5 (976
-// TFLOP/s of 1904 measured); 256 behind 8K tokens with up to 1K of their own 111.
+// Measured in a graph, 64 heads of 128: one question behind 777 tokens 13.0 us; eight requests behind 32K
+// tokens 22, with five drafts each 54.6 (975 TFLOP/s of 1904 measured); 256 behind 8K tokens with up to 1K of
+// their own 111; 8 x 128 prompt rows behind 32K tokens 835 (1320 TFLOP/s), behind 4K 167.  Beside the attention
+// of whole contexts (k_attend.cu), whose queries are the N and need not fill 128: eight requests behind 32K
+// tokens 22 us, 38 there, behind 1K 14.0 and 13.6; 64 behind 1K with 500 of their own 25 and 28, behind 256 23.4
+// and 21.9; one question behind 777 tokens 13.0 and 12.0, behind 8K 14.1 and 21.3; 256 requests that share nothing, 127 tokens
+// each 32 and 46, 511 54 and 55, 1023 76 and 67.
 #include <cfloat>
 #include <cstddef>
 
@@ -666,23 +670,24 @@ __global__ void __maxnreg__(REGS) attend_shared_kernel(const __grid_constant__ A
               *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
               *reinterpret_cast<uint4*>(dst + row * 128 + (((c ^ 1) ^ (row & 7)) << 4)) = make_uint4(0, 0, 0, 0);
             }
-          } else
+          } else {
 #pragma unroll 1
-          for (int e0 = 0; e0 < N; e0 += 4) {
-            uint4 v[4];
+            for (int e0 = 0; e0 < N; e0 += 4) {
+              uint4 v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = lds128(src + (e0 + e) * ROWS * DH);
+              for (int e = 0; e < 4; ++e) v[e] = lds128(src + (e0 + e) * ROWS * DH);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int row = t0 + (e0 + e) * ROWS + r0, c = 2 * (piece & 3) + odd;
-              uint4 x, y;
-              uint32_t f[2];
-              e4m3x4_to_f16x4(odd ? v[e].z : v[e].x, f), x.x = f[0], x.y = f[1];
-              e4m3x4_to_f16x4(odd ? v[e].w : v[e].y, f), x.z = f[0], x.w = f[1];
-              e4m3x4_to_f16x4(odd ? v[e].x : v[e].z, f), y.x = f[0], y.y = f[1];
-              e4m3x4_to_f16x4(odd ? v[e].y : v[e].w, f), y.z = f[0], y.w = f[1];
-              *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = x;
-              *reinterpret_cast<uint4*>(dst + row * 128 + (((c ^ 1) ^ (row & 7)) << 4)) = y;
+              for (int e = 0; e < 4; ++e) {
+                const int row = t0 + (e0 + e) * ROWS + r0, c = 2 * (piece & 3) + odd;
+                uint4 x, y;
+                uint32_t f[2];
+                e4m3x4_to_f16x4(odd ? v[e].z : v[e].x, f), x.x = f[0], x.y = f[1];
+                e4m3x4_to_f16x4(odd ? v[e].w : v[e].y, f), x.z = f[0], x.w = f[1];
+                e4m3x4_to_f16x4(odd ? v[e].x : v[e].z, f), y.x = f[0], y.y = f[1];
+                e4m3x4_to_f16x4(odd ? v[e].y : v[e].w, f), y.z = f[0], y.w = f[1];
+                *reinterpret_cast<uint4*>(dst + row * 128 + ((c ^ (row & 7)) << 4)) = x;
+                *reinterpret_cast<uint4*>(dst + row * 128 + (((c ^ 1) ^ (row & 7)) << 4)) = y;
+              }
             }
           }
           __syncwarp();

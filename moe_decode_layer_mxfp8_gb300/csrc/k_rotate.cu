@@ -14,20 +14,21 @@
 // of a warp, or whole warps, its largest element one reduction away from its codes.
 //
 // Bound by DRAM where steps are large, by latency (launch, position, table) where they are small.  Measured
-// in a graph: one request's token 2.5 us; 48 rows of 64 heads 2.7, back 2.6; 20001 rows of 16 heads of 64,
-// f16, 15.6 (5.4 TB/s of 6.8; a head a thread: 47); 22K prompt rows of 64 heads of 128 with their latents 134
-// (5.7 TB/s; with CTAs of 256 threads 40 more, with twice as many loads in flight 10; latents by the
-// heads' threads need 72 registers: 7 more), without latents 6.6 TB/s; 14K narrow f32 latents 5.1 (a warp
-// each: 10).
+// in a graph: one request's token 2.6 us; 48 rows of 64 heads 2.8, back 2.7; 20001 rows of 16 heads of 64 in
+// f16 15.5 (5.4 TB/s of 6.8 measured), bf16 15.2, f32 26.0 (6.4 TB/s); 22K prompt rows of 64 heads of 128 with
+// their latents in bf16 134 (5.7 TB/s), f32 228 (6.6 TB/s), their heads alone 109 (6.7 TB/s); 14K narrow f32
+// latents 5.2 (a warp each: 8.5), with 16 heads of queries 21.7 (6.0 TB/s; bf16 14.0).  With CTAs of 256 threads
+// the prompts take 138 and 232.
 #include "cache_kernels.h"
 
 namespace mono {
 namespace {
 
 constexpr int THREADS = 128, WARPS = THREADS / 32;
-constexpr int AHEAD = 4;  // a thread's loads in flight
-constexpr int PER = 8;    // heads of a thread where there are rows enough to fill the GPU,
-constexpr int FULL = 1024;  // which takes so many threads an SM
+constexpr int AHEAD = 4;  // a thread's loads in flight (2: prompts 142 us, 48 rows 3.2; 8: prompts 142)
+// Heads of a thread where there are rows enough to fill the GPU (20001 rows of 16 heads 15.5 us; 1: 34.3, 4: 16.7,
+// 16: 17.6), which takes so many threads an SM (512 and 2048: no change where rows are many).
+constexpr int PER = 8, FULL = 1024;
 static_assert(WARPS * 256 >= 1024, "the widest latent a CTA");
 
 template <typename T>
@@ -71,7 +72,8 @@ template <typename T>
 __device__ __forceinline__ Run<T> load_run(const T* p) {
   return *reinterpret_cast<const Run<T>*>(p);
 }
-// The same of what is read or written once: heads (48 rows of 64 2.67 -> 2.56 us, 23K prompt rows 143 -> 140).
+// The same of what is read or written once: heads (20001 rows of 16 heads 15.5 us, with plain loads and stores 17.0;
+// narrow f32 prompts with queries 21.7 and 24.4).
 template <typename T>
 __device__ __forceinline__ Run<T> load_once(const T* p) {
   Run<T> v;
@@ -152,8 +154,8 @@ __device__ __forceinline__ int rope_position(const RotateArgs& a, int p, int t, 
 }
 
 // Heads of rows, or latents where there are any (kv_blocks CTAs among the others, so that their chains of latencies
-// and the heads' bandwidth overlap: 23K prompt rows 148 us with the latents first; without heads all, in fewer
-// registers).  Heads: a thread's 8 dimensions of a slot of heads; as many rows a CTA as its threads hold.
+// and the heads' bandwidth overlap: 22K prompt rows 134 us, 140 with the latents first; in f32 228 and 246; without
+// heads all, in fewer registers).  Heads: a thread's 8 dimensions of a slot of heads; as many rows a CTA as its threads hold.
 template <typename T, bool HEADS>
 __global__ void __launch_bounds__(THREADS) rotate_kernel(const RotateArgs a) {
   // (the warp, and what loops depend on, from one lane: the compiler then knows the shuffles to be whole warps')
